@@ -97,6 +97,13 @@ typedef enum fs_order {
     FS_ORDER_JOINT = 1
 } fs_order;
 
+/* Element types of the entries that take more than float32. */
+typedef enum fs_dtype {
+    FS_F32 = 0,
+    FS_BF16 = 1,
+    FS_F16 = 2
+} fs_dtype;
+
 #define FS_MAX_VOCAB 2097152   /* largest supported vocab */
 #define FS_MAX_ROUNDS 256      /* rejection rounds before a row is reported invalid */
 #define FS_NOALLOC_SCRATCH_BYTES (8u << 20)  /* fixed scratch of fs_top_k_top_p_sampling_noalloc */
@@ -351,6 +358,139 @@ fs_status fs_top_k_top_p_sampling_noalloc(const float* probs, int32_t batch_in, 
                                           uint64_t seed, uint64_t offset,
                                           int32_t* out_token, uint8_t* out_valid,
                                           int32_t* out_rounds, void* stream);
+
+/* ------------------------------------------------------------------ the decode step
+ *
+ * The entries below are the steps of a decode loop around the samplers: draw one token
+ * per sample from numbers of the caller's, append the tokens' keys and values to a paged
+ * cache, and attend over a prefix that the samples share and over each sample's own
+ * suffix.  Conventions as above (device pointers, asynchronous on `stream`, any number of
+ * host threads), except:
+ *  - Scratch memory is the caller's: `workspace` holds at least the bytes that the
+ *    ..._workspace_bytes function gives for the same sizes.  Its contents need no
+ *    initialisation and are undefined afterwards.  Two calls, or replays of captured
+ *    graphs, that may run at the same time need workspaces of their own.
+ *  - Strides are in elements and may be any, also negative or 0 for inputs; the last dimension is
+ *    contiguous.  Offsets are 64-bit.  Tensors that are written must not overlap others of the call
+ *    unless stated.
+ *  - The data of tables, lengths and positions is on the device and is not checked by the
+ *    host: what the kernels do with values out of range is stated at each entry; none
+ *    reads or writes outside the tensors given. */
+
+/* Sampling from logits with given random numbers: one number decides each row.
+ * With w_i = exp((z_i - max z) / T) over row b's logits z:
+ *   top-k   keeps z >= t, t the largest threshold with count(z >= t) >= k (ties with the
+ *           k-th are kept);
+ *   top-p   keeps z >= t, t the largest threshold with mass(z >= t) >= top_p * M, M the row's
+ *           mass (FS_ORDER_JOINT) or that of the top k (FS_ORDER_TOP_K_FIRST);
+ *   min-p   keeps w >= min_p;
+ *   token = the first i of the kept set, in index order, with
+ *           sum of w_j over kept j <= i  >  u * sum of w over the kept set.
+ * Decided on 64-bit fixed-point weights (round(2^42 w) within 1 unit and a relative 4e-11),
+ * whose sums are exact: the answer is that of real arithmetic but for numbers u, or masses
+ * at a threshold, within about 10^-10 of a border.  Weights below 2^-43 count as 0.
+ *   logits       [batch_in, vocab] of `dtype`, rows `row_stride` elements apart (>= vocab);
+ *                no alignment beyond the element's
+ *   uniforms     [batch_out] float32 in [0, 1)
+ *   temperature, top_k, top_p, min_p   [batch_out], nullable (1, off, off, off); values as in the conventions above
+ *   indices      nullable, as in the conventions above
+ * A row is invalid (token -1, valid 0) for a NaN or +inf logit, no finite logit, u
+ * outside [0, 1), T below the smallest normal float (1.18e-38) or NaN, NaN top_p or min_p,
+ * min_p > 1, or indices[b] out of range.  T = +inf draws uniformly. */
+fs_status fs_top_k_top_p_sampling_from_uniforms(const void* logits, int32_t dtype, int64_t row_stride,
+                                                int32_t batch_in, int32_t vocab,
+                                                const int32_t* indices, int32_t batch_out,
+                                                const float* uniforms, const float* temperature,
+                                                const int32_t* top_k, const float* top_p,
+                                                const float* min_p, int32_t order,
+                                                int32_t* out_token, uint8_t* out_valid,
+                                                void* workspace, size_t workspace_bytes, void* stream);
+
+/* Workspace of fs_top_k_top_p_sampling_from_uniforms: 4 bytes for every 512 bytes of a row. */
+fs_status fs_from_uniforms_workspace_bytes(int32_t dtype, int32_t batch_in, int32_t vocab, size_t* bytes);
+
+/* A paged cache of keys and values: page i, slot s, head h is the vector of head_dim
+ * elements at k + i * k_strides[0] + s * k_strides[1] + h * k_strides[2] (v alike).  Any order of
+ * slots and heads, and keys and values interleaved in one tensor, are views of this.
+ * A sequence's token t lives in slot t % page_size of the page that its table row names
+ * at t / page_size. */
+typedef struct fs_paged_kv {
+    void* k;
+    void* v;
+    int32_t dtype;      /* fs_dtype */
+    int32_t num_pages;
+    int32_t page_size;  /* any, >= 1 */
+    int32_t num_heads;  /* key/value heads */
+    int32_t head_dim;
+    int64_t k_strides[3];
+    int64_t v_strides[3];
+} fs_paged_kv;
+
+/* Append the keys and values of `tokens` tokens to a paged cache, the keys rotated by
+ * their position on the way; the tokens' queries, if given, are rotated by the same angles.
+ *   key, value     [tokens, num_heads, head_dim] of the cache's type; strides {token, head}
+ *   page_table     [table_rows, table_width] int32, contiguous
+ *   rows           [tokens] int32: token t's table row; nullable (row t; table_rows >= tokens)
+ *   positions      [tokens] int32: the token's place in its table row's pages
+ *   rotary_positions  [tokens] int32: the position that rotates it; nullable (positions).  A
+ *                  sample's suffix has places from 0 on and positions from its prefix's length on
+ *   inv_freq       [rotary_dim / 2] float32, finite: the angle per position of each pair
+ *   rotary_dim     even, <= head_dim, 0 for no rotation; the rest of a head is copied
+ *   interleaved    1: pair i is elements (2i, 2i + 1); 0: (i, i + rotary_dim / 2)
+ *   query          [tokens, q_heads, head_dim], nullable; query_out alike, may be query itself
+ * (x, y) becomes (x cos a - y sin a, y cos a + x sin a) with a = position * inv_freq[i],
+ * reduced exactly for every 32-bit position and rounded once to the type.
+ * A token with positions[t] < 0 is padding: nothing of it is written to the cache, and its
+ * query goes to query_out as it is.  A token whose table row, page entry or page does not
+ * exist (rows[t] or the page out of range, positions[t] beyond the table's width) is not
+ * written to the cache either (its query is rotated).  No two tokens of a call may name
+ * the same slot; if they do, each 16-byte word of it comes from one of them. */
+fs_status fs_append_paged_kv(const fs_paged_kv* cache, const void* key, const int64_t* key_strides,
+                             const void* value, const int64_t* value_strides, int32_t tokens,
+                             const int32_t* page_table, int32_t table_rows, int32_t table_width,
+                             const int32_t* rows, const int32_t* positions,
+                             const int32_t* rotary_positions, const float* inv_freq,
+                             int32_t rotary_dim, int32_t interleaved, const void* query,
+                             const int64_t* query_strides, int32_t q_heads, void* query_out,
+                             const int64_t* query_out_strides, void* stream);
+
+/* Attention of a batch whose rows share long prefixes, over a paged cache:
+ *   out = softmax(scale * q [Kp; Ks]^T) [Vp; Vs],
+ * Kp, Vp the keys and values of the prefix of the row's group, Ks, Vs those of the row's own
+ * suffix.  A prefix is read once for all the queries of its group.
+ *   query, out     [batch, queries, q_heads, head_dim]; strides {row, query, head}.  The
+ *                  `queries` tokens of a row are the last ones of its suffix, in order: token j
+ *                  sees the whole prefix and the first suffix_len - (queries - 1 - j)
+ *                  tokens of the suffix.  Query head h reads key/value head
+ *                  h / (q_heads / num_heads); q_heads is a multiple of num_heads
+ *   group_starts   [groups + 1] int32, not decreasing: rows [group_starts[g], group_starts[g + 1])
+ *                  share prefix g; rows of no group have no prefix.  Nullable when groups <= 1: every row
+ *                  is of group 0
+ *   prefix_table   [groups, prefix_width] int32 pages; prefix_lens [groups] int32 tokens
+ *   suffix_table   [batch, suffix_width] int32 pages; suffix_lens [batch] int32 tokens, the
+ *                  row's own `queries` tokens included
+ *   out_lse        [batch, queries, q_heads] float32, nullable: log of the sum of exp(scale * q k)
+ * Types bf16 and f16, head_dim 64, 128 or 256 (else FS_ERR_UNSUPPORTED); every address, and
+ * every stride in bytes, is a multiple of 16 (else FS_ERR_INVALID_ARG).  Scores, maxima and sums are float32; the weights
+ * enter the product with the values in 16 bits.
+ * Lengths are clamped to what the tables can name (0 .. width * page_size).  A query that sees no
+ * key gives zeros and lse = -inf.  A row that needs a page outside [0, num_pages) gives NaN, and so
+ * does a NaN in a key it sees; keys and values that a query does not see do not reach it. */
+fs_status fs_shared_prefix_attention(const fs_paged_kv* cache, const void* query, const int64_t* query_strides,
+                                     int32_t batch, int32_t queries, int32_t q_heads,
+                                     const int32_t* group_starts, int32_t groups,
+                                     const int32_t* prefix_table, int32_t prefix_width,
+                                     const int32_t* prefix_lens, const int32_t* suffix_table,
+                                     int32_t suffix_width, const int32_t* suffix_lens, float scale,
+                                     void* out, const int64_t* out_strides, float* out_lse,
+                                     void* workspace, size_t workspace_bytes, void* stream);
+
+/* Workspace of fs_shared_prefix_attention for these sizes on the current device: the parts of the
+ * output over the ranges that the keys are cut into. */
+fs_status fs_shared_prefix_attention_workspace_bytes(const fs_paged_kv* cache, int32_t batch,
+                                                     int32_t queries, int32_t q_heads,
+                                                     int32_t groups, int32_t prefix_width,
+                                                     int32_t suffix_width, size_t* bytes);
 
 /* Free every scratch buffer of the library on every device.  Only when no call of
  * this library is in flight on any stream (and no captured graph that uses one will

@@ -23,6 +23,7 @@ __all__ = [
     "top_k_top_p_sampling_pivots", "top_k_top_p_sampling_from_logits", "sampling_plan",
     "chain_speculative_sampling", "top_k_renorm_probs", "top_p_renorm_probs",
     "top_k_mask_logits", "philox4x32_10",
+    "top_k_top_p_sampling_from_uniforms", "append_paged_kv", "shared_prefix_attention",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libfs_sampling.so")
@@ -35,6 +36,17 @@ _I32 = ctypes.c_int32
 _I64 = ctypes.c_int64
 _U64 = ctypes.c_uint64
 
+_SZ = ctypes.c_size_t
+_STRIDES = ctypes.POINTER(ctypes.c_int64)
+
+
+class _PagedKv(ctypes.Structure):
+    """fs_paged_kv."""
+    _fields_ = [("k", _P), ("v", _P), ("dtype", _I32), ("num_pages", _I32), ("page_size", _I32), ("num_heads", _I32),
+                ("head_dim", _I32), ("k_strides", _I64 * 3), ("v_strides", _I64 * 3)]
+
+
+_KV = ctypes.POINTER(_PagedKv)
 _SIGNATURES = {
     "fs_sampling_from_probs": [_P, _I32, _I32, _P, _I32, _U64, _U64, _P, _P, _P, _P],
     "fs_top_k_sampling": [_P, _I32, _I32, _P, _I32, _P, _U64, _U64, _P, _P, _P, _P],
@@ -55,7 +67,16 @@ _SIGNATURES = {
     "fs_top_p_renorm_probs": [_P, _I32, _I32, _P, _P, _P, _P],
     "fs_top_k_mask_logits": [_P, _I32, _I32, _P, _P, _P, _P],
     "fs_philox4x32_10": [_P, _P, _I64, _P, _P],
+    "fs_top_k_top_p_sampling_from_uniforms": [_P, _I32, _I64, _I32, _I32, _P, _I32, _P, _P, _P, _P, _P, _I32, _P, _P,
+                                              _P, _SZ, _P],
+    "fs_from_uniforms_workspace_bytes": [_I32, _I32, _I32, ctypes.POINTER(_SZ)],
+    "fs_append_paged_kv": [_KV, _P, _STRIDES, _P, _STRIDES, _I32, _P, _I32, _I32, _P, _P, _P, _P, _I32, _I32, _P,
+                           _STRIDES, _I32, _P, _STRIDES, _P],
+    "fs_shared_prefix_attention": [_KV, _P, _STRIDES, _I32, _I32, _I32, _P, _I32, _P, _I32, _P, _P, _I32, _P,
+                                   ctypes.c_float, _P, _STRIDES, _P, _P, _SZ, _P],
+    "fs_shared_prefix_attention_workspace_bytes": [_KV, _I32, _I32, _I32, _I32, _I32, _I32, ctypes.POINTER(_SZ)],
 }
+_DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
 
 
 class FsError(RuntimeError):
@@ -377,3 +398,193 @@ def philox4x32_10(ctr: torch.Tensor, key: torch.Tensor) -> torch.Tensor:
     out = torch.empty((ctr.shape[0], 4), dtype=torch.int32, device=ctr.device)
     _run(ctr.device, "fs_philox4x32_10", _ptr(ctr), _ptr(key), ctr.shape[0], _ptr(out))
     return out
+
+
+# ------------------------------------------------------------------ the decode step
+
+def _strides(t: torch.Tensor, n: int):
+    """The first n strides, 0 for a dimension of one element (its stride addresses nothing)."""
+    return (ctypes.c_int64 * n)(*[t.stride(i) if t.shape[i] > 1 else 0 for i in range(n)])
+
+
+def _heads(t, name: str, dims: int, dtype=None, device=None, shape=None) -> torch.Tensor:
+    """A CUDA tensor of vectors: `dims` dimensions, the last one contiguous."""
+    if not isinstance(t, torch.Tensor) or t.dim() != dims:
+        raise ValueError(f"{name} must be a {dims}-D tensor")
+    if not t.is_cuda or t.dtype not in _DTYPES:
+        raise ValueError(f"{name} must be a float32, bfloat16 or float16 CUDA tensor")
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError(f"{name} must be of type {dtype}")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, but the call's tensors are on {device}")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be of shape {tuple(shape)}, not {tuple(t.shape)}")
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name}'s last dimension must be contiguous")
+    return t
+
+
+def _ints(t, name: str, shape, device) -> torch.Tensor:
+    if not (isinstance(t, torch.Tensor) and t.dtype == torch.int32 and t.device == device and t.is_contiguous()
+            and t.dim() == len(shape) and all(w is None or g == w for g, w in zip(t.shape, shape))):
+        want = ", ".join("*" if w is None else str(w) for w in shape)
+        raise ValueError(f"{name} must be a contiguous [{want}] int32 tensor on {device}")
+    return t
+
+
+def _paged_kv(k_cache, v_cache) -> _PagedKv:
+    _heads(k_cache, "k_cache", 4)
+    _heads(v_cache, "v_cache", 4, k_cache.dtype, k_cache.device, k_cache.shape)
+    pages, page, heads, dim = k_cache.shape
+    if page < 1 or heads < 1 or dim < 1:
+        raise ValueError("the caches must be [num_pages, page_size, num_heads, head_dim] with at least one element a page")
+    return _PagedKv(_ptr(k_cache), _ptr(v_cache), _DTYPES[k_cache.dtype], pages, page, heads, dim,
+                    _strides(k_cache, 3), _strides(v_cache, 3))
+
+
+def _workspace(nbytes: int, device) -> Optional[torch.Tensor]:
+    return torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
+
+
+def top_k_top_p_sampling_from_uniforms(logits, uniforms, temperature=None, top_k=None, top_p=None, min_p=None,
+                                       order="joint", indices=None):
+    """One token per output row from logits and one given number each: the first kept token
+    whose running mass exceeds ``uniforms[b]`` times the kept mass (inverse transform over
+    the row filtered by top-k, top-p and min-p at the given temperature).
+
+    logits: [B, V] float32, bfloat16 or float16, rows of any stride >= V.  uniforms: [B_out] float32 in
+    [0, 1).  Returns (tokens int32, valid uint8); a row that cannot be sampled gives -1 and 0."""
+    if not isinstance(logits, torch.Tensor) or logits.dim() != 2:
+        raise ValueError("logits must be a 2-D tensor")
+    if logits.dtype not in _DTYPES or not logits.is_cuda:
+        raise ValueError("logits must be a float32, bfloat16 or float16 CUDA tensor")
+    b_in, V = logits.shape
+    dev = logits.device
+    if V < 1 or (V > 1 and logits.stride(1) != 1) or (b_in > 1 and logits.stride(0) < V):
+        raise ValueError("logits must have at least one column, contiguous columns and rows that do not overlap")
+    indices, b_out = _indices(indices, b_in, dev)
+    if not (isinstance(uniforms, torch.Tensor) and uniforms.dtype == torch.float32 and uniforms.device == dev
+            and tuple(uniforms.shape) == (b_out,) and uniforms.is_contiguous()):
+        raise ValueError(f"uniforms must be a contiguous [{b_out}] float32 tensor on {dev}")
+    ps = [None if v is None else _rows(v, b_out, dt, dev, n)
+          for v, dt, n in ((temperature, torch.float32, "temperature"), (top_k, torch.int32, "top_k"),
+                           (top_p, torch.float32, "top_p"), (min_p, torch.float32, "min_p"))]
+    order = _order(order)
+    dt = _DTYPES[logits.dtype]
+    need = _SZ(0)
+    _check(_lib().fs_from_uniforms_workspace_bytes(dt, b_in, V, ctypes.byref(need)))
+    ws = _workspace(need.value, dev)
+    tok = torch.empty(b_out, dtype=torch.int32, device=dev)
+    valid = torch.empty(b_out, dtype=torch.uint8, device=dev)
+    _run(dev, "fs_top_k_top_p_sampling_from_uniforms", _ptr(logits), dt, logits.stride(0) if b_in > 1 else V, b_in, V,
+         _ptr(indices), b_out, _ptr(uniforms), *[_ptr(t) for t in ps], order, _ptr(tok), _ptr(valid), _ptr(ws),
+         need.value)
+    return tok, valid
+
+
+def append_paged_kv(key, value, k_cache, v_cache, page_table, positions, rows=None, *, rotary_positions=None,
+                    inv_freq=None, interleaved=False, query=None, query_out=None):
+    """Append keys and values to a paged cache, the keys rotated by their positions on the
+    way, and rotate the tokens' queries by the same angles.
+
+    key, value: [N, heads, dim]; k_cache, v_cache: [pages, page_size, heads, dim], any
+    strides with a contiguous last dimension (pass ``cache.transpose(1, 2)`` for pages laid
+    out heads first).  page_table: [R, width] int32; positions: [N] int32, the token's place in its table
+    row (negative: padding, skipped); rows: [N] int32, the token's table row (default: row t).
+    rotary_positions: [N] int32 (default: positions); inv_freq: [r / 2] float32 rotates the
+    first r elements of each head, in halves or, with ``interleaved``, in neighbouring pairs (None: no
+    rotation).  query: [N, q_heads, dim] is rotated into query_out (default: a new tensor; may be query itself),
+    which is returned (None without a query)."""
+    kv = _paged_kv(k_cache, v_cache)
+    dev, dtype = k_cache.device, k_cache.dtype
+    _heads(key, "key", 3, dtype, dev)
+    n = key.shape[0]
+    _heads(key, "key", 3, dtype, dev, (n, kv.num_heads, kv.head_dim))
+    _heads(value, "value", 3, dtype, dev, (n, kv.num_heads, kv.head_dim))
+    _ints(page_table, "page_table", (None, None), dev)
+    _ints(positions, "positions", (n,), dev)
+    if rows is None:
+        if page_table.shape[0] < n:
+            raise ValueError("page_table needs a row for every token when rows is not given")
+    else:
+        _ints(rows, "rows", (n,), dev)
+    if rotary_positions is not None:
+        _ints(rotary_positions, "rotary_positions", (n,), dev)
+    rotary = 0
+    if inv_freq is not None:
+        if not (isinstance(inv_freq, torch.Tensor) and inv_freq.dim() == 1 and inv_freq.dtype == torch.float32
+                and inv_freq.device == dev and inv_freq.is_contiguous()):
+            raise ValueError(f"inv_freq must be a contiguous 1-D float32 tensor on {dev}")
+        rotary = 2 * inv_freq.shape[0]
+        if rotary > kv.head_dim:
+            raise ValueError("inv_freq has more pairs than a head")
+    q_heads, qs, qos = 0, None, None
+    if query is not None:
+        _heads(query, "query", 3, dtype, dev)
+        q_heads = query.shape[1]
+        _heads(query, "query", 3, dtype, dev, (n, q_heads, kv.head_dim))
+        if q_heads < 1:
+            raise ValueError("query must have at least one head")
+        query_out = torch.empty(query.shape, dtype=dtype, device=dev) if query_out is None else \
+            _heads(query_out, "query_out", 3, dtype, dev, query.shape)
+        qs, qos = _strides(query, 2), _strides(query_out, 2)
+    elif query_out is not None:
+        raise ValueError("query_out needs a query")
+    _run(dev, "fs_append_paged_kv", ctypes.byref(kv), _ptr(key), _strides(key, 2), _ptr(value), _strides(value, 2), n,
+         _ptr(page_table), page_table.shape[0], page_table.shape[1], _ptr(rows), _ptr(positions),
+         _ptr(rotary_positions), _ptr(inv_freq), rotary, int(bool(interleaved)), _ptr(query), qs, q_heads,
+         _ptr(query_out), qos)
+    return query_out
+
+
+def shared_prefix_attention(query, k_cache, v_cache, prefix_table, prefix_lens, suffix_table, suffix_lens,
+                            group_starts=None, *, scale=None, out=None, return_lse=False):
+    """Attention of a batch whose rows share long prefixes, over a paged cache; each prefix
+    is computed once for all queries of its group.
+
+    query: [B, heads, dim], or [B, Q, heads, dim] for the last Q tokens of each row's suffix (causal among
+    them); k_cache, v_cache: [pages, page_size, kv_heads, dim] bfloat16 or float16, dim 64, 128 or 256.  prefix_table [G, w]
+    and prefix_lens [G] int32 name the prefixes (None: there are none), suffix_table [B, w] and suffix_lens [B]
+    int32 the rows' own tokens; group_starts [G + 1] int32: rows group_starts[g] up to
+    group_starts[g + 1] share prefix g (default: one prefix for all).  scale defaults to dim ** -0.5.
+    Returns out (query's shape), and with return_lse the log of the sum of exponentials,
+    float32 [B, (Q,) heads]."""
+    kv = _paged_kv(k_cache, v_cache)
+    dev, dtype = k_cache.device, k_cache.dtype
+    if not isinstance(query, torch.Tensor) or query.dim() not in (3, 4):
+        raise ValueError("query must be a 3-D or 4-D tensor")
+    one = query.dim() == 3
+    _heads(query, "query", query.dim(), dtype, dev)
+    out = torch.empty(query.shape, dtype=dtype, device=dev) if out is None else \
+        _heads(out, "out", query.dim(), dtype, dev, query.shape)
+    q4, o4 = (query.unsqueeze(1), out.unsqueeze(1)) if one else (query, out)
+    B, Q, Hq, D = q4.shape
+    if D != kv.head_dim or Q < 1 or Hq < 1 or Hq % kv.num_heads:
+        raise ValueError("query must have the caches' head size, at least one token, and a multiple of their heads")
+    G, pw = 0, 0
+    if prefix_table is not None:
+        _ints(prefix_table, "prefix_table", (None, None), dev)
+        G, pw = prefix_table.shape
+        _ints(prefix_lens, "prefix_lens", (G,), dev)
+    elif prefix_lens is not None or group_starts is not None:
+        raise ValueError("prefix_lens and group_starts need a prefix_table")
+    if group_starts is not None:
+        _ints(group_starts, "group_starts", (G + 1,), dev)
+    elif G > 1:
+        raise ValueError("several prefixes need group_starts")
+    _ints(suffix_table, "suffix_table", (B, None), dev)
+    _ints(suffix_lens, "suffix_lens", (B,), dev)
+    lse = torch.empty(q4.shape[:3], dtype=torch.float32, device=dev) if return_lse else None
+    sw = suffix_table.shape[1]
+    need = _SZ(0)
+    with torch.cuda.device(dev):
+        _check(_lib().fs_shared_prefix_attention_workspace_bytes(ctypes.byref(kv), B, Q, Hq, G, pw, sw,
+                                                                 ctypes.byref(need)))
+    ws = _workspace(need.value, dev)
+    _run(dev, "fs_shared_prefix_attention", ctypes.byref(kv), _ptr(query), _strides(q4, 3), B, Q, Hq,
+         _ptr(group_starts), G, _ptr(prefix_table), pw, _ptr(prefix_lens), _ptr(suffix_table), sw, _ptr(suffix_lens),
+         float(D) ** -0.5 if scale is None else float(scale), _ptr(out), _strides(o4, 3), _ptr(lse), _ptr(ws),
+         need.value)
+    if not return_lse:
+        return out
+    return out, (lse[:, 0] if one else lse)

@@ -11,7 +11,9 @@ been built (``python -m min_sampling_gb300.build``).
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
+import struct
 from typing import Optional, Union
 
 import torch
@@ -37,16 +39,6 @@ _I64 = ctypes.c_int64
 _U64 = ctypes.c_uint64
 
 _SZ = ctypes.c_size_t
-_STRIDES = ctypes.POINTER(ctypes.c_int64)
-
-
-class _PagedKv(ctypes.Structure):
-    """fs_paged_kv."""
-    _fields_ = [("k", _P), ("v", _P), ("dtype", _I32), ("num_pages", _I32), ("page_size", _I32), ("num_heads", _I32),
-                ("head_dim", _I32), ("k_strides", _I64 * 3), ("v_strides", _I64 * 3)]
-
-
-_KV = ctypes.POINTER(_PagedKv)
 _SIGNATURES = {
     "fs_sampling_from_probs": [_P, _I32, _I32, _P, _I32, _U64, _U64, _P, _P, _P, _P],
     "fs_top_k_sampling": [_P, _I32, _I32, _P, _I32, _P, _U64, _U64, _P, _P, _P, _P],
@@ -70,11 +62,11 @@ _SIGNATURES = {
     "fs_top_k_top_p_sampling_from_uniforms": [_P, _I32, _I64, _I32, _I32, _P, _I32, _P, _P, _P, _P, _P, _I32, _P, _P,
                                               _P, _SZ, _P],
     "fs_from_uniforms_workspace_bytes": [_I32, _I32, _I32, ctypes.POINTER(_SZ)],
-    "fs_append_paged_kv": [_KV, _P, _STRIDES, _P, _STRIDES, _I32, _P, _I32, _I32, _P, _P, _P, _P, _I32, _I32, _P,
-                           _STRIDES, _I32, _P, _STRIDES, _P],
-    "fs_shared_prefix_attention": [_KV, _P, _STRIDES, _I32, _I32, _I32, _P, _I32, _P, _I32, _P, _P, _I32, _P,
-                                   ctypes.c_float, _P, _STRIDES, _P, _P, _SZ, _P],
-    "fs_shared_prefix_attention_workspace_bytes": [_KV, _I32, _I32, _I32, _I32, _I32, _I32, ctypes.POINTER(_SZ)],
+    "fs_append_paged_kv": [_P, _P, _P, _P, _P, _I32, _P, _I32, _I32, _P, _P, _P, _P, _I32, _I32, _P, _P, _I32, _P, _P,
+                           _P],
+    "fs_shared_prefix_attention": [_P, _P, _P, _I32, _I32, _I32, _P, _I32, _P, _I32, _P, _P, _I32, _P,
+                                   ctypes.c_float, _P, _P, _P, _P, _SZ, _P],
+    "fs_shared_prefix_attention_workspace_bytes": [_P, _I32, _I32, _I32, _I32, _I32, _I32, ctypes.POINTER(_SZ)],
 }
 _DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
 
@@ -401,49 +393,77 @@ def philox4x32_10(ctr: torch.Tensor, key: torch.Tensor) -> torch.Tensor:
 
 
 # ------------------------------------------------------------------ the decode step
+#
+# These entries run once or more per generated token, often on a few rows, where the
+# host's own time decides: checks read each attribute once, pointers travel as plain
+# integers and structures and strides as packed bytes (the header's layout).
 
-def _strides(t: torch.Tensor, n: int):
-    """The first n strides, 0 for a dimension of one element (its stride addresses nothing)."""
-    return (ctypes.c_int64 * n)(*[t.stride(i) if t.shape[i] > 1 else 0 for i in range(n)])
+_PAGED_KV = struct.Struct("@PPiiiii6q")   # fs_paged_kv
+_S2, _S3 = struct.Struct("@2q"), struct.Struct("@3q")
 
 
-def _heads(t, name: str, dims: int, dtype=None, device=None, shape=None) -> torch.Tensor:
-    """A CUDA tensor of vectors: `dims` dimensions, the last one contiguous."""
-    if not isinstance(t, torch.Tensor) or t.dim() != dims:
-        raise ValueError(f"{name} must be a {dims}-D tensor")
-    if not t.is_cuda or t.dtype not in _DTYPES:
+def _launch(fn: str, idx: int, *args) -> None:
+    """Call a library entry on device `idx`, made current, and its current stream."""
+    f = getattr(_lib(), fn)
+    if torch.cuda.current_device() == idx:
+        status = f(*args, torch._C._cuda_getCurrentRawStream(idx))
+    else:
+        with torch.cuda.device(idx):
+            status = f(*args, torch._C._cuda_getCurrentRawStream(idx))
+    if status:
+        _check(status)
+
+
+def _float_cuda(t, name: str, dims) -> int:
+    """The device index of a CUDA tensor of a type the entries take."""
+    if not isinstance(t, torch.Tensor) or t.dim() not in dims:
+        raise ValueError(f"{name} must be a {' or '.join(f'{d}-D' for d in dims)} tensor")
+    if t.dtype not in _DTYPES or not t.is_cuda:
         raise ValueError(f"{name} must be a float32, bfloat16 or float16 CUDA tensor")
-    if dtype is not None and t.dtype != dtype:
-        raise ValueError(f"{name} must be of type {dtype}")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name} is on {t.device}, but the call's tensors are on {device}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must be of shape {tuple(shape)}, not {tuple(t.shape)}")
-    if t.shape[-1] > 1 and t.stride(-1) != 1:
+    return t.get_device()
+
+
+def _strides(shape, st):
+    """Strides, 0 for a dimension of one element (its stride addresses nothing)."""
+    return st if 1 not in shape else tuple(0 if n == 1 else v for n, v in zip(shape, st))
+
+
+def _vectors(t, name: str, shape, dtype, idx: int):
+    """Strides of a tensor of vectors (contiguous last dimension) of the given shape, type and device."""
+    if not (isinstance(t, torch.Tensor) and t.shape == shape and t.dtype is dtype and t.get_device() == idx):
+        raise ValueError(f"{name} must be a {list(shape)} {dtype} tensor on cuda:{idx}")
+    st = t.stride()
+    if st[-1] != 1 and shape[-1] > 1:
         raise ValueError(f"{name}'s last dimension must be contiguous")
-    return t
+    return _strides(shape, st)
 
 
-def _ints(t, name: str, shape, device) -> torch.Tensor:
-    if not (isinstance(t, torch.Tensor) and t.dtype == torch.int32 and t.device == device and t.is_contiguous()
-            and t.dim() == len(shape) and all(w is None or g == w for g, w in zip(t.shape, shape))):
-        want = ", ".join("*" if w is None else str(w) for w in shape)
-        raise ValueError(f"{name} must be a contiguous [{want}] int32 tensor on {device}")
-    return t
+def _flat(t, name: str, shape, dtype, idx: int) -> int:
+    """The address of a contiguous tensor of the given shape, type and device."""
+    if not (isinstance(t, torch.Tensor) and t.shape == shape and t.dtype is dtype and t.get_device() == idx
+            and t.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous {list(shape)} {dtype} tensor on cuda:{idx}")
+    return t.data_ptr()
 
 
-def _paged_kv(k_cache, v_cache) -> _PagedKv:
-    _heads(k_cache, "k_cache", 4)
-    _heads(v_cache, "v_cache", 4, k_cache.dtype, k_cache.device, k_cache.shape)
-    pages, page, heads, dim = k_cache.shape
+def _table(t, name: str, rows, idx: int):
+    """Address, rows and width of a page table."""
+    if not (isinstance(t, torch.Tensor) and t.dim() == 2 and t.dtype is torch.int32 and t.get_device() == idx
+            and t.is_contiguous() and (rows is None or t.shape[0] == rows)):
+        raise ValueError(f"{name} must be a contiguous [{'*' if rows is None else rows}, *] int32 tensor on cuda:{idx}")
+    return t.data_ptr(), *t.shape
+
+
+def _paged_kv(k_cache, v_cache):
+    """(packed fs_paged_kv, its shape, type and device index)."""
+    idx = _float_cuda(k_cache, "k_cache", (4,))
+    shape, dtype = k_cache.shape, k_cache.dtype
+    pages, page, heads, dim = shape
     if page < 1 or heads < 1 or dim < 1:
         raise ValueError("the caches must be [num_pages, page_size, num_heads, head_dim] with at least one element a page")
-    return _PagedKv(_ptr(k_cache), _ptr(v_cache), _DTYPES[k_cache.dtype], pages, page, heads, dim,
-                    _strides(k_cache, 3), _strides(v_cache, 3))
-
-
-def _workspace(nbytes: int, device) -> Optional[torch.Tensor]:
-    return torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
+    ks, vs = _vectors(k_cache, "k_cache", shape, dtype, idx), _vectors(v_cache, "v_cache", shape, dtype, idx)
+    return (_PAGED_KV.pack(k_cache.data_ptr(), v_cache.data_ptr(), _DTYPES[dtype], pages, page, heads, dim, *ks[:3],
+                           *vs[:3]), shape, dtype, idx)
 
 
 def top_k_top_p_sampling_from_uniforms(logits, uniforms, temperature=None, top_k=None, top_p=None, min_p=None,
@@ -454,32 +474,41 @@ def top_k_top_p_sampling_from_uniforms(logits, uniforms, temperature=None, top_k
 
     logits: [B, V] float32, bfloat16 or float16, rows of any stride >= V.  uniforms: [B_out] float32 in
     [0, 1).  Returns (tokens int32, valid uint8); a row that cannot be sampled gives -1 and 0."""
-    if not isinstance(logits, torch.Tensor) or logits.dim() != 2:
-        raise ValueError("logits must be a 2-D tensor")
-    if logits.dtype not in _DTYPES or not logits.is_cuda:
-        raise ValueError("logits must be a float32, bfloat16 or float16 CUDA tensor")
+    idx = _float_cuda(logits, "logits", (2,))
     b_in, V = logits.shape
-    dev = logits.device
-    if V < 1 or (V > 1 and logits.stride(1) != 1) or (b_in > 1 and logits.stride(0) < V):
+    stride, col = logits.stride()
+    if V < 1 or (V > 1 and col != 1) or (b_in > 1 and stride < V):
         raise ValueError("logits must have at least one column, contiguous columns and rows that do not overlap")
+    dev = logits.device
     indices, b_out = _indices(indices, b_in, dev)
-    if not (isinstance(uniforms, torch.Tensor) and uniforms.dtype == torch.float32 and uniforms.device == dev
-            and tuple(uniforms.shape) == (b_out,) and uniforms.is_contiguous()):
-        raise ValueError(f"uniforms must be a contiguous [{b_out}] float32 tensor on {dev}")
-    ps = [None if v is None else _rows(v, b_out, dt, dev, n)
-          for v, dt, n in ((temperature, torch.float32, "temperature"), (top_k, torch.int32, "top_k"),
-                           (top_p, torch.float32, "top_p"), (min_p, torch.float32, "min_p"))]
-    order = _order(order)
+    n = (b_out,)
+    u = _flat(uniforms, "uniforms", n, torch.float32, idx)
+    held, ptrs = [], []
+    for v, dt, name in ((temperature, torch.float32, "temperature"), (top_k, torch.int32, "top_k"),
+                        (top_p, torch.float32, "top_p"), (min_p, torch.float32, "min_p")):
+        if v is None:
+            ptrs.append(None)
+            continue
+        if not isinstance(v, torch.Tensor):
+            v = torch.full(n, v, dtype=dt, device=dev)
+            held.append(v)
+        ptrs.append(_flat(v, name, n, dt, idx))
     dt = _DTYPES[logits.dtype]
-    need = _SZ(0)
-    _check(_lib().fs_from_uniforms_workspace_bytes(dt, b_in, V, ctypes.byref(need)))
-    ws = _workspace(need.value, dev)
-    tok = torch.empty(b_out, dtype=torch.int32, device=dev)
-    valid = torch.empty(b_out, dtype=torch.uint8, device=dev)
-    _run(dev, "fs_top_k_top_p_sampling_from_uniforms", _ptr(logits), dt, logits.stride(0) if b_in > 1 else V, b_in, V,
-         _ptr(indices), b_out, _ptr(uniforms), *[_ptr(t) for t in ps], order, _ptr(tok), _ptr(valid), _ptr(ws),
-         need.value)
+    need = _uniforms_bytes(dt, b_in, V)
+    ws = torch.empty(need, dtype=torch.uint8, device=dev)
+    tok = torch.empty(n, dtype=torch.int32, device=dev)
+    valid = torch.empty(n, dtype=torch.uint8, device=dev)
+    _launch("fs_top_k_top_p_sampling_from_uniforms", idx, logits.data_ptr(), dt, stride if b_in > 1 else V, b_in, V,
+            None if indices is None else indices.data_ptr(), b_out, u, *ptrs, _order(order), tok.data_ptr(),
+            valid.data_ptr(), ws.data_ptr(), need)
     return tok, valid
+
+
+@functools.lru_cache(maxsize=256)
+def _uniforms_bytes(dtype: int, b_in: int, V: int) -> int:
+    need = _SZ(0)
+    _check(_lib().fs_from_uniforms_workspace_bytes(dtype, b_in, V, ctypes.byref(need)))
+    return need.value
 
 
 def append_paged_kv(key, value, k_cache, v_cache, page_table, positions, rows=None, *, rotary_positions=None,
@@ -495,45 +524,38 @@ def append_paged_kv(key, value, k_cache, v_cache, page_table, positions, rows=No
     first r elements of each head, in halves or, with ``interleaved``, in neighbouring pairs (None: no
     rotation).  query: [N, q_heads, dim] is rotated into query_out (default: a new tensor; may be query itself),
     which is returned (None without a query)."""
-    kv = _paged_kv(k_cache, v_cache)
-    dev, dtype = k_cache.device, k_cache.dtype
-    _heads(key, "key", 3, dtype, dev)
-    n = key.shape[0]
-    _heads(key, "key", 3, dtype, dev, (n, kv.num_heads, kv.head_dim))
-    _heads(value, "value", 3, dtype, dev, (n, kv.num_heads, kv.head_dim))
-    _ints(page_table, "page_table", (None, None), dev)
-    _ints(positions, "positions", (n,), dev)
-    if rows is None:
-        if page_table.shape[0] < n:
-            raise ValueError("page_table needs a row for every token when rows is not given")
-    else:
-        _ints(rows, "rows", (n,), dev)
-    if rotary_positions is not None:
-        _ints(rotary_positions, "rotary_positions", (n,), dev)
-    rotary = 0
+    kv, (_, _, heads, dim), dtype, idx = _paged_kv(k_cache, v_cache)
+    n = key.shape[0] if isinstance(key, torch.Tensor) and key.dim() == 3 else 0
+    ks = _vectors(key, "key", (n, heads, dim), dtype, idx)
+    vs = _vectors(value, "value", (n, heads, dim), dtype, idx)
+    table, table_rows, width = _table(page_table, "page_table", None, idx)
+    pos = _flat(positions, "positions", (n,), torch.int32, idx)
+    if rows is None and table_rows < n:
+        raise ValueError("page_table needs a row for every token when rows is not given")
+    row = None if rows is None else _flat(rows, "rows", (n,), torch.int32, idx)
+    rpos = None if rotary_positions is None else _flat(rotary_positions, "rotary_positions", (n,), torch.int32, idx)
+    freq, rotary = None, 0
     if inv_freq is not None:
-        if not (isinstance(inv_freq, torch.Tensor) and inv_freq.dim() == 1 and inv_freq.dtype == torch.float32
-                and inv_freq.device == dev and inv_freq.is_contiguous()):
-            raise ValueError(f"inv_freq must be a contiguous 1-D float32 tensor on {dev}")
+        freq = _flat(inv_freq, "inv_freq", inv_freq.shape[:1] if isinstance(inv_freq, torch.Tensor) else (), torch.float32,
+                     idx)
         rotary = 2 * inv_freq.shape[0]
-        if rotary > kv.head_dim:
+        if rotary > dim:
             raise ValueError("inv_freq has more pairs than a head")
-    q_heads, qs, qos = 0, None, None
+    q, qs, qo, qos, q_heads = None, None, None, None, 0
     if query is not None:
-        _heads(query, "query", 3, dtype, dev)
-        q_heads = query.shape[1]
-        _heads(query, "query", 3, dtype, dev, (n, q_heads, kv.head_dim))
+        q_heads = query.shape[1] if isinstance(query, torch.Tensor) and query.dim() == 3 else 1
+        shape = (n, q_heads, dim)
+        qs = _S2.pack(*_vectors(query, "query", shape, dtype, idx)[:2])
         if q_heads < 1:
             raise ValueError("query must have at least one head")
-        query_out = torch.empty(query.shape, dtype=dtype, device=dev) if query_out is None else \
-            _heads(query_out, "query_out", 3, dtype, dev, query.shape)
-        qs, qos = _strides(query, 2), _strides(query_out, 2)
+        if query_out is None:
+            query_out = torch.empty(shape, dtype=dtype, device=key.device)
+        qos = _S2.pack(*_vectors(query_out, "query_out", shape, dtype, idx)[:2])
+        q, qo = query.data_ptr(), query_out.data_ptr()
     elif query_out is not None:
         raise ValueError("query_out needs a query")
-    _run(dev, "fs_append_paged_kv", ctypes.byref(kv), _ptr(key), _strides(key, 2), _ptr(value), _strides(value, 2), n,
-         _ptr(page_table), page_table.shape[0], page_table.shape[1], _ptr(rows), _ptr(positions),
-         _ptr(rotary_positions), _ptr(inv_freq), rotary, int(bool(interleaved)), _ptr(query), qs, q_heads,
-         _ptr(query_out), qos)
+    _launch("fs_append_paged_kv", idx, kv, key.data_ptr(), _S2.pack(*ks[:2]), value.data_ptr(), _S2.pack(*vs[:2]), n,
+            table, table_rows, width, row, pos, rpos, freq, rotary, 1 if interleaved else 0, q, qs, q_heads, qo, qos)
     return query_out
 
 
@@ -549,42 +571,46 @@ def shared_prefix_attention(query, k_cache, v_cache, prefix_table, prefix_lens, 
     group_starts[g + 1] share prefix g (default: one prefix for all).  scale defaults to dim ** -0.5.
     Returns out (query's shape), and with return_lse the log of the sum of exponentials,
     float32 [B, (Q,) heads]."""
-    kv = _paged_kv(k_cache, v_cache)
-    dev, dtype = k_cache.device, k_cache.dtype
-    if not isinstance(query, torch.Tensor) or query.dim() not in (3, 4):
-        raise ValueError("query must be a 3-D or 4-D tensor")
-    one = query.dim() == 3
-    _heads(query, "query", query.dim(), dtype, dev)
-    out = torch.empty(query.shape, dtype=dtype, device=dev) if out is None else \
-        _heads(out, "out", query.dim(), dtype, dev, query.shape)
-    q4, o4 = (query.unsqueeze(1), out.unsqueeze(1)) if one else (query, out)
-    B, Q, Hq, D = q4.shape
-    if D != kv.head_dim or Q < 1 or Hq < 1 or Hq % kv.num_heads:
+    kv, (_, page, heads, dim), dtype, idx = _paged_kv(k_cache, v_cache)
+    _float_cuda(query, "query", (3, 4))
+    shape, dev = query.shape, query.device
+    qs = _vectors(query, "query", shape, dtype, idx)
+    if out is None:
+        out = torch.empty(shape, dtype=dtype, device=dev)
+    os_ = _vectors(out, "out", shape, dtype, idx)
+    if len(shape) == 3:
+        (B, Hq, D), Q = shape, 1
+        qs, os_ = (qs[0], 0, qs[1]), (os_[0], 0, os_[1])
+    else:
+        B, Q, Hq, D = shape
+    if D != dim or Q < 1 or Hq < 1 or Hq % heads:
         raise ValueError("query must have the caches' head size, at least one token, and a multiple of their heads")
-    G, pw = 0, 0
+    G, pw, ptab, plens, starts = 0, 0, None, None, None
     if prefix_table is not None:
-        _ints(prefix_table, "prefix_table", (None, None), dev)
-        G, pw = prefix_table.shape
-        _ints(prefix_lens, "prefix_lens", (G,), dev)
+        ptab, G, pw = _table(prefix_table, "prefix_table", None, idx)
+        plens = _flat(prefix_lens, "prefix_lens", (G,), torch.int32, idx)
     elif prefix_lens is not None or group_starts is not None:
         raise ValueError("prefix_lens and group_starts need a prefix_table")
     if group_starts is not None:
-        _ints(group_starts, "group_starts", (G + 1,), dev)
+        starts = _flat(group_starts, "group_starts", (G + 1,), torch.int32, idx)
     elif G > 1:
         raise ValueError("several prefixes need group_starts")
-    _ints(suffix_table, "suffix_table", (B, None), dev)
-    _ints(suffix_lens, "suffix_lens", (B,), dev)
-    lse = torch.empty(q4.shape[:3], dtype=torch.float32, device=dev) if return_lse else None
-    sw = suffix_table.shape[1]
+    stab, _, sw = _table(suffix_table, "suffix_table", B, idx)
+    slens = _flat(suffix_lens, "suffix_lens", (B,), torch.int32, idx)
+    lse = torch.empty(shape[:-1], dtype=torch.float32, device=dev) if return_lse else None
+    need = _attention_bytes(idx, _DTYPES[dtype], page, heads, dim, B, Q, Hq, G, pw, sw)
+    ws = torch.empty(need, dtype=torch.uint8, device=dev)
+    _launch("fs_shared_prefix_attention", idx, kv, query.data_ptr(), _S3.pack(*qs[:3]), B, Q, Hq, starts, G, ptab, pw,
+            plens, stab, sw, slens, dim ** -0.5 if scale is None else scale, out.data_ptr(), _S3.pack(*os_[:3]),
+            None if lse is None else lse.data_ptr(), ws.data_ptr(), need)
+    return (out, lse) if return_lse else out
+
+
+@functools.lru_cache(maxsize=256)
+def _attention_bytes(idx: int, dtype: int, page: int, heads: int, dim: int, B: int, Q: int, Hq: int, G: int, pw: int,
+                     sw: int) -> int:
     need = _SZ(0)
-    with torch.cuda.device(dev):
-        _check(_lib().fs_shared_prefix_attention_workspace_bytes(ctypes.byref(kv), B, Q, Hq, G, pw, sw,
-                                                                 ctypes.byref(need)))
-    ws = _workspace(need.value, dev)
-    _run(dev, "fs_shared_prefix_attention", ctypes.byref(kv), _ptr(query), _strides(q4, 3), B, Q, Hq,
-         _ptr(group_starts), G, _ptr(prefix_table), pw, _ptr(prefix_lens), _ptr(suffix_table), sw, _ptr(suffix_lens),
-         float(D) ** -0.5 if scale is None else float(scale), _ptr(out), _strides(o4, 3), _ptr(lse), _ptr(ws),
-         need.value)
-    if not return_lse:
-        return out
-    return out, (lse[:, 0] if one else lse)
+    kv = _PAGED_KV.pack(0, 0, dtype, 0, page, heads, dim, 0, 0, 0, 0, 0, 0)
+    with torch.cuda.device(idx):
+        _check(_lib().fs_shared_prefix_attention_workspace_bytes(kv, B, Q, Hq, G, pw, sw, ctypes.byref(need)))
+    return need.value

@@ -17,11 +17,11 @@ def ms():
 
 
 def _kv(ms, k=0x1000, v=0x1000, dtype=1, pages=4, page=16, heads=2, dim=64, ks=(2048, 128, 64), vs=(2048, 128, 64)):
-    return ms._PagedKv(k, v, dtype, pages, page, heads, dim, (ctypes.c_int64 * 3)(*ks), (ctypes.c_int64 * 3)(*vs))
+    return ms._PAGED_KV.pack(k or 0, v or 0, dtype, pages, page, heads, dim, *ks, *vs)
 
 
 def _s(*v):
-    return (ctypes.c_int64 * len(v))(*v)
+    return (ctypes.c_int64 * len(v))(*v) if v else None
 
 
 def test_uniforms_arguments(ms):
@@ -46,7 +46,7 @@ def test_append_arguments(ms):
     def call(kv=None, key=FAKE, value=FAKE, n=3, table=FAKE, R=4, w=2, rows=FAKE, pos=FAKE, inv=FAKE, rotary=64, inter=0,
              q=FAKE, hq=4, qo=FAKE, ks=_s(128, 64), qs=_s(256, 64)):
         kv = _kv(ms) if kv is None else kv
-        return ms.lib.fs_append_paged_kv(ctypes.byref(kv), key, ks, value, _s(128, 64), n, table, R, w, rows, pos, None, inv,
+        return ms.lib.fs_append_paged_kv(kv, key, ks, value, _s(128, 64), n, table, R, w, rows, pos, None, inv,
                                          rotary, inter, q, qs, hq, qo, _s(256, 64), None)
     assert call(key=None) == 1 and call(value=None) == 1 and call(pos=None) == 1 and call(inv=None) == 1
     assert call(table=None) == 1 and call(ks=None) == 1 and call(qs=None) == 1 and call(qo=None) == 1 and call(hq=0) == 1
@@ -63,7 +63,7 @@ def test_attention_arguments(ms):
     def call(kv=None, q=FAKE, qs=_s(512, 512, 64), B=4, Q=1, hq=4, starts=FAKE, G=2, ptab=FAKE, pw=4, pl=FAKE, stab=FAKE,
              sw=2, sl=FAKE, out=FAKE, os=_s(512, 512, 64)):
         kv = _kv(ms) if kv is None else kv
-        return ms.lib.fs_shared_prefix_attention(ctypes.byref(kv), q, qs, B, Q, hq, starts, G, ptab, pw, pl, stab, sw, sl,
+        return ms.lib.fs_shared_prefix_attention(kv, q, qs, B, Q, hq, starts, G, ptab, pw, pl, stab, sw, sl,
                                                  1.0, out, os, None, FAKE, 0, None)
     assert call(q=None) == 1 and call(out=None) == 1 and call(qs=None) == 1 and call(os=None) == 1
     assert call(ptab=None) == 1 and call(pl=None) == 1 and call(stab=None) == 1 and call(sl=None) == 1
@@ -93,10 +93,15 @@ def test_binding_refuses(ms):
         ms.append_paged_kv(f(1, 2, 64), f(1, 2, 64), kc[0], kc[0], i(1, 1), i(1))
     with pytest.raises(ValueError, match="CUDA"):
         ms.shared_prefix_attention(f(1, 4, 64), kc, kc, i(1, 1), i(1), i(1, 1), i(1))
-    cpu = torch.device("cpu")
-    assert ms._ints(i(2, 3), "t", (2, None), cpu) is not None
-    for bad in (i(2), i(3, 2).t(), i(2, 3).long(), i(1, 3), [1], i(2, 3).to("meta")):
+    for bad in (i(2), i(3, 2).t(), i(2, 3).long(), i(1, 3), [1], None):
         with pytest.raises(ValueError, match="int32"):
-            ms._ints(bad, "t", (2, None), cpu)
+            ms._table(bad, "t", 2, -1)
+    assert ms._table(i(2, 3), "t", 2, -1)[1:] == (2, 3)    # -1 stands for the device here: a CPU tensor's index
+    for bad in (i(3), i(2).long(), i(4)[::2], i(2, 1), 5):
+        with pytest.raises(ValueError, match="contiguous"):
+            ms._flat(bad, "x", (2,), torch.int32, -1)
+    for bad in (f(3, 4), f(2, 4).half(), f(2, 8)[:, ::2], None):
+        with pytest.raises(ValueError):
+            ms._vectors(bad, "x", (2, 4), torch.float32, -1)
     # strides of dimensions of one element address nothing
-    assert list(ms._strides(torch.empty_strided((1, 3, 4), (5, 4, 1)), 2)) == [0, 4]
+    assert ms._vectors(torch.empty_strided((1, 3, 4), (5, 4, 1)), "x", (1, 3, 4), torch.float32, -1) == (0, 4, 1)

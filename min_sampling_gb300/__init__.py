@@ -1,7 +1,8 @@
 """Sorting-free top-k / top-p / min-p sampling on GB300 (sm_103a).
 
 Thin Python binding of ``libfs_sampling.so`` (C ABI declared in
-``include/fs_sampling.h``).  This module only marshals arguments: it checks
+``include/fs_sampling.h``; the decode step's entries through the compiled ``_decode``).
+This module only marshals arguments: it checks
 tensor shapes, dtypes and devices, turns scalar parameters into per-row device
 arrays, and passes raw device pointers and the current CUDA stream to the library.
 Every step of the computation runs in the library's CUDA kernels; there is no
@@ -11,9 +12,7 @@ been built (``python -m min_sampling_gb300.build``).
 from __future__ import annotations
 
 import ctypes
-import functools
 import os
-import struct
 from typing import Optional, Union
 
 import torch
@@ -38,7 +37,6 @@ _I32 = ctypes.c_int32
 _I64 = ctypes.c_int64
 _U64 = ctypes.c_uint64
 
-_SZ = ctypes.c_size_t
 _SIGNATURES = {
     "fs_sampling_from_probs": [_P, _I32, _I32, _P, _I32, _U64, _U64, _P, _P, _P, _P],
     "fs_top_k_sampling": [_P, _I32, _I32, _P, _I32, _P, _U64, _U64, _P, _P, _P, _P],
@@ -59,16 +57,7 @@ _SIGNATURES = {
     "fs_top_p_renorm_probs": [_P, _I32, _I32, _P, _P, _P, _P],
     "fs_top_k_mask_logits": [_P, _I32, _I32, _P, _P, _P, _P],
     "fs_philox4x32_10": [_P, _P, _I64, _P, _P],
-    "fs_top_k_top_p_sampling_from_uniforms": [_P, _I32, _I64, _I32, _I32, _P, _I32, _P, _P, _P, _P, _P, _I32, _P, _P,
-                                              _P, _SZ, _P],
-    "fs_from_uniforms_workspace_bytes": [_I32, _I32, _I32, ctypes.POINTER(_SZ)],
-    "fs_append_paged_kv": [_P, _P, _P, _P, _P, _I32, _P, _I32, _I32, _P, _P, _P, _P, _I32, _I32, _P, _P, _I32, _P, _P,
-                           _P],
-    "fs_shared_prefix_attention": [_P, _P, _P, _I32, _I32, _I32, _P, _I32, _P, _I32, _P, _P, _I32, _P,
-                                   ctypes.c_float, _P, _P, _P, _P, _SZ, _P],
-    "fs_shared_prefix_attention_workspace_bytes": [_P, _I32, _I32, _I32, _I32, _I32, _I32, ctypes.POINTER(_SZ)],
 }
-_DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
 
 
 class FsError(RuntimeError):
@@ -394,76 +383,19 @@ def philox4x32_10(ctr: torch.Tensor, key: torch.Tensor) -> torch.Tensor:
 
 # ------------------------------------------------------------------ the decode step
 #
-# These entries run once or more per generated token, often on a few rows, where the
-# host's own time decides: checks read each attribute once, pointers travel as plain
-# integers and structures and strides as packed bytes (the header's layout).
+# These entries run once or more per generated token, often on a few rows, where the host's own
+# time decides; their checks and marshalling are compiled (csrc/decode_binding.cpp).
 
-_PAGED_KV = struct.Struct("@PPiiiii6q")   # fs_paged_kv
-_S2, _S3 = struct.Struct("@2q"), struct.Struct("@3q")
+_NATIVE = None
 
 
-def _launch(fn: str, idx: int, *args) -> None:
-    """Call a library entry on device `idx`, made current, and its current stream."""
-    f = getattr(_lib(), fn)
-    if torch.cuda.current_device() == idx:
-        status = f(*args, torch._C._cuda_getCurrentRawStream(idx))
-    else:
-        with torch.cuda.device(idx):
-            status = f(*args, torch._C._cuda_getCurrentRawStream(idx))
-    if status:
-        _check(status)
-
-
-def _float_cuda(t, name: str, dims) -> int:
-    """The device index of a CUDA tensor of a type the entries take."""
-    if not isinstance(t, torch.Tensor) or t.dim() not in dims:
-        raise ValueError(f"{name} must be a {' or '.join(f'{d}-D' for d in dims)} tensor")
-    if t.dtype not in _DTYPES or not t.is_cuda:
-        raise ValueError(f"{name} must be a float32, bfloat16 or float16 CUDA tensor")
-    return t.get_device()
-
-
-def _strides(shape, st):
-    """Strides, 0 for a dimension of one element (its stride addresses nothing)."""
-    return st if 1 not in shape else tuple(0 if n == 1 else v for n, v in zip(shape, st))
-
-
-def _vectors(t, name: str, shape, dtype, idx: int):
-    """Strides of a tensor of vectors (contiguous last dimension) of the given shape, type and device."""
-    if not (isinstance(t, torch.Tensor) and t.shape == shape and t.dtype is dtype and t.get_device() == idx):
-        raise ValueError(f"{name} must be a {list(shape)} {dtype} tensor on cuda:{idx}")
-    st = t.stride()
-    if st[-1] != 1 and shape[-1] > 1:
-        raise ValueError(f"{name}'s last dimension must be contiguous")
-    return _strides(shape, st)
-
-
-def _flat(t, name: str, shape, dtype, idx: int) -> int:
-    """The address of a contiguous tensor of the given shape, type and device."""
-    if not (isinstance(t, torch.Tensor) and t.shape == shape and t.dtype is dtype and t.get_device() == idx
-            and t.is_contiguous()):
-        raise ValueError(f"{name} must be a contiguous {list(shape)} {dtype} tensor on cuda:{idx}")
-    return t.data_ptr()
-
-
-def _table(t, name: str, rows, idx: int):
-    """Address, rows and width of a page table."""
-    if not (isinstance(t, torch.Tensor) and t.dim() == 2 and t.dtype is torch.int32 and t.get_device() == idx
-            and t.is_contiguous() and (rows is None or t.shape[0] == rows)):
-        raise ValueError(f"{name} must be a contiguous [{'*' if rows is None else rows}, *] int32 tensor on cuda:{idx}")
-    return t.data_ptr(), *t.shape
-
-
-def _paged_kv(k_cache, v_cache):
-    """(packed fs_paged_kv, its shape, type and device index)."""
-    idx = _float_cuda(k_cache, "k_cache", (4,))
-    shape, dtype = k_cache.shape, k_cache.dtype
-    pages, page, heads, dim = shape
-    if page < 1 or heads < 1 or dim < 1:
-        raise ValueError("the caches must be [num_pages, page_size, num_heads, head_dim] with at least one element a page")
-    ks, vs = _vectors(k_cache, "k_cache", shape, dtype, idx), _vectors(v_cache, "v_cache", shape, dtype, idx)
-    return (_PAGED_KV.pack(k_cache.data_ptr(), v_cache.data_ptr(), _DTYPES[dtype], pages, page, heads, dim, *ks[:3],
-                           *vs[:3]), shape, dtype, idx)
+def _native():
+    global _NATIVE
+    if _NATIVE is None:
+        _lib()  # fails loudly if the library is missing
+        from . import _decode
+        _NATIVE = _decode
+    return _NATIVE
 
 
 def top_k_top_p_sampling_from_uniforms(logits, uniforms, temperature=None, top_k=None, top_p=None, min_p=None,
@@ -473,42 +405,10 @@ def top_k_top_p_sampling_from_uniforms(logits, uniforms, temperature=None, top_k
     the row filtered by top-k, top-p and min-p at the given temperature).
 
     logits: [B, V] float32, bfloat16 or float16, rows of any stride >= V.  uniforms: [B_out] float32 in
-    [0, 1).  Returns (tokens int32, valid uint8); a row that cannot be sampled gives -1 and 0."""
-    idx = _float_cuda(logits, "logits", (2,))
-    b_in, V = logits.shape
-    stride, col = logits.stride()
-    if V < 1 or (V > 1 and col != 1) or (b_in > 1 and stride < V):
-        raise ValueError("logits must have at least one column, contiguous columns and rows that do not overlap")
-    dev = logits.device
-    indices, b_out = _indices(indices, b_in, dev)
-    n = (b_out,)
-    u = _flat(uniforms, "uniforms", n, torch.float32, idx)
-    held, ptrs = [], []
-    for v, dt, name in ((temperature, torch.float32, "temperature"), (top_k, torch.int32, "top_k"),
-                        (top_p, torch.float32, "top_p"), (min_p, torch.float32, "min_p")):
-        if v is None:
-            ptrs.append(None)
-            continue
-        if not isinstance(v, torch.Tensor):
-            v = torch.full(n, v, dtype=dt, device=dev)
-            held.append(v)
-        ptrs.append(_flat(v, name, n, dt, idx))
-    dt = _DTYPES[logits.dtype]
-    need = _uniforms_bytes(dt, b_in, V)
-    ws = torch.empty(need, dtype=torch.uint8, device=dev)
-    tok = torch.empty(n, dtype=torch.int32, device=dev)
-    valid = torch.empty(n, dtype=torch.uint8, device=dev)
-    _launch("fs_top_k_top_p_sampling_from_uniforms", idx, logits.data_ptr(), dt, stride if b_in > 1 else V, b_in, V,
-            None if indices is None else indices.data_ptr(), b_out, u, *ptrs, _order(order), tok.data_ptr(),
-            valid.data_ptr(), ws.data_ptr(), need)
-    return tok, valid
-
-
-@functools.lru_cache(maxsize=256)
-def _uniforms_bytes(dtype: int, b_in: int, V: int) -> int:
-    need = _SZ(0)
-    _check(_lib().fs_from_uniforms_workspace_bytes(dtype, b_in, V, ctypes.byref(need)))
-    return need.value
+    [0, 1).  Parameters are numbers or per-row tensors.  Returns (tokens int32, valid uint8); a row
+    that cannot be sampled gives -1 and 0."""
+    r = _native().from_uniforms(logits, uniforms, temperature, top_k, top_p, min_p, _order(order), indices)
+    return r if type(r) is tuple else _check(r)
 
 
 def append_paged_kv(key, value, k_cache, v_cache, page_table, positions, rows=None, *, rotary_positions=None,
@@ -524,39 +424,9 @@ def append_paged_kv(key, value, k_cache, v_cache, page_table, positions, rows=No
     first r elements of each head, in halves or, with ``interleaved``, in neighbouring pairs (None: no
     rotation).  query: [N, q_heads, dim] is rotated into query_out (default: a new tensor; may be query itself),
     which is returned (None without a query)."""
-    kv, (_, _, heads, dim), dtype, idx = _paged_kv(k_cache, v_cache)
-    n = key.shape[0] if isinstance(key, torch.Tensor) and key.dim() == 3 else 0
-    ks = _vectors(key, "key", (n, heads, dim), dtype, idx)
-    vs = _vectors(value, "value", (n, heads, dim), dtype, idx)
-    table, table_rows, width = _table(page_table, "page_table", None, idx)
-    pos = _flat(positions, "positions", (n,), torch.int32, idx)
-    if rows is None and table_rows < n:
-        raise ValueError("page_table needs a row for every token when rows is not given")
-    row = None if rows is None else _flat(rows, "rows", (n,), torch.int32, idx)
-    rpos = None if rotary_positions is None else _flat(rotary_positions, "rotary_positions", (n,), torch.int32, idx)
-    freq, rotary = None, 0
-    if inv_freq is not None:
-        freq = _flat(inv_freq, "inv_freq", inv_freq.shape[:1] if isinstance(inv_freq, torch.Tensor) else (), torch.float32,
-                     idx)
-        rotary = 2 * inv_freq.shape[0]
-        if rotary > dim:
-            raise ValueError("inv_freq has more pairs than a head")
-    q, qs, qo, qos, q_heads = None, None, None, None, 0
-    if query is not None:
-        q_heads = query.shape[1] if isinstance(query, torch.Tensor) and query.dim() == 3 else 1
-        shape = (n, q_heads, dim)
-        qs = _S2.pack(*_vectors(query, "query", shape, dtype, idx)[:2])
-        if q_heads < 1:
-            raise ValueError("query must have at least one head")
-        if query_out is None:
-            query_out = torch.empty(shape, dtype=dtype, device=key.device)
-        qos = _S2.pack(*_vectors(query_out, "query_out", shape, dtype, idx)[:2])
-        q, qo = query.data_ptr(), query_out.data_ptr()
-    elif query_out is not None:
-        raise ValueError("query_out needs a query")
-    _launch("fs_append_paged_kv", idx, kv, key.data_ptr(), _S2.pack(*ks[:2]), value.data_ptr(), _S2.pack(*vs[:2]), n,
-            table, table_rows, width, row, pos, rpos, freq, rotary, 1 if interleaved else 0, q, qs, q_heads, qo, qos)
-    return query_out
+    r = _native().append(key, value, k_cache, v_cache, page_table, positions, rows, rotary_positions, inv_freq,
+                         interleaved, query, query_out)
+    return _check(r) if type(r) is int else r
 
 
 def shared_prefix_attention(query, k_cache, v_cache, prefix_table, prefix_lens, suffix_table, suffix_lens,
@@ -571,46 +441,6 @@ def shared_prefix_attention(query, k_cache, v_cache, prefix_table, prefix_lens, 
     group_starts[g + 1] share prefix g (default: one prefix for all).  scale defaults to dim ** -0.5.
     Returns out (query's shape), and with return_lse the log of the sum of exponentials,
     float32 [B, (Q,) heads]."""
-    kv, (_, page, heads, dim), dtype, idx = _paged_kv(k_cache, v_cache)
-    _float_cuda(query, "query", (3, 4))
-    shape, dev = query.shape, query.device
-    qs = _vectors(query, "query", shape, dtype, idx)
-    if out is None:
-        out = torch.empty(shape, dtype=dtype, device=dev)
-    os_ = _vectors(out, "out", shape, dtype, idx)
-    if len(shape) == 3:
-        (B, Hq, D), Q = shape, 1
-        qs, os_ = (qs[0], 0, qs[1]), (os_[0], 0, os_[1])
-    else:
-        B, Q, Hq, D = shape
-    if D != dim or Q < 1 or Hq < 1 or Hq % heads:
-        raise ValueError("query must have the caches' head size, at least one token, and a multiple of their heads")
-    G, pw, ptab, plens, starts = 0, 0, None, None, None
-    if prefix_table is not None:
-        ptab, G, pw = _table(prefix_table, "prefix_table", None, idx)
-        plens = _flat(prefix_lens, "prefix_lens", (G,), torch.int32, idx)
-    elif prefix_lens is not None or group_starts is not None:
-        raise ValueError("prefix_lens and group_starts need a prefix_table")
-    if group_starts is not None:
-        starts = _flat(group_starts, "group_starts", (G + 1,), torch.int32, idx)
-    elif G > 1:
-        raise ValueError("several prefixes need group_starts")
-    stab, _, sw = _table(suffix_table, "suffix_table", B, idx)
-    slens = _flat(suffix_lens, "suffix_lens", (B,), torch.int32, idx)
-    lse = torch.empty(shape[:-1], dtype=torch.float32, device=dev) if return_lse else None
-    need = _attention_bytes(idx, _DTYPES[dtype], page, heads, dim, B, Q, Hq, G, pw, sw)
-    ws = torch.empty(need, dtype=torch.uint8, device=dev)
-    _launch("fs_shared_prefix_attention", idx, kv, query.data_ptr(), _S3.pack(*qs[:3]), B, Q, Hq, starts, G, ptab, pw,
-            plens, stab, sw, slens, dim ** -0.5 if scale is None else scale, out.data_ptr(), _S3.pack(*os_[:3]),
-            None if lse is None else lse.data_ptr(), ws.data_ptr(), need)
-    return (out, lse) if return_lse else out
-
-
-@functools.lru_cache(maxsize=256)
-def _attention_bytes(idx: int, dtype: int, page: int, heads: int, dim: int, B: int, Q: int, Hq: int, G: int, pw: int,
-                     sw: int) -> int:
-    need = _SZ(0)
-    kv = _PAGED_KV.pack(0, 0, dtype, 0, page, heads, dim, 0, 0, 0, 0, 0, 0)
-    with torch.cuda.device(idx):
-        _check(_lib().fs_shared_prefix_attention_workspace_bytes(kv, B, Q, Hq, G, pw, sw, ctypes.byref(need)))
-    return need.value
+    r = _native().attention(query, k_cache, v_cache, prefix_table, prefix_lens, suffix_table, suffix_lens, group_starts,
+                            scale, out, return_lse)
+    return _check(r) if type(r) is int else r

@@ -1,0 +1,350 @@
+// Python entries of the decode step: argument checks and marshalling of torch tensors for
+// the C ABI, in C++.
+//
+// These calls run once or more per generated token, often on a few rows, where the host's
+// time decides: with the checks in Python a call took 21 to 31 us of the host for kernels of 3 to 13;
+// here it takes 4 to 10 (Grace).  Nothing is computed
+// and nothing kept from one call for the next.  Every function returns its result, or an
+// fs_status other than FS_OK as an int, which the caller in __init__.py raises.
+#include <torch/csrc/autograd/python_variable.h>
+
+#include <ATen/ops/empty.h>
+#include <ATen/ops/full.h>
+#include <c10/core/DeviceGuard.h>
+#include <c10/cuda/CUDAStream.h>
+
+#include <cmath>
+#include <initializer_list>
+#include <string>
+#include <utility>
+
+#include "fs_sampling.h"
+
+namespace {
+
+struct Refused {
+    std::string what;
+};
+
+[[noreturn]] void refuse(const std::string& what) { throw Refused{what}; }
+
+bool none(PyObject* o) { return o == nullptr || o == Py_None; }
+
+const at::Tensor* tensor(PyObject* o) { return THPVariable_Check(o) ? &THPVariable_Unpack(o) : nullptr; }
+
+int dtype_of(at::ScalarType t) {
+    switch (t) {
+        case at::kFloat: return FS_F32;
+        case at::kBFloat16: return FS_BF16;
+        case at::kHalf: return FS_F16;
+        default: return -1;
+    }
+}
+
+std::string shape_text(at::IntArrayRef s) {
+    std::string r = "[";
+    for (size_t i = 0; i < s.size(); ++i) r += (i ? ", " : "") + (s[i] < 0 ? std::string("*") : std::to_string(s[i]));
+    return r + "]";
+}
+
+// A CUDA tensor of a type the entries take, of lo to hi dimensions.
+const at::Tensor& float_cuda(PyObject* o, const char* name, int lo, int hi) {
+    const at::Tensor* t = tensor(o);
+    if (!t || t->dim() < lo || t->dim() > hi)
+        refuse(std::string(name) + " must be a " + (lo == hi ? "" : std::to_string(lo) + "-D or ") + std::to_string(hi) +
+               "-D tensor");
+    if (dtype_of(t->scalar_type()) < 0 || !t->is_cuda())
+        refuse(std::string(name) + " must be a float32, bfloat16 or float16 CUDA tensor");
+    return *t;
+}
+
+bool matches(const at::Tensor& t, at::IntArrayRef shape, at::ScalarType type, c10::DeviceIndex dev) {
+    if (!t.is_cuda() || t.get_device() != dev || t.scalar_type() != type || t.dim() != int64_t(shape.size())) return false;
+    for (size_t i = 0; i < shape.size(); ++i)
+        if (shape[i] >= 0 && t.size(i) != shape[i]) return false;  // -1: any
+    return true;
+}
+
+// A tensor of vectors (contiguous last dimension) of the given shape, type and device.
+const at::Tensor& vectors(PyObject* o, const char* name, at::IntArrayRef shape, at::ScalarType type, c10::DeviceIndex dev) {
+    const at::Tensor* t = tensor(o);
+    if (!t || !matches(*t, shape, type, dev))
+        refuse(std::string(name) + " must be a " + shape_text(shape) + " " + c10::toString(type) + " tensor on cuda:" +
+               std::to_string(int(dev)));
+    if (t->size(-1) > 1 && t->stride(-1) != 1) refuse(std::string(name) + "'s last dimension must be contiguous");
+    return *t;
+}
+
+// A contiguous tensor of the given shape (-1: any size), type and device.
+const at::Tensor& flat(PyObject* o, const char* name, at::IntArrayRef shape, at::ScalarType type, c10::DeviceIndex dev) {
+    const at::Tensor* t = tensor(o);
+    if (!t || !matches(*t, shape, type, dev) || !t->is_contiguous())
+        refuse(std::string(name) + " must be a contiguous " + shape_text(shape) + " " + c10::toString(type) +
+               " tensor on cuda:" + std::to_string(int(dev)));
+    return *t;
+}
+
+template <typename X>
+const X* flat_ptr(PyObject* o, const char* name, int64_t n, at::ScalarType type, c10::DeviceIndex dev) {
+    return none(o) ? nullptr : static_cast<const X*>(flat(o, name, {n}, type, dev).data_ptr());
+}
+
+// Strides of the first n dimensions, 0 for a dimension of one element (its stride addresses nothing).
+void strides(const at::Tensor& t, int n, int64_t* out) {
+    for (int i = 0; i < n; ++i) out[i] = t.size(i) > 1 ? t.stride(i) : 0;
+}
+
+fs_paged_kv paged_kv(PyObject* k, PyObject* v) {
+    const at::Tensor& kt = float_cuda(k, "k_cache", 4, 4);
+    vectors(k, "k_cache", kt.sizes(), kt.scalar_type(), kt.get_device());
+    const at::Tensor& vt = vectors(v, "v_cache", kt.sizes(), kt.scalar_type(), kt.get_device());
+    if (kt.size(1) < 1 || kt.size(2) < 1 || kt.size(3) < 1)
+        refuse("the caches must be [num_pages, page_size, num_heads, head_dim] with at least one element a page");
+    for (int i = 0; i < 4; ++i)
+        if (kt.size(i) > INT32_MAX) refuse("the caches are too large in one dimension");
+    fs_paged_kv kv;
+    kv.k = kt.data_ptr();
+    kv.v = vt.data_ptr();
+    kv.dtype = dtype_of(kt.scalar_type());
+    kv.num_pages = int32_t(kt.size(0));
+    kv.page_size = int32_t(kt.size(1));
+    kv.num_heads = int32_t(kt.size(2));
+    kv.head_dim = int32_t(kt.size(3));
+    strides(kt, 3, kv.k_strides);
+    strides(vt, 3, kv.v_strides);
+    return kv;
+}
+
+int32_t size32(int64_t n, const char* what) {
+    if (n > INT32_MAX) refuse(std::string(what) + " is too large");
+    return int32_t(n);
+}
+
+at::Tensor scratch(size_t bytes, const at::Tensor& like) {
+    return at::empty({int64_t(bytes)}, like.options().dtype(at::kByte));
+}
+
+// Runs `f(stream)` with the device current; FS_OK -> `ok()`.
+template <typename F, typename R>
+PyObject* launch(const at::Tensor& on, F f, R ok) {
+    const fs_status st = f(static_cast<void*>(c10::cuda::getCurrentCUDAStream(on.get_device()).stream()));
+    return st == FS_OK ? ok() : PyLong_FromLong(st);
+}
+
+template <typename F>
+PyObject* guarded(F f) {
+    try {
+        return f();
+    } catch (const Refused& r) {
+        PyErr_SetString(PyExc_ValueError, r.what.c_str());
+    } catch (const std::exception& e) {  // an allocation, a conversion
+        if (!PyErr_Occurred()) PyErr_SetString(PyExc_RuntimeError, e.what());
+    }
+    return nullptr;
+}
+
+struct py_owned {
+    PyObject* p;
+    explicit py_owned(PyObject* o) : p(o) {}
+    ~py_owned() { Py_XDECREF(p); }
+};
+
+PyObject* wrap(at::Tensor t) { return THPVariable_Wrap(std::move(t)); }
+
+PyObject* pair(at::Tensor x, at::Tensor y) {
+    PyObject* r = PyTuple_New(2);
+    if (r) {
+        PyTuple_SET_ITEM(r, 0, wrap(std::move(x)));
+        PyTuple_SET_ITEM(r, 1, wrap(std::move(y)));
+    }
+    return r;
+}
+
+bool arity(Py_ssize_t n, Py_ssize_t want) {
+    if (n == want) return true;
+    PyErr_SetString(PyExc_TypeError, "wrong number of arguments");
+    return false;
+}
+
+// (logits, uniforms, temperature, top_k, top_p, min_p, order, indices) -> (tokens, valid)
+PyObject* from_uniforms(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    if (!arity(n, 8)) return nullptr;
+    return guarded([&]() -> PyObject* {
+        const at::Tensor& x = float_cuda(a[0], "logits", 2, 2);
+        const int64_t b_in = x.size(0), V = x.size(1), stride = b_in > 1 ? x.stride(0) : V;
+        const auto dev = x.get_device();
+        if (V < 1 || (V > 1 && x.stride(1) != 1) || stride < V)
+            refuse("logits must have at least one column, contiguous columns and rows that do not overlap");
+        const at::Tensor* idx = none(a[7]) ? nullptr : &flat(a[7], "indices", {-1}, at::kInt, dev);
+        const int32_t b_out = size32(idx ? idx->size(0) : b_in, "the batch");
+        const c10::DeviceGuard guard(x.device());
+        const auto* u = flat_ptr<float>(a[1], "uniforms", b_out, at::kFloat, dev);
+        if (!u && none(a[1])) refuse("uniforms must be given");
+        // Per-row parameters; a number is the same for every row.
+        at::Tensor held[4];
+        const void* ps[4];
+        static const char* const names[4] = {"temperature", "top_k", "top_p", "min_p"};
+        for (int i = 0; i < 4; ++i) {
+            PyObject* o = a[2 + i];
+            const auto type = i == 1 ? at::kInt : at::kFloat;
+            ps[i] = nullptr;
+            if (none(o)) continue;
+            if (!tensor(o)) {
+                const double v = PyFloat_AsDouble(o);
+                if (v == -1.0 && PyErr_Occurred()) return nullptr;
+                held[i] = at::full({b_out}, v, x.options().dtype(type));
+                ps[i] = held[i].data_ptr();
+            } else {
+                ps[i] = flat(o, names[i], {b_out}, type, dev).data_ptr();
+            }
+        }
+        const long order = PyLong_AsLong(a[6]);
+        if (order == -1 && PyErr_Occurred()) return nullptr;
+        const int dtype = dtype_of(x.scalar_type());
+        size_t need = 0;
+        const fs_status st = fs_from_uniforms_workspace_bytes(dtype, size32(b_in, "the batch"), size32(V, "the vocabulary"), &need);
+        if (st != FS_OK) return PyLong_FromLong(st);
+        const at::Tensor ws = scratch(need, x);
+        at::Tensor tok = at::empty({b_out}, x.options().dtype(at::kInt)), valid = at::empty({b_out}, x.options().dtype(at::kByte));
+        return launch(x, [&](void* s) {
+            return fs_top_k_top_p_sampling_from_uniforms(
+                x.data_ptr(), dtype, stride, int32_t(b_in), int32_t(V), idx ? static_cast<const int32_t*>(idx->data_ptr()) : nullptr,
+                b_out, u, static_cast<const float*>(ps[0]), static_cast<const int32_t*>(ps[1]), static_cast<const float*>(ps[2]),
+                static_cast<const float*>(ps[3]), int32_t(order), static_cast<int32_t*>(tok.data_ptr()),
+                static_cast<uint8_t*>(valid.data_ptr()), ws.data_ptr(), need, s);
+        }, [&] { return pair(tok, valid); });
+    });
+}
+
+// (key, value, k_cache, v_cache, page_table, positions, rows, rotary_positions, inv_freq, interleaved, query, query_out)
+// -> query_out or None
+PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    if (!arity(n, 12)) return nullptr;
+    return guarded([&]() -> PyObject* {
+        const fs_paged_kv kv = paged_kv(a[2], a[3]);
+        const at::Tensor& cache = *tensor(a[2]);
+        const auto type = cache.scalar_type();
+        const auto dev = cache.get_device();
+        const at::Tensor& key = vectors(a[0], "key", {-1, kv.num_heads, kv.head_dim}, type, dev);
+        const int32_t tokens = size32(key.size(0), "the number of tokens");
+        const at::Tensor& value = vectors(a[1], "value", {tokens, kv.num_heads, kv.head_dim}, type, dev);
+        const at::Tensor& table = flat(a[4], "page_table", {-1, -1}, at::kInt, dev);
+        const auto* pos = static_cast<const int32_t*>(flat(a[5], "positions", {tokens}, at::kInt, dev).data_ptr());
+        const auto* rows = flat_ptr<int32_t>(a[6], "rows", tokens, at::kInt, dev);
+        if (none(a[6]) && table.size(0) < tokens) refuse("page_table needs a row for every token when rows is not given");
+        const auto* rpos = flat_ptr<int32_t>(a[7], "rotary_positions", tokens, at::kInt, dev);
+        const auto* freq = flat_ptr<float>(a[8], "inv_freq", -1, at::kFloat, dev);
+        const int64_t rotary = none(a[8]) ? 0 : 2 * tensor(a[8])->size(0);
+        if (rotary > kv.head_dim) refuse("inv_freq has more pairs than a head");
+        const int interleaved = PyObject_IsTrue(a[9]);
+        if (interleaved < 0) return nullptr;
+        int64_t ks[2], vs[2], qs[2] = {0, 0}, qos[2] = {0, 0};
+        strides(key, 2, ks);
+        strides(value, 2, vs);
+        const c10::DeviceGuard guard(cache.device());
+        const at::Tensor* q = nullptr;
+        at::Tensor qo;
+        int32_t q_heads = 0;
+        if (!none(a[10])) {
+            q = &vectors(a[10], "query", {tokens, -1, kv.head_dim}, type, dev);
+            q_heads = size32(q->size(1), "the number of heads");
+            if (q_heads < 1) refuse("query must have at least one head");
+            qo = none(a[11]) ? at::empty(q->sizes(), q->options()) : vectors(a[11], "query_out", q->sizes(), type, dev);
+            strides(*q, 2, qs);
+            strides(qo, 2, qos);
+        } else if (!none(a[11])) {
+            refuse("query_out needs a query");
+        }
+        return launch(cache, [&](void* s) {
+            return fs_append_paged_kv(&kv, key.data_ptr(), ks, value.data_ptr(), vs, tokens,
+                                      static_cast<const int32_t*>(table.data_ptr()), size32(table.size(0), "the table"),
+                                      size32(table.size(1), "the table"), rows, pos, rpos, freq, int32_t(rotary), interleaved,
+                                      q ? q->data_ptr() : nullptr, qs, q_heads, q ? qo.data_ptr() : nullptr, qos, s);
+        }, [&]() -> PyObject* {
+            if (!q) Py_RETURN_NONE;
+            if (none(a[11])) return wrap(qo);
+            Py_INCREF(a[11]);
+            return a[11];
+        });
+    });
+}
+
+// (query, k_cache, v_cache, prefix_table, prefix_lens, suffix_table, suffix_lens, group_starts, scale, out, return_lse)
+// -> out or (out, lse)
+PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    if (!arity(n, 11)) return nullptr;
+    return guarded([&]() -> PyObject* {
+        const fs_paged_kv kv = paged_kv(a[1], a[2]);
+        const at::Tensor& cache = *tensor(a[1]);
+        const auto type = cache.scalar_type();
+        const auto dev = cache.get_device();
+        const at::Tensor& given = float_cuda(a[0], "query", 3, 4);
+        const at::Tensor& q = vectors(a[0], "query", given.sizes(), type, dev);
+        const c10::DeviceGuard guard(cache.device());
+        at::Tensor out = none(a[9]) ? at::empty(q.sizes(), q.options()) : vectors(a[9], "out", q.sizes(), type, dev);
+        const bool one = q.dim() == 3;
+        const int32_t B = size32(q.size(0), "the batch"), Q = one ? 1 : size32(q.size(1), "the number of queries");
+        const int32_t Hq = size32(q.size(-2), "the number of heads");
+        if (q.size(-1) != kv.head_dim || Q < 1 || Hq < 1 || Hq % kv.num_heads != 0)
+            refuse("query must have the caches' head size, at least one token, and a multiple of their heads");
+        int64_t qs[3], os[3];
+        for (const auto& [t, s] : {std::pair<const at::Tensor&, int64_t*>(q, qs), std::pair<const at::Tensor&, int64_t*>(out, os)}) {
+            strides(t, one ? 2 : 3, s);
+            if (one) s[2] = s[1], s[1] = 0;
+        }
+        int32_t G = 0, pw = 0;
+        const int32_t *ptab = nullptr, *plens = nullptr, *starts = nullptr;
+        if (!none(a[3])) {
+            const at::Tensor& t = flat(a[3], "prefix_table", {-1, -1}, at::kInt, dev);
+            G = size32(t.size(0), "the table"), pw = size32(t.size(1), "the table");
+            ptab = static_cast<const int32_t*>(t.data_ptr());
+            plens = static_cast<const int32_t*>(flat(a[4], "prefix_lens", {G}, at::kInt, dev).data_ptr());
+        } else if (!none(a[4]) || !none(a[7])) {
+            refuse("prefix_lens and group_starts need a prefix_table");
+        }
+        starts = flat_ptr<int32_t>(a[7], "group_starts", int64_t(G) + 1, at::kInt, dev);
+        if (G > 1 && none(a[7])) refuse("several prefixes need group_starts");
+        const at::Tensor& stab = flat(a[5], "suffix_table", {B, -1}, at::kInt, dev);
+        const int32_t sw = size32(stab.size(1), "the table");
+        const auto* slens = static_cast<const int32_t*>(flat(a[6], "suffix_lens", {B}, at::kInt, dev).data_ptr());
+        double scale = 1.0 / std::sqrt(double(kv.head_dim));
+        if (!none(a[8])) {
+            scale = PyFloat_AsDouble(a[8]);
+            if (scale == -1.0 && PyErr_Occurred()) return nullptr;
+        }
+        const int want_lse = PyObject_IsTrue(a[10]);
+        if (want_lse < 0) return nullptr;
+        at::Tensor lse;
+        if (want_lse) lse = at::empty(q.sizes().slice(0, q.dim() - 1), q.options().dtype(at::kFloat));
+        size_t need = 0;
+        const fs_status st = fs_shared_prefix_attention_workspace_bytes(&kv, B, Q, Hq, G, pw, sw, &need);
+        if (st != FS_OK) return PyLong_FromLong(st);
+        const at::Tensor ws = scratch(need, q);
+        return launch(q, [&](void* s) {
+            return fs_shared_prefix_attention(&kv, q.data_ptr(), qs, B, Q, Hq, starts, G, ptab, pw, plens,
+                                              static_cast<const int32_t*>(stab.data_ptr()), sw, slens, float(scale), out.data_ptr(), os,
+                                              want_lse ? static_cast<float*>(lse.data_ptr()) : nullptr, ws.data_ptr(), need, s);
+        }, [&]() -> PyObject* {
+            if (none(a[9])) return want_lse ? pair(out, lse) : wrap(out);
+            PyObject* o = a[9];
+            if (!want_lse) {
+                Py_INCREF(o);
+                return o;
+            }
+            return PyTuple_Pack(2, o, py_owned(wrap(lse)).p);
+        });
+    });
+}
+
+PyMethodDef METHODS[] = {
+    {"from_uniforms", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(from_uniforms)), METH_FASTCALL, nullptr},
+    {"append", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(append)), METH_FASTCALL, nullptr},
+    {"attention", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(attention)), METH_FASTCALL, nullptr},
+    {nullptr, nullptr, 0, nullptr}};
+
+PyModuleDef MODULE = {PyModuleDef_HEAD_INIT, "_decode", "The decode step's entries of libfs_sampling.so for torch tensors.",
+                      -1, METHODS, nullptr, nullptr, nullptr, nullptr};
+
+}  // namespace
+
+PyMODINIT_FUNC PyInit__decode() { return PyModule_Create(&MODULE); }

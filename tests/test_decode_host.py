@@ -1,6 +1,7 @@
 """Host-side checks of the decode-step entries, without a GPU: the C ABI refuses bad arguments before
 touching the device, and the binding refuses tensors the kernels cannot read."""
 import ctypes
+import struct
 
 import pytest
 
@@ -13,11 +14,20 @@ P, FAKE = ctypes.c_void_p, ctypes.c_void_p(0x1000)   # never dereferenced: every
 def ms():
     ensure_built()
     import min_sampling_gb300
+    lib, sz, i32 = min_sampling_gb300.lib, ctypes.c_size_t, ctypes.c_int32
+    lib.fs_top_k_top_p_sampling_from_uniforms.argtypes = [P, i32, ctypes.c_int64, i32, i32, P, i32, P, P, P, P, P, i32, P, P,
+                                                          P, sz, P]
+    lib.fs_append_paged_kv.argtypes = [P, P, P, P, P, i32, P, i32, i32, P, P, P, P, i32, i32, P, P, i32, P, P, P]
+    lib.fs_shared_prefix_attention.argtypes = [P, P, P, i32, i32, i32, P, i32, P, i32, P, P, i32, P, ctypes.c_float, P, P, P,
+                                               P, sz, P]
     return min_sampling_gb300
 
 
+KV = struct.Struct("@PPiiiii6q")   # fs_paged_kv
+
+
 def _kv(ms, k=0x1000, v=0x1000, dtype=1, pages=4, page=16, heads=2, dim=64, ks=(2048, 128, 64), vs=(2048, 128, 64)):
-    return ms._PAGED_KV.pack(k or 0, v or 0, dtype, pages, page, heads, dim, *ks, *vs)
+    return KV.pack(k or 0, v or 0, dtype, pages, page, heads, dim, *ks, *vs)
 
 
 def _s(*v):
@@ -93,15 +103,12 @@ def test_binding_refuses(ms):
         ms.append_paged_kv(f(1, 2, 64), f(1, 2, 64), kc[0], kc[0], i(1, 1), i(1))
     with pytest.raises(ValueError, match="CUDA"):
         ms.shared_prefix_attention(f(1, 4, 64), kc, kc, i(1, 1), i(1), i(1, 1), i(1))
-    for bad in (i(2), i(3, 2).t(), i(2, 3).long(), i(1, 3), [1], None):
-        with pytest.raises(ValueError, match="int32"):
-            ms._table(bad, "t", 2, -1)
-    assert ms._table(i(2, 3), "t", 2, -1)[1:] == (2, 3)    # -1 stands for the device here: a CPU tensor's index
-    for bad in (i(3), i(2).long(), i(4)[::2], i(2, 1), 5):
-        with pytest.raises(ValueError, match="contiguous"):
-            ms._flat(bad, "x", (2,), torch.int32, -1)
-    for bad in (f(3, 4), f(2, 4).half(), f(2, 8)[:, ::2], None):
+    for bad in (None, 3, "x"):
         with pytest.raises(ValueError):
-            ms._vectors(bad, "x", (2, 4), torch.float32, -1)
-    # strides of dimensions of one element address nothing
-    assert ms._vectors(torch.empty_strided((1, 3, 4), (5, 4, 1)), "x", (1, 3, 4), torch.float32, -1) == (0, 4, 1)
+            ms.top_k_top_p_sampling_from_uniforms(bad, f(1))
+        with pytest.raises(ValueError):
+            ms.append_paged_kv(f(1, 2, 64), f(1, 2, 64), bad, kc, i(1, 1), i(1))
+        with pytest.raises(ValueError):
+            ms.shared_prefix_attention(f(1, 4, 64), bad, kc, i(1, 1), i(1), i(1, 1), i(1))
+    with pytest.raises(ValueError, match="order"):
+        ms.top_k_top_p_sampling_from_uniforms(f(2, 8), f(2), order="sideways")

@@ -386,9 +386,9 @@ fs_status fs_top_k_top_p_sampling_noalloc(const float* probs, int32_t batch_in, 
  *   min-p   keeps w >= min_p;
  *   token = the first i of the kept set, in index order, with
  *           sum of w_j over kept j <= i  >  u * sum of w over the kept set.
- * Decided on 64-bit fixed-point weights (round(2^42 w) within 1 unit and a relative 4e-11),
+ * Decided on 64-bit fixed-point weights (2^42 w within a relative 5e-10 and half a unit),
  * whose sums are exact: the answer is that of real arithmetic but for numbers u, or masses
- * at a threshold, within about 10^-10 of a border.  Weights below 2^-43 count as 0.
+ * at a threshold, within 10^-9 of a border.  Weights below 2^-43 count as 0.
  *   logits       [batch_in, vocab] of `dtype`, rows `row_stride` elements apart (>= vocab);
  *                no alignment beyond the element's
  *   uniforms     [batch_out] float32 in [0, 1)
@@ -406,7 +406,7 @@ fs_status fs_top_k_top_p_sampling_from_uniforms(const void* logits, int32_t dtyp
                                                 int32_t* out_token, uint8_t* out_valid,
                                                 void* workspace, size_t workspace_bytes, void* stream);
 
-/* Workspace of fs_top_k_top_p_sampling_from_uniforms: 4 bytes for every 512 bytes of a row. */
+/* Workspace of fs_top_k_top_p_sampling_from_uniforms: 8 bytes for every 512 bytes of a row. */
 fs_status fs_from_uniforms_workspace_bytes(int32_t dtype, int32_t batch_in, int32_t vocab, size_t* bytes);
 
 /* A paged cache of keys and values: page i, slot s, head h is the vector of head_dim

@@ -6,22 +6,27 @@
 // Unlike the rejection sampler this needs the masses themselves, not only an accepted
 // draw, and the decisions (which token the top-p mass ends on, which token u falls on)
 // are borders between neighbours that may differ by 10^-6 of the row: a float32 sum would
-// answer another token for flat rows.  So weights are 64-bit fixed-point integers,
-// round(2^42 w) to within one unit and a relative 4e-11 (weight_of), and every sum and
+// answer another token for flat rows.  So weights are 64-bit fixed-point integers, 2^42 w to
+// a relative 5e-10 (2e-10 rms) and half a unit (weight_of), and every sum and
 // comparison is exact integer arithmetic.  Sums then do not depend on their order, the
 // launch shape or atomics.
 //
 // Two launches.  seg_max_kernel streams every input row once, spread evenly over the GPU,
 // and writes the largest order key of each segment (one 16-byte load per lane of a warp).
 // uniform_kernel, one cluster of C CTAs per output row, reads those keys and then:
-//   small top-k  segments whose maximum reaches the k-th largest segment maximum hold
-//                every element of the top k; their elements at or above that bound (a
-//                few dozen more than k) go into a list in shared memory, and every
-//                decision is made there;
-//   otherwise    a histogram of the weights over 2048 bins linear in m - z finds the bin
-//                a threshold lies in, further histograms over the order keys inside it
-//                find the exact key; one pass then leaves each segment's kept mass, and
-//                one segment is read to find the token.
+//   small sets  top-k: the segments whose maximum reaches the k-th largest segment maximum hold
+//               every element of the top k; min-p: those whose maximum reaches the
+//               threshold hold every kept element.  Their elements at or above the bound (for top-k
+//               a few dozen more than k) go into a list in shared memory in index
+//               order, and every decision is made there.  The whole row's mass, where top-p is
+//               measured against it, is a float32 sum with a bound on its error; only a row with a
+//               candidate inside that bound sums its weights exactly.
+//   other sets  a histogram of the weights over 2048 bins linear in m - z finds the bin a
+//               threshold lies in; one more pass lists that bin's elements and sums the masses of
+//               the elements above it per segment (queued, so that a warp weighs 32 of
+//               them at a time); the list decides the threshold.  Bins too full for the list (16-bit
+//               logits tie by thousands) are narrowed by histograms over the order keys.
+//               The token is found from the segments' masses and one read of its segment.
 #include <algorithm>
 
 #include <cuda_bf16.h>
@@ -35,7 +40,8 @@ namespace fsd {
 constexpr int UNT = 512;          // threads of uniform_kernel
 constexpr int UNW = UNT / 32;
 constexpr int UB = 2048;          // histogram bins
-constexpr int UCAP = 512;         // candidates of the small top-k path
+constexpr int UCAP = 1024;        // candidates in a list
+constexpr int UQ = 64;            // queued elements per warp
 constexpr int USEG_TRIP = 4;      // segments a warp has in flight
 constexpr uint32_t KEY_NINF = 0x007fffffu;  // order keys of -inf and +inf (a NaN's is above the latter or below the former)
 constexpr uint32_t KEY_PINF = 0xff800000u;
@@ -55,6 +61,7 @@ struct UniformArgs {
     int* out_token;
     unsigned char* out_valid;
     uint32_t* skey;             // [batch_in][ls] segment maxima
+    float* ssum;                // [batch_in][ls] sums of exp((z - segment maximum) / T), nullable
     int ls;                     // segments of a row, at most
     int nsc;                    // segments per CTA of a cluster, at most
 };
@@ -109,11 +116,19 @@ __device__ __forceinline__ void unpack(const uint4& w, float (&z)[8], __half) {
 // Order key with -0 equal to +0.
 __device__ __forceinline__ uint32_t ukey(float z) { return logit_key(z + 0.f); }
 
+__device__ __forceinline__ float exp2_approx(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 // ------------------------------------------------------------------ segment maxima
 
 // Warp w of the grid takes trips of USEG_TRIP segments w, w + W, ...; bound by the HBM
 // read.  A NaN marks its segment with the largest key.
-template <typename T>
+// With SUMS also each segment's float32 mass relative to its own maximum, at the row's
+// temperature (rows map one to one): the total mass then takes no second read.
+template <typename T, bool SUMS>
 __global__ void __launch_bounds__(256) seg_max_kernel(const UniformArgs a) {
     using R = URow<T>;
     grid_dependency_wait();
@@ -138,37 +153,73 @@ __global__ void __launch_bounds__(256) seg_max_kernel(const UniformArgs a) {
             for (int e = 0; e < R::N; ++e) k = max(k, z[e] == z[e] ? ukey(z[e]) : 0xffffffffu);
             k = warp_max_u(k);
             if (lane == 0) a.skey[int64_t(r) * a.ls + s0 + j] = k;
+            if (SUMS) {
+                const float c = 1.44269504f / (a.temperature ? a.temperature[r] : 1.f), mc = from_logit_key(k);
+                float sum = 0.f;
+#pragma unroll
+                for (int e = 0; e < R::N; ++e) sum += z[e] > -INFINITY ? exp2_approx((z[e] - mc) * c) : 0.f;
+                sum = warp_sum(sum);
+                if (lane == 0) a.ssum[int64_t(r) * a.ls + s0 + j] = sum;
+            }
         }
     }
 }
 
 // ------------------------------------------------------------------ weights
 
-// 2^(j / 32) * 2^42, rounded.
-__constant__ unsigned long long EXP2_32[32] = {
-    0x40000000000ull, 0x4166c34c561ull, 0x42d561b3e62ull, 0x444c0740497ull, 0x45cae0f1f54ull, 0x47521cc5a2eull,
-    0x48e1e9b9d59ull, 0x4a7a77d47f8ull, 0x4c1bf828c6eull, 0x4dc69cdceaaull, 0x4f7a993048dull, 0x51382181862ull,
-    0x52ff6b54d8bull, 0x54d0ad5a754ull, 0x56ac1f75215ull, 0x5891fac0e95ull, 0x5a827999fcfull, 0x5c7dd7a3b18ull,
-    0x5e8451cfac0ull, 0x60962665334ull, 0x62b39508aa8ull, 0x64dcdec3371ull, 0x6712460a8fcull, 0x69540ec8f89ull,
-    0x6ba27e656b5ull, 0x6dfddbcbed8ull, 0x70666f76155ull, 0x72dc8373be4ull, 0x75606373ee9ull, 0x77f25ccdee7ull,
-    0x7a92be8a924ull, 0x7d41d96db91ull};
+// 2^(j / 256) * 2^31, rounded.
+__constant__ uint32_t EXP2_256[256] = {
+    0x80000000u, 0x8058d7d3u, 0x80b1ed50u, 0x810b40a2u, 0x8164d1f4u, 0x81bea171u, 0x8218af43u, 0x8272fb98u,
+    0x82cd8699u, 0x83285072u, 0x8383594fu, 0x83dea15cu, 0x843a28c4u, 0x8495efb3u, 0x84f1f656u, 0x854e3cd9u,
+    0x85aac368u, 0x86078a2fu, 0x8664915cu, 0x86c1d91au, 0x871f6197u, 0x877d2affu, 0x87db3580u, 0x88398147u,
+    0x88980e81u, 0x88f6dd5bu, 0x8955ee03u, 0x89b540a8u, 0x8a14d575u, 0x8a74ac9au, 0x8ad4c645u, 0x8b3522a4u,
+    0x8b95c1e4u, 0x8bf6a435u, 0x8c57c9c4u, 0x8cb932c2u, 0x8d1adf5bu, 0x8d7ccfc1u, 0x8ddf0420u, 0x8e417ca9u,
+    0x8ea4398bu, 0x8f073af6u, 0x8f6a8118u, 0x8fce0c22u, 0x9031dc43u, 0x9095f1acu, 0x90fa4c8cu, 0x915eed14u,
+    0x91c3d374u, 0x9228ffdcu, 0x928e727eu, 0x92f42b89u, 0x935a2b2fu, 0x93c071a1u, 0x9426ff10u, 0x948dd3adu,
+    0x94f4efa9u, 0x955c5337u, 0x95c3fe87u, 0x962bf1ccu, 0x96942d37u, 0x96fcb0fbu, 0x97657d4au, 0x97ce9256u,
+    0x9837f052u, 0x98a1976fu, 0x990b87e2u, 0x9975c1ddu, 0x99e04593u, 0x9a4b1337u, 0x9ab62afdu, 0x9b218d17u,
+    0x9b8d39bau, 0x9bf93119u, 0x9c657368u, 0x9cd200dcu, 0x9d3ed9a7u, 0x9dabfdffu, 0x9e196e19u, 0x9e872a27u,
+    0x9ef53261u, 0x9f6386f9u, 0x9fd22825u, 0xa041161bu, 0xa0b05110u, 0xa11fd938u, 0xa18faecbu, 0xa1ffd1fcu,
+    0xa2704303u, 0xa2e10215u, 0xa3520f69u, 0xa3c36b34u, 0xa43515aeu, 0xa4a70f0du, 0xa5195787u, 0xa58bef53u,
+    0xa5fed6aau, 0xa6720dc1u, 0xa6e594d0u, 0xa7596c0fu, 0xa7cd93b5u, 0xa8420bfau, 0xa8b6d516u, 0xa92bef42u,
+    0xa9a15ab5u, 0xaa1717a8u, 0xaa8d2653u, 0xab0386efu, 0xab7a39b6u, 0xabf13edfu, 0xac6896a5u, 0xace04140u,
+    0xad583eeau, 0xadd08fddu, 0xae493453u, 0xaec22c85u, 0xaf3b78adu, 0xafb51907u, 0xb02f0dccu, 0xb0a95736u,
+    0xb123f582u, 0xb19ee8e9u, 0xb21a31a6u, 0xb295cff6u, 0xb311c413u, 0xb38e0e38u, 0xb40aaea2u, 0xb487a58du,
+    0xb504f334u, 0xb58297d4u, 0xb60093a8u, 0xb67ee6efu, 0xb6fd91e3u, 0xb77c94c3u, 0xb7fbefcbu, 0xb87ba338u,
+    0xb8fbaf47u, 0xb97c1437u, 0xb9fcd245u, 0xba7de9afu, 0xbaff5ab2u, 0xbb81258du, 0xbc034a7fu, 0xbc85c9c5u,
+    0xbd08a39fu, 0xbd8bd84cu, 0xbe0f680au, 0xbe935318u, 0xbf1799b6u, 0xbf9c3c25u, 0xc0213aa2u, 0xc0a6956fu,
+    0xc12c4ccau, 0xc1b260f6u, 0xc238d231u, 0xc2bfa0bdu, 0xc346ccdau, 0xc3ce56cau, 0xc4563eccu, 0xc4de8524u,
+    0xc5672a11u, 0xc5f02dd7u, 0xc67990b6u, 0xc70352f0u, 0xc78d74c9u, 0xc817f681u, 0xc8a2d85du, 0xc92e1a9du,
+    0xc9b9bd86u, 0xca45c15bu, 0xcad2265eu, 0xcb5eecd4u, 0xcbec14ffu, 0xcc799f24u, 0xcd078b86u, 0xcd95da6bu,
+    0xce248c15u, 0xceb3a0cau, 0xcf4318cfu, 0xcfd2f468u, 0xd06333dbu, 0xd0f3d76cu, 0xd184df62u, 0xd2164c02u,
+    0xd2a81d92u, 0xd33a5458u, 0xd3ccf09au, 0xd45ff29eu, 0xd4f35aacu, 0xd587290au, 0xd61b5dffu, 0xd6aff9d2u,
+    0xd744fccbu, 0xd7da6731u, 0xd870394cu, 0xd9067365u, 0xd99d15c2u, 0xda3420aeu, 0xdacb946fu, 0xdb637150u,
+    0xdbfbb798u, 0xdc946791u, 0xdd2d8185u, 0xddc705bdu, 0xde60f482u, 0xdefb4e20u, 0xdf9612dfu, 0xe031430au,
+    0xe0ccdeecu, 0xe168e6d0u, 0xe2055b00u, 0xe2a23bc8u, 0xe33f8973u, 0xe3dd444cu, 0xe47b6ca0u, 0xe51a02bbu,
+    0xe5b906e7u, 0xe6587973u, 0xe6f85aabu, 0xe798aadbu, 0xe8396a50u, 0xe8da9958u, 0xe97c3840u, 0xea1e4756u,
+    0xeac0c6e8u, 0xeb63b743u, 0xec0718b6u, 0xecaaeb90u, 0xed4f301fu, 0xedf3e6b2u, 0xee990f98u, 0xef3eab21u,
+    0xefe4b99cu, 0xf08b3b59u, 0xf13230a8u, 0xf1d999d9u, 0xf281773cu, 0xf329c923u, 0xf3d28fdeu, 0xf47bcbbeu,
+    0xf5257d15u, 0xf5cfa434u, 0xf67a416cu, 0xf7255511u, 0xf7d0df73u, 0xf87ce0e6u, 0xf92959bbu, 0xf9d64a47u,
+    0xfa83b2dbu, 0xfb3193ccu, 0xfbdfed6du, 0xfc8ec011u, 0xfd3e0c0du, 0xfdedd1b5u, 0xfe9e115cu, 0xff4ecb59u,};
 
 struct Weigher {
     float hm;          // m / 2
     float ch, cl;      // 2 log2(e) / T as a sum of two floats
     float m, inv_w;    // bins: (m - z) / 2 * inv_w, 2048 bins up to m - z = 30.5 T (weights there round to 0)
-    const unsigned long long* tab;  // EXP2_32 in shared memory
-    __device__ __forceinline__ Weigher(float m_, float T, const unsigned long long* t) : m(m_), tab(t) {
+    const uint32_t* tab;  // EXP2_256 in shared memory
+    __device__ __forceinline__ Weigher(float m_, float T, const uint32_t* t) : m(m_), tab(t) {
         hm = 0.5f * m_;
         const double c = 2.8853900817779268 / double(T);
         ch = float(c);
         cl = float(c - double(ch));
         inv_w = fminf(float(UB) / (15.25f * T), 3.0e38f);
     }
-    // round(2^42 exp((z - m) / T)), z <= m.  The exponent (z - m) log2(e) / T as a sum of two
+    // 2^42 exp((z - m) / T), z <= m, rounded.  The exponent (z - m) log2(e) / T as a sum of two
     // floats (halved operands, so that the difference cannot overflow; its rounding error
-    // by the two-sum); split into n + j / 32 + r, |r| <= 1/64; 2^r - 1 as the product r ln 2 in two
-    // floats plus a cubic remainder in one; then integers.  About 45 instructions.
+    // by the two-sum); split into n + j / 256 + r, |r| <= 1/512; 2^r - 1 as a cubic in float32 (below
+    // 2^-9, so its rounding is 2^-33 of the weight); the table's 2^(j / 256) times that in
+    // integers.  About 36 instructions; with a table of 32 and 2^r - 1 in two floats it
+    // took 58 for a relative 4e-11.
     __device__ __forceinline__ unsigned long long weight_of(float z) const {
         const float h = 0.5f * z;
         const float d = __fsub_rn(h, hm), bb = __fsub_rn(d, h);
@@ -178,24 +229,14 @@ struct Weigher {
         float yl = fmaf(d, ch, -yh);
         yl = fmaf(d, cl, yl);
         yl = fmaf(dl, ch, yl);
-        const float t = fmaf(yh, 32.f, 12582912.f);  // + 1.5 * 2^23: the nearest integer in the low bits
+        const float t = fmaf(yh, 256.f, 12582912.f);  // + 1.5 * 2^23: the nearest integer in the low bits
         const int q = __float_as_int(t) - 0x4B400000;
-        const float r0 = fmaf(__fsub_rn(t, 12582912.f), -0.03125f, yh);
-        const float r = __fadd_rn(r0, yl), rl = __fsub_rn(yl, __fsub_rn(r, r0));
-        constexpr float L = 0.693147182464599609375f, LL = -1.904654323148236017e-9f;  // ln 2
-        const float sh = __fmul_rn(r, L);
-        float sl = fmaf(r, L, -sh);
-        sl = fmaf(r, LL, sl);
-        sl = fmaf(rl, L, sl);
-        const float c = fmaf(r, fmaf(r, 0.009618129107628477f, 0.05550410866482158f), 0.2402265069591007f);
-        sl = fmaf(__fmul_rn(r, r), c, sl);
-        // 2^r - 1 in units of 2^-36
-        const int s = __float2int_rn(sh * 0x1p36f) + (__float_as_int(fmaf(sl, 0x1p36f, 12582912.f)) - 0x4B400000);
-        const unsigned long long tj = tab[q & 31];
-        const long long prod = (long long)int(tj >> 12) * s + (1 << 23);
-        const unsigned long long v = tj + (unsigned long long)(prod >> 24);
-        const int n = -(q >> 5);
-        return (v + ((1ull << n) >> 1)) >> n;
+        const float r = __fadd_rn(fmaf(__fsub_rn(t, 12582912.f), -0.00390625f, yh), yl);
+        const float s = __fmul_rn(r, fmaf(r, fmaf(r, 0.05550410866482158f, 0.2402265069591007f), 0.6931471805599453f));
+        const uint32_t tj = tab[q & 255];
+        const long long p = (long long)int(tj >> 1) * __float2int_rn(s * 0x1p33f) + (1ll << 31);
+        const uint32_t v = tj + uint32_t(p >> 32);
+        return (((unsigned long long)v << 12 >> -(q >> 8)) + 1) >> 1;
     }
     // Bin of z: 0 the largest.  Each step is monotone in z, so a lower bin means larger z.
     __device__ __forceinline__ int bin_of(float z) const {
@@ -227,28 +268,32 @@ __device__ __forceinline__ unsigned long long mul_frac(float f, unsigned long lo
 
 // Words every CTA holds; other CTAs of the cluster write `flag`, `cmass` and the totals.
 struct UCtl {
-    unsigned long long tab[32];
+    uint32_t tab[256];
     unsigned long long red[UNW];
     uint32_t redc[UNW];
     unsigned long long cmass[MAX_CLUSTER];
     unsigned long long above, in_mass;  // find_bin's results
     uint32_t above_cnt, in_cnt;
     int bin;
-    int n;               // candidates
+    int n;               // entries of the list
     int nlive;
-    unsigned long long fmass;
-    int flag;
+    int flag, flag2;
+    int cn[MAX_CLUSTER]; // every CTA's entries
+    int wcnt[64];
     int seg;
     unsigned long long rest;
 };
 
 struct USmem {
     static constexpr size_t CTL = 0;
-    static constexpr size_t LKEY = align16(sizeof(UCtl));
+    static constexpr size_t LKEY = align16(sizeof(UCtl));        // this CTA's list: keys, places, weights
     static constexpr size_t LPOS = LKEY + UCAP * 4;
     static constexpr size_t LW = LPOS + UCAP * 4;
-    static constexpr size_t LK = LW + UCAP * 8;
-    static constexpr size_t HIST = LK + UCAP * 8;     // masses, counts, their totals; later the segments' masses
+    static constexpr size_t AKEY = LW + UCAP * 8;                // the cluster's list: keys, weights
+    static constexpr size_t AW = AKEY + UCAP * 4;
+    static constexpr size_t QZ = AW + UCAP * 8;                  // queues: logits, segments
+    static constexpr size_t QS = QZ + UNW * UQ * 4;
+    static constexpr size_t HIST = QS + UNW * UQ * 4;            // masses, counts, their totals; later the segments' masses
     static constexpr size_t HIST_BYTES = size_t(UB) * 24;
     static __host__ __device__ size_t seg_at(int nsc) { return HIST + (size_t(nsc) * 8 > HIST_BYTES ? align16(size_t(nsc) * 8) : HIST_BYTES); }
     static __host__ __device__ size_t total(int nsc, int ls) { return seg_at(nsc) + align16(size_t(ls) * 4); }
@@ -284,6 +329,52 @@ __device__ __forceinline__ void block_prefix(unsigned long long& v, uint32_t& n,
     for (int w = 0; w < warp; ++w) b += c->red[w], bn += c->redc[w];
     v = iv - v + b;
     n = in - n + bn;
+}
+
+// The same of a count alone, and of a mass alone with the total returned.
+__device__ __forceinline__ uint32_t block_prefix_count(uint32_t n, UCtl* c) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const uint32_t in = warp_incl_scan_t(n, lane);
+    __syncthreads();
+    if (lane == 31) c->redc[warp] = in;
+    __syncthreads();
+    const uint32_t w = c->redc[lane & (UNW - 1)];
+    return in - n + warp_sum_i(lane < warp ? int(w) : 0);
+}
+__device__ __forceinline__ unsigned long long block_prefix_mass(unsigned long long& v, UCtl* c) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const unsigned long long iv = warp_incl_scan_u64(v, lane);
+    __syncthreads();
+    if (lane == 31) c->red[warp] = iv;
+    __syncthreads();
+    unsigned long long b = 0, all = 0;
+#pragma unroll
+    for (int w = 0; w < UNW; ++w) {
+        const unsigned long long x = c->red[w];
+        if (w < warp) b += x;
+        all += x;
+    }
+    v = iv - v + b;
+    return all;
+}
+
+// The first bin at which the running count reaches k >= 1 (UB: never), in c->bin.  Block-wide.
+__device__ __forceinline__ void find_count(const uint32_t* cnt, uint32_t k, UCtl* c) {
+    constexpr int PER = UB / UNT;
+    const int b0 = threadIdx.x * PER;
+    uint32_t x[PER], n = 0;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) n += x[i] = cnt[b0 + i];
+    if (threadIdx.x == 0) c->bin = UB;
+    uint32_t before = block_prefix_count(n, c);
+    if (before < k && before + n >= k) {
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            if (before < k && before + x[i] >= k) c->bin = b0 + i;
+            before += x[i];
+        }
+    }
+    __syncthreads();
 }
 
 // The first bin at which the running mass (by_mass) or count reaches target >= 1; the sums before it
@@ -335,7 +426,8 @@ __global__ void __launch_bounds__(UNT, 2) uniform_kernel(const UniformArgs a) {
     uint32_t* lkey = reinterpret_cast<uint32_t*>(smem + USmem::LKEY);
     int* lpos = reinterpret_cast<int*>(smem + USmem::LPOS);
     unsigned long long* lw = reinterpret_cast<unsigned long long*>(smem + USmem::LW);
-    unsigned long long* lk = reinterpret_cast<unsigned long long*>(smem + USmem::LK);
+    uint32_t* akey = reinterpret_cast<uint32_t*>(smem + USmem::AKEY);
+    unsigned long long* aw = reinterpret_cast<unsigned long long*>(smem + USmem::AW);
     unsigned long long* hmass = reinterpret_cast<unsigned long long*>(smem + USmem::HIST);
     unsigned long long* tmass = hmass + UB;
     uint32_t* hcnt = reinterpret_cast<uint32_t*>(tmass + UB);
@@ -344,23 +436,27 @@ __global__ void __launch_bounds__(UNT, 2) uniform_kernel(const UniformArgs a) {
     uint32_t* segs = reinterpret_cast<uint32_t*>(smem + USmem::seg_at(a.nsc));
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int C = int(cluster_nctarank()), rank = int(cluster_ctarank()), b = int(cluster_id_x());
-    if (tid < 32) c->tab[tid] = EXP2_32[tid];
-    if (tid == 0) c->n = 0, c->nlive = 0, c->flag = 0;
-    cluster_sync();  // every CTA of the cluster runs before another writes into its memory
-    grid_dependency_wait();
-    allow_dependents();
-
-    // ---- parameters; the row's maximum
+    // The parameters were written before the scan began (it waits for its predecessors before
+    // it lets this launch start), so they are read while it runs.
     const int r = a.indices ? a.indices[b] : b;
     const float u = a.u[b];
     const float temp = a.temperature ? a.temperature[b] : 1.f;
     const int k = a.top_k ? a.top_k[b] : 0;
     const float p = a.top_p ? a.top_p[b] : 1.f;
     const float mp = a.min_p ? a.min_p[b] : 0.f;
+    if (tid < 256) c->tab[tid] = EXP2_256[tid];
+    if (tid == 0) c->n = 0, c->nlive = 0, c->flag = 0, c->flag2 = 0;
+    for (int i = tid; i < UB; i += UNT) hcnt[i] = 0;
+    cluster_sync();  // every CTA of the cluster runs before another writes into its memory
+    grid_dependency_wait();
+    allow_dependents();
+
+    // ---- the row's maximum
     bool bad = r < 0 || r >= a.batch_in || !(u >= 0.f && u < 1.f) || !(temp >= 1.17549435e-38f) || !(p == p) || !(mp <= 1.f);
     uint32_t kmax = 0;
     if (!bad) {
         const R row(a.x, a.stride, r, a.V);
+#pragma unroll 4
         for (int s = tid; s < row.nseg; s += UNT) {
             const uint32_t sk = a.skey[int64_t(r) * a.ls + s];
             segs[s] = sk;
@@ -369,183 +465,438 @@ __global__ void __launch_bounds__(UNT, 2) uniform_kernel(const UniformArgs a) {
         kmax = warp_max_u(kmax);
         if (lane == 0) c->redc[warp] = kmax;
         __syncthreads();
-#pragma unroll
-        for (int w = 0; w < UNW; ++w) kmax = max(kmax, c->redc[w]);
+        kmax = warp_max_u(c->redc[lane & (UNW - 1)]);
         bad = kmax >= KEY_PINF || kmax <= KEY_NINF;
     }
     if (bad) {  // the same in every thread of the cluster
         if (rank == 0 && tid == 0) a.out_token[b] = -1, a.out_valid[b] = 0;
         return;
     }
-    __syncthreads();
     const R row(a.x, a.stride, r, a.V);
     const Weigher wt(from_logit_key(kmax), temp, c->tab);
     const unsigned long long ONE = 1ull << 42;
     const bool has_k = k > 0 && k < a.V, has_p = p < 1.f;
-    // min-p: w >= mp * max w; the integers are compared, rounded up
+    const bool joint = a.order == FS_ORDER_JOINT || !has_k;  // top-p is measured against the whole row
+    // min-p: w >= mp * max w; the integers are compared, rounded up.  floor_key: no element below it
+    // passes (ln and the product within 2^-18 of their size).
     unsigned long long wmin = 1;
-    if (mp > 0.f && mp < 1.f) {
-        bool cut;
-        wmin = mul_frac(mp, ONE, cut);
+    uint32_t floor_key = KEY_NINF + 1;
+    if (mp > 0.f) {
+        bool cut = false;
+        wmin = mp < 1.f ? mul_frac(mp, ONE, cut) : ONE;
         wmin = max(1ull, wmin + (cut ? 1 : 0));
-    } else if (mp >= 1.f) {
-        wmin = ONE;
+        const float drop = temp * logf(mp);
+        const float zf = wt.m + drop - 0x1p-18f * (fabsf(wt.m) + fabsf(drop));
+        if (zf >= -3.402823466e38f) floor_key = max(floor_key, ukey(zf));
     }
     // This CTA's segments.
     const int per = (row.nseg + C - 1) / C;
     const int s0 = min(row.nseg, rank * per), s1 = min(row.nseg, s0 + per);
-    // fn(z, position) over the elements of this CTA's segments.
-    auto each = [&](auto fn) {
+    // fn(z) over the elements of this CTA's segments whose maximum passes.
+    auto each = [&](auto pass, auto fn) {
         for (int s = s0 + warp; s < s1; s += UNW * 2) {
-            const bool two = s + UNW < s1;
-            const uint4 v0 = row.load(s, lane);
-            uint4 v1 = v0;
+            const bool one = pass(segs[s]), two = s + UNW < s1 && pass(segs[s + UNW]);
+            uint4 v0, v1;
+            if (one) v0 = row.load(s, lane);
             if (two) v1 = row.load(s + UNW, lane);
             float z[R::N];
-            unpack(v0, z, T());
+            if (one) {
+                unpack(v0, z, T());
 #pragma unroll
-            for (int e = 0; e < R::N; ++e) fn(z[e]);
+                for (int e = 0; e < R::N; ++e) fn(z[e], s, e);
+            }
             if (two) {
                 unpack(v1, z, T());
 #pragma unroll
-                for (int e = 0; e < R::N; ++e) fn(z[e]);
+                for (int e = 0; e < R::N; ++e) fn(z[e], s + UNW, e);
             }
         }
     };
-    auto clear = [&]() {
-        for (int i = tid; i < UB; i += UNT) hmass[i] = 0, hcnt[i] = 0;
-        __syncthreads();
-    };
-    // The cluster's histograms summed into every CTA's totals.
-    auto totals = [&]() {
+    auto all = [](uint32_t) { return true; };
+    // The row's mass from exact weights.  Cluster-wide.
+    auto exact_mass = [&]() {
+        unsigned long long v = 0, M = 0;
+        each(all, [&](float z, int, int) { v += wt.weight_of(z); });
+        v = block_sum(v, c);
+        if (tid < C) peer(c->cmass, tid)[rank] = v;
         cluster_sync();
-        const int n = UB / C;
-        for (int i = rank * n + tid; i < (rank + 1) * n; i += UNT) {
-            unsigned long long v = 0;
-            uint32_t m = 0;
-            for (int q = 0; q < C; ++q) v += *peer(hmass + i, q), m += *peer(hcnt + i, q);
-            for (int q = 0; q < C; ++q) *peer(tmass + i, q) = v, *peer(tcnt + i, q) = m;
-        }
-        cluster_sync();
+        for (int q = 0; q < C; ++q) M += c->cmass[q];
+        return M;
     };
 
-    // ---- the row's total mass, where top-p is measured against it
-    const bool joint = a.order == FS_ORDER_JOINT || !has_k;
-    // ---- small top-k: everything in a list
+    // ---- small sets: everything in a list
     bool small = false;
-    if (has_k && k <= UCAP) {
-        for (int i = tid; i < UB; i += UNT) hcnt[i] = 0;
-        __syncthreads();
-        for (int s = tid; s < row.nseg; s += UNT) atomicAdd(&hcnt[wt.bin_of(from_logit_key(segs[s]))], 1u);
-        __syncthreads();
-        find_bin(nullptr, hcnt, false, (unsigned long long)k, c);
-        const int kb = c->bin;
+    const bool try_k = has_k && k <= UCAP;
+    if (try_k || (mp > 0.f && !has_k)) {
+        int kb = UB;
+        if (try_k) {
+            for (int s = tid; s < row.nseg; s += UNT) atomicAdd(&hcnt[wt.bin_of(from_logit_key(segs[s]))], 1u);
+            __syncthreads();
+            find_count(hcnt, uint32_t(k), c);
+            kb = c->bin;
+        }
+        // (top-p inside the top k is measured against all of the top k, min-p or not)
+        if (mp > 0.f && !(has_p && !joint)) kb = min(kb, wt.bin_of(from_logit_key(floor_key)));
         small = kb < UB - 1;  // the last bin has no weight, and UB means fewer segments than k
         if (small) {
             if (rank == 0) {
-                // The live segments, one per warp and turn; elements in bins up to kb.
+                // The live segments in order, then 64 of them at a time, four per warp: their elements in
+                // bins up to kb, counted, placed by a prefix over the segments, written in index order.
                 int* live = reinterpret_cast<int*>(hmass);
-                for (int s = tid; s < row.nseg; s += UNT)
+                const int chunk = (row.nseg + UNT - 1) / UNT;
+                const int f0 = min(row.nseg, tid * chunk), f1 = min(row.nseg, f0 + chunk);
+                uint32_t nl = 0;
+                for (int s = f0; s < f1; ++s) nl += wt.bin_of(from_logit_key(segs[s])) <= kb;
+                uint32_t at = block_prefix_count(nl, c);
+                if (tid == UNT - 1) c->nlive = int(at + nl);
+                for (int s = f0; s < f1 && nl; ++s)
                     if (wt.bin_of(from_logit_key(segs[s])) <= kb) {
-                        const int at = atomicAdd(&c->nlive, 1);
                         if (at < UCAP) live[at] = s;
+                        ++at;
                     }
                 __syncthreads();
                 // each live segment holds a candidate, so more of them than UCAP are too many
-                const int nl = min(c->nlive, UCAP);
-                for (int i = warp; i < nl; i += UNW) {
-                    float z[R::N];
-                    unpack(row.load(live[i], lane), z, T());
+                const int n_live = min(c->nlive, UCAP);
+                int base = 0;
+                for (int i0 = 0; i0 < n_live; i0 += 64) {
+                    float z[4][R::N];
+                    uint4 v[4];
 #pragma unroll
-                    for (int e = 0; e < R::N; ++e) {
-                        if (wt.bin_of(z[e]) <= kb) {
-                            const int at = atomicAdd(&c->n, 1);
-                            if (at < UCAP) {
-                                lkey[at] = ukey(z[e]);
-                                lpos[at] = live[i] * R::SEG + lane * R::N + e;
-                                lw[at] = wt.weight_of(z[e]);
-                            }
+                    for (int j = 0; j < 4; ++j)
+                        if (i0 + warp * 4 + j < n_live) v[j] = row.load(live[i0 + warp * 4 + j], lane);
+                    int pre[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        int m = 0;
+                        if (i0 + warp * 4 + j < n_live) {
+                            unpack(v[j], z[j], T());
+#pragma unroll
+                            for (int e = 0; e < R::N; ++e) m += wt.bin_of(z[j][e]) <= kb;
+                        }
+                        const int incl = warp_incl_scan_i(m, lane);
+                        pre[j] = incl - m;
+                        if (lane == 31) c->wcnt[warp * 4 + j] = incl;
+                    }
+                    __syncthreads();
+                    const int c0 = c->wcnt[lane * 2], c1 = c->wcnt[lane * 2 + 1];
+                    const int incl = warp_incl_scan_i(c0 + c1, lane);
+                    const int total = __shfl_sync(FULL, incl, 31);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const int i = warp * 4 + j;
+                        int off = __shfl_sync(FULL, incl - c0 - c1, i >> 1);
+                        if (i & 1) off += __shfl_sync(FULL, c0, i >> 1);
+                        if (i0 + i < n_live) {
+                            int w = base + off + pre[j];
+#pragma unroll
+                            for (int e = 0; e < R::N; ++e)
+                                if (wt.bin_of(z[j][e]) <= kb) {
+                                    if (w < UCAP) {
+                                        lkey[w] = ukey(z[j][e]);
+                                        lpos[w] = live[i0 + i] * R::SEG + lane * R::N + e;
+                                    }
+                                    ++w;
+                                }
                         }
                     }
+                    base += total;
+                    __syncthreads();
                 }
-                __syncthreads();
-                if (tid < C) *peer(&c->flag, tid) = c->nlive <= UCAP && c->n <= UCAP ? 1 : 0;
+                if (tid == 0) c->n = base;
+                if (tid < C) *peer(&c->flag, tid) = c->nlive <= UCAP && base <= UCAP ? 1 : 0;
             }
             cluster_sync();
             small = c->flag != 0;
         }
     }
-    unsigned long long M = 0;
-    if (small && has_p && a.order == FS_ORDER_JOINT) {
-        unsigned long long v = 0;
-        each([&](float z) { v += wt.weight_of(z); });
-        v = block_sum(v, c);
-        if (tid < C) peer(c->cmass, tid)[rank] = v;
-        cluster_sync();
-        for (int q = 0; q < C; ++q) M += c->cmass[q];
-    }
     if (small) {
+        const bool whole = has_p && joint;   // M is needed
+        float Mf = 0.f;
+        unsigned long long M = 0;
+        if (whole) {
+            // float32, relative to the maximum.  Each exponent y is off by 4 2^-24 |y|, and most of
+            // a row's mass lies above y = -log2(V) >= -21: 2^-18 of the mass; 2^y by 2^-22; at most 40 additions
+            // in a row (a double takes the long runs): under 2^-17 together.
+            double run = 0.0;
+            const float cc = 1.44269504f / temp;
+            if (a.ssum) {
+                for (int s = tid; s < row.nseg; s += UNT) {
+                    const float z = from_logit_key(segs[s]);
+                    if (z > -INFINITY) run += double(a.ssum[int64_t(r) * a.ls + s] * exp2_approx((z - wt.m) * cc));
+                }
+            } else {
+                float part = 0.f;
+                each(all, [&](float z, int, int e) {
+                    part += z > -INFINITY ? exp2_approx((z - wt.m) * cc) : 0.f;
+                    if (e == R::N - 1) run += double(part), part = 0.f;
+                });
+            }
+            float v = warp_sum(float(run));
+            if (lane == 0) c->redc[warp] = __float_as_uint(v);
+            __syncthreads();
+            v = warp_sum(lane < UNW ? __uint_as_float(c->redc[lane]) : 0.f);
+            if (!a.ssum) {
+                if (tid < C) peer(c->cmass, tid)[rank] = __float_as_uint(v);
+                cluster_sync();
+                for (int q = 0; q < C; ++q) Mf += __uint_as_float(uint32_t(c->cmass[q]));
+            } else {
+                Mf = v;
+            }
+        }
+        int n = 0, tpc = 1;
+        if (rank == 0) {
+            n = c->n;
+            for (int i = tid; i < n; i += UNT) lw[i] = wt.weight_of(from_logit_key(lkey[i]));
+            __syncthreads();
+            // Threads per candidate (a power of two, within a warp), each over its share of the list.
+            while (tpc < 32 && tpc * 2 * n <= UNT) tpc *= 2;
+        }
+        const int sub = tid % tpc;
+        constexpr int PER = UCAP / UNT;   // candidates per thread, at most
+        unsigned long long above[PER], wi[PER];
+        bool keep[PER];
+        bool exact = !whole;
+        for (int turn = 0; turn < 2; ++turn) {
+            bool unsure = false;
+            if (rank == 0 && turn == 0) {
+#pragma unroll
+                for (int x = 0; x < PER; ++x) {
+                    const int i = tid / tpc + x * UNT;
+                    wi[x] = i < n ? lw[i] : 0;
+                    keep[x] = i < n;
+                    above[x] = 0;
+                    if ((has_k || has_p) && x * UNT < n) {
+                        const uint32_t ki = i < n ? lkey[i] : 0xffffffffu;
+                        int cnt = 0;
+#pragma unroll 4
+                        for (int j = sub; j < n; j += tpc)
+                            if (lkey[j] > ki) ++cnt, above[x] += lw[j];
+                        for (int d = 1; d < tpc; d *= 2) {
+                            cnt += __shfl_xor_sync(FULL, cnt, d);
+                            above[x] += __shfl_xor_sync(FULL, above[x], d);
+                        }
+                        if (has_k) keep[x] = keep[x] && cnt < k;  // ties with the k-th are kept
+                    }
+                }
+            }
+            if (rank == 0 && has_p && !whole) {
+                unsigned long long F = 0;
+#pragma unroll
+                for (int x = 0; x < PER; ++x) F += keep[x] && sub == 0 ? wi[x] : 0;
+                M = block_sum(F, c);
+            }
+            if (rank == 0 && has_p) {
+                bool cut = false;
+                unsigned long long G = 0;
+                float lo = 0.f, hi = 0.f;
+                if (exact) {
+                    G = p > 0.f ? mul_frac(p, M, cut) : 0;
+                    G = max(1ull, G + (cut ? 1 : 0));
+                } else {
+                    const float t = p > 0.f ? p * Mf * 0x1p42f : 0.f;
+                    lo = t * (1.f - 0x1p-16f), hi = t * (1.f + 0x1p-16f);
+                    unsure = !(Mf > 0.f && Mf < INFINITY);
+                }
+#pragma unroll
+                for (int x = 0; x < PER; ++x) {
+                    if (exact) {
+                        keep[x] = keep[x] && above[x] < G;
+                    } else if (keep[x] && wi[x] >= wmin) {
+                        const float f = float(above[x]);
+                        if (p > 0.f) unsure |= f >= lo && f <= hi;
+                        else keep[x] = above[x] == 0;
+                        if (p > 0.f && f > hi) keep[x] = false;
+                    }
+                }
+            }
+            if (exact) break;
+            // A candidate too close to call: the row's mass is summed exactly.
+            if (rank == 0) {
+                unsure = __syncthreads_or(unsure);
+                if (tid < C) *peer(&c->flag2, tid) = unsure ? 1 : 0;
+            }
+            cluster_sync();
+            if (!c->flag2) break;
+            M = exact_mass();
+            exact = true;
+        }
         if (rank != 0) return;
-        const int n = c->n;
-        // Threads per candidate (a power of two, within a warp), each over its share of the list.
-        int tpc = 1;
-        while (tpc < 32 && tpc * 2 * n <= UNT) tpc *= 2;
-        const int i = tid / tpc, sub = tid % tpc;
-        const uint32_t ki = i < n ? lkey[i] : 0xffffffffu;
-        int cnt = 0;
-        unsigned long long above = 0;
-        for (int j = sub; j < n; j += tpc)
-            if (lkey[j] > ki) ++cnt, above += lw[j];
-        for (int d = 1; d < tpc; d *= 2) {
-            cnt += __shfl_xor_sync(FULL, cnt, d);
-            above += __shfl_xor_sync(FULL, above, d);
+        // ---- the draw: candidates are in index order
+        unsigned long long own[PER], v = 0;
+        if (tpc == 1) {
+            // thread t holds candidates t and t + UNT: written back, then taken as neighbours
+#pragma unroll
+            for (int x = 0; x < PER; ++x) {
+                const int i = tid + x * UNT;
+                if (i < n) aw[i] = keep[x] && wi[x] >= wmin ? wi[x] : 0;
+            }
+        } else if (sub == 0 && tid / tpc < n) {
+            aw[tid / tpc] = keep[0] && wi[0] >= wmin ? wi[0] : 0;
         }
-        bool keep = i < n && cnt < k;  // ties with the k-th are kept
-        const unsigned long long wi = i < n ? lw[i] : 0;
-        if (has_p) {
-            const unsigned long long F = joint ? M : block_sum(keep && sub == 0 ? wi : 0, c);
-            bool cut = false;
-            unsigned long long G = p > 0.f ? mul_frac(p, F, cut) : 0;
-            G = max(1ull, G + (cut ? 1 : 0));
-            keep = keep && above < G;
+        __syncthreads();
+#pragma unroll
+        for (int x = 0; x < PER; ++x) {
+            const int i = tid * PER + x;
+            own[x] = i < n ? aw[i] : 0;
+            v += own[x];
         }
-        keep = keep && wi >= wmin;
-        const unsigned long long kept = keep ? wi : 0;
-        if (i < n && sub == 0) lk[i] = kept;
-        const unsigned long long Z = block_sum(sub == 0 ? kept : 0, c);
+        const unsigned long long mine = v;
+        const unsigned long long Z = block_prefix_mass(v, c);
+        if (Z == 0) {
+            if (tid == 0) a.out_token[b] = -1, a.out_valid[b] = 0;
+            return;
+        }
         bool cut;
         const unsigned long long t = u > 0.f ? mul_frac(u, Z, cut) : 0;
-        unsigned long long incl = 0;
-        const int pi = i < n ? lpos[i] : -1;
-        for (int j = sub; j < n; j += tpc)
-            if (lpos[j] <= pi) incl += lk[j];
-        for (int d = 1; d < tpc; d *= 2) incl += __shfl_xor_sync(FULL, incl, d);
-        if (keep && sub == 0 && incl > t && incl - kept <= t) a.out_token[b] = pi - row.a0, a.out_valid[b] = 1;
-        if (Z == 0 && tid == 0) a.out_token[b] = -1, a.out_valid[b] = 0;
+        if (v <= t && t - v < mine) {
+#pragma unroll
+            for (int x = 0; x < PER; ++x) {
+                if (v <= t && t - v < own[x]) a.out_token[b] = lpos[tid * PER + x] - row.a0, a.out_valid[b] = 1;
+                v += own[x];
+            }
+        }
         return;
     }
 
-    // ---- thresholds from histograms
-    uint32_t theta = KEY_NINF + 1;
-    const bool want_k = has_k;
-    if (want_k || has_p) {
-        clear();
-        each([&](float z) {
-            const int q = wt.bin_of(z);
-            const unsigned long long w = wt.weight_of(z);
-            if (w) add64(hmass + q, w);
-            atomicAdd(hcnt + q, 1u);
-        });
-        totals();
+    // ---- other sets: thresholds from histograms
+    uint32_t theta = floor_key;
+    bool summed = false;   // the segments' masses are there
+    if (has_k || has_p) {
+        for (int i = tid; i < UB; i += UNT) hmass[i] = 0, hcnt[i] = 0;
+        __syncthreads();
+        if (has_k)
+            each(all, [&](float z, int, int) {
+                const int q = wt.bin_of(z);
+                const unsigned long long w = wt.weight_of(z);
+                if (w) add64(hmass + q, w);
+                atomicAdd(hcnt + q, 1u);
+            });
+        else
+            each(all, [&](float z, int, int) {
+                const unsigned long long w = wt.weight_of(z);
+                if (w) add64(hmass + wt.bin_of(z), w);
+            });
+        // The cluster's histograms summed into every CTA's totals.
+        cluster_sync();
+        {
+            const int n = UB / C;
+            for (int i = rank * n + tid; i < (rank + 1) * n; i += UNT) {
+                unsigned long long v = 0;
+                uint32_t m = 0;
+                for (int q = 0; q < C; ++q) v += *peer(hmass + i, q), m += *peer(hcnt + i, q);
+                for (int q = 0; q < C; ++q) *peer(tmass + i, q) = v, *peer(tcnt + i, q) = m;
+            }
+        }
+        cluster_sync();
         // The largest key whose elements at or above it reach `target` (count or mass); the mass at
-        // or above it goes into `fmass`.  Keys are narrowed by histograms inside the bin.
-        auto search = [&](bool by_mass, unsigned long long target, unsigned long long& fmass) -> uint32_t {
+        // or above it goes into `fmass`.  With `last`, the masses of this CTA's segments are
+        // left in smass, of elements at or above that key and `also`.
+        auto search = [&](bool by_mass, unsigned long long target, unsigned long long& fmass, bool last,
+                          uint32_t also) -> uint32_t {
             find_bin(tmass, tcnt, by_mass, target, c);
             const int qb = c->bin;
             if (qb >= UB - 1) return 0;  // reached only among elements without weight
             unsigned long long above = c->above;
             unsigned long long above_t = by_mass ? c->above : c->above_cnt;
             fmass = above + c->in_mass;
+            __syncthreads();
+            if (tid == 0) c->n = 0;
+            if (last)
+                for (int i = tid; i < s1 - s0; i += UNT) smass[i] = 0;
+            __syncthreads();
+            // The bin's elements into this CTA's list; the weights of those above it summed, 32 at a time.
+            float* qz = reinterpret_cast<float*>(smem + USmem::QZ) + warp * UQ;
+            int* qs = reinterpret_cast<int*>(smem + USmem::QS) + warp * UQ;
+            int queued = 0;
+            auto weigh = [&](int m) {
+                __syncwarp();
+                if (lane < m) {
+                    const unsigned long long w = wt.weight_of(qz[lane]);
+                    if (w >= wmin) add64(smass + qs[lane], w);
+                }
+                __syncwarp();
+            };
+            each([&](uint32_t key) { return wt.bin_of(from_logit_key(key)) <= qb; }, [&](float z, int s, int e) {
+                const int q = wt.bin_of(z);
+                if (q == qb) {
+                    const int at = atomicAdd(&c->n, 1);
+                    if (at < UCAP) {
+                        lkey[at] = ukey(z);
+                        lpos[at] = s - s0;
+                    }
+                }
+                if (last) {
+                    const unsigned in = __ballot_sync(FULL, q < qb && ukey(z) >= also);
+                    if (in) {
+                        if (in >> lane & 1) {
+                            const int at = queued + __popc(in & ((1u << lane) - 1));
+                            qz[at] = z;
+                            qs[at] = s - s0;
+                        }
+                        queued += __popc(in);
+                        if (queued >= 32) {
+                            weigh(32);
+                            queued -= 32;
+                            const float mz = lane < queued ? qz[32 + lane] : 0.f;
+                            const int ms = lane < queued ? qs[32 + lane] : 0;
+                            __syncwarp();
+                            if (lane < queued) qz[lane] = mz, qs[lane] = ms;
+                        }
+                    }
+                }
+            });
+            if (last) weigh(queued);
+            __syncthreads();
+            const int ln = c->n;
+            for (int i = tid; i < min(ln, UCAP); i += UNT) lw[i] = wt.weight_of(from_logit_key(lkey[i]));
+            if (tid < C) peer(c->cn, tid)[rank] = ln;
+            cluster_sync();
+            int n = 0;
+            for (int q = 0; q < C; ++q) n += c->cn[q];
+            if (n <= UCAP) {
+                // every CTA gathers the whole list and decides
+                int at = 0;
+                for (int q = 0; q < C; ++q) {
+                    for (int i = tid; i < c->cn[q]; i += UNT) akey[at + i] = *peer(lkey + i, q), aw[at + i] = *peer(lw + i, q);
+                    at += c->cn[q];
+                }
+                __syncthreads();
+                int tpc = 1;
+                while (tpc < 32 && tpc * 2 * n <= UNT) tpc *= 2;
+                uint32_t least = 0xffffffffu;
+                unsigned long long kept = 0;
+                for (int i0 = 0; i0 < n; i0 += UNT / tpc) {
+                    const int i = i0 + tid / tpc;
+                    const uint32_t ki = i < n ? akey[i] : 0xffffffffu;
+                    int cnt = 0;
+                    unsigned long long m = 0;
+#pragma unroll 4
+                    for (int j = tid % tpc; j < n; j += tpc)
+                        if (akey[j] > ki) ++cnt, m += aw[j];
+                    for (int d = 1; d < tpc; d *= 2) {
+                        cnt += __shfl_xor_sync(FULL, cnt, d);
+                        m += __shfl_xor_sync(FULL, m, d);
+                    }
+                    if (i < n && (by_mass ? above_t + m : above_t + cnt) < target) {
+                        least = min(least, ki);
+                        if (tid % tpc == 0) kept += aw[i];
+                    }
+                }
+                fmass = above + block_sum(kept, c);
+                least = warp_min_u(least);
+                __syncthreads();
+                if (lane == 0) c->redc[warp] = least;
+                __syncthreads();
+                least = warp_min_u(c->redc[lane & (UNW - 1)]);
+                if (last) {
+                    for (int i = tid; i < ln; i += UNT)
+                        if (lkey[i] >= max(least, also) && lw[i] >= wmin) add64(smass + lpos[i], lw[i]);
+                    summed = true;
+                    __syncthreads();
+                }
+                cluster_sync();  // the lists have been read: they may be used again
+                return least;
+            }
             // Keys the bin can hold, with some slack for the rounding of its edges.
             const float wid = 2.f / wt.inv_w;
             const float lo = wt.m - float(qb + 1) * wid, hi = wt.m - float(qb) * wid;
@@ -555,10 +906,10 @@ __global__ void __launch_bounds__(UNT, 2) uniform_kernel(const UniformArgs a) {
             while (kh > kl) {
                 const int bits = 32 - __clz(kh - kl);
                 const int sh = bits > 11 ? bits - 11 : 0;
-                // the totals of the linear bins are needed again by a later search: own ones here
                 __syncthreads();
-                clear();
-                each([&](float z) {
+                for (int i = tid; i < UB; i += UNT) hmass[i] = 0, hcnt[i] = 0;
+                __syncthreads();
+                each([&](uint32_t key) { return key >= kl; }, [&](float z, int, int) {
                     const uint32_t key = ukey(z);
                     if (key >= kl && key <= kh && wt.bin_of(z) == qb) {
                         const int q = int((kh - key) >> sh);
@@ -566,7 +917,7 @@ __global__ void __launch_bounds__(UNT, 2) uniform_kernel(const UniformArgs a) {
                         atomicAdd(hcnt + q, 1u);
                     }
                 });
-                // Summed into the leader's own bins first, then copied to every CTA.
+                // Every CTA sums its share of the bins over the cluster, then hands it to all.
                 cluster_sync();
                 const int n = UB / C;
                 unsigned long long v[UB / UNT];
@@ -597,42 +948,48 @@ __global__ void __launch_bounds__(UNT, 2) uniform_kernel(const UniformArgs a) {
             }
             return kl;
         };
-        unsigned long long F = 0, dummy = 0;
+        unsigned long long F = 0, none = 0;
         for (int q = tid; q < UB; q += UNT) F += tmass[q];
         F = block_sum(F, c);
-        if (want_k) {
+        if (has_k) {
             unsigned long long fk = F;
-            theta = max(theta, search(false, (unsigned long long)k, fk));
+            theta = max(theta, search(false, (unsigned long long)k, fk, !has_p, floor_key));
             if (!joint) F = fk;
         }
         if (has_p) {
             bool cut = false;
             unsigned long long G = p > 0.f ? mul_frac(p, F, cut) : 0;
             G = max(1ull, G + (cut ? 1 : 0));
-            theta = max(theta, search(true, G, dummy));
+            theta = max(theta, search(true, G, none, true, theta));
         }
         cluster_sync();  // every CTA has read the others' bins: the segments' masses may take their place
     }
     // ---- kept mass of every segment, then of every CTA
     unsigned long long own = 0;
-    for (int s = s0 + warp; s < s1; s += UNW) {
-        unsigned long long v = 0;
-        if (segs[s] >= theta) {
-            float z[R::N];
-            unpack(row.load(s, lane), z, T());
+    if (summed) {
+        for (int i = tid; i < s1 - s0; i += UNT) own += smass[i];
+    } else {
+        for (int s = s0 + warp; s < s1; s += UNW) {
+            unsigned long long v = 0;
+            if (segs[s] >= theta) {
+                float z[R::N];
+                unpack(row.load(s, lane), z, T());
 #pragma unroll
-            for (int e = 0; e < R::N; ++e) {
-                if (ukey(z[e]) >= theta) {
-                    const unsigned long long w = wt.weight_of(z[e]);
-                    if (w >= wmin) v += w;
+                for (int e = 0; e < R::N; ++e) {
+                    if (ukey(z[e]) >= theta) {
+                        const unsigned long long w = wt.weight_of(z[e]);
+                        if (w >= wmin) v += w;
+                    }
                 }
+                v = warp_sum_u64(v);
             }
-            v = warp_sum_u64(v);
+            if (lane == 0) {
+                smass[s - s0] = v;
+                own += v;
+            }
         }
-        if (lane == 0) smass[s - s0] = v;
-        own += v;
     }
-    own = block_sum(lane == 0 ? own : 0, c);
+    own = block_sum(own, c);
     if (tid < C) peer(c->cmass, tid)[rank] = own;
     cluster_sync();
     unsigned long long Z = 0, before = 0;
@@ -651,11 +1008,10 @@ __global__ void __launch_bounds__(UNT, 2) uniform_kernel(const UniformArgs a) {
     const unsigned long long tl = t - before;
     const int ns = s1 - s0, each_t = (ns + UNT - 1) / UNT;
     unsigned long long v = 0;
-    uint32_t none = 0;
     const int f0 = min(ns, tid * each_t), f1 = min(ns, f0 + each_t);
     for (int s = f0; s < f1; ++s) v += smass[s];
     const unsigned long long mine = v;
-    block_prefix(v, none, c);
+    block_prefix_mass(v, c);
     if (v <= tl && tl - v < mine) {
         for (int s = f0; s < f1; ++s) {
             if (tl - v < smass[s]) {
@@ -723,7 +1079,8 @@ static fs_status run_uniform(UniformArgs& a, int C, void* stream) {
     cfg.blockDim = dim3(256, 1, 1);
     const int64_t trips = int64_t(a.batch_in) * ((a.ls + USEG_TRIP - 1) / USEG_TRIP);
     cfg.gridDim = dim3(unsigned(std::max<int64_t>(1, std::min<int64_t>((trips + 7) / 8, int64_t(sms) * 8))), 1, 1);
-    cudaError_t e = cudaLaunchKernelEx(&cfg, seg_max_kernel<T>, a);
+    cudaError_t e = a.ssum ? cudaLaunchKernelEx(&cfg, seg_max_kernel<T, true>, a)
+                           : cudaLaunchKernelEx(&cfg, seg_max_kernel<T, false>, a);
     if (e != cudaSuccess) return cuda_fail(e);
     cfg.numAttrs = 2;
     cfg.blockDim = dim3(UNT, 1, 1);
@@ -741,7 +1098,7 @@ fs_status fs_from_uniforms_workspace_bytes(int32_t dtype, int32_t batch_in, int3
     if (!bytes || batch_in < 0 || vocab < 1) return FS_ERR_INVALID_ARG;
     if (dtype != FS_F32 && dtype != FS_BF16 && dtype != FS_F16) return FS_ERR_INVALID_ARG;
     if (vocab > FS_MAX_VOCAB) return FS_ERR_UNSUPPORTED;
-    *bytes = size_t(batch_in) * size_t(fsd::row_segments(vocab, dtype == FS_F32 ? 4 : 2)) * 4;
+    *bytes = size_t(batch_in) * size_t(fsd::row_segments(vocab, dtype == FS_F32 ? 4 : 2)) * 8;
     return FS_OK;
 }
 
@@ -784,10 +1141,14 @@ fs_status fs_top_k_top_p_sampling_from_uniforms(const void* logits, int32_t dtyp
     a.out_valid = out_valid;
     a.skey = static_cast<uint32_t*>(workspace);
     a.ls = row_segments(vocab, es);
-    // CTAs per row: one where the list path needs only the summary (top-k without a total mass),
+    // The total mass of a row goes with its segments' maxima where a small set is measured
+    // against it and the row has one temperature.
+    if (!indices && order == FS_ORDER_JOINT && top_p && (top_k || min_p))
+        a.ssum = reinterpret_cast<float*>(a.skey + size_t(batch_in) * a.ls);
+    // CTAs per row: one where a small set needs only the summary,
     // else as many as fill the GPU with two per SM; a power of two.
     int C = 1;
-    const bool whole = !top_k || (order == FS_ORDER_JOINT && top_p);
+    const bool whole = (!top_k && (top_p || !min_p)) || (order == FS_ORDER_JOINT && top_p && !a.ssum);
     if (whole)
         while (C < 8 && int64_t(batch_out) * C * 2 <= 304 && a.ls >= C * 2 * 16) C *= 2;
     while (C < 8 && USmem::total((a.ls + C - 1) / C, a.ls) > (200u << 10)) C *= 2;

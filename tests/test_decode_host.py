@@ -48,8 +48,8 @@ def test_uniforms_arguments(ms):
     assert call(b_in=0, b_out=0, x=None, u=None) == 0
     n = ctypes.c_size_t(0)
     assert ms.lib.fs_from_uniforms_workspace_bytes(0, 64, 151936, ctypes.byref(n)) == 0
-    assert n.value == 64 * 4 * -(-(151936 + 3) // 128)
-    assert ms.lib.fs_from_uniforms_workspace_bytes(1, 2, 1, ctypes.byref(n)) == 0 and n.value == 8
+    assert n.value == 64 * 8 * -(-(151936 + 3) // 128)
+    assert ms.lib.fs_from_uniforms_workspace_bytes(1, 2, 1, ctypes.byref(n)) == 0 and n.value == 16
 
 
 def test_append_arguments(ms):

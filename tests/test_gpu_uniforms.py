@@ -1,5 +1,5 @@
 """Sampling from given uniforms (fs_top_k_top_p_sampling_from_uniforms) against the float64
-definition: the same token on every row.  The kernels decide on weights with a relative error of 4e-11
+definition: the same token on every row.  The kernels decide on weights with a relative error of 5e-10
 and an absolute one of 2^-43, so a row whose decisive mass lies within MARGIN of a border
 proves nothing and is left out; the drawn rows hardly ever do."""
 import numpy as np

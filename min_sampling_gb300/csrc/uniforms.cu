@@ -23,8 +23,7 @@
 //               candidate inside that bound sums its weights exactly.
 //   other sets  a histogram of the weights over 2048 bins linear in m - z finds the bin a
 //               threshold lies in; one more pass lists that bin's elements and sums the masses of
-//               the elements above it per segment (queued, so that a warp weighs 32 of
-//               them at a time); the list decides the threshold.  Bins too full for the list (16-bit
+//               the elements above it per segment; the list decides the threshold.  Bins too full for the list (16-bit
 //               logits tie by thousands) are narrowed by histograms over the order keys.
 //               The token is found from the segments' masses and one read of its segment.
 #include <algorithm>
@@ -41,7 +40,6 @@ constexpr int UNT = 512;          // threads of uniform_kernel
 constexpr int UNW = UNT / 32;
 constexpr int UB = 2048;          // histogram bins
 constexpr int UCAP = 1024;        // candidates in a list
-constexpr int UQ = 64;            // queued elements per warp
 constexpr int USEG_TRIP = 4;      // segments a warp has in flight
 constexpr uint32_t KEY_NINF = 0x007fffffu;  // order keys of -inf and +inf (a NaN's is above the latter or below the former)
 constexpr uint32_t KEY_PINF = 0xff800000u;
@@ -113,9 +111,45 @@ __device__ __forceinline__ void unpack(const uint4& w, float (&z)[8], __half) {
         z[2 * i + 1] = f.y;
     }
 }
+// Element e of a word, e not known at compile time.
+__device__ __forceinline__ float element(const uint4& w, int e, float) {
+    return __uint_as_float(e < 2 ? (e == 0 ? w.x : w.y) : (e == 2 ? w.z : w.w));
+}
+template <typename H>
+__device__ __forceinline__ uint32_t half_of(const uint4& w, int e, H) {
+    const uint32_t v = e < 4 ? (e < 2 ? w.x : w.y) : (e < 6 ? w.z : w.w);
+    return e & 1 ? v >> 16 : v & 0xffffu;
+}
+__device__ __forceinline__ float element(const uint4& w, int e, __nv_bfloat16 t) { return __uint_as_float(half_of(w, e, t) << 16); }
+__device__ __forceinline__ float element(const uint4& w, int e, __half t) {
+    return __half2float(__ushort_as_half((unsigned short)half_of(w, e, t)));
+}
+// The largest element of a word, NaN if one is.
+__device__ __forceinline__ float max_nan(float x, float y) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(y));
+    return r;
+}
+__device__ __forceinline__ float max_of(const uint4& w, float) {
+    return max_nan(max_nan(__uint_as_float(w.x), __uint_as_float(w.y)), max_nan(__uint_as_float(w.z), __uint_as_float(w.w)));
+}
+__device__ __forceinline__ float max_of(const uint4& w, __nv_bfloat16) {
+    uint32_t x, y;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(x) : "r"(w.x), "r"(w.y));
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(y) : "r"(w.z), "r"(w.w));
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(x) : "r"(x), "r"(y));
+    return max_nan(__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u));
+}
+__device__ __forceinline__ float max_of(const uint4& w, __half) {
+    uint32_t x, y;
+    asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(x) : "r"(w.x), "r"(w.y));
+    asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(y) : "r"(w.z), "r"(w.w));
+    asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(x) : "r"(x), "r"(y));
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&x));
+    return max_nan(f.x, f.y);
+}
 // Order key with -0 equal to +0.
 __device__ __forceinline__ uint32_t ukey(float z) { return logit_key(z + 0.f); }
-
 __device__ __forceinline__ float exp2_approx(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -146,20 +180,18 @@ __global__ void __launch_bounds__(256) seg_max_kernel(const UniformArgs a) {
 #pragma unroll
         for (int j = 0; j < USEG_TRIP; ++j) {
             if (s0 + j >= row.nseg) continue;
-            float z[R::N];
-            unpack(v[j], z, T());
-            uint32_t k = 0;
-#pragma unroll
-            for (int e = 0; e < R::N; ++e) k = max(k, z[e] == z[e] ? ukey(z[e]) : 0xffffffffu);
-            k = warp_max_u(k);
+            const float top = max_of(v[j], T());
+            const uint32_t k = warp_max_u(top == top ? ukey(top) : 0xffffffffu);
             if (lane == 0) a.skey[int64_t(r) * a.ls + s0 + j] = k;
             if (SUMS) {
+                // Without a finite logit nothing; a NaN (a row with one, or an infinite temperature) makes the sum NaN.
                 const float c = 1.44269504f / (a.temperature ? a.temperature[r] : 1.f), mc = from_logit_key(k);
-                float sum = 0.f;
+                float z[R::N], sum = 0.f;
+                unpack(v[j], z, T());
 #pragma unroll
-                for (int e = 0; e < R::N; ++e) sum += z[e] > -INFINITY ? exp2_approx((z[e] - mc) * c) : 0.f;
+                for (int e = 0; e < R::N; ++e) sum += exp2_approx((z[e] - mc) * c);
                 sum = warp_sum(sum);
-                if (lane == 0) a.ssum[int64_t(r) * a.ls + s0 + j] = sum;
+                if (lane == 0) a.ssum[int64_t(r) * a.ls + s0 + j] = k > KEY_NINF ? sum : 0.f;
             }
         }
     }
@@ -209,9 +241,10 @@ struct Weigher {
     const uint32_t* tab;  // EXP2_256 in shared memory
     __device__ __forceinline__ Weigher(float m_, float T, const uint32_t* t) : m(m_), tab(t) {
         hm = 0.5f * m_;
-        const double c = 2.8853900817779268 / double(T);
-        ch = float(c);
-        cl = float(c - double(ch));
+        // 2 log2(e) / T: the quotient, then the quotient of its remainder
+        constexpr float K = 2.885390043258667f, KL = 3.8519254e-8f;
+        ch = __fdiv_rn(K, T);
+        cl = ch > 0.f ? __fdiv_rn(__fadd_rn(fmaf(-ch, T, K), KL), T) : 0.f;
         inv_w = fminf(float(UB) / (15.25f * T), 3.0e38f);
     }
     // 2^42 exp((z - m) / T), z <= m, rounded.  The exponent (z - m) log2(e) / T as a sum of two
@@ -291,9 +324,7 @@ struct USmem {
     static constexpr size_t LW = LPOS + UCAP * 4;
     static constexpr size_t AKEY = LW + UCAP * 8;                // the cluster's list: keys, weights
     static constexpr size_t AW = AKEY + UCAP * 4;
-    static constexpr size_t QZ = AW + UCAP * 8;                  // queues: logits, segments
-    static constexpr size_t QS = QZ + UNW * UQ * 4;
-    static constexpr size_t HIST = QS + UNW * UQ * 4;            // masses, counts, their totals; later the segments' masses
+    static constexpr size_t HIST = AW + UCAP * 8;                // masses, counts, their totals; later the segments' masses
     static constexpr size_t HIST_BYTES = size_t(UB) * 24;
     static __host__ __device__ size_t seg_at(int nsc) { return HIST + (size_t(nsc) * 8 > HIST_BYTES ? align16(size_t(nsc) * 8) : HIST_BYTES); }
     static __host__ __device__ size_t total(int nsc, int ls) { return seg_at(nsc) + align16(size_t(ls) * 4); }
@@ -302,6 +333,12 @@ struct USmem {
 template <typename X>
 __device__ __forceinline__ X* peer(X* p, int rank) {
     return static_cast<X*>(__cluster_map_shared_rank(p, unsigned(rank)));
+}
+
+// The cluster's barrier; a CTA's alone where the cluster is one.
+__device__ __forceinline__ void sync(int C) {
+    if (C == 1) __syncthreads();
+    else cluster_sync();
 }
 
 // Block-wide sum of a 64-bit value, in every thread.
@@ -447,7 +484,7 @@ __global__ void __launch_bounds__(UNT, 2) uniform_kernel(const UniformArgs a) {
     if (tid < 256) c->tab[tid] = EXP2_256[tid];
     if (tid == 0) c->n = 0, c->nlive = 0, c->flag = 0, c->flag2 = 0;
     for (int i = tid; i < UB; i += UNT) hcnt[i] = 0;
-    cluster_sync();  // every CTA of the cluster runs before another writes into its memory
+    sync(C);  // every CTA of the cluster runs before another writes into its memory
     grid_dependency_wait();
     allow_dependents();
 
@@ -519,7 +556,7 @@ __global__ void __launch_bounds__(UNT, 2) uniform_kernel(const UniformArgs a) {
         each(all, [&](float z, int, int) { v += wt.weight_of(z); });
         v = block_sum(v, c);
         if (tid < C) peer(c->cmass, tid)[rank] = v;
-        cluster_sync();
+        sync(C);
         for (int q = 0; q < C; ++q) M += c->cmass[q];
         return M;
     };
@@ -527,30 +564,39 @@ __global__ void __launch_bounds__(UNT, 2) uniform_kernel(const UniformArgs a) {
     // ---- small sets: everything in a list
     bool small = false;
     const bool try_k = has_k && k <= UCAP;
-    if (try_k || (mp > 0.f && !has_k)) {
-        int kb = UB;
+    if (try_k || (mp > 0.f && !(has_p && !joint))) {
+        // zt: a bound that every element the decisions need reaches.  The bin of the k-th largest
+        // segment maximum, its lower edge less the edge's rounding.
+        float zt = -INFINITY;
+        small = true;
         if (try_k) {
             for (int s = tid; s < row.nseg; s += UNT) atomicAdd(&hcnt[wt.bin_of(from_logit_key(segs[s]))], 1u);
             __syncthreads();
             find_count(hcnt, uint32_t(k), c);
-            kb = c->bin;
+            const int kb = c->bin;  // the last bin has no weight, and UB means fewer segments than k
+            const float drop = 2.f * float(kb + 1) / wt.inv_w;
+            if (kb < UB - 1) zt = wt.m - drop - 0x1p-18f * (fabsf(wt.m) + drop);
+            small = kb < UB - 1;
         }
         // (top-p inside the top k is measured against all of the top k, min-p or not)
-        if (mp > 0.f && !(has_p && !joint)) kb = min(kb, wt.bin_of(from_logit_key(floor_key)));
-        small = kb < UB - 1;  // the last bin has no weight, and UB means fewer segments than k
+        if (mp > 0.f && !(has_p && !joint)) {
+            zt = fmaxf(zt, from_logit_key(floor_key));
+            small = true;
+        }
         if (small) {
             if (rank == 0) {
-                // The live segments in order, then 64 of them at a time, four per warp: their elements in
-                // bins up to kb, counted, placed by a prefix over the segments, written in index order.
+                // The live segments in order, then 64 of them at a time, four per warp: their elements at
+                // or above zt, counted, placed by a prefix over the segments, written in index order.
                 int* live = reinterpret_cast<int*>(hmass);
+                const uint32_t kt = ukey(zt);
                 const int chunk = (row.nseg + UNT - 1) / UNT;
                 const int f0 = min(row.nseg, tid * chunk), f1 = min(row.nseg, f0 + chunk);
                 uint32_t nl = 0;
-                for (int s = f0; s < f1; ++s) nl += wt.bin_of(from_logit_key(segs[s])) <= kb;
+                for (int s = f0; s < f1; ++s) nl += segs[s] >= kt;
                 uint32_t at = block_prefix_count(nl, c);
                 if (tid == UNT - 1) c->nlive = int(at + nl);
                 for (int s = f0; s < f1 && nl; ++s)
-                    if (wt.bin_of(from_logit_key(segs[s])) <= kb) {
+                    if (segs[s] >= kt) {
                         if (at < UCAP) live[at] = s;
                         ++at;
                     }
@@ -559,21 +605,22 @@ __global__ void __launch_bounds__(UNT, 2) uniform_kernel(const UniformArgs a) {
                 const int n_live = min(c->nlive, UCAP);
                 int base = 0;
                 for (int i0 = 0; i0 < n_live; i0 += 64) {
-                    float z[4][R::N];
                     uint4 v[4];
+                    uint32_t hit[4];
+                    int pre[4];
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
                         if (i0 + warp * 4 + j < n_live) v[j] = row.load(live[i0 + warp * 4 + j], lane);
-                    int pre[4];
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        int m = 0;
+                        hit[j] = 0;
                         if (i0 + warp * 4 + j < n_live) {
-                            unpack(v[j], z[j], T());
+                            float z[R::N];
+                            unpack(v[j], z, T());
 #pragma unroll
-                            for (int e = 0; e < R::N; ++e) m += wt.bin_of(z[j][e]) <= kb;
+                            for (int e = 0; e < R::N; ++e) hit[j] |= z[e] >= zt ? 1u << e : 0u;
                         }
-                        const int incl = warp_incl_scan_i(m, lane);
+                        const int m = __popc(hit[j]), incl = warp_incl_scan_i(m, lane);
                         pre[j] = incl - m;
                         if (lane == 31) c->wcnt[warp * 4 + j] = incl;
                     }
@@ -584,19 +631,16 @@ __global__ void __launch_bounds__(UNT, 2) uniform_kernel(const UniformArgs a) {
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         const int i = warp * 4 + j;
-                        int off = __shfl_sync(FULL, incl - c0 - c1, i >> 1);
-                        if (i & 1) off += __shfl_sync(FULL, c0, i >> 1);
-                        if (i0 + i < n_live) {
-                            int w = base + off + pre[j];
-#pragma unroll
-                            for (int e = 0; e < R::N; ++e)
-                                if (wt.bin_of(z[j][e]) <= kb) {
-                                    if (w < UCAP) {
-                                        lkey[w] = ukey(z[j][e]);
-                                        lpos[w] = live[i0 + i] * R::SEG + lane * R::N + e;
-                                    }
-                                    ++w;
-                                }
+                        int w = base + pre[j] + __shfl_sync(FULL, incl - c0 - c1, i >> 1);
+                        if (i & 1) w += __shfl_sync(FULL, c0, i >> 1);
+                        while (hit[j]) {
+                            const int e = __ffs(hit[j]) - 1;
+                            hit[j] &= hit[j] - 1;
+                            if (w < UCAP) {
+                                lkey[w] = ukey(element(v[j], e, T()));
+                                lpos[w] = live[i0 + i] * R::SEG + lane * R::N + e;
+                            }
+                            ++w;
                         }
                     }
                     base += total;
@@ -605,7 +649,7 @@ __global__ void __launch_bounds__(UNT, 2) uniform_kernel(const UniformArgs a) {
                 if (tid == 0) c->n = base;
                 if (tid < C) *peer(&c->flag, tid) = c->nlive <= UCAP && base <= UCAP ? 1 : 0;
             }
-            cluster_sync();
+            sync(C);
             small = c->flag != 0;
         }
     }
@@ -627,7 +671,7 @@ __global__ void __launch_bounds__(UNT, 2) uniform_kernel(const UniformArgs a) {
             } else {
                 float part = 0.f;
                 each(all, [&](float z, int, int e) {
-                    part += z > -INFINITY ? exp2_approx((z - wt.m) * cc) : 0.f;
+                    part += exp2_approx((z - wt.m) * cc);
                     if (e == R::N - 1) run += double(part), part = 0.f;
                 });
             }
@@ -637,7 +681,7 @@ __global__ void __launch_bounds__(UNT, 2) uniform_kernel(const UniformArgs a) {
             v = warp_sum(lane < UNW ? __uint_as_float(c->redc[lane]) : 0.f);
             if (!a.ssum) {
                 if (tid < C) peer(c->cmass, tid)[rank] = __float_as_uint(v);
-                cluster_sync();
+                sync(C);
                 for (int q = 0; q < C; ++q) Mf += __uint_as_float(uint32_t(c->cmass[q]));
             } else {
                 Mf = v;
@@ -715,7 +759,7 @@ __global__ void __launch_bounds__(UNT, 2) uniform_kernel(const UniformArgs a) {
                 unsure = __syncthreads_or(unsure);
                 if (tid < C) *peer(&c->flag2, tid) = unsure ? 1 : 0;
             }
-            cluster_sync();
+            sync(C);
             if (!c->flag2) break;
             M = exact_mass();
             exact = true;
@@ -777,7 +821,7 @@ __global__ void __launch_bounds__(UNT, 2) uniform_kernel(const UniformArgs a) {
                 if (w) add64(hmass + wt.bin_of(z), w);
             });
         // The cluster's histograms summed into every CTA's totals.
-        cluster_sync();
+        sync(C);
         {
             const int n = UB / C;
             for (int i = rank * n + tid; i < (rank + 1) * n; i += UNT) {
@@ -787,7 +831,7 @@ __global__ void __launch_bounds__(UNT, 2) uniform_kernel(const UniformArgs a) {
                 for (int q = 0; q < C; ++q) *peer(tmass + i, q) = v, *peer(tcnt + i, q) = m;
             }
         }
-        cluster_sync();
+        sync(C);
         // The largest key whose elements at or above it reach `target` (count or mass); the mass at
         // or above it goes into `fmass`.  With `last`, the masses of this CTA's segments are
         // left in smass, of elements at or above that key and `also`.
@@ -804,53 +848,52 @@ __global__ void __launch_bounds__(UNT, 2) uniform_kernel(const UniformArgs a) {
             if (last)
                 for (int i = tid; i < s1 - s0; i += UNT) smass[i] = 0;
             __syncthreads();
-            // The bin's elements into this CTA's list; the weights of those above it summed, 32 at a time.
-            float* qz = reinterpret_cast<float*>(smem + USmem::QZ) + warp * UQ;
-            int* qs = reinterpret_cast<int*>(smem + USmem::QS) + warp * UQ;
-            int queued = 0;
-            auto weigh = [&](int m) {
-                __syncwarp();
-                if (lane < m) {
-                    const unsigned long long w = wt.weight_of(qz[lane]);
-                    if (w >= wmin) add64(smass + qs[lane], w);
-                }
-                __syncwarp();
-            };
-            each([&](uint32_t key) { return wt.bin_of(from_logit_key(key)) <= qb; }, [&](float z, int s, int e) {
-                const int q = wt.bin_of(z);
-                if (q == qb) {
-                    const int at = atomicAdd(&c->n, 1);
-                    if (at < UCAP) {
-                        lkey[at] = ukey(z);
-                        lpos[at] = s - s0;
+            // The bin's elements into this CTA's list; the weights of those above it summed.  Few lanes
+            // hold an element at or above the bin (zl: its lower edge less the edge's rounding), so
+            // each lane walks its own.
+            const float drop = 2.f * float(qb + 1) / wt.inv_w;
+            const float zl = wt.m - drop - 0x1p-18f * (fabsf(wt.m) + drop);
+            const uint32_t kz = zl == zl ? ukey(zl) : 0u;
+            auto walk = [&](int s, const uint4& v) {
+                float z[R::N];
+                unpack(v, z, T());
+                uint32_t hit = 0;
+#pragma unroll
+                for (int e = 0; e < R::N; ++e) hit |= z[e] >= zl || kz == 0u ? 1u << e : 0u;
+                unsigned long long sum = 0;
+                while (hit) {
+                    const int e = __ffs(hit) - 1;
+                    hit &= hit - 1;
+                    const float x = element(v, e, T());
+                    const int q = wt.bin_of(x);
+                    if (q < qb) {
+                        if (last && ukey(x) >= also) {
+                            const unsigned long long w = wt.weight_of(x);
+                            if (w >= wmin) sum += w;
+                        }
+                    } else if (q == qb) {
+                        const int at = atomicAdd(&c->n, 1);
+                        if (at < UCAP) lkey[at] = ukey(x), lpos[at] = s - s0;
                     }
                 }
                 if (last) {
-                    const unsigned in = __ballot_sync(FULL, q < qb && ukey(z) >= also);
-                    if (in) {
-                        if (in >> lane & 1) {
-                            const int at = queued + __popc(in & ((1u << lane) - 1));
-                            qz[at] = z;
-                            qs[at] = s - s0;
-                        }
-                        queued += __popc(in);
-                        if (queued >= 32) {
-                            weigh(32);
-                            queued -= 32;
-                            const float mz = lane < queued ? qz[32 + lane] : 0.f;
-                            const int ms = lane < queued ? qs[32 + lane] : 0;
-                            __syncwarp();
-                            if (lane < queued) qz[lane] = mz, qs[lane] = ms;
-                        }
-                    }
+                    sum = warp_sum_u64(sum);
+                    if (lane == 0) smass[s - s0] = sum;
                 }
-            });
-            if (last) weigh(queued);
+            };
+            for (int s = s0 + warp; s < s1; s += UNW * 2) {
+                const bool one = segs[s] >= kz, two = s + UNW < s1 && segs[s + UNW] >= kz;
+                uint4 v0, v1;
+                if (one) v0 = row.load(s, lane);
+                if (two) v1 = row.load(s + UNW, lane);
+                if (one) walk(s, v0);
+                if (two) walk(s + UNW, v1);
+            }
             __syncthreads();
             const int ln = c->n;
             for (int i = tid; i < min(ln, UCAP); i += UNT) lw[i] = wt.weight_of(from_logit_key(lkey[i]));
             if (tid < C) peer(c->cn, tid)[rank] = ln;
-            cluster_sync();
+            sync(C);
             int n = 0;
             for (int q = 0; q < C; ++q) n += c->cn[q];
             if (n <= UCAP) {
@@ -894,7 +937,7 @@ __global__ void __launch_bounds__(UNT, 2) uniform_kernel(const UniformArgs a) {
                     summed = true;
                     __syncthreads();
                 }
-                cluster_sync();  // the lists have been read: they may be used again
+                sync(C);  // the lists have been read: they may be used again
                 return least;
             }
             // Keys the bin can hold, with some slack for the rounding of its edges.
@@ -918,7 +961,7 @@ __global__ void __launch_bounds__(UNT, 2) uniform_kernel(const UniformArgs a) {
                     }
                 });
                 // Every CTA sums its share of the bins over the cluster, then hands it to all.
-                cluster_sync();
+                sync(C);
                 const int n = UB / C;
                 unsigned long long v[UB / UNT];
                 uint32_t m[UB / UNT];
@@ -929,14 +972,14 @@ __global__ void __launch_bounds__(UNT, 2) uniform_kernel(const UniformArgs a) {
                     if (tid + i * UNT < n)
                         for (int q = 0; q < C; ++q) v[i] += *peer(hmass + at, q), m[i] += *peer(hcnt + at, q);
                 }
-                cluster_sync();
+                sync(C);
 #pragma unroll
                 for (int i = 0; i < UB / UNT; ++i) {
                     const int at = rank * n + tid + i * UNT;
                     if (tid + i * UNT < n)
                         for (int q = 0; q < C; ++q) *peer(hmass + at, q) = v[i], *peer(hcnt + at, q) = m[i];
                 }
-                cluster_sync();
+                sync(C);
                 find_bin(hmass, hcnt, by_mass, target - above_t, c);
                 const uint32_t q = uint32_t(c->bin);
                 above += c->above;
@@ -962,7 +1005,7 @@ __global__ void __launch_bounds__(UNT, 2) uniform_kernel(const UniformArgs a) {
             G = max(1ull, G + (cut ? 1 : 0));
             theta = max(theta, search(true, G, none, true, theta));
         }
-        cluster_sync();  // every CTA has read the others' bins: the segments' masses may take their place
+        sync(C);  // every CTA has read the others' bins: the segments' masses may take their place
     }
     // ---- kept mass of every segment, then of every CTA
     unsigned long long own = 0;
@@ -991,7 +1034,7 @@ __global__ void __launch_bounds__(UNT, 2) uniform_kernel(const UniformArgs a) {
     }
     own = block_sum(own, c);
     if (tid < C) peer(c->cmass, tid)[rank] = own;
-    cluster_sync();
+    sync(C);
     unsigned long long Z = 0, before = 0;
     for (int q = 0; q < C; ++q) {
         if (q < rank) before += c->cmass[q];

@@ -26,7 +26,8 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libfs_sampling.so")
 DECODE = os.path.join(PKG, "_decode.so")
-SOURCES = ["sampling.cu", "renorm.cu", "speculative.cu", "uniforms.cu", "paged_kv.cu", "prefix_attention.cu", "api.cu"]
+SOURCES = ["sampling.cu", "renorm.cu", "speculative.cu", "uniforms.cu", "paged_kv.cu", "prefix_attention.cu",
+           "prefix_tensor.cu", "api.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -8,130 +8,17 @@
 // by their maxima and sums:
 //   m = max_i m_i,  l = sum_i 2^(m_i - m) l_i,  out = sum_i 2^(m_i - m) l_i out_i / l.
 //
+// prefix_tensor.cu: the prefix's part where a group has many queries.
 // attend_kernel: one CTA per (tile of queries, key/value head, range of keys), of the
-// prefixes and of the suffixes in one launch; scores, running maximum, sum and output stay
+// suffixes and of small groups' prefixes in one launch; scores, running maximum, sum and output stay
 // in registers.  join_kernel: one warp per query joins the parts in a fixed order (no
 // atomics, the same result on every run).
-#include <algorithm>
-
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
-
-#include "fs_device.cuh"
-#include "fs_host.h"
+#include "attention.cuh"
 
 namespace fsd {
 
-constexpr int KT = 64;        // keys per tile
 constexpr int ANT = 128;      // threads of attend_kernel
 constexpr int ASTAGES = 2;    // tiles of keys and values in flight
-
-struct AttnArgs {
-    const void* q;
-    void* out;
-    float* lse;                 // [B][Q][Hq], nullable
-    int64_t qs[3], os[3];       // strides: row, query, head
-    const void* k;
-    const void* v;
-    int64_t kc[3], vc[3];       // strides: page, slot, head
-    int num_pages, page_size, page_shift;  // page_shift: log2(page_size), -1 when it is no power of two
-    const int* ptab;            // [G][pw]
-    const int* plens;           // [G]
-    const int* starts;          // [G + 1], nullable (one group of every row)
-    int G, pw;
-    const int* stab;            // [B][sw]
-    const int* slens;           // [B]
-    int sw;
-    int B, Q, Hq, Hkv, gs;      // gs = Hq / Hkv
-    float scale;                // the score's scale times log2(e)
-    float* part_o;              // [SP + SS][B * Q * Hq][D], each part's own softmax output
-    float* part_l;              // [SP + SS][B * Q * Hq], log2 of each part's sum of 2^score
-    int SP, SS;                 // key ranges: prefix, suffix
-    int ptiles, stiles;         // query tiles: of all groups together (at most), of one row
-};
-
-// ------------------------------------------------------------------ groups and ranges
-
-__device__ __forceinline__ int clamp_row(int x, int B) { return min(max(x, 0), B); }
-__device__ __forceinline__ int group_begin(const AttnArgs& a, int g) { return a.starts ? clamp_row(a.starts[g], a.B) : 0; }
-__device__ __forceinline__ int group_end(const AttnArgs& a, int g) {
-    return a.starts ? max(group_begin(a, g), clamp_row(a.starts[g + 1], a.B)) : a.B;
-}
-__device__ __forceinline__ int prefix_len(const AttnArgs& a, int g) {
-    return int(min(int64_t(max(a.plens[g], 0)), int64_t(a.pw) * a.page_size));
-}
-__device__ __forceinline__ int suffix_len(const AttnArgs& a, int b) {
-    return int(min(int64_t(max(a.slens[b], 0)), int64_t(a.sw) * a.page_size));
-}
-// Keys per range when `len` keys are cut into at most `splits` ranges of whole tiles.
-__device__ __forceinline__ int range_len(int len, int splits) {
-    return ((len + splits - 1) / splits + KT - 1) / KT * KT;
-}
-
-// The group that row b belongs to, -1 for none: the last one that starts at or before b.
-// Warp-collective.
-__device__ __forceinline__ int group_of(const AttnArgs& a, int b, int lane) {
-    if (!a.starts) return a.G > 0 ? 0 : -1;
-    int n = 0;
-    for (int g0 = 0; g0 < a.G; g0 += 32) {
-        const bool le = g0 + lane < a.G && a.starts[g0 + lane] <= b;
-        n += __popc(__ballot_sync(FULL, le));
-    }
-    return n > 0 && b < group_end(a, n - 1) ? n - 1 : -1;
-}
-
-// The group and the tile inside it of the `tile`-th query tile of all groups (tiles of MT
-// queries per key/value head); group -1 past the last.  Warp-collective.
-template <int MT>
-__device__ __forceinline__ int2 group_tile(const AttnArgs& a, int tile, int lane) {
-    int before = 0;
-    for (int g0 = 0; g0 < a.G; g0 += 32) {
-        const int g = g0 + lane;
-        const int rows = g < a.G ? group_end(a, g) - group_begin(a, g) : 0;
-        const int n = int((int64_t(rows) * a.Q * a.gs + MT - 1) / MT);
-        const int incl = warp_incl_scan_i(n, lane);
-        const unsigned hit = __ballot_sync(FULL, before + incl > tile);
-        if (hit) {
-            const int l = __ffs(hit) - 1;
-            const int excl = __shfl_sync(FULL, incl - n, l);
-            return make_int2(g0 + l, tile - before - excl);
-        }
-        before += __shfl_sync(FULL, incl, 31);
-    }
-    return make_int2(-1, 0);
-}
-
-// ------------------------------------------------------------------ matrix fragments
-
-template <typename T> struct Mma;
-template <> struct Mma<__nv_bfloat16> {
-    static __device__ __forceinline__ void run(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-        asm volatile(
-            "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-    }
-    static __device__ __forceinline__ uint32_t pack(float x, float y) {
-        const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
-        return *reinterpret_cast<const uint32_t*>(&h);
-    }
-    static __device__ __forceinline__ float get(__nv_bfloat16 x) { return __bfloat162float(x); }
-    static __device__ __forceinline__ __nv_bfloat16 put(float x) { return __float2bfloat16_rn(x); }
-};
-template <> struct Mma<__half> {
-    static __device__ __forceinline__ void run(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-        asm volatile(
-            "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-    }
-    static __device__ __forceinline__ uint32_t pack(float x, float y) {
-        const __half2 h = __floats2half2_rn(x, y);
-        return *reinterpret_cast<const uint32_t*>(&h);
-    }
-    static __device__ __forceinline__ float get(__half x) { return __half2float(x); }
-    static __device__ __forceinline__ __half put(float x) { return __float2half_rn(x); }
-};
 
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -140,14 +27,6 @@ __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
 __device__ __forceinline__ void ldsm4_t(uint32_t (&r)[4], uint32_t addr) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr));
-}
-__device__ __forceinline__ float exp2_fast(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool on) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0) : "memory");
 }
 // Byte offset of 16-byte chunk c of row r in a tile of D 16-bit values a row: chunks are
 // permuted within each row by its index, so that the eight rows of a matrix fragment fall
@@ -586,33 +465,44 @@ static fs_status launch_pdl(K kernel, unsigned grid, unsigned block, size_t smem
     return e == cudaSuccess ? FS_OK : cuda_fail(e);
 }
 
-// Queries per tile: the smallest tile that holds the queries of an average group (or of
-// one row, without a prefix); a group's keys are then read once.
-static int tile_rows(int B, int Q, int gs, int G) {
-    const int64_t per = G > 0 ? int64_t(B) * Q * gs / G : int64_t(Q) * gs;
-    return per <= 16 ? 16 : (per <= 32 ? 32 : 64);
-}
+// Queries per tile of attend_kernel: the smallest tile that holds `per` queries, so that keys are read once.
+static int tile_rows(int64_t per) { return per <= 16 ? 16 : (per <= 32 ? 32 : 64); }
 
 struct AttnPlan {
     int MT, SP, SS, ptiles, stiles;
+    int tensor;     // queries per tile on the tensor cores, 0: the prefix runs in attend_kernel
     size_t bytes;
 };
 
-// Key ranges: about three CTAs for every SM, no range shorter than four tiles.  The lengths are
-// on the device, so the plan goes by the most that the tables can name.
+// The lengths are on the device, so the plan goes by the most that the tables can name.
 static AttnPlan attn_plan(int B, int Q, int Hq, int Hkv, int D, int G, int64_t max_prefix, int64_t max_suffix, int sms) {
     AttnPlan p;
     const int gs = Hq / Hkv;
-    p.MT = tile_rows(B, Q, gs, G);
-    const int64_t all = int64_t(B) * Q * gs;
-    p.ptiles = G > 0 && max_prefix > 0 ? int(std::min<int64_t>(all, all / p.MT + G)) : 0;
+    const int64_t all = int64_t(B) * Q * gs, per = G > 0 ? all / G : 0;
+    const bool prefix = G > 0 && max_prefix > 0;
+    p.tensor = prefix && D <= 128 && per > 32 && max_prefix >= 512 ? (per > 128 ? 256 : 128) : 0;
+    p.MT = tile_rows(prefix && !p.tensor ? per : int64_t(Q) * gs);
+    const int rows = p.tensor ? p.tensor : p.MT;
+    // the most tiles that `all` queries in G groups can take
+    p.ptiles = prefix ? int(std::min<int64_t>(all, (all + int64_t(G) * (rows - 1)) / rows)) : 0;
     p.stiles = max_suffix > 0 ? int((int64_t(Q) * gs + p.MT - 1) / p.MT) : 0;
+    // Key ranges in attend_kernel: about three CTAs for every SM, no range shorter than four tiles.
     auto splits = [&](int64_t items, int64_t len) {
         if (items == 0 || len <= 0) return int64_t(0);
         const int64_t by_len = (len + 4 * KT - 1) / (4 * KT);
         return std::max<int64_t>(1, std::min<int64_t>({(int64_t(sms) * 3 + items - 1) / items, by_len, 256}));
     };
     p.SP = int(splits(int64_t(p.ptiles) * Hkv, max_prefix));
+    if (p.tensor) {
+        // One CTA per SM: the number of ranges that takes the least time in whole waves, a
+        // range's start and end counted as four tiles.
+        const int64_t items = int64_t(p.ptiles) * Hkv, n = (max_prefix + 127) / 128;
+        int64_t best = INT64_MAX;
+        for (int64_t s = 1; s <= std::min<int64_t>(n, 64); ++s) {
+            const int64_t cost = (items * s + sms - 1) / sms * ((n + s - 1) / s + 4);
+            if (cost < best) best = cost, p.SP = int(s);
+        }
+    }
     p.SS = int(splits(int64_t(B) * p.stiles * Hkv, max_suffix));
     p.bytes = size_t(p.SP + p.SS) * size_t(B) * Q * Hq * (size_t(D) + 1) * 4;
     return p;
@@ -627,10 +517,16 @@ static fs_status launch_attend(const AttnArgs& a, unsigned grid, void* stream) {
 }
 
 template <typename T, int D>
-static fs_status run_attention(AttnArgs& a, const AttnPlan& p, void* stream) {
-    const int64_t items = int64_t(p.ptiles) * a.Hkv * p.SP + int64_t(a.B) * p.stiles * a.Hkv * p.SS;
-    if (items > 0x7fffffffLL) return FS_ERR_UNSUPPORTED;
+static fs_status run_attention(AttnArgs& a, const AttnPlan& p, int dtype, void* stream) {
+    const int64_t pre = int64_t(p.ptiles) * a.Hkv * p.SP;
+    const int64_t items = (p.tensor ? 0 : pre) + int64_t(a.B) * p.stiles * a.Hkv * p.SS;
+    if (items > 0x7fffffffLL || pre > 0x7fffffffLL) return FS_ERR_UNSUPPORTED;
     fs_status st = FS_OK;
+    if (p.tensor) {
+        st = launch_prefix_tensor(a, dtype, D, p.tensor, stream);
+        if (st != FS_OK) return st;
+        a.ptiles = 0;
+    }
     if (items > 0) {
         if (p.MT == 16) st = launch_attend<T, D, 16, 1, 4, 1>(a, unsigned(items), stream);
         else if (p.MT == 32) st = launch_attend<T, D, 32, 2, 2, 1>(a, unsigned(items), stream);
@@ -751,12 +647,12 @@ fs_status fs_shared_prefix_attention(const fs_paged_kv* cache, const void* query
     a.part_l = a.part_o + size_t(p.SP + p.SS) * batch * queries * q_heads * cache->head_dim;
     const int D = cache->head_dim;
     if (cache->dtype == FS_BF16)
-        return D == 64    ? run_attention<__nv_bfloat16, 64>(a, p, stream)
-               : D == 128 ? run_attention<__nv_bfloat16, 128>(a, p, stream)
-                          : run_attention<__nv_bfloat16, 256>(a, p, stream);
-    return D == 64    ? run_attention<__half, 64>(a, p, stream)
-           : D == 128 ? run_attention<__half, 128>(a, p, stream)
-                      : run_attention<__half, 256>(a, p, stream);
+        return D == 64    ? run_attention<__nv_bfloat16, 64>(a, p, FS_BF16, stream)
+               : D == 128 ? run_attention<__nv_bfloat16, 128>(a, p, FS_BF16, stream)
+                          : run_attention<__nv_bfloat16, 256>(a, p, FS_BF16, stream);
+    return D == 64    ? run_attention<__half, 64>(a, p, FS_F16, stream)
+           : D == 128 ? run_attention<__half, 128>(a, p, FS_F16, stream)
+                      : run_attention<__half, 256>(a, p, FS_F16, stream);
 }
 
 }  // extern "C"

@@ -21,7 +21,7 @@
 //               order, and every decision is made there.  The whole row's mass, where top-p is
 //               measured against it, is a float32 sum with a bound on its error; only a row with a
 //               candidate inside that bound sums its weights exactly.
-//   other sets  a histogram of the weights over 2048 bins linear in m - z finds the bin a
+//   other sets  a histogram of the weights over bins linear in m - z finds the bin a
 //               threshold lies in; one more pass lists that bin's elements and sums the masses of
 //               the elements above it per segment; the list decides the threshold.  Bins too full for the list (16-bit
 //               logits tie by thousands) are narrowed by histograms over the order keys.
@@ -38,7 +38,7 @@ namespace fsd {
 
 constexpr int UNT = 512;          // threads of uniform_kernel
 constexpr int UNW = UNT / 32;
-constexpr int UB = 2048;          // histogram bins
+constexpr int UB = 2048;          // histogram bins (of the linear ones, 1377 are used)
 constexpr int UCAP = 1024;        // candidates in a list
 constexpr int USEG_TRIP = 4;      // segments a warp has in flight
 constexpr uint32_t KEY_NINF = 0x007fffffu;  // order keys of -inf and +inf (a NaN's is above the latter or below the former)
@@ -237,7 +237,7 @@ __constant__ uint32_t EXP2_256[256] = {
 struct Weigher {
     float hm;          // m / 2
     float ch, cl;      // 2 log2(e) / T as a sum of two floats
-    float m, inv_w;    // bins: (m - z) / 2 * inv_w, 2048 bins up to m - z = 30.5 T (weights there round to 0)
+    float m;
     const uint32_t* tab;  // EXP2_256 in shared memory
     __device__ __forceinline__ Weigher(float m_, float T, const uint32_t* t) : m(m_), tab(t) {
         hm = 0.5f * m_;
@@ -245,36 +245,52 @@ struct Weigher {
         constexpr float K = 2.885390043258667f, KL = 3.8519254e-8f;
         ch = __fdiv_rn(K, T);
         cl = ch > 0.f ? __fdiv_rn(__fadd_rn(fmaf(-ch, T, K), KL), T) : 0.f;
-        inv_w = fminf(float(UB) / (15.25f * T), 3.0e38f);
     }
-    // 2^42 exp((z - m) / T), z <= m, rounded.  The exponent (z - m) log2(e) / T as a sum of two
+    // 2^42 exp((z - m) / T), z <= m, rounded; 0 below 2^-43.  The exponent (z - m) log2(e) / T as a sum of two
     // floats (halved operands, so that the difference cannot overflow; its rounding error
     // by the two-sum); split into n + j / 256 + r, |r| <= 1/512; 2^r - 1 as a cubic in float32 (below
     // 2^-9, so its rounding is 2^-33 of the weight); the table's 2^(j / 256) times that in
     // integers.  About 36 instructions; with a table of 32 and 2^r - 1 in two floats it
     // took 58 for a relative 4e-11.
     __device__ __forceinline__ unsigned long long weight_of(float z) const {
+        int q;
+        return weight_of(z, q);
+    }
+    // ... and the exponent in 1/256 of a binary order, rounded, negated: 0 for the maximum.
+    __device__ __forceinline__ unsigned long long weight_of(float z, int& steps) const {
         const float h = 0.5f * z;
         const float d = __fsub_rn(h, hm), bb = __fsub_rn(d, h);
         const float dl = __fadd_rn(__fsub_rn(h, __fsub_rn(d, bb)), __fsub_rn(-hm, bb));
         const float yh = __fmul_rn(d, ch);
-        if (!(yh > -44.f)) return 0;  // also -inf, whose product with a zero slope is NaN
+        steps = LAST;
+        if (!(yh > -43.f)) return 0;  // also -inf, whose product with a zero slope is NaN
         float yl = fmaf(d, ch, -yh);
         yl = fmaf(d, cl, yl);
         yl = fmaf(dl, ch, yl);
         const float t = fmaf(yh, 256.f, 12582912.f);  // + 1.5 * 2^23: the nearest integer in the low bits
-        const int q = __float_as_int(t) - 0x4B400000;
+        const int q = 0x4B400000 - __float_as_int(t);
         const float r = __fadd_rn(fmaf(__fsub_rn(t, 12582912.f), -0.00390625f, yh), yl);
-        const float s = __fmul_rn(r, fmaf(r, fmaf(r, 0.05550410866482158f, 0.2402265069591007f), 0.6931471805599453f));
-        const uint32_t tj = tab[q & 255];
-        const long long p = (long long)int(tj >> 1) * __float2int_rn(s * 0x1p33f) + (1ll << 31);
-        const uint32_t v = tj + uint32_t(p >> 32);
-        return (((unsigned long long)v << 12 >> -(q >> 8)) + 1) >> 1;
+        // (2^r - 1) 2^33
+        const float s = __fmul_rn(r, fmaf(r, fmaf(r, 0.05550410866482158f * 0x1p33f, 0.2402265069591007f * 0x1p33f),
+                                          0.6931471805599453f * 0x1p33f));
+        const uint32_t tj = tab[-q & 255];
+        const long long p = (long long)int(tj >> 1) * __float2int_rn(s) + (1ll << 31);
+        const uint32_t v = tj + uint32_t(p >> 32);  // 2^31 times the significand
+        const int n = (q + 255) >> 8;               // its binary orders below the maximum
+        steps = q;
+        if (n > 12) return ((v >> (n - 12)) + 1) >> 1;
+        return (((unsigned long long)v << (12 - n)) + 1) >> 1;
     }
-    // Bin of z: 0 the largest.  Each step is monotone in z, so a lower bin means larger z.
+    // Bin of z, 0 the largest: 8 of those steps (0.022 T).  Each operation is monotone in z, so a lower
+    // bin means larger z; the last bin's weights all round to 0.
+    static constexpr int STEPS = 8, LAST = 43 * 256;
     __device__ __forceinline__ int bin_of(float z) const {
-        return int(fminf(__fmul_rn(__fsub_rn(hm, 0.5f * z), inv_w), float(UB - 1)));
+        const float yh = __fmul_rn(__fsub_rn(0.5f * z, hm), ch);
+        if (!(yh > -43.f)) return LAST / STEPS;
+        return (0x4B400000 - __float_as_int(fmaf(yh, 256.f, 12582912.f))) / STEPS;
     }
+    // m - z at the lower edge of bin q, at least.
+    __device__ __forceinline__ float drop_of(int q) const { return float(q + 1) * float(2 * STEPS / 256.0) / ch; }
 };
 
 // f * x for a float f in (0, 1): the floor, and whether a fraction was cut off.
@@ -312,7 +328,7 @@ struct UCtl {
     int nlive;
     int flag, flag2;
     int cn[MAX_CLUSTER]; // every CTA's entries
-    int wcnt[64];
+    alignas(16) int wcnt[64];
     int seg;
     unsigned long long rest;
 };
@@ -416,7 +432,8 @@ __device__ __forceinline__ void find_count(const uint32_t* cnt, uint32_t k, UCtl
 
 // The first bin at which the running mass (by_mass) or count reaches target >= 1; the sums before it
 // and in it go into the control words (bin UB when it is never reached).  Block-wide.
-__device__ __forceinline__ void find_bin(const unsigned long long* mass, const uint32_t* cnt, bool by_mass,
+template <typename X>
+__device__ __forceinline__ void find_bin(const X mass, const uint32_t* cnt, bool by_mass,
                                          unsigned long long target, UCtl* c) {
     constexpr int PER = UB / UNT;
     const int b0 = threadIdx.x * PER;
@@ -424,7 +441,7 @@ __device__ __forceinline__ void find_bin(const unsigned long long* mass, const u
     uint32_t n = 0;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-        if (mass) v += mass[b0 + i];
+        v += mass[b0 + i];
         n += cnt[b0 + i];
     }
     const unsigned long long own = by_mass ? v : n;
@@ -434,7 +451,7 @@ __device__ __forceinline__ void find_bin(const unsigned long long* mass, const u
     const unsigned long long before = by_mass ? v : n;
     if (before < target && before + own >= target) {
         for (int i = 0; i < PER; ++i) {
-            const unsigned long long mi = mass ? mass[b0 + i] : 0;
+            const unsigned long long mi = mass[b0 + i];
             const uint32_t ni = cnt[b0 + i];
             if ((by_mass ? v + mi : n + ni) >= target) {
                 c->bin = b0 + i;
@@ -446,6 +463,19 @@ __device__ __forceinline__ void find_bin(const unsigned long long* mass, const u
     }
     __syncthreads();
 }
+
+// Masses of the bins: low words, then high words (each over all 32 banks).
+struct Hist {
+    uint32_t* lo;
+    __device__ __forceinline__ unsigned long long operator[](int i) const { return (unsigned long long)lo[UB + i] << 32 | lo[i]; }
+    __device__ __forceinline__ void set(int i, unsigned long long v) const { lo[i] = uint32_t(v), lo[UB + i] = uint32_t(v >> 32); }
+    __device__ __forceinline__ void add(int i, unsigned long long v) const {
+        const uint32_t w = uint32_t(v), old = atomicAdd(lo + i, w);
+        const uint32_t h = uint32_t(v >> 32) + (old + w < old ? 1u : 0u);
+        if (h) atomicAdd(lo + UB + i, h);
+    }
+    __device__ __forceinline__ Hist of(int rank) const { return Hist{peer(lo, rank)}; }
+};
 
 // A 64-bit add into a shared counter by 32-bit atomics: the low word's carry goes on.
 __device__ __forceinline__ void add64(unsigned long long* p, unsigned long long v) {
@@ -465,11 +495,11 @@ __global__ void __launch_bounds__(UNT, 2) uniform_kernel(const UniformArgs a) {
     unsigned long long* lw = reinterpret_cast<unsigned long long*>(smem + USmem::LW);
     uint32_t* akey = reinterpret_cast<uint32_t*>(smem + USmem::AKEY);
     unsigned long long* aw = reinterpret_cast<unsigned long long*>(smem + USmem::AW);
-    unsigned long long* hmass = reinterpret_cast<unsigned long long*>(smem + USmem::HIST);
-    unsigned long long* tmass = hmass + UB;
+    const Hist hist{reinterpret_cast<uint32_t*>(smem + USmem::HIST)};
+    unsigned long long* smass = reinterpret_cast<unsigned long long*>(smem + USmem::HIST);  // [nsc], after the histograms
+    unsigned long long* tmass = smass + UB;
     uint32_t* hcnt = reinterpret_cast<uint32_t*>(tmass + UB);
     uint32_t* tcnt = hcnt + UB;
-    unsigned long long* smass = hmass;  // [nsc], after the histograms
     uint32_t* segs = reinterpret_cast<uint32_t*>(smem + USmem::seg_at(a.nsc));
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int C = int(cluster_nctarank()), rank = int(cluster_ctarank()), b = int(cluster_id_x());
@@ -512,6 +542,7 @@ __global__ void __launch_bounds__(UNT, 2) uniform_kernel(const UniformArgs a) {
     const R row(a.x, a.stride, r, a.V);
     const Weigher wt(from_logit_key(kmax), temp, c->tab);
     const unsigned long long ONE = 1ull << 42;
+    constexpr int LASTB = Weigher::LAST / Weigher::STEPS;
     const bool has_k = k > 0 && k < a.V, has_p = p < 1.f;
     const bool joint = a.order == FS_ORDER_JOINT || !has_k;  // top-p is measured against the whole row
     // min-p: w >= mp * max w; the integers are compared, rounded up.  floor_key: no element below it
@@ -574,9 +605,9 @@ __global__ void __launch_bounds__(UNT, 2) uniform_kernel(const UniformArgs a) {
             __syncthreads();
             find_count(hcnt, uint32_t(k), c);
             const int kb = c->bin;  // the last bin has no weight, and UB means fewer segments than k
-            const float drop = 2.f * float(kb + 1) / wt.inv_w;
-            if (kb < UB - 1) zt = wt.m - drop - 0x1p-18f * (fabsf(wt.m) + drop);
-            small = kb < UB - 1;
+            const float drop = wt.drop_of(kb);
+            if (kb < LASTB) zt = wt.m - drop - 0x1p-18f * (fabsf(wt.m) + drop);
+            small = kb < LASTB;
         }
         // (top-p inside the top k is measured against all of the top k, min-p or not)
         if (mp > 0.f && !(has_p && !joint)) {
@@ -587,7 +618,7 @@ __global__ void __launch_bounds__(UNT, 2) uniform_kernel(const UniformArgs a) {
             if (rank == 0) {
                 // The live segments in order, then 64 of them at a time, four per warp: their elements at
                 // or above zt, counted, placed by a prefix over the segments, written in index order.
-                int* live = reinterpret_cast<int*>(hmass);
+                int* live = reinterpret_cast<int*>(hist.lo);
                 const uint32_t kt = ukey(zt);
                 const int chunk = (row.nseg + UNT - 1) / UNT;
                 const int f0 = min(row.nseg, tid * chunk), f1 = min(row.nseg, f0 + chunk);
@@ -606,41 +637,40 @@ __global__ void __launch_bounds__(UNT, 2) uniform_kernel(const UniformArgs a) {
                 int base = 0;
                 for (int i0 = 0; i0 < n_live; i0 += 64) {
                     uint4 v[4];
-                    uint32_t hit[4];
-                    int pre[4];
+                    uint32_t hit = 0, cnt[2] = {0, 0};   // four segments' hits; their counts, two to a word
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
                         if (i0 + warp * 4 + j < n_live) v[j] = row.load(live[i0 + warp * 4 + j], lane);
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        hit[j] = 0;
                         if (i0 + warp * 4 + j < n_live) {
                             float z[R::N];
                             unpack(v[j], z, T());
+                            uint32_t h = 0;
 #pragma unroll
-                            for (int e = 0; e < R::N; ++e) hit[j] |= z[e] >= zt ? 1u << e : 0u;
+                            for (int e = 0; e < R::N; ++e) h |= z[e] >= zt ? 1u << e : 0u;
+                            hit |= h << (8 * j);
+                            cnt[j >> 1] += __popc(h) << (16 * (j & 1));
                         }
-                        const int m = __popc(hit[j]), incl = warp_incl_scan_i(m, lane);
-                        pre[j] = incl - m;
-                        if (lane == 31) c->wcnt[warp * 4 + j] = incl;
                     }
+                    const uint32_t in0 = warp_incl_scan_t(cnt[0], lane), in1 = warp_incl_scan_t(cnt[1], lane);
+                    if (lane == 31) *reinterpret_cast<uint4*>(c->wcnt + warp * 4) =
+                        make_uint4(in0 & 0xffff, in0 >> 16, in1 & 0xffff, in1 >> 16);
                     __syncthreads();
                     const int c0 = c->wcnt[lane * 2], c1 = c->wcnt[lane * 2 + 1];
                     const int incl = warp_incl_scan_i(c0 + c1, lane);
                     const int total = __shfl_sync(FULL, incl, 31);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const int i = warp * 4 + j;
-                        int w = base + pre[j] + __shfl_sync(FULL, incl - c0 - c1, i >> 1);
-                        if (i & 1) w += __shfl_sync(FULL, c0, i >> 1);
-                        while (hit[j]) {
-                            const int e = __ffs(hit[j]) - 1;
-                            hit[j] &= hit[j] - 1;
-                            if (w < UCAP) {
-                                lkey[w] = ukey(element(v[j], e, T()));
-                                lpos[w] = live[i0 + i] * R::SEG + lane * R::N + e;
-                            }
-                            ++w;
+                    // where the lane's elements of each segment go
+                    const int b0 = base + __shfl_sync(FULL, incl - c0 - c1, warp * 2), b2 = base + __shfl_sync(FULL, incl - c0 - c1, warp * 2 + 1);
+                    const int w0 = b0 + int((in0 - cnt[0]) & 0xffff), w1 = b0 + __shfl_sync(FULL, c0, warp * 2) + int((in0 - cnt[0]) >> 16);
+                    const int w2 = b2 + int((in1 - cnt[1]) & 0xffff), w3 = b2 + __shfl_sync(FULL, c0, warp * 2 + 1) + int((in1 - cnt[1]) >> 16);
+                    for (uint32_t left = hit; left; left &= left - 1) {
+                        const int bit = __ffs(left) - 1, j = bit >> 3, e = bit & 7;
+                        const int w = (j < 2 ? (j == 0 ? w0 : w1) : (j == 2 ? w2 : w3)) + __popc(hit >> (8 * j) & ((1u << e) - 1));
+                        if (w < UCAP) {
+                            const uint4 x = j < 2 ? (j == 0 ? v[0] : v[1]) : (j == 2 ? v[2] : v[3]);
+                            lkey[w] = ukey(element(x, e, T()));
+                            lpos[w] = live[i0 + warp * 4 + j] * R::SEG + lane * R::N + e;
                         }
                     }
                     base += total;
@@ -806,19 +836,21 @@ __global__ void __launch_bounds__(UNT, 2) uniform_kernel(const UniformArgs a) {
     uint32_t theta = floor_key;
     bool summed = false;   // the segments' masses are there
     if (has_k || has_p) {
-        for (int i = tid; i < UB; i += UNT) hmass[i] = 0, hcnt[i] = 0;
+        for (int i = tid; i < UB; i += UNT) hist.set(i, 0), hcnt[i] = 0;
         __syncthreads();
         if (has_k)
             each(all, [&](float z, int, int) {
-                const int q = wt.bin_of(z);
-                const unsigned long long w = wt.weight_of(z);
-                if (w) add64(hmass + q, w);
+                int q;
+                const unsigned long long w = wt.weight_of(z, q);
+                q /= Weigher::STEPS;
+                if (w) hist.add(q, w);
                 atomicAdd(hcnt + q, 1u);
             });
         else
             each(all, [&](float z, int, int) {
-                const unsigned long long w = wt.weight_of(z);
-                if (w) add64(hmass + wt.bin_of(z), w);
+                int q;
+                const unsigned long long w = wt.weight_of(z, q);
+                if (w) hist.add(q / Weigher::STEPS, w);
             });
         // The cluster's histograms summed into every CTA's totals.
         sync(C);
@@ -827,7 +859,7 @@ __global__ void __launch_bounds__(UNT, 2) uniform_kernel(const UniformArgs a) {
             for (int i = rank * n + tid; i < (rank + 1) * n; i += UNT) {
                 unsigned long long v = 0;
                 uint32_t m = 0;
-                for (int q = 0; q < C; ++q) v += *peer(hmass + i, q), m += *peer(hcnt + i, q);
+                for (int q = 0; q < C; ++q) v += hist.of(q)[i], m += *peer(hcnt + i, q);
                 for (int q = 0; q < C; ++q) *peer(tmass + i, q) = v, *peer(tcnt + i, q) = m;
             }
         }
@@ -837,9 +869,9 @@ __global__ void __launch_bounds__(UNT, 2) uniform_kernel(const UniformArgs a) {
         // left in smass, of elements at or above that key and `also`.
         auto search = [&](bool by_mass, unsigned long long target, unsigned long long& fmass, bool last,
                           uint32_t also) -> uint32_t {
-            find_bin(tmass, tcnt, by_mass, target, c);
+            find_bin(static_cast<const unsigned long long*>(tmass), tcnt, by_mass, target, c);
             const int qb = c->bin;
-            if (qb >= UB - 1) return 0;  // reached only among elements without weight
+            if (qb >= LASTB) return 0;  // reached only among elements without weight
             unsigned long long above = c->above;
             unsigned long long above_t = by_mass ? c->above : c->above_cnt;
             fmass = above + c->in_mass;
@@ -851,7 +883,7 @@ __global__ void __launch_bounds__(UNT, 2) uniform_kernel(const UniformArgs a) {
             // The bin's elements into this CTA's list; the weights of those above it summed.  Few lanes
             // hold an element at or above the bin (zl: its lower edge less the edge's rounding), so
             // each lane walks its own.
-            const float drop = 2.f * float(qb + 1) / wt.inv_w;
+            const float drop = wt.drop_of(qb);
             const float zl = wt.m - drop - 0x1p-18f * (fabsf(wt.m) + drop);
             const uint32_t kz = zl == zl ? ukey(zl) : 0u;
             auto walk = [&](int s, const uint4& v) {
@@ -941,22 +973,21 @@ __global__ void __launch_bounds__(UNT, 2) uniform_kernel(const UniformArgs a) {
                 return least;
             }
             // Keys the bin can hold, with some slack for the rounding of its edges.
-            const float wid = 2.f / wt.inv_w;
-            const float lo = wt.m - float(qb + 1) * wid, hi = wt.m - float(qb) * wid;
-            const float sl = 0x1p-20f * (fabsf(wt.m) + float(qb + 1) * wid);
+            const float lo = wt.m - drop, hi = qb > 0 ? wt.m - wt.drop_of(qb - 1) * (1.f - 1.f / 16.f / float(qb)) : wt.m;
+            const float sl = 0x1p-18f * (fabsf(wt.m) + drop);
             uint32_t kl = max(KEY_NINF + 1, ukey(lo - sl == lo - sl ? fmaxf(lo - sl, -3.402823466e38f) : -3.402823466e38f));
             uint32_t kh = min(kmax, ukey(hi + sl == hi + sl ? fminf(hi + sl, 3.402823466e38f) : 3.402823466e38f));
             while (kh > kl) {
                 const int bits = 32 - __clz(kh - kl);
                 const int sh = bits > 11 ? bits - 11 : 0;
                 __syncthreads();
-                for (int i = tid; i < UB; i += UNT) hmass[i] = 0, hcnt[i] = 0;
+                for (int i = tid; i < UB; i += UNT) hist.set(i, 0), hcnt[i] = 0;
                 __syncthreads();
                 each([&](uint32_t key) { return key >= kl; }, [&](float z, int, int) {
                     const uint32_t key = ukey(z);
                     if (key >= kl && key <= kh && wt.bin_of(z) == qb) {
                         const int q = int((kh - key) >> sh);
-                        add64(hmass + q, wt.weight_of(z));
+                        hist.add(q, wt.weight_of(z));
                         atomicAdd(hcnt + q, 1u);
                     }
                 });
@@ -970,17 +1001,17 @@ __global__ void __launch_bounds__(UNT, 2) uniform_kernel(const UniformArgs a) {
                     const int at = rank * n + tid + i * UNT;
                     v[i] = 0, m[i] = 0;
                     if (tid + i * UNT < n)
-                        for (int q = 0; q < C; ++q) v[i] += *peer(hmass + at, q), m[i] += *peer(hcnt + at, q);
+                        for (int q = 0; q < C; ++q) v[i] += hist.of(q)[at], m[i] += *peer(hcnt + at, q);
                 }
                 sync(C);
 #pragma unroll
                 for (int i = 0; i < UB / UNT; ++i) {
                     const int at = rank * n + tid + i * UNT;
                     if (tid + i * UNT < n)
-                        for (int q = 0; q < C; ++q) *peer(hmass + at, q) = v[i], *peer(hcnt + at, q) = m[i];
+                        for (int q = 0; q < C; ++q) hist.of(q).set(at, v[i]), *peer(hcnt + at, q) = m[i];
                 }
                 sync(C);
-                find_bin(hmass, hcnt, by_mass, target - above_t, c);
+                find_bin(hist, hcnt, by_mass, target - above_t, c);
                 const uint32_t q = uint32_t(c->bin);
                 above += c->above;
                 above_t += by_mass ? c->above : c->above_cnt;

@@ -11,7 +11,7 @@
 // prefix_tensor.cu: the prefix's part where a group has many queries.
 // attend_kernel: one CTA per (tile of queries, key/value head, range of keys), of the
 // suffixes and of small groups' prefixes in one launch; scores, running maximum, sum and output stay
-// in registers.  join_kernel: one warp per query joins the parts in a fixed order (no
+// in registers.  join_kernel: one CTA per query joins the parts in a fixed order (no
 // atomics, the same result on every run).
 #include "attention.cuh"
 
@@ -403,16 +403,23 @@ __global__ void __launch_bounds__(ANT) attend_kernel(const AttnArgs a) {
 
 // ------------------------------------------------------------------ the parts joined
 
+template <int E>
+struct alignas(E >= 4 ? 16 : E * 4) Run {
+    float v[E];
+};
+
+// One CTA of four warps per query: the warps take the parts in turn, each lane E neighbouring
+// elements; the warps' sums are added in order.
 template <typename T, int D>
-__global__ void __launch_bounds__(256) join_kernel(const AttnArgs a) {
-    constexpr int E = D / 32;
-    const int lane = threadIdx.x & 31;
+__global__ void __launch_bounds__(128) join_kernel(const AttnArgs a) {
+    constexpr int E = D / 32, W = 4;
+    __shared__ float so[W][D], sl[W];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     grid_dependency_wait();
     allow_dependents();
     const int64_t rows = int64_t(a.B) * a.Q * a.Hq;
-    const int64_t row = int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5);
-    if (row >= rows) return;
-    const int h = int(row % a.Hq), qi = int(row / a.Hq % a.Q), b = int(row / a.Hq / a.Q);
+    const int row = blockIdx.x;
+    const int h = row % a.Hq, qi = row / a.Hq % a.Q, b = row / a.Hq / a.Q;
     const int g = group_of(a, b, lane);
     int n0 = 0, n1 = 0;  // parts of the prefix, of the suffix
     if (g >= 0) {
@@ -423,9 +430,11 @@ __global__ void __launch_bounds__(256) join_kernel(const AttnArgs a) {
         const int len = suffix_len(a, b);
         if (len > 0) { const int step = range_len(len, a.SS); n1 = (len + step - 1) / step; }
     }
+    const int n = n0 + n1;
     auto slot = [&](int i) { return int64_t(i < n0 ? i : a.SP + i - n0) * rows + row; };
+    // (a NaN part makes the maximum's users NaN through its own weight)
     float m = -INFINITY;
-    for (int i = lane; i < n0 + n1; i += 32) m = fmaxf(m, a.part_l[slot(i)]);
+    for (int i = lane; i < n; i += 32) m = fmaxf(m, a.part_l[slot(i)]);
 #pragma unroll
     for (int s = 16; s > 0; s >>= 1) m = fmaxf(m, __shfl_xor_sync(FULL, m, s));
     const float ms = m == -INFINITY ? 0.f : m;
@@ -433,18 +442,30 @@ __global__ void __launch_bounds__(256) join_kernel(const AttnArgs a) {
 #pragma unroll
     for (int e = 0; e < E; ++e) x[e] = 0.f;
 #pragma unroll 4
-    for (int i = 0; i < n0 + n1; ++i) {
+    for (int i = warp; i < n; i += W) {
         const int64_t at = slot(i);
         const float f = exp2f(a.part_l[at] - ms);
+        Run<E> y = *reinterpret_cast<const Run<E>*>(a.part_o + at * D + lane * E);
         l += f;
 #pragma unroll
-        for (int e = 0; e < E; ++e) x[e] += f * a.part_o[at * D + lane * E + e];
+        for (int e = 0; e < E; ++e) x[e] += f * y.v[e];
     }
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    T* out = static_cast<T*>(a.out) + b * a.os[0] + qi * a.os[1] + h * a.os[2] + lane * E;
 #pragma unroll
-    for (int e = 0; e < E; ++e) out[e] = Mma<T>::put(x[e] * inv);
-    if (a.lse && lane == 0) a.lse[row] = (l == 0.f ? -INFINITY : m + log2f(l)) * 0.693147180559945309f;
+    for (int e = 0; e < E; ++e) so[warp][lane * E + e] = x[e];
+    if (lane == 0) sl[warp] = l;
+    __syncthreads();
+    l = 0.f;
+#pragma unroll
+    for (int w = 0; w < W; ++w) l += sl[w];
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    T* out = static_cast<T*>(a.out) + b * a.os[0] + qi * a.os[1] + h * a.os[2];
+    for (int i = threadIdx.x * 2; i < D; i += 256) {
+        float y0 = 0.f, y1 = 0.f;
+#pragma unroll
+        for (int w = 0; w < W; ++w) y0 += so[w][i], y1 += so[w][i + 1];
+        *reinterpret_cast<uint32_t*>(out + i) = Mma<T>::pack(y0 * inv, y1 * inv);
+    }
+    if (a.lse && threadIdx.x == 0) a.lse[row] = (l == 0.f ? -INFINITY : m + log2f(l)) * 0.693147180559945309f;
 }
 
 // ------------------------------------------------------------------ host
@@ -535,7 +556,7 @@ static fs_status run_attention(AttnArgs& a, const AttnPlan& p, int dtype, void* 
         if (st != FS_OK) return st;
     }
     const int64_t rows = int64_t(a.B) * a.Q * a.Hq;
-    return launch_pdl(join_kernel<T, D>, unsigned((rows + 7) / 8), 256, 0, stream, a);
+    return launch_pdl(join_kernel<T, D>, unsigned(rows), 128, 0, stream, a);
 }
 
 static fs_status check_shape(const fs_paged_kv* c, int B, int Q, int Hq, int G, int pw, int sw) {

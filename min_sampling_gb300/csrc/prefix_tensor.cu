@@ -33,7 +33,9 @@ struct TensorSmem {
     static constexpr int STAGES = D == 128 ? 7 - NQ : 8;
     static constexpr int KV = NQ * TILE;
     static constexpr int BARS = KV + STAGES * TILE;
-    static constexpr int TOTAL = BARS + 256 + 1024;          // 1024: the base's alignment
+    static constexpr int OUTS = BARS + 256;                  // the query rows' output rows
+    static constexpr int OFFS = BARS - TILE;                 // their addresses, in the ring's last tile until it is loaded
+    static constexpr int TOTAL = OUTS + NQ * TK * 4 + 1024;  // 1024: the base's alignment
 };
 
 // ------------------------------------------------------------------ barriers
@@ -91,6 +93,10 @@ __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&x)[16]
 }
 #undef R8
 #undef W8
+
+// The i-th run of N registers of an array.
+template <int N, int K>
+__device__ __forceinline__ uint32_t (&part(uint32_t (&x)[K], int i))[N] { return reinterpret_cast<uint32_t (&)[N]>(x[i * N]); }
 
 // Shared-memory operand with 128-byte swizzle.  lead: byte stride between blocks of 64
 // elements along the rows' contiguous direction (operands whose rows run along M or N only);
@@ -162,6 +168,21 @@ __global__ void __launch_bounds__(TNT, 1) prefix_tensor_kernel(const AttnArgs a)
     const int units = SPLIT ? tiles : 2 * tiles;         // (query tile, key tile) pairs: unit u is of tile u & 1
     const int* table = a.ptab + int64_t(gt.x) * a.pw;
 
+    // Where each query row lies (and its part of the output goes), one thread per row.
+    int64_t* q_off = reinterpret_cast<int64_t*>(mem + S::OFFS);
+    int* o_row = reinterpret_cast<int*>(mem + S::OUTS);
+    if (tid < ROWS) {
+        const int g = row0 + tid;
+        int64_t off = -1;
+        int row = -1;
+        if (g < M) {
+            const int b = b0 + g / per, rem = g % per, qi = rem / a.gs, h = head * a.gs + rem % a.gs;
+            off = b * a.qs[0] + qi * a.qs[1] + h * a.qs[2];
+            row = (b * a.Q + qi) * a.Hq + h;
+        }
+        q_off[tid] = off;
+        o_row[tid] = row;
+    }
     if (tid == 0) {
         words[1] = 0, words[2] = 0;
         for (int i = 0; i < ST; ++i) bar_init(full + 8 * i, 128), bar_init(empty + 8 * i, 1);
@@ -180,19 +201,21 @@ __global__ void __launch_bounds__(TNT, 1) prefix_tensor_kernel(const AttnArgs a)
     // columns: S of tile 0, S of tile 1, O of tile 0, O of tile 1
     const uint32_t s_at[2] = {tmem, tmem + 128}, o_at[2] = {tmem + 256, tmem + 256 + D};
 
+    // Registers: 128 a thread at launch (512 threads); 176 for the softmax's two warpgroups and 80 for the
+    // other two are the same total.
     if (warp >= 8 && warp < 12) {
         // ================================================ keys and values
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
         const int w = warp - 8;
-        // Queries: row r of the CTA's tiles, in the group of copies before the first tile's.
+        // Queries, in the group of copies before the first tile's.
+#pragma unroll 4
         for (int i = tid - 256; i < ROWS * DC; i += 128) {
-            const int r = i / DC, c = i % DC, g = row0 + r;
-            const bool on = g < M;
-            const int b = on ? b0 + g / per : 0, rem = on ? g % per : 0;
-            cp16(base + (r >> 7) * S::TILE + tile_at(r & 127, c),
-                 static_cast<const T*>(a.q) + b * a.qs[0] + (rem / a.gs) * a.qs[1] + (head * a.gs + rem % a.gs) * a.qs[2] + c * 8,
-                 on);
+            const int r = i / DC, c = i % DC;
+            const int64_t off = q_off[r];
+            cp16(base + (r >> 7) * S::TILE + tile_at(r & 127, c), static_cast<const T*>(a.q) + (off < 0 ? 0 : off + c * 8), off >= 0);
         }
         cp_async_commit();
+        asm volatile("bar.sync 2, 128;" ::: "memory");   // the addresses have been read
         // The page of this lane's key of tile t (32 keys a warp), -1 past the end, -2 for one that does not exist.
         auto page_of = [&](int t) {
             const int key = begin + t * TK + w * 32 + lane;
@@ -261,9 +284,10 @@ __global__ void __launch_bounds__(TNT, 1) prefix_tensor_kernel(const AttnArgs a)
         cp_async_wait<0>();
         if (alive)
             for (int i = max(0, count - LAG); i < count; ++i) hand_over(i);
-    } else if (warp == 12) {
+    } else if (warp >= 12) {
         // ================================================ matrix instructions
-        if (lane == 0) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+        if (warp == 12 && lane == 0) {
             constexpr uint32_t QK = product<T>(TK, false), PV = product<T>(D, true);
             int got = 0;      // copy tiles taken
             auto take = [&](int& st) {
@@ -324,12 +348,12 @@ __global__ void __launch_bounds__(TNT, 1) prefix_tensor_kernel(const AttnArgs a)
             }
         }
         __syncwarp();
-    } else if (warp < 8) {
+    } else {
         // ================================================ softmax
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
         const int t = warp >> 2, r = tid & 127;
         const uint32_t lanes = uint32_t(warp & 3) << 21;   // the warp's 32 lanes of tensor memory
         const int n = SPLIT ? (tiles + 1 - t) / 2 : tiles;
-        const bool neg = a.scale < 0.f;
         float m = -INFINITY, l = 0.f;
         bool ok = true;
         for (int i = 0; i < n && ok; ++i) {
@@ -337,26 +361,28 @@ __global__ void __launch_bounds__(TNT, 1) prefix_tensor_kernel(const AttnArgs a)
             ok = __all_sync(FULL, bar_wait(sbar + 8 * t, i & 1, dead));
             if (!ok) break;
             tmem_fence_after();
-            uint32_t x[32];
-            float mx = -INFINITY;
+            uint32_t x[TK];
 #pragma unroll
-            for (int c = 0; c < TK / 32; ++c) {
-                if (c * 32 >= valid) break;
-                tmem_ld32(x, s_at[t] + lanes + c * 32);
-                tmem_wait_ld();
-                if (valid < TK)
+            for (int c = 0; c < TK / 32; ++c) tmem_ld32(part<32>(x, c), s_at[t] + lanes + c * 32);
+            tmem_wait_ld();
+            float mul = a.scale;
+            if (valid < TK) {   // scaled here, so that scores past the end are -infinity whatever the scale
+                mul = 1.f;
 #pragma unroll
-                    for (int e = 0; e < 32; ++e)
-                        if (c * 32 + e >= valid) x[e] = neg ? 0x7f800000u : 0xff800000u;
-                if (neg) {
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) mx = fmaxf(mx, -__uint_as_float(x[e]));
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) mx = fmaxf(mx, __uint_as_float(x[e]));
-                }
+                for (int e = 0; e < TK; ++e)
+                    x[e] = e < valid ? __float_as_uint(__uint_as_float(x[e]) * a.scale) : 0xff800000u;
             }
-            mx *= fabsf(a.scale);
+            float mx = -INFINITY;
+            if (mul < 0.f) {
+#pragma unroll
+                for (int e = 0; e < TK; ++e) mx = fmaxf(mx, -__uint_as_float(x[e]));
+            } else {
+                float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                for (int e = 0; e < TK; ++e) m4[e & 3] = fmaxf(m4[e & 3], __uint_as_float(x[e]));
+                mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+            }
+            mx *= fabsf(mul);
             if (!(mx > -INFINITY)) mx = m;   // a scale of 0 times infinity, or nothing but NaN
             if (__any_sync(FULL, mx > m + 8.f)) {
                 const float mn = fmaxf(m, mx);
@@ -366,51 +392,42 @@ __global__ void __launch_bounds__(TNT, 1) prefix_tensor_kernel(const AttnArgs a)
                 if (i > 0) {
 #pragma unroll
                     for (int c = 0; c < D / 32; ++c) {
-                        tmem_ld32(x, o_at[t] + lanes + c * 32);
+                        uint32_t y[32];
+                        tmem_ld32(y, o_at[t] + lanes + c * 32);
                         tmem_wait_ld();
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * f);
-                        tmem_st32(o_at[t] + lanes + c * 32, x);
+                        for (int e = 0; e < 32; ++e) y[e] = __float_as_uint(__uint_as_float(y[e]) * f);
+                        tmem_st32(o_at[t] + lanes + c * 32, y);
                     }
                 }
             }
             const float ms = m == -INFINITY ? 0.f : m;
+            float sum[2] = {0.f, 0.f};
 #pragma unroll
-            for (int c = 0; c < TK / 32; ++c) {
-                uint32_t p[16];
-                tmem_ld32(x, s_at[t] + lanes + c * 32);
-                tmem_wait_ld();
-                float sum = 0.f;
-#pragma unroll
-                for (int e = 0; e < 32; e += 2) {
-                    float p0 = exp2_fast(fmaf(__uint_as_float(x[e]), a.scale, -ms));
-                    float p1 = exp2_fast(fmaf(__uint_as_float(x[e + 1]), a.scale, -ms));
-                    if (valid < TK) {
-                        if (c * 32 + e >= valid) p0 = 0.f;
-                        if (c * 32 + e + 1 >= valid) p1 = 0.f;
-                    }
-                    sum += p0 + p1;
-                    p[e / 2] = Mma<T>::pack(p0, p1);
-                }
-                l += sum;
-                tmem_st16(s_at[t] + lanes + c * 16, p);
+            for (int e = 0; e < TK; e += 2) {
+                float p0 = exp2_fast(fmaf(__uint_as_float(x[e]), mul, -ms));
+                float p1 = exp2_fast(fmaf(__uint_as_float(x[e + 1]), mul, -ms));
+                sum[0] += p0;
+                sum[1] += p1;
+                x[e / 2] = Mma<T>::pack(p0, p1);
             }
+            l += sum[0] + sum[1];
+            tmem_st32(s_at[t] + lanes, part<32>(x, 0));
+            tmem_st32(s_at[t] + lanes + 32, part<32>(x, 1));
             tmem_wait_st();
             tmem_fence_before();
             bar_arrive(pbar + 8 * t);
         }
         // ---- this CTA's part
         if (ok && n > 0) ok = __all_sync(FULL, bar_wait(obar + 8 * t, 0, dead));
-        if (SPLIT && ok && tiles > 1) ok = __all_sync(FULL, bar_wait(obar + 8 * (1 - t), 0, dead));
+        // (the ring is written below: no product may read it any more)
+        if (ok && units > 1) ok = __all_sync(FULL, bar_wait(obar + 8 * (1 - t), 0, dead));
         tmem_fence_after();
-        const int g = row0 + (SPLIT ? r : t * 128 + r);
         const int64_t rows = int64_t(a.B) * a.Q * a.Hq;
-        const int rem = g % per;
-        const int64_t at = split * rows + (int64_t(b0 + g / per) * a.Q + rem / a.gs) * a.Hq + head * a.gs + rem % a.gs;
         // joined with the other tile's through shared memory (the ring is done with)
         constexpr int PITCH = D + 4;
-        float* other = reinterpret_cast<float*>(mem + S::KV);   // [128][PITCH], then maxima, sums
-        static_assert(!SPLIT || 128 * PITCH * 4 + 1024 <= ST * S::TILE, "a tile's part fits in the ring");
+        float* other = reinterpret_cast<float*>(mem + S::KV);   // [128][PITCH], then maxima, sums (SPLIT); staged rows
+        static_assert((SPLIT ? 128 * PITCH * 4 + 1024 : 256 * PITCH * 4) <= ST * S::TILE, "a tile's part fits in the ring");
         float f0 = 1.f, f1 = 0.f, ls = l;
         if (SPLIT && tiles > 1) {
             if (t == 1) {
@@ -436,26 +453,37 @@ __global__ void __launch_bounds__(TNT, 1) prefix_tensor_kernel(const AttnArgs a)
             // (tensor memory is read by whole warps)
             const float bad = (*poison || !ok || *dead) ? __int_as_float(0x7fffffff) : 0.f;
             const float inv = (ls == 0.f ? 0.f : 1.f / ls) + bad;
+            // Each warp's 32 rows through shared memory, so that a row is written as one line.
+            float* mine = other + (SPLIT ? r : t * 128 + r) * PITCH;
 #pragma unroll
             for (int c = 0; c < D / 32; ++c) {
                 uint32_t x[32];
                 tmem_ld32(x, o_at[t] + lanes + c * 32);
                 tmem_wait_ld();
-                if (g < M) {
 #pragma unroll
-                    for (int e = 0; e < 32; e += 4) {
-                        float4 y = make_float4(__uint_as_float(x[e]), __uint_as_float(x[e + 1]), __uint_as_float(x[e + 2]),
-                                               __uint_as_float(x[e + 3]));
-                        if (SPLIT && tiles > 1) {
-                            const float4 z = *reinterpret_cast<const float4*>(other + r * PITCH + c * 32 + e);
-                            y = make_float4(y.x * f0 + z.x * f1, y.y * f0 + z.y * f1, y.z * f0 + z.z * f1, y.w * f0 + z.w * f1);
-                        }
-                        *reinterpret_cast<float4*>(a.part_o + at * D + c * 32 + e) =
-                            make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv);
+                for (int e = 0; e < 32; e += 4) {
+                    float4 y = make_float4(__uint_as_float(x[e]), __uint_as_float(x[e + 1]), __uint_as_float(x[e + 2]),
+                                           __uint_as_float(x[e + 3]));
+                    float4* at = reinterpret_cast<float4*>(mine + c * 32 + e);
+                    if (SPLIT && tiles > 1) {
+                        const float4 z = *at;
+                        y = make_float4(y.x * f0 + z.x * f1, y.y * f0 + z.y * f1, y.z * f0 + z.z * f1, y.w * f0 + z.w * f1);
                     }
+                    *at = make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv);
                 }
             }
-            if (g < M) a.part_l[at] = (ls == 0.f ? -INFINITY : m + log2f(ls)) + bad;
+            const int own = o_row[SPLIT ? r : t * 128 + r];
+            if (own >= 0) a.part_l[split * rows + own] = (ls == 0.f ? -INFINITY : m + log2f(ls)) + bad;
+            __syncwarp();
+            const float* first = mine - lane * PITCH;
+#pragma unroll 4
+            for (int i = 0; i < 32; ++i) {
+                const int row = __shfl_sync(FULL, own, i);
+                if (row < 0) break;
+                if (lane < D / 4)
+                    *reinterpret_cast<float4*>(a.part_o + (split * rows + row) * D + lane * 4) =
+                        *reinterpret_cast<const float4*>(first + i * PITCH + lane * 4);
+            }
         }
     }
     tmem_fence_before();

@@ -68,25 +68,39 @@ __device__ __forceinline__ int group_of(const AttnArgs& a, int b, int lane) {
     return n > 0 && b < group_end(a, n - 1) ? n - 1 : -1;
 }
 
-// The group and the tile inside it of the `tile`-th query tile of all groups (tiles of MT
-// queries per key/value head); group -1 past the last.  Warp-collective.
+// A group's query tile: its rows [b0, b1), prefix length, and the tile's number inside it.
+struct GroupTile {
+    int g, tile, b0, b1, len;
+};
+
+// The `tile`-th query tile of all groups (tiles of MT queries per key/value head); g = -1
+// past the last.  Each lane reads one group, all its words in one round trip.  Warp-collective.
 template <int MT>
-__device__ __forceinline__ int2 group_tile(const AttnArgs& a, int tile, int lane) {
+__device__ __forceinline__ GroupTile group_tile(const AttnArgs& a, int tile, int lane) {
     int before = 0;
     for (int g0 = 0; g0 < a.G; g0 += 32) {
         const int g = g0 + lane;
-        const int rows = g < a.G ? group_end(a, g) - group_begin(a, g) : 0;
-        const int n = int((int64_t(rows) * a.Q * a.gs + MT - 1) / MT);
+        int lo = 0, hi = 0, len = 0;
+        if (g < a.G) {
+            if (a.starts) {
+                lo = clamp_row(a.starts[g], a.B);
+                hi = max(lo, clamp_row(a.starts[g + 1], a.B));
+            } else {
+                hi = a.B;
+            }
+            len = prefix_len(a, g);
+        }
+        const int n = int((int64_t(hi - lo) * a.Q * a.gs + MT - 1) / MT);
         const int incl = warp_incl_scan_i(n, lane);
         const unsigned hit = __ballot_sync(FULL, before + incl > tile);
         if (hit) {
             const int l = __ffs(hit) - 1;
-            const int excl = __shfl_sync(FULL, incl - n, l);
-            return make_int2(g0 + l, tile - before - excl);
+            return GroupTile{g0 + l, tile - before - __shfl_sync(FULL, incl - n, l), __shfl_sync(FULL, lo, l),
+                             __shfl_sync(FULL, hi, l), __shfl_sync(FULL, len, l)};
         }
         before += __shfl_sync(FULL, incl, 31);
     }
-    return make_int2(-1, 0);
+    return GroupTile{-1, 0, 0, 0, 0};
 }
 
 // ------------------------------------------------------------------ matrix fragments

@@ -77,17 +77,17 @@ __global__ void __launch_bounds__(ANT) attend_kernel(const AttnArgs a) {
         item /= a.ptiles;
         head = item % a.Hkv;
         split = item / a.Hkv;
-        const int2 gt = group_tile<MT>(a, tile, lane);
-        if (gt.x < 0) return;
-        b0 = group_begin(a, gt.x);
-        M = (group_end(a, gt.x) - b0) * a.Q * a.gs;
-        row0 = gt.y * MT;
-        len = prefix_len(a, gt.x);
+        const GroupTile gt = group_tile<MT>(a, tile, lane);
+        if (gt.g < 0) return;
+        b0 = gt.b0;
+        M = (gt.b1 - b0) * a.Q * a.gs;
+        row0 = gt.tile * MT;
+        len = gt.len;
         const int step = range_len(len, a.SP);
         begin = split * step;
         if (begin >= len) return;
         len = min(len, begin + step);
-        table = a.ptab + int64_t(gt.x) * a.pw;
+        table = a.ptab + int64_t(gt.g) * a.pw;
         slot = split;
     } else {
         item -= np;

@@ -2,8 +2,8 @@
 //
 // One CTA per (query tile of a group, key/value head, range of keys).  The queries of all
 // rows of a group that read one key/value head form the rows of two matrix products per
-// tile of 128 keys: S = Q K^T, then O += P V with P = 2^(S - m).  S, P and O live in tensor
-// memory: S (128 x 128 float32) is turned into P (16 bits) in place, and P feeds the second product from
+// tile of 64 keys: S = Q K^T, then O += P V with P = 2^(S - m).  S, P and O live in tensor
+// memory: S (128 x 64 float32) is turned into P (16 bits) in place, and P feeds the second product from
 // there.  Roles of the 16 warps:
 //   warps 0-3, 4-7  softmax of tile 0 / tile 1, one thread per query: maximum, weights,
 //                   sum; O is rescaled only when a maximum grows by more than 2^8 (P and the
@@ -11,7 +11,10 @@
 //   warps 8-11      keys and values: page look-ups and 16-byte asynchronous copies into
 //                   a ring of swizzled tiles (any page size and strides)
 //   warp 12         one thread issues the matrix instructions
-// Two tiles are in flight so that one tile's softmax runs under the other's products:
+// Two query tiles of 128 are in flight, each with two S, so that the next scores are there when
+// a tile's softmax asks for them: the softmax warps never wait for a product of their own.
+// (With one S of 128 keys per tile, softmax 2800 cycles and the products behind it 2400 ran one
+// after the other: 5300 cycles for 256 queries and 128 keys.)
 //   SPLIT = false   256 queries, both tiles over the same keys
 //   SPLIT = true    up to 128 queries, the tiles take alternate key tiles and are joined at
 //                   the end
@@ -21,21 +24,22 @@
 
 namespace fsd {
 
-constexpr int TK = 128;          // keys per tile
+constexpr int TM = 128;          // queries per tile
+constexpr int TK = 64;           // keys per tile
 constexpr int TNT = 512;         // threads
-constexpr int LAG = 2;           // tiles of copies in flight behind the newest before one is handed over
+constexpr int LAG = 3;           // tiles of copies in flight behind the newest before one is handed over
 constexpr uint32_t SPIN = 1u << 22;
 
 template <int D, bool SPLIT>
 struct TensorSmem {
-    static constexpr int TILE = TK * D * 2;                  // 128 rows of queries, keys or values
+    static constexpr int QTILE = TM * D * 2, TILE = TK * D * 2;  // a tile of queries; of keys or values
     static constexpr int NQ = SPLIT ? 1 : 2;
-    static constexpr int STAGES = D == 128 ? 7 - NQ : 8;
-    static constexpr int KV = NQ * TILE;
+    static constexpr int STAGES = SPLIT ? 12 : 10;
+    static constexpr int KV = NQ * QTILE;
     static constexpr int BARS = KV + STAGES * TILE;
-    static constexpr int OUTS = BARS + 256;                  // the query rows' output rows
+    static constexpr int OUTS = BARS + 384;                  // the query rows' output rows
     static constexpr int OFFS = BARS - TILE;                 // their addresses, in the ring's last tile until it is loaded
-    static constexpr int TOTAL = OUTS + NQ * TK * 4 + 1024;  // 1024: the base's alignment
+    static constexpr int TOTAL = OUTS + NQ * TM * 4 + 1024;  // 1024: the base's alignment
 };
 
 // ------------------------------------------------------------------ barriers
@@ -111,23 +115,33 @@ constexpr uint32_t product(int n, bool b_rows) {
     const uint32_t f = sizeof(T) == 2 && std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
     return 1u << 4 | f << 7 | f << 10 | (b_rows ? 1u << 16 : 0u) | uint32_t(n / 8) << 17 | (128u / 16) << 24;
 }
-__device__ __forceinline__ void mma_smem(uint32_t d, uint64_t a, uint64_t b, uint32_t desc, bool add) {
-    asm volatile("{ .reg .pred p; setp.ne.u32 p, %4, 0; tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p; }"
-                 ::"r"(d), "l"(a), "l"(b), "r"(desc), "r"(uint32_t(add)) : "memory");
+// Issued where `lead` holds, by one lane of a warp whose operands are uniform.
+__device__ __forceinline__ bool elect() {
+    uint32_t p;
+    asm volatile("{ .reg .pred p; elect.sync _|p, 0xffffffff; selp.u32 %0, 1, 0, p; }" : "=r"(p));
+    return p != 0;
 }
-__device__ __forceinline__ void mma_tmem(uint32_t d, uint32_t a, uint64_t b, uint32_t desc, bool add) {
-    asm volatile("{ .reg .pred p; setp.ne.u32 p, %4, 0; tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p; }"
-                 ::"r"(d), "r"(a), "l"(b), "r"(desc), "r"(uint32_t(add)) : "memory");
+__device__ __forceinline__ void mma_smem(bool lead, uint32_t d, uint64_t a, uint64_t b, uint32_t desc, bool add) {
+    if (lead)
+        asm volatile("{ .reg .pred p; setp.ne.u32 p, %4, 0; tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p; }"
+                     ::"r"(d), "l"(a), "l"(b), "r"(desc), "r"(uint32_t(add)) : "memory");
+}
+__device__ __forceinline__ void mma_tmem(bool lead, uint32_t d, uint32_t a, uint64_t b, uint32_t desc, bool add) {
+    if (lead)
+        asm volatile("{ .reg .pred p; setp.ne.u32 p, %4, 0; tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p; }"
+                     ::"r"(d), "r"(a), "l"(b), "r"(desc), "r"(uint32_t(add)) : "memory");
 }
 // The barrier completes once every matrix instruction issued so far by this thread has.
-__device__ __forceinline__ void mma_commit(uint32_t bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+__device__ __forceinline__ void mma_commit(bool lead, uint32_t bar) {
+    if (lead)
+        asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
 
-// Byte offset of 16-byte chunk c of row r in a tile: blocks of 64 elements (128 bytes a row), chunks
-// permuted by the row's index within eight.
+// Byte offset of 16-byte chunk c of row r in a tile of ROWS rows: blocks of 64 elements (128 bytes a
+// row), chunks permuted by the row's index within eight.
+template <int ROWS>
 __device__ __forceinline__ uint32_t tile_at(int r, int c) {
-    return uint32_t((c >> 3) * (TK * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4));
+    return uint32_t((c >> 3) * (ROWS * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4));
 }
 
 // ------------------------------------------------------------------ the kernel
@@ -140,11 +154,15 @@ __global__ void __launch_bounds__(TNT, 1) prefix_tensor_kernel(const AttnArgs a)
     extern __shared__ unsigned char raw[];
     const uint32_t base = (smem_u32(raw) + 1023) & ~1023u;
     unsigned char* mem = raw + (base - smem_u32(raw));
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    // barriers: full[ST], empty[ST], S[2], P[2], O[2]; the tensor memory's address, flags; the last barrier
+    const int tid = threadIdx.x, warp = __shfl_sync(FULL, tid >> 5, 0), lane = tid & 31;
+    // barriers: full[ST], empty[ST]; S[tile][2], P[tile][2], O[tile] (a product P V is done); the
+    // queries; every product done; then the tensor memory's address and the flags
     const uint32_t bars = base + S::BARS;
-    const uint32_t full = bars, empty = bars + 8 * ST, sbar = bars + 16 * ST, pbar = sbar + 16, obar = sbar + 32, xbar = sbar + 64;
-    volatile int* words = reinterpret_cast<volatile int*>(mem + S::BARS + 16 * ST + 48);
+    const uint32_t full = bars, empty = full + 8 * ST, sbar = empty + 8 * ST, pbar = sbar + 32, obar = pbar + 32;
+    const uint32_t qbar = obar + 16, xbar = qbar + 8;
+    constexpr int WORDS = S::BARS + 16 * ST + 96;
+    static_assert(16 * ST + 96 + 12 <= 384, "the barriers fit");
+    volatile int* words = reinterpret_cast<volatile int*>(mem + WORDS);
     volatile int* dead = words + 1;
     volatile int* poison = words + 2;
     grid_dependency_wait();
@@ -155,18 +173,17 @@ __global__ void __launch_bounds__(TNT, 1) prefix_tensor_kernel(const AttnArgs a)
     const int tile = item % a.ptiles;
     item /= a.ptiles;
     const int head = item % a.Hkv, split = item / a.Hkv;
-    const int2 gt = group_tile<ROWS>(a, tile, lane);
-    if (gt.x < 0) return;
-    const int b0 = group_begin(a, gt.x);
+    const GroupTile gt = group_tile<ROWS>(a, tile, lane);
+    if (gt.g < 0) return;
     const int per = a.Q * a.gs;
-    const int M = (group_end(a, gt.x) - b0) * per, row0 = gt.y * ROWS;
-    const int len = prefix_len(a, gt.x), step = range_len(len, a.SP);
+    const int M = (gt.b1 - gt.b0) * per, row0 = gt.tile * ROWS;
+    const int step = range_len(gt.len, a.SP);
     const int begin = split * step;
-    if (begin >= len) return;
-    const int end = min(len, begin + step);
+    if (begin >= gt.len) return;
+    const int end = min(gt.len, begin + step);
     const int tiles = (end - begin + TK - 1) / TK;      // key tiles
     const int units = SPLIT ? tiles : 2 * tiles;         // (query tile, key tile) pairs: unit u is of tile u & 1
-    const int* table = a.ptab + int64_t(gt.x) * a.pw;
+    const int* table = a.ptab + int64_t(gt.g) * a.pw;
 
     // Where each query row lies (and its part of the output goes), one thread per row.
     int64_t* q_off = reinterpret_cast<int64_t*>(mem + S::OFFS);
@@ -176,50 +193,46 @@ __global__ void __launch_bounds__(TNT, 1) prefix_tensor_kernel(const AttnArgs a)
         int64_t off = -1;
         int row = -1;
         if (g < M) {
-            const int b = b0 + g / per, rem = g % per, qi = rem / a.gs, h = head * a.gs + rem % a.gs;
+            const int b = gt.b0 + g / per, rem = g % per, qi = rem / a.gs, h = head * a.gs + rem % a.gs;
             off = b * a.qs[0] + qi * a.qs[1] + h * a.qs[2];
             row = (b * a.Q + qi) * a.Hq + h;
         }
         q_off[tid] = off;
         o_row[tid] = row;
     }
-    if (tid == 0) {
-        words[1] = 0, words[2] = 0;
-        for (int i = 0; i < ST; ++i) bar_init(full + 8 * i, 128), bar_init(empty + 8 * i, 1);
-        for (int i = 0; i < 2; ++i) bar_init(sbar + 8 * i, 1), bar_init(pbar + 8 * i, 128), bar_init(obar + 8 * i, 1);
-        bar_init(xbar, 1);
+    if (warp == 13) {
+        if (lane < ST) bar_init(full + 8 * lane, 128), bar_init(empty + 8 * lane, 1);
+        if (lane < 4) bar_init(sbar + 8 * lane, 1), bar_init(pbar + 8 * lane, 128);
+        if (lane < 2) bar_init(obar + 8 * lane, 1);
+        if (lane == 0) {
+            words[1] = 0, words[2] = 0;
+            bar_init(qbar, 256);
+            bar_init(xbar, 1);
+        }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 12) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(base + S::BARS + 16 * ST + 48) : "memory");
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(base + WORDS) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
     tmem_fence_before();
     __syncthreads();
     tmem_fence_after();
-    const uint32_t tmem = uint32_t(words[0]);
-    // columns: S of tile 0, S of tile 1, O of tile 0, O of tile 1
-    const uint32_t s_at[2] = {tmem, tmem + 128}, o_at[2] = {tmem + 256, tmem + 256 + D};
+    const uint32_t tmem = __shfl_sync(FULL, uint32_t(words[0]), 0);
+    // columns: S of tile 0 (twice TK), S of tile 1, O of tile 0, O of tile 1
+    const uint32_t s_at[2] = {tmem, tmem + 2 * TK}, o_at[2] = {tmem + 4 * TK, tmem + 4 * TK + D};
 
-    // Registers: 128 a thread at launch (512 threads); 176 for the softmax's two warpgroups and 80 for the
+    // Registers: 128 a thread at launch (512 threads); 160 for the softmax's two warpgroups and 96 for the
     // other two are the same total.
     if (warp >= 8 && warp < 12) {
         // ================================================ keys and values
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
+        constexpr int WK = TK / 4;   // keys per warp
         const int w = warp - 8;
-        // Queries, in the group of copies before the first tile's.
-#pragma unroll 4
-        for (int i = tid - 256; i < ROWS * DC; i += 128) {
-            const int r = i / DC, c = i % DC;
-            const int64_t off = q_off[r];
-            cp16(base + (r >> 7) * S::TILE + tile_at(r & 127, c), static_cast<const T*>(a.q) + (off < 0 ? 0 : off + c * 8), off >= 0);
-        }
-        cp_async_commit();
-        asm volatile("bar.sync 2, 128;" ::: "memory");   // the addresses have been read
-        // The page of this lane's key of tile t (32 keys a warp), -1 past the end, -2 for one that does not exist.
+        // The page of this lane's key of tile t, -1 past the end, -2 for one that does not exist.
         auto page_of = [&](int t) {
-            const int key = begin + t * TK + w * 32 + lane;
-            if (t >= tiles || key >= end) return -1;
+            const int key = begin + t * TK + w * WK + lane;
+            if (t >= tiles || lane >= WK || key >= end) return -1;
             const int page = table[a.page_shift >= 0 ? key >> a.page_shift : key / a.page_size];
             return page >= 0 && page < a.num_pages ? page : -2;
         };
@@ -236,7 +249,7 @@ __global__ void __launch_bounds__(TNT, 1) prefix_tensor_kernel(const AttnArgs a)
                 alive = false;
                 return;
             }
-            const int key = begin + t * TK + w * 32 + lane;
+            const int key = begin + t * TK + w * WK + lane;
             const int64_t* str = value ? a.vc : a.kc;
             int64_t off = -1;
             if (page >= 0) {
@@ -249,10 +262,10 @@ __global__ void __launch_bounds__(TNT, 1) prefix_tensor_kernel(const AttnArgs a)
             const uint32_t dst = base + S::KV + st * S::TILE;
             constexpr int RPI = 32 / DC;   // rows a warp copies at a time
 #pragma unroll
-            for (int i = 0; i < 32 / RPI; ++i) {
+            for (int i = 0; i < WK / RPI; ++i) {
                 const int r = i * RPI + lane / DC, c = lane % DC;
                 const int64_t o = __shfl_sync(FULL, off, r);
-                cp16(dst + tile_at(w * 32 + r, c), src + (o < 0 ? 0 : o + c * 8), o >= 0);
+                cp16(dst + tile_at<TK>(w * WK + r, c), src + (o < 0 ? 0 : o + c * 8), o >= 0);
             }
             cp_async_commit();
             if (count >= LAG) {
@@ -261,109 +274,117 @@ __global__ void __launch_bounds__(TNT, 1) prefix_tensor_kernel(const AttnArgs a)
             }
             ++count;
         };
-        int pk = page_of(0);
-        if (SPLIT) {
-            // K0, K1, V0, K2, V1, K3, ...: the order in which the products first need them
-            int p0 = pk, p1 = page_of(1);
-            load(0, false, p0);
-            if (tiles > 1) load(1, false, p1);
-            for (int t = 0; t < tiles && alive; ++t) {
-                const int p2 = page_of(t + 2);
-                load(t, true, p0);
-                if (t + 2 < tiles) load(t + 2, false, p2);
-                p0 = p1, p1 = p2;
-            }
-        } else {
-            for (int t = 0; t < tiles && alive; ++t) {
-                const int next = page_of(t + 1);
-                load(t, false, pk);
-                load(t, true, pk);
-                pk = next;
-            }
+        // Keys of the first units, then values and keys in turn: the order in which the products first
+        // need them.  AHEAD: key tiles before the first values.
+        constexpr int AHEAD = SPLIT ? 4 : 2;
+        int pg[AHEAD];
+#pragma unroll
+        for (int t = 0; t < AHEAD; ++t) pg[t] = page_of(t);
+        asm volatile("bar.sync 2, 384;" ::: "memory");   // the queries' addresses, in the ring, have been read
+#pragma unroll
+        for (int t = 0; t < AHEAD; ++t)
+            if (t < tiles) load(t, false, pg[t]);
+#pragma unroll 1
+        for (int t = 0; t < tiles && alive; ++t) {
+            const int next = page_of(t + AHEAD);
+            load(t, true, pg[0]);
+            if (t + AHEAD < tiles) load(t + AHEAD, false, next);
+#pragma unroll
+            for (int i = 0; i + 1 < AHEAD; ++i) pg[i] = pg[i + 1];
+            pg[AHEAD - 1] = next;
         }
         cp_async_wait<0>();
         if (alive)
             for (int i = max(0, count - LAG); i < count; ++i) hand_over(i);
     } else if (warp >= 12) {
         // ================================================ matrix instructions
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
-        if (warp == 12 && lane == 0) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
+        // The whole warp runs this, so that addresses and descriptors stay in uniform registers; one elected
+        // lane issues.  (With one lane in a branch of its own each instruction took about 120 cycles to issue.)
+        if (warp == 12) {
             constexpr uint32_t QK = product<T>(TK, false), PV = product<T>(D, true);
-            int got = 0;      // copy tiles taken
+            const bool lead = elect();
+            const uint64_t q_op = operand(base, 0), k_op = operand(base + S::KV, 0), v_op = operand(base + S::KV, TK * 128);
+            int next = 0;       // the next copy tile: its stage and phase
+            uint32_t phase = 0;
             auto take = [&](int& st) {
-                st = got % ST;
-                const bool ok = bar_wait(full + 8 * st, (got / ST) & 1, dead);
-                ++got;
+                st = next;
+                const bool ok = __all_sync(FULL, bar_wait(full + 8 * st, phase, dead));
+                if (++next == ST) next = 0, phase ^= 1;
                 tmem_fence_after();
                 return ok;
             };
-            auto scores = [&](int t, int st) {
-                const uint32_t q = base + (SPLIT ? 0 : t * S::TILE), k = base + S::KV + st * S::TILE;
-#pragma unroll
-                for (int i = 0; i < D / 16; ++i) {
-                    const uint32_t at = (i >> 2) * (TK * 128) + (i & 3) * 32;
-                    mma_smem(s_at[t], operand(q + at, 0), operand(k + at, 0), QK, i > 0);
-                }
-                mma_commit(sbar + 8 * t);
-            };
+            // The scores of unit u; a key tile is taken by the first unit that needs it and given back by the last.
             int kst = 0, vst = 0;
-            bool ok = take(kst);
-            if (ok) {
-                scores(0, kst);
-                if (SPLIT) {
-                    mma_commit(empty + 8 * kst);
-                    if (units > 1 && (ok = take(kst))) {
-                        scores(1, kst);
-                        mma_commit(empty + 8 * kst);
-                    }
-                } else {
-                    scores(1, kst);
-                    mma_commit(empty + 8 * kst);
-                }
-            }
+            auto scores = [&](int u) {
+                const int t = u & 1, half = u >> 1 & 1;
+                if ((SPLIT || t == 0) && !take(kst)) return false;
+                const uint64_t q = q_op + (SPLIT ? 0 : t * (S::QTILE >> 4)), k = k_op + kst * (S::TILE >> 4);
+                const uint32_t d = tmem + (t * 2 + half) * TK;
+#pragma unroll
+                for (int i = 0; i < D / 16; ++i)
+                    mma_smem(lead, d, q + (((i >> 2) * (TM * 128) + (i & 3) * 32) >> 4),
+                             k + (((i >> 2) * (TK * 128) + (i & 3) * 32) >> 4), QK, i > 0);
+                mma_commit(lead, sbar + 16 * t + 8 * half);
+                if (SPLIT || t == 1) mma_commit(lead, empty + 8 * kst);
+                return true;
+            };
+            bool ok = __all_sync(FULL, bar_wait(qbar, 0, dead));
+            tmem_fence_after();
+            for (int u = 0; ok && u < min(units, 4); ++u) ok = scores(u);
+#pragma unroll 1
             for (int u = 0; ok && u < units; ++u) {
-                const int t = u & 1;
+                const int t = u & 1, half = u >> 1 & 1;
                 if (SPLIT || t == 0) ok = take(vst);
-                ok = ok && bar_wait(pbar + 8 * t, (u >> 1) & 1, dead);
+                if (ok) ok = __all_sync(FULL, bar_wait(pbar + 16 * t + 8 * half, (u >> 2) & 1, dead));
                 if (!ok) break;
                 tmem_fence_after();
-                const uint32_t v = base + S::KV + vst * S::TILE;
+                const uint64_t v = v_op + vst * (S::TILE >> 4);
+                const uint32_t p = tmem + (t * 2 + half) * TK, o = tmem + 4 * TK + t * D;
 #pragma unroll
-                for (int i = 0; i < TK / 16; ++i)
-                    mma_tmem(o_at[t], s_at[t] + 8 * i, operand(v + i * 2048, TK * 128), PV, u > 1 || i > 0);
-                if (SPLIT || t == 1) mma_commit(empty + 8 * vst);
-                if (u + 2 < units) {
-                    if (SPLIT || t == 0) ok = take(kst);
-                    if (!ok) break;
-                    scores(t, kst);
-                    if (SPLIT || t == 1) mma_commit(empty + 8 * kst);
-                } else {
-                    mma_commit(obar + 8 * t);
-                }
+                for (int i = 0; i < TK / 16; ++i) mma_tmem(lead, o, p + 8 * i, v + i * (2048 >> 4), PV, u > 1 || i > 0);
+                mma_commit(lead, obar + 8 * t);
+                if (SPLIT || t == 1) mma_commit(lead, empty + 8 * vst);
+                if (u + 4 < units) ok = scores(u + 4);
             }
-            if (!ok) {   // what has been issued finishes before the tensor memory is freed
+            mma_commit(lead, xbar);   // every product is done
+            if (!ok) {                // what has been issued finishes before the tensor memory is freed
                 *dead = 1;
-                mma_commit(xbar);
                 for (uint32_t i = 0; i < SPIN && !bar_try(xbar, 0); ++i) {}
             }
         }
-        __syncwarp();
     } else {
         // ================================================ softmax
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 160;");
+        // Queries first, by all 256 threads.
+#pragma unroll 4
+        for (int i = tid; i < ROWS * DC; i += 256) {
+            const int r = i / DC, c = i % DC;
+            const int64_t off = q_off[r];
+            cp16(base + (r >> 7) * S::QTILE + tile_at<TM>(r & 127, c), static_cast<const T*>(a.q) + (off < 0 ? 0 : off + c * 8),
+                 off >= 0);
+        }
+        cp_async_commit();
+        asm volatile("bar.sync 2, 384;" ::: "memory");   // the addresses have been read
+        cp_async_wait<0>();
+        proxy_fence();
+        bar_arrive(qbar);
+
         const int t = warp >> 2, r = tid & 127;
         const uint32_t lanes = uint32_t(warp & 3) << 21;   // the warp's 32 lanes of tensor memory
         const int n = SPLIT ? (tiles + 1 - t) / 2 : tiles;
         float m = -INFINITY, l = 0.f;
         bool ok = true;
+#pragma unroll 1
         for (int i = 0; i < n && ok; ++i) {
             const int valid = end - (begin + (SPLIT ? 2 * i + t : i) * TK);   // keys of this tile
-            ok = __all_sync(FULL, bar_wait(sbar + 8 * t, i & 1, dead));
+            const uint32_t sc = s_at[t] + (i & 1) * TK + lanes;
+            ok = __all_sync(FULL, bar_wait(sbar + 16 * t + 8 * (i & 1), (i >> 1) & 1, dead));
             if (!ok) break;
             tmem_fence_after();
             uint32_t x[TK];
 #pragma unroll
-            for (int c = 0; c < TK / 32; ++c) tmem_ld32(part<32>(x, c), s_at[t] + lanes + c * 32);
+            for (int c = 0; c < TK / 32; ++c) tmem_ld32(part<32>(x, c), sc + c * 32);
             tmem_wait_ld();
             float mul = a.scale;
             if (valid < TK) {   // scaled here, so that scores past the end are -infinity whatever the scale
@@ -390,6 +411,10 @@ __global__ void __launch_bounds__(TNT, 1) prefix_tensor_kernel(const AttnArgs a)
                 m = mn;
                 l *= f;
                 if (i > 0) {
+                    // (the product before the last was done before these scores were)
+                    ok = __all_sync(FULL, bar_wait(obar + 8 * t, (i - 1) & 1, dead));
+                    if (!ok) break;
+                    tmem_fence_after();
 #pragma unroll
                     for (int c = 0; c < D / 32; ++c) {
                         uint32_t y[32];
@@ -412,28 +437,25 @@ __global__ void __launch_bounds__(TNT, 1) prefix_tensor_kernel(const AttnArgs a)
                 x[e / 2] = Mma<T>::pack(p0, p1);
             }
             l += sum[0] + sum[1];
-            tmem_st32(s_at[t] + lanes, part<32>(x, 0));
-            tmem_st32(s_at[t] + lanes + 32, part<32>(x, 1));
+            tmem_st32(sc, part<32>(x, 0));
             tmem_wait_st();
             tmem_fence_before();
-            bar_arrive(pbar + 8 * t);
+            bar_arrive(pbar + 16 * t + 8 * (i & 1));
         }
-        // ---- this CTA's part
-        if (ok && n > 0) ok = __all_sync(FULL, bar_wait(obar + 8 * t, 0, dead));
-        // (the ring is written below: no product may read it any more)
-        if (ok && units > 1) ok = __all_sync(FULL, bar_wait(obar + 8 * (1 - t), 0, dead));
+        // ---- this CTA's part, once every product of both tiles is done (the ring is written below)
+        ok = ok && __all_sync(FULL, bar_wait(xbar, 0, dead));
         tmem_fence_after();
         const int64_t rows = int64_t(a.B) * a.Q * a.Hq;
-        // joined with the other tile's through shared memory (the ring is done with)
+        // SPLIT: joined with the other tile's through shared memory
         constexpr int PITCH = D + 4;
         float* other = reinterpret_cast<float*>(mem + S::KV);   // [128][PITCH], then maxima, sums (SPLIT); staged rows
         static_assert((SPLIT ? 128 * PITCH * 4 + 1024 : 256 * PITCH * 4) <= ST * S::TILE, "a tile's part fits in the ring");
         float f0 = 1.f, f1 = 0.f, ls = l;
         if (SPLIT && tiles > 1) {
             if (t == 1) {
-                uint32_t x[32];
-#pragma unroll
+#pragma unroll 1
                 for (int c = 0; c < D / 32; ++c) {
+                    uint32_t x[32];
                     tmem_ld32(x, o_at[1] + lanes + c * 32);
                     tmem_wait_ld();
 #pragma unroll
@@ -453,9 +475,9 @@ __global__ void __launch_bounds__(TNT, 1) prefix_tensor_kernel(const AttnArgs a)
             // (tensor memory is read by whole warps)
             const float bad = (*poison || !ok || *dead) ? __int_as_float(0x7fffffff) : 0.f;
             const float inv = (ls == 0.f ? 0.f : 1.f / ls) + bad;
-            // Each warp's 32 rows through shared memory, so that a row is written as one line.
+            // Each row through shared memory, from where one bulk copy writes it.
             float* mine = other + (SPLIT ? r : t * 128 + r) * PITCH;
-#pragma unroll
+#pragma unroll 1
             for (int c = 0; c < D / 32; ++c) {
                 uint32_t x[32];
                 tmem_ld32(x, o_at[t] + lanes + c * 32);
@@ -473,16 +495,13 @@ __global__ void __launch_bounds__(TNT, 1) prefix_tensor_kernel(const AttnArgs a)
                 }
             }
             const int own = o_row[SPLIT ? r : t * 128 + r];
-            if (own >= 0) a.part_l[split * rows + own] = (ls == 0.f ? -INFINITY : m + log2f(ls)) + bad;
-            __syncwarp();
-            const float* first = mine - lane * PITCH;
-#pragma unroll 4
-            for (int i = 0; i < 32; ++i) {
-                const int row = __shfl_sync(FULL, own, i);
-                if (row < 0) break;
-                if (lane < D / 4)
-                    *reinterpret_cast<float4*>(a.part_o + (split * rows + row) * D + lane * 4) =
-                        *reinterpret_cast<const float4*>(first + i * PITCH + lane * 4);
+            if (own >= 0) {
+                proxy_fence();
+                asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;"
+                             ::"l"(a.part_o + (split * rows + own) * D), "r"(smem_u32(mine)), "r"(D * 4) : "memory");
+                asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+                a.part_l[split * rows + own] = (ls == 0.f ? -INFINITY : m + log2f(ls)) + bad;
+                asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
             }
         }
     }

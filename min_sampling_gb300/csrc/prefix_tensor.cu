@@ -27,7 +27,6 @@ namespace fsd {
 constexpr int TM = 128;          // queries per tile
 constexpr int TK = 64;           // keys per tile
 constexpr int TNT = 512;         // threads
-constexpr int LAG = 3;           // tiles of copies in flight behind the newest before one is handed over
 constexpr uint32_t SPIN = 1u << 22;
 
 template <int D, bool SPLIT>
@@ -201,7 +200,7 @@ __global__ void __launch_bounds__(TNT, 1) prefix_tensor_kernel(const AttnArgs a)
         o_row[tid] = row;
     }
     if (warp == 13) {
-        if (lane < ST) bar_init(full + 8 * lane, 128), bar_init(empty + 8 * lane, 1);
+        if (lane < ST) bar_init(full + 8 * lane, 1), bar_init(empty + 8 * lane, 1);
         if (lane < 4) bar_init(sbar + 8 * lane, 1), bar_init(pbar + 8 * lane, 128);
         if (lane < 2) bar_init(obar + 8 * lane, 1);
         if (lane == 0) {
@@ -227,75 +226,82 @@ __global__ void __launch_bounds__(TNT, 1) prefix_tensor_kernel(const AttnArgs a)
     if (warp >= 8 && warp < 12) {
         // ================================================ keys and values
         asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
-        constexpr int WK = TK / 4;   // keys per warp
+        // Each warp copies every fourth tile: the waits, the fence and the look-ups of a tile then cost
+        // one warp, not four.  (All four on every tile: 940 cycles a tile of 16 KB.)
         const int w = warp - 8;
-        // The page of this lane's key of tile t, -1 past the end, -2 for one that does not exist.
-        auto page_of = [&](int t) {
-            const int key = begin + t * TK + w * WK + lane;
-            if (t >= tiles || lane >= WK || key >= end) return -1;
-            const int page = table[a.page_shift >= 0 ? key >> a.page_shift : key / a.page_size];
-            return page >= 0 && page < a.num_pages ? page : -2;
-        };
-        int count = 0;       // tiles of copies issued
-        bool alive = true;
-        auto hand_over = [&](int i) {   // copy tile i is there
-            proxy_fence();
-            bar_arrive(full + 8 * (i % ST));
-        };
-        auto load = [&](int t, bool value, int page) {
-            if (!alive) return;
-            const int st = count % ST;
-            if (count >= ST && !__all_sync(FULL, bar_wait(empty + 8 * st, (count / ST - 1) & 1, dead))) {
-                alive = false;
-                return;
-            }
-            const int key = begin + t * TK + w * WK + lane;
-            const int64_t* str = value ? a.vc : a.kc;
-            int64_t off = -1;
-            if (page >= 0) {
-                const int slot = a.page_shift >= 0 ? key & (a.page_size - 1) : key % a.page_size;
-                off = page * str[0] + slot * str[1] + head * str[2];
-            } else if (page == -2) {
-                *poison = 1;
-            }
-            const T* src = static_cast<const T*>(value ? a.v : a.k);
-            const uint32_t dst = base + S::KV + st * S::TILE;
-            constexpr int RPI = 32 / DC;   // rows a warp copies at a time
-#pragma unroll
-            for (int i = 0; i < WK / RPI; ++i) {
-                const int r = i * RPI + lane / DC, c = lane % DC;
-                const int64_t o = __shfl_sync(FULL, off, r);
-                cp16(dst + tile_at<TK>(w * WK + r, c), src + (o < 0 ? 0 : o + c * 8), o >= 0);
-            }
-            cp_async_commit();
-            if (count >= LAG) {
-                cp_async_wait<LAG>();
-                hand_over(count - LAG);
-            }
-            ++count;
-        };
         // Keys of the first units, then values and keys in turn: the order in which the products first
         // need them.  AHEAD: key tiles before the first values.
         constexpr int AHEAD = SPLIT ? 4 : 2;
-        int pg[AHEAD];
-#pragma unroll
-        for (int t = 0; t < AHEAD; ++t) pg[t] = page_of(t);
+        const int ka = min(AHEAD, tiles), both = 2 * (tiles - ka);
+        // Copy tile c: its key tile, negated (less one) for values.
+        auto which = [&](int c) {
+            if (c < ka) return c;
+            c -= ka;
+            if (c < both) return c & 1 ? (c >> 1) + ka : -1 - (c >> 1);
+            return -1 - (c - both / 2);
+        };
+        // The pages of this lane's keys of a tile: keys lane and lane + 32; -1 past the end, -2 for one
+        // that does not exist.
+        auto page_of = [&](int key) {
+            if (key >= end) return -1;
+            const int page = table[a.page_shift >= 0 ? key >> a.page_shift : key / a.page_size];
+            return page >= 0 && page < a.num_pages ? page : -2;
+        };
+        auto keys_of = [&](int c) {
+            const int x = which(c);
+            return begin + (x < 0 ? -1 - x : x) * TK + lane;
+        };
+        int pg[2] = {-1, -1};
+        if (w < 2 * tiles) pg[0] = page_of(keys_of(w)), pg[1] = page_of(keys_of(w) + 32);
         asm volatile("bar.sync 2, 384;" ::: "memory");   // the queries' addresses, in the ring, have been read
-#pragma unroll
-        for (int t = 0; t < AHEAD; ++t)
-            if (t < tiles) load(t, false, pg[t]);
+        int before = -1;     // the stage of the copies that are still to be handed over
+        auto hand_over = [&]() {
+            proxy_fence();
+            __syncwarp();
+            if (lane == 0) bar_arrive(full + 8 * before);
+        };
+        int st = w;
+        uint32_t lap = 0;
 #pragma unroll 1
-        for (int t = 0; t < tiles && alive; ++t) {
-            const int next = page_of(t + AHEAD);
-            load(t, true, pg[0]);
-            if (t + AHEAD < tiles) load(t + AHEAD, false, next);
+        for (int c = w; c < 2 * tiles; c += 4) {
+            const bool value = which(c) < 0;
+            const int key = keys_of(c);
+            if (lap > 0 && !__all_sync(FULL, bar_wait(empty + 8 * st, (lap - 1) & 1, dead))) break;
+            const int64_t* str = value ? a.vc : a.kc;
+            const T* src = static_cast<const T*>(value ? a.v : a.k) + head * str[2];
+            int64_t off[2];
 #pragma unroll
-            for (int i = 0; i + 1 < AHEAD; ++i) pg[i] = pg[i + 1];
-            pg[AHEAD - 1] = next;
+            for (int h = 0; h < 2; ++h) {
+                off[h] = -1;
+                if (pg[h] >= 0) {
+                    const int slot = a.page_shift >= 0 ? (key + 32 * h) & (a.page_size - 1) : (key + 32 * h) % a.page_size;
+                    off[h] = pg[h] * str[0] + slot * str[1];
+                } else if (pg[h] == -2) {
+                    *poison = 1;
+                }
+            }
+            const uint32_t dst = base + S::KV + st * S::TILE;
+            // eight lanes a row: a 128-byte line of each block of 64 elements
+#pragma unroll
+            for (int i = 0; i < TK / 4; ++i) {
+                const int r = i * 4 + (lane >> 3), c8 = lane & 7;
+                const int64_t o = __shfl_sync(FULL, off[i >> 3], r & 31);
+                const T* from = src + (o < 0 ? 0 : o + c8 * 8);
+#pragma unroll
+                for (int h = 0; h < D / 64; ++h) cp16(dst + tile_at<TK>(r, c8 + 8 * h), from + (o < 0 ? 0 : 64 * h), o >= 0);
+            }
+            cp_async_commit();
+            if (c + 4 < 2 * tiles) pg[0] = page_of(keys_of(c + 4)), pg[1] = page_of(keys_of(c + 4) + 32);
+            if (before >= 0) {
+                cp_async_wait<1>();
+                hand_over();
+            }
+            before = st;
+            st += 4;
+            if (st >= ST) st -= ST, ++lap;
         }
         cp_async_wait<0>();
-        if (alive)
-            for (int i = max(0, count - LAG); i < count; ++i) hand_over(i);
+        if (before >= 0 && !*dead) hand_over();
     } else if (warp >= 12) {
         // ================================================ matrix instructions
         asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");

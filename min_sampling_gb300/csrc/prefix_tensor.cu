@@ -10,7 +10,7 @@
 //                   sum then stay within 2^8 of their range: exact in float32, no overflow in f16)
 //   warps 8-11      keys and values: page look-ups and 16-byte asynchronous copies into
 //                   a ring of swizzled tiles (any page size and strides)
-//   warp 12         one thread issues the matrix instructions
+//   warps 12, 13    issue the first and the second product
 // Two query tiles of 128 are in flight, each with two S, so that the next scores are there when
 // a tile's softmax asks for them: the softmax warps never wait for a product of their own.
 // (With one S of 128 keys per tile, softmax 2800 cycles and the products behind it 2400 ran one
@@ -101,13 +101,11 @@ __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&x)[16]
 template <int N, int K>
 __device__ __forceinline__ uint32_t (&part(uint32_t (&x)[K], int i))[N] { return reinterpret_cast<uint32_t (&)[N]>(x[i * N]); }
 
-// Shared-memory operand with 128-byte swizzle.  lead: byte stride between blocks of 64
-// elements along the rows' contiguous direction (operands whose rows run along M or N only);
-// groups of eight 128-byte rows are 1024 bytes apart.
-__device__ __forceinline__ uint64_t operand(uint32_t addr, uint32_t lead) {
-    return uint64_t((addr & 0x3ffff) >> 4) | uint64_t(lead >> 4) << 16 | uint64_t(1024 >> 4) << 32 | uint64_t(1) << 46 |
-           uint64_t(2) << 61;
-}
+// Shared-memory operand with 128-byte swizzle: low word, the address / 16 and, above it, the byte
+// stride / 16 between blocks of 64 elements along the rows' contiguous direction (operands
+// whose rows run along M or N only); high word, groups of eight 128-byte rows 1024 bytes apart, the
+// format's version, the swizzle.
+__device__ __forceinline__ uint32_t operand_high() { return (1024u >> 4) | 1u << 14 | 2u << 29; }
 // Float32 accumulator, 128 rows, n columns; b_rows: B's rows run along N.
 template <typename T>
 constexpr uint32_t product(int n, bool b_rows) {
@@ -120,15 +118,20 @@ __device__ __forceinline__ bool elect() {
     asm volatile("{ .reg .pred p; elect.sync _|p, 0xffffffff; selp.u32 %0, 1, 0, p; }" : "=r"(p));
     return p != 0;
 }
-__device__ __forceinline__ void mma_smem(bool lead, uint32_t d, uint64_t a, uint64_t b, uint32_t desc, bool add) {
+__device__ __forceinline__ void mma_smem(bool lead, uint32_t d, uint32_t a, int a_lead, uint32_t b, int b_lead, uint32_t hi,
+                                         uint32_t desc, bool add) {
     if (lead)
-        asm volatile("{ .reg .pred p; setp.ne.u32 p, %4, 0; tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p; }"
-                     ::"r"(d), "l"(a), "l"(b), "r"(desc), "r"(uint32_t(add)) : "memory");
+        asm volatile("{ .reg .pred p; .reg .b64 x, y; mov.b64 x, {%1, %3}; mov.b64 y, {%2, %3}; setp.ne.u32 p, %5, 0;"
+                     " tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %4, p; }"
+                     ::"r"(d), "r"(a | uint32_t(a_lead >> 4) << 16), "r"(b | uint32_t(b_lead >> 4) << 16), "r"(hi), "r"(desc),
+                     "r"(uint32_t(add)) : "memory");
 }
-__device__ __forceinline__ void mma_tmem(bool lead, uint32_t d, uint32_t a, uint64_t b, uint32_t desc, bool add) {
+__device__ __forceinline__ void mma_tmem(bool lead, uint32_t d, uint32_t a, uint32_t b, int b_lead, uint32_t hi, uint32_t desc,
+                                         bool add) {
     if (lead)
-        asm volatile("{ .reg .pred p; setp.ne.u32 p, %4, 0; tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p; }"
-                     ::"r"(d), "r"(a), "l"(b), "r"(desc), "r"(uint32_t(add)) : "memory");
+        asm volatile("{ .reg .pred p; .reg .b64 y; mov.b64 y, {%2, %3}; setp.ne.u32 p, %5, 0;"
+                     " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %4, p; }"
+                     ::"r"(d), "r"(a), "r"(b | uint32_t(b_lead >> 4) << 16), "r"(hi), "r"(desc), "r"(uint32_t(add)) : "memory");
 }
 // The barrier completes once every matrix instruction issued so far by this thread has.
 __device__ __forceinline__ void mma_commit(bool lead, uint32_t bar) {
@@ -143,6 +146,35 @@ __device__ __forceinline__ uint32_t tile_at(int r, int c) {
     return uint32_t((c >> 3) * (ROWS * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4));
 }
 
+// ------------------------------------------------------------------ the order of the copies
+
+// Keys of the first units, then values and keys in turn: the order in which the products first
+// need them.  AHEAD: key tiles before the first values.
+template <bool SPLIT>
+struct CopyOrder {
+    static constexpr int AHEAD = SPLIT ? 4 : 2;
+};
+// The key tile of copy c of 2 tiles, negated (less one) for its values.
+template <bool SPLIT>
+__device__ __forceinline__ int copy_tile(int c, int tiles) {
+    const int ka = min(CopyOrder<SPLIT>::AHEAD, tiles), both = 2 * (tiles - ka);
+    if (c < ka) return c;
+    c -= ka;
+    if (c < both) return c & 1 ? (c >> 1) + ka : -1 - (c >> 1);
+    return -1 - (c - both / 2);
+}
+// The inverse: the copies of keys and of values of tile t.
+template <bool SPLIT>
+__device__ __forceinline__ int copy_of_keys(int t, int tiles) {
+    const int ka = min(CopyOrder<SPLIT>::AHEAD, tiles);
+    return t < ka ? t : ka + 2 * (t - ka) + 1;
+}
+template <bool SPLIT>
+__device__ __forceinline__ int copy_of_values(int t, int tiles) {
+    const int ka = min(CopyOrder<SPLIT>::AHEAD, tiles);
+    return ka + (t < tiles - ka ? 2 * t : t + tiles - ka);
+}
+
 // ------------------------------------------------------------------ the kernel
 
 template <typename T, int D, bool SPLIT>
@@ -154,13 +186,13 @@ __global__ void __launch_bounds__(TNT, 1) prefix_tensor_kernel(const AttnArgs a)
     const uint32_t base = (smem_u32(raw) + 1023) & ~1023u;
     unsigned char* mem = raw + (base - smem_u32(raw));
     const int tid = threadIdx.x, warp = __shfl_sync(FULL, tid >> 5, 0), lane = tid & 31;
-    // barriers: full[ST], empty[ST]; S[tile][2], P[tile][2], O[tile] (a product P V is done); the
-    // queries; every product done; then the tensor memory's address and the flags
+    // barriers: full[ST], empty[ST]; of each S: scores there, weights there, product P V done; the
+    // queries; every product done (twice); then the tensor memory's address and the flags
     const uint32_t bars = base + S::BARS;
-    const uint32_t full = bars, empty = full + 8 * ST, sbar = empty + 8 * ST, pbar = sbar + 32, obar = pbar + 32;
-    const uint32_t qbar = obar + 16, xbar = qbar + 8;
-    constexpr int WORDS = S::BARS + 16 * ST + 96;
-    static_assert(16 * ST + 96 + 12 <= 384, "the barriers fit");
+    const uint32_t full = bars, empty = full + 8 * ST, sbar = empty + 8 * ST, pbar = sbar + 32, vbar = pbar + 32;
+    const uint32_t qbar = vbar + 32, xbar = qbar + 8, ybar = xbar + 8;
+    constexpr int WORDS = S::BARS + 16 * ST + 128;
+    static_assert(16 * ST + 128 + 12 <= 384, "the barriers fit");
     volatile int* words = reinterpret_cast<volatile int*>(mem + WORDS);
     volatile int* dead = words + 1;
     volatile int* poison = words + 2;
@@ -201,12 +233,12 @@ __global__ void __launch_bounds__(TNT, 1) prefix_tensor_kernel(const AttnArgs a)
     }
     if (warp == 13) {
         if (lane < ST) bar_init(full + 8 * lane, 1), bar_init(empty + 8 * lane, 1);
-        if (lane < 4) bar_init(sbar + 8 * lane, 1), bar_init(pbar + 8 * lane, 128);
-        if (lane < 2) bar_init(obar + 8 * lane, 1);
+        if (lane < 4) bar_init(sbar + 8 * lane, 1), bar_init(pbar + 8 * lane, 128), bar_init(vbar + 8 * lane, 1);
         if (lane == 0) {
             words[1] = 0, words[2] = 0;
             bar_init(qbar, 256);
             bar_init(xbar, 1);
+            bar_init(ybar, 1);
         }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -218,8 +250,8 @@ __global__ void __launch_bounds__(TNT, 1) prefix_tensor_kernel(const AttnArgs a)
     __syncthreads();
     tmem_fence_after();
     const uint32_t tmem = __shfl_sync(FULL, uint32_t(words[0]), 0);
-    // columns: S of tile 0 (twice TK), S of tile 1, O of tile 0, O of tile 1
-    const uint32_t s_at[2] = {tmem, tmem + 2 * TK}, o_at[2] = {tmem + 4 * TK, tmem + 4 * TK + D};
+    // columns: S of units u % 4 (tile u % 2), O of tile 0, O of tile 1
+    const uint32_t o_at[2] = {tmem + 4 * TK, tmem + 4 * TK + D};
 
     // Registers: 128 a thread at launch (512 threads); 160 for the softmax's two warpgroups and 96 for the
     // other two are the same total.
@@ -229,17 +261,6 @@ __global__ void __launch_bounds__(TNT, 1) prefix_tensor_kernel(const AttnArgs a)
         // Each warp copies every fourth tile: the waits, the fence and the look-ups of a tile then cost
         // one warp, not four.  (All four on every tile: 940 cycles a tile of 16 KB.)
         const int w = warp - 8;
-        // Keys of the first units, then values and keys in turn: the order in which the products first
-        // need them.  AHEAD: key tiles before the first values.
-        constexpr int AHEAD = SPLIT ? 4 : 2;
-        const int ka = min(AHEAD, tiles), both = 2 * (tiles - ka);
-        // Copy tile c: its key tile, negated (less one) for values.
-        auto which = [&](int c) {
-            if (c < ka) return c;
-            c -= ka;
-            if (c < both) return c & 1 ? (c >> 1) + ka : -1 - (c >> 1);
-            return -1 - (c - both / 2);
-        };
         // The pages of this lane's keys of a tile: keys lane and lane + 32; -1 past the end, -2 for one
         // that does not exist.
         auto page_of = [&](int key) {
@@ -248,7 +269,7 @@ __global__ void __launch_bounds__(TNT, 1) prefix_tensor_kernel(const AttnArgs a)
             return page >= 0 && page < a.num_pages ? page : -2;
         };
         auto keys_of = [&](int c) {
-            const int x = which(c);
+            const int x = copy_tile<SPLIT>(c, tiles);
             return begin + (x < 0 ? -1 - x : x) * TK + lane;
         };
         int pg[2] = {-1, -1};
@@ -264,7 +285,7 @@ __global__ void __launch_bounds__(TNT, 1) prefix_tensor_kernel(const AttnArgs a)
         uint32_t lap = 0;
 #pragma unroll 1
         for (int c = w; c < 2 * tiles; c += 4) {
-            const bool value = which(c) < 0;
+            const bool value = copy_tile<SPLIT>(c, tiles) < 0;
             const int key = keys_of(c);
             if (lap > 0 && !__all_sync(FULL, bar_wait(empty + 8 * st, (lap - 1) & 1, dead))) break;
             const int64_t* str = value ? a.vc : a.kc;
@@ -305,60 +326,74 @@ __global__ void __launch_bounds__(TNT, 1) prefix_tensor_kernel(const AttnArgs a)
     } else if (warp >= 12) {
         // ================================================ matrix instructions
         asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
-        // The whole warp runs this, so that addresses and descriptors stay in uniform registers; one elected
-        // lane issues.  (With one lane in a branch of its own each instruction took about 120 cycles to issue.)
+        // Two warps, one for each product: a unit's waits, commits and instructions take one warp
+        // about as long as its products run.  A whole warp runs each loop, so that addresses and descriptors
+        // stay in uniform registers; one elected lane issues.  (With one lane in a branch of its own each
+        // instruction took about 120 cycles to issue.)
+        const bool lead = elect();
         if (warp == 12) {
-            constexpr uint32_t QK = product<T>(TK, false), PV = product<T>(D, true);
-            const bool lead = elect();
-            const uint64_t q_op = operand(base, 0), k_op = operand(base + S::KV, 0), v_op = operand(base + S::KV, TK * 128);
-            int next = 0;       // the next copy tile: its stage and phase
-            uint32_t phase = 0;
-            auto take = [&](int& st) {
-                st = next;
-                const bool ok = __all_sync(FULL, bar_wait(full + 8 * st, phase, dead));
-                if (++next == ST) next = 0, phase ^= 1;
-                tmem_fence_after();
-                return ok;
-            };
-            // The scores of unit u; a key tile is taken by the first unit that needs it and given back by the last.
-            int kst = 0, vst = 0;
-            auto scores = [&](int u) {
-                const int t = u & 1, half = u >> 1 & 1;
-                if ((SPLIT || t == 0) && !take(kst)) return false;
-                const uint64_t q = q_op + (SPLIT ? 0 : t * (S::QTILE >> 4)), k = k_op + kst * (S::TILE >> 4);
-                const uint32_t d = tmem + (t * 2 + half) * TK;
-#pragma unroll
-                for (int i = 0; i < D / 16; ++i)
-                    mma_smem(lead, d, q + (((i >> 2) * (TM * 128) + (i & 3) * 32) >> 4),
-                             k + (((i >> 2) * (TK * 128) + (i & 3) * 32) >> 4), QK, i > 0);
-                mma_commit(lead, sbar + 16 * t + 8 * half);
-                if (SPLIT || t == 1) mma_commit(lead, empty + 8 * kst);
-                return true;
-            };
+            // ---- scores.  A key tile is taken by the first unit that needs it and given back by the last.
+            constexpr uint32_t QK = product<T>(TK, false);
+            const uint32_t q_op = (base & 0x3ffff) >> 4, k_op = ((base + S::KV) & 0x3ffff) >> 4, hi = operand_high();
             bool ok = __all_sync(FULL, bar_wait(qbar, 0, dead));
-            tmem_fence_after();
-            for (int u = 0; ok && u < min(units, 4); ++u) ok = scores(u);
+            uint32_t kst = 0;
 #pragma unroll 1
-            for (int u = 0; ok && u < units; ++u) {
-                const int t = u & 1, half = u >> 1 & 1;
-                if (SPLIT || t == 0) ok = take(vst);
-                if (ok) ok = __all_sync(FULL, bar_wait(pbar + 16 * t + 8 * half, (u >> 2) & 1, dead));
+            for (int u = 0; u < units; ++u) {
+                const int t = u & 1, buf = u & 3;   // buffer: tile t, half u / 2 % 2
+                if (SPLIT || t == 0) {
+                    const uint32_t c = copy_of_keys<SPLIT>(SPLIT ? u : u >> 1, tiles), lap = c / ST;
+                    kst = c - lap * ST;
+                    ok = ok && __all_sync(FULL, bar_wait(full + 8 * kst, lap & 1, dead));
+                }
+                if (u >= 4) ok = ok && __all_sync(FULL, bar_wait(vbar + 8 * buf, ((u >> 2) - 1) & 1, dead));
                 if (!ok) break;
                 tmem_fence_after();
-                const uint64_t v = v_op + vst * (S::TILE >> 4);
-                const uint32_t p = tmem + (t * 2 + half) * TK, o = tmem + 4 * TK + t * D;
+                const uint32_t q = q_op + (SPLIT ? 0 : t * (S::QTILE >> 4)), k = k_op + kst * (S::TILE >> 4);
+                const uint32_t d = tmem + buf * TK;
 #pragma unroll
-                for (int i = 0; i < TK / 16; ++i) mma_tmem(lead, o, p + 8 * i, v + i * (2048 >> 4), PV, u > 1 || i > 0);
-                mma_commit(lead, obar + 8 * t);
+                for (int i = 0; i < D / 16; ++i)
+                    mma_smem(lead, d, q + (((i >> 2) * (TM * 128) + (i & 3) * 32) >> 4), 0,
+                             k + (((i >> 2) * (TK * 128) + (i & 3) * 32) >> 4), 0, hi, QK, i > 0);
+                mma_commit(lead, sbar + 8 * buf);
+                if (SPLIT || t == 1) mma_commit(lead, empty + 8 * kst);
+            }
+            if (!ok) {   // what has been issued finishes before the tensor memory is freed
+                *dead = 1;
+                mma_commit(lead, ybar);
+                for (uint32_t i = 0; i < SPIN && !bar_try(ybar, 0); ++i) {}
+            }
+        } else if (warp == 13) {
+            // ---- weights times values
+            constexpr uint32_t PV = product<T>(D, true);
+            const uint32_t v_op = ((base + S::KV) & 0x3ffff) >> 4, hi = operand_high();
+            bool ok = true;
+            uint32_t vst = 0;
+#pragma unroll 1
+            for (int u = 0; u < units; ++u) {
+                const int t = u & 1, buf = u & 3;
+                if (SPLIT || t == 0) {
+                    const uint32_t c = copy_of_values<SPLIT>(SPLIT ? u : u >> 1, tiles), lap = c / ST;
+                    vst = c - lap * ST;
+                    ok = ok && __all_sync(FULL, bar_wait(full + 8 * vst, lap & 1, dead));
+                }
+                ok = ok && __all_sync(FULL, bar_wait(pbar + 8 * buf, (u >> 2) & 1, dead));
+                if (!ok) break;
+                tmem_fence_after();
+                const uint32_t v = v_op + vst * (S::TILE >> 4);
+                const uint32_t p = tmem + buf * TK, o = tmem + 4 * TK + t * D;
+                const bool add = u > 1;
+#pragma unroll
+                for (int i = 0; i < TK / 16; ++i) mma_tmem(lead, o, p + 8 * i, v + i * (2048 >> 4), TK * 128, hi, PV, add || i > 0);
+                mma_commit(lead, vbar + 8 * buf);
                 if (SPLIT || t == 1) mma_commit(lead, empty + 8 * vst);
-                if (u + 4 < units) ok = scores(u + 4);
             }
             mma_commit(lead, xbar);   // every product is done
-            if (!ok) {                // what has been issued finishes before the tensor memory is freed
+            if (!ok) {
                 *dead = 1;
                 for (uint32_t i = 0; i < SPIN && !bar_try(xbar, 0); ++i) {}
             }
         }
+        __syncwarp();
     } else {
         // ================================================ softmax
         asm volatile("setmaxnreg.inc.sync.aligned.u32 160;");
@@ -384,8 +419,9 @@ __global__ void __launch_bounds__(TNT, 1) prefix_tensor_kernel(const AttnArgs a)
 #pragma unroll 1
         for (int i = 0; i < n && ok; ++i) {
             const int valid = end - (begin + (SPLIT ? 2 * i + t : i) * TK);   // keys of this tile
-            const uint32_t sc = s_at[t] + (i & 1) * TK + lanes;
-            ok = __all_sync(FULL, bar_wait(sbar + 16 * t + 8 * (i & 1), (i >> 1) & 1, dead));
+            const int buf = t + 2 * (i & 1);
+            const uint32_t sc = tmem + buf * TK + lanes;
+            ok = __all_sync(FULL, bar_wait(sbar + 8 * buf, (i >> 1) & 1, dead));
             if (!ok) break;
             tmem_fence_after();
             uint32_t x[TK];
@@ -417,8 +453,8 @@ __global__ void __launch_bounds__(TNT, 1) prefix_tensor_kernel(const AttnArgs a)
                 m = mn;
                 l *= f;
                 if (i > 0) {
-                    // (the product before the last was done before these scores were)
-                    ok = __all_sync(FULL, bar_wait(obar + 8 * t, (i - 1) & 1, dead));
+                    // the last product of this tile (the one before was done before these scores were)
+                    ok = __all_sync(FULL, bar_wait(vbar + 8 * (buf ^ 2), ((i - 1) >> 1) & 1, dead));
                     if (!ok) break;
                     tmem_fence_after();
 #pragma unroll
@@ -446,7 +482,7 @@ __global__ void __launch_bounds__(TNT, 1) prefix_tensor_kernel(const AttnArgs a)
             tmem_st32(sc, part<32>(x, 0));
             tmem_wait_st();
             tmem_fence_before();
-            bar_arrive(pbar + 16 * t + 8 * (i & 1));
+            bar_arrive(pbar + 8 * buf);
         }
         // ---- this CTA's part, once every product of both tiles is done (the ring is written below)
         ok = ok && __all_sync(FULL, bar_wait(xbar, 0, dead));

@@ -12,7 +12,7 @@
 
 namespace fsd {
 
-constexpr int KT = 64;        // keys per tile of attend_kernel, and the unit of key ranges
+constexpr int RANGE = 64;     // unit of key ranges: whole tiles of every kernel
 
 struct AttnArgs {
     const void* q;
@@ -35,6 +35,7 @@ struct AttnArgs {
     float* part_o;              // [SP + SS][B * Q * Hq][D], each part's own softmax output
     float* part_l;              // [SP + SS][B * Q * Hq], log2 of each part's sum of 2^score
     int SP, SS;                 // key ranges: prefix, suffix
+    int finish;                 // attend_kernel joins its suffix part with the prefix's parts (of an earlier launch) itself
     int ptiles, stiles;         // query tiles: of all groups together (at most), of one row
 };
 
@@ -51,9 +52,9 @@ __device__ __forceinline__ int prefix_len(const AttnArgs& a, int g) {
 __device__ __forceinline__ int suffix_len(const AttnArgs& a, int b) {
     return int(min(int64_t(max(a.slens[b], 0)), int64_t(a.sw) * a.page_size));
 }
-// Keys per range when `len` keys are cut into at most `splits` ranges of whole tiles.
+// Keys per range when `len` keys are cut into at most `splits` ranges.
 __device__ __forceinline__ int range_len(int len, int splits) {
-    return ((len + splits - 1) / splits + KT - 1) / KT * KT;
+    return ((len + splits - 1) / splits + RANGE - 1) / RANGE * RANGE;
 }
 
 // The group that row b belongs to, -1 for none: the last one that starts at or before b.

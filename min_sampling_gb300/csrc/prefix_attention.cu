@@ -17,7 +17,6 @@
 
 namespace fsd {
 
-constexpr int ANT = 128;      // threads of attend_kernel
 constexpr int ASTAGES = 2;    // tiles of keys and values in flight
 
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
@@ -37,7 +36,7 @@ __device__ __forceinline__ uint32_t chunk_at(int r, int c) { return uint32_t(r *
 // ------------------------------------------------------------------ parts
 
 // Shared memory: queries, then ASTAGES x (keys, values), then two slots of row offsets.
-template <int D, int MT>
+template <int D, int MT, int KT>
 struct AttnSmem {
     static constexpr int Q = 0;
     static constexpr int TILE = KT * D * 2;
@@ -48,11 +47,15 @@ struct AttnSmem {
 };
 
 // WM x WN warps over a tile of MT = 16 RM WM queries and KT keys; each warp keeps its own
-// running maximum, sum and output over its share of the keys.
-template <typename T, int D, int MT, int WM, int WN, int RM>
-__global__ void __launch_bounds__(ANT) attend_kernel(const AttnArgs a) {
-    static_assert(WM * WN == ANT / 32 && MT == 16 * RM * WM, "warp layout");
-    using S = AttnSmem<D, MT>;
+// running maximum, sum and output over its share of the keys.  Bound by the reads of keys and
+// values; what it loses are the ends of its short ranges (look-ups, first tile, joining the
+// warps).  Two warps and tiles of 32 keys, six CTAs on an SM instead of three, were slower (64 rows of
+// 1000 keys 54.7 -> 64.7 us): a tile's chain of instructions, not its load, sets its time.
+template <typename T, int D, int MT, int WM, int WN, int RM, int KT>
+__global__ void __launch_bounds__(32 * WM * WN) attend_kernel(const AttnArgs a) {
+    constexpr int ANT = 32 * WM * WN;
+    static_assert(MT == 16 * RM * WM && KT <= ANT && RANGE % KT == 0, "warp layout");
+    using S = AttnSmem<D, MT, KT>;
     constexpr int KW = KT / WN;       // keys per warp and tile
     constexpr int NF = KW / 8;        // score fragments
     constexpr int DC = D / 8;         // 16-byte chunks per row
@@ -63,14 +66,17 @@ __global__ void __launch_bounds__(ANT) attend_kernel(const AttnArgs a) {
     int* poison = reinterpret_cast<int*>(smem + S::OFF + 2 * 2 * KT * 8);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int wm = warp / WN, wn = warp % WN;
-    grid_dependency_wait();
+    // When finishing, the launch before is the prefix's own: what that one waited for is there, and its
+    // parts are waited for at the end, so that suffixes run where and as soon as it leaves room.
+    if (!a.finish) grid_dependency_wait();
     allow_dependents();
 
     // ---- this CTA's queries and keys
     int item = blockIdx.x;
     const int np = a.ptiles * a.Hkv * a.SP;
     const bool pre = item < np;
-    int head, split, b0, M, row0, len, begin, slot;
+    int head, split, b0, M, row0, len, begin, slot, page0 = -1;
+    bool early = false;
     const int* table;
     if (pre) {
         const int tile = item % a.ptiles;
@@ -99,16 +105,22 @@ __global__ void __launch_bounds__(ANT) attend_kernel(const AttnArgs a) {
         b0 = item / a.stiles;
         M = a.Q * a.gs;
         row0 = tile * MT;
+        table = a.stab + int64_t(b0) * a.sw;
+        // One range starts at the first key whatever the length: its first pages are read beside the length.
+        early = a.SS == 1;
+        if (early && tid < KT) {
+            const int pi = a.page_shift >= 0 ? tid >> a.page_shift : tid / a.page_size;
+            if (pi < a.sw) page0 = table[pi];
+        }
         len = suffix_len(a, b0);
         const int step = range_len(len, a.SS);
         begin = split * step;
-        if (begin >= len) return;
-        table = a.stab + int64_t(b0) * a.sw;
+        if (begin >= len && !a.finish) return;
         slot = a.SP + split;
     }
     const int full = pre ? len : suffix_len(a, b0);          // the row's whole suffix
     const int end = pre ? len : min(len, begin + range_len(len, a.SS));
-    const int tiles = (end - begin + KT - 1) / KT;
+    const int tiles = (end - begin + KT - 1) / KT;   // 0: only when finishing
 
     // Query r of the tile: row b0 + r / (Q gs), query token, head; -1 past the last.
     auto query_at = [&](int r, int& b, int& qi, int& h) {
@@ -136,7 +148,7 @@ __global__ void __launch_bounds__(ANT) attend_kernel(const AttnArgs a) {
         const int key = begin + tile * KT + tid;
         if (tid < KT && key < end) {
             const int pi = a.page_shift >= 0 ? key >> a.page_shift : key / a.page_size;
-            const int page = table[pi];
+            const int page = tile == 0 && early ? page0 : table[pi];
             if (page >= 0 && page < a.num_pages) {
                 const int s = key - pi * a.page_size;
                 ko = page * a.kc[0] + s * a.kc[1] + head * a.kc[2];
@@ -177,6 +189,14 @@ __global__ void __launch_bounds__(ANT) attend_kernel(const AttnArgs a) {
     }
     look_up(ASTAGES - 1, ko, vo, bad);
     put_offsets(ASTAGES - 1, ko, vo, bad);
+    int parts = 0;      // of the prefix, to be joined here
+    if (a.finish) {
+        const int g = group_of(a, b0, lane);
+        if (g >= 0) {
+            const int plen = prefix_len(a, g);
+            if (plen > 0) { const int pstep = range_len(plen, a.SP); parts = (plen + pstep - 1) / pstep; }
+        }
+    }
 
     float o[RM][D / 8][4];
     float mrow[RM][2], lrow[RM][2];
@@ -316,10 +336,12 @@ __global__ void __launch_bounds__(ANT) attend_kernel(const AttnArgs a) {
                         sum += x;
                     }
                 lrow[i][j] = lrow[i][j] * alpha + sum;
+                if (__any_sync(FULL, alpha != 1.f)) {
 #pragma unroll
-                for (int f = 0; f < D / 8; ++f) {
-                    o[i][f][j * 2] *= alpha;
-                    o[i][f][j * 2 + 1] *= alpha;
+                    for (int f = 0; f < D / 8; ++f) {
+                        o[i][f][j * 2] *= alpha;
+                        o[i][f][j * 2 + 1] *= alpha;
+                    }
                 }
             }
             // The weights enter the product in 16 bits (each off by half a step of the type);
@@ -376,12 +398,18 @@ __global__ void __launch_bounds__(ANT) attend_kernel(const AttnArgs a) {
     __syncthreads();
     const float nan = *poison ? __int_as_float(0x7fffffff) : 0.f;
     const int64_t rows = int64_t(a.B) * a.Q * a.Hq;
+    if (a.finish) grid_dependency_wait();
     for (int i = tid; i < MT * (D / 4); i += ANT) {
         const int r = i / (D / 4), c = i % (D / 4);
         if (row0 + r >= M) continue;
+        int b, qi, h;
+        query_at(row0 + r, b, qi, h);
+        const int64_t row = (int64_t(b) * a.Q + qi) * a.Hq + h;
         float m = -INFINITY;
 #pragma unroll
         for (int w = 0; w < WN; ++w) m = fmaxf(m, sm[w * MT + r]);
+#pragma unroll 8
+        for (int s = 0; s < parts; ++s) m = fmaxf(m, a.part_l[s * rows + row]);
         const float ms = m == -INFINITY ? 0.f : m;
         float l = 0.f;
         float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -392,12 +420,24 @@ __global__ void __launch_bounds__(ANT) attend_kernel(const AttnArgs a) {
             l += f * sl[w * MT + r];
             x.x += f * y.x, x.y += f * y.y, x.z += f * y.z, x.w += f * y.w;
         }
+#pragma unroll 4
+        for (int s = 0; s < parts; ++s) {
+            const float f = exp2f(a.part_l[s * rows + row] - ms);
+            const float4 y = *reinterpret_cast<const float4*>(a.part_o + (s * rows + row) * D + c * 4);
+            l += f;
+            x.x += f * y.x, x.y += f * y.y, x.z += f * y.z, x.w += f * y.w;
+        }
         const float inv = (l == 0.f ? 0.f : 1.f / l) + nan;
-        int b, qi, h;
-        query_at(row0 + r, b, qi, h);
-        const int64_t at = slot * rows + (int64_t(b) * a.Q + qi) * a.Hq + h;
-        *reinterpret_cast<float4*>(a.part_o + at * D + c * 4) = make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv);
-        if (c == 0) a.part_l[at] = (l == 0.f ? -INFINITY : m + log2f(l)) + nan;
+        const float lse = (l == 0.f ? -INFINITY : m + log2f(l)) + nan;
+        if (a.finish) {
+            T* out = static_cast<T*>(a.out) + b * a.os[0] + qi * a.os[1] + h * a.os[2] + c * 4;
+            *reinterpret_cast<uint2*>(out) = make_uint2(Mma<T>::pack(x.x * inv, x.y * inv), Mma<T>::pack(x.z * inv, x.w * inv));
+            if (c == 0 && a.lse) a.lse[row] = lse * 0.693147180559945309f;
+        } else {
+            const int64_t at = slot * rows + row;
+            *reinterpret_cast<float4*>(a.part_o + at * D + c * 4) = make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv);
+            if (c == 0) a.part_l[at] = lse;
+        }
     }
 }
 
@@ -507,10 +547,11 @@ static AttnPlan attn_plan(int B, int Q, int Hq, int Hkv, int D, int G, int64_t m
     // the most tiles that `all` queries in G groups can take
     p.ptiles = prefix ? int(std::min<int64_t>(all, (all + int64_t(G) * (rows - 1)) / rows)) : 0;
     p.stiles = max_suffix > 0 ? int((int64_t(Q) * gs + p.MT - 1) / p.MT) : 0;
-    // Key ranges in attend_kernel: about three CTAs for every SM, no range shorter than four tiles.
+    // Key ranges in attend_kernel: about three CTAs for every SM, no range shorter than 128 keys (of 64,
+    // 128 and 256, 128 was the fastest for one to eight rows over 256 to 64000 keys).
     auto splits = [&](int64_t items, int64_t len) {
         if (items == 0 || len <= 0) return int64_t(0);
-        const int64_t by_len = (len + 4 * KT - 1) / (4 * KT);
+        const int64_t by_len = (len + 2 * RANGE - 1) / (2 * RANGE);
         return std::max<int64_t>(1, std::min<int64_t>({(int64_t(sms) * 3 + items - 1) / items, by_len, 256}));
     };
     p.SP = int(splits(int64_t(p.ptiles) * Hkv, max_prefix));
@@ -525,16 +566,20 @@ static AttnPlan attn_plan(int B, int Q, int Hq, int Hkv, int D, int G, int64_t m
         }
     }
     p.SS = int(splits(int64_t(B) * p.stiles * Hkv, max_suffix));
+    // Behind the prefix's own launch a suffix of one range is joined where it is computed, which
+    // saves a launch: 48 rows of up to 700 keys 53.7 -> 43.9 us, 16 of 300 66.3 -> 62.5; but 16 of
+    // 1000 28.2 -> 34.5, so not where the ranges shorten it by more than that.
+    if (p.tensor && (max_suffix <= 5 * RANGE || (p.SS <= 2 && max_suffix <= 16 * RANGE))) p.SS = std::min(p.SS, 1);
     p.bytes = size_t(p.SP + p.SS) * size_t(B) * Q * Hq * (size_t(D) + 1) * 4;
     return p;
 }
 
-template <typename T, int D, int MT, int WM, int WN, int RM>
+template <typename T, int D, int MT, int WM, int WN, int RM, int KT>
 static fs_status launch_attend(const AttnArgs& a, unsigned grid, void* stream) {
-    const void* fn = reinterpret_cast<const void*>(attend_kernel<T, D, MT, WM, WN, RM>);
+    const void* fn = reinterpret_cast<const void*>(attend_kernel<T, D, MT, WM, WN, RM, KT>);
     const fs_status st = prepare_kernel(fn);
     if (st != FS_OK) return st;
-    return launch_pdl(attend_kernel<T, D, MT, WM, WN, RM>, grid, ANT, size_t(AttnSmem<D, MT>::TOTAL), stream, a);
+    return launch_pdl(attend_kernel<T, D, MT, WM, WN, RM, KT>, grid, 32 * WM * WN, size_t(AttnSmem<D, MT, KT>::TOTAL), stream, a);
 }
 
 template <typename T, int D>
@@ -547,13 +592,14 @@ static fs_status run_attention(AttnArgs& a, const AttnPlan& p, int dtype, void* 
         st = launch_prefix_tensor(a, dtype, D, p.tensor, stream);
         if (st != FS_OK) return st;
         a.ptiles = 0;
+        a.finish = p.SS == 1;
     }
     if (items > 0) {
-        if (p.MT == 16) st = launch_attend<T, D, 16, 1, 4, 1>(a, unsigned(items), stream);
-        else if (p.MT == 32) st = launch_attend<T, D, 32, 2, 2, 1>(a, unsigned(items), stream);
-        else if constexpr (D <= 128) st = launch_attend<T, D, 64, 2, 2, 2>(a, unsigned(items), stream);
-        else st = launch_attend<T, D, 64, 4, 1, 1>(a, unsigned(items), stream);
-        if (st != FS_OK) return st;
+        if (p.MT == 16) st = launch_attend<T, D, 16, 1, 4, 1, 64>(a, unsigned(items), stream);
+        else if (p.MT == 32) st = launch_attend<T, D, 32, 2, 2, 1, 64>(a, unsigned(items), stream);
+        else if constexpr (D <= 128) st = launch_attend<T, D, 64, 2, 2, 2, 64>(a, unsigned(items), stream);
+        else st = launch_attend<T, D, 64, 4, 1, 1, 64>(a, unsigned(items), stream);
+        if (st != FS_OK || a.finish) return st;
     }
     const int64_t rows = int64_t(a.B) * a.Q * a.Hq;
     return launch_pdl(join_kernel<T, D>, unsigned(rows), 128, 0, stream, a);

@@ -148,6 +148,37 @@ __device__ __forceinline__ float max_of(const uint4& w, __half) {
     const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&x));
     return max_nan(f.x, f.y);
 }
+// A bound for `hits`: rounded down to the type.
+__device__ __forceinline__ uint32_t bound_of(float z, float) { return __float_as_uint(z); }
+__device__ __forceinline__ uint32_t bound_of(float z, __nv_bfloat16) {
+    const uint32_t h = __bfloat16_as_ushort(__float2bfloat16_rd(z));
+    return h | h << 16;
+}
+__device__ __forceinline__ uint32_t bound_of(float z, __half) {
+    const uint32_t h = __half_as_ushort(__float2half_rd(z));
+    return h | h << 16;
+}
+// Bit e: element e of the word is at or above the bound (a NaN never is).  The 16-bit types compare two at a time.
+__device__ __forceinline__ uint32_t hits(const uint4& w, uint32_t bound, float) {
+    const float z = __uint_as_float(bound);
+    return (__uint_as_float(w.x) >= z ? 1u : 0u) | (__uint_as_float(w.y) >= z ? 2u : 0u) |
+           (__uint_as_float(w.z) >= z ? 4u : 0u) | (__uint_as_float(w.w) >= z ? 8u : 0u);
+}
+__device__ __forceinline__ uint32_t squeeze(uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+    // words of 0xffff where a half passes: bits 2 j of the low halves, 2 j + 1 of the high ones
+    const uint32_t m = (x & 0x00010001u) | (y & 0x00040004u) | (z & 0x00100010u) | (w & 0x00400040u);
+    return (m | m >> 15) & 0xffu;
+}
+__device__ __forceinline__ uint32_t hits(const uint4& w, uint32_t bound, __nv_bfloat16) {
+    const __nv_bfloat162 z = *reinterpret_cast<const __nv_bfloat162*>(&bound);
+    const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&w);
+    return squeeze(__hge2_mask(h[0], z), __hge2_mask(h[1], z), __hge2_mask(h[2], z), __hge2_mask(h[3], z));
+}
+__device__ __forceinline__ uint32_t hits(const uint4& w, uint32_t bound, __half) {
+    const __half2 z = *reinterpret_cast<const __half2*>(&bound);
+    const __half2* h = reinterpret_cast<const __half2*>(&w);
+    return squeeze(__hge2_mask(h[0], z), __hge2_mask(h[1], z), __hge2_mask(h[2], z), __hge2_mask(h[3], z));
+}
 // Order key with -0 equal to +0.
 __device__ __forceinline__ uint32_t ukey(float z) { return logit_key(z + 0.f); }
 __device__ __forceinline__ float exp2_approx(float x) {
@@ -169,9 +200,9 @@ __global__ void __launch_bounds__(256) seg_max_kernel(const UniformArgs a) {
     allow_dependents();
     const int lane = threadIdx.x & 31;
     const int trips = (a.ls + USEG_TRIP - 1) / USEG_TRIP;
-    const int64_t total = int64_t(a.batch_in) * trips;
-    for (int64_t w = int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5); w < total; w += int64_t(gridDim.x) * 8) {
-        const int r = int(w / trips), s0 = int(w - int64_t(r) * trips) * USEG_TRIP;
+    const uint32_t total = uint32_t(a.batch_in) * uint32_t(trips);   // (of 2 KB each: far below 2^32)
+    for (uint32_t w = blockIdx.x * 8 + (threadIdx.x >> 5); w < total; w += gridDim.x * 8) {
+        const int r = int(w / uint32_t(trips)), s0 = int(w - uint32_t(r) * uint32_t(trips)) * USEG_TRIP;
         const R row(a.x, a.stride, r, a.V);
         uint4 v[USEG_TRIP];
 #pragma unroll
@@ -355,6 +386,12 @@ __device__ __forceinline__ X* peer(X* p, int rank) {
 __device__ __forceinline__ void sync(int C) {
     if (C == 1) __syncthreads();
     else cluster_sync();
+}
+
+// Sum over the warp of masses below 2^48 each, in every lane: three words whose sums fit in 32 bits.
+__device__ __forceinline__ unsigned long long warp_mass(unsigned long long v) {
+    const uint32_t a = __reduce_add_sync(FULL, uint32_t(v) & 0xffffffu), b = __reduce_add_sync(FULL, uint32_t(v >> 24) & 0xffffffu);
+    return (unsigned long long)b * (1u << 24) + a;
 }
 
 // Block-wide sum of a 64-bit value, in every thread.
@@ -619,7 +656,7 @@ __global__ void __launch_bounds__(UNT, 2) uniform_kernel(const UniformArgs a) {
                 // The live segments in order, then 64 of them at a time, four per warp: their elements at
                 // or above zt, counted, placed by a prefix over the segments, written in index order.
                 int* live = reinterpret_cast<int*>(hist.lo);
-                const uint32_t kt = ukey(zt);
+                const uint32_t kt = ukey(zt), zb = bound_of(zt, T());
                 const int chunk = (row.nseg + UNT - 1) / UNT;
                 const int f0 = min(row.nseg, tid * chunk), f1 = min(row.nseg, f0 + chunk);
                 uint32_t nl = 0;
@@ -644,11 +681,7 @@ __global__ void __launch_bounds__(UNT, 2) uniform_kernel(const UniformArgs a) {
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         if (i0 + warp * 4 + j < n_live) {
-                            float z[R::N];
-                            unpack(v[j], z, T());
-                            uint32_t h = 0;
-#pragma unroll
-                            for (int e = 0; e < R::N; ++e) h |= z[e] >= zt ? 1u << e : 0u;
+                            const uint32_t h = hits(v[j], zb, T());
                             hit |= h << (8 * j);
                             cnt[j >> 1] += __popc(h) << (16 * (j & 1));
                         }
@@ -722,35 +755,47 @@ __global__ void __launch_bounds__(UNT, 2) uniform_kernel(const UniformArgs a) {
             n = c->n;
             for (int i = tid; i < n; i += UNT) lw[i] = wt.weight_of(from_logit_key(lkey[i]));
             __syncthreads();
-            // Threads per candidate (a power of two, within a warp), each over its share of the list.
-            while (tpc < 32 && tpc * 2 * n <= UNT) tpc *= 2;
+            while (tpc < 32 && tpc * 2 * ((n + 3) / 4) <= UNT) tpc *= 2;
         }
-        const int sub = tid % tpc;
-        constexpr int PER = UCAP / UNT;   // candidates per thread, at most
+        // Four candidates a thread, `tpc` threads for the same four, each over its share of the list.
+        constexpr int PER = 4;
+        const int sub = tid % tpc, i0 = tid / tpc * PER;
         unsigned long long above[PER], wi[PER];
         bool keep[PER];
         bool exact = !whole;
         for (int turn = 0; turn < 2; ++turn) {
             bool unsure = false;
             if (rank == 0 && turn == 0) {
+                uint32_t ki[PER];
+                int cnt[PER];
 #pragma unroll
                 for (int x = 0; x < PER; ++x) {
-                    const int i = tid / tpc + x * UNT;
-                    wi[x] = i < n ? lw[i] : 0;
-                    keep[x] = i < n;
+                    const bool in = i0 + x < n;
+                    wi[x] = in ? lw[i0 + x] : 0;
+                    ki[x] = in ? lkey[i0 + x] : 0xffffffffu;
+                    keep[x] = in;
                     above[x] = 0;
-                    if ((has_k || has_p) && x * UNT < n) {
-                        const uint32_t ki = i < n ? lkey[i] : 0xffffffffu;
-                        int cnt = 0;
-#pragma unroll 4
-                        for (int j = sub; j < n; j += tpc)
-                            if (lkey[j] > ki) ++cnt, above[x] += lw[j];
-                        for (int d = 1; d < tpc; d *= 2) {
-                            cnt += __shfl_xor_sync(FULL, cnt, d);
+                    cnt[x] = 0;
+                }
+                if (has_k || has_p) {
+#pragma unroll 2
+                    for (int j = sub; j < n; j += tpc) {
+                        const uint32_t kj = lkey[j];
+                        const unsigned long long wj = lw[j];
+#pragma unroll
+                        for (int x = 0; x < PER; ++x)
+                            if (kj > ki[x]) ++cnt[x], above[x] += wj;
+                    }
+                    for (int d = 1; d < tpc; d *= 2) {
+#pragma unroll
+                        for (int x = 0; x < PER; ++x) {
+                            cnt[x] += __shfl_xor_sync(FULL, cnt[x], d);
                             above[x] += __shfl_xor_sync(FULL, above[x], d);
                         }
-                        if (has_k) keep[x] = keep[x] && cnt < k;  // ties with the k-th are kept
                     }
+#pragma unroll
+                    for (int x = 0; x < PER; ++x)
+                        if (has_k) keep[x] = keep[x] && cnt[x] < k;  // ties with the k-th are kept
                 }
             }
             if (rank == 0 && has_p && !whole) {
@@ -796,22 +841,11 @@ __global__ void __launch_bounds__(UNT, 2) uniform_kernel(const UniformArgs a) {
         }
         if (rank != 0) return;
         // ---- the draw: candidates are in index order
+        // (the threads that share candidates sit beside one another: the first of them holds them)
         unsigned long long own[PER], v = 0;
-        if (tpc == 1) {
-            // thread t holds candidates t and t + UNT: written back, then taken as neighbours
-#pragma unroll
-            for (int x = 0; x < PER; ++x) {
-                const int i = tid + x * UNT;
-                if (i < n) aw[i] = keep[x] && wi[x] >= wmin ? wi[x] : 0;
-            }
-        } else if (sub == 0 && tid / tpc < n) {
-            aw[tid / tpc] = keep[0] && wi[0] >= wmin ? wi[0] : 0;
-        }
-        __syncthreads();
 #pragma unroll
         for (int x = 0; x < PER; ++x) {
-            const int i = tid * PER + x;
-            own[x] = i < n ? aw[i] : 0;
+            own[x] = sub == 0 && keep[x] && wi[x] >= wmin ? wi[x] : 0;
             v += own[x];
         }
         const unsigned long long mine = v;
@@ -825,7 +859,7 @@ __global__ void __launch_bounds__(UNT, 2) uniform_kernel(const UniformArgs a) {
         if (v <= t && t - v < mine) {
 #pragma unroll
             for (int x = 0; x < PER; ++x) {
-                if (v <= t && t - v < own[x]) a.out_token[b] = lpos[tid * PER + x] - row.a0, a.out_valid[b] = 1;
+                if (v <= t && t - v < own[x]) a.out_token[b] = lpos[i0 + x] - row.a0, a.out_valid[b] = 1;
                 v += own[x];
             }
         }
@@ -885,13 +919,9 @@ __global__ void __launch_bounds__(UNT, 2) uniform_kernel(const UniformArgs a) {
             // each lane walks its own.
             const float drop = wt.drop_of(qb);
             const float zl = wt.m - drop - 0x1p-18f * (fabsf(wt.m) + drop);
-            const uint32_t kz = zl == zl ? ukey(zl) : 0u;
+            const uint32_t kz = zl == zl ? ukey(zl) : 0u, zb = bound_of(zl, T());
             auto walk = [&](int s, const uint4& v) {
-                float z[R::N];
-                unpack(v, z, T());
-                uint32_t hit = 0;
-#pragma unroll
-                for (int e = 0; e < R::N; ++e) hit |= z[e] >= zl || kz == 0u ? 1u << e : 0u;
+                uint32_t hit = kz ? hits(v, zb, T()) : (1u << R::N) - 1;
                 unsigned long long sum = 0;
                 while (hit) {
                     const int e = __ffs(hit) - 1;
@@ -909,7 +939,7 @@ __global__ void __launch_bounds__(UNT, 2) uniform_kernel(const UniformArgs a) {
                     }
                 }
                 if (last) {
-                    sum = warp_sum_u64(sum);
+                    sum = warp_mass(sum);
                     if (lane == 0) smass[s - s0] = sum;
                 }
             };
@@ -1040,22 +1070,19 @@ __global__ void __launch_bounds__(UNT, 2) uniform_kernel(const UniformArgs a) {
     }
     // ---- kept mass of every segment, then of every CTA
     unsigned long long own = 0;
+    const uint32_t zb = bound_of(from_logit_key(theta), T());   // (theta is an element's or the floor's key)
     if (summed) {
         for (int i = tid; i < s1 - s0; i += UNT) own += smass[i];
     } else {
         for (int s = s0 + warp; s < s1; s += UNW) {
             unsigned long long v = 0;
             if (segs[s] >= theta) {
-                float z[R::N];
-                unpack(row.load(s, lane), z, T());
-#pragma unroll
-                for (int e = 0; e < R::N; ++e) {
-                    if (ukey(z[e]) >= theta) {
-                        const unsigned long long w = wt.weight_of(z[e]);
-                        if (w >= wmin) v += w;
-                    }
+                const uint4 x = row.load(s, lane);
+                for (uint32_t hit = hits(x, zb, T()); hit; hit &= hit - 1) {
+                    const unsigned long long w = wt.weight_of(element(x, __ffs(hit) - 1, T()));
+                    if (w >= wmin) v += w;
                 }
-                v = warp_sum_u64(v);
+                v = warp_mass(v);
             }
             if (lane == 0) {
                 smass[s - s0] = v;

@@ -425,13 +425,13 @@ static fs_status launch_append(AppendArgs& a, void* stream) {
     a.units = int(units);
     const int heads = (a.query ? a.q_heads : 0) + a.kv_heads;
     int threads;
-    int64_t per;   // tokens of a CTA, as long as every SM still gets eight CTAs
+    int64_t per;   // tokens of a CTA, as long as every SM still gets four (eight) CTAs
     if (VW > 1) {
         // Whole rounds of heads: as few as 256 threads take, each as full as the others.
         const int rounds = (heads * a.per_rot + 255) / 256;
         const int at_once = std::min(256 / a.per_rot, (heads + rounds - 1) / rounds);
         threads = (at_once * a.per_rot + 31) / 32 * 32;
-        per = std::min<int64_t>(4, a.tokens / (int64_t(sms) * 8));
+        per = std::min<int64_t>(4, a.tokens / (int64_t(sms) * 4));
     } else {
         threads = int(std::min<int64_t>(256, (units + 31) / 32 * 32));
         per = std::min<int64_t>((2048 + units - 1) / units, a.tokens / (int64_t(sms) * 8));

@@ -31,6 +31,8 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <type_traits>
+
 #include "fs_device.cuh"
 #include "fs_host.h"
 
@@ -265,6 +267,30 @@ __constant__ uint32_t EXP2_256[256] = {
     0xf5257d15u, 0xf5cfa434u, 0xf67a416cu, 0xf7255511u, 0xf7d0df73u, 0xf87ce0e6u, 0xf92959bbu, 0xf9d64a47u,
     0xfa83b2dbu, 0xfb3193ccu, 0xfbdfed6du, 0xfc8ec011u, 0xfd3e0c0du, 0xfdedd1b5u, 0xfe9e115cu, 0xff4ecb59u,};
 
+// Two floats in one register pair.
+__device__ __forceinline__ uint64_t two(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float low2(uint64_t x) { return __uint_as_float(uint32_t(x)); }
+__device__ __forceinline__ float high2(uint64_t x) { return __uint_as_float(uint32_t(x >> 32)); }
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+
 struct Weigher {
     float hm;          // m / 2
     float ch, cl;      // 2 log2(e) / T as a sum of two floats
@@ -281,8 +307,8 @@ struct Weigher {
     // floats (halved operands, so that the difference cannot overflow; its rounding error
     // by the two-sum); split into n + j / 256 + r, |r| <= 1/512; 2^r - 1 as a cubic in float32 (below
     // 2^-9, so its rounding is 2^-33 of the weight); the table's 2^(j / 256) times that in
-    // integers.  About 36 instructions; with a table of 32 and 2^r - 1 in two floats it
-    // took 58 for a relative 4e-11.
+    // integers.  About 40 instructions, 30 by twos; with a table of 32 and 2^r - 1 in two
+    // floats it took 58 for a relative 4e-11.
     __device__ __forceinline__ unsigned long long weight_of(float z) const {
         int q;
         return weight_of(z, q);
@@ -293,24 +319,47 @@ struct Weigher {
         const float d = __fsub_rn(h, hm), bb = __fsub_rn(d, h);
         const float dl = __fadd_rn(__fsub_rn(h, __fsub_rn(d, bb)), __fsub_rn(-hm, bb));
         const float yh = __fmul_rn(d, ch);
-        steps = LAST;
-        if (!(yh > -43.f)) return 0;  // also -inf, whose product with a zero slope is NaN
         float yl = fmaf(d, ch, -yh);
         yl = fmaf(d, cl, yl);
         yl = fmaf(dl, ch, yl);
         const float t = fmaf(yh, 256.f, 12582912.f);  // + 1.5 * 2^23: the nearest integer in the low bits
-        const int q = 0x4B400000 - __float_as_int(t);
         const float r = __fadd_rn(fmaf(__fsub_rn(t, 12582912.f), -0.00390625f, yh), yl);
         // (2^r - 1) 2^33
         const float s = __fmul_rn(r, fmaf(r, fmaf(r, 0.05550410866482158f * 0x1p33f, 0.2402265069591007f * 0x1p33f),
                                           0.6931471805599453f * 0x1p33f));
-        const uint32_t tj = tab[-q & 255];
+        return assemble(yh, t, s, steps);
+    }
+    // The same of two, by instructions on two floats: the same operations, the same results.
+    __device__ __forceinline__ void weights_of(float z0, float z1, unsigned long long (&w)[2], int (&steps)[2]) const {
+        const uint64_t one = two(-1.f, -1.f), h = mul2(two(z0, z1), two(0.5f, 0.5f)), nhm = two(-hm, -hm), c = two(ch, ch),
+                       nc = two(-ch, -ch);
+        const uint64_t d = add2(h, nhm), bb = fma2(h, one, d);
+        const uint64_t dl = add2(fma2(fma2(bb, one, d), one, h), fma2(bb, one, nhm));
+        const uint64_t yh = mul2(d, c);
+        // the low part of the exponent, negated
+        const uint64_t yl = fma2(dl, nc, fma2(d, two(-cl, -cl), fma2(d, nc, yh)));
+        const uint64_t magic = two(12582912.f, 12582912.f), t = fma2(yh, two(256.f, 256.f), magic);
+        const uint64_t r0 = fma2(add2(t, two(-12582912.f, -12582912.f)), two(-0.00390625f, -0.00390625f), yh);
+        const uint64_t r = fma2(yl, one, r0);
+        constexpr float C3 = 0.05550410866482158f * 0x1p33f, C2 = 0.2402265069591007f * 0x1p33f, C1 = 0.6931471805599453f * 0x1p33f;
+        const uint64_t s = mul2(r, fma2(r, fma2(r, two(C3, C3), two(C2, C2)), two(C1, C1)));
+        w[0] = assemble(low2(yh), low2(t), low2(s), steps[0]);
+        w[1] = assemble(high2(yh), high2(t), high2(s), steps[1]);
+    }
+    // From the exponent yh, its steps t and 2^r - 1 (times 2^33): 2^42 of the weight, rounded.
+    __device__ __forceinline__ unsigned long long assemble(float yh, float t, float s, int& steps) const {
+        steps = LAST;
+        if (!(yh > -43.f)) return 0;  // also -inf, whose product with a zero slope is NaN
+        const uint32_t bits = __float_as_uint(t), tj = tab[bits & 255];
         const long long p = (long long)int(tj >> 1) * __float2int_rn(s) + (1ll << 31);
-        const uint32_t v = tj + uint32_t(p >> 32);  // 2^31 times the significand
-        const int n = (q + 255) >> 8;               // its binary orders below the maximum
-        steps = q;
-        if (n > 12) return ((v >> (n - 12)) + 1) >> 1;
-        return (((unsigned long long)v << (12 - n)) + 1) >> 1;
+        const uint32_t v = tj + uint32_t(p >> 32);                // 2^31 times the significand
+        const uint32_t n = (0x4B400000u >> 8) - (bits >> 8);       // its binary orders below the maximum
+        steps = int(0x4B400000u - bits);
+        // v 2^(11 - n): the product's low words while that is whole, else its high word (the factor is
+        // 2^32 larger), rounded.
+        const bool whole = n <= 11;
+        const unsigned long long x = (unsigned long long)v * (1u << ((11 - n) & 31)) + (whole ? 0u : 0x80000000u);
+        return whole ? x : x >> 32;
     }
     // Bin of z, 0 the largest: 8 of those steps (0.022 T).  Each operation is monotone in z, so a lower
     // bin means larger z; the last bin's weights all round to 0.
@@ -351,7 +400,7 @@ struct UCtl {
     uint32_t tab[256];
     unsigned long long red[UNW];
     uint32_t redc[UNW];
-    unsigned long long cmass[MAX_CLUSTER];
+    unsigned long long cmass[MAX_CLUSTER], cin[MAX_CLUSTER];
     unsigned long long above, in_mass;  // find_bin's results
     uint32_t above_cnt, in_cnt;
     int bin;
@@ -534,8 +583,8 @@ __global__ void __launch_bounds__(UNT, 2) uniform_kernel(const UniformArgs a) {
     unsigned long long* aw = reinterpret_cast<unsigned long long*>(smem + USmem::AW);
     const Hist hist{reinterpret_cast<uint32_t*>(smem + USmem::HIST)};
     unsigned long long* smass = reinterpret_cast<unsigned long long*>(smem + USmem::HIST);  // [nsc], after the histograms
-    unsigned long long* tmass = smass + UB;
-    uint32_t* hcnt = reinterpret_cast<uint32_t*>(tmass + UB);
+    uint32_t* tmass = reinterpret_cast<uint32_t*>(smass + UB);   // the cluster's masses, rounded, and counts
+    uint32_t* hcnt = tmass + 2 * UB;
     uint32_t* tcnt = hcnt + UB;
     uint32_t* segs = reinterpret_cast<uint32_t*>(smem + USmem::seg_at(a.nsc));
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -618,10 +667,33 @@ __global__ void __launch_bounds__(UNT, 2) uniform_kernel(const UniformArgs a) {
         }
     };
     auto all = [](uint32_t) { return true; };
+    // fn(z0, z1) over neighbouring elements of all of them.
+    auto pairs = [&](auto fn) {
+        for (int s = s0 + warp; s < s1; s += UNW * 2) {
+            const bool more = s + UNW < s1;
+            const uint4 v0 = row.load(s, lane);
+            uint4 v1 = v0;
+            if (more) v1 = row.load(s + UNW, lane);
+            float z[R::N];
+            unpack(v0, z, T());
+#pragma unroll
+            for (int e = 0; e < R::N; e += 2) fn(z[e], z[e + 1]);
+            if (more) {
+                unpack(v1, z, T());
+#pragma unroll
+                for (int e = 0; e < R::N; e += 2) fn(z[e], z[e + 1]);
+            }
+        }
+    };
     // The row's mass from exact weights.  Cluster-wide.
     auto exact_mass = [&]() {
         unsigned long long v = 0, M = 0;
-        each(all, [&](float z, int, int) { v += wt.weight_of(z); });
+        pairs([&](float z0, float z1) {
+            unsigned long long w[2];
+            int q[2];
+            wt.weights_of(z0, z1, w, q);
+            v += w[0] + w[1];
+        });
         v = block_sum(v, c);
         if (tid < C) peer(c->cmass, tid)[rank] = v;
         sync(C);
@@ -750,53 +822,58 @@ __global__ void __launch_bounds__(UNT, 2) uniform_kernel(const UniformArgs a) {
                 Mf = v;
             }
         }
-        int n = 0, tpc = 1;
+        int n = 0, tpc = 1, per_thread = 1;
         if (rank == 0) {
             n = c->n;
             for (int i = tid; i < n; i += UNT) lw[i] = wt.weight_of(from_logit_key(lkey[i]));
             __syncthreads();
-            while (tpc < 32 && tpc * 2 * ((n + 3) / 4) <= UNT) tpc *= 2;
+            per_thread = n <= 128 ? 1 : 4;
+            while (tpc < (n <= 128 ? 8 : 32) && tpc * 2 * ((n + per_thread - 1) / per_thread) <= UNT) tpc *= 2;
         }
-        // Four candidates a thread, `tpc` threads for the same four, each over its share of the list.
+        // Four candidates a thread (one, up to 128), `tpc` threads for the same ones, each over its
+        // share of the list.
         constexpr int PER = 4;
-        const int sub = tid % tpc, i0 = tid / tpc * PER;
-        unsigned long long above[PER], wi[PER];
-        bool keep[PER];
+        const int sub = tid % tpc, i0 = tid / tpc * per_thread;
+        unsigned long long above[PER] = {0, 0, 0, 0}, wi[PER] = {0, 0, 0, 0};
+        bool keep[PER] = {false, false, false, false};
+        auto compare = [&](auto count) {
+            constexpr int N = decltype(count)::value;
+            uint32_t ki[N];
+            int cnt[N];
+#pragma unroll
+            for (int x = 0; x < N; ++x) {
+                const bool in = i0 + x < n;
+                wi[x] = in ? lw[i0 + x] : 0;
+                ki[x] = in ? lkey[i0 + x] : 0xffffffffu;
+                keep[x] = in;
+                cnt[x] = 0;
+            }
+            if (!has_k && !has_p) return;
+#pragma unroll 2
+            for (int j = sub; j < n; j += tpc) {
+                const uint32_t kj = lkey[j];
+                const unsigned long long wj = lw[j];
+#pragma unroll
+                for (int x = 0; x < N; ++x)
+                    if (kj > ki[x]) ++cnt[x], above[x] += wj;
+            }
+            for (int d = 1; d < tpc; d *= 2) {
+#pragma unroll
+                for (int x = 0; x < N; ++x) {
+                    cnt[x] += __shfl_xor_sync(FULL, cnt[x], d);
+                    above[x] += __shfl_xor_sync(FULL, above[x], d);
+                }
+            }
+#pragma unroll
+            for (int x = 0; x < N; ++x)
+                if (has_k) keep[x] = keep[x] && cnt[x] < k;  // ties with the k-th are kept
+        };
         bool exact = !whole;
         for (int turn = 0; turn < 2; ++turn) {
             bool unsure = false;
             if (rank == 0 && turn == 0) {
-                uint32_t ki[PER];
-                int cnt[PER];
-#pragma unroll
-                for (int x = 0; x < PER; ++x) {
-                    const bool in = i0 + x < n;
-                    wi[x] = in ? lw[i0 + x] : 0;
-                    ki[x] = in ? lkey[i0 + x] : 0xffffffffu;
-                    keep[x] = in;
-                    above[x] = 0;
-                    cnt[x] = 0;
-                }
-                if (has_k || has_p) {
-#pragma unroll 2
-                    for (int j = sub; j < n; j += tpc) {
-                        const uint32_t kj = lkey[j];
-                        const unsigned long long wj = lw[j];
-#pragma unroll
-                        for (int x = 0; x < PER; ++x)
-                            if (kj > ki[x]) ++cnt[x], above[x] += wj;
-                    }
-                    for (int d = 1; d < tpc; d *= 2) {
-#pragma unroll
-                        for (int x = 0; x < PER; ++x) {
-                            cnt[x] += __shfl_xor_sync(FULL, cnt[x], d);
-                            above[x] += __shfl_xor_sync(FULL, above[x], d);
-                        }
-                    }
-#pragma unroll
-                    for (int x = 0; x < PER; ++x)
-                        if (has_k) keep[x] = keep[x] && cnt[x] < k;  // ties with the k-th are kept
-                }
+                if (per_thread == 1) compare(std::integral_constant<int, 1>());
+                else compare(std::integral_constant<int, PER>());
             }
             if (rank == 0 && has_p && !whole) {
                 unsigned long long F = 0;
@@ -870,32 +947,56 @@ __global__ void __launch_bounds__(UNT, 2) uniform_kernel(const UniformArgs a) {
     uint32_t theta = floor_key;
     bool summed = false;   // the segments' masses are there
     if (has_k || has_p) {
-        for (int i = tid; i < UB; i += UNT) hist.set(i, 0), hcnt[i] = 0;
+        // Masses go into the bins as 32-bit words, in units of 2^-shift of an integer weight: at
+        // most SEG times the segment maxima's weights, the row fits. (Adds that return nothing are
+        // nearly free; 64-bit sums, whose carry needs the old value, cost 10 us of 60.)  They only
+        // choose the bin: the masses above it and in it are summed exactly afterwards.
+        float ml = 0.f;
+        for (int s = tid; s < row.nseg; s += UNT)
+            if (segs[s] > KEY_NINF) ml += exp2_approx((from_logit_key(segs[s]) - wt.m) * (1.44269504f / temp));
+        ml = warp_sum(ml);
         __syncthreads();
-        if (has_k)
-            each(all, [&](float z, int, int) {
-                int q;
-                const unsigned long long w = wt.weight_of(z, q);
-                q /= Weigher::STEPS;
-                if (w) hist.add(q, w);
-                atomicAdd(hcnt + q, 1u);
-            });
-        else
-            each(all, [&](float z, int, int) {
-                int q;
-                const unsigned long long w = wt.weight_of(z, q);
-                if (w) hist.add(q / Weigher::STEPS, w);
-            });
-        // The cluster's histograms summed into every CTA's totals.
+        if (lane == 0) c->redc[warp] = __float_as_uint(ml);
+        for (int i = tid; i < UB; i += UNT) hist.lo[i] = 0, hcnt[i] = 0;
+        __syncthreads();
+        ml = warp_sum(lane < UNW ? __uint_as_float(c->redc[lane]) : 0.f);
+        const int shift = 11 + int(__float_as_uint(ml * (1.01f * R::SEG)) >> 23) - 126;  // 2^31 and its rounding
+        const unsigned long long half = 1ull << shift >> 1;
+        unsigned long long F = 0;
+        pairs([&](float z0, float z1) {
+            unsigned long long w[2];
+            int q[2];
+            wt.weights_of(z0, z1, w, q);
+            F += w[0] + w[1];
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                const uint32_t bin = uint32_t(q[x]) / Weigher::STEPS;
+                if (w[x]) atomicAdd(hist.lo + bin, uint32_t((w[x] + half) >> shift));
+                if (has_k) atomicAdd(hcnt + bin, 1u);
+            }
+        });
+        F = block_sum(F, c);
+        // The cluster's histograms summed into every CTA's totals, and the row's mass.
+        if (tid < C) peer(c->cmass, tid)[rank] = F;
         sync(C);
+        F = 0;
+        for (int q = 0; q < C; ++q) F += c->cmass[q];
         {
             const int n = UB / C;
-            for (int i = rank * n + tid; i < (rank + 1) * n; i += UNT) {
-                unsigned long long v = 0;
-                uint32_t m = 0;
-                for (int q = 0; q < C; ++q) v += hist.of(q)[i], m += *peer(hcnt + i, q);
-                for (int q = 0; q < C; ++q) *peer(tmass + i, q) = v, *peer(tcnt + i, q) = m;
+            for (int i = rank * n + tid; i < (rank + 1) * n && i <= LASTB; i += UNT) {
+                uint32_t v = 0, m = 0;
+                for (int q = 0; q < C; ++q) {
+                    v += *peer(hist.lo + i, q);
+                    if (has_k) m += *peer(hcnt + i, q);
+                }
+                for (int q = 0; q < C; ++q) {
+                    *peer(tmass + i, q) = v;
+                    if (has_k) *peer(tcnt + i, q) = m;
+                }
             }
+            for (int i = LASTB + 1 + tid; i < UB; i += UNT) tmass[i] = 0, tcnt[i] = 0;
+            if (!has_k)
+                for (int i = tid; i <= LASTB; i += UNT) tcnt[i] = 0;
         }
         sync(C);
         // The largest key whose elements at or above it reach `target` (count or mass); the mass at
@@ -903,62 +1004,74 @@ __global__ void __launch_bounds__(UNT, 2) uniform_kernel(const UniformArgs a) {
         // left in smass, of elements at or above that key and `also`.
         auto search = [&](bool by_mass, unsigned long long target, unsigned long long& fmass, bool last,
                           uint32_t also) -> uint32_t {
-            find_bin(static_cast<const unsigned long long*>(tmass), tcnt, by_mass, target, c);
-            const int qb = c->bin;
-            if (qb >= LASTB) return 0;  // reached only among elements without weight
-            unsigned long long above = c->above;
-            unsigned long long above_t = by_mass ? c->above : c->above_cnt;
-            fmass = above + c->in_mass;
-            __syncthreads();
-            if (tid == 0) c->n = 0;
-            if (last)
-                for (int i = tid; i < s1 - s0; i += UNT) smass[i] = 0;
-            __syncthreads();
-            // The bin's elements into this CTA's list; the weights of those above it summed.  Few lanes
-            // hold an element at or above the bin (zl: its lower edge less the edge's rounding), so
-            // each lane walks its own.
-            const float drop = wt.drop_of(qb);
-            const float zl = wt.m - drop - 0x1p-18f * (fabsf(wt.m) + drop);
-            const uint32_t kz = zl == zl ? ukey(zl) : 0u, zb = bound_of(zl, T());
-            auto walk = [&](int s, const uint4& v) {
-                uint32_t hit = kz ? hits(v, zb, T()) : (1u << R::N) - 1;
-                unsigned long long sum = 0;
-                while (hit) {
-                    const int e = __ffs(hit) - 1;
-                    hit &= hit - 1;
-                    const float x = element(v, e, T());
-                    const int q = wt.bin_of(x);
-                    if (q < qb) {
-                        if (last && ukey(x) >= also) {
-                            const unsigned long long w = wt.weight_of(x);
-                            if (w >= wmin) sum += w;
+            // (the last bin that the rounded masses reach, if rounding keeps them from the target)
+            find_bin(static_cast<const uint32_t*>(tmass), tcnt, by_mass, by_mass ? max(1ull, target >> shift) : target, c);
+            int qb = c->bin;
+            if (by_mass && qb > LASTB - 1) qb = LASTB - 1;
+            unsigned long long above = 0, above_t = c->above_cnt;
+            for (int turn = 0; turn < UB; ++turn) {
+                if (qb >= LASTB) return 0;  // reached only among elements without weight
+                __syncthreads();
+                if (tid == 0) c->n = 0;
+                if (last)
+                    for (int i = tid; i < s1 - s0; i += UNT) smass[i] = 0;
+                __syncthreads();
+                // The bin's elements into this CTA's list; the weights of those above it summed.  Few lanes
+                // hold an element at or above the bin (zl: its lower edge less the edge's rounding), so
+                // each lane walks its own.
+                const float drop = wt.drop_of(qb);
+                const float zl = wt.m - drop - 0x1p-18f * (fabsf(wt.m) + drop);
+                const uint32_t kz = zl == zl ? ukey(zl) : 0u, zb = bound_of(zl, T());
+                unsigned long long over = 0, inside = 0;   // mass above the bin, in it
+                auto walk = [&](int s, const uint4& v) {
+                    uint32_t hit = kz ? hits(v, zb, T()) : (1u << R::N) - 1;
+                    unsigned long long sum = 0;
+                    while (hit) {
+                        const int e = __ffs(hit) - 1;
+                        hit &= hit - 1;
+                        const float x = element(v, e, T());
+                        int q;
+                        const unsigned long long w = wt.weight_of(x, q);
+                        q /= Weigher::STEPS;
+                        if (q < qb) {
+                            over += w;
+                            if (ukey(x) >= also && w >= wmin) sum += w;
+                        } else if (q == qb) {
+                            inside += w;
+                            const int at = atomicAdd(&c->n, 1);
+                            if (at < UCAP) lkey[at] = ukey(x), lpos[at] = s - s0, lw[at] = w;
                         }
-                    } else if (q == qb) {
-                        const int at = atomicAdd(&c->n, 1);
-                        if (at < UCAP) lkey[at] = ukey(x), lpos[at] = s - s0;
                     }
+                    if (last) {
+                        sum = warp_mass(sum);
+                        if (lane == 0) smass[s - s0] = sum;
+                    }
+                };
+                for (int s = s0 + warp; s < s1; s += UNW * 2) {
+                    const bool one = segs[s] >= kz, two = s + UNW < s1 && segs[s + UNW] >= kz;
+                    uint4 v0, v1;
+                    if (one) v0 = row.load(s, lane);
+                    if (two) v1 = row.load(s + UNW, lane);
+                    if (one) walk(s, v0);
+                    if (two) walk(s + UNW, v1);
                 }
-                if (last) {
-                    sum = warp_mass(sum);
-                    if (lane == 0) smass[s - s0] = sum;
+                over = block_sum(over, c);
+                inside = block_sum(inside, c);
+                const int ln = c->n;
+                if (tid < C) peer(c->cn, tid)[rank] = ln, peer(c->cmass, tid)[rank] = over, peer(c->cin, tid)[rank] = inside;
+                sync(C);
+                int n = 0;
+                above = 0;
+                inside = 0;
+                for (int q = 0; q < C; ++q) n += c->cn[q], above += c->cmass[q], inside += c->cin[q];
+                fmass = above + inside;
+                if (by_mass && (above >= target || fmass < target)) {   // a rounded border: the bin beside
+                    qb += above >= target ? -1 : 1;
+                    sync(C);
+                    continue;
                 }
-            };
-            for (int s = s0 + warp; s < s1; s += UNW * 2) {
-                const bool one = segs[s] >= kz, two = s + UNW < s1 && segs[s + UNW] >= kz;
-                uint4 v0, v1;
-                if (one) v0 = row.load(s, lane);
-                if (two) v1 = row.load(s + UNW, lane);
-                if (one) walk(s, v0);
-                if (two) walk(s + UNW, v1);
-            }
-            __syncthreads();
-            const int ln = c->n;
-            for (int i = tid; i < min(ln, UCAP); i += UNT) lw[i] = wt.weight_of(from_logit_key(lkey[i]));
-            if (tid < C) peer(c->cn, tid)[rank] = ln;
-            sync(C);
-            int n = 0;
-            for (int q = 0; q < C; ++q) n += c->cn[q];
-            if (n <= UCAP) {
+                if (by_mass) above_t = above;
+                if (n > UCAP) break;
                 // every CTA gathers the whole list and decides
                 int at = 0;
                 for (int q = 0; q < C; ++q) {
@@ -1002,6 +1115,7 @@ __global__ void __launch_bounds__(UNT, 2) uniform_kernel(const UniformArgs a) {
                 sync(C);  // the lists have been read: they may be used again
                 return least;
             }
+            const float drop = wt.drop_of(qb);
             // Keys the bin can hold, with some slack for the rounding of its edges.
             const float lo = wt.m - drop, hi = qb > 0 ? wt.m - wt.drop_of(qb - 1) * (1.f - 1.f / 16.f / float(qb)) : wt.m;
             const float sl = 0x1p-18f * (fabsf(wt.m) + drop);
@@ -1052,9 +1166,7 @@ __global__ void __launch_bounds__(UNT, 2) uniform_kernel(const UniformArgs a) {
             }
             return kl;
         };
-        unsigned long long F = 0, none = 0;
-        for (int q = tid; q < UB; q += UNT) F += tmass[q];
-        F = block_sum(F, c);
+        unsigned long long none = 0;
         if (has_k) {
             unsigned long long fk = F;
             theta = max(theta, search(false, (unsigned long long)k, fk, !has_p, floor_key));

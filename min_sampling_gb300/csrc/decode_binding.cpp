@@ -3,9 +3,9 @@
 //
 // These calls run once or more per generated token, often on a few rows, where the host's
 // time decides: with the checks in Python a call took 21 to 31 us of the host for kernels of 3 to 13;
-// here it takes 4 to 10 (Grace).  Nothing is computed
-// and nothing kept from one call for the next.  Every function returns its result, or an
+// here it takes 4 to 10 (Grace).  Nothing is computed and nothing kept from one call for the next.  Every function returns its result, or an
 // fs_status other than FS_OK as an int, which the caller in __init__.py raises.
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <ATen/ops/empty.h>
@@ -131,16 +131,17 @@ PyObject* launch(const at::Tensor& on, F f, R ok) {
     return st == FS_OK ? ok() : PyLong_FromLong(st);
 }
 
+// A refusal becomes a ValueError; what torch throws (out of memory, say) its own Python error.
 template <typename F>
 PyObject* guarded(F f) {
+    HANDLE_TH_ERRORS
     try {
         return f();
     } catch (const Refused& r) {
         PyErr_SetString(PyExc_ValueError, r.what.c_str());
-    } catch (const std::exception& e) {  // an allocation, a conversion
-        if (!PyErr_Occurred()) PyErr_SetString(PyExc_RuntimeError, e.what());
+        return nullptr;
     }
-    return nullptr;
+    END_HANDLE_TH_ERRORS
 }
 
 struct py_owned {

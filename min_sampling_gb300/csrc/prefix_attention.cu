@@ -685,8 +685,8 @@ fs_status fs_shared_prefix_attention(const fs_paged_kv* cache, const void* query
     a.q = query;
     a.out = out;
     a.lse = out_lse;
-    a.k = cache->k;
-    a.v = cache->v;
+    a.k = cache->num_pages > 0 ? cache->k : query;   // (without pages an address that nothing is read from)
+    a.v = cache->num_pages > 0 ? cache->v : query;
     a.num_pages = cache->num_pages;
     a.page_size = cache->page_size;
     a.page_shift = -1;

@@ -27,7 +27,7 @@ namespace fsd {
 constexpr int TM = 128;          // queries per tile
 constexpr int TK = 64;           // keys per tile
 constexpr int TNT = 512;         // threads
-constexpr uint32_t SPIN = 1u << 22;
+constexpr uint32_t SPIN = 1u << 20;  // tries of at most about 2 us before a wait gives up
 
 template <int D, bool SPLIT>
 struct TensorSmem {
@@ -52,7 +52,7 @@ __device__ __forceinline__ void bar_arrive(uint32_t bar) {
 __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
     uint32_t ok;
     asm volatile(
-        "{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
+        "{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 2000; selp.u32 %0, 1, 0, p; }"
         : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
     return ok != 0;
 }

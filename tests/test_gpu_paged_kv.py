@@ -184,3 +184,24 @@ def test_captured_and_replayed(ms):
         g.replay()
         want = call(*ref)
         assert torch.equal(q, want) and torch.equal(c["k"], ref[0]) and torch.equal(c["v"], ref[1])
+
+
+def test_refusals(ms):
+    import torch
+    c = _case(12, "bf16", 4, 2, 4, 64, 16, 64, 8, 4)
+    cu = lambda x: torch.from_numpy(x).cuda()
+    good = dict(key=c["key"], value=c["value"], k_cache=c["k"], v_cache=c["v"], page_table=cu(c["table"]),
+                positions=cu(c["pos"]), rows=cu(c["rows"]), inv_freq=cu(_inv(32)), query=c["query"])
+    before = c["k"].clone(), c["v"].clone()
+    f = ms.append_paged_kv
+    for bad in (dict(key=c["key"].half()), dict(key=c["key"][:3]), dict(key=c["key"][..., ::2]), dict(value=c["value"][:, :1]),
+                dict(v_cache=c["v"][:5]), dict(k_cache=c["k"].cpu()), dict(k_cache=c["k"].double(), v_cache=c["v"].double()),
+                dict(k_cache=c["k"].transpose(2, 3), v_cache=c["v"].transpose(2, 3)), dict(page_table=cu(c["table"]).long()),
+                dict(page_table=cu(c["table"])[:, ::2]), dict(page_table=torch.from_numpy(c["table"])),
+                dict(positions=cu(c["pos"])[:2]), dict(positions=cu(c["pos"]).long()), dict(rows=cu(c["rows"]).cpu()),
+                dict(rows=None, page_table=cu(c["table"])[:3]), dict(inv_freq=cu(_inv(33))), dict(inv_freq=cu(_inv(32)).double()),
+                dict(inv_freq=cu(_inv(32))[None]), dict(rotary_positions=cu(c["pos"])[:1]), dict(query=c["query"][..., :32]),
+                dict(query=c["query"][:, :0]), dict(query_out=c["query"][:2]), dict(query=None, query_out=c["query"])):
+        with pytest.raises(ValueError):
+            f(**{**good, **bad})
+    assert torch.equal(c["k"], before[0]) and torch.equal(c["v"], before[1])

@@ -273,3 +273,37 @@ def test_the_same_bits_every_time_captured_and_on_two_streams(ms):
         torch.cuda.synchronize()
         for d, o in zip(dev, outs):
             assert torch.equal(o, call(d))
+
+
+def test_a_prefix_without_pages_shows_as_nan(ms):
+    import torch
+    k = torch.zeros(0, 16, 2, 64, dtype=torch.bfloat16, device="cuda")
+    z = lambda *s: torch.zeros(s, dtype=torch.int32, device="cuda")
+    for rows in (2, 40):
+        q = torch.randn(rows, 4, 64, device="cuda").bfloat16()
+        out = ms.shared_prefix_attention(q, k, k, z(1, 40), z(1) + 600, z(rows, 1), z(rows))
+        assert bool(torch.isnan(out).all())
+
+
+def test_refusals(ms):
+    import torch
+    c = _case(13, "bf16", [2, 2], 4, 1, 8, 2, 64, [100, 30], [5, 9, 70, 2], 16)
+    cu = lambda x: torch.from_numpy(x).cuda()
+    good = dict(query=c["q"], k_cache=c["k"], v_cache=c["v"], prefix_table=cu(c["ptab"]), prefix_lens=cu(c["plens"]),
+                suffix_table=cu(c["stab"]), suffix_lens=cu(c["slens"]), group_starts=cu(c["starts"]))
+    f = ms.shared_prefix_attention
+    for bad in (dict(query=c["q"].half()), dict(query=c["q"][..., :32]), dict(query=c["q"][:, :, :3]), dict(query=c["q"][:, :0]),
+                dict(query=c["q"][0, 0]), dict(query=c["q"].cpu()), dict(k_cache=c["k"][..., ::2], v_cache=c["v"][..., ::2]),
+                dict(v_cache=c["v"][:3]), dict(prefix_table=cu(c["ptab"]).long()), dict(prefix_table=None),
+                dict(prefix_lens=cu(c["plens"])[:1]), dict(prefix_lens=None), dict(suffix_table=cu(c["stab"])[:3]),
+                dict(suffix_lens=cu(c["slens"])[:3]), dict(suffix_lens=torch.from_numpy(c["slens"])), dict(suffix_table=None),
+                dict(group_starts=cu(c["starts"])[:2]), dict(group_starts=None), dict(out=c["q"][:2]), dict(out=c["q"].half())):
+        with pytest.raises(ValueError):
+            f(**{**good, **bad})
+    wide = torch.zeros(4, 1, 8, 68, dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(ms.FsError):      # a stride of 136 bytes
+        f(**{**good, "query": wide[..., :64]})
+    with pytest.raises(ms.FsError):      # float32, and heads of 32
+        f(**{**good, "query": c["q"].float(), "k_cache": c["k"].float(), "v_cache": c["v"].float()})
+    with pytest.raises(ms.FsError):
+        f(**{**good, **{n: good[n][..., :32].contiguous() for n in ("query", "k_cache", "v_cache")}})

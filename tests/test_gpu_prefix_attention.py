@@ -115,6 +115,30 @@ def test_several_tokens_a_row(ms, Q):
     _check(ms, _case(Q, "f16", [2], 2, Q, 4, 4, 128, [0], [Q, max(Q - 2, 0)], 5))
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("plen", [40, 2100, 9000])
+def test_wide_heads(ms, dtype, plen):
+    """Heads of 256: tiles of 16, 32 and 64 queries, few key ranges (tiles of 64 keys) and many (of 32)."""
+    rng = np.random.default_rng(plen)
+    for rows, Q in ((1, 1), (4, 1), (7, 1), (18, 1), (3, 5), (6, 5), (40, 2)):
+        _check(ms, _case(plen + rows, dtype, [rows], rows, Q, 16, 4, 256, [plen], rng.integers(0, 300, rows), 16))
+    _check(ms, _case(plen, dtype, [2, 5, 0, 30], 40, 1, 8, 2, 256, [plen, 31, 7, 65], rng.integers(0, 70, 40), 5))
+
+
+@pytest.mark.parametrize("rows", [1, 90])
+def test_wide_heads_unseen_values(ms, rows):
+    """NaN and infinite values in tokens behind a query's own, at the border of a tile of keys."""
+    import torch
+    Q = 5
+    for length in (32, 34, 64, 66, 97):
+        c = _case(length, "bf16", [rows], rows, Q, 8, 2, 256, [100], [length] * rows, 16)
+        want = _check(ms, c)[0][:, :Q - 2].clone()
+        for b in range(rows):
+            for t, x in ((length - 1, float("nan")), (length - 2, float("inf"))):
+                c["v"][int(c["stab"][b, t // 16]), t % 16] = x
+        assert torch.equal(_call(ms, c)[0][:, :Q - 2], want)
+
+
 def test_groups_of_every_size(ms):
     """Empty groups, empty prefixes, rows of no group, many groups."""
     _check(ms, _case(1, "bf16", [3, 0, 1, 4], 10, 1, 8, 2, 128, [500, 10, 0, 65], [1, 2, 3, 4, 5, 6, 7, 8, 0, 64], 16))

@@ -419,11 +419,13 @@ def append_paged_kv(key, value, k_cache, v_cache, page_table, positions, rows=No
     key, value: [N, heads, dim]; k_cache, v_cache: [pages, page_size, heads, dim], any
     strides with a contiguous last dimension (pass ``cache.transpose(1, 2)`` for pages laid
     out heads first).  page_table: [R, width] int32; positions: [N] int32, the token's place in its table
-    row (negative: padding, skipped); rows: [N] int32, the token's table row (default: row t).
+    row (negative: padding, skipped); rows: [N] int32, the token's table row (default: row t).  The places of one
+    call must differ: of two tokens at one place either's elements may stay.
     rotary_positions: [N] int32 (default: positions); inv_freq: [r / 2] float32 rotates the
     first r elements of each head, in halves or, with ``interleaved``, in neighbouring pairs (None: no
     rotation).  query: [N, q_heads, dim] is rotated into query_out (default: a new tensor; may be query itself),
-    which is returned (None without a query)."""
+    which is returned (None without a query).  No backward pass: tensors that require a gradient are refused
+    outside of torch.no_grad()."""
     r = _native().append(key, value, k_cache, v_cache, page_table, positions, rows, rotary_positions, inv_freq,
                          interleaved, query, query_out)
     return _check(r) if type(r) is int else r
@@ -438,9 +440,11 @@ def shared_prefix_attention(query, k_cache, v_cache, prefix_table, prefix_lens, 
     them); k_cache, v_cache: [pages, page_size, kv_heads, dim] bfloat16 or float16, dim 64, 128 or 256.  prefix_table [G, w]
     and prefix_lens [G] int32 name the prefixes (None: there are none), suffix_table [B, w] and suffix_lens [B]
     int32 the rows' own tokens; group_starts [G + 1] int32: rows group_starts[g] up to
-    group_starts[g + 1] share prefix g (default: one prefix for all).  scale defaults to dim ** -0.5.
+    group_starts[g + 1] share prefix g (default: one prefix for all); it ascends, and rows outside of it have no
+    prefix.  scale defaults to dim ** -0.5.
     Returns out (query's shape), and with return_lse the log of the sum of exponentials,
-    float32 [B, (Q,) heads]."""
+    float32 [B, (Q,) heads].  No backward pass: tensors that require a gradient are refused outside of
+    torch.no_grad()."""
     r = _native().attention(query, k_cache, v_cache, prefix_table, prefix_lens, suffix_table, suffix_lens, group_starts,
                             scale, out, return_lse)
     return _check(r) if type(r) is int else r

@@ -3,11 +3,13 @@
 //
 // These calls run once or more per generated token, often on a few rows, where the host's
 // time decides: with the checks in Python a call took 21 to 31 us of the host for kernels of 3 to 13;
-// here it takes 4 to 10 (Grace).  Nothing is computed and nothing kept from one call for the next.  Every function returns its result, or an
-// fs_status other than FS_OK as an int, which the caller in __init__.py raises.
+// here it takes 5 to 11 (Grace).  Nothing is computed and nothing kept from one call for the
+// next.  Every function returns its result, or an fs_status other than FS_OK as an int, which the caller in
+// __init__.py raises.
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <ATen/core/grad_mode.h>
 #include <ATen/ops/empty.h>
 #include <ATen/ops/full.h>
 #include <c10/core/DeviceGuard.h>
@@ -92,6 +94,19 @@ const X* flat_ptr(PyObject* o, const char* name, int64_t n, at::ScalarType type,
 // Strides of the first n dimensions, 0 for a dimension of one element (its stride addresses nothing).
 void strides(const at::Tensor& t, int n, int64_t* out) {
     for (int i = 0; i < n; ++i) out[i] = t.size(i) > 1 ? t.stride(i) : 0;
+}
+
+// A tensor that is written: no two elements at one address (an expanded dimension).
+void writable(const at::Tensor& t, const char* name) {
+    for (int64_t i = 0; i < t.dim(); ++i)
+        if (t.size(i) > 1 && t.stride(i) == 0) refuse(std::string(name) + " is written, but some of its elements share memory");
+}
+
+// There is no backward pass: a gradient would be lost without a word.
+void no_gradient(std::initializer_list<const at::Tensor*> ts) {
+    if (!at::GradMode::is_enabled()) return;
+    for (const at::Tensor* t : ts)
+        if (t && t->requires_grad()) refuse("there is no backward pass: detach tensors that require a gradient, or call under torch.no_grad()");
 }
 
 fs_paged_kv paged_kv(PyObject* k, PyObject* v) {
@@ -251,11 +266,15 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
             q_heads = size32(q->size(1), "the number of heads");
             if (q_heads < 1) refuse("query must have at least one head");
             qo = none(a[11]) ? at::empty(q->sizes(), q->options()) : vectors(a[11], "query_out", q->sizes(), type, dev);
+            writable(qo, "query_out");
             strides(*q, 2, qs);
             strides(qo, 2, qos);
         } else if (!none(a[11])) {
             refuse("query_out needs a query");
         }
+        writable(cache, "k_cache");
+        writable(*tensor(a[3]), "v_cache");
+        no_gradient({&key, &value, &cache, tensor(a[3]), q, tensor(a[11])});
         return launch(cache, [&](void* s) {
             return fs_append_paged_kv(&kv, key.data_ptr(), ks, value.data_ptr(), vs, tokens,
                                       static_cast<const int32_t*>(table.data_ptr()), size32(table.size(0), "the table"),
@@ -283,6 +302,8 @@ PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const at::Tensor& q = vectors(a[0], "query", given.sizes(), type, dev);
         const c10::DeviceGuard guard(cache.device());
         at::Tensor out = none(a[9]) ? at::empty(q.sizes(), q.options()) : vectors(a[9], "out", q.sizes(), type, dev);
+        writable(out, "out");
+        no_gradient({&q, &cache, tensor(a[2]), tensor(a[9])});
         const bool one = q.dim() == 3;
         const int32_t B = size32(q.size(0), "the batch"), Q = one ? 1 : size32(q.size(1), "the number of queries");
         const int32_t Hq = size32(q.size(-2), "the number of heads");

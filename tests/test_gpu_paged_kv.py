@@ -205,3 +205,28 @@ def test_refusals(ms):
         with pytest.raises(ValueError):
             f(**{**good, **bad})
     assert torch.equal(c["k"], before[0]) and torch.equal(c["v"], before[1])
+
+
+def test_gradients_and_shared_memory_are_refused(ms):
+    """No gradient is lost without a word, no cache or output whose elements share memory is written."""
+    import torch
+    mk = lambda *s: torch.randn(s, device="cuda")
+    t = dict(key=mk(3, 2, 64), value=mk(3, 2, 64), k_cache=mk(4, 8, 2, 64), v_cache=mk(4, 8, 2, 64),
+             page_table=torch.arange(3, dtype=torch.int32, device="cuda")[:, None].contiguous(),
+             positions=torch.tensor([0, 5, 7], dtype=torch.int32, device="cuda"), query=mk(3, 4, 64))
+    kept = t["k_cache"].clone(), t["v_cache"].clone()
+    for name in ("key", "value", "k_cache", "v_cache", "query"):
+        bad = dict(t, **{name: t[name].clone().requires_grad_()})
+        with pytest.raises(ValueError, match="no backward"):
+            ms.append_paged_kv(**bad)
+    for name in ("k_cache", "v_cache"):
+        with pytest.raises(ValueError, match="share memory"):
+            ms.append_paged_kv(**dict(t, **{name: t[name][:1].expand_as(t[name])}))
+    with pytest.raises(ValueError, match="share memory"):
+        ms.append_paged_kv(**t, query_out=t["query"][:, :1].expand_as(t["query"]))
+    assert torch.equal(t["k_cache"], kept[0]) and torch.equal(t["v_cache"], kept[1])
+    with torch.no_grad():
+        q = ms.append_paged_kv(**dict(t, key=t["key"].clone().requires_grad_()))
+    assert torch.equal(q, t["query"])
+    for i, p in enumerate((0, 5, 7)):
+        assert torch.equal(t["k_cache"][i, p], t["key"][i]) and torch.equal(t["v_cache"][i, p], t["value"][i])

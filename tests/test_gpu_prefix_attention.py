@@ -331,3 +331,22 @@ def test_refusals(ms):
         f(**{**good, "query": c["q"].float(), "k_cache": c["k"].float(), "v_cache": c["v"].float()})
     with pytest.raises(ms.FsError):
         f(**{**good, **{n: good[n][..., :32].contiguous() for n in ("query", "k_cache", "v_cache")}})
+
+
+def test_gradients_and_shared_memory_are_refused(ms):
+    """No gradient is lost without a word, no output whose elements share memory is written."""
+    import torch
+    c = _case(13, "bf16", [4], 4, 1, 8, 2, 64, [100], [5, 9, 70, 2], 16)
+    want, _ = _call(ms, c)
+    for name in ("q", "k", "v"):
+        bad = dict(c, **{name: c[name].clone().requires_grad_()})
+        with pytest.raises(ValueError, match="no backward"):
+            _call(ms, bad)
+        with torch.no_grad():
+            assert torch.equal(_call(ms, bad)[0], want)
+        assert torch.equal(_call(ms, dict(c, **{name: bad[name].detach()}))[0], want)
+    with pytest.raises(ValueError, match="share memory"):
+        _call(ms, c, out=c["q"][:1].clone().expand_as(c["q"]))
+    assert torch.equal(_call(ms, dict(c, q=c["q"].clone()), out=torch.empty_like(c["q"]))[0], want)
+    shared = dict(c, q=c["q"][:1].expand_as(c["q"]))     # reading a broadcast query is fine
+    assert torch.equal(_call(ms, shared)[0], _call(ms, dict(c, q=shared["q"].contiguous()))[0])

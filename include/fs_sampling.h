@@ -370,7 +370,7 @@ fs_status fs_top_k_top_p_sampling_noalloc(const float* probs, int32_t batch_in, 
  *    ..._workspace_bytes function gives for the same sizes.  Its contents need no
  *    initialisation and are undefined afterwards.  Two calls, or replays of captured
  *    graphs, that may run at the same time need workspaces of their own.
- *  - Strides are in elements and may be any, also negative or 0 for inputs; the last dimension is
+ *  - Strides are in elements and may be any, also negative, and 0 for inputs; the last dimension is
  *    contiguous.  Offsets are 64-bit.  Tensors that are written must not overlap others of the call
  *    unless stated.
  *  - The data of tables, lengths and positions is on the device and is not checked by the

@@ -3,6 +3,7 @@
 #pragma once
 
 #include <algorithm>
+#include <cstdint>
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -13,6 +14,7 @@
 namespace fsd {
 
 constexpr int RANGE = 64;     // unit of key ranges: whole tiles of every kernel
+constexpr int64_t NOWHERE = INT64_MIN;  // the offset of what is not there (strides, and so offsets, may be negative)
 
 struct AttnArgs {
     const void* q;

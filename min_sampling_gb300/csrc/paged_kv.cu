@@ -146,7 +146,7 @@ __device__ __forceinline__ Unit unit_of(const AppendArgs& a, int i) {
 // Any alignment: single elements (VW = 1).
 template <typename T, int VW>
 __global__ void __launch_bounds__(256, 4) append_kernel(const AppendArgs a) {
-    // per token: cache offsets of keys and values (-1: not written), whether it is padding, then the turns
+    // per token: cache offsets of keys and values, whether it is padding or not written, then the turns
     extern __shared__ __align__(16) unsigned char smem[];
     int64_t* slots = reinterpret_cast<int64_t*>(smem);            // [per_cta][2]
     int* pads = reinterpret_cast<int*>(slots + 2 * a.per_cta);    // [per_cta]
@@ -184,18 +184,20 @@ __global__ void __launch_bounds__(256, 4) append_kernel(const AppendArgs a) {
         const int row = a.rows ? a.rows[t] : t;
         const bool pad = pos < 0;
         const int pi = pad ? 0 : pos / a.page_size;
-        int64_t k_at = -1, v_at = -1;
+        int64_t k_at = 0, v_at = 0;
+        bool there = false;
         if (!pad && row >= 0 && row < a.table_rows && pi < a.table_width) {
             const int page = a.table[int64_t(row) * a.table_width + pi];
             if (page >= 0 && page < a.num_pages) {
                 const int slot = pos - pi * a.page_size;
                 k_at = page * a.kc[0] + slot * a.kc[1];
                 v_at = page * a.vc[0] + slot * a.vc[1];
+                there = true;
             }
         }
         slots[2 * threadIdx.x] = k_at;
         slots[2 * threadIdx.x + 1] = v_at;
-        pads[threadIdx.x] = pad ? 1 : (k_at < 0 ? 2 : 0);   // 1 padding, 2 not written
+        pads[threadIdx.x] = pad ? 1 : (there ? 0 : 2);   // 1 padding, 2 not written
     }
     for (int i = threadIdx.x; i < tokens * a.half; i += blockDim.x) {
         const int k = i / a.half, t = t0 + k;
@@ -326,18 +328,20 @@ __global__ void __launch_bounds__(256, 4) append_heads_kernel(const AppendArgs a
         const int row = a.rows ? a.rows[t] : t;
         const bool pad = pos < 0;
         const int pi = pad ? 0 : pos / a.page_size;
-        int64_t k_at = -1, v_at = -1;
+        int64_t k_at = 0, v_at = 0;
+        bool there = false;
         if (!pad && row >= 0 && row < a.table_rows && pi < a.table_width) {
             const int page = a.table[int64_t(row) * a.table_width + pi];
             if (page >= 0 && page < a.num_pages) {
                 const int slot = pos - pi * a.page_size;
                 k_at = page * a.kc[0] + slot * a.kc[1];
                 v_at = page * a.vc[0] + slot * a.vc[1];
+                there = true;
             }
         }
         slots[2 * threadIdx.x] = k_at;
         slots[2 * threadIdx.x + 1] = v_at;
-        pads[threadIdx.x] = pad ? 1 : (k_at < 0 ? 2 : 0);   // 1 padding, 2 not written
+        pads[threadIdx.x] = pad ? 1 : (there ? 0 : 2);   // 1 padding, 2 not written
     }
     for (int i = threadIdx.x; i < tokens * a.half; i += blockDim.x) {
         const int k = i / a.half, t = t0 + k;

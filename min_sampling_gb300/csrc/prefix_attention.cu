@@ -144,7 +144,7 @@ __global__ void __launch_bounds__(32 * WM * WN) attend_kernel(const AttnArgs a) 
     // ---- pipeline of key/value tiles.  A key's offsets are looked up one tile before its
     // loads are issued, by one thread per key.
     auto look_up = [&](int tile, int64_t& ko, int64_t& vo, bool& bad) {
-        ko = vo = -1;
+        ko = vo = NOWHERE;
         bad = false;
         const int key = begin + tile * KT + tid;
         if (tid < KT && key < end) {
@@ -173,8 +173,9 @@ __global__ void __launch_bounds__(32 * WM * WN) attend_kernel(const AttnArgs a) 
         for (int i = 0; i < KT * DC / ANT; ++i) {
             const int r = (tid + i * ANT) / DC, c = (tid + i * ANT) % DC;
             const int64_t ko = off[r], vo = off[KT + r];
-            cp16(kd + chunk_at<D>(r, c), static_cast<const T*>(a.k) + (ko < 0 ? 0 : ko + c * 8), ko >= 0);
-            cp16(kd + S::TILE + chunk_at<D>(r, c), static_cast<const T*>(a.v) + (vo < 0 ? 0 : vo + c * 8), vo >= 0);
+            const bool on = ko != NOWHERE;
+            cp16(kd + chunk_at<D>(r, c), static_cast<const T*>(a.k) + (on ? ko + c * 8 : 0), on);
+            cp16(kd + S::TILE + chunk_at<D>(r, c), static_cast<const T*>(a.v) + (on ? vo + c * 8 : 0), on);
         }
     };
     int64_t ko, vo;

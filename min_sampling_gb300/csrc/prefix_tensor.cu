@@ -224,7 +224,7 @@ __global__ void __launch_bounds__(TNT, 1) prefix_tensor_kernel(const AttnArgs a)
     int* o_row = reinterpret_cast<int*>(mem + S::OUTS);
     if (tid < ROWS) {
         const int g = row0 + tid;
-        int64_t off = -1;
+        int64_t off = NOWHERE;
         int row = -1;
         if (g < M) {
             const int b = gt.b0 + g / per, rem = g % per, qi = rem / a.gs, h = head * a.gs + rem % a.gs;
@@ -296,7 +296,7 @@ __global__ void __launch_bounds__(TNT, 1) prefix_tensor_kernel(const AttnArgs a)
             int64_t off[2];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                off[h] = -1;
+                off[h] = NOWHERE;
                 if (pg[h] >= 0) {
                     const int slot = a.page_shift >= 0 ? (key + 32 * h) & (a.page_size - 1) : (key + 32 * h) % a.page_size;
                     off[h] = pg[h] * str[0] + slot * str[1];
@@ -310,9 +310,10 @@ __global__ void __launch_bounds__(TNT, 1) prefix_tensor_kernel(const AttnArgs a)
             for (int i = 0; i < TK / 4; ++i) {
                 const int r = i * 4 + (lane >> 3), c8 = lane & 7;
                 const int64_t o = __shfl_sync(FULL, off[i >> 3], r & 31);
-                const T* from = src + (o < 0 ? 0 : o + c8 * 8);
+                const bool on = o != NOWHERE;
+                const T* from = src + (on ? o + c8 * 8 : 0);
 #pragma unroll
-                for (int h = 0; h < D / 64; ++h) cp16(dst + tile_at<TK>(r, c8 + 8 * h), from + (o < 0 ? 0 : 64 * h), o >= 0);
+                for (int h = 0; h < D / 64; ++h) cp16(dst + tile_at<TK>(r, c8 + 8 * h), from + (on ? 64 * h : 0), on);
             }
             cp_async_commit();
             if (c + 4 < 2 * tiles) pg[0] = page_of(keys_of(c + 4)), pg[1] = page_of(keys_of(c + 4) + 32);
@@ -405,8 +406,8 @@ __global__ void __launch_bounds__(TNT, 1) prefix_tensor_kernel(const AttnArgs a)
         for (int i = tid; i < ROWS * DC; i += 256) {
             const int r = i / DC, c = i % DC;
             const int64_t off = q_off[r];
-            cp16(base + (r >> 7) * S::QTILE + tile_at<TM>(r & 127, c), static_cast<const T*>(a.q) + (off < 0 ? 0 : off + c * 8),
-                 off >= 0);
+            const bool on = off != NOWHERE;
+            cp16(base + (r >> 7) * S::QTILE + tile_at<TM>(r & 127, c), static_cast<const T*>(a.q) + (on ? off + c * 8 : 0), on);
         }
         cp_async_commit();
         asm volatile("bar.sync 2, 384;" ::: "memory");   // the addresses have been read

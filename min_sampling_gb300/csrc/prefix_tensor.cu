@@ -419,7 +419,7 @@ __global__ void __launch_bounds__(TNT, 1) prefix_tensor_kernel(const AttnArgs a)
         const uint32_t lanes = uint32_t(warp & 3) << 21;   // the warp's 32 lanes of tensor memory
         const int n = SPLIT ? (tiles + 1 - t) / 2 : tiles;
         float m = -INFINITY, l = 0.f;
-        bool ok = true;
+        bool ok = true, huge = false;
 #pragma unroll 1
         for (int i = 0; i < n && ok; ++i) {
             const int valid = end - (begin + (SPLIT ? 2 * i + t : i) * TK);   // keys of this tile
@@ -451,11 +451,12 @@ __global__ void __launch_bounds__(TNT, 1) prefix_tensor_kernel(const AttnArgs a)
             }
             mx *= fabsf(mul);
             if (!(mx > -INFINITY)) mx = m;   // a scale of 0 times infinity, or nothing but NaN
-            if (__any_sync(FULL, mx > m + 8.f)) {
+            if (__any_sync(FULL, mx - m > 8.f)) {   // (the difference is exact where it decides; m + 8 may round to m)
                 const float mn = fmaxf(m, mx);
                 const float f = m == -INFINITY ? 0.f : exp2_fast(m - mn);
                 m = mn;
                 l *= f;
+                huge = __any_sync(FULL, fabsf(m) > 0x1p20f);
                 if (i > 0) {
                     // the last product of this tile (the one before was done before these scores were)
                     ok = __all_sync(FULL, bar_wait(vbar + 8 * (buf ^ 2), ((i - 1) >> 1) & 1, dead));
@@ -473,6 +474,13 @@ __global__ void __launch_bounds__(TNT, 1) prefix_tensor_kernel(const AttnArgs a)
                 }
             }
             const float ms = m == -INFINITY ? 0.f : m;
+            // A maximum is a rounded product and a weight's exponent below is not: beyond 2^20 their difference, up to
+            // 2^-25 of the maximum, would count in the exponent (at 2^31 it is 2^6 and more).
+            if (huge) {
+#pragma unroll
+                for (int e = 0; e < TK; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * mul);
+                mul = 1.f;
+            }
             float sum[2] = {0.f, 0.f};
 #pragma unroll
             for (int e = 0; e < TK; e += 2) {

@@ -472,7 +472,8 @@ fs_status fs_append_paged_kv(const fs_paged_kv* cache, const void* key, const in
  *   out_lse        [batch, queries, q_heads] float32, nullable: log of the sum of exp(scale * q k)
  * Types bf16 and f16, head_dim 64, 128 or 256 (else FS_ERR_UNSUPPORTED); every address, and
  * every stride in bytes, is a multiple of 16 (else FS_ERR_INVALID_ARG).  Scores, maxima and sums are float32; the weights
- * enter the product with the values in 16 bits.
+ * enter the product with the values rounded to the type, each by up to half a step (f16: down to 2^-25 of the row's largest
+ * weight; a smaller one by up to 2^-36 of that).
  * Lengths are clamped to what the tables can name (0 .. width * page_size).  A query that sees no
  * key gives zeros and lse = -inf.  A row that needs a page outside [0, num_pages) gives NaN, and so
  * does a NaN in a key it sees; keys and values that a query does not see do not reach it. */

@@ -15,6 +15,8 @@
 // atomics, the same result on every run).
 #include "attention.cuh"
 
+#include <type_traits>
+
 namespace fsd {
 
 constexpr int ASTAGES = 2;    // tiles of keys and values in flight
@@ -60,6 +62,7 @@ __global__ void __launch_bounds__(32 * WM * WN) attend_kernel(const AttnArgs a) 
     constexpr int KW = KT / WN;       // keys per warp and tile
     constexpr int NF = KW / 8;        // score fragments
     constexpr int DC = D / 8;         // 16-byte chunks per row
+    constexpr float UP = std::is_same<T, __half>::value ? 32768.f : 1.f;   // the weights' factor in the product
     static_assert(WN * MT * (D + 2) * 4 <= S::OFF, "the warps' parts fit where the tiles were");
     extern __shared__ __align__(128) unsigned char smem[];
     const uint32_t sbase = smem_u32(smem);
@@ -334,14 +337,18 @@ __global__ void __launch_bounds__(32 * WM * WN) attend_kernel(const AttnArgs a) 
                     }
                 }
             }
-            // The weights enter the product in 16 bits (each off by half a step of the type);
-            // their sum stays in 32.
+            // The weights enter the product in 16 bits, as the matrix instruction takes them, each off by half a
+            // step of the type; their sum stays in 32.  In f16 they are 2^15 larger: half a step down to 2^-29 of the
+            // maximum, 2^-40 of it below.
+            auto weights = [&](int f, int e) {
+                return Mma<T>::pack(s[i][f][e] * UP, s[i][f][e + 1] * UP);
+            };
 #pragma unroll
             for (int f = 0; f < NF / 2; ++f) {
-                pf[i][f][0] = Mma<T>::pack(s[i][2 * f][0], s[i][2 * f][1]);
-                pf[i][f][1] = Mma<T>::pack(s[i][2 * f][2], s[i][2 * f][3]);
-                pf[i][f][2] = Mma<T>::pack(s[i][2 * f + 1][0], s[i][2 * f + 1][1]);
-                pf[i][f][3] = Mma<T>::pack(s[i][2 * f + 1][2], s[i][2 * f + 1][3]);
+                pf[i][f][0] = weights(2 * f, 0);
+                pf[i][f][1] = weights(2 * f, 2);
+                pf[i][f][2] = weights(2 * f + 1, 0);
+                pf[i][f][3] = weights(2 * f + 1, 2);
             }
         }
         // ---- values
@@ -383,7 +390,7 @@ __global__ void __launch_bounds__(32 * WM * WN) attend_kernel(const AttnArgs a) 
 #pragma unroll
             for (int f = 0; f < D / 8; ++f)
                 *reinterpret_cast<float2*>(so + (wn * MT + r) * D + f * 8 + (lane & 3) * 2) =
-                    make_float2(o[i][f][j * 2], o[i][f][j * 2 + 1]);
+                    make_float2(o[i][f][j * 2] * (1.f / UP), o[i][f][j * 2 + 1] * (1.f / UP));
         }
     __syncthreads();
     const float nan = *poison ? __int_as_float(0x7fffffff) : 0.f;

@@ -6,8 +6,8 @@
 // memory: S (128 x 64 float32) is turned into P (16 bits) in place, and P feeds the second product from
 // there.  Roles of the 16 warps:
 //   warps 0-3, 4-7  softmax of tile 0 / tile 1, one thread per query: maximum, weights,
-//                   sum; O is rescaled only when a maximum grows by more than 2^8 (P and the
-//                   sum then stay within 2^8 of their range: exact in float32, no overflow in f16)
+//                   sum; O is rescaled only when a maximum grows by more than 2^GROWTH, which P and the
+//                   sum then exceed 1 by (exact in float32; for f16 see Weights)
 //   warps 8-11      keys and values: page look-ups and 16-byte asynchronous copies into
 //                   a ring of swizzled tiles (any page size and strides)
 //   warps 12, 13    issue the first and the second product
@@ -100,6 +100,14 @@ __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&x)[16]
 #undef R8
 #undef W8
 
+// The weights of the second product are 16 bits, as its matrix instruction takes them: each is off by half a step of the
+// type, and their sum is not.  bf16 has float32's exponents; f16 ends at 2^-14 (in steps of 2^-24) and 65504, so its weights
+// are 2^SHIFT larger: rounded by half a step down to 2^-(14 + SHIFT) of the maximum, by 2^-(25 + SHIFT) below.  (Unshifted,
+// 65536 keys 17 nats below one were off by 1.5 % together.)  With a maximum that may lag by GROWTH they stay
+// below 2^15.
+template <typename T> struct Weights { static constexpr float GROWTH = 8.f, SHIFT = 0.f; };
+template <> struct Weights<__half> { static constexpr float GROWTH = 4.f, SHIFT = 11.f; };
+
 // The i-th run of N registers of an array.
 template <int N, int K>
 __device__ __forceinline__ uint32_t (&part(uint32_t (&x)[K], int i))[N] { return reinterpret_cast<uint32_t (&)[N]>(x[i * N]); }
@@ -183,6 +191,7 @@ __device__ __forceinline__ int copy_of_values(int t, int tiles) {
 template <typename T, int D, bool SPLIT>
 __global__ void __launch_bounds__(TNT, 1) prefix_tensor_kernel(const AttnArgs a) {
     using S = TensorSmem<D, SPLIT>;
+    using W = Weights<T>;
     constexpr int ST = S::STAGES, DC = D / 8;
     constexpr int ROWS = SPLIT ? 128 : 256;
     extern __shared__ unsigned char raw[];
@@ -451,7 +460,7 @@ __global__ void __launch_bounds__(TNT, 1) prefix_tensor_kernel(const AttnArgs a)
             }
             mx *= fabsf(mul);
             if (!(mx > -INFINITY)) mx = m;   // a scale of 0 times infinity, or nothing but NaN
-            if (__any_sync(FULL, mx - m > 8.f)) {   // (the difference is exact where it decides; m + 8 may round to m)
+            if (__any_sync(FULL, mx - m > W::GROWTH)) {   // (the difference is exact where it decides; m + 8 may round to m)
                 const float mn = fmaxf(m, mx);
                 const float f = m == -INFINITY ? 0.f : exp2_fast(m - mn);
                 m = mn;
@@ -474,18 +483,20 @@ __global__ void __launch_bounds__(TNT, 1) prefix_tensor_kernel(const AttnArgs a)
                 }
             }
             const float ms = m == -INFINITY ? 0.f : m;
+            float off = W::SHIFT - ms;
             // A maximum is a rounded product and a weight's exponent below is not: beyond 2^20 their difference, up to
             // 2^-25 of the maximum, would count in the exponent (at 2^31 it is 2^6 and more).
             if (huge) {
 #pragma unroll
-                for (int e = 0; e < TK; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * mul);
+                for (int e = 0; e < TK; ++e) x[e] = __float_as_uint(__fmul_rn(__uint_as_float(x[e]), mul) - ms);
                 mul = 1.f;
+                off = W::SHIFT;
             }
             float sum[2] = {0.f, 0.f};
 #pragma unroll
             for (int e = 0; e < TK; e += 2) {
-                float p0 = exp2_fast(fmaf(__uint_as_float(x[e]), mul, -ms));
-                float p1 = exp2_fast(fmaf(__uint_as_float(x[e + 1]), mul, -ms));
+                float p0 = exp2_fast(fmaf(__uint_as_float(x[e]), mul, off));
+                float p1 = exp2_fast(fmaf(__uint_as_float(x[e + 1]), mul, off));
                 sum[0] += p0;
                 sum[1] += p1;
                 x[e / 2] = Mma<T>::pack(p0, p1);
@@ -554,7 +565,7 @@ __global__ void __launch_bounds__(TNT, 1) prefix_tensor_kernel(const AttnArgs a)
                 asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;"
                              ::"l"(a.part_o + (split * rows + own) * D), "r"(smem_u32(mine)), "r"(D * 4) : "memory");
                 asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-                a.part_l[split * rows + own] = (ls == 0.f ? -INFINITY : m + log2f(ls)) + bad;
+                a.part_l[split * rows + own] = (ls == 0.f ? -INFINITY : m + (log2f(ls) - W::SHIFT)) + bad;
                 asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
             }
         }

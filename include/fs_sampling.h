@@ -476,7 +476,8 @@ fs_status fs_append_paged_kv(const fs_paged_kv* cache, const void* key, const in
  * weight; a smaller one by up to 2^-36 of that).
  * Lengths are clamped to what the tables can name (0 .. width * page_size).  A query that sees no
  * key gives zeros and lse = -inf.  A row that needs a page outside [0, num_pages) gives NaN, and so
- * does a NaN in a key it sees; keys and values that a query does not see do not reach it. */
+ * does a NaN in a key it sees; keys and values that a query does not see do not reach it.  Infinite and NaN values
+ * that it sees reach its output as the sum has them (an infinite one whose weight rounds to 0 may show as NaN). */
 fs_status fs_shared_prefix_attention(const fs_paged_kv* cache, const void* query, const int64_t* query_strides,
                                      int32_t batch, int32_t queries, int32_t q_heads,
                                      const int32_t* group_starts, int32_t groups,

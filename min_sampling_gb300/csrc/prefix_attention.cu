@@ -67,7 +67,8 @@ __global__ void __launch_bounds__(32 * WM * WN) attend_kernel(const AttnArgs a) 
     extern __shared__ __align__(128) unsigned char smem[];
     const uint32_t sbase = smem_u32(smem);
     int64_t* soff = reinterpret_cast<int64_t*>(smem + S::OFF);  // [2][2][KT]
-    int* poison = reinterpret_cast<int*>(smem + S::OFF + 2 * 2 * KT * 8);
+    int* poison = reinterpret_cast<int*>(smem + S::OFF + 2 * 2 * KT * 8);  // a page that does not exist
+    int* odd_seen = poison + 1;                                            // infinite or NaN values taken out
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int wm = warp / WN, wn = warp % WN;
     // When finishing, the launch before is the prefix's own: what that one waited for is there, and its
@@ -134,7 +135,7 @@ __global__ void __launch_bounds__(32 * WM * WN) attend_kernel(const AttnArgs a) 
         qi = rem / a.gs;
         h = head * a.gs + rem % a.gs;
     };
-    if (tid == 0) *poison = 0;
+    if (tid == 0) *poison = 0, *odd_seen = 0;
     for (int i = tid; i < MT * DC; i += ANT) {
         const int r = i / DC, c = i % DC;
         int b = 0, qi = 0, h = 0;
@@ -234,8 +235,8 @@ __global__ void __launch_bounds__(32 * WM * WN) attend_kernel(const AttnArgs a) 
         look_up(t + ASTAGES, ko, vo, bad);
         const uint32_t ks = sbase + S::KV + (t % ASTAGES) * 2 * S::TILE, vs = ks + S::TILE;
         // A value that only some of the queries see may be infinite or NaN, which a weight of
-        // zero does not cancel: such values are taken out of the tile, and the queries that
-        // see them take them directly.
+        // zero does not cancel: such values are taken out of the tile, and added at the end to the
+        // outputs of the queries that see them.
         const int k0 = begin + t * KT;
         if (!pre && a.Q > 1 && k0 + KT > full - (a.Q - 1)) {
             const int lo = max(0, full - (a.Q - 1) - k0), hi = min(KT, end - k0);
@@ -247,21 +248,7 @@ __global__ void __launch_bounds__(32 * WM * WN) attend_kernel(const AttnArgs a) 
                 odd |= !(fabsf(x) <= 3.402823466e38f);
             }
             if (__syncthreads_or(odd)) {
-                if (wn == 0) {
-                    for (int r = lo; r < hi; ++r)
-#pragma unroll
-                        for (int i = 0; i < RM; ++i)
-#pragma unroll
-                            for (int f = 0; f < D / 8; ++f)
-#pragma unroll
-                                for (int e = 0; e < 4; ++e) {
-                                    const int c = f * 8 + (lane & 3) * 2 + (e & 1);
-                                    const float x = Mma<T>::get(
-                                        *reinterpret_cast<const T*>(vb + chunk_at<D>(r, c >> 3) + (c & 7) * 2));
-                                    if (!(fabsf(x) <= 3.402823466e38f) && k0 + r < limit[i][e >> 1]) o[i][f][e] += x;
-                                }
-                }
-                __syncthreads();
+                if (tid == 0) *odd_seen = 1;
                 for (int i = tid; i < (hi - lo) * D; i += ANT) {
                     const int r = lo + i / D, d = i % D;
                     T* p = reinterpret_cast<T*>(vb + chunk_at<D>(r, d >> 3) + (d & 7) * 2);
@@ -394,6 +381,7 @@ __global__ void __launch_bounds__(32 * WM * WN) attend_kernel(const AttnArgs a) 
         }
     __syncthreads();
     const float nan = *poison ? __int_as_float(0x7fffffff) : 0.f;
+    const bool add_odd = a.Q > 1 && *odd_seen;
     const int64_t rows = int64_t(a.B) * a.Q * a.Hq;
     if (a.finish) grid_dependency_wait();
     for (int i = tid; i < MT * (D / 4); i += ANT) {
@@ -426,13 +414,27 @@ __global__ void __launch_bounds__(32 * WM * WN) attend_kernel(const AttnArgs a) 
         }
         const float inv = (l == 0.f ? 0.f : 1.f / l) + nan;
         const float lse = (l == 0.f ? -INFINITY : m + log2f(l)) + nan;
+        x = make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv);
+        if (add_odd) {   // (their weights are positive: exp(s - m) > 0)
+            const int last = min(end, full - (a.Q - 1 - qi));
+            for (int key = max(begin, full - (a.Q - 1)); key < last; ++key) {
+                const int pi = key / a.page_size, page = table[pi];
+                if (page < 0 || page >= a.num_pages) continue;
+                const T* v = static_cast<const T*>(a.v) + page * a.vc[0] + (key - pi * a.page_size) * a.vc[1] + head * a.vc[2] + c * 4;
+                auto odd = [&](int e) {
+                    const float y = Mma<T>::get(v[e]);
+                    return fabsf(y) <= 3.402823466e38f ? 0.f : y;
+                };
+                x = make_float4(x.x + odd(0), x.y + odd(1), x.z + odd(2), x.w + odd(3));
+            }
+        }
         if (a.finish) {
             T* out = static_cast<T*>(a.out) + b * a.os[0] + qi * a.os[1] + h * a.os[2] + c * 4;
-            *reinterpret_cast<uint2*>(out) = make_uint2(Mma<T>::pack(x.x * inv, x.y * inv), Mma<T>::pack(x.z * inv, x.w * inv));
+            *reinterpret_cast<uint2*>(out) = make_uint2(Mma<T>::pack(x.x, x.y), Mma<T>::pack(x.z, x.w));
             if (c == 0 && a.lse) a.lse[row] = lse * 0.693147180559945309f;
         } else {
             const int64_t at = slot * rows + row;
-            *reinterpret_cast<float4*>(a.part_o + at * D + c * 4) = make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv);
+            *reinterpret_cast<float4*>(a.part_o + at * D + c * 4) = x;
             if (c == 0) a.part_l[at] = lse;
         }
     }

@@ -458,7 +458,7 @@ fs_status fs_append_paged_kv(const fs_paged_kv* cache, const void* key, const in
  *   out = softmax(scale * q [Kp; Ks]^T) [Vp; Vs],
  * Kp, Vp the keys and values of the prefix of the row's group, Ks, Vs those of the row's own
  * suffix.  A prefix is read once for all the queries of its group.
- *   query, out     [batch, queries, q_heads, head_dim]; strides {row, query, head}.  The
+ *   query, out     [batch, queries, q_heads, head_dim]; strides {row, query, head}; out may be query itself.  The
  *                  `queries` tokens of a row are the last ones of its suffix, in order: token j
  *                  sees the whole prefix and the first suffix_len - (queries - 1 - j)
  *                  tokens of the suffix.  Query head h reads key/value head

@@ -424,7 +424,8 @@ def append_paged_kv(key, value, k_cache, v_cache, page_table, positions, rows=No
     rotary_positions: [N] int32 (default: positions); inv_freq: [r / 2] float32 rotates the
     first r elements of each head, in halves or, with ``interleaved``, in neighbouring pairs (None: no
     rotation).  query: [N, q_heads, dim] is rotated into query_out (default: a new tensor; may be query itself),
-    which is returned (None without a query).  No backward pass: tensors that require a gradient are refused
+    which is returned (None without a query).  The caches and query_out share no memory with one another or with key,
+    value and query otherwise: such calls are refused.  No backward pass: tensors that require a gradient are refused
     outside of torch.no_grad()."""
     r = _native().append(key, value, k_cache, v_cache, page_table, positions, rows, rotary_positions, inv_freq,
                          interleaved, query, query_out)
@@ -442,6 +443,7 @@ def shared_prefix_attention(query, k_cache, v_cache, prefix_table, prefix_lens, 
     int32 the rows' own tokens; group_starts [G + 1] int32: rows group_starts[g] up to
     group_starts[g + 1] share prefix g (default: one prefix for all); it ascends, and rows outside of it have no
     prefix.  scale defaults to dim ** -0.5.
+    out may be query itself; it shares no memory with it or the caches otherwise.
     Returns out (query's shape), and with return_lse the log of the sum of exponentials,
     float32 [B, (Q,) heads].  No backward pass: tensors that require a gradient are refused outside of
     torch.no_grad()."""

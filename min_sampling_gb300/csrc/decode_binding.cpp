@@ -15,7 +15,9 @@
 #include <c10/core/DeviceGuard.h>
 #include <c10/cuda/CUDAStream.h>
 
+#include <algorithm>
 #include <cmath>
+#include <cstdint>
 #include <initializer_list>
 #include <string>
 #include <utility>
@@ -96,10 +98,115 @@ void strides(const at::Tensor& t, int n, int64_t* out) {
     for (int i = 0; i < n; ++i) out[i] = t.size(i) > 1 ? t.stride(i) : 0;
 }
 
-// A tensor that is written: no two elements at one address (an expanded dimension).
-void writable(const at::Tensor& t, const char* name) {
-    for (int64_t i = 0; i < t.dim(); ++i)
-        if (t.size(i) > 1 && t.stride(i) == 0) refuse(std::string(name) + " is written, but some of its elements share memory");
+// ------------------------------------------------------------------ shared memory
+//
+// Two elements at index i of one tensor and j of another (or of the same) lie at one address where
+//   sum_d i_d s_d - sum_d j_d t_d = the distance of their first elements,
+// an equation in bounded integers.  Its terms are searched from the largest stride down: each coefficient has to leave a rest
+// that the smaller terms can reach, which leaves one or two values for strides that nest (a
+// dimension's stride is at least the extent of the smaller ones), as those of nearly all views do.
+
+struct Term {
+    int64_t stride, lo, hi;   // coefficients lo .. hi, lo <= 0 <= hi
+};
+
+struct Terms {
+    Term t[16];
+    int n = 0;
+    void add(int64_t stride, int64_t lo, int64_t hi) {
+        if (stride == 0 || lo == hi) return;
+        int i = n;
+        for (int j = 0; j < n; ++j)
+            if (t[j].stride == stride) {
+                t[j].lo += lo, t[j].hi += hi;
+                return;
+            }
+        for (; i > 0 && t[i - 1].stride < stride; --i) t[i] = t[i - 1];
+        t[i] = Term{stride, lo, hi};
+        ++n;
+    }
+};
+
+int64_t floor_div(int64_t a, int64_t b) { return a / b - (a % b != 0 && (a < 0) != (b < 0)); }
+
+// Whether the terms from i on can sum to `rest`, with a coefficient other than 0 if `other` asks for one.  `tries` bounds the
+// search; when it runs out the answer is yes.
+bool reaches(const Terms& e, int i, int64_t rest, bool other, int& tries) {
+    if (--tries < 0) return true;
+    if (i == e.n) return rest == 0 && !other;
+    int64_t least = 0, most = 0;   // of the smaller terms
+    for (int j = i + 1; j < e.n; ++j) least += e.t[j].lo * e.t[j].stride, most += e.t[j].hi * e.t[j].stride;
+    const Term& x = e.t[i];
+    const int64_t from = std::max(x.lo, -floor_div(most - rest, x.stride)), to = std::min(x.hi, floor_div(rest - least, x.stride));
+    for (int64_t c = from; c <= to; ++c)
+        if (reaches(e, i + 1, rest - c * x.stride, other && c == 0, tries)) return true;
+    return false;
+}
+
+constexpr int TRIES = 4096;
+
+// A tensor's sizes, strides and the bytes from its first element to its last.
+struct Span {
+    const int64_t *sizes, *strides;
+    int dims;
+    intptr_t first, end;   // equal: no elements
+    int64_t element;
+    explicit Span(const at::Tensor& t) : sizes(t.sizes().data()), strides(t.strides().data()), dims(int(t.dim())), element(t.element_size()) {
+        first = end = reinterpret_cast<intptr_t>(t.const_data_ptr());
+        int64_t last = 0;
+        for (int i = 0; i < dims; ++i) {
+            if (sizes[i] == 0) return;
+            last += (sizes[i] - 1) * strides[i];
+        }
+        end += (last + 1) * element;
+    }
+};
+
+bool overlaps_itself(const Span& t) {
+    if (t.first == t.end) return false;
+    if (t.dims > 16) return true;
+    Terms e;
+    int dims = 0;
+    for (int i = 0; i < t.dims; ++i) {
+        if (t.sizes[i] < 2) continue;
+        if (t.strides[i] == 0) return true;
+        e.add(t.strides[i], 1 - t.sizes[i], t.sizes[i] - 1);
+        ++dims;
+    }
+    if (dims != e.n) return true;   // two dimensions of one stride
+    int64_t reach = 0;
+    int i = e.n;
+    for (; i > 0 && e.t[i - 1].stride > reach; --i) reach += e.t[i - 1].hi * e.t[i - 1].stride;
+    if (i == 0) return false;       // the strides nest
+    int tries = TRIES;
+    return reaches(e, 0, 0, true, tries);
+}
+
+// (tensors of one element size)
+bool shares_memory(const Span& a, const Span& b) {
+    if (a.first == a.end || b.first == b.end || a.first >= b.end || b.first >= a.end) return false;
+    if ((b.first - a.first) % a.element != 0 || a.dims + b.dims > 16) return true;
+    Terms e;
+    for (int i = 0; i < a.dims; ++i) e.add(a.strides[i], 0, a.sizes[i] - 1);
+    for (int i = 0; i < b.dims; ++i) e.add(b.strides[i], 1 - b.sizes[i], 0);
+    int tries = TRIES;
+    return reaches(e, 0, (b.first - a.first) / a.element, false, tries);
+}
+
+bool same_view(const Span& a, const Span& b) {
+    if (a.first != b.first || a.dims != b.dims) return false;
+    for (int i = 0; i < a.dims; ++i)
+        if (a.sizes[i] != b.sizes[i] || (a.sizes[i] > 1 && a.strides[i] != b.strides[i])) return false;
+    return true;
+}
+
+// A tensor that is written: no two of its elements at one address, ...
+void writable(const Span& t, const char* name) {
+    if (overlaps_itself(t)) refuse(std::string(name) + " is written, but some of its elements share memory");
+}
+// ... and none where another tensor of the call has one.
+void apart(const Span& written, const char* name, const Span& other, const char* other_name) {
+    if (shares_memory(written, other)) refuse(std::string(name) + " is written, but shares memory with " + other_name);
 }
 
 // There is no backward pass: a gradient would be lost without a word.
@@ -266,14 +373,34 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
             q_heads = size32(q->size(1), "the number of heads");
             if (q_heads < 1) refuse("query must have at least one head");
             qo = none(a[11]) ? at::empty(q->sizes(), q->options()) : vectors(a[11], "query_out", q->sizes(), type, dev);
-            writable(qo, "query_out");
             strides(*q, 2, qs);
             strides(qo, 2, qos);
         } else if (!none(a[11])) {
             refuse("query_out needs a query");
         }
-        writable(cache, "k_cache");
-        writable(*tensor(a[3]), "v_cache");
+        const at::Tensor& v_cache = *tensor(a[3]);
+        const Span k_span(cache), v_span(v_cache), in_key(key), in_value(value);
+        writable(k_span, "k_cache");
+        writable(v_span, "v_cache");
+        apart(k_span, "k_cache", v_span, "v_cache");
+        auto off_caches = [&](const Span& t, const char* name) {
+            apart(k_span, "k_cache", t, name);
+            apart(v_span, "v_cache", t, name);
+        };
+        off_caches(in_key, "key");
+        off_caches(in_value, "value");
+        if (q) {
+            const Span in_query(*q);
+            off_caches(in_query, "query");
+            if (!none(a[11])) {
+                const Span to(qo);
+                writable(to, "query_out");
+                off_caches(to, "query_out");
+                apart(to, "query_out", in_key, "key");
+                apart(to, "query_out", in_value, "value");
+                if (!same_view(in_query, to)) apart(to, "query_out", in_query, "query");
+            }
+        }
         no_gradient({&key, &value, &cache, tensor(a[3]), q, tensor(a[11])});
         return launch(cache, [&](void* s) {
             return fs_append_paged_kv(&kv, key.data_ptr(), ks, value.data_ptr(), vs, tokens,
@@ -302,7 +429,13 @@ PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const at::Tensor& q = vectors(a[0], "query", given.sizes(), type, dev);
         const c10::DeviceGuard guard(cache.device());
         at::Tensor out = none(a[9]) ? at::empty(q.sizes(), q.options()) : vectors(a[9], "out", q.sizes(), type, dev);
-        writable(out, "out");
+        if (!none(a[9])) {
+            const Span to(out), in_query(q);
+            writable(to, "out");
+            apart(to, "out", Span(cache), "k_cache");
+            apart(to, "out", Span(*tensor(a[2])), "v_cache");
+            if (!same_view(in_query, to)) apart(to, "out", in_query, "query");
+        }
         no_gradient({&q, &cache, tensor(a[2]), tensor(a[9])});
         const bool one = q.dim() == 3;
         const int32_t B = size32(q.size(0), "the batch"), Q = one ? 1 : size32(q.size(1), "the number of queries");
@@ -358,10 +491,21 @@ PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
     });
 }
 
+// (a, b) -> whether two elements of tensors of one type share memory; of one tensor, with itself.
+PyObject* shares(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    if (!arity(n, 2)) return nullptr;
+    return guarded([&]() -> PyObject* {
+        const at::Tensor *x = tensor(a[0]), *y = tensor(a[1]);
+        if (!x || !y || x->scalar_type() != y->scalar_type()) refuse("two tensors of one type are needed");
+        return PyBool_FromLong(a[0] == a[1] ? overlaps_itself(Span(*x)) : shares_memory(Span(*x), Span(*y)));
+    });
+}
+
 PyMethodDef METHODS[] = {
     {"from_uniforms", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(from_uniforms)), METH_FASTCALL, nullptr},
     {"append", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(append)), METH_FASTCALL, nullptr},
     {"attention", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(attention)), METH_FASTCALL, nullptr},
+    {"shares_memory", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(shares)), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef MODULE = {PyModuleDef_HEAD_INIT, "_decode", "The decode step's entries of libfs_sampling.so for torch tensors.",

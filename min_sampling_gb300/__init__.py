@@ -426,7 +426,7 @@ def append_paged_kv(key, value, k_cache, v_cache, page_table, positions, rows=No
     rotation).  query: [N, q_heads, dim] is rotated into query_out (default: a new tensor; may be query itself),
     which is returned (None without a query).  The caches and query_out share no memory with one another or with key,
     value and query otherwise: such calls are refused.  No backward pass: tensors that require a gradient are refused
-    outside of torch.no_grad()."""
+    outside of torch.no_grad(), tensors with a forward-mode tangent always."""
     r = _native().append(key, value, k_cache, v_cache, page_table, positions, rows, rotary_positions, inv_freq,
                          interleaved, query, query_out)
     return _check(r) if type(r) is int else r
@@ -446,7 +446,7 @@ def shared_prefix_attention(query, k_cache, v_cache, prefix_table, prefix_lens, 
     out may be query itself; it shares no memory with it or the caches otherwise.
     Returns out (query's shape), and with return_lse the log of the sum of exponentials,
     float32 [B, (Q,) heads].  No backward pass: tensors that require a gradient are refused outside of
-    torch.no_grad()."""
+    torch.no_grad(), tensors with a forward-mode tangent always."""
     r = _native().attention(query, k_cache, v_cache, prefix_table, prefix_lens, suffix_table, suffix_lens, group_starts,
                             scale, out, return_lse)
     return _check(r) if type(r) is int else r

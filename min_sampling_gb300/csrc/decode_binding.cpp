@@ -209,8 +209,11 @@ void apart(const Span& written, const char* name, const Span& other, const char*
     if (shares_memory(written, other)) refuse(std::string(name) + " is written, but shares memory with " + other_name);
 }
 
-// There is no backward pass: a gradient would be lost without a word.
+// There is no backward pass and no forward-mode derivative: either would be lost without a word.
 void no_gradient(std::initializer_list<const at::Tensor*> ts) {
+    for (const at::Tensor* t : ts)
+        if (t && t->_fw_grad(0).defined())
+            refuse("there is no forward-mode derivative: take the primal of tensors with a tangent (torch.autograd.forward_ad.unpack_dual)");
     if (!at::GradMode::is_enabled()) return;
     for (const at::Tensor* t : ts)
         if (t && t->requires_grad()) refuse("there is no backward pass: detach tensors that require a gradient, or call under torch.no_grad()");

@@ -32,6 +32,24 @@ def _attend_args():
                 suffix_table=i([2], [3], [4]), suffix_lens=i(3, 16, 1))
 
 
+# ------------------------------------------------------------------ forward-mode tangents
+
+def test_tangents_are_refused(ms):
+    """No forward-mode derivative is lost without a word, whether gradients are recorded or not."""
+    import torch
+    import torch.autograd.forward_ad as fw
+    for f, args, names in ((ms.append_paged_kv, _append_args(torch.float32), ("key", "value", "k_cache", "v_cache", "query")),
+                           (ms.shared_prefix_attention, _attend_args(), ("query", "k_cache", "v_cache"))):
+        for name in names:
+            with fw.dual_level():
+                dual = fw.make_dual(args[name], torch.ones_like(args[name]))
+                with pytest.raises(ValueError, match="tangent"):
+                    f(**dict(args, **{name: dual}))
+                with torch.no_grad(), pytest.raises(ValueError, match="tangent"):
+                    f(**dict(args, **{name: dual}))
+                f(**dict(args, **{name: fw.unpack_dual(dual).primal}))
+
+
 # ------------------------------------------------------------------ shared memory
 
 def test_appending_refuses_tensors_that_share_memory(ms):

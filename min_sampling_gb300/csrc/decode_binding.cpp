@@ -219,6 +219,12 @@ void no_gradient(std::initializer_list<const at::Tensor*> ts) {
         if (t && t->requires_grad()) refuse("there is no backward pass: detach tensors that require a gradient, or call under torch.no_grad()");
 }
 
+// The caller's tensors that a launch has written: autograd learns that what it saved of them has changed.
+void written(std::initializer_list<const at::Tensor*> ts) {
+    for (const at::Tensor* t : ts)
+        if (t && !t->is_inference()) t->unsafeGetTensorImpl()->bump_version();
+}
+
 fs_paged_kv paged_kv(PyObject* k, PyObject* v) {
     const at::Tensor& kt = float_cuda(k, "k_cache", 4, 4);
     vectors(k, "k_cache", kt.sizes(), kt.scalar_type(), kt.get_device());
@@ -411,6 +417,7 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
                                       size32(table.size(1), "the table"), rows, pos, rpos, freq, int32_t(rotary), interleaved,
                                       q ? q->data_ptr() : nullptr, qs, q_heads, q ? qo.data_ptr() : nullptr, qos, s);
         }, [&]() -> PyObject* {
+            written({&cache, &v_cache, tensor(a[11])});
             if (!q) Py_RETURN_NONE;
             if (none(a[11])) return wrap(qo);
             Py_INCREF(a[11]);
@@ -483,6 +490,7 @@ PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
                                               static_cast<const int32_t*>(stab.data_ptr()), sw, slens, float(scale), out.data_ptr(), os,
                                               want_lse ? static_cast<float*>(lse.data_ptr()) : nullptr, ws.data_ptr(), need, s);
         }, [&]() -> PyObject* {
+            written({tensor(a[9])});
             if (none(a[9])) return want_lse ? pair(out, lse) : wrap(out);
             PyObject* o = a[9];
             if (!want_lse) {

@@ -50,6 +50,53 @@ def test_tangents_are_refused(ms):
                 f(**dict(args, **{name: fw.unpack_dual(dual).primal}))
 
 
+# ------------------------------------------------------------------ versions
+
+def test_written_tensors_get_a_new_version(ms):
+    import torch
+    t = _append_args()
+    before = t["k_cache"]._version, t["v_cache"]._version, t["key"]._version, t["query"]._version
+    q = ms.append_paged_kv(**t)
+    assert t["k_cache"]._version > before[0] and t["v_cache"]._version > before[1]
+    assert t["key"]._version == before[2] and t["query"]._version == before[3]
+    res = torch.empty_like(t["query"])
+    v = res._version
+    assert ms.append_paged_kv(**t, query_out=res) is res and res._version > v and torch.equal(res, q)
+    t = _attend_args()
+    res = torch.empty_like(t["query"])
+    v, kv = res._version, t["k_cache"]._version
+    ms.shared_prefix_attention(**t, out=res)
+    assert res._version > v and t["k_cache"]._version == kv
+
+
+def test_a_saved_cache_that_changed_fails_the_backward_pass(ms):
+    import torch
+    t = _append_args(torch.float32)
+    w = torch.ones(64, device="cuda", requires_grad=True)
+    y = (t["k_cache"] * w).sum()          # saves the cache for w's gradient
+    ms.append_paged_kv(**t)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        y.backward()
+
+
+def test_inference_tensors_work(ms):
+    import torch
+    with torch.inference_mode():
+        t, u = _append_args(), _attend_args()
+        ms.append_paged_kv(**t, query_out=torch.empty_like(t["query"]))
+        ms.shared_prefix_attention(**u, out=torch.empty_like(u["query"]))
+    q = ms.append_paged_kv(**t)           # and outside of it
+    assert torch.equal(q, t["query"])
+
+
+def test_a_refused_call_changes_no_version(ms):
+    t = _append_args()
+    before = t["k_cache"]._version
+    with pytest.raises(ValueError):
+        ms.append_paged_kv(**dict(t, positions=t["positions"][:2]))
+    assert t["k_cache"]._version == before
+
+
 # ------------------------------------------------------------------ shared memory
 
 def test_appending_refuses_tensors_that_share_memory(ms):

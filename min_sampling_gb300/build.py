@@ -3,8 +3,9 @@
 Each CUDA source is compiled to an object in parallel with nvcc
 (-gencode arch=compute_103a,code=sm_103a), then linked into a shared library with
 the CUDA runtime linked statically, so the library loads on a machine without a
-GPU and without a CUDA runtime on the loader path.  _decode.so, the argument checks
-and marshalling of torch tensors for the decode step, is host C++ against torch's headers.
+GPU and without a CUDA runtime on the loader path.  It needs nothing but nvcc.  _decode.so, the
+argument checks and marshalling of torch tensors for the decode step, is host C++ against torch's
+headers; it is left out where torch is not installed.
 
     python -m min_sampling_gb300.build [--debug]
 """
@@ -51,11 +52,14 @@ def run(cmd: list[str], what: str) -> None:
         raise RuntimeError(f"{what} failed:\n{r.stdout}\n{r.stderr}")
 
 
-def torch_dir() -> str:
-    return os.path.dirname(importlib.util.find_spec("torch").origin)
+def torch_dir() -> str | None:
+    spec = importlib.util.find_spec("torch")
+    return None if spec is None else os.path.dirname(spec.origin)
 
 
-def compile_binding() -> str:
+def compile_binding() -> str | None:
+    if torch_dir() is None:
+        return None
     obj = os.path.join(BUILD, "decode_binding.o")
     include = [INCLUDE, os.path.join(torch_dir(), "include"), os.path.join(torch_dir(), "include/torch/csrc/api/include"),
                sysconfig.get_paths()["include"], os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")]
@@ -92,14 +96,17 @@ def build(debug: bool = False, verbose: bool = False, ptxas_info: bool = False) 
     with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
         binding = ex.submit(compile_binding)
         objs = list(ex.map(compile_one, SOURCES))
-        binding = binding.result()
     tmp = LIB + ".tmp"
     cmd = [cc, "-shared", "-o", tmp] + objs + ARCH + ["-cudart", "static", "-Xcompiler", "-fPIC"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
-    link_binding(binding)
+    obj = binding.result()   # the library is there whatever becomes of the binding
+    if obj is None:
+        sys.stderr.write("torch is not installed: _decode.so is left out\n")
+    else:
+        link_binding(obj)
     return LIB
 
 

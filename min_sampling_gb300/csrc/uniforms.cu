@@ -27,7 +27,7 @@
 //               logits tie by thousands) are narrowed by histograms over the order keys.
 //               The token is found from the segments' masses and one read of its segment.
 // Back to back on a GB300: 64 rows of 151936 float32, top-k 50 and top-p 0.9, 15.6 us (a copy of
-// the input at the memory's rate: 5.7); 64 of 151665 bf16, top-p 0.95, 61; 512 of 128256 f16 (128 rows),
+// the input at the memory's rate: 5.7); 64 of 151665 bf16, top-p 0.95, 61 to 72 (by the lists that the slowest row takes); 512 of 128256 f16 (128 rows),
 // min-p about 0.05, 41; 256 of 256000 bf16, all filters in the joint order, 72.  Small sets are bound
 // by the chain of barriers behind the scan, other sets by instructions (120 a logit).
 #include <algorithm>
@@ -368,7 +368,7 @@ struct Weigher {
         return whole ? x : x >> 32;
     }
     // Bin of z, 0 the largest: 8 of those steps (0.022 T).  Each operation is monotone in z, so a lower
-    // bin means larger z; the last bin's weights all round to 0.
+    // bin means larger z; the last bin's weights round to 0, or to one unit (2^-42) just above its edge.
     static constexpr int STEPS = 8, LAST = 43 * 256;
     __device__ __forceinline__ int bin_of(float z) const {
         const float yh = __fmul_rn(__fsub_rn(0.5f * z, hm), ch);
@@ -758,7 +758,7 @@ __global__ void __launch_bounds__(UNT, 2) uniform_kernel(const UniformArgs a) {
             for (int s = tid; s < row.nseg; s += UNT) atomicAdd(&hcnt[wt.bin_of(from_logit_key(segs[s]))], 1u);
             __syncthreads();
             find_count(hcnt, uint32_t(k), c);
-            const int kb = c->bin;  // the last bin has no weight, and UB means fewer segments than k
+            const int kb = c->bin;  // the last bin has next to no weight, and UB means fewer segments than k
             const float drop = wt.drop_of(kb);
             if (kb < LASTB) zt = wt.m - drop - 0x1p-18f * (fabsf(wt.m) + drop);
             small = kb < LASTB;
@@ -1060,7 +1060,7 @@ __global__ void __launch_bounds__(UNT, 2) uniform_kernel(const UniformArgs a) {
             bool lost = by_mass && qb > LASTB - 1;
             for (int turn = 0; turn < 5; ++turn) {
                 if (lost) qb = exact_bin<T>(row, wt, hist, hcnt, segs, s0, s1, target, c), lost = false;
-                if (qb >= LASTB) return 0;  // reached only among elements without weight
+                if (qb >= LASTB) return 0;  // reached only among elements of no weight or one unit
                 __syncthreads();
                 if (tid == 0) c->n = 0;
                 if (last)
@@ -1326,13 +1326,9 @@ __global__ void __launch_bounds__(UNT, 2) uniform_kernel(const UniformArgs a) {
 static int row_segments(int vocab, int es) { return int((int64_t(vocab) + 16 / es - 1 + 512 / es - 1) / (512 / es)); }
 
 template <typename T>
-static fs_status run_uniform(UniformArgs& a, int C, void* stream) {
-    int sms = 0;
-    size_t optin = 0;
-    fs_status st = device_limits(sms, optin);
-    if (st != FS_OK) return st;
+static fs_status run_uniform(UniformArgs& a, int C, int sms, size_t optin, void* stream) {
     const void* fn = reinterpret_cast<const void*>(uniform_kernel<T>);
-    st = prepare_kernel(fn);
+    const fs_status st = prepare_kernel(fn);
     if (st != FS_OK) return st;
     a.nsc = (a.ls + C - 1) / C;
     const size_t smem = USmem::total(a.nsc, a.ls);
@@ -1418,17 +1414,21 @@ fs_status fs_top_k_top_p_sampling_from_uniforms(const void* logits, int32_t dtyp
     if (!indices && order == FS_ORDER_JOINT && top_p && (top_k || min_p))
         a.ssum = reinterpret_cast<float*>(a.skey + size_t(batch_in) * a.ls);
     // CTAs per row: one where a small set needs only the summary,
-    // else as many as fill the GPU with two per SM; a power of two.
-    int C = 1;
+    // else as many as fill the GPU with two per SM; a power of two.  (By the arguments given: a row whose top_k
+    // or min_p turns out to be off, or whose set is too large for the list, has one CTA too.)
+    int C = 1, sms = 0;
+    size_t optin = 0;
+    const fs_status found = device_limits(sms, optin);
+    if (found != FS_OK) return found;
     const bool whole = (!top_k && (top_p || !min_p)) || (order == FS_ORDER_JOINT && top_p && !a.ssum);
     if (whole)
-        while (C < 8 && int64_t(batch_out) * C * 2 <= 304 && a.ls >= C * 2 * 16) C *= 2;
+        while (C < 8 && int64_t(batch_out) * C * 2 <= int64_t(sms) * 2 && a.ls >= C * 2 * 16) C *= 2;
     while (C < 8 && USmem::total((a.ls + C - 1) / C, a.ls) > (200u << 10)) C *= 2;
     if (int64_t(batch_out) * C > 0x7fffffffLL) return FS_ERR_UNSUPPORTED;
     switch (dtype) {
-        case FS_F32: return run_uniform<float>(a, C, stream);
-        case FS_BF16: return run_uniform<__nv_bfloat16>(a, C, stream);
-        default: return run_uniform<__half>(a, C, stream);
+        case FS_F32: return run_uniform<float>(a, C, sms, optin, stream);
+        case FS_BF16: return run_uniform<__nv_bfloat16>(a, C, sms, optin, stream);
+        default: return run_uniform<__half>(a, C, sms, optin, stream);
     }
 }
 

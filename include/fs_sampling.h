@@ -444,7 +444,7 @@ typedef struct fs_paged_kv {
  * query goes to query_out as it is.  A token whose table row, page entry or page does not
  * exist (rows[t] or the page out of range, positions[t] beyond the table's width) is not
  * written to the cache either (its query is rotated).  No two tokens of a call may name
- * the same slot; if they do, each 16-byte word of it comes from one of them. */
+ * the same slot; if they do, each element of it comes from one of them. */
 fs_status fs_append_paged_kv(const fs_paged_kv* cache, const void* key, const int64_t* key_strides,
                              const void* value, const int64_t* value_strides, int32_t tokens,
                              const int32_t* page_table, int32_t table_rows, int32_t table_width,

@@ -454,6 +454,23 @@ fs_status fs_append_paged_kv(const fs_paged_kv* cache, const void* key, const in
                              const int64_t* query_strides, int32_t q_heads, void* query_out,
                              const int64_t* query_out_strides, void* stream);
 
+/* fs_append_paged_kv with the norms of queries and keys in the same pass: before the rotation each
+ * head x of them becomes x / sqrt(mean(x^2) + eps) * weight, in float32 (sums of squares included),
+ * and is rounded once behind the rotation.
+ *   query_weight, key_weight   [head_dim] float32, contiguous; nullable: that side has no norm (query_weight needs a query)
+ *   eps                        >= 0
+ * Values are appended as they are; the query of a padding token goes to query_out as it is.  Everything else
+ * as above. */
+fs_status fs_append_paged_kv_normed(const fs_paged_kv* cache, const void* key, const int64_t* key_strides,
+                                    const void* value, const int64_t* value_strides, int32_t tokens,
+                                    const int32_t* page_table, int32_t table_rows, int32_t table_width,
+                                    const int32_t* rows, const int32_t* positions,
+                                    const int32_t* rotary_positions, const float* inv_freq,
+                                    int32_t rotary_dim, int32_t interleaved, const void* query,
+                                    const int64_t* query_strides, int32_t q_heads, void* query_out,
+                                    const int64_t* query_out_strides, const float* query_weight,
+                                    const float* key_weight, float eps, void* stream);
+
 /* Attention of a batch whose rows share long prefixes, over a paged cache:
  *   out = softmax(scale * q [Kp; Ks]^T) [Vp; Vs],
  * Kp, Vp the keys and values of the prefix of the row's group, Ks, Vs those of the row's own
@@ -493,6 +510,94 @@ fs_status fs_shared_prefix_attention_workspace_bytes(const fs_paged_kv* cache, i
                                                      int32_t queries, int32_t q_heads,
                                                      int32_t groups, int32_t prefix_width,
                                                      int32_t suffix_width, size_t* bytes);
+
+/* ------------------------------------------------------------------ a step of requests of any kind
+ *
+ * The entries below are the steps of a batch in which some requests decode a token each and others
+ * get a chunk of their prompt; the tokens of all requests lie one behind the other.  Conventions as for the decode step. */
+
+/* Page tables and token places of one step, from the requests' lengths.  Request r holds lens[r] tokens and
+ * asks for new_lens[r] more (0 or less: none).  Its new pages, those of tokens lens[r] .. lens[r] + new_lens[r] - 1 that
+ * start a page, come from the top of a stack of free pages and are written to its table row.
+ *   lens, new_lens  [requests] int32
+ *   page_table      [requests, table_width] int32, contiguous; only the new pages' entries are written
+ *   free_pages      [free_size] int32, a stack: its top is entry free_count - 1.  Request by request, page by page,
+ *                   pages are taken downwards
+ *   free_count      one int32 (clamped to 0 .. free_size)
+ *   budget          tokens of the step at most
+ *   query_starts    [requests + 1] int32, written: request r's tokens are query_starts[r] .. query_starts[r + 1] - 1
+ *   rows, positions [budget] int32, written: each token's request, and its place in that
+ *                   request, as fs_append_paged_kv takes them; -1 behind the last token
+ *   totals          [requests] int32, written: tokens held behind the step
+ *   free_left       one int32, written: the stack's new count
+ * A request gets all that it asks for or nothing.  It is granted if the pages that requests 0 .. r ask for together
+ * are no more than the free ones (or it needs none itself) and the tokens that they ask for together
+ * are no more than the budget; a request whose lens[r] is negative or which would
+ * have more than table_width * page_size tokens asks for nothing.  Page numbers are copied, not checked.  What is
+ * written shares no memory with what is read. */
+fs_status fs_paged_step_tables(const int32_t* lens, const int32_t* new_lens, int32_t requests, int32_t* page_table,
+                               int32_t table_width, const int32_t* free_pages, int32_t free_size,
+                               const int32_t* free_count, int32_t page_size, int32_t budget,
+                               int32_t* query_starts, int32_t* rows, int32_t* positions, int32_t* totals,
+                               int32_t* free_left, void* stream);
+
+/* Attention of chunks of new tokens over a paged cache that holds them already:
+ *   out = softmax(scale * q K^T) V  over the keys that the query sees.
+ * Request r's queries are tokens query_starts[r] .. query_starts[r + 1] - 1 of the batch, the last ones of its
+ * lens[r] tokens, in order: the query at position p of the request sees the keys k <= p with k > p - window
+ * (window > 0; 0: all of them) or k < sinks.  Query head h reads key/value head h / (q_heads / num_heads).
+ *   query, out     [tokens, q_heads, head_dim]; strides {token, head}; out may be query itself
+ *   page_table     [requests, table_width] int32, contiguous
+ *   query_starts   [requests + 1] int32, not decreasing (clamped to 0 .. tokens)
+ *   lens           [requests] int32, the request's tokens with its new ones (clamped to what the table can name)
+ *   max_queries    the most queries of a request, >= 1: chooses kernels and the workspace.  Requests with more
+ *                  are answered as well, slower
+ *   zero_rest      1: rows of no request (before query_starts[0], behind query_starts[requests]) become zeros, lse
+ *                  -infinity; 0: they are left as they are
+ *   out_lse        [tokens, q_heads] float32, nullable: log of the sum of exp(scale * q k)
+ * Types bf16 and f16, head_dim 64, 128 or 256 (else FS_ERR_UNSUPPORTED); every address, and every stride in
+ * bytes, is a multiple of 16 (else FS_ERR_INVALID_ARG).  Arithmetic as in fs_shared_prefix_attention.  A query that sees no
+ * key gives zeros and lse = -inf; one that sees a key whose page does not exist, or a NaN in a key, gives NaN.
+ * Keys and values that a query does not see do not reach it; infinite and NaN values that it sees do (an infinite one
+ * whose weight rounds to 0 may show as NaN). */
+fs_status fs_paged_chunk_attention(const fs_paged_kv* cache, const void* query, const int64_t* query_strides,
+                                   int32_t tokens, int32_t q_heads, const int32_t* page_table, int32_t requests,
+                                   int32_t table_width, const int32_t* query_starts, const int32_t* lens,
+                                   int32_t max_queries, int32_t window, int32_t sinks, float scale,
+                                   int32_t zero_rest, void* out, const int64_t* out_strides, float* out_lse,
+                                   void* workspace, size_t workspace_bytes, void* stream);
+
+/* Workspace of fs_paged_chunk_attention for these sizes on the current device. */
+fs_status fs_paged_chunk_attention_workspace_bytes(const fs_paged_kv* cache, int32_t tokens, int32_t requests,
+                                                   int32_t q_heads, int32_t table_width, int32_t max_queries,
+                                                   size_t* bytes);
+
+/* Penalties, biases and grammar masks on logits, row by row, in this order, in float32 and rounded once:
+ *   repetition  of a token that is in the row's history: z > 0 ? z / repetition : z * repetition
+ *   frequency   z - frequency * count, count: how often the token is in the history behind the prompt
+ *   presence    z - presence where count > 0
+ *   bias        z + bias
+ *   mask        -infinity where the row's mask has no bit
+ *   logits, out    [batch, vocab] of `dtype`, rows `row_stride` / `out_stride` elements apart (>= vocab); out may be
+ *                  logits itself, with its stride (then only what changes is written).  No alignment beyond the element's
+ *   tokens         [batch, history] int32, rows `token_stride` apart; nullable: no penalties (then lens to
+ *                  frequency are NULL too).  Tokens outside [0, vocab) are skipped
+ *   lens           [batch] int32: the row's tokens (clamped to 0 .. history); nullable: history
+ *   prompt_lens    [batch] int32: the first of them that are the prompt; nullable: 0
+ *   repetition, presence, frequency   [batch] float32, nullable: 1, 0, 0
+ *   bias_starts    [batch + 1] int32, not decreasing, nullable: row b's biases are entries bias_starts[b] ..
+ *                  bias_starts[b + 1] - 1 (clamped to 0 .. biases) of bias_tokens and bias_values; of several for one token
+ *                  the last one counts; tokens outside [0, vocab) are skipped
+ *   allowed        [masks, ceil(vocab / 32)] 32-bit words, nullable: bit v % 32 of word v / 32 allows token v
+ *   allowed_rows   [batch] int32: the row's mask, negative: none (one that is `masks` or more allows nothing);
+ *                  nullable: mask b (masks >= batch)
+ * Every other logit is copied.  Fits between a model's logits and fs_top_k_top_p_sampling_from_uniforms. */
+fs_status fs_adjust_logits(const void* logits, int32_t dtype, int64_t row_stride, int32_t batch, int32_t vocab,
+                           const int32_t* tokens, int64_t token_stride, int32_t history, const int32_t* lens,
+                           const int32_t* prompt_lens, const float* repetition, const float* presence,
+                           const float* frequency, const int32_t* bias_starts, const int32_t* bias_tokens,
+                           const float* bias_values, int32_t biases, const uint32_t* allowed, int32_t masks,
+                           const int32_t* allowed_rows, void* out, int64_t out_stride, void* stream);
 
 /* Free every scratch buffer of the library on every device.  Only when no call of
  * this library is in flight on any stream (and no captured graph that uses one will

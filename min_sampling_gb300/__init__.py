@@ -25,6 +25,7 @@ __all__ = [
     "chain_speculative_sampling", "top_k_renorm_probs", "top_p_renorm_probs",
     "top_k_mask_logits", "philox4x32_10",
     "top_k_top_p_sampling_from_uniforms", "append_paged_kv", "shared_prefix_attention",
+    "paged_step_tables", "paged_chunk_attention", "adjust_logits",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libfs_sampling.so")
@@ -412,7 +413,8 @@ def top_k_top_p_sampling_from_uniforms(logits, uniforms, temperature=None, top_k
 
 
 def append_paged_kv(key, value, k_cache, v_cache, page_table, positions, rows=None, *, rotary_positions=None,
-                    inv_freq=None, interleaved=False, query=None, query_out=None):
+                    inv_freq=None, interleaved=False, query=None, query_out=None, query_norm=None, key_norm=None,
+                    norm_eps=1e-6):
     """Append keys and values to a paged cache, the keys rotated by their positions on the
     way, and rotate the tokens' queries by the same angles.
 
@@ -424,11 +426,12 @@ def append_paged_kv(key, value, k_cache, v_cache, page_table, positions, rows=No
     rotary_positions: [N] int32 (default: positions); inv_freq: [r / 2] float32 rotates the
     first r elements of each head, in halves or, with ``interleaved``, in neighbouring pairs (None: no
     rotation).  query: [N, q_heads, dim] is rotated into query_out (default: a new tensor; may be query itself),
-    which is returned (None without a query).  The caches and query_out share no memory with one another or with key,
+    which is returned (None without a query).  query_norm, key_norm: [dim] float32 weights; before the rotation
+    each head x of the queries, of the keys becomes x / sqrt(mean(x^2) + norm_eps) * weight in float32 (None: no norm).  The caches and query_out share no memory with one another or with key,
     value and query otherwise: such calls are refused.  No backward pass: tensors that require a gradient are refused
     outside of torch.no_grad(), tensors with a forward-mode tangent always."""
     r = _native().append(key, value, k_cache, v_cache, page_table, positions, rows, rotary_positions, inv_freq,
-                         interleaved, query, query_out)
+                         interleaved, query, query_out, query_norm, key_norm, norm_eps)
     return _check(r) if type(r) is int else r
 
 
@@ -449,4 +452,61 @@ def shared_prefix_attention(query, k_cache, v_cache, prefix_table, prefix_lens, 
     torch.no_grad(), tensors with a forward-mode tangent always."""
     r = _native().attention(query, k_cache, v_cache, prefix_table, prefix_lens, suffix_table, suffix_lens, group_starts,
                             scale, out, return_lse)
+    return _check(r) if type(r) is int else r
+
+
+# ------------------------------------------------------------------ a step of requests of any kind
+
+def paged_step_tables(lens, new_lens, page_table, free_pages, free_count, page_size, max_tokens):
+    """Page tables and token places of one step in which request r, which holds ``lens[r]`` tokens, gets
+    ``new_lens[r]`` more (one that decodes 1, one whose prompt is read a chunk, an idle one 0).
+
+    lens, new_lens: [R] int32.  page_table: [R, width] int32; the entries of the new pages are written, with pages from
+    the top of the stack free_pages ([F] int32), of whose entries the first free_count[0] are free.  A request gets
+    all that it asks for or nothing: it is granted if the requests up to it ask for no more pages than
+    are free (or it needs none) and for no more than max_tokens tokens together.
+    Returns (query_starts [R + 1], rows [max_tokens], positions [max_tokens], totals [R], free_left [1]), all
+    int32: the tokens of request r lie at query_starts[r] up to query_starts[r + 1] in the step's batch; each
+    token's request and place, as append_paged_kv takes them (-1 behind the last one); the tokens that each
+    request holds now; the stack's new count."""
+    r = _native().step_tables(lens, new_lens, page_table, free_pages, free_count, page_size, max_tokens)
+    return r if type(r) is tuple else _check(r)
+
+
+def paged_chunk_attention(query, k_cache, v_cache, page_table, query_starts, lens, *, window=None, sinks=0,
+                          max_queries=None, scale=None, out=None, return_lse=False):
+    """Attention of chunks of new tokens over a paged cache that holds them: request r's queries are
+    the tokens query_starts[r] up to query_starts[r + 1] of the batch, the last ones of its lens[r] tokens.
+
+    query: [N, heads, dim]; k_cache, v_cache: [pages, page_size, kv_heads, dim] bfloat16 or float16, dim 64, 128 or 256.
+    page_table: [R, width], query_starts: [R + 1] (ascending), lens: [R], all int32.  The query at position p sees the keys
+    k <= p; with a window only the last `window` of them and the first `sinks` keys.  max_queries: the most queries of
+    a request (default: N), by which kernels and workspace are chosen; requests with more are answered as well, slower.
+    scale defaults to dim ** -0.5.  out may be query itself; it shares no memory with it or the caches otherwise.
+    Rows of no request (before query_starts[0], behind the last one) are left as they are in a given out and
+    zeros in a new one; their lse is -inf.  Returns out, and with return_lse the log of the sum of exponentials, float32 [N, heads].
+    No backward pass: tensors that require a gradient are refused outside of torch.no_grad(), tensors with a
+    forward-mode tangent always."""
+    r = _native().chunk_attention(query, k_cache, v_cache, page_table, query_starts, lens, window, sinks, max_queries, scale,
+                                  out, return_lse)
+    return _check(r) if type(r) is int else r
+
+
+def adjust_logits(logits, tokens=None, lens=None, prompt_lens=None, *, repetition=None, presence=None, frequency=None,
+                  bias_starts=None, bias_tokens=None, bias_values=None, allowed=None, allowed_rows=None, out=None):
+    """Penalties for repeated tokens, biases and grammar masks on logits, before they are sampled.
+
+    logits: [B, V] float32, bfloat16 or float16, rows of any stride >= V.  tokens: [B, L] int32, each row's history, of which the
+    first lens[b] count (default: all); the first prompt_lens[b] of those are the prompt (default: none).  In this
+    order: a logit z of a token in the history becomes z / repetition if positive and z * repetition otherwise;
+    frequency times its count behind the prompt is taken off, and presence if that count is not 0; the row's bias is
+    added; what its mask does not allow becomes -inf.  Penalties are numbers or [B] float32 tensors.
+    bias_starts [B + 1], bias_tokens int32, bias_values float32: row b's biases are the entries bias_starts[b] up to
+    bias_starts[b + 1] (of several for a token the last one counts).  allowed: [M, ceil(V / 32)] int32, bit v % 32 of word v // 32
+    allows token v; allowed_rows: [B] int32, each row's mask (negative: none; default: mask b).
+    out: [B, V] (default: a new tensor); logits itself for in place, where only what changes is written.
+    Returns out.  No backward pass: tensors that require a gradient are refused outside of torch.no_grad(), tensors
+    with a forward-mode tangent always."""
+    r = _native().adjust(logits, tokens, lens, prompt_lens, repetition, presence, frequency, bias_starts, bias_tokens,
+                         bias_values, allowed, allowed_rows, out)
     return _check(r) if type(r) is int else r

@@ -1,0 +1,124 @@
+// What the kernels of chunk attention have in common: arguments, the requests' query tiles and
+// the keys that a tile sees.
+#pragma once
+
+#include <type_traits>
+
+#include "attention.cuh"
+
+namespace fsd {
+
+constexpr int FEW = 16;         // query rows that a tile of chunk_rows_kernel holds beside the tensor cores' tiles
+constexpr int MANY = 256;       // query rows of a tensor-core tile
+
+struct ChunkArgs {
+    const void* q;
+    void* out;
+    float* lse;                 // [N][Hq], nullable
+    int64_t qs[2], os[2];       // strides: token, head
+    const void* k;
+    const void* v;
+    int64_t kc[3], vc[3];       // strides: page, slot, head
+    int num_pages, page_size, page_shift;  // page_shift: log2(page_size), -1 when it is no power of two
+    const int* table;           // [R][width]
+    const int* starts;          // [R + 1]
+    const int* lens;            // [R]
+    int R, width, N, Hq, Hkv, gs;   // gs = Hq / Hkv
+    int window, sinks;          // window: INT_MAX without one
+    float scale;                // the score's scale times log2(e)
+    int zero_rest;              // rows of no request get zeros (and lse -infinity)
+    int rows_upto;              // chunk_rows_kernel takes requests of up to this many query rows a key/value head
+    // chunk_rows_kernel: CTAs, their parts, what the parts belong to
+    int grid, least;            // least: units (key tiles) of a CTA at least
+    float* part_o;              // [2 grid][MT][D]
+    float* part_l;              // [2 grid][MT], log2 of each part's sum of 2^score
+    int4* split;                // [grid]: request, head, row0, parts; parts 0: none
+    // chunk_tensor_kernel's
+    int t_grid, t_tiles;
+    float* t_part_o;            // [2 t_grid][MANY][D]
+    float* t_part_l;
+    int4* t_split;
+    int4* t_items;              // [t_tiles]: request, row0, units before (low, high word)
+    int* t_plan;                // tiles, units (low, high word) of a key/value head
+};
+
+// A request: its queries [q0, q0 + nq), query rows per key/value head (a row is a token's query head: token
+// j's heads follow one another), tokens.
+struct Request {
+    int q0, nq, len;
+    __device__ __forceinline__ int rows(const ChunkArgs& a) const { return nq * a.gs; }
+    // Position of the token of a query row; below 0 it sees nothing.
+    __device__ __forceinline__ int pos(const ChunkArgs& a, int row) const { return len - nq + row / a.gs; }
+};
+__device__ __forceinline__ Request request(const ChunkArgs& a, int r) {
+    Request x;
+    x.q0 = min(max(a.starts[r], 0), a.N);
+    x.nq = max(min(max(a.starts[r + 1], 0), a.N) - x.q0, 0);
+    x.len = int(min(int64_t(max(a.lens[r], 0)), int64_t(a.width) * a.page_size));
+    return x;
+}
+
+// The keys that the tokens at positions p_lo .. p_hi see between them, [lo, hi) and [0, sink), in tiles of KT keys:
+// tile i holds the keys from at(i) on.
+template <int KT>
+struct KeyTiles {
+    int lo, hi, sink;
+    int few, skip, n;           // tiles before the gap, first tile behind it, tiles (at least 1)
+    __device__ __forceinline__ KeyTiles(const ChunkArgs& a, int p_lo, int p_hi) {
+        hi = max(p_hi + 1, 0);
+        lo = max(0, max(p_lo, 0) - a.window + 1);
+        sink = min(a.sinks, hi);
+        skip = lo / KT;
+        few = min((sink + KT - 1) / KT, skip);
+        n = max(few + (hi + KT - 1) / KT - skip, 1);
+    }
+    __device__ __forceinline__ int at(int i) const { return (i < few ? i : i - few + skip) * KT; }
+    // Whether some token sees key k.
+    __device__ __forceinline__ bool seen(int k) const { return k < hi && (k >= lo || k < sink); }
+};
+// Whether the token at position p sees key k.
+__device__ __forceinline__ bool sees(const ChunkArgs& a, int p, int k) {
+    return k <= p && (p - k < a.window || k < a.sinks);
+}
+
+// ------------------------------------------------------------------ infinite and NaN values
+
+// Whether an element of a 16-byte word is infinite or NaN, and the word with zeros in their place.
+template <typename T>
+constexpr uint32_t exponent_bits() { return std::is_same<T, __half>::value ? 0x7c00u : 0x7f80u; }
+template <typename T>
+__device__ __forceinline__ bool odd_half(uint32_t x) { return (x & exponent_bits<T>()) == exponent_bits<T>(); }
+template <typename T>
+__device__ __forceinline__ bool odd_words(uint4 w) {
+    return odd_half<T>(w.x) || odd_half<T>(w.x >> 16) || odd_half<T>(w.y) || odd_half<T>(w.y >> 16) || odd_half<T>(w.z) ||
+           odd_half<T>(w.z >> 16) || odd_half<T>(w.w) || odd_half<T>(w.w >> 16);
+}
+template <typename T>
+__device__ __forceinline__ uint32_t even_word(uint32_t x) {
+    return (odd_half<T>(x) ? 0u : x & 0xffffu) | (odd_half<T>(x >> 16) ? 0u : x & 0xffff0000u);
+}
+template <typename T>
+__device__ __forceinline__ uint4 even_words(uint4 w) {
+    return make_uint4(even_word<T>(w.x), even_word<T>(w.y), even_word<T>(w.z), even_word<T>(w.w));
+}
+// The infinite and NaN values, elements d .. d + 3 of a head, of the keys k0 .. k0 + n - 1 that the
+// token at position p sees, added to y.
+template <typename T>
+__device__ __noinline__ void add_odd(const ChunkArgs& a, const int* table, int p, int k0, int n, int head, int d, float4& y) {
+    for (int k = k0; k < k0 + n && k <= p; ++k) {
+        if (!sees(a, p, k)) continue;
+        const int pi = k / a.page_size, page = table[pi];
+        if (page < 0 || page >= a.num_pages) continue;
+        const T* v = static_cast<const T*>(a.v) + page * a.vc[0] + (k - pi * a.page_size) * a.vc[1] + head * a.vc[2] + d;
+        auto odd = [&](int e) {
+            const float z = Mma<T>::get(v[e]);
+            return fabsf(z) <= 3.402823466e38f ? 0.f : z;
+        };
+        y = make_float4(y.x + odd(0), y.y + odd(1), y.z + odd(2), y.w + odd(3));
+    }
+}
+
+// The tensor cores' part (chunk_tensor.cu): requests of more than rows_upto query rows, for heads of 64 or 128.
+fs_status launch_chunk_tensor(const ChunkArgs& a, int dtype, int head_dim, void* stream);
+
+}  // namespace fsd

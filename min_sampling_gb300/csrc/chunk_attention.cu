@@ -1,0 +1,663 @@
+// Attention of chunks of new tokens over a paged key/value cache (sm_103a).
+//
+// Request r has nq queries, its last nq tokens of len.  The query at position p sees the keys k <= p
+// with k > p - window or k < sinks:
+//   out = softmax(scale * q K^T) V  over those keys.
+// The queries of all heads that share a key/value head are the rows of one matrix, so that a key is
+// read once for all of them: nq * (heads / key-value heads) rows, in tiles.
+//
+// The work of a launch is one line of units, (request, key/value head, query tile, key tile), cut into
+// equal runs, one for each CTA, whatever the mix of lengths.  A CTA takes the tiles in its run one after the
+// other; a tile that lies in one run is written at once, the parts of one that is cut are joined by
+// their maxima and sums in a fixed order (join_chunk_kernel; no atomics):
+//   m = max_i m_i,  l = sum_i 2^(m_i - m) l_i,  out = sum_i 2^(m_i - m) l_i out_i / l.
+//
+// chunk_rows_kernel: mma.sync, tiles of 16 rows (single tokens) or 64.  chunk_tensor.cu: more rows, on
+// the 5th-generation tensor cores.
+#include "chunk.cuh"
+
+#include <type_traits>
+
+#include "fragments.cuh"
+
+namespace fsd {
+
+constexpr int CSTAGES = 2;      // tiles of keys and values in flight
+
+// Shared memory: queries, CSTAGES x (keys, values), the keys' offsets.
+template <int D, int MT, int KT>
+struct ChunkSmem {
+    static constexpr int TILE = KT * D * 2;
+    static constexpr int KV = MT * D * 2;
+    static constexpr int OFF = KV + CSTAGES * 2 * TILE;
+    static constexpr int TOTAL = OFF + 2 * 2 * KT * 8 + 256;
+};
+
+// A CTA's place in the line of units.
+struct Place {
+    int r;              // request
+    int64_t at, before; // unit, and the units before the request's
+    int64_t units;      // the request's units of one key/value head
+};
+
+// Units of one key/value head of a request that chunk_rows_kernel takes.
+template <int MT, int KT>
+__device__ __forceinline__ int64_t units_of(const ChunkArgs& a, const Request& x) {
+    const int M = x.rows(a);
+    if (M == 0 || M > a.rows_upto) return 0;
+    int64_t n = 0;
+    for (int row = 0; row < M; row += MT) n += KeyTiles<KT>(a, x.pos(a, row), x.pos(a, min(row + MT, M) - 1)).n;
+    return n;
+}
+
+// WM x WN warps over a tile of MT = 16 RM WM query rows and KT keys; each warp keeps its own running
+// maximum, sum and output over its share of the keys.  Bound by the reads of keys and values.
+template <typename T, int D, int MT, int WM, int WN, int RM, int KT>
+__global__ void __launch_bounds__(32 * WM * WN) chunk_rows_kernel(const ChunkArgs a) {
+    constexpr int NT = 32 * WM * WN;
+    static_assert(MT == 16 * RM * WM && KT <= NT, "warp layout");
+    using S = ChunkSmem<D, MT, KT>;
+    constexpr int KW = KT / WN;       // keys per warp and tile
+    constexpr int NF = KW / 8;        // score fragments
+    constexpr int DC = D / 8;         // 16-byte chunks per row
+    constexpr float UP = std::is_same<T, __half>::value ? 32768.f : 1.f;   // the weights' factor in the product
+    static_assert(WN * MT * (D + 2) * 4 <= S::OFF, "the warps' parts fit where the tiles were");
+    extern __shared__ __align__(128) unsigned char smem[];
+    const uint32_t sbase = smem_u32(smem);
+    int64_t* soff = reinterpret_cast<int64_t*>(smem + S::OFF);                       // [2][2][KT]
+    int64_t* words = reinterpret_cast<int64_t*>(smem + S::OFF + 2 * 2 * KT * 8);     // scan, then the place found
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int wm = warp / WN, wn = warp % WN;
+    grid_dependency_wait();
+    allow_dependents();
+
+    // ---- this CTA's run of units
+    int64_t unit, last, run;
+    Place pl;
+    {
+        const int per = (a.R + NT - 1) / NT, r0 = min(tid * per, a.R), r1 = min(r0 + per, a.R);
+        int64_t mine = 0;
+        for (int r = r0; r < r1; ++r) mine += units_of<MT, KT>(a, request(a, r));
+        int64_t x = mine;
+#pragma unroll
+        for (int s = 1; s < 32; s <<= 1) {
+            const int64_t y = __shfl_up_sync(FULL, x, s);
+            if (lane >= s) x += y;
+        }
+        if (lane == 31) words[warp] = x;
+        __syncthreads();
+        int64_t before = 0, total = 0;
+#pragma unroll
+        for (int w = 0; w < NT / 32; ++w) {
+            if (w == warp) before = total;
+            total += words[w];
+        }
+        before += x - mine;
+        total *= a.Hkv;
+        run = max(int64_t(a.least), (total + a.grid - 1) / a.grid);
+        unit = min(blockIdx.x * run, total);
+        last = min(unit + run, total);
+        if (unit < last && before * a.Hkv <= unit && unit < (before + mine) * a.Hkv) {
+            for (int r = r0; r < r1; ++r) {
+                const int64_t n = units_of<MT, KT>(a, request(a, r));
+                if (unit < (before + n) * a.Hkv) {
+                    words[16] = r, words[17] = before * a.Hkv, words[18] = n;
+                    break;
+                }
+                before += n;
+            }
+        }
+        if (tid == 0) a.split[blockIdx.x] = make_int4(0, 0, 0, 0);
+        __syncthreads();
+        pl = Place{int(words[16]), unit, words[17], words[18]};
+    }
+    if (a.zero_rest) {
+        // rows of no request
+        const int lo = a.R > 0 ? min(max(a.starts[0], 0), a.N) : a.N, hi = a.R > 0 ? max(min(max(a.starts[a.R], 0), a.N), lo) : a.N;
+        const int rest = lo + a.N - hi;
+        for (int64_t i = int64_t(blockIdx.x) * NT + tid; i < int64_t(rest) * a.Hq * DC; i += int64_t(gridDim.x) * NT) {
+            const int c = int(i % DC), h = int(i / DC % a.Hq), j = int(i / DC / a.Hq), t = j < lo ? j : hi + j - lo;
+            *reinterpret_cast<uint4*>(static_cast<T*>(a.out) + t * a.os[0] + h * a.os[1] + c * 8) = make_uint4(0, 0, 0, 0);
+            if (c == 0 && a.lse) a.lse[int64_t(t) * a.Hq + h] = -INFINITY;
+        }
+    }
+
+#pragma unroll 1
+    while (unit < last) {
+        // ---- the tile that the unit lies in
+        Request x = request(a, pl.r);
+        while (unit >= pl.before + pl.units * a.Hkv) {
+            pl.before += pl.units * a.Hkv;
+            x = request(a, ++pl.r);
+            pl.units = units_of<MT, KT>(a, x);
+        }
+        const int head = int((unit - pl.before) / pl.units);
+        const int M = x.rows(a);
+        int64_t first = pl.before + head * pl.units;   // the tile's first unit
+        int row0 = 0;
+        KeyTiles<KT> kt(a, x.pos(a, 0), x.pos(a, min(MT, M) - 1));
+        while (unit >= first + kt.n) {
+            first += kt.n;
+            row0 += MT;
+            kt = KeyTiles<KT>(a, x.pos(a, row0), x.pos(a, min(row0 + MT, M) - 1));
+        }
+        const int i0 = int(unit - first), i1 = int(min(int64_t(kt.n), last - first));   // its key tiles in this run
+        const bool whole = i0 == 0 && i1 == kt.n;
+        const int p_lo = x.pos(a, row0), p_hi = x.pos(a, min(row0 + MT, M) - 1);
+        const int* table = a.table + int64_t(pl.r) * a.width;
+        const int tiles = i1 - i0;
+        // A key tile of which some token of the query tile does not see all the keys that are loaded.
+        auto partial = [&](int k0) {
+            return p_lo != p_hi && (k0 + KT > p_lo + 1 || (p_hi - k0 >= a.window && k0 + KT > a.sinks));
+        };
+
+        __syncthreads();   // the tile before is done with shared memory
+        for (int i = tid; i < MT * DC; i += NT) {
+            const int r = i / DC, c = i % DC, row = row0 + r;
+            const bool on = row < M;
+            const int j = on ? row / a.gs : 0, h = head * a.gs + (on ? row % a.gs : 0);
+            cp16(sbase + chunk_at<D>(r, c), static_cast<const T*>(a.q) + (x.q0 + j) * a.qs[0] + h * a.qs[1] + c * 8, on);
+        }
+        // ---- pipeline of key/value tiles.  A key's offsets are looked up one tile before its
+        // loads are issued, by one thread per key.
+        constexpr int64_t MISSING = NOWHERE + 1;   // of a page that does not exist
+        auto look_up = [&](int tile, int64_t& ko, int64_t& vo) {
+            ko = vo = NOWHERE;
+            if (tid >= KT || tile >= tiles) return;
+            const int key = kt.at(i0 + tile) + tid;
+            if (kt.seen(key)) {
+                const int pi = a.page_shift >= 0 ? key >> a.page_shift : key / a.page_size;
+                const int page = table[pi];
+                if (page >= 0 && page < a.num_pages) {
+                    const int s = key - pi * a.page_size;
+                    ko = page * a.kc[0] + s * a.kc[1] + head * a.kc[2];
+                    vo = page * a.vc[0] + s * a.vc[1] + head * a.vc[2];
+                } else {
+                    ko = MISSING;
+                }
+            }
+        };
+        auto put_offsets = [&](int tile, int64_t ko, int64_t vo) {
+            if (tid < KT) {
+                soff[(tile & 1) * 2 * KT + tid] = ko;
+                soff[(tile & 1) * 2 * KT + KT + tid] = vo;
+            }
+        };
+        auto issue = [&](int tile) {
+            const int64_t* off = soff + (tile & 1) * 2 * KT;
+            const uint32_t kd = sbase + S::KV + (tile % CSTAGES) * 2 * S::TILE;
+#pragma unroll
+            for (int i = 0; i < KT * DC / NT; ++i) {
+                const int r = (tid + i * NT) / DC, c = (tid + i * NT) % DC;
+                const int64_t ko = off[r], vo = off[KT + r];
+                const bool on = vo != NOWHERE;
+                if (ko == MISSING)   // its keys are NaN, and so is every query that sees it
+                    *reinterpret_cast<uint4*>(smem + (kd - sbase) + chunk_at<D>(r, c)) =
+                        make_uint4(0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu);
+                else
+                    cp16(kd + chunk_at<D>(r, c), static_cast<const T*>(a.k) + (on ? ko + c * 8 : 0), on);
+                cp16(kd + S::TILE + chunk_at<D>(r, c), static_cast<const T*>(a.v) + (on ? vo + c * 8 : 0), on);
+            }
+        };
+        int64_t ko, vo;
+#pragma unroll
+        for (int t = 0; t < CSTAGES - 1; ++t) {
+            look_up(t, ko, vo);
+            put_offsets(t, ko, vo);
+            __syncthreads();
+            if (t < tiles) issue(t);
+            cp_async_commit();
+        }
+        look_up(CSTAGES - 1, ko, vo);
+        put_offsets(CSTAGES - 1, ko, vo);
+
+        float o[RM][D / 8][4];
+        float mrow[RM][2], lrow[RM][2];
+        int pos[RM][2];
+        bool odd_seen = false;
+#pragma unroll
+        for (int i = 0; i < RM; ++i) {
+#pragma unroll
+            for (int f = 0; f < D / 8; ++f)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[i][f][e] = 0.f;
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                mrow[i][j] = -INFINITY;
+                lrow[i][j] = 0.f;
+                pos[i][j] = x.pos(a, min(row0 + (wm * RM + i) * 16 + j * 8 + (lane >> 2), M - 1));
+            }
+        }
+        const int qrow = (wm * RM) * 16 + (lane & 15), qch = lane >> 4;
+
+#pragma unroll 1
+        for (int t = 0; t < tiles; ++t) {
+            cp_async_wait<CSTAGES - 2>();
+            __syncthreads();  // tile t is there, tile t - 1 is done with, the next offsets are written
+            if (t + CSTAGES - 1 < tiles) issue(t + CSTAGES - 1);
+            cp_async_commit();
+            look_up(t + CSTAGES, ko, vo);
+            const uint32_t ks = sbase + S::KV + (t % CSTAGES) * 2 * S::TILE, vs = ks + S::TILE;
+            const int k0 = kt.at(i0 + t);
+            // A value that only some of the tokens see may be infinite or NaN, which a weight of
+            // zero does not cancel: such values are taken out of the tile, and added at the end to the
+            // outputs of the queries that see them.
+            if (partial(k0)) {
+                unsigned char* vb = smem + (vs - sbase);
+                bool odd = false;
+                for (int i = tid; i < KT * DC; i += NT) odd |= odd_words<T>(*reinterpret_cast<const uint4*>(vb + i * 16));
+                if (__syncthreads_or(odd)) {
+                    odd_seen = true;
+                    for (int i = tid; i < KT * DC; i += NT) {
+                        uint4* w = reinterpret_cast<uint4*>(vb + i * 16);
+                        *w = even_words<T>(*w);
+                    }
+                    __syncthreads();
+                }
+            }
+
+            // ---- scores of this warp's keys
+            float s[RM][NF][4];
+#pragma unroll
+            for (int i = 0; i < RM; ++i)
+#pragma unroll
+                for (int f = 0; f < NF; ++f)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) s[i][f][e] = 0.f;
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+                uint32_t af[RM][4];
+#pragma unroll
+                for (int i = 0; i < RM; ++i) ldsm4(af[i], sbase + chunk_at<D>(qrow + i * 16, kk * 2 + qch));
+#pragma unroll
+                for (int f = 0; f < NF; f += 2) {
+                    uint32_t bf[4];
+                    const int kr = wn * KW + f * 8 + ((lane >> 4) << 3) + (lane & 7);
+                    ldsm4(bf, ks + chunk_at<D>(kr, kk * 2 + ((lane >> 3) & 1)));
+#pragma unroll
+                    for (int i = 0; i < RM; ++i) {
+                        Mma<T>::run(s[i][f], af[i], bf[0], bf[1]);
+                        Mma<T>::run(s[i][f + 1], af[i], bf[2], bf[3]);
+                    }
+                }
+            }
+            // ---- running maximum, weights and sum
+            const int kbase = k0 + wn * KW + (lane & 3) * 2;
+            const bool edge = p_hi - k0 >= a.window;   // (uniform) below some token's window
+            uint32_t pf[RM][NF / 2][4];
+#pragma unroll
+            for (int i = 0; i < RM; ++i) {
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const int lim = pos[i][j] + 1 - kbase;
+                    float mx = -INFINITY;
+#pragma unroll
+                    for (int f = 0; f < NF; ++f)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            float& y = s[i][f][j * 2 + e];
+                            y = f * 8 + e < lim ? y * a.scale : -INFINITY;
+                        }
+                    if (edge) {
+                        const int low = pos[i][j] - a.window + 1 - kbase, few = a.sinks - kbase;
+#pragma unroll
+                        for (int f = 0; f < NF; ++f)
+#pragma unroll
+                            for (int e = 0; e < 2; ++e)
+                                if (f * 8 + e < low && f * 8 + e >= few) s[i][f][j * 2 + e] = -INFINITY;
+                    }
+#pragma unroll
+                    for (int f = 0; f < NF; ++f) mx = fmaxf(mx, fmaxf(s[i][f][j * 2], s[i][f][j * 2 + 1]));
+                    mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, 1));
+                    mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, 2));
+                    const float mn = fmaxf(mrow[i][j], mx);
+                    const float ms = mn == -INFINITY ? 0.f : mn;
+                    const float alpha = exp2_fast(mrow[i][j] - ms);
+                    mrow[i][j] = mn;
+                    float sum = 0.f;
+#pragma unroll
+                    for (int f = 0; f < NF; ++f)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            float& y = s[i][f][j * 2 + e];
+                            y = exp2_fast(y - ms);
+                            sum += y;
+                        }
+                    lrow[i][j] = lrow[i][j] * alpha + sum;
+                    if (__any_sync(FULL, alpha != 1.f)) {
+#pragma unroll
+                        for (int f = 0; f < D / 8; ++f) {
+                            o[i][f][j * 2] *= alpha;
+                            o[i][f][j * 2 + 1] *= alpha;
+                        }
+                    }
+                }
+                // The weights enter the product in 16 bits, as the matrix instruction takes them, each off by half a
+                // step of the type; their sum stays in 32.  In f16 they are 2^15 larger: half a step down to 2^-29 of
+                // the maximum, 2^-40 of it below.
+                auto weights = [&](int f, int e) { return Mma<T>::pack(s[i][f][e] * UP, s[i][f][e + 1] * UP); };
+#pragma unroll
+                for (int f = 0; f < NF / 2; ++f) {
+                    pf[i][f][0] = weights(2 * f, 0);
+                    pf[i][f][1] = weights(2 * f, 2);
+                    pf[i][f][2] = weights(2 * f + 1, 0);
+                    pf[i][f][3] = weights(2 * f + 1, 2);
+                }
+            }
+            // ---- values
+#pragma unroll
+            for (int f = 0; f < NF / 2; ++f) {
+#pragma unroll
+                for (int d = 0; d < D / 16; ++d) {
+                    uint32_t bf[4];
+                    const int kr = wn * KW + f * 16 + (((lane >> 3) & 1) << 3) + (lane & 7);
+                    ldsm4_t(bf, vs + chunk_at<D>(kr, d * 2 + (lane >> 4)));
+#pragma unroll
+                    for (int i = 0; i < RM; ++i) {
+                        Mma<T>::run(o[i][2 * d], pf[i][f], bf[0], bf[1]);
+                        Mma<T>::run(o[i][2 * d + 1], pf[i][f], bf[2], bf[3]);
+                    }
+                }
+            }
+            put_offsets(t + CSTAGES, ko, vo);
+        }
+
+        // ---- the warps' parts joined through shared memory
+        cp_async_wait<0>();
+        __syncthreads();
+        float* so = reinterpret_cast<float*>(smem);                  // [WN][MT][D]
+        float* sm = so + WN * MT * D;                                // [WN][MT]
+        float* sl = sm + WN * MT;                                    // [WN][MT]
+#pragma unroll
+        for (int i = 0; i < RM; ++i)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const int r = (wm * RM + i) * 16 + j * 8 + (lane >> 2);
+                float l = lrow[i][j];
+                l += __shfl_xor_sync(FULL, l, 1);
+                l += __shfl_xor_sync(FULL, l, 2);
+                if ((lane & 3) == 0) {
+                    sm[wn * MT + r] = mrow[i][j];
+                    sl[wn * MT + r] = l;
+                }
+#pragma unroll
+                for (int f = 0; f < D / 8; ++f)
+                    *reinterpret_cast<float2*>(so + (wn * MT + r) * D + f * 8 + (lane & 3) * 2) =
+                        make_float2(o[i][f][j * 2] * (1.f / UP), o[i][f][j * 2 + 1] * (1.f / UP));
+            }
+        __syncthreads();
+        const int slot = 2 * blockIdx.x + (i0 == 0);   // (a run has two parts at most, one of them from a tile's start)
+        for (int i = tid; i < MT * (D / 4); i += NT) {
+            const int r = i / (D / 4), c = i % (D / 4), row = row0 + r;
+            if (row >= M) continue;
+            float m = -INFINITY;
+#pragma unroll
+            for (int w = 0; w < WN; ++w) m = fmaxf(m, sm[w * MT + r]);
+            const float ms = m == -INFINITY ? 0.f : m;
+            float l = 0.f;
+            float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int w = 0; w < WN; ++w) {
+                const float f = exp2_fast(sm[w * MT + r] - ms);
+                const float4 z = *reinterpret_cast<const float4*>(so + (w * MT + r) * D + c * 4);
+                l += f * sl[w * MT + r];
+                y.x += f * z.x, y.y += f * z.y, y.z += f * z.z, y.w += f * z.w;
+            }
+            const float inv = l == 0.f ? 0.f : 1.f / l;
+            const float lse = l == 0.f ? -INFINITY : m + log2f(l);
+            y = make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv);
+            if (odd_seen) {   // (their weights are positive: exp(s - m) > 0)
+                const int p = x.pos(a, row);
+                for (int t = 0; t < tiles; ++t) {
+                    const int k0 = kt.at(i0 + t);
+                    if (partial(k0)) add_odd<T>(a, table, p, k0, KT, head, c * 4, y);
+                }
+            }
+            const int j = row / a.gs, h = head * a.gs + row % a.gs;
+            if (whole) {
+                T* out = static_cast<T*>(a.out) + (x.q0 + j) * a.os[0] + h * a.os[1] + c * 4;
+                *reinterpret_cast<uint2*>(out) = make_uint2(Mma<T>::pack(y.x, y.y), Mma<T>::pack(y.z, y.w));
+                if (c == 0 && a.lse) a.lse[int64_t(x.q0 + j) * a.Hq + h] = lse * 0.693147180559945309f;
+            } else {
+                const int64_t at = int64_t(slot) * MT + r;
+                *reinterpret_cast<float4*>(a.part_o + at * D + c * 4) = y;
+                if (c == 0) a.part_l[at] = lse;
+            }
+        }
+        if (!whole && i0 == 0 && tid == 0)   // this CTA has the tile's first part and says how many CTAs have one
+            a.split[blockIdx.x] = make_int4(pl.r, head, row0, int((first + kt.n - 1) / run) - int(blockIdx.x) + 1);
+        unit += tiles;
+    }
+}
+
+// ------------------------------------------------------------------ parts joined
+
+// CTA (c, y): rows 16 y .. 16 y + 15 of the tile whose first part CTA c of the launch before has. A warp takes a
+// row at a time, each lane E neighbouring elements.
+template <typename T, int D, int MT>
+__global__ void __launch_bounds__(128) join_chunk_kernel(const ChunkArgs a, const int4* split, const float* part_o, const float* part_l) {
+    constexpr int E = D / 32;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = blockIdx.x;
+    grid_dependency_wait();
+    allow_dependents();
+    const int4 s = split[c];
+    if (s.w == 0) return;
+    const Request x = request(a, s.x);
+    const int M = x.rows(a);
+    // the first part is the one that starts its tile
+    auto slot = [&](int i) { return int64_t(2 * (c + i) + (i == 0)) * MT; };
+    for (int i = warp; i < 16; i += 4) {
+        const int r = blockIdx.y * 16 + i, row = s.z + r;
+        if (row >= M) return;
+        float m = -INFINITY;
+        for (int p = lane; p < s.w; p += 32) m = fmaxf(m, part_l[slot(p) + r]);
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(FULL, m, d));
+        const float ms = m == -INFINITY ? 0.f : m;
+        // (a NaN part makes the sum NaN through its own weight)
+        float l = 0.f, y[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e) y[e] = 0.f;
+#pragma unroll 4
+        for (int p = 0; p < s.w; ++p) {
+            const float f = exp2f(part_l[slot(p) + r] - ms);
+            const float* o = part_o + (slot(p) + r) * D + lane * E;
+            l += f;
+#pragma unroll
+            for (int e = 0; e < E; ++e) y[e] += f * o[e];
+        }
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        const int j = row / a.gs, h = s.y * a.gs + row % a.gs;
+        T* out = static_cast<T*>(a.out) + (x.q0 + j) * a.os[0] + h * a.os[1] + lane * E;
+#pragma unroll
+        for (int e = 0; e < E; e += 2) *reinterpret_cast<uint32_t*>(out + e) = Mma<T>::pack(y[e] * inv, y[e + 1] * inv);
+        if (a.lse && lane == 0) a.lse[int64_t(x.q0 + j) * a.Hq + h] = (l == 0.f ? -INFINITY : m + log2f(l)) * 0.693147180559945309f;
+    }
+}
+
+// ------------------------------------------------------------------ host
+
+template <typename... P, typename... A>
+static fs_status launch_pdl(void (*kernel)(P...), dim3 grid, unsigned block, size_t smem, void* stream, const A&... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(block, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = static_cast<cudaStream_t>(stream);
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
+    return e == cudaSuccess ? FS_OK : cuda_fail(e);
+}
+
+// Tiles and CTAs of a call, and the bytes of its parts.
+struct ChunkPlan {
+    int MT, KT;         // chunk_rows_kernel's tile
+    int grid, least;    // its CTAs; key tiles of a CTA at least
+    size_t part_o, part_l, split, bytes;   // offsets
+};
+
+static size_t add_bytes(size_t& at, size_t n) {
+    const size_t here = at;
+    at += (n + 255) & ~size_t(255);
+    return here;
+}
+
+static ChunkPlan chunk_plan(const fs_paged_kv& c, int N, int R, int Hq, int width, int most, int sms) {
+    ChunkPlan p = {};
+    const int gs = Hq / c.num_heads, D = c.head_dim;
+    // The most query rows that a request can have: all of them.
+    const int64_t rows = int64_t(std::min(most, N)) * gs;
+    p.MT = rows <= FEW ? FEW : 64;
+    p.KT = D == 256 && p.MT == 64 ? 32 : 64;
+    // Three CTAs fit an SM (two with heads of 256); no more than there can be units.
+    p.least = 2;
+    const int64_t tiles = (int64_t(N) * gs + p.MT - 1) / p.MT + R;
+    const int64_t units = tiles * c.num_heads * ((int64_t(width) * c.page_size + p.KT - 1) / p.KT + 2);
+    p.grid = int(std::max<int64_t>(1, std::min<int64_t>(int64_t(sms) * (D == 256 ? 2 : 3), (units + p.least - 1) / p.least)));
+    size_t at = 0;
+    p.part_o = add_bytes(at, size_t(2) * p.grid * p.MT * D * 4);
+    p.part_l = add_bytes(at, size_t(2) * p.grid * p.MT * 4);
+    p.split = add_bytes(at, size_t(p.grid) * sizeof(int4));
+    p.bytes = at;
+    return p;
+}
+
+template <typename T, int D, int MT, int WM, int WN, int RM, int KT>
+static fs_status launch_rows(const ChunkArgs& a, void* stream) {
+    const fs_status st = prepare_kernel(reinterpret_cast<const void*>(chunk_rows_kernel<T, D, MT, WM, WN, RM, KT>));
+    if (st != FS_OK) return st;
+    const fs_status s2 = launch_pdl(chunk_rows_kernel<T, D, MT, WM, WN, RM, KT>, dim3(unsigned(a.grid)), 32 * WM * WN,
+                                    size_t(ChunkSmem<D, MT, KT>::TOTAL), stream, a);
+    if (s2 != FS_OK) return s2;
+    return launch_pdl(join_chunk_kernel<T, D, MT>, dim3(unsigned(a.grid), MT / 16), 128, 0, stream, a,
+                      static_cast<const int4*>(a.split), static_cast<const float*>(a.part_o), static_cast<const float*>(a.part_l));
+}
+
+template <typename T, int D>
+static fs_status run_chunk(ChunkArgs& a, const ChunkPlan& p, void* stream) {
+    if (p.MT == FEW) return launch_rows<T, D, FEW, 1, 4, 1, 64>(a, stream);
+    if constexpr (D == 256) return launch_rows<T, D, 64, 4, 1, 1, 32>(a, stream);
+    else return launch_rows<T, D, 64, 2, 2, 2, 64>(a, stream);
+}
+
+static fs_status check_chunk(const fs_paged_kv* c, int N, int R, int Hq, int width, int most) {
+    if (!c || N < 0 || R < 0 || Hq < 1 || width < 0 || most < 1) return FS_ERR_INVALID_ARG;
+    if (c->num_pages < 0 || c->page_size < 1 || c->num_heads < 1 || c->head_dim < 1) return FS_ERR_INVALID_ARG;
+    if (Hq % c->num_heads != 0) return FS_ERR_INVALID_ARG;
+    if (c->dtype != FS_F32 && c->dtype != FS_BF16 && c->dtype != FS_F16) return FS_ERR_INVALID_ARG;
+    if (c->dtype == FS_F32 || (c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 256)) {
+        set_last_error("chunk attention takes bf16 or f16 and heads of 64, 128 or 256");
+        return FS_ERR_UNSUPPORTED;
+    }
+    const int64_t lim = 0x7fffffff - 4096;
+    if (int64_t(N) * Hq > lim || int64_t(width) * c->page_size > lim) return FS_ERR_UNSUPPORTED;
+    return FS_OK;
+}
+
+}  // namespace fsd
+
+extern "C" {
+
+fs_status fs_paged_chunk_attention_workspace_bytes(const fs_paged_kv* cache, int32_t tokens, int32_t requests,
+                                                   int32_t q_heads, int32_t table_width, int32_t max_queries,
+                                                   size_t* bytes) {
+    using namespace fsd;
+    if (!bytes) return FS_ERR_INVALID_ARG;
+    fs_status st = check_chunk(cache, tokens, requests, q_heads, table_width, max_queries);
+    if (st != FS_OK) return st;
+    *bytes = 0;
+    if (tokens == 0) return FS_OK;
+    int sms = 0;
+    size_t optin = 0;
+    st = device_limits(sms, optin);
+    if (st != FS_OK) return st;
+    *bytes = chunk_plan(*cache, tokens, requests, q_heads, table_width, max_queries, sms).bytes;
+    return FS_OK;
+}
+
+fs_status fs_paged_chunk_attention(const fs_paged_kv* cache, const void* query, const int64_t* query_strides,
+                                   int32_t tokens, int32_t q_heads, const int32_t* page_table, int32_t requests,
+                                   int32_t table_width, const int32_t* query_starts, const int32_t* lens,
+                                   int32_t max_queries, int32_t window, int32_t sinks, float scale, int32_t zero_rest,
+                                   void* out, const int64_t* out_strides, float* out_lse, void* workspace,
+                                   size_t workspace_bytes, void* stream) {
+    using namespace fsd;
+    fs_status st = check_chunk(cache, tokens, requests, q_heads, table_width, max_queries);
+    if (st != FS_OK) return st;
+    if (window < 0 || sinks < 0 || (zero_rest != 0 && zero_rest != 1)) return FS_ERR_INVALID_ARG;
+    if (tokens == 0) return FS_OK;
+    if (!query || !query_strides || !out || !out_strides) return FS_ERR_INVALID_ARG;
+    if (requests > 0 && (!query_starts || !lens || (table_width > 0 && !page_table))) return FS_ERR_INVALID_ARG;
+    if (cache->num_pages > 0 && (!cache->k || !cache->v)) return FS_ERR_INVALID_ARG;
+    ChunkArgs a = {};
+    uintptr_t bits = reinterpret_cast<uintptr_t>(query) | reinterpret_cast<uintptr_t>(out) |
+                     reinterpret_cast<uintptr_t>(cache->k) | reinterpret_cast<uintptr_t>(cache->v) |
+                     reinterpret_cast<uintptr_t>(workspace);
+    for (int i = 0; i < 3; ++i) {
+        a.kc[i] = cache->k_strides[i];
+        a.vc[i] = cache->v_strides[i];
+        bits |= uintptr_t(a.kc[i] * 2) | uintptr_t(a.vc[i] * 2);
+    }
+    for (int i = 0; i < 2; ++i) {
+        a.qs[i] = query_strides[i];
+        a.os[i] = out_strides[i];
+        bits |= uintptr_t(a.qs[i] * 2) | uintptr_t(a.os[i] * 2);
+    }
+    if (bits & 15) {
+        set_last_error("chunk attention needs 16-byte aligned addresses and strides");
+        return FS_ERR_INVALID_ARG;
+    }
+    int sms = 0;
+    size_t optin = 0;
+    st = device_limits(sms, optin);
+    if (st != FS_OK) return st;
+    const ChunkPlan p = chunk_plan(*cache, tokens, requests, q_heads, table_width, max_queries, sms);
+    if (!workspace || workspace_bytes < p.bytes) {
+        set_last_error("chunk attention: the workspace is too small");
+        return FS_ERR_INVALID_ARG;
+    }
+    a.q = query;
+    a.out = out;
+    a.lse = out_lse;
+    a.k = cache->num_pages > 0 ? cache->k : query;   // (without pages an address that nothing is read from)
+    a.v = cache->num_pages > 0 ? cache->v : query;
+    a.num_pages = cache->num_pages;
+    a.page_size = cache->page_size;
+    a.page_shift = -1;
+    for (int s = 0; s < 31; ++s)
+        if (cache->page_size == (1 << s)) a.page_shift = s;
+    a.table = page_table;
+    a.starts = query_starts;
+    a.lens = lens;
+    a.R = requests;
+    a.width = table_width;
+    a.N = tokens;
+    a.Hq = q_heads;
+    a.Hkv = cache->num_heads;
+    a.gs = q_heads / cache->num_heads;
+    a.window = window == 0 ? 0x7fffffff : window;
+    a.sinks = window == 0 ? 0 : sinks;
+    a.scale = scale * 1.44269504088896341f;
+    a.zero_rest = zero_rest;
+    a.rows_upto = 0x7fffffff;
+    a.grid = p.grid;
+    a.least = p.least;
+    unsigned char* ws = static_cast<unsigned char*>(workspace);
+    a.part_o = reinterpret_cast<float*>(ws + p.part_o);
+    a.part_l = reinterpret_cast<float*>(ws + p.part_l);
+    a.split = reinterpret_cast<int4*>(ws + p.split);
+    const int D = cache->head_dim;
+    if (cache->dtype == FS_BF16)
+        return D == 64    ? run_chunk<__nv_bfloat16, 64>(a, p, stream)
+               : D == 128 ? run_chunk<__nv_bfloat16, 128>(a, p, stream)
+                          : run_chunk<__nv_bfloat16, 256>(a, p, stream);
+    return D == 64    ? run_chunk<__half, 64>(a, p, stream)
+           : D == 128 ? run_chunk<__half, 128>(a, p, stream)
+                      : run_chunk<__half, 256>(a, p, stream);
+}
+
+}  // extern "C"

@@ -209,6 +209,12 @@ void apart(const Span& written, const char* name, const Span& other, const char*
     if (shares_memory(written, other)) refuse(std::string(name) + " is written, but shares memory with " + other_name);
 }
 
+// The same for a tensor of another type, by the bytes between first and last.
+void apart_bytes(const Span& written, const char* name, const Span& other, const char* other_name) {
+    if (written.first != written.end && other.first != other.end && written.first < other.end && other.first < written.end)
+        refuse(std::string(name) + " is written, but shares memory with " + other_name);
+}
+
 // There is no backward pass and no forward-mode derivative: either would be lost without a word.
 void no_gradient(std::initializer_list<const at::Tensor*> ts) {
     for (const at::Tensor* t : ts)
@@ -348,10 +354,10 @@ PyObject* from_uniforms(PyObject*, PyObject* const* a, Py_ssize_t n) {
     });
 }
 
-// (key, value, k_cache, v_cache, page_table, positions, rows, rotary_positions, inv_freq, interleaved, query, query_out)
-// -> query_out or None
+// (key, value, k_cache, v_cache, page_table, positions, rows, rotary_positions, inv_freq, interleaved, query, query_out,
+//  query_norm, key_norm, norm_eps) -> query_out or None
 PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
-    if (!arity(n, 12)) return nullptr;
+    if (!arity(n, 15)) return nullptr;
     return guarded([&]() -> PyObject* {
         const fs_paged_kv kv = paged_kv(a[2], a[3]);
         const at::Tensor& cache = *tensor(a[2]);
@@ -387,6 +393,15 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
         } else if (!none(a[11])) {
             refuse("query_out needs a query");
         }
+        const auto* q_norm = flat_ptr<float>(a[12], "query_norm", kv.head_dim, at::kFloat, dev);
+        const auto* k_norm = flat_ptr<float>(a[13], "key_norm", kv.head_dim, at::kFloat, dev);
+        double eps = 0.0;
+        if (q_norm || k_norm) {
+            if (q_norm && !q) refuse("query_norm needs a query");
+            eps = PyFloat_AsDouble(a[14]);
+            if (eps == -1.0 && PyErr_Occurred()) return nullptr;
+            if (!(eps >= 0.0)) refuse("norm_eps must not be negative");
+        }
         const at::Tensor& v_cache = *tensor(a[3]);
         const Span k_span(cache), v_span(v_cache), in_key(key), in_value(value);
         writable(k_span, "k_cache");
@@ -410,8 +425,14 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
                 if (!same_view(in_query, to)) apart(to, "query_out", in_query, "query");
             }
         }
-        no_gradient({&key, &value, &cache, tensor(a[3]), q, tensor(a[11])});
+        no_gradient({&key, &value, &cache, tensor(a[3]), q, tensor(a[11]), tensor(a[12]), tensor(a[13])});
         return launch(cache, [&](void* s) {
+            if (q_norm || k_norm)
+                return fs_append_paged_kv_normed(&kv, key.data_ptr(), ks, value.data_ptr(), vs, tokens,
+                                                 static_cast<const int32_t*>(table.data_ptr()), size32(table.size(0), "the table"),
+                                                 size32(table.size(1), "the table"), rows, pos, rpos, freq, int32_t(rotary),
+                                                 interleaved, q ? q->data_ptr() : nullptr, qs, q_heads, q ? qo.data_ptr() : nullptr,
+                                                 qos, q_norm, k_norm, float(eps), s);
             return fs_append_paged_kv(&kv, key.data_ptr(), ks, value.data_ptr(), vs, tokens,
                                       static_cast<const int32_t*>(table.data_ptr()), size32(table.size(0), "the table"),
                                       size32(table.size(1), "the table"), rows, pos, rpos, freq, int32_t(rotary), interleaved,
@@ -502,6 +523,224 @@ PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
     });
 }
 
+// (lens, new_lens, page_table, free_pages, free_count, page_size, max_tokens)
+// -> (query_starts, rows, positions, totals, free_left)
+PyObject* step_tables(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    if (!arity(n, 7)) return nullptr;
+    return guarded([&]() -> PyObject* {
+        const at::Tensor* t = tensor(a[2]);
+        if (!t || !t->is_cuda()) refuse("page_table must be a CUDA tensor");
+        const auto dev = t->get_device();
+        const at::Tensor& table = flat(a[2], "page_table", {-1, -1}, at::kInt, dev);
+        const int32_t R = size32(table.size(0), "the table"), width = size32(table.size(1), "the table");
+        const at::Tensor& lens = flat(a[0], "lens", {R}, at::kInt, dev);
+        const at::Tensor& fresh = flat(a[1], "new_lens", {R}, at::kInt, dev);
+        const at::Tensor& pages = flat(a[3], "free_pages", {-1}, at::kInt, dev);
+        const at::Tensor& count = flat(a[4], "free_count", {1}, at::kInt, dev);
+        const int64_t page = PyLong_AsLongLong(a[5]), budget = page == -1 && PyErr_Occurred() ? -1 : PyLong_AsLongLong(a[6]);
+        if (PyErr_Occurred()) return nullptr;
+        if (page < 1 || page > INT32_MAX) refuse("page_size must be at least 1");
+        if (budget < 0 || budget > INT32_MAX) refuse("max_tokens must not be negative");
+        const Span to(table);
+        apart(to, "page_table", Span(lens), "lens");
+        apart(to, "page_table", Span(fresh), "new_lens");
+        apart(to, "page_table", Span(pages), "free_pages");
+        apart(to, "page_table", Span(count), "free_count");
+        const c10::DeviceGuard guard(table.device());
+        const auto like = lens.options();
+        at::Tensor starts = at::empty({int64_t(R) + 1}, like), rows = at::empty({budget}, like), pos = at::empty({budget}, like),
+                   totals = at::empty({R}, like), left = at::empty({1}, like);
+        auto in = [](const at::Tensor& x) { return static_cast<const int32_t*>(x.const_data_ptr()); };
+        auto out = [](const at::Tensor& x) { return static_cast<int32_t*>(x.data_ptr()); };
+        return launch(table, [&](void* s) {
+            return fs_paged_step_tables(in(lens), in(fresh), R, out(table), width, in(pages), size32(pages.size(0), "free_pages"),
+                                        in(count), int32_t(page), int32_t(budget), out(starts), out(rows), out(pos), out(totals),
+                                        out(left), s);
+        }, [&]() -> PyObject* {
+            written({&table});
+            PyObject* r = PyTuple_New(5);
+            int i = 0;
+            if (r)
+                for (at::Tensor* x : {&starts, &rows, &pos, &totals, &left}) PyTuple_SET_ITEM(r, i++, wrap(std::move(*x)));
+            return r;
+        });
+    });
+}
+
+// (query, k_cache, v_cache, page_table, query_starts, lens, window, sinks, max_queries, scale, out, return_lse)
+// -> out or (out, lse)
+PyObject* chunk_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    if (!arity(n, 12)) return nullptr;
+    return guarded([&]() -> PyObject* {
+        const fs_paged_kv kv = paged_kv(a[1], a[2]);
+        const at::Tensor& cache = *tensor(a[1]);
+        const auto type = cache.scalar_type();
+        const auto dev = cache.get_device();
+        const at::Tensor& q = vectors(a[0], "query", {-1, -1, kv.head_dim}, type, dev);
+        const c10::DeviceGuard guard(cache.device());
+        at::Tensor out = none(a[10]) ? at::empty(q.sizes(), q.options()) : vectors(a[10], "out", q.sizes(), type, dev);
+        if (!none(a[10])) {
+            const Span to(out), in_query(q);
+            writable(to, "out");
+            apart(to, "out", Span(cache), "k_cache");
+            apart(to, "out", Span(*tensor(a[2])), "v_cache");
+            if (!same_view(in_query, to)) apart(to, "out", in_query, "query");
+        }
+        no_gradient({&q, &cache, tensor(a[2]), tensor(a[10])});
+        const int32_t N = size32(q.size(0), "the number of tokens"), Hq = size32(q.size(1), "the number of heads");
+        if (Hq < 1 || Hq % kv.num_heads != 0) refuse("query must have a multiple of the caches' heads");
+        int64_t qs[2], os[2];
+        strides(q, 2, qs);
+        strides(out, 2, os);
+        const at::Tensor& table = flat(a[3], "page_table", {-1, -1}, at::kInt, dev);
+        const int32_t R = size32(table.size(0), "the table"), width = size32(table.size(1), "the table");
+        const auto* starts = static_cast<const int32_t*>(flat(a[4], "query_starts", {int64_t(R) + 1}, at::kInt, dev).data_ptr());
+        const auto* lens = static_cast<const int32_t*>(flat(a[5], "lens", {R}, at::kInt, dev).data_ptr());
+        // None: no window; every token may be of one request
+        int64_t window = 0, most = std::max(N, 1);
+        if (!none(a[6])) {
+            window = PyLong_AsLongLong(a[6]);
+            if (window == -1 && PyErr_Occurred()) return nullptr;
+            if (window < 1) refuse("window must be at least 1 (None: no window)");
+        }
+        const int64_t sinks = PyLong_AsLongLong(a[7]);
+        if (sinks == -1 && PyErr_Occurred()) return nullptr;
+        if (sinks < 0) refuse("sinks must not be negative");
+        if (!none(a[8])) {
+            most = PyLong_AsLongLong(a[8]);
+            if (most == -1 && PyErr_Occurred()) return nullptr;
+            if (most < 1) refuse("max_queries must be at least 1");
+        }
+        double scale = 1.0 / std::sqrt(double(kv.head_dim));
+        if (!none(a[9])) {
+            scale = PyFloat_AsDouble(a[9]);
+            if (scale == -1.0 && PyErr_Occurred()) return nullptr;
+        }
+        const int want_lse = PyObject_IsTrue(a[11]);
+        if (want_lse < 0) return nullptr;
+        at::Tensor lse;
+        // (what a given out keeps of rows of no request, its lse does not have)
+        if (want_lse) lse = none(a[10]) ? at::empty({N, Hq}, q.options().dtype(at::kFloat))
+                                        : at::full({N, Hq}, -INFINITY, q.options().dtype(at::kFloat));
+        auto clamp32 = [](int64_t x) { return int32_t(std::min<int64_t>(x, INT32_MAX)); };
+        size_t need = 0;
+        const fs_status st = fs_paged_chunk_attention_workspace_bytes(&kv, N, R, Hq, width, clamp32(most), &need);
+        if (st != FS_OK) return PyLong_FromLong(st);
+        const at::Tensor ws = scratch(need, q);
+        return launch(q, [&](void* s) {
+            return fs_paged_chunk_attention(&kv, q.data_ptr(), qs, N, Hq, static_cast<const int32_t*>(table.data_ptr()), R, width, starts,
+                                            lens, clamp32(most), clamp32(window), clamp32(sinks), float(scale), none(a[10]),
+                                            out.data_ptr(), os, want_lse ? static_cast<float*>(lse.data_ptr()) : nullptr,
+                                            ws.data_ptr(), need, s);
+        }, [&]() -> PyObject* {
+            written({tensor(a[10])});
+            if (none(a[10])) return want_lse ? pair(out, lse) : wrap(out);
+            PyObject* o = a[10];
+            if (!want_lse) {
+                Py_INCREF(o);
+                return o;
+            }
+            return PyTuple_Pack(2, o, py_owned(wrap(lse)).p);
+        });
+    });
+}
+
+// (logits, tokens, lens, prompt_lens, repetition, presence, frequency, bias_starts, bias_tokens, bias_values, allowed,
+//  allowed_rows, out) -> out
+PyObject* adjust(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    if (!arity(n, 13)) return nullptr;
+    return guarded([&]() -> PyObject* {
+        const at::Tensor& x = float_cuda(a[0], "logits", 2, 2);
+        const int64_t B = x.size(0), V = x.size(1), stride = B > 1 ? x.stride(0) : V;
+        const auto dev = x.get_device();
+        if (V < 1 || (V > 1 && x.stride(1) != 1) || stride < V)
+            refuse("logits must have at least one column, contiguous columns and rows that do not overlap");
+        const c10::DeviceGuard guard(x.device());
+        at::Tensor out = none(a[12]) ? at::empty({B, V}, x.options()) : vectors(a[12], "out", x.sizes(), x.scalar_type(), dev);
+        const int64_t out_stride = B > 1 ? out.stride(0) : V;
+        if (out_stride < V) refuse("out must have rows that do not overlap");
+        // the history
+        const at::Tensor* tok = nullptr;
+        const int32_t *lens = nullptr, *prompts = nullptr;
+        if (!none(a[1])) {
+            tok = &vectors(a[1], "tokens", {B, -1}, at::kInt, dev);
+            lens = flat_ptr<int32_t>(a[2], "lens", B, at::kInt, dev);
+            prompts = flat_ptr<int32_t>(a[3], "prompt_lens", B, at::kInt, dev);
+        } else {
+            for (int i = 2; i < 7; ++i)
+                if (!none(a[i])) refuse("lens, prompt_lens and penalties need tokens");
+        }
+        const int64_t tok_stride = tok && B > 1 ? tok->stride(0) : tok ? tok->size(1) : 0;
+        if (tok && tok_stride < tok->size(1)) refuse("tokens must have rows that do not overlap");
+        at::Tensor held[3];
+        const float* ps[3] = {};
+        static const char* const names[3] = {"repetition", "presence", "frequency"};
+        for (int i = 0; i < 3; ++i) {
+            PyObject* o = a[4 + i];
+            if (none(o)) continue;
+            if (!tensor(o)) {
+                const double v = PyFloat_AsDouble(o);
+                if (v == -1.0 && PyErr_Occurred()) return nullptr;
+                held[i] = at::full({B}, v, x.options().dtype(at::kFloat));
+                ps[i] = static_cast<const float*>(held[i].data_ptr());
+            } else {
+                ps[i] = static_cast<const float*>(flat(o, names[i], {B}, at::kFloat, dev).data_ptr());
+            }
+        }
+        // biases
+        const bool biased = !none(a[7]);
+        if (biased != !none(a[8]) || biased != !none(a[9])) refuse("bias_starts, bias_tokens and bias_values belong together");
+        int32_t biases = 0;
+        const int32_t *bs = nullptr, *bt = nullptr;
+        const float* bv = nullptr;
+        if (biased) {
+            bs = static_cast<const int32_t*>(flat(a[7], "bias_starts", {B + 1}, at::kInt, dev).data_ptr());
+            const at::Tensor& t = flat(a[8], "bias_tokens", {-1}, at::kInt, dev);
+            biases = size32(t.size(0), "the number of biases");
+            bt = static_cast<const int32_t*>(t.data_ptr());
+            bv = static_cast<const float*>(flat(a[9], "bias_values", {biases}, at::kFloat, dev).data_ptr());
+        }
+        // masks
+        int32_t masks = 0;
+        const uint32_t* allowed = nullptr;
+        const int32_t* mrows = nullptr;
+        if (!none(a[10])) {
+            const at::Tensor& t = flat(a[10], "allowed", {-1, (V + 31) / 32}, at::kInt, dev);
+            masks = size32(t.size(0), "the number of masks");
+            mrows = flat_ptr<int32_t>(a[11], "allowed_rows", B, at::kInt, dev);
+            if (none(a[11]) && masks < B) refuse("allowed needs a mask for every row when allowed_rows is not given");
+            // (no masks at all: every row's is one that does not exist, or none)
+            allowed = masks > 0 ? static_cast<const uint32_t*>(t.const_data_ptr()) : reinterpret_cast<const uint32_t*>(mrows);
+        } else if (!none(a[11])) {
+            refuse("allowed_rows needs allowed");
+        }
+        if (!none(a[12])) {
+            const Span to(out), in(x);
+            writable(to, "out");
+            if (!same_view(in, to)) apart(to, "out", in, "logits");
+            static const char* const others[] = {"tokens", "lens", "prompt_lens", "repetition", "presence", "frequency",
+                                                 "bias_starts", "bias_tokens", "bias_values", "allowed", "allowed_rows"};
+            for (int i = 0; i < 11; ++i)
+                if (const at::Tensor* t = tensor(a[1 + i])) apart_bytes(to, "out", Span(*t), others[i]);
+        }
+        no_gradient({&x, tensor(a[4]), tensor(a[5]), tensor(a[6]), tensor(a[9]), tensor(a[12])});
+        return launch(x, [&](void* s) {
+            const bool hist = tok && tok->size(1) > 0;   // (an empty history penalises nothing)
+            return fs_adjust_logits(x.data_ptr(), dtype_of(x.scalar_type()), stride, size32(B, "the batch"), size32(V, "the vocabulary"),
+                                    hist ? static_cast<const int32_t*>(tok->data_ptr()) : nullptr, tok_stride,
+                                    hist ? size32(tok->size(1), "the history") : 0, hist ? lens : nullptr, hist ? prompts : nullptr,
+                                    hist ? ps[0] : nullptr, hist ? ps[1] : nullptr, hist ? ps[2] : nullptr, biases ? bs : nullptr,
+                                    biases ? bt : nullptr, biases ? bv : nullptr, biases, allowed, masks, mrows, out.data_ptr(),
+                                    out_stride, s);
+        }, [&]() -> PyObject* {
+            written({tensor(a[12])});
+            if (none(a[12])) return wrap(out);
+            Py_INCREF(a[12]);
+            return a[12];
+        });
+    });
+}
+
 // (a, b) -> whether two elements of tensors of one type share memory; of one tensor, with itself.
 PyObject* shares(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (!arity(n, 2)) return nullptr;
@@ -516,6 +755,9 @@ PyMethodDef METHODS[] = {
     {"from_uniforms", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(from_uniforms)), METH_FASTCALL, nullptr},
     {"append", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(append)), METH_FASTCALL, nullptr},
     {"attention", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(attention)), METH_FASTCALL, nullptr},
+    {"step_tables", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(step_tables)), METH_FASTCALL, nullptr},
+    {"chunk_attention", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(chunk_attention)), METH_FASTCALL, nullptr},
+    {"adjust", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(adjust)), METH_FASTCALL, nullptr},
     {"shares_memory", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(shares)), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 

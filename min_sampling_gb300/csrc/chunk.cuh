@@ -34,11 +34,12 @@ struct ChunkArgs {
     float* part_l;              // [2 grid][MT], log2 of each part's sum of 2^score
     int4* split;                // [grid]: request, head, row0, parts; parts 0: none
     // chunk_tensor_kernel's
-    int t_grid, t_tiles;
+    int t_grid, t_tiles, t_least;   // t_grid 0: not launched
     float* t_part_o;            // [2 t_grid][MANY][D]
     float* t_part_l;
     int4* t_split;
-    int4* t_items;              // [t_tiles]: request, row0, units before (low, high word)
+    int4* t_items;              // [t_tiles]: request, row0, units of a key/value head before (low, high word)
+    int* t_first;               // [R + 1]: tiles before a request
     int* t_plan;                // tiles, units (low, high word) of a key/value head
 };
 

@@ -50,6 +50,73 @@ __device__ __forceinline__ int64_t units_of(const ChunkArgs& a, const Request& x
     return n;
 }
 
+// Exclusive sum over a block of NT threads, and the total.
+template <int NT>
+__device__ __forceinline__ int64_t block_sum_before(int64_t mine, int64_t* words, int64_t& total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int64_t x = mine;
+#pragma unroll
+    for (int s = 1; s < 32; s <<= 1) {
+        const int64_t y = __shfl_up_sync(FULL, x, s);
+        if (lane >= s) x += y;
+    }
+    if (lane == 31) words[warp] = x;
+    __syncthreads();
+    int64_t before = 0;
+    total = 0;
+#pragma unroll
+    for (int w = 0; w < NT / 32; ++w) {
+        if (w == warp) before = total;
+        total += words[w];
+    }
+    __syncthreads();
+    return before + x - mine;
+}
+
+// The tensor cores' tiles: MANY query rows of a request each, with the units before them. By one CTA.
+template <int NT>
+__device__ __forceinline__ void plan_tiles(const ChunkArgs& a, int64_t* words) {
+    const int tid = threadIdx.x;
+    auto tiles_of = [&](int r) {
+        const int M = request(a, r).rows(a);
+        return M > a.rows_upto ? (M + MANY - 1) / MANY : 0;
+    };
+    int64_t total, mine = 0;
+    const int per = (a.R + NT - 1) / NT, r0 = min(tid * per, a.R), r1 = min(r0 + per, a.R);
+    for (int r = r0; r < r1; ++r) mine += tiles_of(r);
+    int64_t at = block_sum_before<NT>(mine, words, total);
+    for (int r = r0; r < r1; ++r) {
+        a.t_first[r] = int(min(at, int64_t(a.t_tiles)));
+        at += tiles_of(r);
+    }
+    const int n = int(min(total, int64_t(a.t_tiles)));   // (no more unless query_starts descends)
+    if (tid == 0) a.t_first[a.R] = n;
+    __syncthreads();
+    const int each = (n + NT - 1) / NT, i0 = min(tid * each, n), i1 = min(i0 + each, n);
+    int first = 0;      // the request of tile i0: the last one that has no more than i0 tiles before it
+    for (int hi = a.R; i0 < i1 && hi - first > 1;) {
+        const int mid = (first + hi) / 2;
+        if (a.t_first[mid] <= i0) first = mid;
+        else hi = mid;
+    }
+    auto units = [&](int& r, int i, int& row0) {
+        while (a.t_first[r + 1] <= i) ++r;
+        row0 = (i - a.t_first[r]) * MANY;
+        const Request x = request(a, r);
+        return KeyTiles<128>(a, x.pos(a, row0), x.pos(a, min(row0 + MANY, x.rows(a)) - 1)).n;
+    };
+    mine = 0;
+    int row0;
+    for (int i = i0, r = first; i < i1; ++i) mine += units(r, i, row0);
+    at = block_sum_before<NT>(mine, words, total);
+    for (int i = i0, r = first; i < i1; ++i) {
+        const int u = units(r, i, row0);
+        a.t_items[i] = make_int4(r, row0, int(uint32_t(at)), int(at >> 32));
+        at += u;
+    }
+    if (tid == 0) a.t_plan[0] = n, a.t_plan[1] = int(uint32_t(total)), a.t_plan[2] = int(total >> 32);
+}
+
 // WM x WN warps over a tile of MT = 16 RM WM query rows and KT keys; each warp keeps its own running
 // maximum, sum and output over its share of the keys.  Bound by the reads of keys and values.
 template <typename T, int D, int MT, int WM, int WN, int RM, int KT>
@@ -71,6 +138,14 @@ __global__ void __launch_bounds__(32 * WM * WN) chunk_rows_kernel(const ChunkArg
     grid_dependency_wait();
     allow_dependents();
 
+    if (a.t_grid > 0) {   // one CTA more, the first, for the tensor cores' plan
+        if (blockIdx.x == 0) {
+            plan_tiles<NT>(a, words);
+            return;
+        }
+    }
+    const int cta = int(blockIdx.x) - (a.t_grid > 0);
+
     // ---- this CTA's run of units
     int64_t unit, last, run;
     Place pl;
@@ -78,24 +153,10 @@ __global__ void __launch_bounds__(32 * WM * WN) chunk_rows_kernel(const ChunkArg
         const int per = (a.R + NT - 1) / NT, r0 = min(tid * per, a.R), r1 = min(r0 + per, a.R);
         int64_t mine = 0;
         for (int r = r0; r < r1; ++r) mine += units_of<MT, KT>(a, request(a, r));
-        int64_t x = mine;
-#pragma unroll
-        for (int s = 1; s < 32; s <<= 1) {
-            const int64_t y = __shfl_up_sync(FULL, x, s);
-            if (lane >= s) x += y;
-        }
-        if (lane == 31) words[warp] = x;
-        __syncthreads();
-        int64_t before = 0, total = 0;
-#pragma unroll
-        for (int w = 0; w < NT / 32; ++w) {
-            if (w == warp) before = total;
-            total += words[w];
-        }
-        before += x - mine;
+        int64_t total, before = block_sum_before<NT>(mine, words, total);
         total *= a.Hkv;
         run = max(int64_t(a.least), (total + a.grid - 1) / a.grid);
-        unit = min(blockIdx.x * run, total);
+        unit = min(cta * run, total);
         last = min(unit + run, total);
         if (unit < last && before * a.Hkv <= unit && unit < (before + mine) * a.Hkv) {
             for (int r = r0; r < r1; ++r) {
@@ -107,7 +168,7 @@ __global__ void __launch_bounds__(32 * WM * WN) chunk_rows_kernel(const ChunkArg
                 before += n;
             }
         }
-        if (tid == 0) a.split[blockIdx.x] = make_int4(0, 0, 0, 0);
+        if (tid == 0) a.split[cta] = make_int4(0, 0, 0, 0);
         __syncthreads();
         pl = Place{int(words[16]), unit, words[17], words[18]};
     }
@@ -115,7 +176,7 @@ __global__ void __launch_bounds__(32 * WM * WN) chunk_rows_kernel(const ChunkArg
         // rows of no request
         const int lo = a.R > 0 ? min(max(a.starts[0], 0), a.N) : a.N, hi = a.R > 0 ? max(min(max(a.starts[a.R], 0), a.N), lo) : a.N;
         const int rest = lo + a.N - hi;
-        for (int64_t i = int64_t(blockIdx.x) * NT + tid; i < int64_t(rest) * a.Hq * DC; i += int64_t(gridDim.x) * NT) {
+        for (int64_t i = int64_t(cta) * NT + tid; i < int64_t(rest) * a.Hq * DC; i += int64_t(a.grid) * NT) {
             const int c = int(i % DC), h = int(i / DC % a.Hq), j = int(i / DC / a.Hq), t = j < lo ? j : hi + j - lo;
             *reinterpret_cast<uint4*>(static_cast<T*>(a.out) + t * a.os[0] + h * a.os[1] + c * 8) = make_uint4(0, 0, 0, 0);
             if (c == 0 && a.lse) a.lse[int64_t(t) * a.Hq + h] = -INFINITY;
@@ -386,7 +447,7 @@ __global__ void __launch_bounds__(32 * WM * WN) chunk_rows_kernel(const ChunkArg
                         make_float2(o[i][f][j * 2] * (1.f / UP), o[i][f][j * 2 + 1] * (1.f / UP));
             }
         __syncthreads();
-        const int slot = 2 * blockIdx.x + (i0 == 0);   // (a run has two parts at most, one of them from a tile's start)
+        const int slot = 2 * cta + (i0 == 0);   // (a run has two parts at most, one of them from a tile's start)
         for (int i = tid; i < MT * (D / 4); i += NT) {
             const int r = i / (D / 4), c = i % (D / 4), row = row0 + r;
             if (row >= M) continue;
@@ -425,29 +486,34 @@ __global__ void __launch_bounds__(32 * WM * WN) chunk_rows_kernel(const ChunkArg
             }
         }
         if (!whole && i0 == 0 && tid == 0)   // this CTA has the tile's first part and says how many CTAs have one
-            a.split[blockIdx.x] = make_int4(pl.r, head, row0, int((first + kt.n - 1) / run) - int(blockIdx.x) + 1);
+            a.split[cta] = make_int4(pl.r, head, row0, int((first + kt.n - 1) / run) - cta + 1);
         unit += tiles;
     }
 }
 
 // ------------------------------------------------------------------ parts joined
 
-// CTA (c, y): rows 16 y .. 16 y + 15 of the tile whose first part CTA c of the launch before has. A warp takes a
-// row at a time, each lane E neighbouring elements.
-template <typename T, int D, int MT>
-__global__ void __launch_bounds__(128) join_chunk_kernel(const ChunkArgs a, const int4* split, const float* part_o, const float* part_l) {
+// 16 rows of a tile that was cut; `ys` CTAs for the tile whose first part CTA c of chunk_rows_kernel has, then as many
+// as it takes for each of the tensor cores'.  A warp takes a row at a time, each lane E neighbouring elements.
+template <typename T, int D>
+__global__ void __launch_bounds__(128) join_chunk_kernel(const ChunkArgs a, int ys) {
     constexpr int E = D / 32;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = blockIdx.x;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const bool few = int(blockIdx.x) < a.grid * ys;
+    const int b = int(blockIdx.x) - (few ? 0 : a.grid * ys), per = few ? ys : MANY / 16;
+    const int c = b / per, y16 = (b - c * per) * 16, MT = per * 16;
+    const float* part_o = few ? a.part_o : a.t_part_o;
+    const float* part_l = few ? a.part_l : a.t_part_l;
     grid_dependency_wait();
     allow_dependents();
-    const int4 s = split[c];
+    const int4 s = (few ? a.split : a.t_split)[c];
     if (s.w == 0) return;
     const Request x = request(a, s.x);
     const int M = x.rows(a);
     // the first part is the one that starts its tile
     auto slot = [&](int i) { return int64_t(2 * (c + i) + (i == 0)) * MT; };
     for (int i = warp; i < 16; i += 4) {
-        const int r = blockIdx.y * 16 + i, row = s.z + r;
+        const int r = y16 + i, row = s.z + r;
         if (row >= M) return;
         float m = -INFINITY;
         for (int p = lane; p < s.w; p += 32) m = fmaxf(m, part_l[slot(p) + r]);
@@ -498,6 +564,8 @@ struct ChunkPlan {
     int MT, KT;         // chunk_rows_kernel's tile
     int grid, least;    // its CTAs; key tiles of a CTA at least
     size_t part_o, part_l, split, bytes;   // offsets
+    int t_grid, t_least, t_tiles;          // the tensor cores' CTAs (0: not launched)
+    size_t t_part_o, t_part_l, t_split, t_items, t_first, t_plan;
 };
 
 static size_t add_bytes(size_t& at, size_t n) {
@@ -511,7 +579,8 @@ static ChunkPlan chunk_plan(const fs_paged_kv& c, int N, int R, int Hq, int widt
     const int gs = Hq / c.num_heads, D = c.head_dim;
     // The most query rows that a request can have: all of them.
     const int64_t rows = int64_t(std::min(most, N)) * gs;
-    p.MT = rows <= FEW ? FEW : 64;
+    const bool tensor = D <= 128 && rows > FEW;
+    p.MT = rows <= FEW || tensor ? FEW : 64;
     p.KT = D == 256 && p.MT == 64 ? 32 : 64;
     // Three CTAs fit an SM (two with heads of 256); no more than there can be units.
     p.least = 2;
@@ -522,6 +591,20 @@ static ChunkPlan chunk_plan(const fs_paged_kv& c, int N, int R, int Hq, int widt
     p.part_o = add_bytes(at, size_t(2) * p.grid * p.MT * D * 4);
     p.part_l = add_bytes(at, size_t(2) * p.grid * p.MT * 4);
     p.split = add_bytes(at, size_t(p.grid) * sizeof(int4));
+    if (tensor) {
+        // One CTA per SM.  A request of FEW rows or less has no tile there.
+        const int64_t all = int64_t(N) * gs;
+        p.t_least = 2;
+        p.t_tiles = int(std::min<int64_t>(all / MANY + std::min<int64_t>(R, all / (FEW + 1) + 1), 0x7fffffff));
+        const int64_t t_units = int64_t(p.t_tiles) * c.num_heads * ((int64_t(width) * c.page_size + 127) / 128 + 2);
+        p.t_grid = int(std::max<int64_t>(1, std::min<int64_t>(sms, (t_units + p.t_least - 1) / p.t_least)));
+        p.t_part_o = add_bytes(at, size_t(2) * p.t_grid * MANY * D * 4);
+        p.t_part_l = add_bytes(at, size_t(2) * p.t_grid * MANY * 4);
+        p.t_split = add_bytes(at, size_t(p.t_grid) * sizeof(int4));
+        p.t_items = add_bytes(at, size_t(p.t_tiles) * sizeof(int4));
+        p.t_first = add_bytes(at, (size_t(R) + 1) * 4);
+        p.t_plan = add_bytes(at, 16);
+    }
     p.bytes = at;
     return p;
 }
@@ -530,18 +613,20 @@ template <typename T, int D, int MT, int WM, int WN, int RM, int KT>
 static fs_status launch_rows(const ChunkArgs& a, void* stream) {
     const fs_status st = prepare_kernel(reinterpret_cast<const void*>(chunk_rows_kernel<T, D, MT, WM, WN, RM, KT>));
     if (st != FS_OK) return st;
-    const fs_status s2 = launch_pdl(chunk_rows_kernel<T, D, MT, WM, WN, RM, KT>, dim3(unsigned(a.grid)), 32 * WM * WN,
-                                    size_t(ChunkSmem<D, MT, KT>::TOTAL), stream, a);
-    if (s2 != FS_OK) return s2;
-    return launch_pdl(join_chunk_kernel<T, D, MT>, dim3(unsigned(a.grid), MT / 16), 128, 0, stream, a,
-                      static_cast<const int4*>(a.split), static_cast<const float*>(a.part_o), static_cast<const float*>(a.part_l));
+    return launch_pdl(chunk_rows_kernel<T, D, MT, WM, WN, RM, KT>, dim3(unsigned(a.grid + (a.t_grid > 0))), 32 * WM * WN,
+                      size_t(ChunkSmem<D, MT, KT>::TOTAL), stream, a);
 }
 
 template <typename T, int D>
-static fs_status run_chunk(ChunkArgs& a, const ChunkPlan& p, void* stream) {
-    if (p.MT == FEW) return launch_rows<T, D, FEW, 1, 4, 1, 64>(a, stream);
-    if constexpr (D == 256) return launch_rows<T, D, 64, 4, 1, 1, 32>(a, stream);
-    else return launch_rows<T, D, 64, 2, 2, 2, 64>(a, stream);
+static fs_status run_chunk(ChunkArgs& a, const ChunkPlan& p, int dtype, void* stream) {
+    fs_status st;
+    if (p.MT == FEW) st = launch_rows<T, D, FEW, 1, 4, 1, 64>(a, stream);
+    else if constexpr (D == 256) st = launch_rows<T, D, 64, 4, 1, 1, 32>(a, stream);
+    else st = FS_ERR_INVALID_ARG;   // (heads of up to 128 go to the tensor cores)
+    if (st == FS_OK && a.t_grid > 0) st = launch_chunk_tensor(a, dtype, D, stream);
+    if (st != FS_OK) return st;
+    return launch_pdl(join_chunk_kernel<T, D>, dim3(unsigned(a.grid * (p.MT / 16) + a.t_grid * (MANY / 16))), 128, 0, stream, a,
+                      p.MT / 16);
 }
 
 static fs_status check_chunk(const fs_paged_kv* c, int N, int R, int Hq, int width, int most) {
@@ -643,21 +728,32 @@ fs_status fs_paged_chunk_attention(const fs_paged_kv* cache, const void* query, 
     a.sinks = window == 0 ? 0 : sinks;
     a.scale = scale * 1.44269504088896341f;
     a.zero_rest = zero_rest;
-    a.rows_upto = 0x7fffffff;
+    a.rows_upto = p.t_grid > 0 ? FEW : 0x7fffffff;
     a.grid = p.grid;
     a.least = p.least;
     unsigned char* ws = static_cast<unsigned char*>(workspace);
     a.part_o = reinterpret_cast<float*>(ws + p.part_o);
     a.part_l = reinterpret_cast<float*>(ws + p.part_l);
     a.split = reinterpret_cast<int4*>(ws + p.split);
-    const int D = cache->head_dim;
-    if (cache->dtype == FS_BF16)
-        return D == 64    ? run_chunk<__nv_bfloat16, 64>(a, p, stream)
-               : D == 128 ? run_chunk<__nv_bfloat16, 128>(a, p, stream)
-                          : run_chunk<__nv_bfloat16, 256>(a, p, stream);
-    return D == 64    ? run_chunk<__half, 64>(a, p, stream)
-           : D == 128 ? run_chunk<__half, 128>(a, p, stream)
-                      : run_chunk<__half, 256>(a, p, stream);
+    a.t_grid = p.t_grid;
+    a.t_least = p.t_least;
+    a.t_tiles = p.t_tiles;
+    if (p.t_grid > 0) {
+        a.t_part_o = reinterpret_cast<float*>(ws + p.t_part_o);
+        a.t_part_l = reinterpret_cast<float*>(ws + p.t_part_l);
+        a.t_split = reinterpret_cast<int4*>(ws + p.t_split);
+        a.t_items = reinterpret_cast<int4*>(ws + p.t_items);
+        a.t_first = reinterpret_cast<int*>(ws + p.t_first);
+        a.t_plan = reinterpret_cast<int*>(ws + p.t_plan);
+    }
+    const int D = cache->head_dim, dt = cache->dtype;
+    if (dt == FS_BF16)
+        return D == 64    ? run_chunk<__nv_bfloat16, 64>(a, p, dt, stream)
+               : D == 128 ? run_chunk<__nv_bfloat16, 128>(a, p, dt, stream)
+                          : run_chunk<__nv_bfloat16, 256>(a, p, dt, stream);
+    return D == 64    ? run_chunk<__half, 64>(a, p, dt, stream)
+           : D == 128 ? run_chunk<__half, 128>(a, p, dt, stream)
+                      : run_chunk<__half, 256>(a, p, dt, stream);
 }
 
 }  // extern "C"

@@ -65,6 +65,7 @@ template <int KT>
 struct KeyTiles {
     int lo, hi, sink;
     int few, skip, n;           // tiles before the gap, first tile behind it, tiles (at least 1)
+    KeyTiles() = default;
     __device__ __forceinline__ KeyTiles(const ChunkArgs& a, int p_lo, int p_hi) {
         hi = max(p_hi + 1, 0);
         lo = max(0, max(p_lo, 0) - a.window + 1);
@@ -117,6 +118,18 @@ __device__ __noinline__ void add_odd(const ChunkArgs& a, const int* table, int p
         };
         y = make_float4(y.x + odd(0), y.y + odd(1), y.z + odd(2), y.w + odd(3));
     }
+}
+
+// Which of the keys k0 .. k0 + 31 of request r have no page (within what its table can name).
+static __device__ __noinline__ unsigned missing_pages(const ChunkArgs& a, int r, int k0) {
+    unsigned bits = 0;
+    for (int e = 0; e < 32; ++e) {
+        const int pi = (k0 + e) / a.page_size;
+        if (pi >= a.width) break;
+        const int page = a.table[int64_t(r) * a.width + pi];
+        if (page < 0 || page >= a.num_pages) bits |= 1u << e;
+    }
+    return bits;
 }
 
 // The tensor cores' part (chunk_tensor.cu): requests of more than rows_upto query rows, for heads of 64 or 128.

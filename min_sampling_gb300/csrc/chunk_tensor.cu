@@ -8,12 +8,25 @@
 // Roles of the 16 warps:
 //   warps 0-3, 4-7  softmax of tile 0 / tile 1, one thread per row: maximum, weights, sum; O is rescaled
 //                   only when a maximum grows by more than 2^GROWTH; at the end the row's output
-//   warps 8-11      keys and values: page look-ups and 16-byte asynchronous copies into a ring of
-//                   swizzled tiles (any page size and strides)
+//   warps 8, 9      keys, half a tile each; warps 10, 11 values: page look-ups and copies into a ring of swizzled tiles
 //   warps 12, 13    issue the first and the second product
+//   warp 14         what the next tiles are, into a ring that all roles read
+//   warp 15         queries of the next tile, as soon as the last product that reads the old ones is done
 // While one tile's softmax runs, the tensor cores have the other tile's products. (Keys 128 at a time and
 // not 64: the first product reads both operands from shared memory, at 64 keys 48 cycles an instruction of
 // 32, at 128 as many as it takes.)
+//
+// Copies go by TMA (GATHER).  Key tiles of which every key is there are boxes of up to 64 slots of a page, for pages of
+// 8, 16, 32 ... slots.  The others, and all of other page sizes, are gathers of four rows: caches and queries are
+// matrices whose rows lie a common divisor of their strides apart, so any page size and order of slots and heads is
+// a list of row numbers, and a key that no query sees is a row outside, which reads as zeros.  (A gather
+// of 512 bytes takes the copy engine about 33 cycles, 4250 for the keys and values of 128.)  Where the
+// strides have no such divisor, 16-byte asynchronous copies.
+//
+// The softmax's code is short loops over 32 scores, read from tensor memory once for the maximum and once for
+// the weights: with 128 scores in registers and everything unrolled the warps of the other roles and the two tiles'
+// kept throwing one another out of the instruction cache (6700 cycles for 256 rows and 128 keys). What
+// is rare (keys not seen, negative scales, huge scores) is done to the scores in tensor memory first.
 //
 // One CTA per SM takes an equal run of units (key tiles) of the launch's line of work, see chunk_attention.cu; all
 // roles walk the run's tiles at their own pace, so keys of the next tile are on their way while one is finished.
@@ -22,11 +35,30 @@
 #include "chunk.cuh"
 #include "tensor_core.cuh"
 
+#include <numeric>
+
+#include <cuda.h>
+
 namespace fsd {
 
 constexpr int CM = 128;         // query rows of a tile of one warpgroup
 constexpr int CK = 128;         // keys per tile
 constexpr int CNT = 512;        // threads
+constexpr int AHEAD = 4;        // tiles that are described ahead
+
+// The part of a query tile that lies in a CTA's run: n key tiles (0: no more), i0 on, of one key/value head.
+struct Segment {
+    int n, r, row0, head, i0, M;
+    int whole, parts;           // all of the tile's keys; the CTAs that have a part of it (of its first part)
+    Request x;
+    KeyTiles<CK> kt;
+    int p_lo, p_hi;             // positions of the first and last token
+    __device__ __forceinline__ bool two() const { return M - row0 > CM; }   // rows for the second tile
+    // Key tile of which some token of the query tile does not see all the keys that are loaded.
+    __device__ __forceinline__ bool partial(const ChunkArgs& a, int k0) const {
+        return p_lo != p_hi && (k0 + CK > p_lo + 1 || (p_hi - k0 >= a.window && k0 + CK > a.sinks));
+    }
+};
 
 template <int D>
 struct ChunkTensorSmem {
@@ -34,8 +66,18 @@ struct ChunkTensorSmem {
     static constexpr int STAGES = D == 128 ? 5 : 11;
     static constexpr int KV = 2 * QTILE;
     static constexpr int BARS = KV + STAGES * TILE;
-    static constexpr int WORDS = BARS + 16 * STAGES + 12 * 8;
-    static constexpr int TOTAL = WORDS + 32 + 1024;   // 1024: the base's alignment
+    static constexpr int NBARS = 2 * STAGES + 16 + 2 * AHEAD;
+    static constexpr int SEGS = BARS + NBARS * 8;
+    static constexpr int WORDS = SEGS + AHEAD * int(sizeof(Segment));
+    static constexpr int TOTAL = WORDS + 160 + 1024;   // 1024: the base's alignment
+};
+
+// Matrices of which the copies gather rows: row numbers of a page, a slot, a head (a token, a head).
+struct ChunkMaps {
+    CUtensorMap k, v, q;
+    int ks[3], vs[3], qs[2];
+    int box;                    // rows of a box, 0: gathers only
+    CUtensorMap kbox, vbox;     // [pages][heads][slots][dim]
 };
 
 // Two floats at a time.
@@ -48,47 +90,29 @@ __device__ __forceinline__ void add_pair(float& x, float& y, float a, float b) {
         : "+f"(x), "+f"(y) : "f"(a), "f"(b));
 }
 
-// ------------------------------------------------------------------ a run's tiles
-
-// The part of a query tile that lies in a CTA's run: key tiles i0 .. i1 - 1 of one key/value head.
-struct Segment {
-    Request x;
-    KeyTiles<CK> kt;
-    int64_t end;            // the query tile's last unit, all heads, plus one
-    int r, row0, head, i0, i1, M;
-    __device__ __forceinline__ Segment(const ChunkArgs& a, int tile, int64_t unit, int64_t last)
-        : Segment(a, a.t_items[tile], unit, last) {}
-    __device__ __forceinline__ Segment(const ChunkArgs& a, int4 it, int64_t unit, int64_t last)
-        : x(request(a, it.x)), kt(a, x.pos(a, it.y), x.pos(a, min(it.y + MANY, x.rows(a)) - 1)), r(it.x), row0(it.y), M(x.rows(a)) {
-        const int64_t before = (int64_t(it.w) << 32 | uint32_t(it.z)) * a.Hkv, rel = unit - before;
-        end = before + int64_t(kt.n) * a.Hkv;
-        head = int(rel / kt.n);
-        i0 = int(rel - int64_t(head) * kt.n);
-        i1 = int(min(int64_t(kt.n), i0 + (last - unit)));
-    }
-    __device__ __forceinline__ int tiles() const { return i1 - i0; }
-    __device__ __forceinline__ bool two() const { return M - row0 > CM; }   // rows for the second tile
-    // Key tile of which some token of the query tile does not see all the keys that are loaded.
-    __device__ __forceinline__ bool partial(const ChunkArgs& a, int k0) const {
-        const int p_lo = x.pos(a, row0), p_hi = x.pos(a, min(row0 + MANY, M) - 1);
-        return p_lo != p_hi && (k0 + CK > p_lo + 1 || (p_hi - k0 >= a.window && k0 + CK > a.sinks));
-    }
-};
+// Four rows of 64 elements from element x of each on, into 512 bytes of a swizzled tile.
+__device__ __forceinline__ void gather4(uint32_t dst, const CUtensorMap* map, int x, const int (&row)[4], uint32_t bar) {
+    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5, %6}], [%7];"
+                 ::"r"(dst), "l"(map), "r"(x), "r"(row[0]), "r"(row[1]), "r"(row[2]), "r"(row[3]), "r"(bar) : "memory");
+}
+// A box of a page's slots, 64 elements of each.
+__device__ __forceinline__ void copy_box(uint32_t dst, const CUtensorMap* map, int x, int slot, int head, int page, uint32_t bar) {
+    asm volatile("cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];"
+                 ::"r"(dst), "l"(map), "r"(x), "r"(slot), "r"(head), "r"(page), "r"(bar) : "memory");
+}
+__device__ __forceinline__ void bar_expect(uint32_t bar, uint32_t bytes) {
+    asm volatile("{ .reg .b64 t; mbarrier.arrive.expect_tx.shared::cta.b64 t, [%0], %1; }" ::"r"(bar), "r"(bytes) : "memory");
+}
 
 // Copies of a segment of n key tiles, in the order in which the products need them: keys one tile ahead
-// of values.  The key tile of copy c, negated (less one) for its values; and the inverse.
-__device__ __forceinline__ int copy_of(int c, int n) {
-    if (c == 0) return 0;
-    if (c == 2 * n - 1) return -n;
-    return c & 1 ? (c + 1) >> 1 : -(c >> 1);
-}
+// of values.
 __device__ __forceinline__ int keys_copy(int i) { return i == 0 ? 0 : 2 * i - 1; }
 __device__ __forceinline__ int values_copy(int i, int n) { return i == n - 1 ? 2 * n - 1 : 2 * i + 2; }
 
 // ------------------------------------------------------------------ the kernel
 
-template <typename T, int D>
-__global__ void __launch_bounds__(CNT, 1) chunk_tensor_kernel(const ChunkArgs a) {
+template <typename T, int D, bool GATHER>
+__global__ void __launch_bounds__(CNT, 1) chunk_tensor_kernel(const ChunkArgs a, const __grid_constant__ ChunkMaps maps) {
     using S = ChunkTensorSmem<D>;
     using W = Weights<T>;
     constexpr int ST = S::STAGES, DC = D / 8;
@@ -96,14 +120,17 @@ __global__ void __launch_bounds__(CNT, 1) chunk_tensor_kernel(const ChunkArgs a)
     const uint32_t base = (smem_u32(raw) + 1023) & ~1023u;
     unsigned char* mem = raw + (base - smem_u32(raw));
     const int tid = threadIdx.x, warp = __shfl_sync(FULL, tid >> 5, 0), lane = tid & 31;
-    // barriers: full[ST], empty[ST]; of each tile: queries there, scores there, weights there (in two
-    // halves), product P V done; of each product, all done when a wait ran out.  Then the tensor memory's
-    // address, a flag and, for four segments, whose values had infinities taken out
-    const uint32_t full = base + S::BARS, empty = full + 8 * ST, qbar = empty + 8 * ST, sbar = qbar + 16, pbar = sbar + 16,
-                   vbar = pbar + 32, xbar = vbar + 16;
+    // barriers: full[ST], empty[ST]; of each tile: queries there, queries done with, scores there, weights there
+    // (in two halves), product P V done; of each product, all done when a wait ran out; of each half of a value
+    // tile, landed; segments there, done with [AHEAD].  Then the segments, the tensor memory's address, a
+    // flag, whose values had infinities taken out (four segments), which half key tiles miss pages (of sixteen tiles).
+    const uint32_t full = base + S::BARS, empty = full + 8 * ST, qbar = empty + 8 * ST, qfree = qbar + 16, sbar = qfree + 16,
+                   pbar = sbar + 16, vbar = pbar + 32, xbar = vbar + 16, land = xbar + 16, segbar = land + 16, segfree = segbar + 8 * AHEAD;
     volatile int* words = reinterpret_cast<volatile int*>(mem + S::WORDS);
     volatile int* dead = words + 1;
     volatile int* odd = words + 2;      // [4]
+    volatile int* missing = words + 8;  // [16][2]
+    Segment* segs = reinterpret_cast<Segment*>(mem + S::SEGS);
     grid_dependency_wait();
     allow_dependents();
 
@@ -111,9 +138,9 @@ __global__ void __launch_bounds__(CNT, 1) chunk_tensor_kernel(const ChunkArgs a)
     const int n_tiles = a.t_plan[0];
     const int64_t total = (int64_t(a.t_plan[2]) << 32 | uint32_t(a.t_plan[1])) * a.Hkv;
     const int64_t run = max(int64_t(a.t_least), (total + a.t_grid - 1) / a.t_grid);
-    const int64_t unit = min(blockIdx.x * run, total), last = min(unit + run, total);
+    const int64_t first_unit = min(blockIdx.x * run, total), last = min(first_unit + run, total);
     if (tid == 0) a.t_split[blockIdx.x] = make_int4(0, 0, 0, 0);
-    if (unit >= last) return;
+    if (first_unit >= last) return;
     for (int i = tid; i < n_tiles; i += CNT) {
         const int4 it = a.t_items[i];
         const int64_t before = (int64_t(it.w) << 32 | uint32_t(it.z)) * a.Hkv;
@@ -122,12 +149,16 @@ __global__ void __launch_bounds__(CNT, 1) chunk_tensor_kernel(const ChunkArgs a)
             const int4 up = a.t_items[i + 1];
             next = (int64_t(up.w) << 32 | uint32_t(up.z)) * a.Hkv;
         }
-        if (before <= unit && unit < next) words[6] = i;
+        if (before <= first_unit && first_unit < next) words[6] = i;
     }
     if (warp == 13) {
-        if (lane < ST) bar_init(full + 8 * lane, 1), bar_init(empty + 8 * lane, 1);
-        if (lane < 2) bar_init(qbar + 8 * lane, 128), bar_init(sbar + 8 * lane, 1), bar_init(vbar + 8 * lane, 1), bar_init(xbar + 8 * lane, 1);
-        if (lane < 4) bar_init(pbar + 8 * lane, 128), odd[lane] = 0;
+        if (lane < ST) bar_init(full + 8 * lane, 2), bar_init(empty + 8 * lane, 1);
+        if (lane < 2) {
+            bar_init(qbar + 8 * lane, 1), bar_init(qfree + 8 * lane, 1), bar_init(sbar + 8 * lane, 1);
+            bar_init(vbar + 8 * lane, 1), bar_init(xbar + 8 * lane, 1), bar_init(land + 8 * lane, 1);
+        }
+        // (a segment is read by four copying warps, two that issue products, the queries' and eight of the softmax)
+        if (lane < AHEAD) bar_init(pbar + 8 * lane, 128), odd[lane] = 0, bar_init(segbar + 8 * lane, 1), bar_init(segfree + 8 * lane, 15);
         if (lane == 0) *dead = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -139,273 +170,332 @@ __global__ void __launch_bounds__(CNT, 1) chunk_tensor_kernel(const ChunkArgs a)
     __syncthreads();
     tmem_fence_after();
     const uint32_t tmem = __shfl_sync(FULL, uint32_t(words[0]), 0);
-    int tile = __shfl_sync(FULL, words[6], 0);
 
-    // Registers: 128 a thread at launch (512 threads); 200 for the softmax's two warpgroups and 56 for the
-    // other two are the same total.
+    // The s-th segment, once it is described; and given back, by each warp.
+    auto next_segment = [&](uint32_t s, bool& ok) -> const Segment& {
+        ok = ok && __all_sync(FULL, bar_wait(segbar + 8 * (s % AHEAD), (s / AHEAD) & 1, dead));
+        return segs[s % AHEAD];
+    };
+    auto give_back = [&](uint32_t s) {
+        __syncwarp();
+        if (lane == 0) bar_arrive(segfree + 8 * (s % AHEAD));
+    };
+
     if (warp >= 8 && warp < 12) {
-        // ================================================ keys and values
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
-        // Each warp copies every fourth tile: its waits, fence and look-ups cost one warp.
-        const int w = warp - 8;
-        uint32_t seq = 0;        // copies before the segment
-        int before = -1;         // the stage of the copies that are still to be handed over
-        int st = w;
-        uint32_t lap = 0;
+        // ================================================ keys (warps 8, 9) and values (10, 11), half a tile each
+        const bool value = warp >= 10;
+        const int half = warp & 1, quad = lane & 15, row = half * 64 + quad * 4, block = lane >> 4;
+        const int64_t* str = value ? a.vc : a.kc;
+        const int* step = value ? maps.vs : maps.ks;
+        const CUtensorMap* map = value ? &maps.v : &maps.k;
+        uint32_t seq = 0, unit = 0, landed = 0;   // copies and key tiles before the segment; value tiles looked through
         bool ok = true;
-        int segment = 0;
-        bool check = false;      // the copies to be handed over are values that not every query sees: looked through
-        int check_segment = 0;
-        auto hand_over = [&]() {
-            if (check) {
-                unsigned char* tb = mem + S::KV + before * S::TILE;
-                __syncwarp();
-                bool any = false;
-#pragma unroll 4
-                for (int i = lane; i < CK * DC; i += 32) any |= odd_words<T>(*reinterpret_cast<const uint4*>(tb + i * 16));
-                if (__any_sync(FULL, any)) {
-                    for (int i = lane; i < CK * DC; i += 32) {
-                        uint4* p = reinterpret_cast<uint4*>(tb + i * 16);
-                        *p = even_words<T>(*p);
-                    }
-                    odd[check_segment & 3] = check_segment + 1;
-                }
-            }
-            proxy_fence();
-            __syncwarp();
-            if (lane == 0) bar_arrive(full + 8 * before);
-        };
-#pragma unroll 1
-        for (int64_t u = unit; u < last && ok; ++segment) {
-            const Segment sg(a, tile, u, last);
-            const int n = sg.tiles();
+        for (uint32_t s = 0;; ++s) {
+            const Segment& sg = next_segment(s, ok);
+            if (!ok) break;
+            const int n = sg.n, i0 = sg.i0, head = sg.head;
+            if (n == 0) break;
+            const KeyTiles<CK> kt = sg.kt;
             const int* table = a.table + int64_t(sg.r) * a.width;
-            // The page of a key; -1 for one that no query of the tile sees, -2 for one that does not exist.
-            auto page_of = [&](int key) {
-                if (!sg.kt.seen(key)) return -1;
-                const int page = table[a.page_shift >= 0 ? key >> a.page_shift : key / a.page_size];
-                return page >= 0 && page < a.num_pages ? page : -2;
-            };
-            auto first_key = [&](int c) {
-                const int i = copy_of(c, n);
-                return sg.kt.at(sg.i0 + (i < 0 ? -1 - i : i));
-            };
-            int pg[CK / 32];
-            int c = int((w - seq) & 3);
-            auto look_up = [&](int c) {
-                if (c >= 2 * n) return;
-                const int key = first_key(c) + lane;
+            // The pages of this lane's four keys of a tile; -1 for a key that no query of the tile sees, -2 for a
+            // page that does not exist.
+            int pg[4];
+            auto look_up = [&](int i) {
+                if (i >= n) return;
+                const int key = kt.at(i0 + i) + row;
+                const bool one = a.page_shift >= 2;   // four keys of one page
+                int page = -1;
 #pragma unroll
-                for (int h = 0; h < CK / 32; ++h) pg[h] = page_of(key + 32 * h);
-            };
-            look_up(c);
-#pragma unroll 1
-            for (; c < 2 * n; c += 4) {
-                const bool value = copy_of(c, n) < 0;
-                const int k0 = first_key(c);
-                if (lap > 0) {
-                    // (what this warp has copied may be what the stage waits for)
-                    if (before >= 0 && !__all_sync(FULL, bar_test(empty + 8 * st, (lap - 1) & 1))) {
-                        cp_async_wait<0>();
-                        hand_over();
-                        before = -1;
+                for (int j = 0; j < 4; ++j) {
+                    if (j == 0 || !one) {
+                        const int pi = a.page_shift >= 0 ? (key + j) >> a.page_shift : (key + j) / a.page_size;
+                        page = pi < a.width ? table[pi] : -2;
+                        if (page < 0 || page >= a.num_pages) page = -2;
                     }
-                    if (!__all_sync(FULL, bar_wait(empty + 8 * st, (lap - 1) & 1, dead))) {
-                        ok = false;
-                        break;
-                    }
+                    pg[j] = kt.seen(key + j) ? page : -1;
                 }
-                const int64_t* str = value ? a.vc : a.kc;
-                const T* src = static_cast<const T*>(value ? a.v : a.k) + sg.head * str[2];
+            };
+            look_up(0);
+#pragma unroll 1
+            for (int i = 0; i < n; ++i) {
+                const int k0 = kt.at(i0 + i);
+                const uint32_t c = seq + (value ? values_copy(i, n) : keys_copy(i)), lap = c / ST, st = c - lap * ST;
+                if (lap > 0 && !__all_sync(FULL, bar_wait(empty + 8 * st, (lap - 1) & 1, dead))) {
+                    ok = false;
+                    break;
+                }
+                // Which keys' pages do not exist: their scores are NaN for every query that sees them.
+                const bool gone = pg[0] == -2 || pg[1] == -2 || pg[2] == -2 || pg[3] == -2;
+                if (!value) {
+                    const int any = __any_sync(FULL, gone);
+                    if (lane == 0) missing[2 * ((unit + i) & 15) + half] = any;
+                }
                 const uint32_t dst = base + S::KV + st * S::TILE;
-                bool missing = false;
-#pragma unroll
-                for (int h = 0; h < CK / 32; ++h) {
-                    int64_t off = NOWHERE;
-                    if (pg[h] >= 0) {
-                        const int key = k0 + lane + 32 * h;
-                        const int slot = a.page_shift >= 0 ? key & (a.page_size - 1) : key % a.page_size;
-                        off = pg[h] * str[0] + slot * str[1];
-                    }
-                    missing |= pg[h] == -2;
-                    // eight lanes a row: a 128-byte line of each block of 64 elements
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const int r = i * 4 + (lane >> 3), c8 = lane & 7;
-                        const int64_t o = __shfl_sync(FULL, off, r);
-                        const bool on = o != NOWHERE;
-                        const T* from = src + (on ? o + c8 * 8 : 0);
-#pragma unroll
-                        for (int b = 0; b < D / 64; ++b) cp16(dst + tile_at<CK>(r + 32 * h, c8 + 8 * b), from + (on ? 64 * b : 0), on);
-                    }
-                }
-                cp_async_commit();
-                if (!value && __any_sync(FULL, missing)) {   // such keys are NaN, and so is every query that sees one
-                    cp_async_wait<0>();
+                const bool check = value && sg.partial(a, k0);
+                const uint32_t bar = check ? land + 8 * half : full + 8 * st;
+                if (GATHER && maps.box > 0 && __all_sync(FULL, (pg[0] | pg[1] | pg[2] | pg[3]) >= 0)) {
+                    // lane: box and block of 64 elements
+                    const int b = lane / (D / 64), at = b * maps.box, x = lane % (D / 64);
+                    const int page = __shfl_sync(FULL, pg[0], (at >> 2) & 15);
+                    if (lane == 0) bar_expect(bar, 64 * D * 2);
                     __syncwarp();
+                    if (at < 64)
+                        copy_box(dst + x * (CK * 128) + (half * 64 + at) * 128, value ? &maps.vbox : &maps.kbox, x * 64,
+                                 (k0 + half * 64 + at) & (a.page_size - 1), head, page, bar);
+                } else if (GATHER) {
+                    int rows[4];
 #pragma unroll
-                    for (int h = 0; h < CK / 32; ++h)
-                        if (pg[h] == -2)
-                            for (int e = 0; e < DC; ++e)
-                                *reinterpret_cast<uint4*>(mem + (dst - base) + tile_at<CK>(lane + 32 * h, e)) =
-                                    make_uint4(0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu);
-                }
-                look_up(c + 4);
-                if (before >= 0) {
-                    cp_async_wait<1>();
-                    hand_over();
-                }
-                before = st;
-                check = value && sg.partial(a, k0);
-                check_segment = segment;
-                st += 4;
-                if (st >= ST) st -= ST, ++lap;
-            }
-            // Handed over before the next tile's lengths and pages are read.
-            if (before >= 0) {
-                cp_async_wait<0>();
-                hand_over();
-                before = -1;
-            }
-            seq += 2 * n;
-            u += n;
-            if (u >= sg.end) ++tile;
-        }
-        cp_async_wait<0>();
-    } else if (warp >= 12) {
-        // ================================================ matrix instructions
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
-        // Two warps, one for each product.  A whole warp runs each loop, so that addresses and descriptors
-        // stay in uniform registers; one elected lane issues.
-        const bool lead = elect();
-        if (warp == 12) {
-            // ---- scores
-            constexpr uint32_t QK = product<T>(CK, false);
-            const uint32_t q_op = (base & 0x3ffff) >> 4, k_op = ((base + S::KV) & 0x3ffff) >> 4, hi = operand_high();
-            bool ok = true;
-            uint32_t seq = 0, segs[2] = {0, 0}, done[2] = {0, 0};   // copies; segments and products of each tile
-#pragma unroll 1
-            for (int64_t u = unit; u < last && ok;) {
-                const Segment sg(a, tile, u, last);
-                const int n = sg.tiles();
-                const bool two = sg.two();
-#pragma unroll 1
-                for (int i = 0; i < n && ok; ++i) {
-                    const uint32_t c = seq + keys_copy(i), lap = c / ST, kst = c - lap * ST;
-                    ok = __all_sync(FULL, bar_wait(full + 8 * kst, lap & 1, dead));
-#pragma unroll
-                    for (int t = 0; t < 2; ++t) {
-                        if (t == 1 && !two) break;
-                        if (i == 0) ok = ok && __all_sync(FULL, bar_wait(qbar + 8 * t, segs[t]++ & 1, dead));
-                        // the weights of the product before, in the same columns, have been read
-                        if (done[t] > 0) ok = ok && __all_sync(FULL, bar_wait(vbar + 8 * t, (done[t] - 1) & 1, dead));
-                        if (!ok) break;
-                        ++done[t];
-                        tmem_fence_after();
-                        const uint32_t q = q_op + t * (S::QTILE >> 4), k = k_op + kst * (S::TILE >> 4);
-#pragma unroll
-                        for (int s = 0; s < D / 16; ++s)
-                            mma_smem(lead, tmem + t * CK, q + (((s >> 2) * (CM * 128) + (s & 3) * 32) >> 4), 0,
-                                     k + (((s >> 2) * (CK * 128) + (s & 3) * 32) >> 4), 0, hi, QK, s > 0);
-                        mma_commit(lead, sbar + 8 * t);
+                    for (int j = 0; j < 4; ++j) {
+                        const int key = k0 + row + j, slot = a.page_shift >= 0 ? key & (a.page_size - 1) : key % a.page_size;
+                        rows[j] = pg[j] >= 0 ? pg[j] * step[0] + slot * step[1] + head * step[2] : -1;
                     }
-                    if (ok) mma_commit(lead, empty + 8 * kst);
-                }
-                seq += 2 * n;
-                u += n;
-                if (u >= sg.end) ++tile;
-            }
-            if (!ok) {   // what has been issued finishes before the tensor memory is freed
-                *dead = 1;
-                mma_commit(lead, xbar + 0);
-                for (uint32_t i = 0; i < SPIN && !bar_try(xbar + 0, 0); ++i) {}
-            }
-        } else if (warp == 13) {
-            // ---- weights times values
-            constexpr uint32_t PV = product<T>(D, true);
-            const uint32_t v_op = ((base + S::KV) & 0x3ffff) >> 4, hi = operand_high();
-            bool ok = true;
-            uint32_t seq = 0, done[2] = {0, 0};
-#pragma unroll 1
-            for (int64_t u = unit; u < last && ok;) {
-                const Segment sg(a, tile, u, last);
-                const int n = sg.tiles();
-                const bool two = sg.two();
-#pragma unroll 1
-                for (int i = 0; i < n && ok; ++i) {
-                    const uint32_t c = seq + values_copy(i, n), lap = c / ST, vst = c - lap * ST;
-                    ok = __all_sync(FULL, bar_wait(full + 8 * vst, lap & 1, dead));
-                    const uint32_t v = v_op + vst * (S::TILE >> 4);
+                    if (lane == 0) bar_expect(bar, 64 * D * 2);
+                    __syncwarp();
+                    if (block < D / 64) gather4(dst + block * (CK * 128) + row * 128, map, block * 64, rows, bar);
+                } else {
+                    const T* src = static_cast<const T*>(value ? a.v : a.k) + head * str[2];
 #pragma unroll
-                    for (int t = 0; t < 2; ++t) {
-                        if (t == 1 && !two) break;
-                        const uint32_t p = tmem + t * CK, o = tmem + 2 * CK + t * D;
+                    for (int j = 0; j < 4; ++j) {
+                        const int key = k0 + row + j, slot = a.page_shift >= 0 ? key & (a.page_size - 1) : key % a.page_size;
+                        const int64_t off = pg[j] >= 0 ? pg[j] * str[0] + slot * str[1] : NOWHERE;
+                        // four rows at a time (of quads 4 q .. 4 q + 3), eight lanes a 128-byte line
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            ok = ok && __all_sync(FULL, bar_wait(pbar + 16 * t + 8 * h, done[t] & 1, dead));
-                            if (!ok) break;
-                            tmem_fence_after();
+                        for (int q = 0; q < 4; ++q) {
+                            const int from = q * 4 + (lane >> 3), r = half * 64 + from * 4 + j;
+                            const int64_t o = __shfl_sync(FULL, off, from);
+                            const bool on = o != NOWHERE;
 #pragma unroll
-                            for (int s = 4 * h; s < 4 * h + 4; ++s)
-                                mma_tmem(lead, o, p + 8 * s, v + s * (2048 >> 4), CK * 128, hi, PV, i > 0 || s > 0);
+                            for (int b = 0; b < D / 64; ++b)
+                                cp16(dst + tile_at<CK>(r, (lane & 7) + 8 * b), src + (on ? o + (lane & 7) * 8 + 64 * b : 0), on);
                         }
-                        if (!ok) break;
-                        ++done[t];
-                        mma_commit(lead, vbar + 8 * t);
                     }
-                    if (ok) mma_commit(lead, empty + 8 * vst);
+                    cp_async_commit();
+                    cp_async_wait<0>();
                 }
-                seq += 2 * n;
-                u += n;
-                if (u >= sg.end) ++tile;
+                look_up(i + 1);
+                if (check) {
+                    // A value that only some of the tokens see may be infinite or NaN, which a weight of zero does not
+                    // cancel: such values are taken out of the tile, and added at the end to the outputs of the
+                    // queries that see them.
+                    if (GATHER) ok = __all_sync(FULL, bar_wait(bar, landed++ & 1, dead));
+                    if (!ok) break;
+                    __syncwarp();
+                    bool any = false;
+#pragma unroll 4
+                    for (int e = lane; e < 64 * DC; e += 32) {
+                        const uint32_t at = (e / 512) * (CK * 128) + half * 8192 + (e % 512) * 16;
+                        any |= odd_words<T>(*reinterpret_cast<const uint4*>(mem + (dst - base) + at));
+                    }
+                    if (__any_sync(FULL, any)) {
+                        for (int e = lane; e < 64 * DC; e += 32) {
+                            const uint32_t at = (e / 512) * (CK * 128) + half * 8192 + (e % 512) * 16;
+                            uint4* p = reinterpret_cast<uint4*>(mem + (dst - base) + at);
+                            *p = even_words<T>(*p);
+                        }
+                        odd[s & 3] = int(s) + 1;
+                    }
+                }
+                if (!GATHER || check) {
+                    proxy_fence();
+                    __syncwarp();
+                    if (lane == 0) bar_arrive(full + 8 * st);
+                }
             }
-            if (!ok) {   // what has been issued finishes before the tensor memory is freed
-                *dead = 1;
-                mma_commit(lead, xbar + 8);
-                for (uint32_t i = 0; i < SPIN && !bar_try(xbar + 8, 0); ++i) {}
+            if (!ok) break;
+            seq += 2 * n;
+            unit += n;
+            give_back(s);
+        }
+        if (!ok) *dead = 1;
+    } else if (warp == 12) {
+        // ================================================ the first product
+        // (A whole warp runs each loop, so that addresses and descriptors stay in uniform registers; one elected
+        // lane issues.)
+        const bool lead = elect();
+        constexpr uint32_t QK = product<T>(CK, false);
+        const uint32_t q_op = (base & 0x3ffff) >> 4, k_op = ((base + S::KV) & 0x3ffff) >> 4, hi = operand_high();
+        bool ok = true;
+        uint32_t seq = 0, uses[2] = {0, 0}, done[2] = {0, 0};   // copies; segments and products of each tile
+        for (uint32_t s = 0;; ++s) {
+            const Segment& sg = next_segment(s, ok);
+            if (!ok) break;
+            const int n = sg.n, tiles = sg.two() ? 2 : 1;
+            if (n == 0) break;
+            give_back(s);
+#pragma unroll 1
+            for (int i = 0; i < n && ok; ++i) {
+                const uint32_t c = seq + keys_copy(i), lap = c / ST, kst = c - lap * ST;
+                ok = __all_sync(FULL, bar_wait(full + 8 * kst, lap & 1, dead));
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    if (t >= tiles) break;
+                    if (i == 0) ok = ok && __all_sync(FULL, bar_wait(qbar + 8 * t, uses[t]++ & 1, dead));
+                    // the weights of the product before, in the same columns, have been read
+                    if (done[t] > 0) ok = ok && __all_sync(FULL, bar_wait(vbar + 8 * t, (done[t] - 1) & 1, dead));
+                    if (!ok) break;
+                    ++done[t];
+                    tmem_fence_after();
+                    const uint32_t q = q_op + t * (S::QTILE >> 4), k = k_op + kst * (S::TILE >> 4);
+#pragma unroll
+                    for (int d = 0; d < D / 16; ++d)
+                        mma_smem(lead, tmem + t * CK, q + (((d >> 2) * (CM * 128) + (d & 3) * 32) >> 4), 0,
+                                 k + (((d >> 2) * (CK * 128) + (d & 3) * 32) >> 4), 0, hi, QK, d > 0);
+                    mma_commit(lead, sbar + 8 * t);
+                    if (i == n - 1) mma_commit(lead, qfree + 8 * t);
+                }
+                if (ok) mma_commit(lead, empty + 8 * kst);
             }
+            if (!ok) break;
+            seq += 2 * n;
+        }
+        if (!ok) {   // what has been issued finishes before the tensor memory is freed
+            *dead = 1;
+            mma_commit(lead, xbar);
+            for (uint32_t i = 0; i < SPIN && !bar_try(xbar, 0); ++i) {}
         }
         __syncwarp();
-    } else {
-        // ================================================ softmax
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
-        const int t = warp >> 2, r = tid & 127;
-        const uint32_t lanes = uint32_t(warp & 3) << 21;   // the warp's 32 lanes of tensor memory
-        const uint32_t sc = tmem + t * CK + lanes, oc = tmem + 2 * CK + t * D + lanes;
+    } else if (warp == 13) {
+        // ================================================ the second product
+        const bool lead = elect();
+        constexpr uint32_t PV = product<T>(D, true);
+        const uint32_t v_op = ((base + S::KV) & 0x3ffff) >> 4, hi = operand_high();
         bool ok = true;
-        uint32_t done = 0;      // products of this tile
-        int segment = 0;
+        uint32_t seq = 0, done[2] = {0, 0};
+        for (uint32_t s = 0;; ++s) {
+            const Segment& sg = next_segment(s, ok);
+            if (!ok) break;
+            const int n = sg.n, tiles = sg.two() ? 2 : 1;
+            if (n == 0) break;
+            give_back(s);
 #pragma unroll 1
-        for (int64_t u = unit; u < last; ++segment) {
-            float m = -INFINITY, l = 0.f;
-            bool active;
-            int n, pos, t_lo, t_hi, few, skip, i0;      // (no more than this stays in registers beside a row's scores)
-            {
-                const Segment sg(a, tile, u, last);
-                n = sg.tiles();
-                active = ok && (t == 0 || sg.two());
-                few = sg.kt.few, skip = sg.kt.skip, i0 = sg.i0;
-                pos = sg.x.pos(a, min(sg.row0 + t * CM + r, sg.M - 1));
-                // positions of this tile's first and last token
-                t_lo = sg.x.pos(a, sg.row0 + t * CM), t_hi = sg.x.pos(a, min(sg.row0 + (t + 1) * CM, sg.M) - 1);
-                if (active) {
-                    // The queries of this tile, by its 128 threads (the product that read the ones before is done).
+            for (int i = 0; i < n && ok; ++i) {
+                const uint32_t c = seq + values_copy(i, n), lap = c / ST, vst = c - lap * ST;
+                ok = __all_sync(FULL, bar_wait(full + 8 * vst, lap & 1, dead));
+                const uint32_t v = v_op + vst * (S::TILE >> 4);
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    if (t >= tiles) break;
+                    const uint32_t p = tmem + t * CK, o = tmem + 2 * CK + t * D;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        ok = ok && __all_sync(FULL, bar_wait(pbar + 16 * t + 8 * h, done[t] & 1, dead));
+                        if (!ok) break;
+                        tmem_fence_after();
+#pragma unroll
+                        for (int k = 4 * h; k < 4 * h + 4; ++k)
+                            mma_tmem(lead, o, p + 8 * k, v + k * (2048 >> 4), CK * 128, hi, PV, i > 0 || k > 0);
+                    }
+                    if (!ok) break;
+                    ++done[t];
+                    mma_commit(lead, vbar + 8 * t);
+                }
+                if (ok) mma_commit(lead, empty + 8 * vst);
+            }
+            if (!ok) break;
+            seq += 2 * n;
+        }
+        if (!ok) {
+            *dead = 1;
+            mma_commit(lead, xbar + 8);
+            for (uint32_t i = 0; i < SPIN && !bar_try(xbar + 8, 0); ++i) {}
+        }
+        __syncwarp();
+    } else if (warp == 14) {
+        // ================================================ what the next tiles are
+        int tile = words[6];
+        int64_t u = first_unit;
+        bool ok = true;
+        for (uint32_t s = 0; ok; ++s) {
+            if (s >= AHEAD) ok = __all_sync(FULL, bar_wait(segfree + 8 * (s % AHEAD), (s / AHEAD - 1) & 1, dead));
+            if (!ok) break;
+            Segment sg;
+            sg.n = 0;
+            if (u < last) {
+                const int4 it = a.t_items[tile];
+                sg.r = it.x, sg.row0 = it.y;
+                sg.x = request(a, it.x);
+                sg.M = sg.x.rows(a);
+                sg.p_lo = sg.x.pos(a, it.y), sg.p_hi = sg.x.pos(a, min(it.y + MANY, sg.M) - 1);
+                sg.kt = KeyTiles<CK>(a, sg.p_lo, sg.p_hi);
+                const int64_t before = (int64_t(it.w) << 32 | uint32_t(it.z)) * a.Hkv, rel = u - before;
+                sg.head = int(rel / sg.kt.n);
+                sg.i0 = int(rel - int64_t(sg.head) * sg.kt.n);
+                sg.n = int(min(int64_t(sg.kt.n - sg.i0), last - u));
+                sg.whole = sg.n == sg.kt.n;
+                sg.parts = sg.whole || sg.i0 > 0 ? 0 : int((u + sg.kt.n - 1) / run) - int(blockIdx.x) + 1;
+                u += sg.n;
+                if (u >= before + int64_t(sg.kt.n) * a.Hkv) ++tile;
+            }
+            if (lane == 0) segs[s % AHEAD] = sg;
+            __syncwarp();
+            if (lane == 0) bar_arrive(segbar + 8 * (s % AHEAD));
+            if (sg.n == 0) break;
+        }
+    } else if (warp == 15) {
+        // ================================================ queries
+        bool ok = true;
+        uint32_t uses[2] = {0, 0};
+        for (uint32_t s = 0;; ++s) {
+            const Segment& sg = next_segment(s, ok);
+            if (!ok || sg.n == 0) break;
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                if (t == 1 && !sg.two()) break;
+                if (uses[t] > 0) ok = ok && __all_sync(FULL, bar_wait(qfree + 8 * t, (uses[t] - 1) & 1, dead));
+                if (!ok) break;
+                ++uses[t];
+                const int row0 = sg.row0 + t * CM;
+                if (GATHER) {
+                    int rows[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const int row = row0 + lane * 4 + j, tok = row / a.gs;
+                        rows[j] = row < sg.M ? (sg.x.q0 + tok) * maps.qs[0] + (sg.head * a.gs + row - tok * a.gs) * maps.qs[1] : -1;
+                    }
+                    if (lane == 0) bar_expect(qbar + 8 * t, CM * D * 2);
+                    __syncwarp();
+#pragma unroll
+                    for (int b = 0; b < D / 64; ++b)
+                        gather4(base + t * S::QTILE + b * (CM * 128) + lane * 512, &maps.q, b * 64, rows, qbar + 8 * t);
+                } else {
 #pragma unroll 4
-                    for (int i = r; i < CM * DC; i += 128) {
-                        const int q = i / DC, c = i % DC, qr = sg.row0 + t * CM + q;
-                        const bool there = qr < sg.M;
-                        const int j = there ? qr / a.gs : 0, h = sg.head * a.gs + (there ? qr % a.gs : 0);
+                    for (int i = lane; i < CM * DC; i += 32) {
+                        const int q = i / DC, c = i % DC, row = row0 + q;
+                        const bool there = row < sg.M;
+                        const int tok = there ? row / a.gs : 0, h = sg.head * a.gs + (there ? row % a.gs : 0);
                         cp16(base + t * S::QTILE + tile_at<CM>(q, c),
-                             static_cast<const T*>(a.q) + (sg.x.q0 + j) * a.qs[0] + h * a.qs[1] + c * 8, there);
+                             static_cast<const T*>(a.q) + (sg.x.q0 + tok) * a.qs[0] + h * a.qs[1] + c * 8, there);
                     }
                     cp_async_commit();
                     cp_async_wait<0>();
                     proxy_fence();
-                    bar_arrive(qbar + 8 * t);
+                    __syncwarp();
+                    if (lane == 0) bar_arrive(qbar + 8 * t);
                 }
             }
-            if (active) {
-                bool huge = false;
+            if (!ok) break;
+            give_back(s);
+        }
+        if (!ok) *dead = 1;
+    } else {
+        // ================================================ softmax
+        const int t = warp >> 2, r = tid & 127;
+        const uint32_t lanes = uint32_t(warp & 3) << 21;   // the warp's 32 lanes of tensor memory
+        const uint32_t sc = tmem + t * CK + lanes, oc = tmem + 2 * CK + t * D + lanes;
+        bool ok = true;
+        uint32_t done = 0, unit = 0;      // products of this tile; key tiles of segments before
+#pragma unroll 1
+        for (uint32_t s = 0; ok; ++s) {
+            const Segment& sg = next_segment(s, ok);
+            if (!ok || sg.n == 0) break;
+            const int n = sg.n, row = sg.row0 + t * CM + r;
+            if (t == 0 || sg.two()) {
+                const bool on = row < sg.M;
+                const int pos = sg.x.pos(a, min(row, sg.M - 1));
+                // positions of this tile's first and last token
+                const int t_lo = sg.x.pos(a, sg.row0 + t * CM), t_hi = sg.x.pos(a, min(sg.row0 + (t + 1) * CM, sg.M) - 1);
+                const int few = sg.kt.few, skip = sg.kt.skip, i0 = sg.i0;
+                float m = -INFINITY, l = 0.f;
 #pragma unroll 1
                 for (int i = 0; i < n; ++i) {
                     const int at = i0 + i, k0 = (at < few ? at : at - few + skip) * CK;
@@ -413,53 +503,63 @@ __global__ void __launch_bounds__(CNT, 1) chunk_tensor_kernel(const ChunkArgs a)
                     if (!ok) break;
                     ++done;
                     tmem_fence_after();
-                    uint32_t x[CK];
-#pragma unroll
-                    for (int c = 0; c < CK / 32; ++c) tmem_ld32(part<32>(x, c), sc + c * 32);
-                    tmem_wait_ld();
                     float mul = a.scale;
-                    if (mul < 0.f) {
-                        mul = -mul;
+                    const bool edge = t_hi - k0 >= a.window, gone = missing[2 * ((unit + i) & 15)] | missing[2 * ((unit + i) & 15) + 1];
+                    if (k0 + CK > t_lo + 1 || edge || gone || mul < 0.f) {
+                        // Scaled here where some keys are not seen, so that their scores are -infinity whatever the scale;
+                        // a key whose page does not exist is NaN.
+                        const int lim = pos + 1 - k0, low = edge ? pos - a.window + 1 - k0 : 0, first = a.sinks - k0;
+#pragma unroll 1
+                        for (int c = 0; c < CK; c += 32) {
+                            uint32_t x[32];
+                            tmem_ld32(x, sc + c);
+                            tmem_wait_ld();
 #pragma unroll
-                        for (int e = 0; e < CK; ++e) x[e] ^= 0x80000000u;
-                    }
-                    // Scaled here where some keys are not seen, so that their scores are -infinity whatever the scale.
-                    const bool edge = t_hi - k0 >= a.window;
-                    if (k0 + CK > t_lo + 1 || edge) {
-                        const int lim = pos + 1 - k0;
+                            for (int e = 0; e < 32; ++e) {
+                                const int k = c + e;
+                                x[e] = k < lim && (k >= low || k < first) ? __float_as_uint(__uint_as_float(x[e]) * mul) : 0xff800000u;
+                            }
+                            if (gone) {
+                                const unsigned bits = missing_pages(a, sg.r, k0 + c);
 #pragma unroll
-                        for (int e = 0; e < CK; ++e)
-                            x[e] = e < lim ? __float_as_uint(__uint_as_float(x[e]) * mul) : 0xff800000u;
-                        if (edge) {
-                            const int low = pos - a.window + 1 - k0, few = a.sinks - k0;
-#pragma unroll
-                            for (int e = 0; e < CK; ++e)
-                                if (e < low && e >= few) x[e] = 0xff800000u;
+                                for (int e = 0; e < 32; ++e)
+                                    if (bits >> e & 1 && x[e] != 0xff800000u) x[e] = 0x7fffffffu;
+                            }
+                            tmem_st32(sc + c, x);
                         }
+                        tmem_wait_st();
                         mul = 1.f;
                     }
-                    float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                    float mx = -INFINITY;
+#pragma unroll 1
+                    for (int c = 0; c < CK; c += 64) {
+                        uint32_t x[64];
+                        tmem_ld32(part<32>(x, 0), sc + c);
+                        tmem_ld32(part<32>(x, 1), sc + c + 32);
+                        tmem_wait_ld();
+                        float m4[4] = {mx, mx, mx, mx};
 #pragma unroll
-                    for (int e = 0; e < CK; e += 2)
-                        m4[(e >> 1) & 3] = fmaxf(m4[(e >> 1) & 3], fmaxf(__uint_as_float(x[e]), __uint_as_float(x[e + 1])));
-                    float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * mul;
+                        for (int e = 0; e < 64; e += 2)
+                            m4[(e >> 1) & 3] = fmaxf(m4[(e >> 1) & 3], fmaxf(__uint_as_float(x[e]), __uint_as_float(x[e + 1])));
+                        mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+                    }
+                    mx *= mul;
                     if (!(mx > -INFINITY)) mx = m;   // a scale of 0 times infinity, or nothing but NaN
                     if (__any_sync(FULL, mx - m > W::GROWTH)) {   // (the difference is exact where it decides)
                         const float mn = fmaxf(m, mx);
                         const float f = m == -INFINITY ? 0.f : exp2_fast(m - mn);
                         m = mn;
                         l *= f;
-                        huge = __any_sync(FULL, fabsf(m) > 0x1p20f);
                         if (i > 0) {
                             // (the last product of this tile was done before these scores were begun)
-#pragma unroll
-                            for (int c = 0; c < D / 16; ++c) {
-                                uint32_t y[16];
-                                tmem_ld16(y, oc + c * 16);
+#pragma unroll 1
+                            for (int c = 0; c < D; c += 32) {
+                                uint32_t y[32];
+                                tmem_ld32(y, oc + c);
                                 tmem_wait_ld();
 #pragma unroll
-                                for (int e = 0; e < 16; ++e) y[e] = __float_as_uint(__uint_as_float(y[e]) * f);
-                                tmem_st16(oc + c * 16, y);
+                                for (int e = 0; e < 32; ++e) y[e] = __float_as_uint(__uint_as_float(y[e]) * f);
+                                tmem_st32(oc + c, y);
                             }
                         }
                     }
@@ -467,24 +567,42 @@ __global__ void __launch_bounds__(CNT, 1) chunk_tensor_kernel(const ChunkArgs a)
                     float off = W::SHIFT - ms;
                     // A maximum is a rounded product and a weight's exponent below is not: beyond 2^20 their difference, up
                     // to 2^-25 of the maximum, would count in the exponent (at 2^31 it is 2^6 and more).
-                    if (huge) {
+                    if (__any_sync(FULL, fabsf(m) > 0x1p20f && m > -INFINITY)) {
+#pragma unroll 1
+                        for (int c = 0; c < CK; c += 32) {
+                            uint32_t x[32];
+                            tmem_ld32(x, sc + c);
+                            tmem_wait_ld();
 #pragma unroll
-                        for (int e = 0; e < CK; ++e) x[e] = __float_as_uint(__fmul_rn(__uint_as_float(x[e]), mul) - ms);
+                            for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(__fmul_rn(__uint_as_float(x[e]), mul) - ms);
+                            tmem_st32(sc + c, x);
+                        }
+                        tmem_wait_st();
                         mul = 1.f;
                         off = W::SHIFT;
                     }
+                    // ---- weights, 32 at a time; the next scores are read meanwhile
                     float s0 = 0.f, s1 = 0.f;
-#pragma unroll
+                    uint32_t x[2][32];
+                    tmem_ld32(x[0], sc);
+                    tmem_wait_ld();
+#pragma unroll 1
                     for (int h = 0; h < 2; ++h) {
 #pragma unroll
-                        for (int e = 64 * h; e < 64 * h + 64; e += 2) {
-                            float p0 = __uint_as_float(x[e]), p1 = __uint_as_float(x[e + 1]);
-                            fma_pair(p0, p1, mul, off);
-                            p0 = exp2_fast(p0), p1 = exp2_fast(p1);
-                            add_pair(s0, s1, p0, p1);
-                            x[e / 2] = Mma<T>::pack(p0, p1);
+                        for (int b = 0; b < 2; ++b) {
+                            if (b == 0 || h == 0) tmem_ld32(x[b ^ 1], sc + 64 * h + 32 * b + 32);
+                            uint32_t p[16];
+#pragma unroll
+                            for (int e = 0; e < 32; e += 2) {
+                                float p0 = __uint_as_float(x[b][e]), p1 = __uint_as_float(x[b][e + 1]);
+                                fma_pair(p0, p1, mul, off);
+                                p0 = exp2_fast(p0), p1 = exp2_fast(p1);
+                                add_pair(s0, s1, p0, p1);
+                                p[e / 2] = Mma<T>::pack(p0, p1);
+                            }
+                            tmem_st16(sc + 32 * h + 16 * b, p);
+                            if (b == 0 || h == 0) tmem_wait_ld();
                         }
-                        tmem_st32(sc + 32 * h, part<32>(x, h));
                         tmem_wait_st();
                         tmem_fence_before();
                         bar_arrive(pbar + 16 * t + 8 * h);
@@ -494,35 +612,29 @@ __global__ void __launch_bounds__(CNT, 1) chunk_tensor_kernel(const ChunkArgs a)
                 // ---- the row's output, once the last product is done
                 ok = ok && __all_sync(FULL, bar_wait(vbar + 8 * t, (done - 1) & 1, dead));
                 tmem_fence_after();
-            }
-            const Segment sg(a, tile, u, last);
-            const int row = sg.row0 + t * CM + r;
-            const bool on = row < sg.M;
-            if (t == 0 || sg.two()) {
                 const float bad = (!ok || *dead) ? __int_as_float(0x7fffffff) : 0.f;
                 const float inv = (l == 0.f ? 0.f : 1.f / l) + bad;
                 const float lse = (l == 0.f ? -INFINITY : m + (log2f(l) - W::SHIFT)) + bad;
-                const bool whole = sg.i0 == 0 && sg.i1 == sg.kt.n;
-                const bool fix = odd[segment & 3] == segment + 1;
-                const int j = on ? row / a.gs : 0, h = sg.head * a.gs + (on ? row % a.gs : 0);
+                const bool whole = sg.whole, fix = odd[s & 3] == int(s) + 1;
+                const int j = on ? row / a.gs : 0, h = sg.head * a.gs + (on ? row - j * a.gs : 0);
                 T* out = static_cast<T*>(a.out) + (sg.x.q0 + j) * a.os[0] + h * a.os[1];
-                const int64_t at = int64_t(2 * blockIdx.x + (sg.i0 == 0)) * MANY + t * CM + r;
+                const int64_t slot = int64_t(2 * blockIdx.x + (i0 == 0)) * MANY + t * CM + r;
 #pragma unroll 1
-                for (int c = 0; c < D / 32; ++c) {
+                for (int c = 0; c < D; c += 32) {
                     uint32_t y[32];
-                    tmem_ld32(y, oc + c * 32);
+                    tmem_ld32(y, oc + c);
                     tmem_wait_ld();
 #pragma unroll
                     for (int e = 0; e < 32; ++e) y[e] = __float_as_uint(__uint_as_float(y[e]) * inv);
                     if (on && fix) {   // (their weights are positive: exp(s - m) > 0)
                         for (int i = 0; i < n; ++i) {
-                            const int k0 = sg.kt.at(sg.i0 + i);
+                            const int k0 = sg.kt.at(i0 + i);
                             if (!sg.partial(a, k0)) continue;
 #pragma unroll
                             for (int e = 0; e < 32; e += 4) {
                                 float4 z = make_float4(__uint_as_float(y[e]), __uint_as_float(y[e + 1]), __uint_as_float(y[e + 2]),
                                                        __uint_as_float(y[e + 3]));
-                                add_odd<T>(a, a.table + int64_t(sg.r) * a.width, pos, k0, CK, sg.head, c * 32 + e, z);
+                                add_odd<T>(a, a.table + int64_t(sg.r) * a.width, pos, k0, CK, sg.head, c + e, z);
                                 y[e] = __float_as_uint(z.x), y[e + 1] = __float_as_uint(z.y);
                                 y[e + 2] = __float_as_uint(z.z), y[e + 3] = __float_as_uint(z.w);
                             }
@@ -532,36 +644,100 @@ __global__ void __launch_bounds__(CNT, 1) chunk_tensor_kernel(const ChunkArgs a)
                         auto two = [&](int e) { return Mma<T>::pack(__uint_as_float(y[e]), __uint_as_float(y[e + 1])); };
 #pragma unroll
                         for (int e = 0; e < 32; e += 8)
-                            *reinterpret_cast<uint4*>(out + c * 32 + e) = make_uint4(two(e), two(e + 2), two(e + 4), two(e + 6));
+                            *reinterpret_cast<uint4*>(out + c + e) = make_uint4(two(e), two(e + 2), two(e + 4), two(e + 6));
                     } else if (on) {
 #pragma unroll
                         for (int e = 0; e < 32; e += 4)
-                            *reinterpret_cast<uint4*>(a.t_part_o + at * D + c * 32 + e) = make_uint4(y[e], y[e + 1], y[e + 2], y[e + 3]);
+                            *reinterpret_cast<uint4*>(a.t_part_o + slot * D + c + e) = make_uint4(y[e], y[e + 1], y[e + 2], y[e + 3]);
                     }
                     __syncwarp();   // (tensor memory is read by whole warps)
                 }
                 if (on) {
-                    if (!whole) a.t_part_l[at] = lse;
+                    if (!whole) a.t_part_l[slot] = lse;
                     else if (a.lse) a.lse[int64_t(sg.x.q0 + j) * a.Hq + h] = lse * 0.693147180559945309f;
                 }
-                if (!whole && sg.i0 == 0 && tid == 0)   // this CTA has the tile's first part and says how many CTAs have one
-                    a.t_split[blockIdx.x] = make_int4(sg.r, sg.head, sg.row0, int((u + sg.kt.n - 1) / run) - int(blockIdx.x) + 1);
+                // The CTA that has a tile's first part says how many CTAs have one.
+                if (sg.parts > 0 && tid == 0) a.t_split[blockIdx.x] = make_int4(sg.r, sg.head, sg.row0, sg.parts);
                 tmem_fence_before();   // the reads above, before the next product into the same columns
             }
-            u += n;
-            if (u >= sg.end) ++tile;
+            unit += n;
+            give_back(s);
         }
     }
+    // Copies that a role which gave up has in flight land (a microsecond or two) before their memory is anyone else's.
+    for (int i = 0; *dead && i < 1000; ++i) __nanosleep(1000);
     tmem_fence_before();
     __syncthreads();
     tmem_fence_after();
     if (warp == 12) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
 }
 
-template <typename T, int D>
-static fs_status launch(const ChunkArgs& a, void* stream) {
-    const void* fn = reinterpret_cast<const void*>(chunk_tensor_kernel<T, D>);
-    const fs_status st = prepare_kernel(fn);
+// ------------------------------------------------------------------ host
+
+using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                            const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                            CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+static Encode encoder() {
+    static const Encode fn = [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult found;
+        const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &found);
+        if (e != cudaSuccess) cudaGetLastError();
+        return e == cudaSuccess && found == cudaDriverEntryPointSuccess ? reinterpret_cast<Encode>(p) : nullptr;
+    }();
+    return fn;
+}
+
+static bool tensor_map(CUtensorMap* map, const void* base, int dtype, int rank, const cuuint64_t* dims, const cuuint64_t* pitch,
+                       const cuuint32_t* box) {
+    const cuuint32_t ones[4] = {1, 1, 1, 1};
+    const Encode encode = encoder();
+    return encode && encode(map, dtype == FS_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, rank,
+                            const_cast<void*>(base), dims, pitch, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Rows of `dim` elements at offsets sum_i x_i strides[i], x_i < sizes[i], as the rows of one matrix: row number sum_i x_i
+// steps[i].  False where the strides have no common divisor of a row's length or more.
+static bool row_map(CUtensorMap* map, const void* base, int dtype, int dim, int n, const int64_t* strides, const int64_t* sizes,
+                    int* steps) {
+    int64_t g = 0;
+    for (int i = 0; i < n; ++i) {
+        if (sizes[i] < 2) continue;
+        if (strides[i] < 0) return false;
+        g = std::gcd(g, strides[i]);
+    }
+    if (g == 0) g = dim;
+    if (g < dim || g >= int64_t(1) << 36) return false;
+    int64_t last = 0;
+    for (int i = 0; i < n; ++i) {
+        const int64_t step = sizes[i] < 2 ? 0 : strides[i] / g;
+        if (step > 0 && (sizes[i] - 1) > (int64_t(0x7ffffffe) - last) / step) return false;
+        steps[i] = int(step);
+        last += step * (std::max<int64_t>(sizes[i], 1) - 1);
+    }
+    const cuuint64_t dims[2] = {cuuint64_t(dim), cuuint64_t(last + 1)}, pitch[1] = {cuuint64_t(g) * 2};
+    const cuuint32_t box[2] = {64, 1};
+    return tensor_map(map, base, dtype, 2, dims, pitch, box);
+}
+
+// Boxes of `rows` slots of a page.
+static bool box_map(CUtensorMap* map, const ChunkArgs& a, const void* base, int dtype, int dim, const int64_t* strides, int rows) {
+    const int64_t sizes[3] = {a.page_size, a.Hkv, std::max(a.num_pages, 1)}, by[3] = {strides[1], strides[2], strides[0]};
+    const cuuint64_t dims[4] = {cuuint64_t(dim), cuuint64_t(sizes[0]), cuuint64_t(sizes[1]), cuuint64_t(sizes[2])};
+    cuuint64_t pitch[3];
+    for (int i = 0; i < 3; ++i) {
+        if (sizes[i] > 1 && (by[i] < dim || by[i] >= int64_t(1) << 38)) return false;
+        pitch[i] = sizes[i] > 1 ? cuuint64_t(by[i]) * 2 : cuuint64_t(dim) * 2;
+    }
+    const cuuint32_t box[4] = {64, cuuint32_t(rows), 1, 1};
+    return tensor_map(map, base, dtype, 4, dims, pitch, box);
+}
+template <typename T, int D, bool GATHER>
+static fs_status launch(const ChunkArgs& a, const ChunkMaps& maps, void* stream) {
+    const fs_status st = prepare_kernel(reinterpret_cast<const void*>(chunk_tensor_kernel<T, D, GATHER>));
     if (st != FS_OK) return st;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(unsigned(a.t_grid), 1, 1);
@@ -573,13 +749,28 @@ static fs_status launch(const ChunkArgs& a, void* stream) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, chunk_tensor_kernel<T, D>, a);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, chunk_tensor_kernel<T, D, GATHER>, a, maps);
     return e == cudaSuccess ? FS_OK : cuda_fail(e);
 }
 
+template <typename T>
+static fs_status launch_type(const ChunkArgs& a, int dtype, int head_dim, void* stream) {
+    ChunkMaps maps = {};
+    const int64_t cache[3] = {a.num_pages, a.page_size, a.Hkv}, query[2] = {a.N, a.Hq};
+    const bool gather = row_map(&maps.k, a.k, dtype, head_dim, 3, a.kc, cache, maps.ks) &&
+                        row_map(&maps.v, a.v, dtype, head_dim, 3, a.vc, cache, maps.vs) &&
+                        row_map(&maps.q, a.q, dtype, head_dim, 2, a.qs, query, maps.qs);
+    if (gather && a.page_shift >= 3) {
+        maps.box = std::min(a.page_size, 64);
+        if (!box_map(&maps.kbox, a, a.k, dtype, head_dim, a.kc, maps.box) || !box_map(&maps.vbox, a, a.v, dtype, head_dim, a.vc, maps.box))
+            maps.box = 0;
+    }
+    if (gather) return head_dim == 64 ? launch<T, 64, true>(a, maps, stream) : launch<T, 128, true>(a, maps, stream);
+    return head_dim == 64 ? launch<T, 64, false>(a, maps, stream) : launch<T, 128, false>(a, maps, stream);
+}
+
 fs_status launch_chunk_tensor(const ChunkArgs& a, int dtype, int head_dim, void* stream) {
-    if (dtype == FS_BF16) return head_dim == 64 ? launch<__nv_bfloat16, 64>(a, stream) : launch<__nv_bfloat16, 128>(a, stream);
-    return head_dim == 64 ? launch<__half, 64>(a, stream) : launch<__half, 128>(a, stream);
+    return dtype == FS_BF16 ? launch_type<__nv_bfloat16>(a, dtype, head_dim, stream) : launch_type<__half>(a, dtype, head_dim, stream);
 }
 
 }  // namespace fsd

@@ -10,6 +10,7 @@ namespace fsd {
 
 constexpr int FEW = 16;         // query rows that a tile of chunk_rows_kernel holds beside the tensor cores' tiles
 constexpr int MANY = 256;       // query rows of a tensor-core tile
+constexpr int START = 3;        // key tiles that start and end of a tensor-core tile take as long as
 
 struct ChunkArgs {
     const void* q;
@@ -35,10 +36,11 @@ struct ChunkArgs {
     int4* split;                // [grid]: request, head, row0, parts; parts 0: none
     // chunk_tensor_kernel's
     int t_grid, t_tiles, t_least;   // t_grid 0: not launched
+    int out_32;                 // the output's rows are aligned to 32 bytes
     float* t_part_o;            // [2 t_grid][MANY][D]
     float* t_part_l;
     int4* t_split;
-    int4* t_items;              // [t_tiles]: request, row0, units of a key/value head before (low, high word)
+    int4* t_items;              // [t_tiles]: request, row0, units (and START for each tile) of a key/value head before (low, high word)
     int* t_first;               // [R + 1]: tiles before a request
     int* t_plan;                // tiles, units (low, high word) of a key/value head
 };

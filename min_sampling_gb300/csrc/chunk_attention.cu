@@ -107,10 +107,10 @@ __device__ __forceinline__ void plan_tiles(const ChunkArgs& a, int64_t* words) {
     };
     mine = 0;
     int row0;
-    for (int i = i0, r = first; i < i1; ++i) mine += units(r, i, row0);
+    for (int i = i0, r = first; i < i1; ++i) mine += units(r, i, row0) + START;
     at = block_sum_before<NT>(mine, words, total);
     for (int i = i0, r = first; i < i1; ++i) {
-        const int u = units(r, i, row0);
+        const int u = units(r, i, row0) + START;
         a.t_items[i] = make_int4(r, row0, int(uint32_t(at)), int(at >> 32));
         at += u;
     }
@@ -594,9 +594,9 @@ static ChunkPlan chunk_plan(const fs_paged_kv& c, int N, int R, int Hq, int widt
     if (tensor) {
         // One CTA per SM.  A request of FEW rows or less has no tile there.
         const int64_t all = int64_t(N) * gs;
-        p.t_least = 2;
+        p.t_least = START + 1;
         p.t_tiles = int(std::min<int64_t>(all / MANY + std::min<int64_t>(R, all / (FEW + 1) + 1), 0x7fffffff));
-        const int64_t t_units = int64_t(p.t_tiles) * c.num_heads * ((int64_t(width) * c.page_size + 127) / 128 + 2);
+        const int64_t t_units = int64_t(p.t_tiles) * c.num_heads * ((int64_t(width) * c.page_size + 127) / 128 + 2 + START);
         p.t_grid = int(std::max<int64_t>(1, std::min<int64_t>(sms, (t_units + p.t_least - 1) / p.t_least)));
         p.t_part_o = add_bytes(at, size_t(2) * p.t_grid * MANY * D * 4);
         p.t_part_l = add_bytes(at, size_t(2) * p.t_grid * MANY * 4);
@@ -737,6 +737,7 @@ fs_status fs_paged_chunk_attention(const fs_paged_kv* cache, const void* query, 
     a.split = reinterpret_cast<int4*>(ws + p.split);
     a.t_grid = p.t_grid;
     a.t_least = p.t_least;
+    a.out_32 = (reinterpret_cast<uintptr_t>(out) % 32 == 0 && a.os[0] % 16 == 0 && a.os[1] % 16 == 0);
     a.t_tiles = p.t_tiles;
     if (p.t_grid > 0) {
         a.t_part_o = reinterpret_cast<float*>(ws + p.t_part_o);

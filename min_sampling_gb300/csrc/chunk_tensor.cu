@@ -9,7 +9,8 @@
 //   warps 0-3, 4-7  softmax of tile 0 / tile 1, one thread per row: maximum, weights, sum; O is rescaled
 //                   only when a maximum grows by more than 2^GROWTH; at the end the row's output
 //   warps 8, 9      keys, half a tile each; warps 10, 11 values: page look-ups and copies into a ring of swizzled tiles
-//   warps 12, 13    issue the first and the second product
+//   warp 12         issues the products, PV of one tile and then its next S: in order, so that the weights have been read
+//                   when the scores behind them are written
 //   warp 14         what the next tiles are, into a ring that all roles read
 //   warp 15         queries of the next tile, as soon as the last product that reads the old ones is done
 // While one tile's softmax runs, the tensor cores have the other tile's products. (Keys 128 at a time and
@@ -44,6 +45,7 @@ namespace fsd {
 constexpr int CM = 128;         // query rows of a tile of one warpgroup
 constexpr int CK = 128;         // keys per tile
 constexpr int CNT = 512;        // threads
+constexpr int ROLES = 8;        // the first warp that is not the softmax's
 constexpr int AHEAD = 4;        // tiles that are described ahead
 
 // The part of a query tile that lies in a CTA's run: n key tiles (0: no more), i0 on, of one key/value head.
@@ -69,7 +71,8 @@ struct ChunkTensorSmem {
     static constexpr int NBARS = 2 * STAGES + 16 + 2 * AHEAD;
     static constexpr int SEGS = BARS + NBARS * 8;
     static constexpr int WORDS = SEGS + AHEAD * int(sizeof(Segment));
-    static constexpr int TOTAL = WORDS + 160 + 1024;   // 1024: the base's alignment
+    static constexpr int TOTAL = WORDS + 160;
+    static_assert(TOTAL <= 227 * 1024, "shared memory");
 };
 
 // Matrices of which the copies gather rows: row numbers of a page, a slot, a head (a token, a head).
@@ -78,6 +81,8 @@ struct ChunkMaps {
     int ks[3], vs[3], qs[2];
     int box;                    // rows of a box, 0: gathers only
     CUtensorMap kbox, vbox;     // [pages][heads][slots][dim]
+    int qrows;                  // all of a tile's queries are one box
+    CUtensorMap qbox;           // [tokens][heads][dim]
 };
 
 // Two floats at a time.
@@ -100,8 +105,17 @@ __device__ __forceinline__ void copy_box(uint32_t dst, const CUtensorMap* map, i
     asm volatile("cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];"
                  ::"r"(dst), "l"(map), "r"(x), "r"(slot), "r"(head), "r"(page), "r"(bar) : "memory");
 }
+__device__ __forceinline__ void copy_box(uint32_t dst, const CUtensorMap* map, int x, int head, int token, uint32_t bar) {
+    asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
+                 ::"r"(dst), "l"(map), "r"(x), "r"(head), "r"(token), "r"(bar) : "memory");
+}
 __device__ __forceinline__ void bar_expect(uint32_t bar, uint32_t bytes) {
     asm volatile("{ .reg .b64 t; mbarrier.arrive.expect_tx.shared::cta.b64 t, [%0], %1; }" ::"r"(bar), "r"(bytes) : "memory");
+}
+
+__device__ __forceinline__ void store32(void* p, const uint32_t (&x)[8]) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
+                 ::"l"(p), "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]), "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7]) : "memory");
 }
 
 // Copies of a segment of n key tiles, in the order in which the products need them: keys one tile ahead
@@ -116,9 +130,8 @@ __global__ void __launch_bounds__(CNT, 1) chunk_tensor_kernel(const ChunkArgs a,
     using S = ChunkTensorSmem<D>;
     using W = Weights<T>;
     constexpr int ST = S::STAGES, DC = D / 8;
-    extern __shared__ unsigned char raw[];
-    const uint32_t base = (smem_u32(raw) + 1023) & ~1023u;
-    unsigned char* mem = raw + (base - smem_u32(raw));
+    extern __shared__ __align__(1024) unsigned char mem[];
+    const uint32_t base = smem_u32(mem);
     const int tid = threadIdx.x, warp = __shfl_sync(FULL, tid >> 5, 0), lane = tid & 31;
     // barriers: full[ST], empty[ST]; of each tile: queries there, queries done with, scores there, weights there
     // (in two halves), product P V done; of each product, all done when a wait ran out; of each half of a value
@@ -136,6 +149,7 @@ __global__ void __launch_bounds__(CNT, 1) chunk_tensor_kernel(const ChunkArgs a,
 
     // ---- this CTA's run of units
     const int n_tiles = a.t_plan[0];
+    // (units and, for each tile of each key/value head, START more that its start and end take as long as)
     const int64_t total = (int64_t(a.t_plan[2]) << 32 | uint32_t(a.t_plan[1])) * a.Hkv;
     const int64_t run = max(int64_t(a.t_least), (total + a.t_grid - 1) / a.t_grid);
     const int64_t first_unit = min(blockIdx.x * run, total), last = min(first_unit + run, total);
@@ -151,18 +165,18 @@ __global__ void __launch_bounds__(CNT, 1) chunk_tensor_kernel(const ChunkArgs a,
         }
         if (before <= first_unit && first_unit < next) words[6] = i;
     }
-    if (warp == 13) {
+    if (warp == ROLES + 5) {
         if (lane < ST) bar_init(full + 8 * lane, 2), bar_init(empty + 8 * lane, 1);
         if (lane < 2) {
             bar_init(qbar + 8 * lane, 1), bar_init(qfree + 8 * lane, 1), bar_init(sbar + 8 * lane, 1);
             bar_init(vbar + 8 * lane, 1), bar_init(xbar + 8 * lane, 1), bar_init(land + 8 * lane, 1);
         }
-        // (a segment is read by four copying warps, two that issue products, the queries' and eight of the softmax)
-        if (lane < AHEAD) bar_init(pbar + 8 * lane, 128), odd[lane] = 0, bar_init(segbar + 8 * lane, 1), bar_init(segfree + 8 * lane, 15);
+        // (a segment is read by four copying warps, the one that issues products, the queries' and eight of the softmax)
+        if (lane < AHEAD) bar_init(pbar + 8 * lane, 128), odd[lane] = 0, bar_init(segbar + 8 * lane, 1), bar_init(segfree + 8 * lane, 14);
         if (lane == 0) *dead = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (warp == 12) {
+    if (warp == ROLES + 4) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(base + S::WORDS) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
@@ -181,9 +195,13 @@ __global__ void __launch_bounds__(CNT, 1) chunk_tensor_kernel(const ChunkArgs a,
         if (lane == 0) bar_arrive(segfree + 8 * (s % AHEAD));
     };
 
-    if (warp >= 8 && warp < 12) {
-        // ================================================ keys (warps 8, 9) and values (10, 11), half a tile each
-        const bool value = warp >= 10;
+    // Registers: 128 a thread at launch (512 threads); 200 for the softmax's two warpgroups and 56 for the other
+    // two are the same total.
+    if (warp >= ROLES) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    if (warp < ROLES + 4) {
+        // ================================================ keys (two warps) and values (two), half a tile each
+        const bool value = warp >= ROLES + 2;
         const int half = warp & 1, quad = lane & 15, row = half * 64 + quad * 4, block = lane >> 4;
         const int64_t* str = value ? a.vc : a.kc;
         const int* step = value ? maps.vs : maps.ks;
@@ -307,100 +325,97 @@ __global__ void __launch_bounds__(CNT, 1) chunk_tensor_kernel(const ChunkArgs a,
             give_back(s);
         }
         if (!ok) *dead = 1;
-    } else if (warp == 12) {
-        // ================================================ the first product
-        // (A whole warp runs each loop, so that addresses and descriptors stay in uniform registers; one elected
-        // lane issues.)
+    } else if (warp == ROLES + 4) {
+        // ================================================ products
+        // (The whole warp runs the loop and one elected lane issues; lengths are made uniform by reductions, so that
+        // operands and descriptors are computed in uniform registers.  Where the compiler cannot see that they
+        // are, it moves every one over for every instruction: 80 cycles each, of the 64 that it takes.)
         const bool lead = elect();
-        constexpr uint32_t QK = product<T>(CK, false);
+        constexpr uint32_t QK = product<T>(CK, false), PV = product<T>(D, true);
         const uint32_t q_op = (base & 0x3ffff) >> 4, k_op = ((base + S::KV) & 0x3ffff) >> 4, hi = operand_high();
+        const uint32_t tm = __reduce_max_sync(FULL, tmem);
         bool ok = true;
-        uint32_t seq = 0, uses[2] = {0, 0}, done[2] = {0, 0};   // copies; segments and products of each tile
+        uint32_t at = 0, lap = 0;       // the next copy's stage in the ring, and its parity
+        uint32_t uses[2] = {0, 0}, done[2] = {0, 0};   // segments and products P V of each tile, modulo 2
         for (uint32_t s = 0;; ++s) {
             const Segment& sg = next_segment(s, ok);
             if (!ok) break;
-            const int n = sg.n, tiles = sg.two() ? 2 : 1;
+            const uint32_t n = __reduce_max_sync(FULL, uint32_t(sg.n)), tiles = __reduce_max_sync(FULL, sg.two() ? 2u : 1u);
             if (n == 0) break;
             give_back(s);
-#pragma unroll 1
-            for (int i = 0; i < n && ok; ++i) {
-                const uint32_t c = seq + keys_copy(i), lap = c / ST, kst = c - lap * ST;
-                ok = __all_sync(FULL, bar_wait(full + 8 * kst, lap & 1, dead));
+            auto wait = [&](uint32_t bar, uint32_t parity) { ok = ok && __all_sync(FULL, bar_wait(bar, parity, dead)); };
+            auto scores = [&](bool last, int t, uint32_t st) {
+                const uint32_t q = q_op + t * (S::QTILE >> 4), k = k_op + st * (S::TILE >> 4);
 #pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    if (t >= tiles) break;
-                    if (i == 0) ok = ok && __all_sync(FULL, bar_wait(qbar + 8 * t, uses[t]++ & 1, dead));
-                    // the weights of the product before, in the same columns, have been read
-                    if (done[t] > 0) ok = ok && __all_sync(FULL, bar_wait(vbar + 8 * t, (done[t] - 1) & 1, dead));
-                    if (!ok) break;
-                    ++done[t];
+                for (int d = 0; d < D / 16; ++d)
+                    mma_smem(lead, tm + t * CK, q + (((d >> 2) * (CM * 128) + (d & 3) * 32) >> 4), 0,
+                             k + (((d >> 2) * (CK * 128) + (d & 3) * 32) >> 4), 0, hi, QK, d > 0);
+                mma_commit(lead, sbar + 8 * t);
+                if (last) mma_commit(lead, qfree + 8 * t);
+                if (t + 1 == int(tiles)) mma_commit(lead, empty + 8 * st);
+            };
+            auto weighted = [&](bool add, int t, uint32_t st) {
+                const uint32_t p = tm + t * CK, o = tm + 2 * CK + t * D, v = k_op + st * (S::TILE >> 4);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    wait(pbar + 16 * t + 8 * h, done[t]);
                     tmem_fence_after();
-                    const uint32_t q = q_op + t * (S::QTILE >> 4), k = k_op + kst * (S::TILE >> 4);
+                    if (ok) {
 #pragma unroll
-                    for (int d = 0; d < D / 16; ++d)
-                        mma_smem(lead, tmem + t * CK, q + (((d >> 2) * (CM * 128) + (d & 3) * 32) >> 4), 0,
-                                 k + (((d >> 2) * (CK * 128) + (d & 3) * 32) >> 4), 0, hi, QK, d > 0);
-                    mma_commit(lead, sbar + 8 * t);
-                    if (i == n - 1) mma_commit(lead, qfree + 8 * t);
+                        for (int k = 4 * h; k < 4 * h + 4; ++k)
+                            mma_tmem(lead, o, p + 8 * k, v + k * (2048 >> 4), CK * 128, hi, PV, add || k > 0);
+                    }
                 }
-                if (ok) mma_commit(lead, empty + 8 * kst);
+                done[t] ^= 1;
+                if (t + 1 == int(tiles)) mma_commit(lead, empty + 8 * st);
+            };
+            auto forward = [&](uint32_t& pos, uint32_t& par) { par ^= pos + 1 == ST ? 1 : 0, pos = pos + 1 == ST ? 0 : pos + 1; };
+            // (the segment before is done with the tiles' columns: its last weights have been issued for)
+            wait(full + 8 * at, lap);
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+                if (t < int(tiles)) {
+                    wait(qbar + 8 * t, uses[t]);
+                    uses[t] ^= 1;
+                    tmem_fence_after();
+                    if (ok) scores(n == 1, t, at);
+                }
+            forward(at, lap);
+#pragma unroll 1
+            for (uint32_t i = 0; i < n && ok; ++i) {
+                // the next keys, then these values; the last values alone
+                const bool more = i + 1 < n;
+                const uint32_t kst = at, kpar = lap;
+                if (more) forward(at, lap);
+                const uint32_t vst = at, vpar = lap;
+                forward(at, lap);
+                wait(full + 8 * vst, vpar);
+                weighted(i > 0, 0, vst);
+                if (more) {
+                    wait(full + 8 * kst, kpar);
+                    tmem_fence_after();
+                    if (ok) scores(i + 2 == n, 0, kst);
+                } else {
+                    mma_commit(lead, vbar);
+                }
+                if (tiles == 2) {
+                    weighted(i > 0, 1, vst);
+                    if (more) {
+                        if (ok) scores(i + 2 == n, 1, kst);
+                    } else {
+                        mma_commit(lead, vbar + 8);
+                    }
+                }
             }
             if (!ok) break;
-            seq += 2 * n;
         }
         if (!ok) {   // what has been issued finishes before the tensor memory is freed
             *dead = 1;
             mma_commit(lead, xbar);
-            for (uint32_t i = 0; i < SPIN && !bar_try(xbar, 0); ++i) {}
+            bar_drain(xbar);
         }
         __syncwarp();
-    } else if (warp == 13) {
-        // ================================================ the second product
-        const bool lead = elect();
-        constexpr uint32_t PV = product<T>(D, true);
-        const uint32_t v_op = ((base + S::KV) & 0x3ffff) >> 4, hi = operand_high();
-        bool ok = true;
-        uint32_t seq = 0, done[2] = {0, 0};
-        for (uint32_t s = 0;; ++s) {
-            const Segment& sg = next_segment(s, ok);
-            if (!ok) break;
-            const int n = sg.n, tiles = sg.two() ? 2 : 1;
-            if (n == 0) break;
-            give_back(s);
-#pragma unroll 1
-            for (int i = 0; i < n && ok; ++i) {
-                const uint32_t c = seq + values_copy(i, n), lap = c / ST, vst = c - lap * ST;
-                ok = __all_sync(FULL, bar_wait(full + 8 * vst, lap & 1, dead));
-                const uint32_t v = v_op + vst * (S::TILE >> 4);
-#pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    if (t >= tiles) break;
-                    const uint32_t p = tmem + t * CK, o = tmem + 2 * CK + t * D;
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        ok = ok && __all_sync(FULL, bar_wait(pbar + 16 * t + 8 * h, done[t] & 1, dead));
-                        if (!ok) break;
-                        tmem_fence_after();
-#pragma unroll
-                        for (int k = 4 * h; k < 4 * h + 4; ++k)
-                            mma_tmem(lead, o, p + 8 * k, v + k * (2048 >> 4), CK * 128, hi, PV, i > 0 || k > 0);
-                    }
-                    if (!ok) break;
-                    ++done[t];
-                    mma_commit(lead, vbar + 8 * t);
-                }
-                if (ok) mma_commit(lead, empty + 8 * vst);
-            }
-            if (!ok) break;
-            seq += 2 * n;
-        }
-        if (!ok) {
-            *dead = 1;
-            mma_commit(lead, xbar + 8);
-            for (uint32_t i = 0; i < SPIN && !bar_try(xbar + 8, 0); ++i) {}
-        }
-        __syncwarp();
-    } else if (warp == 14) {
+    } else if (warp == ROLES + 6) {
         // ================================================ what the next tiles are
         int tile = words[6];
         int64_t u = first_unit;
@@ -417,21 +432,25 @@ __global__ void __launch_bounds__(CNT, 1) chunk_tensor_kernel(const ChunkArgs a,
                 sg.M = sg.x.rows(a);
                 sg.p_lo = sg.x.pos(a, it.y), sg.p_hi = sg.x.pos(a, min(it.y + MANY, sg.M) - 1);
                 sg.kt = KeyTiles<CK>(a, sg.p_lo, sg.p_hi);
+                const int each = START + sg.kt.n;
                 const int64_t before = (int64_t(it.w) << 32 | uint32_t(it.z)) * a.Hkv, rel = u - before;
-                sg.head = int(rel / sg.kt.n);
-                sg.i0 = int(rel - int64_t(sg.head) * sg.kt.n);
-                sg.n = int(min(int64_t(sg.kt.n - sg.i0), last - u));
+                sg.head = int(rel / each);
+                const int64_t from = before + int64_t(sg.head) * each;     // of this head
+                sg.i0 = int(max(u - from - START, int64_t(0)));
+                sg.n = int(min(int64_t(each), last - from)) - START - sg.i0;
                 sg.whole = sg.n == sg.kt.n;
-                sg.parts = sg.whole || sg.i0 > 0 ? 0 : int((u + sg.kt.n - 1) / run) - int(blockIdx.x) + 1;
-                u += sg.n;
-                if (u >= before + int64_t(sg.kt.n) * a.Hkv) ++tile;
+                sg.parts = sg.whole || sg.i0 > 0 ? 0 : int((from + each - 1) / run) - int(blockIdx.x) + 1;
+                u = min(from + each, last);
+                if (u >= before + int64_t(each) * a.Hkv) ++tile;
+                // (a run that ends within a tile's START leaves all of it to the next)
+                if (sg.n <= 0) sg.n = 0;
             }
             if (lane == 0) segs[s % AHEAD] = sg;
             __syncwarp();
             if (lane == 0) bar_arrive(segbar + 8 * (s % AHEAD));
             if (sg.n == 0) break;
         }
-    } else if (warp == 15) {
+    } else if (warp == ROLES + 7) {
         // ================================================ queries
         bool ok = true;
         uint32_t uses[2] = {0, 0};
@@ -445,7 +464,15 @@ __global__ void __launch_bounds__(CNT, 1) chunk_tensor_kernel(const ChunkArgs a,
                 if (!ok) break;
                 ++uses[t];
                 const int row0 = sg.row0 + t * CM;
-                if (GATHER) {
+                if (GATHER && maps.qrows) {   // (rows behind the request's are computed, and not written)
+                    if (lane == 0) {
+                        bar_expect(qbar + 8 * t, CM * D * 2);
+#pragma unroll
+                        for (int b = 0; b < D / 64; ++b)
+                            copy_box(base + t * S::QTILE + b * (CM * 128), &maps.qbox, b * 64, sg.head * a.gs, sg.x.q0 + row0 / a.gs,
+                                     qbar + 8 * t);
+                    }
+                } else if (GATHER) {
                     int rows[4];
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
@@ -477,13 +504,15 @@ __global__ void __launch_bounds__(CNT, 1) chunk_tensor_kernel(const ChunkArgs a,
             give_back(s);
         }
         if (!ok) *dead = 1;
+    }
     } else {
         // ================================================ softmax
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
         const int t = warp >> 2, r = tid & 127;
         const uint32_t lanes = uint32_t(warp & 3) << 21;   // the warp's 32 lanes of tensor memory
         const uint32_t sc = tmem + t * CK + lanes, oc = tmem + 2 * CK + t * D + lanes;
         bool ok = true;
-        uint32_t done = 0, unit = 0;      // products of this tile; key tiles of segments before
+        uint32_t done = 0, unit = 0, ends = 0;      // scores of this tile; key tiles of segments before; segments of this tile
 #pragma unroll 1
         for (uint32_t s = 0; ok; ++s) {
             const Segment& sg = next_segment(s, ok);
@@ -530,19 +559,15 @@ __global__ void __launch_bounds__(CNT, 1) chunk_tensor_kernel(const ChunkArgs a,
                         tmem_wait_st();
                         mul = 1.f;
                     }
-                    float mx = -INFINITY;
-#pragma unroll 1
-                    for (int c = 0; c < CK; c += 64) {
-                        uint32_t x[64];
-                        tmem_ld32(part<32>(x, 0), sc + c);
-                        tmem_ld32(part<32>(x, 1), sc + c + 32);
-                        tmem_wait_ld();
-                        float m4[4] = {mx, mx, mx, mx};
+                    uint32_t x[CK];
 #pragma unroll
-                        for (int e = 0; e < 64; e += 2)
-                            m4[(e >> 1) & 3] = fmaxf(m4[(e >> 1) & 3], fmaxf(__uint_as_float(x[e]), __uint_as_float(x[e + 1])));
-                        mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
-                    }
+                    for (int c = 0; c < CK / 32; ++c) tmem_ld32(part<32>(x, c), sc + c * 32);
+                    tmem_wait_ld();
+                    float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                    for (int e = 0; e < CK; e += 2)
+                        m4[(e >> 1) & 3] = fmaxf(m4[(e >> 1) & 3], fmaxf(__uint_as_float(x[e]), __uint_as_float(x[e + 1])));
+                    float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
                     mx *= mul;
                     if (!(mx > -INFINITY)) mx = m;   // a scale of 0 times infinity, or nothing but NaN
                     if (__any_sync(FULL, mx - m > W::GROWTH)) {   // (the difference is exact where it decides)
@@ -553,13 +578,13 @@ __global__ void __launch_bounds__(CNT, 1) chunk_tensor_kernel(const ChunkArgs a,
                         if (i > 0) {
                             // (the last product of this tile was done before these scores were begun)
 #pragma unroll 1
-                            for (int c = 0; c < D; c += 32) {
-                                uint32_t y[32];
-                                tmem_ld32(y, oc + c);
+                            for (int c = 0; c < D; c += 16) {
+                                uint32_t y[16];
+                                tmem_ld16(y, oc + c);
                                 tmem_wait_ld();
 #pragma unroll
-                                for (int e = 0; e < 32; ++e) y[e] = __float_as_uint(__uint_as_float(y[e]) * f);
-                                tmem_st32(oc + c, y);
+                                for (int e = 0; e < 16; ++e) y[e] = __float_as_uint(__uint_as_float(y[e]) * f);
+                                tmem_st16(oc + c, y);
                             }
                         }
                     }
@@ -568,49 +593,36 @@ __global__ void __launch_bounds__(CNT, 1) chunk_tensor_kernel(const ChunkArgs a,
                     // A maximum is a rounded product and a weight's exponent below is not: beyond 2^20 their difference, up
                     // to 2^-25 of the maximum, would count in the exponent (at 2^31 it is 2^6 and more).
                     if (__any_sync(FULL, fabsf(m) > 0x1p20f && m > -INFINITY)) {
-#pragma unroll 1
-                        for (int c = 0; c < CK; c += 32) {
-                            uint32_t x[32];
-                            tmem_ld32(x, sc + c);
-                            tmem_wait_ld();
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(__fmul_rn(__uint_as_float(x[e]), mul) - ms);
-                            tmem_st32(sc + c, x);
-                        }
-                        tmem_wait_st();
+                        for (int e = 0; e < CK; ++e) x[e] = __float_as_uint(__fmul_rn(__uint_as_float(x[e]), mul) - ms);
                         mul = 1.f;
                         off = W::SHIFT;
                     }
-                    // ---- weights, 32 at a time; the next scores are read meanwhile
-                    float s0 = 0.f, s1 = 0.f;
-                    uint32_t x[2][32];
-                    tmem_ld32(x[0], sc);
-                    tmem_wait_ld();
-#pragma unroll 1
+                    // ---- weights
+                    float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
+#pragma unroll
                     for (int h = 0; h < 2; ++h) {
 #pragma unroll
-                        for (int b = 0; b < 2; ++b) {
-                            if (b == 0 || h == 0) tmem_ld32(x[b ^ 1], sc + 64 * h + 32 * b + 32);
-                            uint32_t p[16];
-#pragma unroll
-                            for (int e = 0; e < 32; e += 2) {
-                                float p0 = __uint_as_float(x[b][e]), p1 = __uint_as_float(x[b][e + 1]);
-                                fma_pair(p0, p1, mul, off);
-                                p0 = exp2_fast(p0), p1 = exp2_fast(p1);
-                                add_pair(s0, s1, p0, p1);
-                                p[e / 2] = Mma<T>::pack(p0, p1);
-                            }
-                            tmem_st16(sc + 32 * h + 16 * b, p);
-                            if (b == 0 || h == 0) tmem_wait_ld();
+                        for (int e = 64 * h; e < 64 * h + 64; e += 4) {
+                            float p0 = __uint_as_float(x[e]), p1 = __uint_as_float(x[e + 1]), p2 = __uint_as_float(x[e + 2]),
+                                  p3 = __uint_as_float(x[e + 3]);
+                            fma_pair(p0, p1, mul, off);
+                            fma_pair(p2, p3, mul, off);
+                            p0 = exp2_fast(p0), p1 = exp2_fast(p1), p2 = exp2_fast(p2), p3 = exp2_fast(p3);
+                            add_pair(s0, s1, p0, p1);
+                            add_pair(s2, s3, p2, p3);
+                            x[e / 2] = Mma<T>::pack(p0, p1);
+                            x[e / 2 + 1] = Mma<T>::pack(p2, p3);
                         }
+                        tmem_st32(sc + 32 * h, part<32>(x, h));
                         tmem_wait_st();
                         tmem_fence_before();
                         bar_arrive(pbar + 16 * t + 8 * h);
                     }
-                    l += s0 + s1;
+                    l += (s0 + s1) + (s2 + s3);
                 }
                 // ---- the row's output, once the last product is done
-                ok = ok && __all_sync(FULL, bar_wait(vbar + 8 * t, (done - 1) & 1, dead));
+                ok = ok && __all_sync(FULL, bar_wait(vbar + 8 * t, ends++ & 1, dead));
                 tmem_fence_after();
                 const float bad = (!ok || *dead) ? __int_as_float(0x7fffffff) : 0.f;
                 const float inv = (l == 0.f ? 0.f : 1.f / l) + bad;
@@ -640,15 +652,21 @@ __global__ void __launch_bounds__(CNT, 1) chunk_tensor_kernel(const ChunkArgs a,
                             }
                         }
                     }
+                    // 32 bytes a store, a whole sector, where the rows are aligned to it: 64 KB of 16-byte stores take 4000 cycles.
                     if (on && whole) {
                         auto two = [&](int e) { return Mma<T>::pack(__uint_as_float(y[e]), __uint_as_float(y[e + 1])); };
 #pragma unroll
-                        for (int e = 0; e < 32; e += 8)
-                            *reinterpret_cast<uint4*>(out + c + e) = make_uint4(two(e), two(e + 2), two(e + 4), two(e + 6));
+                        for (int e = 0; e < 32; e += 2) y[e / 2] = two(e);
+                        if (a.out_32) {
+                            store32(out + c, part<8>(y, 0));
+                            store32(out + c + 16, part<8>(y, 1));
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 16; e += 4) *reinterpret_cast<uint4*>(out + c + 2 * e) = make_uint4(y[e], y[e + 1], y[e + 2], y[e + 3]);
+                        }
                     } else if (on) {
 #pragma unroll
-                        for (int e = 0; e < 32; e += 4)
-                            *reinterpret_cast<uint4*>(a.t_part_o + slot * D + c + e) = make_uint4(y[e], y[e + 1], y[e + 2], y[e + 3]);
+                        for (int e = 0; e < 4; ++e) store32(a.t_part_o + slot * D + c + 8 * e, part<8>(y, e));
                     }
                     __syncwarp();   // (tensor memory is read by whole warps)
                 }
@@ -669,7 +687,7 @@ __global__ void __launch_bounds__(CNT, 1) chunk_tensor_kernel(const ChunkArgs a,
     tmem_fence_before();
     __syncthreads();
     tmem_fence_after();
-    if (warp == 12) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+    if (warp == ROLES + 4) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
 }
 
 // ------------------------------------------------------------------ host
@@ -760,6 +778,14 @@ static fs_status launch_type(const ChunkArgs& a, int dtype, int head_dim, void* 
     const bool gather = row_map(&maps.k, a.k, dtype, head_dim, 3, a.kc, cache, maps.ks) &&
                         row_map(&maps.v, a.v, dtype, head_dim, 3, a.vc, cache, maps.vs) &&
                         row_map(&maps.q, a.q, dtype, head_dim, 2, a.qs, query, maps.qs);
+    if (gather && CM % a.gs == 0) {
+        // (strides of dimensions of one element address nothing)
+        const cuuint64_t dims[3] = {cuuint64_t(head_dim), cuuint64_t(a.Hq), cuuint64_t(a.N)};
+        const int64_t by[2] = {a.Hq > 1 ? a.qs[1] : head_dim, a.N > 1 ? a.qs[0] : head_dim};
+        const cuuint64_t pitch[2] = {cuuint64_t(by[0]) * 2, cuuint64_t(by[1]) * 2};
+        const cuuint32_t box[3] = {64, cuuint32_t(a.gs), cuuint32_t(CM / a.gs)};
+        maps.qrows = by[0] >= head_dim && by[1] >= head_dim && tensor_map(&maps.qbox, a.q, dtype, 3, dims, pitch, box);
+    }
     if (gather && a.page_shift >= 3) {
         maps.box = std::min(a.page_size, 64);
         if (!box_map(&maps.kbox, a, a.k, dtype, head_dim, a.kc, maps.box) || !box_map(&maps.vbox, a, a.v, dtype, head_dim, a.vc, maps.box))

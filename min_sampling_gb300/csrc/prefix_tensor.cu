@@ -260,7 +260,7 @@ __global__ void __launch_bounds__(TNT, 1) prefix_tensor_kernel(const AttnArgs a)
             if (!ok) {   // what has been issued finishes before the tensor memory is freed
                 *dead = 1;
                 mma_commit(lead, ybar);
-                for (uint32_t i = 0; i < SPIN && !bar_try(ybar, 0); ++i) {}
+                bar_drain(ybar);
             }
         } else if (warp == 13) {
             // ---- weights times values
@@ -290,7 +290,7 @@ __global__ void __launch_bounds__(TNT, 1) prefix_tensor_kernel(const AttnArgs a)
             mma_commit(lead, xbar);   // every product is done
             if (!ok) {
                 *dead = 1;
-                for (uint32_t i = 0; i < SPIN && !bar_try(xbar, 0); ++i) {}
+                bar_drain(xbar);
             }
         }
         __syncwarp();

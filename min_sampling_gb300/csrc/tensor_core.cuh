@@ -8,7 +8,7 @@
 
 namespace fsd {
 
-constexpr uint32_t SPIN = 1u << 20;  // tries of at most about 2 us before a wait gives up
+constexpr long long PATIENCE = 4000000000ll;  // clock cycles, two seconds or more, before a wait gives up
 
 // ------------------------------------------------------------------ barriers
 
@@ -21,7 +21,7 @@ __device__ __forceinline__ void bar_arrive(uint32_t bar) {
 __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
     uint32_t ok;
     asm volatile(
-        "{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 2000; selp.u32 %0, 1, 0, p; }"
+        "{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
         : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
     return ok != 0;
 }
@@ -32,14 +32,25 @@ __device__ __forceinline__ bool bar_test(uint32_t bar, uint32_t parity) {
                  : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
     return ok != 0;
 }
-// False when the wait ran out here or in another role of the CTA.
+// False when the wait ran out here or in another role of the CTA.  (A try suspends the thread for some time by itself; with
+// a time of 2 us asked for, a warp woke up later: chunks of 1021 tokens behind 16384 431 us, 412 without.)
 __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile int* dead) {
-    for (uint32_t i = 0; i < SPIN; ++i) {
+    if (bar_try(bar, parity)) return true;
+    const long long start = clock64();
+    for (uint32_t i = 1;; ++i) {
         if (bar_try(bar, parity)) return true;
-        if ((i & 63) == 63 && *dead) return false;
+        if ((i & 7) == 0) {
+            if (*dead) return false;
+            if (clock64() - start > PATIENCE) break;
+        }
     }
     *dead = 1;
     return false;
+}
+// What has been issued on its way to a barrier, waited for by a role that gives up.
+__device__ __forceinline__ void bar_drain(uint32_t bar) {
+    const long long start = clock64();
+    while (!bar_try(bar, 0) && clock64() - start < PATIENCE) {}
 }
 
 // ------------------------------------------------------------------ tensor memory and matrix instructions

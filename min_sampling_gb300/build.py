@@ -28,7 +28,7 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libfs_sampling.so")
 DECODE = os.path.join(PKG, "_decode.so")
 SOURCES = ["sampling.cu", "renorm.cu", "speculative.cu", "uniforms.cu", "paged_kv.cu", "prefix_attention.cu",
-           "prefix_tensor.cu", "step_tables.cu", "chunk_attention.cu", "chunk_tensor.cu",
+           "prefix_tensor.cu", "step_tables.cu", "chunk_attention.cu", "chunk_few.cu", "chunk_tensor.cu",
            "adjust.cu", "api.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

@@ -10,6 +10,7 @@ namespace fsd {
 
 constexpr int FEW = 16;         // query rows that a tile of chunk_rows_kernel holds beside the tensor cores' tiles
 constexpr int MANY = 256;       // query rows of a tensor-core tile
+constexpr int FEW_START = 2;    // key tiles of 64 that start and end of such a tile take as long as
 constexpr int START = 3;        // key tiles that start and end of a tensor-core tile take as long as
 
 struct ChunkArgs {
@@ -85,6 +86,142 @@ __device__ __forceinline__ bool sees(const ChunkArgs& a, int p, int k) {
     return k <= p && (p - k < a.window || k < a.sinks);
 }
 
+// A key tile of KT keys from k0 on of which some token at p_lo .. p_hi does not see all the keys that are loaded.
+__device__ __forceinline__ bool partial_keys(const ChunkArgs& a, int p_lo, int p_hi, int k0, int KT) {
+    return p_lo != p_hi && (k0 + KT > p_lo + 1 || (p_hi - k0 >= a.window && k0 + KT > a.sinks));
+}
+
+// ------------------------------------------------------------------ the line of work
+
+// A CTA's place in the line of units.
+struct Place {
+    int r;              // request
+    int64_t before;     // the units before the request's
+    int64_t units;      // the request's units of one key/value head
+};
+
+// Units of one key/value head of a request that is not the tensor cores': key tiles, and FEW_START for each query tile.
+template <int MT, int KT>
+__device__ __forceinline__ int64_t units_of(const ChunkArgs& a, const Request& x) {
+    const int M = x.rows(a);
+    if (M == 0 || M > a.rows_upto) return 0;
+    int64_t n = 0;
+    for (int row = 0; row < M; row += MT) n += KeyTiles<KT>(a, x.pos(a, row), x.pos(a, min(row + MT, M) - 1)).n + FEW_START;
+    return n;
+}
+
+// Exclusive sum over a block of NT threads, and the total.
+template <int NT>
+__device__ __forceinline__ int64_t block_sum_before(int64_t mine, int64_t* words, int64_t& total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int64_t x = mine;
+#pragma unroll
+    for (int s = 1; s < 32; s <<= 1) {
+        const int64_t y = __shfl_up_sync(FULL, x, s);
+        if (lane >= s) x += y;
+    }
+    if (lane == 31) words[warp] = x;
+    __syncthreads();
+    int64_t before = 0;
+    total = 0;
+#pragma unroll
+    for (int w = 0; w < NT / 32; ++w) {
+        if (w == warp) before = total;
+        total += words[w];
+    }
+    __syncthreads();
+    return before + x - mine;
+}
+
+// The tensor cores' tiles: MANY query rows of a request each, with the units before them. By one CTA.
+template <int NT>
+__device__ __forceinline__ void plan_tiles(const ChunkArgs& a, int64_t* words) {
+    const int tid = threadIdx.x;
+    auto tiles_of = [&](int r) {
+        const int M = request(a, r).rows(a);
+        return M > a.rows_upto ? (M + MANY - 1) / MANY : 0;
+    };
+    int64_t total, mine = 0;
+    const int per = (a.R + NT - 1) / NT, r0 = min(tid * per, a.R), r1 = min(r0 + per, a.R);
+    for (int r = r0; r < r1; ++r) mine += tiles_of(r);
+    int64_t at = block_sum_before<NT>(mine, words, total);
+    for (int r = r0; r < r1; ++r) {
+        a.t_first[r] = int(min(at, int64_t(a.t_tiles)));
+        at += tiles_of(r);
+    }
+    const int n = int(min(total, int64_t(a.t_tiles)));   // (no more unless query_starts descends)
+    if (tid == 0) a.t_first[a.R] = n;
+    __syncthreads();
+    const int each = (n + NT - 1) / NT, i0 = min(tid * each, n), i1 = min(i0 + each, n);
+    int first = 0;      // the request of tile i0: the last one that has no more than i0 tiles before it
+    for (int hi = a.R; i0 < i1 && hi - first > 1;) {
+        const int mid = (first + hi) / 2;
+        if (a.t_first[mid] <= i0) first = mid;
+        else hi = mid;
+    }
+    auto units = [&](int& r, int i, int& row0) {
+        while (a.t_first[r + 1] <= i) ++r;
+        row0 = (i - a.t_first[r]) * MANY;
+        const Request x = request(a, r);
+        return KeyTiles<128>(a, x.pos(a, row0), x.pos(a, min(row0 + MANY, x.rows(a)) - 1)).n;
+    };
+    mine = 0;
+    int row0;
+    for (int i = i0, r = first; i < i1; ++i) mine += units(r, i, row0) + START;
+    at = block_sum_before<NT>(mine, words, total);
+    for (int i = i0, r = first; i < i1; ++i) {
+        const int u = units(r, i, row0) + START;
+        a.t_items[i] = make_int4(r, row0, int(uint32_t(at)), int(at >> 32));
+        at += u;
+    }
+    if (tid == 0) a.t_plan[0] = n, a.t_plan[1] = int(uint32_t(total)), a.t_plan[2] = int(total >> 32);
+}
+
+// A CTA's run of units, cut from all of the launch's in equal lengths.
+struct Run {
+    int64_t first, last, length;
+    Place place;
+};
+template <int NT, int MT, int KT>
+__device__ __forceinline__ Run run_of(const ChunkArgs& a, int cta, int64_t* words) {
+    const int tid = threadIdx.x, per = (a.R + NT - 1) / NT, r0 = min(tid * per, a.R), r1 = min(r0 + per, a.R);
+    int64_t mine = 0;
+    for (int r = r0; r < r1; ++r) mine += units_of<MT, KT>(a, request(a, r));
+    int64_t total, before = block_sum_before<NT>(mine, words, total);
+    total *= a.Hkv;
+    Run run;
+    run.length = max(int64_t(a.least), (total + a.grid - 1) / a.grid);
+    run.first = min(cta * run.length, total);
+    run.last = min(run.first + run.length, total);
+    if (run.first < run.last && before * a.Hkv <= run.first && run.first < (before + mine) * a.Hkv) {
+        for (int r = r0; r < r1; ++r) {
+            const int64_t n = units_of<MT, KT>(a, request(a, r));
+            if (run.first < (before + n) * a.Hkv) {
+                words[16] = r, words[17] = before * a.Hkv, words[18] = n;
+                break;
+            }
+            before += n;
+        }
+    }
+    __syncthreads();
+    run.place = Place{run.first < run.last ? int(words[16]) : 0, words[17], words[18]};
+    __syncthreads();
+    return run;
+}
+
+// Rows of no request become zeros.
+template <typename T, int D>
+__device__ __forceinline__ void zero_rest(const ChunkArgs& a, int cta, int threads) {
+    constexpr int DC = D / 8;
+    const int lo = a.R > 0 ? min(max(a.starts[0], 0), a.N) : a.N, hi = a.R > 0 ? max(min(max(a.starts[a.R], 0), a.N), lo) : a.N;
+    const int rest = lo + a.N - hi;
+    for (int64_t i = int64_t(cta) * threads + threadIdx.x; i < int64_t(rest) * a.Hq * DC; i += int64_t(a.grid) * threads) {
+        const int c = int(i % DC), h = int(i / DC % a.Hq), j = int(i / DC / a.Hq), t = j < lo ? j : hi + j - lo;
+        *reinterpret_cast<uint4*>(static_cast<T*>(a.out) + t * a.os[0] + h * a.os[1] + c * 8) = make_uint4(0, 0, 0, 0);
+        if (c == 0 && a.lse) a.lse[int64_t(t) * a.Hq + h] = -INFINITY;
+    }
+}
+
 // ------------------------------------------------------------------ infinite and NaN values
 
 // Whether an element of a 16-byte word is infinite or NaN, and the word with zeros in their place.
@@ -134,7 +271,10 @@ static __device__ __noinline__ unsigned missing_pages(const ChunkArgs& a, int r,
     return bits;
 }
 
-// The tensor cores' part (chunk_tensor.cu): requests of more than rows_upto query rows, for heads of 64 or 128.
-fs_status launch_chunk_tensor(const ChunkArgs& a, int dtype, int head_dim, void* stream);
+// Requests of up to FEW query rows (chunk_few.cu); of more, for heads of 64 or 128, on the tensor cores (chunk_tensor.cu; without
+// maps: nullptr).
+struct ChunkMaps;
+fs_status launch_chunk_few(const ChunkArgs& a, const ChunkMaps& maps, int dtype, int head_dim, void* stream);
+fs_status launch_chunk_tensor(const ChunkArgs& a, const ChunkMaps* maps, int dtype, int head_dim, void* stream);
 
 }  // namespace fsd

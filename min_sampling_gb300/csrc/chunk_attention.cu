@@ -12,12 +12,15 @@
 // their maxima and sums in a fixed order (join_chunk_kernel; no atomics):
 //   m = max_i m_i,  l = sum_i 2^(m_i - m) l_i,  out = sum_i 2^(m_i - m) l_i out_i / l.
 //
-// chunk_rows_kernel: mma.sync, tiles of 16 rows (single tokens) or 64.  chunk_tensor.cu: more rows, on
-// the 5th-generation tensor cores.
+// chunk_few.cu: requests of up to 16 rows, single tokens above all.  chunk_tensor.cu: more rows, on the
+// 5th-generation tensor cores.  chunk_rows_kernel (mma.sync): many rows of heads of 256, and a few where the caches'
+// strides have no map for the copy engine.
 #include "chunk.cuh"
 
+#include <numeric>
 #include <type_traits>
 
+#include "chunk_copy.cuh"
 #include "fragments.cuh"
 
 namespace fsd {
@@ -32,90 +35,6 @@ struct ChunkSmem {
     static constexpr int OFF = KV + CSTAGES * 2 * TILE;
     static constexpr int TOTAL = OFF + 2 * 2 * KT * 8 + 256;
 };
-
-// A CTA's place in the line of units.
-struct Place {
-    int r;              // request
-    int64_t at, before; // unit, and the units before the request's
-    int64_t units;      // the request's units of one key/value head
-};
-
-// Units of one key/value head of a request that chunk_rows_kernel takes.
-template <int MT, int KT>
-__device__ __forceinline__ int64_t units_of(const ChunkArgs& a, const Request& x) {
-    const int M = x.rows(a);
-    if (M == 0 || M > a.rows_upto) return 0;
-    int64_t n = 0;
-    for (int row = 0; row < M; row += MT) n += KeyTiles<KT>(a, x.pos(a, row), x.pos(a, min(row + MT, M) - 1)).n;
-    return n;
-}
-
-// Exclusive sum over a block of NT threads, and the total.
-template <int NT>
-__device__ __forceinline__ int64_t block_sum_before(int64_t mine, int64_t* words, int64_t& total) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int64_t x = mine;
-#pragma unroll
-    for (int s = 1; s < 32; s <<= 1) {
-        const int64_t y = __shfl_up_sync(FULL, x, s);
-        if (lane >= s) x += y;
-    }
-    if (lane == 31) words[warp] = x;
-    __syncthreads();
-    int64_t before = 0;
-    total = 0;
-#pragma unroll
-    for (int w = 0; w < NT / 32; ++w) {
-        if (w == warp) before = total;
-        total += words[w];
-    }
-    __syncthreads();
-    return before + x - mine;
-}
-
-// The tensor cores' tiles: MANY query rows of a request each, with the units before them. By one CTA.
-template <int NT>
-__device__ __forceinline__ void plan_tiles(const ChunkArgs& a, int64_t* words) {
-    const int tid = threadIdx.x;
-    auto tiles_of = [&](int r) {
-        const int M = request(a, r).rows(a);
-        return M > a.rows_upto ? (M + MANY - 1) / MANY : 0;
-    };
-    int64_t total, mine = 0;
-    const int per = (a.R + NT - 1) / NT, r0 = min(tid * per, a.R), r1 = min(r0 + per, a.R);
-    for (int r = r0; r < r1; ++r) mine += tiles_of(r);
-    int64_t at = block_sum_before<NT>(mine, words, total);
-    for (int r = r0; r < r1; ++r) {
-        a.t_first[r] = int(min(at, int64_t(a.t_tiles)));
-        at += tiles_of(r);
-    }
-    const int n = int(min(total, int64_t(a.t_tiles)));   // (no more unless query_starts descends)
-    if (tid == 0) a.t_first[a.R] = n;
-    __syncthreads();
-    const int each = (n + NT - 1) / NT, i0 = min(tid * each, n), i1 = min(i0 + each, n);
-    int first = 0;      // the request of tile i0: the last one that has no more than i0 tiles before it
-    for (int hi = a.R; i0 < i1 && hi - first > 1;) {
-        const int mid = (first + hi) / 2;
-        if (a.t_first[mid] <= i0) first = mid;
-        else hi = mid;
-    }
-    auto units = [&](int& r, int i, int& row0) {
-        while (a.t_first[r + 1] <= i) ++r;
-        row0 = (i - a.t_first[r]) * MANY;
-        const Request x = request(a, r);
-        return KeyTiles<128>(a, x.pos(a, row0), x.pos(a, min(row0 + MANY, x.rows(a)) - 1)).n;
-    };
-    mine = 0;
-    int row0;
-    for (int i = i0, r = first; i < i1; ++i) mine += units(r, i, row0) + START;
-    at = block_sum_before<NT>(mine, words, total);
-    for (int i = i0, r = first; i < i1; ++i) {
-        const int u = units(r, i, row0) + START;
-        a.t_items[i] = make_int4(r, row0, int(uint32_t(at)), int(at >> 32));
-        at += u;
-    }
-    if (tid == 0) a.t_plan[0] = n, a.t_plan[1] = int(uint32_t(total)), a.t_plan[2] = int(total >> 32);
-}
 
 // WM x WN warps over a tile of MT = 16 RM WM query rows and KT keys; each warp keeps its own running
 // maximum, sum and output over its share of the keys.  Bound by the reads of keys and values.
@@ -147,41 +66,12 @@ __global__ void __launch_bounds__(32 * WM * WN) chunk_rows_kernel(const ChunkArg
     const int cta = int(blockIdx.x) - (a.t_grid > 0);
 
     // ---- this CTA's run of units
-    int64_t unit, last, run;
-    Place pl;
-    {
-        const int per = (a.R + NT - 1) / NT, r0 = min(tid * per, a.R), r1 = min(r0 + per, a.R);
-        int64_t mine = 0;
-        for (int r = r0; r < r1; ++r) mine += units_of<MT, KT>(a, request(a, r));
-        int64_t total, before = block_sum_before<NT>(mine, words, total);
-        total *= a.Hkv;
-        run = max(int64_t(a.least), (total + a.grid - 1) / a.grid);
-        unit = min(cta * run, total);
-        last = min(unit + run, total);
-        if (unit < last && before * a.Hkv <= unit && unit < (before + mine) * a.Hkv) {
-            for (int r = r0; r < r1; ++r) {
-                const int64_t n = units_of<MT, KT>(a, request(a, r));
-                if (unit < (before + n) * a.Hkv) {
-                    words[16] = r, words[17] = before * a.Hkv, words[18] = n;
-                    break;
-                }
-                before += n;
-            }
-        }
-        if (tid == 0) a.split[cta] = make_int4(0, 0, 0, 0);
-        __syncthreads();
-        pl = Place{int(words[16]), unit, words[17], words[18]};
-    }
-    if (a.zero_rest) {
-        // rows of no request
-        const int lo = a.R > 0 ? min(max(a.starts[0], 0), a.N) : a.N, hi = a.R > 0 ? max(min(max(a.starts[a.R], 0), a.N), lo) : a.N;
-        const int rest = lo + a.N - hi;
-        for (int64_t i = int64_t(cta) * NT + tid; i < int64_t(rest) * a.Hq * DC; i += int64_t(a.grid) * NT) {
-            const int c = int(i % DC), h = int(i / DC % a.Hq), j = int(i / DC / a.Hq), t = j < lo ? j : hi + j - lo;
-            *reinterpret_cast<uint4*>(static_cast<T*>(a.out) + t * a.os[0] + h * a.os[1] + c * 8) = make_uint4(0, 0, 0, 0);
-            if (c == 0 && a.lse) a.lse[int64_t(t) * a.Hq + h] = -INFINITY;
-        }
-    }
+    const Run line = run_of<NT, MT, KT>(a, cta, words);
+    const int64_t run = line.length, last = line.last;
+    int64_t unit = line.first;
+    Place pl = line.place;
+    if (tid == 0) a.split[cta] = make_int4(0, 0, 0, 0);
+    if (a.zero_rest) zero_rest<T, D>(a, cta, NT);
 
 #pragma unroll 1
     while (unit < last) {
@@ -197,20 +87,21 @@ __global__ void __launch_bounds__(32 * WM * WN) chunk_rows_kernel(const ChunkArg
         int64_t first = pl.before + head * pl.units;   // the tile's first unit
         int row0 = 0;
         KeyTiles<KT> kt(a, x.pos(a, 0), x.pos(a, min(MT, M) - 1));
-        while (unit >= first + kt.n) {
-            first += kt.n;
+        while (unit >= first + kt.n + FEW_START) {
+            first += kt.n + FEW_START;
             row0 += MT;
             kt = KeyTiles<KT>(a, x.pos(a, row0), x.pos(a, min(row0 + MT, M) - 1));
         }
-        const int i0 = int(unit - first), i1 = int(min(int64_t(kt.n), last - first));   // its key tiles in this run
+        // its key tiles in this run
+        const int64_t after = first + kt.n + FEW_START;
+        const int i0 = int(max(unit - first - FEW_START, int64_t(0))), i1 = max(int(min(after, last) - first) - FEW_START, i0);
+        unit = min(after, last);
+        if (i1 == i0) break;   // (a run that ends within a tile's FEW_START leaves all of it to the next)
         const bool whole = i0 == 0 && i1 == kt.n;
         const int p_lo = x.pos(a, row0), p_hi = x.pos(a, min(row0 + MT, M) - 1);
         const int* table = a.table + int64_t(pl.r) * a.width;
         const int tiles = i1 - i0;
-        // A key tile of which some token of the query tile does not see all the keys that are loaded.
-        auto partial = [&](int k0) {
-            return p_lo != p_hi && (k0 + KT > p_lo + 1 || (p_hi - k0 >= a.window && k0 + KT > a.sinks));
-        };
+        auto partial = [&](int k0) { return partial_keys(a, p_lo, p_hi, k0, KT); };
 
         __syncthreads();   // the tile before is done with shared memory
         for (int i = tid; i < MT * DC; i += NT) {
@@ -486,8 +377,7 @@ __global__ void __launch_bounds__(32 * WM * WN) chunk_rows_kernel(const ChunkArg
             }
         }
         if (!whole && i0 == 0 && tid == 0)   // this CTA has the tile's first part and says how many CTAs have one
-            a.split[cta] = make_int4(pl.r, head, row0, int((first + kt.n - 1) / run) - cta + 1);
-        unit += tiles;
+            a.split[cta] = make_int4(pl.r, head, row0, int((after - 1) / run) - cta + 1);
     }
 }
 
@@ -559,6 +449,90 @@ static fs_status launch_pdl(void (*kernel)(P...), dim3 grid, unsigned block, siz
     return e == cudaSuccess ? FS_OK : cuda_fail(e);
 }
 
+using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                            const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                            CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+static Encode encoder() {
+    static const Encode fn = [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult found;
+        const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &found);
+        if (e != cudaSuccess) cudaGetLastError();
+        return e == cudaSuccess && found == cudaDriverEntryPointSuccess ? reinterpret_cast<Encode>(p) : nullptr;
+    }();
+    return fn;
+}
+
+static bool tensor_map(CUtensorMap* map, const void* base, int dtype, int rank, const cuuint64_t* dims, const cuuint64_t* pitch,
+                       const cuuint32_t* box) {
+    const cuuint32_t ones[4] = {1, 1, 1, 1};
+    const Encode encode = encoder();
+    return encode && encode(map, dtype == FS_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, rank,
+                            const_cast<void*>(base), dims, pitch, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Rows of `dim` elements at offsets sum_i x_i strides[i], x_i < sizes[i], as the rows of one matrix: row number sum_i x_i
+// steps[i].  False where the strides have no common divisor of a row's length or more.
+static bool row_map(CUtensorMap* map, const void* base, int dtype, int dim, int n, const int64_t* strides, const int64_t* sizes,
+                    int* steps) {
+    int64_t g = 0;
+    for (int i = 0; i < n; ++i) {
+        if (sizes[i] < 2) continue;
+        if (strides[i] < 0) return false;
+        g = std::gcd(g, strides[i]);
+    }
+    if (g == 0) g = dim;
+    if (g < dim || g >= int64_t(1) << 36) return false;
+    int64_t last = 0;
+    for (int i = 0; i < n; ++i) {
+        const int64_t step = sizes[i] < 2 ? 0 : strides[i] / g;
+        if (step > 0 && (sizes[i] - 1) > (int64_t(0x7ffffffe) - last) / step) return false;
+        steps[i] = int(step);
+        last += step * (std::max<int64_t>(sizes[i], 1) - 1);
+    }
+    const cuuint64_t dims[2] = {cuuint64_t(dim), cuuint64_t(last + 1)}, pitch[1] = {cuuint64_t(g) * 2};
+    const cuuint32_t box[2] = {64, 1};
+    return tensor_map(map, base, dtype, 2, dims, pitch, box);
+}
+
+// Boxes of `rows` slots of a page.
+static bool box_map(CUtensorMap* map, const ChunkArgs& a, const void* base, int dtype, int dim, const int64_t* strides, int rows) {
+    const int64_t sizes[3] = {a.page_size, a.Hkv, std::max(a.num_pages, 1)}, by[3] = {strides[1], strides[2], strides[0]};
+    const cuuint64_t dims[4] = {cuuint64_t(dim), cuuint64_t(sizes[0]), cuuint64_t(sizes[1]), cuuint64_t(sizes[2])};
+    cuuint64_t pitch[3];
+    for (int i = 0; i < 3; ++i) {
+        if (sizes[i] > 1 && (by[i] < dim || by[i] >= int64_t(1) << 38)) return false;
+        pitch[i] = sizes[i] > 1 ? cuuint64_t(by[i]) * 2 : cuuint64_t(dim) * 2;
+    }
+    const cuuint32_t box[4] = {64, cuuint32_t(rows), 1, 1};
+    return tensor_map(map, base, dtype, 4, dims, pitch, box);
+}
+bool chunk_maps(const ChunkArgs& a, int dtype, int head_dim, ChunkMaps& m) {
+    const int64_t cache[3] = {a.num_pages, a.page_size, a.Hkv}, query[2] = {a.N, a.Hq};
+    if (!row_map(&m.k.rows, a.k, dtype, head_dim, 3, a.kc, cache, m.k.step) ||
+        !row_map(&m.v.rows, a.v, dtype, head_dim, 3, a.vc, cache, m.v.step) ||
+        !row_map(&m.q.rows, a.q, dtype, head_dim, 2, a.qs, query, m.q.step))
+        return false;
+    if (a.page_shift >= 3) {
+        m.k.box = m.v.box = std::min(a.page_size, 64);
+        if (!box_map(&m.k.boxes, a, a.k, dtype, head_dim, a.kc, m.k.box)) m.k.box = 0;
+        if (!box_map(&m.v.boxes, a, a.v, dtype, head_dim, a.vc, m.v.box)) m.v.box = 0;
+    }
+    constexpr int ROWS = MANY / 2;
+    if (ROWS % a.gs == 0) {
+        // (strides of dimensions of one element address nothing)
+        const cuuint64_t dims[3] = {cuuint64_t(head_dim), cuuint64_t(a.Hq), cuuint64_t(a.N)};
+        const int64_t by[2] = {a.Hq > 1 ? a.qs[1] : head_dim, a.N > 1 ? a.qs[0] : head_dim};
+        const cuuint64_t pitch[2] = {cuuint64_t(by[0]) * 2, cuuint64_t(by[1]) * 2};
+        const cuuint32_t box[3] = {64, cuuint32_t(a.gs), cuuint32_t(ROWS / a.gs)};
+        m.qrows = by[0] >= head_dim && by[1] >= head_dim && tensor_map(&m.q.boxes, a.q, dtype, 3, dims, pitch, box);
+    }
+    return true;
+}
+
 // Tiles and CTAs of a call, and the bytes of its parts.
 struct ChunkPlan {
     int MT, KT;         // chunk_rows_kernel's tile
@@ -582,11 +556,11 @@ static ChunkPlan chunk_plan(const fs_paged_kv& c, int N, int R, int Hq, int widt
     const bool tensor = D <= 128 && rows > FEW;
     p.MT = rows <= FEW || tensor ? FEW : 64;
     p.KT = D == 256 && p.MT == 64 ? 32 : 64;
-    // Three CTAs fit an SM (two with heads of 256); no more than there can be units.
-    p.least = 2;
+    // Two CTAs fit an SM (one with heads of 256); no more than there can be units.
+    p.least = FEW_START + 2;
     const int64_t tiles = (int64_t(N) * gs + p.MT - 1) / p.MT + R;
-    const int64_t units = tiles * c.num_heads * ((int64_t(width) * c.page_size + p.KT - 1) / p.KT + 2);
-    p.grid = int(std::max<int64_t>(1, std::min<int64_t>(int64_t(sms) * (D == 256 ? 2 : 3), (units + p.least - 1) / p.least)));
+    const int64_t units = tiles * c.num_heads * ((int64_t(width) * c.page_size + p.KT - 1) / p.KT + 2 + FEW_START);
+    p.grid = int(std::max<int64_t>(1, std::min<int64_t>(int64_t(sms) * (D == 256 && p.MT == FEW ? 1 : 2), (units + p.least - 1) / p.least)));
     size_t at = 0;
     p.part_o = add_bytes(at, size_t(2) * p.grid * p.MT * D * 4);
     p.part_l = add_bytes(at, size_t(2) * p.grid * p.MT * 4);
@@ -619,11 +593,13 @@ static fs_status launch_rows(const ChunkArgs& a, void* stream) {
 
 template <typename T, int D>
 static fs_status run_chunk(ChunkArgs& a, const ChunkPlan& p, int dtype, void* stream) {
+    ChunkMaps maps = {};
+    const bool mapped = chunk_maps(a, dtype, D, maps);
     fs_status st;
-    if (p.MT == FEW) st = launch_rows<T, D, FEW, 1, 4, 1, 64>(a, stream);
+    if (p.MT == FEW) st = mapped ? launch_chunk_few(a, maps, dtype, D, stream) : launch_rows<T, D, FEW, 1, 4, 1, 64>(a, stream);
     else if constexpr (D == 256) st = launch_rows<T, D, 64, 4, 1, 1, 32>(a, stream);
     else st = FS_ERR_INVALID_ARG;   // (heads of up to 128 go to the tensor cores)
-    if (st == FS_OK && a.t_grid > 0) st = launch_chunk_tensor(a, dtype, D, stream);
+    if (st == FS_OK && a.t_grid > 0) st = launch_chunk_tensor(a, mapped ? &maps : nullptr, dtype, D, stream);
     if (st != FS_OK) return st;
     return launch_pdl(join_chunk_kernel<T, D>, dim3(unsigned(a.grid * (p.MT / 16) + a.t_grid * (MANY / 16))), 128, 0, stream, a,
                       p.MT / 16);

@@ -17,12 +17,7 @@
 // not 64: the first product reads both operands from shared memory, at 64 keys 48 cycles an instruction of
 // 32, at 128 as many as it takes.)
 //
-// Copies go by TMA (GATHER).  Key tiles of which every key is there are boxes of up to 64 slots of a page, for pages of
-// 8, 16, 32 ... slots.  The others, and all of other page sizes, are gathers of four rows: caches and queries are
-// matrices whose rows lie a common divisor of their strides apart, so any page size and order of slots and heads is
-// a list of row numbers, and a key that no query sees is a row outside, which reads as zeros.  (A gather
-// of 512 bytes takes the copy engine about 33 cycles, 4250 for the keys and values of 128.)  Where the
-// strides have no such divisor, 16-byte asynchronous copies.
+// Copies: see chunk_copy.cuh; without maps (GATHER = false) 16-byte asynchronous copies.
 //
 // The softmax's code is short loops over 32 scores, read from tensor memory once for the maximum and once for
 // the weights: with 128 scores in registers and everything unrolled the warps of the other roles and the two tiles'
@@ -33,12 +28,7 @@
 // roles walk the run's tiles at their own pace, so keys of the next tile are on their way while one is finished.
 // Every wait on a barrier is bounded; one that runs out marks the CTA, which then drains its copies
 // and products, frees its tensor memory and writes NaN.
-#include "chunk.cuh"
-#include "tensor_core.cuh"
-
-#include <numeric>
-
-#include <cuda.h>
+#include "chunk_copy.cuh"
 
 namespace fsd {
 
@@ -56,10 +46,7 @@ struct Segment {
     KeyTiles<CK> kt;
     int p_lo, p_hi;             // positions of the first and last token
     __device__ __forceinline__ bool two() const { return M - row0 > CM; }   // rows for the second tile
-    // Key tile of which some token of the query tile does not see all the keys that are loaded.
-    __device__ __forceinline__ bool partial(const ChunkArgs& a, int k0) const {
-        return p_lo != p_hi && (k0 + CK > p_lo + 1 || (p_hi - k0 >= a.window && k0 + CK > a.sinks));
-    }
+    __device__ __forceinline__ bool partial(const ChunkArgs& a, int k0) const { return partial_keys(a, p_lo, p_hi, k0, CK); }
 };
 
 template <int D>
@@ -75,16 +62,6 @@ struct ChunkTensorSmem {
     static_assert(TOTAL <= 227 * 1024, "shared memory");
 };
 
-// Matrices of which the copies gather rows: row numbers of a page, a slot, a head (a token, a head).
-struct ChunkMaps {
-    CUtensorMap k, v, q;
-    int ks[3], vs[3], qs[2];
-    int box;                    // rows of a box, 0: gathers only
-    CUtensorMap kbox, vbox;     // [pages][heads][slots][dim]
-    int qrows;                  // all of a tile's queries are one box
-    CUtensorMap qbox;           // [tokens][heads][dim]
-};
-
 // Two floats at a time.
 __device__ __forceinline__ void fma_pair(float& x, float& y, float mul, float add) {
     asm("{ .reg .b64 a, b, c; mov.b64 a, {%0, %1}; mov.b64 b, {%2, %2}; mov.b64 c, {%3, %3};"
@@ -93,24 +70,6 @@ __device__ __forceinline__ void fma_pair(float& x, float& y, float mul, float ad
 __device__ __forceinline__ void add_pair(float& x, float& y, float a, float b) {
     asm("{ .reg .b64 a, b; mov.b64 a, {%0, %1}; mov.b64 b, {%2, %3}; add.rn.f32x2 a, a, b; mov.b64 {%0, %1}, a; }"
         : "+f"(x), "+f"(y) : "f"(a), "f"(b));
-}
-
-// Four rows of 64 elements from element x of each on, into 512 bytes of a swizzled tile.
-__device__ __forceinline__ void gather4(uint32_t dst, const CUtensorMap* map, int x, const int (&row)[4], uint32_t bar) {
-    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5, %6}], [%7];"
-                 ::"r"(dst), "l"(map), "r"(x), "r"(row[0]), "r"(row[1]), "r"(row[2]), "r"(row[3]), "r"(bar) : "memory");
-}
-// A box of a page's slots, 64 elements of each.
-__device__ __forceinline__ void copy_box(uint32_t dst, const CUtensorMap* map, int x, int slot, int head, int page, uint32_t bar) {
-    asm volatile("cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];"
-                 ::"r"(dst), "l"(map), "r"(x), "r"(slot), "r"(head), "r"(page), "r"(bar) : "memory");
-}
-__device__ __forceinline__ void copy_box(uint32_t dst, const CUtensorMap* map, int x, int head, int token, uint32_t bar) {
-    asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
-                 ::"r"(dst), "l"(map), "r"(x), "r"(head), "r"(token), "r"(bar) : "memory");
-}
-__device__ __forceinline__ void bar_expect(uint32_t bar, uint32_t bytes) {
-    asm volatile("{ .reg .b64 t; mbarrier.arrive.expect_tx.shared::cta.b64 t, [%0], %1; }" ::"r"(bar), "r"(bytes) : "memory");
 }
 
 __device__ __forceinline__ void store32(void* p, const uint32_t (&x)[8]) {
@@ -202,10 +161,8 @@ __global__ void __launch_bounds__(CNT, 1) chunk_tensor_kernel(const ChunkArgs a,
     if (warp < ROLES + 4) {
         // ================================================ keys (two warps) and values (two), half a tile each
         const bool value = warp >= ROLES + 2;
-        const int half = warp & 1, quad = lane & 15, row = half * 64 + quad * 4, block = lane >> 4;
+        const int half = warp & 1, row = half * 64 + (lane & 15) * 4;
         const int64_t* str = value ? a.vc : a.kc;
-        const int* step = value ? maps.vs : maps.ks;
-        const CUtensorMap* map = value ? &maps.v : &maps.k;
         uint32_t seq = 0, unit = 0, landed = 0;   // copies and key tiles before the segment; value tiles looked through
         bool ok = true;
         for (uint32_t s = 0;; ++s) {
@@ -215,23 +172,9 @@ __global__ void __launch_bounds__(CNT, 1) chunk_tensor_kernel(const ChunkArgs a,
             if (n == 0) break;
             const KeyTiles<CK> kt = sg.kt;
             const int* table = a.table + int64_t(sg.r) * a.width;
-            // The pages of this lane's four keys of a tile; -1 for a key that no query of the tile sees, -2 for a
-            // page that does not exist.
-            int pg[4];
+            Pages pages;
             auto look_up = [&](int i) {
-                if (i >= n) return;
-                const int key = kt.at(i0 + i) + row;
-                const bool one = a.page_shift >= 2;   // four keys of one page
-                int page = -1;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    if (j == 0 || !one) {
-                        const int pi = a.page_shift >= 0 ? (key + j) >> a.page_shift : (key + j) / a.page_size;
-                        page = pi < a.width ? table[pi] : -2;
-                        if (page < 0 || page >= a.num_pages) page = -2;
-                    }
-                    pg[j] = kt.seen(key + j) ? page : -1;
-                }
+                if (i < n) pages.look_up(a, table, kt.at(i0 + i) + row);
             };
             look_up(0);
 #pragma unroll 1
@@ -242,8 +185,7 @@ __global__ void __launch_bounds__(CNT, 1) chunk_tensor_kernel(const ChunkArgs a,
                     ok = false;
                     break;
                 }
-                // Which keys' pages do not exist: their scores are NaN for every query that sees them.
-                const bool gone = pg[0] == -2 || pg[1] == -2 || pg[2] == -2 || pg[3] == -2;
+                const bool gone = pages.resolve(a, kt, k0 + row);
                 if (!value) {
                     const int any = __any_sync(FULL, gone);
                     if (lane == 0) missing[2 * ((unit + i) & 15) + half] = any;
@@ -251,31 +193,16 @@ __global__ void __launch_bounds__(CNT, 1) chunk_tensor_kernel(const ChunkArgs a,
                 const uint32_t dst = base + S::KV + st * S::TILE;
                 const bool check = value && sg.partial(a, k0);
                 const uint32_t bar = check ? land + 8 * half : full + 8 * st;
-                if (GATHER && maps.box > 0 && __all_sync(FULL, (pg[0] | pg[1] | pg[2] | pg[3]) >= 0)) {
-                    // lane: box and block of 64 elements
-                    const int b = lane / (D / 64), at = b * maps.box, x = lane % (D / 64);
-                    const int page = __shfl_sync(FULL, pg[0], (at >> 2) & 15);
+                if (GATHER) {
                     if (lane == 0) bar_expect(bar, 64 * D * 2);
                     __syncwarp();
-                    if (at < 64)
-                        copy_box(dst + x * (CK * 128) + (half * 64 + at) * 128, value ? &maps.vbox : &maps.kbox, x * 64,
-                                 (k0 + half * 64 + at) & (a.page_size - 1), head, page, bar);
-                } else if (GATHER) {
-                    int rows[4];
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const int key = k0 + row + j, slot = a.page_shift >= 0 ? key & (a.page_size - 1) : key % a.page_size;
-                        rows[j] = pg[j] >= 0 ? pg[j] * step[0] + slot * step[1] + head * step[2] : -1;
-                    }
-                    if (lane == 0) bar_expect(bar, 64 * D * 2);
-                    __syncwarp();
-                    if (block < D / 64) gather4(dst + block * (CK * 128) + row * 128, map, block * 64, rows, bar);
+                    copy_rows<D>(a, value ? maps.v : maps.k, pages, k0 + half * 64, head, dst + half * 8192, CK * 128, bar, lane);
                 } else {
                     const T* src = static_cast<const T*>(value ? a.v : a.k) + head * str[2];
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         const int key = k0 + row + j, slot = a.page_shift >= 0 ? key & (a.page_size - 1) : key % a.page_size;
-                        const int64_t off = pg[j] >= 0 ? pg[j] * str[0] + slot * str[1] : NOWHERE;
+                        const int64_t off = pages.at[j] >= 0 ? pages.at[j] * str[0] + slot * str[1] : NOWHERE;
                         // four rows at a time (of quads 4 q .. 4 q + 3), eight lanes a 128-byte line
 #pragma unroll
                         for (int q = 0; q < 4; ++q) {
@@ -469,7 +396,7 @@ __global__ void __launch_bounds__(CNT, 1) chunk_tensor_kernel(const ChunkArgs a,
                         bar_expect(qbar + 8 * t, CM * D * 2);
 #pragma unroll
                         for (int b = 0; b < D / 64; ++b)
-                            copy_box(base + t * S::QTILE + b * (CM * 128), &maps.qbox, b * 64, sg.head * a.gs, sg.x.q0 + row0 / a.gs,
+                            copy_box(base + t * S::QTILE + b * (CM * 128), &maps.q.boxes, b * 64, sg.head * a.gs, sg.x.q0 + row0 / a.gs,
                                      qbar + 8 * t);
                     }
                 } else if (GATHER) {
@@ -477,13 +404,13 @@ __global__ void __launch_bounds__(CNT, 1) chunk_tensor_kernel(const ChunkArgs a,
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         const int row = row0 + lane * 4 + j, tok = row / a.gs;
-                        rows[j] = row < sg.M ? (sg.x.q0 + tok) * maps.qs[0] + (sg.head * a.gs + row - tok * a.gs) * maps.qs[1] : -1;
+                        rows[j] = row < sg.M ? (sg.x.q0 + tok) * maps.q.step[0] + (sg.head * a.gs + row - tok * a.gs) * maps.q.step[1] : -1;
                     }
                     if (lane == 0) bar_expect(qbar + 8 * t, CM * D * 2);
                     __syncwarp();
 #pragma unroll
                     for (int b = 0; b < D / 64; ++b)
-                        gather4(base + t * S::QTILE + b * (CM * 128) + lane * 512, &maps.q, b * 64, rows, qbar + 8 * t);
+                        gather4(base + t * S::QTILE + b * (CM * 128) + lane * 512, &maps.q.rows, b * 64, rows, qbar + 8 * t);
                 } else {
 #pragma unroll 4
                     for (int i = lane; i < CM * DC; i += 32) {
@@ -692,67 +619,6 @@ __global__ void __launch_bounds__(CNT, 1) chunk_tensor_kernel(const ChunkArgs a,
 
 // ------------------------------------------------------------------ host
 
-using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
-                            const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                            CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-static Encode encoder() {
-    static const Encode fn = [] {
-        void* p = nullptr;
-        cudaDriverEntryPointQueryResult found;
-        const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &found);
-        if (e != cudaSuccess) cudaGetLastError();
-        return e == cudaSuccess && found == cudaDriverEntryPointSuccess ? reinterpret_cast<Encode>(p) : nullptr;
-    }();
-    return fn;
-}
-
-static bool tensor_map(CUtensorMap* map, const void* base, int dtype, int rank, const cuuint64_t* dims, const cuuint64_t* pitch,
-                       const cuuint32_t* box) {
-    const cuuint32_t ones[4] = {1, 1, 1, 1};
-    const Encode encode = encoder();
-    return encode && encode(map, dtype == FS_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, rank,
-                            const_cast<void*>(base), dims, pitch, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-// Rows of `dim` elements at offsets sum_i x_i strides[i], x_i < sizes[i], as the rows of one matrix: row number sum_i x_i
-// steps[i].  False where the strides have no common divisor of a row's length or more.
-static bool row_map(CUtensorMap* map, const void* base, int dtype, int dim, int n, const int64_t* strides, const int64_t* sizes,
-                    int* steps) {
-    int64_t g = 0;
-    for (int i = 0; i < n; ++i) {
-        if (sizes[i] < 2) continue;
-        if (strides[i] < 0) return false;
-        g = std::gcd(g, strides[i]);
-    }
-    if (g == 0) g = dim;
-    if (g < dim || g >= int64_t(1) << 36) return false;
-    int64_t last = 0;
-    for (int i = 0; i < n; ++i) {
-        const int64_t step = sizes[i] < 2 ? 0 : strides[i] / g;
-        if (step > 0 && (sizes[i] - 1) > (int64_t(0x7ffffffe) - last) / step) return false;
-        steps[i] = int(step);
-        last += step * (std::max<int64_t>(sizes[i], 1) - 1);
-    }
-    const cuuint64_t dims[2] = {cuuint64_t(dim), cuuint64_t(last + 1)}, pitch[1] = {cuuint64_t(g) * 2};
-    const cuuint32_t box[2] = {64, 1};
-    return tensor_map(map, base, dtype, 2, dims, pitch, box);
-}
-
-// Boxes of `rows` slots of a page.
-static bool box_map(CUtensorMap* map, const ChunkArgs& a, const void* base, int dtype, int dim, const int64_t* strides, int rows) {
-    const int64_t sizes[3] = {a.page_size, a.Hkv, std::max(a.num_pages, 1)}, by[3] = {strides[1], strides[2], strides[0]};
-    const cuuint64_t dims[4] = {cuuint64_t(dim), cuuint64_t(sizes[0]), cuuint64_t(sizes[1]), cuuint64_t(sizes[2])};
-    cuuint64_t pitch[3];
-    for (int i = 0; i < 3; ++i) {
-        if (sizes[i] > 1 && (by[i] < dim || by[i] >= int64_t(1) << 38)) return false;
-        pitch[i] = sizes[i] > 1 ? cuuint64_t(by[i]) * 2 : cuuint64_t(dim) * 2;
-    }
-    const cuuint32_t box[4] = {64, cuuint32_t(rows), 1, 1};
-    return tensor_map(map, base, dtype, 4, dims, pitch, box);
-}
 template <typename T, int D, bool GATHER>
 static fs_status launch(const ChunkArgs& a, const ChunkMaps& maps, void* stream) {
     const fs_status st = prepare_kernel(reinterpret_cast<const void*>(chunk_tensor_kernel<T, D, GATHER>));
@@ -772,31 +638,14 @@ static fs_status launch(const ChunkArgs& a, const ChunkMaps& maps, void* stream)
 }
 
 template <typename T>
-static fs_status launch_type(const ChunkArgs& a, int dtype, int head_dim, void* stream) {
-    ChunkMaps maps = {};
-    const int64_t cache[3] = {a.num_pages, a.page_size, a.Hkv}, query[2] = {a.N, a.Hq};
-    const bool gather = row_map(&maps.k, a.k, dtype, head_dim, 3, a.kc, cache, maps.ks) &&
-                        row_map(&maps.v, a.v, dtype, head_dim, 3, a.vc, cache, maps.vs) &&
-                        row_map(&maps.q, a.q, dtype, head_dim, 2, a.qs, query, maps.qs);
-    if (gather && CM % a.gs == 0) {
-        // (strides of dimensions of one element address nothing)
-        const cuuint64_t dims[3] = {cuuint64_t(head_dim), cuuint64_t(a.Hq), cuuint64_t(a.N)};
-        const int64_t by[2] = {a.Hq > 1 ? a.qs[1] : head_dim, a.N > 1 ? a.qs[0] : head_dim};
-        const cuuint64_t pitch[2] = {cuuint64_t(by[0]) * 2, cuuint64_t(by[1]) * 2};
-        const cuuint32_t box[3] = {64, cuuint32_t(a.gs), cuuint32_t(CM / a.gs)};
-        maps.qrows = by[0] >= head_dim && by[1] >= head_dim && tensor_map(&maps.qbox, a.q, dtype, 3, dims, pitch, box);
-    }
-    if (gather && a.page_shift >= 3) {
-        maps.box = std::min(a.page_size, 64);
-        if (!box_map(&maps.kbox, a, a.k, dtype, head_dim, a.kc, maps.box) || !box_map(&maps.vbox, a, a.v, dtype, head_dim, a.vc, maps.box))
-            maps.box = 0;
-    }
-    if (gather) return head_dim == 64 ? launch<T, 64, true>(a, maps, stream) : launch<T, 128, true>(a, maps, stream);
-    return head_dim == 64 ? launch<T, 64, false>(a, maps, stream) : launch<T, 128, false>(a, maps, stream);
+static fs_status launch_type(const ChunkArgs& a, const ChunkMaps* maps, int head_dim, void* stream) {
+    static const ChunkMaps none = {};
+    if (maps) return head_dim == 64 ? launch<T, 64, true>(a, *maps, stream) : launch<T, 128, true>(a, *maps, stream);
+    return head_dim == 64 ? launch<T, 64, false>(a, none, stream) : launch<T, 128, false>(a, none, stream);
 }
 
-fs_status launch_chunk_tensor(const ChunkArgs& a, int dtype, int head_dim, void* stream) {
-    return dtype == FS_BF16 ? launch_type<__nv_bfloat16>(a, dtype, head_dim, stream) : launch_type<__half>(a, dtype, head_dim, stream);
+fs_status launch_chunk_tensor(const ChunkArgs& a, const ChunkMaps* maps, int dtype, int head_dim, void* stream) {
+    return dtype == FS_BF16 ? launch_type<__nv_bfloat16>(a, maps, head_dim, stream) : launch_type<__half>(a, maps, head_dim, stream);
 }
 
 }  // namespace fsd

@@ -557,7 +557,7 @@ static ChunkPlan chunk_plan(const fs_paged_kv& c, int N, int R, int Hq, int widt
     p.MT = rows <= FEW || tensor ? FEW : 64;
     p.KT = D == 256 && p.MT == 64 ? 32 : 64;
     // Two CTAs fit an SM (one with heads of 256); no more than there can be units.
-    p.least = FEW_START + 2;
+    p.least = 2;
     const int64_t tiles = (int64_t(N) * gs + p.MT - 1) / p.MT + R;
     const int64_t units = tiles * c.num_heads * ((int64_t(width) * c.page_size + p.KT - 1) / p.KT + 2 + FEW_START);
     p.grid = int(std::max<int64_t>(1, std::min<int64_t>(int64_t(sms) * (D == 256 && p.MT == FEW ? 1 : 2), (units + p.least - 1) / p.least)));
@@ -568,7 +568,7 @@ static ChunkPlan chunk_plan(const fs_paged_kv& c, int N, int R, int Hq, int widt
     if (tensor) {
         // One CTA per SM.  A request of FEW rows or less has no tile there.
         const int64_t all = int64_t(N) * gs;
-        p.t_least = START + 1;
+        p.t_least = 1;
         p.t_tiles = int(std::min<int64_t>(all / MANY + std::min<int64_t>(R, all / (FEW + 1) + 1), 0x7fffffff));
         const int64_t t_units = int64_t(p.t_tiles) * c.num_heads * ((int64_t(width) * c.page_size + 127) / 128 + 2 + START);
         p.t_grid = int(std::max<int64_t>(1, std::min<int64_t>(sms, (t_units + p.t_least - 1) / p.t_least)));

@@ -103,27 +103,7 @@ __global__ void __launch_bounds__(CNT, 1) chunk_tensor_kernel(const ChunkArgs a,
     volatile int* odd = words + 2;      // [4]
     volatile int* missing = words + 8;  // [16][2]
     Segment* segs = reinterpret_cast<Segment*>(mem + S::SEGS);
-    grid_dependency_wait();
-    allow_dependents();
-
-    // ---- this CTA's run of units
-    const int n_tiles = a.t_plan[0];
-    // (units and, for each tile of each key/value head, START more that its start and end take as long as)
-    const int64_t total = (int64_t(a.t_plan[2]) << 32 | uint32_t(a.t_plan[1])) * a.Hkv;
-    const int64_t run = max(int64_t(a.t_least), (total + a.t_grid - 1) / a.t_grid);
-    const int64_t first_unit = min(blockIdx.x * run, total), last = min(first_unit + run, total);
-    if (tid == 0) a.t_split[blockIdx.x] = make_int4(0, 0, 0, 0);
-    if (first_unit >= last) return;
-    for (int i = tid; i < n_tiles; i += CNT) {
-        const int4 it = a.t_items[i];
-        const int64_t before = (int64_t(it.w) << 32 | uint32_t(it.z)) * a.Hkv;
-        int64_t next = total;
-        if (i + 1 < n_tiles) {
-            const int4 up = a.t_items[i + 1];
-            next = (int64_t(up.w) << 32 | uint32_t(up.z)) * a.Hkv;
-        }
-        if (before <= first_unit && first_unit < next) words[6] = i;
-    }
+    // (set up while the launch before runs)
     if (warp == ROLES + 5) {
         if (lane < ST) bar_init(full + 8 * lane, 2), bar_init(empty + 8 * lane, 1);
         if (lane < 2) {
@@ -139,10 +119,34 @@ __global__ void __launch_bounds__(CNT, 1) chunk_tensor_kernel(const ChunkArgs a,
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(base + S::WORDS) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
+    grid_dependency_wait();
+    allow_dependents();
+
+    // ---- this CTA's run of units
+    const int n_tiles = a.t_plan[0];
+    // (units and, for each tile of each key/value head, START more that its start and end take as long as)
+    const int64_t total = (int64_t(a.t_plan[2]) << 32 | uint32_t(a.t_plan[1])) * a.Hkv;
+    const int64_t run = max(int64_t(a.t_least), (total + a.t_grid - 1) / a.t_grid);
+    const int64_t first_unit = min(blockIdx.x * run, total), last = min(first_unit + run, total);
+    if (tid == 0) a.t_split[blockIdx.x] = make_int4(0, 0, 0, 0);
+    for (int i = tid; i < n_tiles; i += CNT) {
+        const int4 it = a.t_items[i];
+        const int64_t before = (int64_t(it.w) << 32 | uint32_t(it.z)) * a.Hkv;
+        int64_t next = total;
+        if (i + 1 < n_tiles) {
+            const int4 up = a.t_items[i + 1];
+            next = (int64_t(up.w) << 32 | uint32_t(up.z)) * a.Hkv;
+        }
+        if (before <= first_unit && first_unit < next) words[6] = i;
+    }
     tmem_fence_before();
     __syncthreads();
     tmem_fence_after();
     const uint32_t tmem = __shfl_sync(FULL, uint32_t(words[0]), 0);
+    if (first_unit >= last) {
+        if (warp == ROLES + 4) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+        return;
+    }
 
     // The s-th segment, once it is described; and given back, by each warp.
     auto next_segment = [&](uint32_t s, bool& ok) -> const Segment& {
@@ -461,25 +465,22 @@ __global__ void __launch_bounds__(CNT, 1) chunk_tensor_kernel(const ChunkArgs a,
                     tmem_fence_after();
                     float mul = a.scale;
                     const bool edge = t_hi - k0 >= a.window, gone = missing[2 * ((unit + i) & 15)] | missing[2 * ((unit + i) & 15) + 1];
-                    if (k0 + CK > t_lo + 1 || edge || gone || mul < 0.f) {
-                        // Scaled here where some keys are not seen, so that their scores are -infinity whatever the scale;
-                        // a key whose page does not exist is NaN.
-                        const int lim = pos + 1 - k0, low = edge ? pos - a.window + 1 - k0 : 0, first = a.sinks - k0;
+                    const bool some = k0 + CK > t_lo + 1 || edge;   // not every row sees all of the keys
+                    const int lim = pos + 1 - k0, low = edge ? pos - a.window + 1 - k0 : 0, first = a.sinks - k0;
+                    if (gone || !(mul > 0.f)) {
+                        // Rare: scaled here, so that scores of keys not seen are -infinity whatever the scale; a key whose
+                        // page does not exist is NaN.
 #pragma unroll 1
                         for (int c = 0; c < CK; c += 32) {
                             uint32_t x[32];
                             tmem_ld32(x, sc + c);
                             tmem_wait_ld();
+                            const unsigned lost = gone ? missing_pages(a, sg.r, k0 + c) : 0u;
 #pragma unroll
                             for (int e = 0; e < 32; ++e) {
                                 const int k = c + e;
-                                x[e] = k < lim && (k >= low || k < first) ? __float_as_uint(__uint_as_float(x[e]) * mul) : 0xff800000u;
-                            }
-                            if (gone) {
-                                const unsigned bits = missing_pages(a, sg.r, k0 + c);
-#pragma unroll
-                                for (int e = 0; e < 32; ++e)
-                                    if (bits >> e & 1 && x[e] != 0xff800000u) x[e] = 0x7fffffffu;
+                                const bool see = k < lim && (k >= low || k < first);
+                                x[e] = !see ? 0xff800000u : lost >> e & 1 ? 0x7fffffffu : __float_as_uint(__uint_as_float(x[e]) * mul);
                             }
                             tmem_st32(sc + c, x);
                         }
@@ -490,6 +491,17 @@ __global__ void __launch_bounds__(CNT, 1) chunk_tensor_kernel(const ChunkArgs a,
 #pragma unroll
                     for (int c = 0; c < CK / 32; ++c) tmem_ld32(part<32>(x, c), sc + c * 32);
                     tmem_wait_ld();
+                    if (some) {
+#pragma unroll
+                        for (int c = 0; c < CK / 32; ++c) {
+                            // the keys of these 32 that the row sees: below `lim`, and from `low` on or below `first`
+                            auto below = [](int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1; };
+                            const uint32_t see = below(lim - 32 * c) & (~below(low - 32 * c) | below(first - 32 * c));
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                if (!(see >> e & 1)) x[32 * c + e] = 0xff800000u;
+                        }
+                    }
                     float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
                     for (int e = 0; e < CK; e += 2)

@@ -547,9 +547,19 @@ PyObject* step_tables(PyObject*, PyObject* const* a, Py_ssize_t n) {
         apart(to, "page_table", Span(pages), "free_pages");
         apart(to, "page_table", Span(count), "free_count");
         const c10::DeviceGuard guard(table.device());
-        const auto like = lens.options();
-        at::Tensor starts = at::empty({int64_t(R) + 1}, like), rows = at::empty({budget}, like), pos = at::empty({budget}, like),
-                   totals = at::empty({R}, like), left = at::empty({1}, like);
+        // The five results lie in one allocation, each from a multiple of 16 bytes on: five of them take the host
+        // longer than the kernel the GPU.
+        const int64_t sizes[5] = {int64_t(R) + 1, budget, budget, R, 1};
+        int64_t at[5], ints = 0;
+        for (int i = 0; i < 5; ++i) at[i] = ints, ints += (sizes[i] + 3) / 4 * 4;
+        const at::Tensor all = at::empty({ints}, lens.options());
+        at::Tensor made[5];
+        for (int i = 0; i < 5; ++i) {
+            made[i] = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(all.storage()), all.key_set(), all.dtype());
+            made[i].unsafeGetTensorImpl()->set_storage_offset(at[i]);
+            made[i].unsafeGetTensorImpl()->set_sizes_contiguous(sizes[i]);
+        }
+        at::Tensor &starts = made[0], &rows = made[1], &pos = made[2], &totals = made[3], &left = made[4];
         auto in = [](const at::Tensor& x) { return static_cast<const int32_t*>(x.const_data_ptr()); };
         auto out = [](const at::Tensor& x) { return static_cast<int32_t*>(x.data_ptr()); };
         return launch(table, [&](void* s) {

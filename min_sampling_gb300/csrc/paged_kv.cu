@@ -429,7 +429,7 @@ __global__ void __launch_bounds__(256, 4) append_heads_kernel(const AppendArgs a
 // weights, cosines and sines across the heads of a token.  ONE = false: heads of more units than lanes, read
 // twice (the second time from L1).  8190 tokens of 32 + 8 + 8 heads of 128 in bf16: 44 us, 4.6 TB/s.
 template <typename T, int VW, bool ONE>
-__global__ void __launch_bounds__(256, VW > 1 && ONE ? 4 : 2) append_norm_kernel(const AppendArgs a) {
+__global__ void __launch_bounds__(256, 2) append_norm_kernel(const AppendArgs a) {
     extern __shared__ __align__(16) unsigned char smem[];
     int64_t* slots = reinterpret_cast<int64_t*>(smem);                  // [per_cta][2]
     int* pads = reinterpret_cast<int*>(slots + 2 * a.per_cta);          // [per_cta], padded to 8 bytes each
@@ -438,7 +438,7 @@ __global__ void __launch_bounds__(256, VW > 1 && ONE ? 4 : 2) append_norm_kernel
     grid_dependency_wait();
     allow_dependents();
     const int t0 = blockIdx.x * a.per_cta, tokens = min(a.per_cta, a.tokens - t0);
-    const int lane = threadIdx.x & (a.group - 1), hs = threadIdx.x / a.group, at_once = 256 / a.group;
+    const int lane = threadIdx.x & (a.group - 1), hs = threadIdx.x / a.group, at_once = blockDim.x / a.group;
     const int nq = a.query ? a.q_heads : 0, heads = nq + a.kv_heads, vals = a.kv_heads * a.per_val;
     const float inv_dim = 1.f / float(a.dim);
 
@@ -477,12 +477,42 @@ __global__ void __launch_bounds__(256, VW > 1 && ONE ? 4 : 2) append_norm_kernel
         }
         return s;
     };
+    auto value_at = [&](int i, int& o) {
+        const int h = quick_div(i, a.per_val, a.m_val);
+        o = (i - h * a.per_val) * VW;
+        return h;
+    };
     // The first loads go out before anything depends on the positions.
     int off, off2, pair;
     place(lane, off, off2, pair);
     const bool mine = lane < a.per_rot;
-    P x, y;
-    if (ONE && mine && hs < heads) load(head_at(t0, hs), off, off2, x, y);
+    constexpr int AT = ONE ? 2 : 1;   // heads in flight per thread
+    P x[AT], y[AT], v;
+    auto load_token = [&](int t) {
+        if (ONE && mine) {
+#pragma unroll
+            for (int j = 0; j < AT; ++j)
+                if (hs + j * at_once < heads) load(head_at(t, hs + j * at_once), off, off2, x[j], y[j]);
+        }
+        if (int(threadIdx.x) < vals) {
+            int o;
+            const int h = value_at(threadIdx.x, o);
+            v = *reinterpret_cast<const P*>(static_cast<const T*>(a.value) + t * a.val_t + h * a.val_h + o);
+        }
+    };
+    load_token(t0);
+    // This unit's weights, of queries and of keys.
+    constexpr int KEEP = ONE ? VW : 1;
+    float wq[2][KEEP] = {}, wk[2][KEEP] = {}, cs[KEEP] = {}, sn[KEEP] = {};
+    if (ONE && mine) {
+#pragma unroll
+        for (int e = 0; e < KEEP; ++e) {
+            wq[0][e] = a.q_weight ? a.q_weight[off + e] : 1.f;
+            wk[0][e] = a.k_weight ? a.k_weight[off + e] : 1.f;
+            wq[1][e] = a.q_weight && off2 >= 0 ? a.q_weight[off2 + e] : 1.f;
+            wk[1][e] = a.k_weight && off2 >= 0 ? a.k_weight[off2 + e] : 1.f;
+        }
+    }
     if (int(threadIdx.x) < tokens) {
         const int t = t0 + threadIdx.x;
         const int pos = a.positions[t];
@@ -513,77 +543,97 @@ __global__ void __launch_bounds__(256, VW > 1 && ONE ? 4 : 2) append_norm_kernel
 
     // One unit of a head: scaled, weighted, rotated, stored.
     auto finish = [&](int k, int h, T* d, int off, int off2, int pair, P& x, P& y, float r) {
-        const float* w = h < nq ? a.q_weight : a.k_weight;
-        const float2* cs = turns + k * a.half;
-        auto normed = [&](T v, int i) { return w ? Io<T>::get(v) * r * w[i] : Io<T>::get(v); };
+        const bool query = h < nq;
+        const float* w = query ? a.q_weight : a.k_weight;
+        const float2* turn = turns + k * a.half;
+        if (!w) r = 1.f;
+        // the e-th element of the unit's first or second word, normed
+        auto normed = [&](T v, int e, int second) {
+            const float f = Io<T>::get(v) * r;
+            if constexpr (ONE) return f * (query ? wq[second][e] : wk[second][e]);
+            else return w ? f * w[(second ? off2 : off) + e] : f;
+        };
+        auto cosine = [&](int e, int p) { if constexpr (ONE) return make_float2(cs[e], sn[e]); else return turn[p]; };
         if (pair >= 0 && off2 >= 0) {
 #pragma unroll
             for (int e = 0; e < VW; ++e) {
-                const float2 c = cs[pair + e];
-                const float f = normed(x.e[e], off + e), g = normed(y.e[e], off2 + e);
+                const float2 c = cosine(e, pair + e);
+                const float f = normed(x.e[e], e, 0), g = normed(y.e[e], e, 1);
                 x.e[e] = Io<T>::put(f * c.x - g * c.y);
                 y.e[e] = Io<T>::put(g * c.x + f * c.y);
             }
         } else if (pair >= 0) {
 #pragma unroll
             for (int e = 0; e + 1 < VW; e += 2) {
-                const float2 c = cs[pair + e / 2];
-                const float f = normed(x.e[e], off + e), g = normed(x.e[e + 1], off + e + 1);
+                const float2 c = cosine(e / 2, pair + e / 2);
+                const float f = normed(x.e[e], e, 0), g = normed(x.e[e + 1], e + 1, 0);
                 x.e[e] = Io<T>::put(f * c.x - g * c.y);
                 x.e[e + 1] = Io<T>::put(g * c.x + f * c.y);
             }
         } else if (w) {
 #pragma unroll
-            for (int e = 0; e < VW; ++e) x.e[e] = Io<T>::put(normed(x.e[e], off + e));
+            for (int e = 0; e < VW; ++e) x.e[e] = Io<T>::put(normed(x.e[e], e, 0));
         }
         *reinterpret_cast<P*>(d + off) = x;
         if (off2 >= 0) *reinterpret_cast<P*>(d + off2) = y;
     };
+    // A round of heads; whole warps, for the shuffles.  `there`: the units' words are in x and y.
+    auto round = [&](int k, int t, int state, int h, P& x, P& y, bool there) {
+        const bool on = h < heads;
+        const T* p = head_at(t, on ? h : 0);
+        float s = 0.f;
+        if (ONE) {
+            if (on && mine) {
+                if (!there) load(p, off, off2, x, y);
+                s = squares(x, y, off2 >= 0);
+            }
+        } else if (on) {
+            for (int u = lane; u < a.per_rot; u += a.group) {
+                int o1, o2, pr;
+                place(u, o1, o2, pr);
+                load(p, o1, o2, x, y);
+                s += squares(x, y, o2 >= 0);
+            }
+        }
+        for (int i = a.group >> 1; i > 0; i >>= 1) s += __shfl_xor_sync(FULL, s, i);
+        if (!on || (h >= nq && state)) return;
+        const float r = rsqrtf(fmaf(s, inv_dim, a.eps));
+        T* d = h < nq ? static_cast<T*>(a.query_out) + t * a.qo_t + h * a.qo_h
+                      : static_cast<T*>(a.k_cache) + slots[2 * k] + (h - nq) * a.kc[2];
+        for (int u = lane; u < a.per_rot; u += a.group) {
+            int o1 = off, o2 = off2, pr = pair;
+            if (!ONE) {
+                place(u, o1, o2, pr);
+                load(p, o1, o2, x, y);
+            }
+            if (state != 1) {
+                finish(k, h, d, o1, o2, pr, x, y, r);
+            } else {   // padding: the query as it is
+                *reinterpret_cast<P*>(d + o1) = x;
+                if (o2 >= 0) *reinterpret_cast<P*>(d + o2) = y;
+            }
+        }
+    };
 #pragma unroll 1
     for (int k = 0; k < tokens; ++k) {
         const int t = t0 + k, state = pads[k];
-#pragma unroll 1
-        for (int h0 = 0; h0 < heads; h0 += at_once) {   // (whole warps, for the shuffles)
-            const int h = h0 + hs;
-            const bool on = h < heads;
-            const T* p = head_at(t, on ? h : 0);
-            float s = 0.f;
-            if (ONE) {
-                if (on && mine) {
-                    if (k + h0 > 0) load(p, off, off2, x, y);
-                    s = squares(x, y, off2 >= 0);
-                }
-            } else if (on) {
-                for (int u = lane; u < a.per_rot; u += a.group) {
-                    int o1, o2, pr;
-                    place(u, o1, o2, pr);
-                    load(p, o1, o2, x, y);
-                    s += squares(x, y, o2 >= 0);
-                }
-            }
-            for (int i = a.group >> 1; i > 0; i >>= 1) s += __shfl_xor_sync(FULL, s, i);
-            if (!on || (h >= nq && state)) continue;
-            const float r = rsqrtf(fmaf(s, inv_dim, a.eps));
-            T* d = h < nq ? static_cast<T*>(a.query_out) + t * a.qo_t + h * a.qo_h
-                          : static_cast<T*>(a.k_cache) + slots[2 * k] + (h - nq) * a.kc[2];
-            for (int u = lane; u < a.per_rot; u += a.group) {
-                int o1 = off, o2 = off2, pr = pair;
-                if (!ONE) {
-                    place(u, o1, o2, pr);
-                    load(p, o1, o2, x, y);
-                }
-                if (state != 1) {
-                    finish(k, h, d, o1, o2, pr, x, y, r);
-                } else {   // padding: the query as it is
-                    *reinterpret_cast<P*>(d + o1) = x;
-                    if (o2 >= 0) *reinterpret_cast<P*>(d + o2) = y;
-                }
+        if (k > 0) load_token(t);
+        if (ONE && mine && pair >= 0) {
+#pragma unroll
+            for (int e = 0; e < KEEP; ++e) {
+                if (off2 < 0 && e >= (KEEP + 1) / 2) break;     // (neighbours: half as many pairs)
+                const float2 c = turns[k * a.half + pair + e];
+                cs[e] = c.x, sn[e] = c.y;
             }
         }
+#pragma unroll
+        for (int j = 0; j < AT; ++j) round(k, t, state, hs + j * at_once, x[j], y[j], ONE);
+        for (int h0 = AT * at_once; h0 < heads; h0 += at_once) round(k, t, state, h0 + hs, x[0], y[0], false);
         for (int i = threadIdx.x; !state && i < vals; i += blockDim.x) {
-            const int h = quick_div(i, a.per_val, a.m_val), o = (i - h * a.per_val) * VW;
-            *reinterpret_cast<P*>(static_cast<T*>(a.v_cache) + slots[2 * k + 1] + h * a.vc[2] + o) =
-                *reinterpret_cast<const P*>(static_cast<const T*>(a.value) + t * a.val_t + h * a.val_h + o);
+            int o;
+            const int h = value_at(i, o);
+            if (i != int(threadIdx.x)) v = *reinterpret_cast<const P*>(static_cast<const T*>(a.value) + t * a.val_t + h * a.val_h + o);
+            *reinterpret_cast<P*>(static_cast<T*>(a.v_cache) + slots[2 * k + 1] + h * a.vc[2] + o) = v;
         }
     }
 }
@@ -620,9 +670,11 @@ static fs_status launch_append(AppendArgs& a, void* stream) {
     a.m_val = magic_of(uint32_t(a.per_val), uint64_t(units));
     const bool norm = a.q_weight || a.k_weight;
     if (norm) {
-        threads = 256;
         a.group = 1;
         while (a.group < a.per_rot && a.group < 32) a.group *= 2;
+        // Whole rounds of heads, as above.
+        const int rounds = (heads * a.group + 255) / 256, at_once = (heads + rounds - 1) / rounds;
+        threads = (at_once * a.group + 31) / 32 * 32;
     }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(unsigned((a.tokens + a.per_cta - 1) / a.per_cta), 1, 1);

@@ -4,11 +4,16 @@
 //   z > 0 ? z / repetition : z * repetition     where the token is in the history,
 //   - frequency * count - presence * (count > 0)   count: how often it is behind the prompt,
 //   + bias,   -infinity where the mask has no bit;
-// in float32, rounded once.  Bound by memory: every logit is read once and written once.  A CTA owns a
-// segment of a row (16 KB): its logits are in flight while it goes through the row's history and
-// counts in shared memory the tokens that fall into the segment, with a bit for each logit that is touched, so that
-// the others look nothing up.  No scratch memory, no order that matters: counts are integers, and of
-// several biases of one token the last one counts.  In place only what changes is read and written.
+// in float32, rounded once.  Bound by memory: every logit is read once and written once.  Two launches:
+//   copy_kernel    streams the matrix with the masks applied, 16 KB a CTA
+//   change_kernel  the logits of the history's and the biases' tokens.  Each of a row's CTAs takes the tokens whose hash
+//                  names it, counts them in a table in shared memory and computes
+//                  their logits, while the copy ends; then it writes them.  Where a table overflows, or there would be too many, the
+//                  tokens are counted by ranges, a word each.
+// In place, and where there is nothing to mask or to change, one of them is left out. (In one launch, each CTA counting
+// for its own 8192 logits: 64 rows of 151936 28 us, 256 of 151665 with masks 64 us; a CTA's way through the history
+// is longer than that through its logits.)  No scratch memory, no order that matters: counts are integers, and of
+// several biases of one token the last one counts.
 #include <algorithm>
 
 #include <cuda_bf16.h>
@@ -19,16 +24,18 @@
 
 namespace fsd {
 
-constexpr int ADJ_NT = 256;      // threads
-// Logits of a CTA: 16 KB, so that five CTAs on an SM are at different points of the way from the first load to the last store.
-// (32 KB, two CTAs of 512 threads: 256 rows of 151665 71 us.)
-template <typename T> constexpr int ADJ_SEG = 16384 / int(sizeof(T));
+constexpr int COPY_NT = 256;                                          // threads of copy_kernel
+template <typename T> constexpr int COPY_SEG = 16384 / int(sizeof(T));   // logits of its CTA
+constexpr int CHANGE_NT = 512;                                        // threads of change_kernel
+constexpr int SLOTS = 4096;                                           // of its table, at most; tokens of a range
+constexpr int STAGED = 4096;                                          // tokens of the history in shared memory at a time
 
 struct AdjustArgs {
     const void* x;
     void* out;
     int64_t xs, os;              // row strides (elements)
-    int B, V, segs;
+    int B, V, segs, split;       // split: log2 of change_kernel's CTAs for a row
+    int copied;                  // behind copy_kernel
     const int* tokens;           // [B][history], rows `ts` apart; nullable
     int64_t ts;
     int history;
@@ -94,16 +101,30 @@ __device__ __forceinline__ uint4 load_words(uintptr_t p, uintptr_t begin, uintpt
                       __funnelshift_r(x3, x4, sh));
 }
 
-// Shared memory: a bit per touched logit, a bit per biased one, then a word per logit: its count and, in the upper half, the
-// number of its last bias plus one; where either may pass 16 bits (WIDE), a word each.
-template <typename T, bool IN_PLACE, bool WIDE>
-__global__ void __launch_bounds__(ADJ_NT, WIDE ? 2 : 5) adjust_kernel(const AdjustArgs a) {
-    constexpr int SEG = ADJ_SEG<T>, VW = 16 / sizeof(T), PER = SEG / VW / ADJ_NT;
-    extern __shared__ __align__(16) uint32_t smem[];
-    uint32_t* touched = smem;                   // [SEG / 32]
-    uint32_t* biased = smem + SEG / 32;         // [SEG / 32]
-    uint32_t* count = smem + SEG / 16;          // [SEG]
-    uint32_t* which = WIDE ? count + SEG : count;
+// A row's mask: bits of the logits from e on (those past the row's end are undefined).
+struct Mask {
+    const uint32_t* words;      // nullptr: none
+    bool nothing;               // a mask that does not exist allows nothing
+    int n;
+    __device__ __forceinline__ Mask(const AdjustArgs& a, int row) : words(nullptr), nothing(false), n(a.words) {
+        if (!a.allowed) return;
+        const int m = a.allowed_rows ? a.allowed_rows[row] : row;
+        nothing = m >= a.masks;
+        if (m >= 0 && !nothing) words = a.allowed + int64_t(m) * a.words;
+    }
+    template <int N>
+    __device__ __forceinline__ uint32_t bits(int e) const {
+        constexpr uint32_t ALL = (1u << N) - 1;
+        if (!words) return nothing ? 0u : ALL;
+        const int k = e >> 5;
+        return __funnelshift_r(words[k], (e & 31) > 32 - N && k + 1 < n ? words[k + 1] : 0u, e & 31) & ALL;
+    }
+};
+
+template <typename T, bool IN_PLACE>
+__global__ void __launch_bounds__(COPY_NT) copy_kernel(const AdjustArgs a) {
+    constexpr int SEG = COPY_SEG<T>, VW = 16 / sizeof(T), PER = SEG / VW / COPY_NT;
+    constexpr uint32_t ALL = (1u << VW) - 1;
     const int tid = threadIdx.x;
     grid_dependency_wait();
     allow_dependents();
@@ -113,133 +134,192 @@ __global__ void __launch_bounds__(ADJ_NT, WIDE ? 2 : 5) adjust_kernel(const Adju
     // The output's 16-byte words: word j of the segment holds logits e0 + j VW on.
     const int mis = int((reinterpret_cast<uintptr_t>(out) & 15) / sizeof(T));
     const int e0 = seg * SEG - mis;
-    auto whole = [&](int j) { return e0 + j * VW >= 0 && e0 + (j + 1) * VW <= a.V; };
-    constexpr uint32_t ALL = (1u << VW) - 1;
+    auto whole = [&](int e) { return e >= 0 && e + VW <= a.V; };
     Words<T> w[PER];
     if (!IN_PLACE) {
         const uintptr_t begin = reinterpret_cast<uintptr_t>(x), end = reinterpret_cast<uintptr_t>(x + a.V);
 #pragma unroll
         for (int i = 0; i < PER; ++i)
-            w[i].w = load_words(begin + (e0 + (tid + i * ADJ_NT) * VW) * int64_t(sizeof(T)), begin, end);
+            w[i].w = load_words(begin + (e0 + (tid + i * COPY_NT) * VW) * int64_t(sizeof(T)), begin, end);
     }
-    const bool hist = a.tokens != nullptr, bias = a.bias_starts != nullptr;
-    // The history's first tokens are on their way before its length is known.
-    const int* tok = a.tokens + row * a.ts;
-    int4 ahead = make_int4(-1, -1, -1, -1);
-    if (hist && a.tokens4 && tid * 4 < a.history) ahead = *reinterpret_cast<const int4*>(tok + tid * 4);
-    // The row's mask: mrow -1 none; one that does not exist allows nothing.  Bits of the VW logits from e on.
-    int mrow = -1;
-    if (a.allowed) mrow = a.allowed_rows ? a.allowed_rows[row] : row;
-    const bool none = a.allowed && mrow >= a.masks;
-    auto mask = [&](int e) {
-        if (none) return 0u;
-        if (mrow < 0 || e < 0 || e >= a.V) return ALL;
-        const uint32_t* m = a.allowed + int64_t(mrow) * a.words;
-        const int k = e >> 5;
-        const uint32_t m0 = m[k], m1 = (e & 31) > 32 - VW && k + 1 < a.words ? m[k + 1] : 0u;
-        return __funnelshift_r(m0, m1, e & 31) & ALL;
-    };
+    const Mask mask(a, row);
     uint32_t allow[PER];
 #pragma unroll
-    for (int i = 0; i < PER; ++i) allow[i] = mask(e0 + (tid + i * ADJ_NT) * VW);
-    const int len = !hist ? 0 : a.lens ? min(max(a.lens[row], 0), a.history) : a.history;
-    const int prompt = a.prompt_lens ? a.prompt_lens[row] : 0;
-    float rep = 1.f, pres = 0.f, freq = 0.f;
-    int b0 = 0, b1 = 0;
-    if (hist) {
-        if (a.repetition) rep = a.repetition[row];
-        if (a.presence) pres = a.presence[row];
-        if (a.frequency) freq = a.frequency[row];
+    for (int i = 0; i < PER; ++i) {
+        const int e = e0 + (tid + i * COPY_NT) * VW;
+        allow[i] = whole(e) ? mask.bits<VW>(e) : ALL;
     }
-    if (bias) b0 = min(max(a.bias_starts[row], 0), a.biases), b1 = min(a.bias_starts[row + 1], a.biases);
-    if (hist || bias) {
-        constexpr int N = SEG / 16 + (WIDE ? 2 : 1) * SEG;
-        for (int i = tid; i < N / 4; i += ADJ_NT) reinterpret_cast<uint4*>(smem)[i] = make_uint4(0, 0, 0, 0);
-        const int lo = max(e0, 0), hi = min(e0 + SEG, a.V);
-        __syncthreads();
-        for (int i = b0 + tid; i < b1; i += ADJ_NT) {
-            const int t = a.bias_tokens[i];
-            if (t >= lo && t < hi) {
-                atomicOr(&biased[(t - e0) >> 5], 1u << ((t - e0) & 31));
-                atomicMax(&which[t - e0], WIDE ? uint32_t(i - b0) + 1 : (uint32_t(i - b0) + 1) << 16);
-            }
-        }
-        if (!WIDE && bias) __syncthreads();     // (counts go into the same words)
-        auto add = [&](int t, int i) {
-            if (t >= lo && t < hi) {
-                atomicOr(&touched[(t - e0) >> 5], 1u << ((t - e0) & 31));
-                if (i >= prompt) atomicAdd(&count[t - e0], 1u);
-            }
-        };
-        if (a.tokens4) {
-#pragma unroll 2
-            for (int i = tid * 4; i < len; i += ADJ_NT * 4) {
-                const int4 t = i == tid * 4 ? ahead : *reinterpret_cast<const int4*>(tok + i);
-                add(t.x, i);
-                if (i + 1 < len) add(t.y, i + 1);
-                if (i + 2 < len) add(t.z, i + 2);
-                if (i + 3 < len) add(t.w, i + 3);
-            }
-        } else {
-#pragma unroll 4
-            for (int i = tid; i < len; i += ADJ_NT) add(tok[i], i);
-        }
-        __syncthreads();
-    }
-    // Logit at place i of the segment.
-    auto value = [&](float z, int i, bool t, bool b, bool ok) {
-        const uint32_t n = t || b ? count[i] : 0u, c = WIDE ? n : n & 0xffffu;
-        if (t) {
-            z = z > 0.f ? z / rep : z * rep;
-            if (c) z = fmaf(-freq, float(c), z) - pres;
-        }
-        if (b) z += a.bias_values[b0 + int(WIDE ? which[i] : n >> 16) - 1];
-        return ok ? z : __int_as_float(0xff800000);
-    };
-    // Bits of the VW logits from place i (a multiple of VW) on.
-    auto bits = [&](const uint32_t* map, int i) { return (map[i >> 5] >> (i & 31)) & ALL; };
+    const T banned = Num<T>::put(__int_as_float(0xff800000));
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-        const int j = tid + i * ADJ_NT, p = j * VW, e = e0 + p;
-        if (whole(j)) {
-            const uint32_t tb = hist ? bits(touched, p) : 0, bb = bias ? bits(biased, p) : 0, ok = allow[i];
+        const int e = e0 + (tid + i * COPY_NT) * VW;
+        if (whole(e)) {
             if (IN_PLACE) {
-                if (!(tb | bb) && ok == ALL) continue;
+                if (allow[i] == ALL) continue;
                 w[i].w = *reinterpret_cast<const uint4*>(x + e);
             }
-            if (tb | bb) {
+            if (allow[i] != ALL) {
 #pragma unroll
                 for (int k = 0; k < VW; ++k)
-                    if ((tb | bb) >> k & 1) w[i].e[k] = Num<T>::put(value(Num<T>::get(w[i].e[k]), p + k, tb >> k & 1, bb >> k & 1, true));
+                    if (!(allow[i] >> k & 1)) w[i].e[k] = banned;
             }
-            if (ok != ALL) {
-#pragma unroll
-                for (int k = 0; k < VW; ++k)
-                    if (!(ok >> k & 1)) w[i].e[k] = Num<T>::put(__int_as_float(0xff800000));
-            }
-            __stcs(reinterpret_cast<uint4*>(out + e), w[i].w);
+            *reinterpret_cast<uint4*>(out + e) = w[i].w;
         } else {
-            for (int k = 0; k < VW; ++k) {
-                if (e + k < 0 || e + k >= a.V) continue;
-                const bool t = hist && (touched[(p + k) >> 5] >> ((p + k) & 31) & 1), b = bias && (biased[(p + k) >> 5] >> ((p + k) & 31) & 1);
-                const bool ok = mask(e + k) & 1;
-                if (t || b || !ok) out[e + k] = Num<T>::put(value(Num<T>::get(x[e + k]), p + k, t, b, ok));
+            for (int k = max(-e, 0); k < VW && e + k < a.V; ++k) {
+                if (!mask.bits<1>(e + k)) out[e + k] = banned;
                 else if (!IN_PLACE) out[e + k] = x[e + k];
             }
         }
     }
 }
 
-template <typename T, bool IN_PLACE, bool WIDE>
-static fs_status launch_adjust(const AdjustArgs& a, void* stream) {
-    const void* fn = reinterpret_cast<const void*>(adjust_kernel<T, IN_PLACE, WIDE>);
-    constexpr int SEG = ADJ_SEG<T>;
-    const size_t smem = a.tokens || a.bias_starts ? (SEG / 16 + (WIDE ? 2 : 1) * SEG) * 4 : 0;
-    const fs_status st = prepare_kernel(fn);
+// Per token: its count, with bit 31 when it is in the history, and the number of its last bias plus one.
+template <typename T>
+__global__ void __launch_bounds__(CHANGE_NT, 3) change_kernel(const AdjustArgs a) {
+    constexpr uint32_t SEEN = 0x80000000u, EMPTY = 0xffffffffu;
+    extern __shared__ __align__(16) uint32_t smem[];
+    const int tid = threadIdx.x;
+    // (behind copy_kernel, what that one waited for is there)
+    if (!a.copied) grid_dependency_wait();
+    allow_dependents();
+    const int row = blockIdx.x >> a.split, part = blockIdx.x & ((1 << a.split) - 1);
+    const T* x = static_cast<const T*>(a.x) + row * a.xs;
+    T* out = static_cast<T*>(a.out) + row * a.os;
+    const bool hist = a.tokens != nullptr;
+    // The history, STAGED tokens at a time; the first are on their way before its length is known.
+    const int* tok = a.tokens + row * a.ts;
+    int* staged = reinterpret_cast<int*>(smem + 3 * SLOTS + 4);
+    auto stage = [&](int first, int last) {
+        if (a.tokens4) {
+            for (int i = first + tid * 4; i < min(first + STAGED, last); i += CHANGE_NT * 4)    // (rows end behind whole words)
+                cp_async16(reinterpret_cast<float*>(staged + i - first), reinterpret_cast<const float*>(tok + i), 16);
+        } else {
+            for (int i = first + tid; i < min(first + STAGED, last); i += CHANGE_NT)
+                cp_async4(reinterpret_cast<float*>(staged + i - first), reinterpret_cast<const float*>(tok + i), 4);
+        }
+        cp_async_commit();
+    };
+    if (hist) stage(0, a.history);
+    const int len = !hist ? 0 : a.lens ? min(max(a.lens[row], 0), a.history) : a.history;
+    const int prompt = a.prompt_lens ? a.prompt_lens[row] : 0;
+    int b0 = 0, b1 = 0;
+    if (a.bias_starts) b0 = min(max(a.bias_starts[row], 0), a.biases), b1 = max(min(a.bias_starts[row + 1], a.biases), b0);
+    const Mask mask(a, row);
+    float rep = 1.f, pres = 0.f, freq = 0.f;
+    if (a.repetition) rep = a.repetition[row];
+    if (a.presence) pres = a.presence[row];
+    if (a.frequency) freq = a.frequency[row];
+    // f(token, number in the history) for every token; the first STAGED are in shared memory.
+    auto history = [&](bool again, auto f) {
+        for (int first = 0; first < len; first += STAGED) {
+            if (first > 0 || (again && len > STAGED)) {
+                __syncthreads();
+                stage(first, len);
+            }
+            cp_async_wait<0>();
+            __syncthreads();
+#pragma unroll 1
+            for (int i = first + tid; i < min(first + STAGED, len); i += CHANGE_NT) f(staged[i - first], i);
+        }
+    };
+    // A token's new logit.
+    auto value = [&](int t, uint32_t count, bool seen, uint32_t bias) {
+        float z = Num<T>::get(x[t]);
+        if (seen) {
+            z = z > 0.f ? z / rep : z * rep;
+            if (count) z = fmaf(-freq, float(count), z) - pres;
+        }
+        if (bias) z += a.bias_values[b0 + int(bias) - 1];
+        return z;
+    };
+    // Twice as many slots as this CTA's tokens are likely to be.
+    const int all = len + b1 - b0, likely = (all >> a.split) + 32;
+    volatile uint32_t& full = smem[3 * SLOTS];
+    if (tid == 0) full = 0;
+    if (all > 0 && 2 * likely <= SLOTS) {
+        int bits = 6;
+        while ((1 << bits) < 2 * likely) ++bits;
+        uint32_t *key = smem, *word = key + (1 << bits), *which = word + (1 << bits);
+        for (int i = tid; i < 1 << bits; i += CHANGE_NT) key[i] = EMPTY, word[i] = which[i] = 0;
+        __syncthreads();
+        // f(slot, number) where the token is this CTA's
+        auto find = [&](int t, int i, auto f) {
+            const uint32_t g = uint32_t(t) * 2654435769u;
+            if (uint32_t(t) >= uint32_t(a.V) || (a.split > 0 && int(g >> (32 - a.split)) != part)) return;
+            uint32_t at = g << a.split >> (32 - bits);
+            for (int n = 0; n < 1 << bits; ++n) {
+                const uint32_t k = atomicCAS(&key[at], EMPTY, uint32_t(t));
+                if (k == EMPTY || k == uint32_t(t)) {
+                    f(at, i);
+                    return;
+                }
+                at = (at + 1) & ((1u << bits) - 1);
+            }
+            full = 1;
+        };
+        history(false, [&](int t, int i) {
+            find(t, i, [&](uint32_t at, int i) {
+                if (i >= prompt) atomicAdd(&word[at], 1u);
+                else atomicOr(&word[at], SEEN);
+            });
+        });
+        for (int i = b0 + tid; i < b1; i += CHANGE_NT)
+            find(a.bias_tokens[i], i, [&](uint32_t at, int i) { atomicMax(&which[at], uint32_t(i - b0 + 1)); });
+        __syncthreads();
+        if (!full) {
+            // Each slot's logit is computed, and once the copy is done written, by one thread.
+#pragma unroll 4
+            for (int i = tid; i < 1 << bits; i += CHANGE_NT) {
+                const uint32_t t = key[i], n = word[i];
+                if (t == EMPTY) continue;
+                if (!mask.bits<1>(int(t))) key[i] = EMPTY;      // (the copy's -infinity stays)
+                else word[i] = __float_as_uint(value(int(t), n & ~SEEN, n != 0, which[i]));
+            }
+            if (a.copied) grid_dependency_wait();
+            for (int i = tid; i < 1 << bits; i += CHANGE_NT)
+                if (key[i] != EMPTY) out[key[i]] = Num<T>::put(__uint_as_float(word[i]));
+            return;
+        }
+    }
+    __syncthreads();
+    if (a.copied) grid_dependency_wait();
+    cp_async_wait<0>();
+    if (all == 0) return;
+    // By ranges.  (A CTA whose table was full takes its own tokens in all of them; else the row's CTAs share the ranges.)
+    const bool own = full;
+    uint32_t *word = smem, *which = smem + SLOTS;
+    auto mine = [&](int t) { return !own || a.split == 0 || int(uint32_t(t) * 2654435769u >> (32 - a.split)) == part; };
+    const int64_t step = int64_t(SLOTS) << (own ? 0 : a.split);
+    for (int64_t lo = own ? 0 : part * SLOTS; lo < a.V; lo += step) {
+        const int first = int(lo), n = min(SLOTS, a.V - first);
+        __syncthreads();
+        for (int i = tid; i < 2 * SLOTS; i += CHANGE_NT) smem[i] = 0;
+        __syncthreads();
+        for (int i = b0 + tid; i < b1; i += CHANGE_NT) {
+            const int t = a.bias_tokens[i];
+            if (t >= first && t - first < n && mine(t)) atomicMax(&which[t - first], uint32_t(i - b0 + 1));
+        }
+        history(true, [&](int t, int i) {
+            if (t >= first && t - first < n && mine(t)) {
+                if (i >= prompt) atomicAdd(&word[t - first], 1u);
+                else atomicOr(&word[t - first], SEEN);
+            }
+        });
+        __syncthreads();
+        for (int i = tid; i < n; i += CHANGE_NT) {
+            const uint32_t c = word[i], b = which[i];
+            if ((c | b) && mask.bits<1>(first + i)) out[first + i] = Num<T>::put(value(first + i, c & ~SEEN, c != 0, b));
+        }
+    }
+}
+
+template <typename K>
+static fs_status launch_adjust(K kernel, unsigned grid, unsigned block, size_t smem, const AdjustArgs& a, void* stream) {
+    const fs_status st = prepare_kernel(reinterpret_cast<const void*>(kernel));
     if (st != FS_OK) return st;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(unsigned(int64_t(a.B) * a.segs), 1, 1);
-    cfg.blockDim = dim3(ADJ_NT, 1, 1);
+    cfg.gridDim = dim3(grid, 1, 1);
+    cfg.blockDim = dim3(block, 1, 1);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = static_cast<cudaStream_t>(stream);
     cudaLaunchAttribute attr[1];
@@ -247,18 +327,34 @@ static fs_status launch_adjust(const AdjustArgs& a, void* stream) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, adjust_kernel<T, IN_PLACE, WIDE>, a);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, a);
     return e == cudaSuccess ? FS_OK : cuda_fail(e);
 }
 
 template <typename T>
 static fs_status adjust_type(AdjustArgs& a, void* stream) {
+    int sms = 0;
+    size_t optin = 0;
+    fs_status st = device_limits(sms, optin);
+    if (st != FS_OK) return st;
     // (a row's first word may start up to 15 bytes before it)
-    a.segs = int((a.V + 16 / int(sizeof(T)) - 1 + ADJ_SEG<T> - 1) / ADJ_SEG<T>);
-    if (int64_t(a.B) * a.segs > 0x7fffffffLL) return FS_ERR_UNSUPPORTED;
-    const bool wide = a.history > 65535 || a.biases > 65534, in_place = a.x == a.out && (a.xs == a.os || a.B == 1);
-    if (in_place) return wide ? launch_adjust<T, true, true>(a, stream) : launch_adjust<T, true, false>(a, stream);
-    return wide ? launch_adjust<T, false, true>(a, stream) : launch_adjust<T, false, false>(a, stream);
+    a.segs = int((a.V + 16 / int(sizeof(T)) - 1 + COPY_SEG<T> - 1) / COPY_SEG<T>);
+    const bool in_place = a.x == a.out && (a.xs == a.os || a.B == 1), change = a.tokens || a.bias_starts;
+    // A row's CTAs: one for about 512 tokens of the history while all of them fit the GPU at once (three on an SM), and more
+    // than that only where the table would be too small.  (64 rows of 4096: 512 CTAs 14.3 us, 256 @@.)
+    a.split = 0;
+    while (a.split < 6 && (512 << a.split) < a.history &&
+           ((int64_t(a.B) << (a.split + 1)) <= 3 * sms || 2 * ((a.history >> a.split) + 64) > SLOTS))
+        ++a.split;
+    if (int64_t(a.B) * std::max(a.segs, 1 << a.split) > 0x7fffffffLL) return FS_ERR_UNSUPPORTED;
+    const auto changes = [&](auto kernel) { return launch_adjust(kernel, unsigned(a.B << a.split), CHANGE_NT, (3 * SLOTS + 4 + STAGED) * 4, a, stream); };
+    a.copied = !in_place || a.allowed;
+    if (a.copied) {
+        st = in_place ? launch_adjust(copy_kernel<T, true>, unsigned(a.B * a.segs), COPY_NT, 0, a, stream)
+                      : launch_adjust(copy_kernel<T, false>, unsigned(a.B * a.segs), COPY_NT, 0, a, stream);
+        if (st != FS_OK) return st;
+    }
+    return change ? changes(change_kernel<T>) : FS_OK;
 }
 
 }  // namespace fsd
@@ -274,7 +370,7 @@ fs_status fs_adjust_logits(const void* logits, int32_t dtype, int64_t row_stride
     using namespace fsd;
     if (batch < 0 || vocab < 1 || history < 0 || biases < 0 || masks < 0) return FS_ERR_INVALID_ARG;
     if (dtype != FS_F32 && dtype != FS_BF16 && dtype != FS_F16) return FS_ERR_INVALID_ARG;
-    if (vocab > FS_MAX_VOCAB) return FS_ERR_UNSUPPORTED;
+    if (vocab > FS_MAX_VOCAB || history >= 1 << 30) return FS_ERR_UNSUPPORTED;
     if (batch > 1 && (row_stride < vocab || out_stride < vocab || (tokens && token_stride < history))) return FS_ERR_INVALID_ARG;
     if (!tokens && (lens || prompt_lens || repetition || presence || frequency)) return FS_ERR_INVALID_ARG;
     if (bias_starts ? biases > 0 && (!bias_tokens || !bias_values) : bias_tokens || bias_values || biases) return FS_ERR_INVALID_ARG;

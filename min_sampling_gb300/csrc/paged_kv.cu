@@ -422,13 +422,158 @@ __global__ void __launch_bounds__(256, 4) append_heads_kernel(const AppendArgs a
     }
 }
 
-// Keys and queries normed on the way: y = x / sqrt(mean(x^2) + eps) * weight over each head, in
-// float32, then the rotation.  Bound by memory like appending without norms.  A head is one
-// group of lanes (a power of two, so that its sum is a few shuffles), a lane has one unit of it (see unit_of):
-// the unit's two words stay in registers between the sum and the rotation, and its
-// weights, cosines and sines across the heads of a token.  ONE = false: heads of more units than lanes, read
-// twice (the second time from L1).  8190 tokens of 32 + 8 + 8 heads of 128 in bf16: 44 us, 4.6 TB/s.
-template <typename T, int VW, bool ONE>
+// Where token t of a CTA's goes: its cache offsets, and 1 padding, 2 not written (a row or page that does not exist).
+__device__ __forceinline__ int place_of(const AppendArgs& a, int t, int64_t& k_at, int64_t& v_at) {
+    const int pos = a.positions[t], row = a.rows ? a.rows[t] : t;
+    k_at = v_at = 0;
+    if (pos < 0) return 1;
+    const int pi = pos / a.page_size;
+    if (row < 0 || row >= a.table_rows || pi >= a.table_width) return 2;
+    const int page = a.table[int64_t(row) * a.table_width + pi];
+    if (page < 0 || page >= a.num_pages) return 2;
+    const int slot = pos - pi * a.page_size;
+    k_at = page * a.kc[0] + slot * a.kc[1];
+    v_at = page * a.vc[0] + slot * a.vc[1];
+    return 0;
+}
+
+// Keys and queries normed on the way: y = x / sqrt(mean(x^2) + eps) * weight over each head, in float32, then the
+// rotation.  Aligned data, heads of up to 32 units.  Bound by memory like appending without norms.  A head is one group
+// of lanes (a power of two, so that its sum is a few shuffles), a lane has one unit of it: VW elements and, for a
+// rotation in halves, their partners, which stay in registers between the sum and the rotation.  Norm
+// and rotation are two products and a sum per element,
+//   x' = r (x A - y B),  y' = r (y C + x D),  A = w_x cos, B = w_y sin, C = w_y cos, D = w_x sin,
+// with r the head's scale and the coefficients in registers over a token's heads, queries first, then keys.  One or a few warps
+// have a token, so that the coefficients are made once or a few times for it: with all eight warps of a CTA on a
+// token their reads from L1 took 84 us for the 8190 tokens below.  8190 tokens of 32 + 8 + 8 heads of 128 in
+// bf16: @@ us, @@ TB/s.
+template <typename T, int VW>
+__global__ void __launch_bounds__(256, 3) append_norm_heads_kernel(const AppendArgs a) {
+    extern __shared__ __align__(16) unsigned char smem[];
+    int64_t* slots = reinterpret_cast<int64_t*>(smem);                  // [per_cta][2]
+    int* pads = reinterpret_cast<int*>(slots + 2 * a.per_cta);          // [per_cta], padded to 8 bytes each
+    float* cosines = reinterpret_cast<float*>(slots + 4 * a.per_cta);   // [per_cta][half]
+    float* sines = cosines + a.per_cta * a.half;
+    using P = Pack<T, VW>;
+    constexpr int H = VW / 2;
+    grid_dependency_wait();
+    allow_dependents();
+    const int t0 = blockIdx.x * a.per_cta, tokens = min(a.per_cta, a.tokens - t0);
+    // 256 / per_cta threads a token
+    const int each = 256 / a.per_cta, k = threadIdx.x / each, me = threadIdx.x - k * each, t = t0 + k;
+    const int lane = me & (a.group - 1), hs = me / a.group, at_once = each / a.group;
+    const int nq = a.query ? a.q_heads : 0, vals = a.kv_heads * a.per_val;
+    const float inv_dim = 1.f / float(a.dim);
+    const bool here = k < tokens, mine = here && lane < a.per_rot, rot = lane < a.per_pairs, halves = rot && !a.interleaved;
+    const int off = rot ? lane * VW : 2 * a.half + (lane - a.per_pairs) * VW;
+
+    auto load = [&](int side, int h, P& x, P& y) {
+        const T* p = side == 0 ? static_cast<const T*>(a.query) + t * a.q_t + h * a.q_h
+                               : static_cast<const T*>(a.key) + t * a.key_t + h * a.key_h;
+        x = *reinterpret_cast<const P*>(p + off);
+        if (halves) y = *reinterpret_cast<const P*>(p + off + a.half);
+    };
+    auto load_value = [&](int i, P& v) {
+        const int h = quick_div(i, a.per_val, a.m_val);
+        v = *reinterpret_cast<const P*>(static_cast<const T*>(a.value) + t * a.val_t + h * a.val_h + (i - h * a.per_val) * VW);
+    };
+    // The first loads go out before anything depends on the positions: a head of each side, a piece of the values.
+    P x[2], y[2], v;
+    if (mine && hs < nq) load(0, hs, x[0], y[0]);
+    if (mine && hs < a.kv_heads) load(1, hs, x[1], y[1]);
+    if (here && me < vals) load_value(me, v);
+    if (int(threadIdx.x) < tokens) pads[threadIdx.x] = place_of(a, t0 + threadIdx.x, slots[2 * threadIdx.x], slots[2 * threadIdx.x + 1]);
+    for (int i = threadIdx.x; i < tokens * a.half; i += 256) {
+        const int j = i / a.half, u = t0 + j;
+        const int pos = a.positions[u], rp = a.rotary_positions ? a.rotary_positions[u] : pos;
+        const float2 w = pos < 0 ? make_float2(1.f, 0.f) : cos_sin_of(a.inv_freq[i - j * a.half], rp);
+        cosines[i] = w.x;
+        sines[i] = w.y;
+    }
+    __syncthreads();
+    const int state = here ? pads[k] : 2;
+#pragma unroll
+    for (int side = 0; side < 2; ++side) {
+        const int heads = side == 0 ? nq : a.kv_heads;
+        const float* w = side == 0 ? a.q_weight : a.k_weight;
+        // this unit's coefficients
+        float2 A[H], B[H], C[H], E[H];
+        if (mine) {
+            const float* cp = cosines + k * a.half + (a.interleaved ? off / 2 : off);
+            const float* sp = sines + k * a.half + (a.interleaved ? off / 2 : off);
+#pragma unroll
+            for (int e = 0; e < H; ++e) {
+                const float2 one = make_float2(1.f, 1.f), wx = w ? *reinterpret_cast<const float2*>(w + off + 2 * e) : one;
+                if (halves) {
+                    const float2 wy = w ? *reinterpret_cast<const float2*>(w + off + a.half + 2 * e) : one;
+                    const float2 c = *reinterpret_cast<const float2*>(cp + 2 * e), s = *reinterpret_cast<const float2*>(sp + 2 * e);
+                    A[e] = make_float2(wx.x * c.x, wx.y * c.y);
+                    B[e] = make_float2(-wy.x * s.x, -wy.y * s.y);
+                    C[e] = make_float2(wy.x * c.x, wy.y * c.y);
+                    E[e] = make_float2(wx.x * s.x, wx.y * s.y);
+                } else {    // (x, y) becomes (x, y) A + (y, x) B
+                    const float c = rot ? cp[e] : 1.f, s = rot ? sp[e] : 0.f;
+                    A[e] = make_float2(wx.x * c, wx.y * c);
+                    B[e] = make_float2(-wx.y * s, wx.x * s);
+                }
+            }
+        }
+        P p = x[side], q = y[side];
+#pragma unroll 1
+        for (int h0 = 0; h0 < heads; h0 += at_once) {   // (whole warps, for the shuffles)
+            const int h = h0 + hs;
+            const bool on = h < heads && mine;
+            P np, nq2;      // the next head is on its way
+            if (mine && h + at_once < heads) load(side, h + at_once, np, nq2);
+            float2 s2 = make_float2(0.f, 0.f);
+            if (on) {
+#pragma unroll
+                for (int e = 0; e < H; ++e) {
+                    const float2 f = Two<T>::get(p.e + 2 * e);
+                    s2 = fma2(f, f, s2);
+                    if (halves) {
+                        const float2 g = Two<T>::get(q.e + 2 * e);
+                        s2 = fma2(g, g, s2);
+                    }
+                }
+            }
+            float s = s2.x + s2.y;
+            for (int i = a.group >> 1; i > 0; i >>= 1) s += __shfl_xor_sync(FULL, s, i);
+            if (on && !(side == 1 && state)) {
+                if (state != 1) {   // (padding: the query as it is)
+                    const float r1 = w ? rsqrtf(fmaf(s, inv_dim, a.eps)) : 1.f;
+                    const float2 r = make_float2(r1, r1);
+#pragma unroll
+                    for (int e = 0; e < H; ++e) {
+                        const float2 f = Two<T>::get(p.e + 2 * e);
+                        if (halves) {
+                            const float2 g = Two<T>::get(q.e + 2 * e);
+                            Two<T>::put(p.e + 2 * e, mul2(r, fma2(f, A[e], mul2(g, B[e]))));
+                            Two<T>::put(q.e + 2 * e, mul2(r, fma2(g, C[e], mul2(f, E[e]))));
+                        } else if (rot) {
+                            Two<T>::put(p.e + 2 * e, mul2(r, fma2(f, A[e], mul2(make_float2(f.y, f.x), B[e]))));
+                        } else if (w) {
+                            Two<T>::put(p.e + 2 * e, mul2(r, mul2(f, A[e])));
+                        }
+                    }
+                }
+                T* d = side == 0 ? static_cast<T*>(a.query_out) + t * a.qo_t + h * a.qo_h
+                                 : static_cast<T*>(a.k_cache) + slots[2 * k] + h * a.kc[2];
+                *reinterpret_cast<P*>(d + off) = p;
+                if (halves) *reinterpret_cast<P*>(d + off + a.half) = q;
+            }
+            p = np, q = nq2;
+        }
+    }
+    for (int i = me; !state && i < vals; i += each) {
+        if (i != me) load_value(i, v);
+        const int h = quick_div(i, a.per_val, a.m_val);
+        *reinterpret_cast<P*>(static_cast<T*>(a.v_cache) + slots[2 * k + 1] + h * a.vc[2] + (i - h * a.per_val) * VW) = v;
+    }
+}
+
+// The same for any alignment (VW = 1) and longer heads: a head's units are read twice, the second time from L1.
+template <typename T, int VW>
 __global__ void __launch_bounds__(256, 2) append_norm_kernel(const AppendArgs a) {
     extern __shared__ __align__(16) unsigned char smem[];
     int64_t* slots = reinterpret_cast<int64_t*>(smem);                  // [per_cta][2]
@@ -459,181 +604,77 @@ __global__ void __launch_bounds__(256, 2) append_norm_kernel(const AppendArgs a)
             pair = u;
         }
     };
-    auto head_at = [&](int t, int h) {
-        return h < nq ? static_cast<const T*>(a.query) + t * a.q_t + h * a.q_h
-                      : static_cast<const T*>(a.key) + t * a.key_t + (h - nq) * a.key_h;
-    };
-    auto load = [&](const T* p, int off, int off2, P& x, P& y) {
-        x = *reinterpret_cast<const P*>(p + off);
-        if (off2 >= 0) y = *reinterpret_cast<const P*>(p + off2);
-    };
-    auto squares = [&](const P& x, const P& y, bool both) {
-        float s = 0.f;
-#pragma unroll
-        for (int e = 0; e < VW; ++e) s = fmaf(Io<T>::get(x.e[e]), Io<T>::get(x.e[e]), s);
-        if (both) {
-#pragma unroll
-            for (int e = 0; e < VW; ++e) s = fmaf(Io<T>::get(y.e[e]), Io<T>::get(y.e[e]), s);
-        }
-        return s;
-    };
-    auto value_at = [&](int i, int& o) {
-        const int h = quick_div(i, a.per_val, a.m_val);
-        o = (i - h * a.per_val) * VW;
-        return h;
-    };
-    // The first loads go out before anything depends on the positions.
-    int off, off2, pair;
-    place(lane, off, off2, pair);
-    const bool mine = lane < a.per_rot;
-    constexpr int AT = ONE ? 2 : 1;   // heads in flight per thread
-    P x[AT], y[AT], v;
-    auto load_token = [&](int t) {
-        if (ONE && mine) {
-#pragma unroll
-            for (int j = 0; j < AT; ++j)
-                if (hs + j * at_once < heads) load(head_at(t, hs + j * at_once), off, off2, x[j], y[j]);
-        }
-        if (int(threadIdx.x) < vals) {
-            int o;
-            const int h = value_at(threadIdx.x, o);
-            v = *reinterpret_cast<const P*>(static_cast<const T*>(a.value) + t * a.val_t + h * a.val_h + o);
-        }
-    };
-    load_token(t0);
-    // This unit's weights, of queries and of keys.
-    constexpr int KEEP = ONE ? VW : 1;
-    float wq[2][KEEP] = {}, wk[2][KEEP] = {}, cs[KEEP] = {}, sn[KEEP] = {};
-    if (ONE && mine) {
-#pragma unroll
-        for (int e = 0; e < KEEP; ++e) {
-            wq[0][e] = a.q_weight ? a.q_weight[off + e] : 1.f;
-            wk[0][e] = a.k_weight ? a.k_weight[off + e] : 1.f;
-            wq[1][e] = a.q_weight && off2 >= 0 ? a.q_weight[off2 + e] : 1.f;
-            wk[1][e] = a.k_weight && off2 >= 0 ? a.k_weight[off2 + e] : 1.f;
-        }
-    }
-    if (int(threadIdx.x) < tokens) {
-        const int t = t0 + threadIdx.x;
-        const int pos = a.positions[t];
-        const int row = a.rows ? a.rows[t] : t;
-        const bool pad = pos < 0;
-        const int pi = pad ? 0 : pos / a.page_size;
-        int64_t k_at = 0, v_at = 0;
-        bool there = false;
-        if (!pad && row >= 0 && row < a.table_rows && pi < a.table_width) {
-            const int page = a.table[int64_t(row) * a.table_width + pi];
-            if (page >= 0 && page < a.num_pages) {
-                const int slot = pos - pi * a.page_size;
-                k_at = page * a.kc[0] + slot * a.kc[1];
-                v_at = page * a.vc[0] + slot * a.vc[1];
-                there = true;
-            }
-        }
-        slots[2 * threadIdx.x] = k_at;
-        slots[2 * threadIdx.x + 1] = v_at;
-        pads[threadIdx.x] = pad ? 1 : (there ? 0 : 2);   // 1 padding, 2 not written
-    }
+    if (int(threadIdx.x) < tokens) pads[threadIdx.x] = place_of(a, t0 + threadIdx.x, slots[2 * threadIdx.x], slots[2 * threadIdx.x + 1]);
     for (int i = threadIdx.x; i < tokens * a.half; i += blockDim.x) {
         const int k = i / a.half, t = t0 + k;
         const int pos = a.positions[t], rp = a.rotary_positions ? a.rotary_positions[t] : pos;
         turns[i] = pos < 0 ? make_float2(1.f, 0.f) : cos_sin_of(a.inv_freq[i - k * a.half], rp);
     }
     __syncthreads();
-
-    // One unit of a head: scaled, weighted, rotated, stored.
-    auto finish = [&](int k, int h, T* d, int off, int off2, int pair, P& x, P& y, float r) {
-        const bool query = h < nq;
-        const float* w = query ? a.q_weight : a.k_weight;
-        const float2* turn = turns + k * a.half;
-        if (!w) r = 1.f;
-        // the e-th element of the unit's first or second word, normed
-        auto normed = [&](T v, int e, int second) {
-            const float f = Io<T>::get(v) * r;
-            if constexpr (ONE) return f * (query ? wq[second][e] : wk[second][e]);
-            else return w ? f * w[(second ? off2 : off) + e] : f;
-        };
-        auto cosine = [&](int e, int p) { if constexpr (ONE) return make_float2(cs[e], sn[e]); else return turn[p]; };
-        if (pair >= 0 && off2 >= 0) {
-#pragma unroll
-            for (int e = 0; e < VW; ++e) {
-                const float2 c = cosine(e, pair + e);
-                const float f = normed(x.e[e], e, 0), g = normed(y.e[e], e, 1);
-                x.e[e] = Io<T>::put(f * c.x - g * c.y);
-                y.e[e] = Io<T>::put(g * c.x + f * c.y);
-            }
-        } else if (pair >= 0) {
-#pragma unroll
-            for (int e = 0; e + 1 < VW; e += 2) {
-                const float2 c = cosine(e / 2, pair + e / 2);
-                const float f = normed(x.e[e], e, 0), g = normed(x.e[e + 1], e + 1, 0);
-                x.e[e] = Io<T>::put(f * c.x - g * c.y);
-                x.e[e + 1] = Io<T>::put(g * c.x + f * c.y);
-            }
-        } else if (w) {
-#pragma unroll
-            for (int e = 0; e < VW; ++e) x.e[e] = Io<T>::put(normed(x.e[e], e, 0));
-        }
-        *reinterpret_cast<P*>(d + off) = x;
-        if (off2 >= 0) *reinterpret_cast<P*>(d + off2) = y;
-    };
-    // A round of heads; whole warps, for the shuffles.  `there`: the units' words are in x and y.
-    auto round = [&](int k, int t, int state, int h, P& x, P& y, bool there) {
-        const bool on = h < heads;
-        const T* p = head_at(t, on ? h : 0);
-        float s = 0.f;
-        if (ONE) {
-            if (on && mine) {
-                if (!there) load(p, off, off2, x, y);
-                s = squares(x, y, off2 >= 0);
-            }
-        } else if (on) {
-            for (int u = lane; u < a.per_rot; u += a.group) {
-                int o1, o2, pr;
-                place(u, o1, o2, pr);
-                load(p, o1, o2, x, y);
-                s += squares(x, y, o2 >= 0);
-            }
-        }
-        for (int i = a.group >> 1; i > 0; i >>= 1) s += __shfl_xor_sync(FULL, s, i);
-        if (!on || (h >= nq && state)) return;
-        const float r = rsqrtf(fmaf(s, inv_dim, a.eps));
-        T* d = h < nq ? static_cast<T*>(a.query_out) + t * a.qo_t + h * a.qo_h
-                      : static_cast<T*>(a.k_cache) + slots[2 * k] + (h - nq) * a.kc[2];
-        for (int u = lane; u < a.per_rot; u += a.group) {
-            int o1 = off, o2 = off2, pr = pair;
-            if (!ONE) {
-                place(u, o1, o2, pr);
-                load(p, o1, o2, x, y);
-            }
-            if (state != 1) {
-                finish(k, h, d, o1, o2, pr, x, y, r);
-            } else {   // padding: the query as it is
-                *reinterpret_cast<P*>(d + o1) = x;
-                if (o2 >= 0) *reinterpret_cast<P*>(d + o2) = y;
-            }
-        }
-    };
 #pragma unroll 1
     for (int k = 0; k < tokens; ++k) {
         const int t = t0 + k, state = pads[k];
-        if (k > 0) load_token(t);
-        if (ONE && mine && pair >= 0) {
+        const float2* turn = turns + k * a.half;
+        for (int h0 = 0; h0 < heads; h0 += at_once) {   // (whole warps, for the shuffles)
+            const int h = h0 + hs;
+            const bool on = h < heads;
+            const T* src = !on || h < nq ? static_cast<const T*>(a.query) + t * a.q_t + (on ? h : 0) * a.q_h
+                                         : static_cast<const T*>(a.key) + t * a.key_t + (h - nq) * a.key_h;
+            const float* w = h < nq ? a.q_weight : a.k_weight;
+            float s = 0.f;
+            for (int u = lane; on && u < a.per_rot; u += a.group) {
+                int off, off2, pair;
+                place(u, off, off2, pair);
+                const P x = *reinterpret_cast<const P*>(src + off);
 #pragma unroll
-            for (int e = 0; e < KEEP; ++e) {
-                if (off2 < 0 && e >= (KEEP + 1) / 2) break;     // (neighbours: half as many pairs)
-                const float2 c = turns[k * a.half + pair + e];
-                cs[e] = c.x, sn[e] = c.y;
+                for (int e = 0; e < VW; ++e) s = fmaf(Io<T>::get(x.e[e]), Io<T>::get(x.e[e]), s);
+                if (off2 >= 0) {
+                    const P y = *reinterpret_cast<const P*>(src + off2);
+#pragma unroll
+                    for (int e = 0; e < VW; ++e) s = fmaf(Io<T>::get(y.e[e]), Io<T>::get(y.e[e]), s);
+                }
+            }
+            for (int i = a.group >> 1; i > 0; i >>= 1) s += __shfl_xor_sync(FULL, s, i);
+            if (!on || (h >= nq && state)) continue;
+            const float r = w ? rsqrtf(fmaf(s, inv_dim, a.eps)) : 1.f;
+            T* d = h < nq ? static_cast<T*>(a.query_out) + t * a.qo_t + h * a.qo_h
+                          : static_cast<T*>(a.k_cache) + slots[2 * k] + (h - nq) * a.kc[2];
+            auto normed = [&](T v, int i) { return w ? Io<T>::get(v) * r * w[i] : Io<T>::get(v); };
+            for (int u = lane; u < a.per_rot; u += a.group) {
+                int off, off2, pair;
+                place(u, off, off2, pair);
+                P x = *reinterpret_cast<const P*>(src + off), y = x;
+                if (off2 >= 0) y = *reinterpret_cast<const P*>(src + off2);
+                if (state == 1) {
+                    // padding: the query as it is
+                } else if (off2 >= 0) {
+#pragma unroll
+                    for (int e = 0; e < VW; ++e) {
+                        const float2 c = turn[pair + e];
+                        const float f = normed(x.e[e], off + e), g = normed(y.e[e], off2 + e);
+                        x.e[e] = Io<T>::put(f * c.x - g * c.y);
+                        y.e[e] = Io<T>::put(g * c.x + f * c.y);
+                    }
+                } else if (pair >= 0) {
+#pragma unroll
+                    for (int e = 0; e + 1 < VW; e += 2) {
+                        const float2 c = turn[pair + e / 2];
+                        const float f = normed(x.e[e], off + e), g = normed(x.e[e + 1], off + e + 1);
+                        x.e[e] = Io<T>::put(f * c.x - g * c.y);
+                        x.e[e + 1] = Io<T>::put(g * c.x + f * c.y);
+                    }
+                } else if (w) {
+#pragma unroll
+                    for (int e = 0; e < VW; ++e) x.e[e] = Io<T>::put(normed(x.e[e], off + e));
+                }
+                *reinterpret_cast<P*>(d + off) = x;
+                if (off2 >= 0) *reinterpret_cast<P*>(d + off2) = y;
             }
         }
-#pragma unroll
-        for (int j = 0; j < AT; ++j) round(k, t, state, hs + j * at_once, x[j], y[j], ONE);
-        for (int h0 = AT * at_once; h0 < heads; h0 += at_once) round(k, t, state, h0 + hs, x[0], y[0], false);
         for (int i = threadIdx.x; !state && i < vals; i += blockDim.x) {
-            int o;
-            const int h = value_at(i, o);
-            if (i != int(threadIdx.x)) v = *reinterpret_cast<const P*>(static_cast<const T*>(a.value) + t * a.val_t + h * a.val_h + o);
-            *reinterpret_cast<P*>(static_cast<T*>(a.v_cache) + slots[2 * k + 1] + h * a.vc[2] + o) = v;
+            const int h = quick_div(i, a.per_val, a.m_val), o = (i - h * a.per_val) * VW;
+            *reinterpret_cast<P*>(static_cast<T*>(a.v_cache) + slots[2 * k + 1] + h * a.vc[2] + o) =
+                *reinterpret_cast<const P*>(static_cast<const T*>(a.value) + t * a.val_t + h * a.val_h + o);
         }
     }
 }
@@ -669,12 +710,16 @@ static fs_status launch_append(AppendArgs& a, void* stream) {
     a.m_rot = magic_of(uint32_t(a.per_rot), uint64_t(units));
     a.m_val = magic_of(uint32_t(a.per_val), uint64_t(units));
     const bool norm = a.q_weight || a.k_weight;
+    bool wide = false;  // append_norm_heads_kernel
     if (norm) {
         a.group = 1;
         while (a.group < a.per_rot && a.group < 32) a.group *= 2;
-        // Whole rounds of heads, as above.
-        const int rounds = (heads * a.group + 255) / 256, at_once = (heads + rounds - 1) / rounds;
-        threads = (at_once * a.group + 31) / 32 * 32;
+        threads = 256;
+        if constexpr (VW > 1) wide = a.per_rot <= 32 && ((reinterpret_cast<uintptr_t>(a.q_weight) | reinterpret_cast<uintptr_t>(a.k_weight)) & 7) == 0;
+        if (wide) {     // one, two or four tokens, as long as every SM still gets four CTAs
+            a.per_cta = 1;
+            while (a.per_cta < 4 && a.tokens >= int64_t(sms) * 8 * a.per_cta) a.per_cta *= 2;
+        }
     }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(unsigned((a.tokens + a.per_cta - 1) / a.per_cta), 1, 1);
@@ -687,9 +732,9 @@ static fs_status launch_append(AppendArgs& a, void* stream) {
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     cudaError_t e;
-    if (norm) e = a.per_rot <= a.group ? cudaLaunchKernelEx(&cfg, append_norm_kernel<T, VW, true>, a)
-                                       : cudaLaunchKernelEx(&cfg, append_norm_kernel<T, VW, false>, a);
-    else if constexpr (VW > 1) e = cudaLaunchKernelEx(&cfg, append_heads_kernel<T, VW>, a);
+    if (norm && !wide) e = cudaLaunchKernelEx(&cfg, append_norm_kernel<T, VW>, a);
+    else if constexpr (VW > 1) e = norm ? cudaLaunchKernelEx(&cfg, append_norm_heads_kernel<T, VW>, a)
+                                        : cudaLaunchKernelEx(&cfg, append_heads_kernel<T, VW>, a);
     else e = cudaLaunchKernelEx(&cfg, append_kernel<T, VW>, a);
     return e == cudaSuccess ? FS_OK : cuda_fail(e);
 }

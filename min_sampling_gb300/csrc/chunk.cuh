@@ -33,13 +33,14 @@ struct ChunkArgs {
     // chunk_rows_kernel: CTAs, their parts, what the parts belong to
     int grid, least;            // least: units (key tiles) of a CTA at least
     float* part_o;              // [2 grid][MT][D]
-    float* part_l;              // [2 grid][MT], log2 of each part's sum of 2^score
+    float2* part_l;             // [2 grid][MT], each part's maximum m and sum of 2^(score - m): apart, for m that swallow the sum's
+                                // logarithm
     int4* split;                // [grid]: request, head, row0, parts; parts 0: none
     // chunk_tensor_kernel's
     int t_grid, t_tiles, t_least;   // t_grid 0: not launched
     int out_32;                 // the output's rows are aligned to 32 bytes
     float* t_part_o;            // [2 t_grid][MANY][D]
-    float* t_part_l;
+    float2* t_part_l;
     int4* t_split;
     int4* t_items;              // [t_tiles]: request, row0, units (and START for each tile) of a key/value head before (low, high word)
     int* t_first;               // [R + 1]: tiles before a request

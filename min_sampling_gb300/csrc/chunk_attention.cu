@@ -373,7 +373,7 @@ __global__ void __launch_bounds__(32 * WM * WN) chunk_rows_kernel(const ChunkArg
             } else {
                 const int64_t at = int64_t(slot) * MT + r;
                 *reinterpret_cast<float4*>(a.part_o + at * D + c * 4) = y;
-                if (c == 0) a.part_l[at] = lse;
+                if (c == 0) a.part_l[at] = make_float2(m, l);
             }
         }
         if (!whole && i0 == 0 && tid == 0)   // this CTA has the tile's first part and says how many CTAs have one
@@ -393,7 +393,7 @@ __global__ void __launch_bounds__(128) join_chunk_kernel(const ChunkArgs a, int 
     const int b = int(blockIdx.x) - (few ? 0 : a.grid * ys), per = few ? ys : MANY / 16;
     const int c = b / per, y16 = (b - c * per) * 16, MT = per * 16;
     const float* part_o = few ? a.part_o : a.t_part_o;
-    const float* part_l = few ? a.part_l : a.t_part_l;
+    const float2* part_l = few ? a.part_l : a.t_part_l;
     grid_dependency_wait();
     allow_dependents();
     const int4 s = (few ? a.split : a.t_split)[c];
@@ -406,7 +406,7 @@ __global__ void __launch_bounds__(128) join_chunk_kernel(const ChunkArgs a, int 
         const int r = y16 + i, row = s.z + r;
         if (row >= M) return;
         float m = -INFINITY;
-        for (int p = lane; p < s.w; p += 32) m = fmaxf(m, part_l[slot(p) + r]);
+        for (int p = lane; p < s.w; p += 32) m = fmaxf(m, part_l[slot(p) + r].x);
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(FULL, m, d));
         const float ms = m == -INFINITY ? 0.f : m;
@@ -416,7 +416,8 @@ __global__ void __launch_bounds__(128) join_chunk_kernel(const ChunkArgs a, int 
         for (int e = 0; e < E; ++e) y[e] = 0.f;
 #pragma unroll 4
         for (int p = 0; p < s.w; ++p) {
-            const float f = exp2f(part_l[slot(p) + r] - ms);
+            const float2 part = part_l[slot(p) + r];
+            const float f = exp2f(part.x - ms) * part.y;
             const float* o = part_o + (slot(p) + r) * D + lane * E;
             l += f;
 #pragma unroll
@@ -563,7 +564,7 @@ static ChunkPlan chunk_plan(const fs_paged_kv& c, int N, int R, int Hq, int widt
     p.grid = int(std::max<int64_t>(1, std::min<int64_t>(int64_t(sms) * (D == 256 && p.MT == FEW ? 1 : 2), (units + p.least - 1) / p.least)));
     size_t at = 0;
     p.part_o = add_bytes(at, size_t(2) * p.grid * p.MT * D * 4);
-    p.part_l = add_bytes(at, size_t(2) * p.grid * p.MT * 4);
+    p.part_l = add_bytes(at, size_t(2) * p.grid * p.MT * 8);
     p.split = add_bytes(at, size_t(p.grid) * sizeof(int4));
     if (tensor) {
         // One CTA per SM.  A request of FEW rows or less has no tile there.
@@ -573,7 +574,7 @@ static ChunkPlan chunk_plan(const fs_paged_kv& c, int N, int R, int Hq, int widt
         const int64_t t_units = int64_t(p.t_tiles) * c.num_heads * ((int64_t(width) * c.page_size + 127) / 128 + 2 + START);
         p.t_grid = int(std::max<int64_t>(1, std::min<int64_t>(sms, (t_units + p.t_least - 1) / p.t_least)));
         p.t_part_o = add_bytes(at, size_t(2) * p.t_grid * MANY * D * 4);
-        p.t_part_l = add_bytes(at, size_t(2) * p.t_grid * MANY * 4);
+        p.t_part_l = add_bytes(at, size_t(2) * p.t_grid * MANY * 8);
         p.t_split = add_bytes(at, size_t(p.t_grid) * sizeof(int4));
         p.t_items = add_bytes(at, size_t(p.t_tiles) * sizeof(int4));
         p.t_first = add_bytes(at, (size_t(R) + 1) * 4);
@@ -709,7 +710,7 @@ fs_status fs_paged_chunk_attention(const fs_paged_kv* cache, const void* query, 
     a.least = p.least;
     unsigned char* ws = static_cast<unsigned char*>(workspace);
     a.part_o = reinterpret_cast<float*>(ws + p.part_o);
-    a.part_l = reinterpret_cast<float*>(ws + p.part_l);
+    a.part_l = reinterpret_cast<float2*>(ws + p.part_l);
     a.split = reinterpret_cast<int4*>(ws + p.split);
     a.t_grid = p.t_grid;
     a.t_least = p.t_least;
@@ -717,7 +718,7 @@ fs_status fs_paged_chunk_attention(const fs_paged_kv* cache, const void* query, 
     a.t_tiles = p.t_tiles;
     if (p.t_grid > 0) {
         a.t_part_o = reinterpret_cast<float*>(ws + p.t_part_o);
-        a.t_part_l = reinterpret_cast<float*>(ws + p.t_part_l);
+        a.t_part_l = reinterpret_cast<float2*>(ws + p.t_part_l);
         a.t_split = reinterpret_cast<int4*>(ws + p.t_split);
         a.t_items = reinterpret_cast<int4*>(ws + p.t_items);
         a.t_first = reinterpret_cast<int*>(ws + p.t_first);

@@ -81,7 +81,8 @@ __global__ void __launch_bounds__(FNT) chunk_few_kernel(const ChunkArgs a, const
     if (warp == 4) {
         // ================================================ what the next tiles are, and their copies
         Place pl = run.place;
-        Request x = request(a, pl.r);
+        Request x = {};
+        if (run.first < run.last) x = request(a, pl.r);     // (there may be no requests at all)
         int64_t unit = run.first;
         uint32_t c = 0;         // key tiles before
         bool ok = true;
@@ -365,7 +366,7 @@ __global__ void __launch_bounds__(FNT) chunk_few_kernel(const ChunkArgs a, const
                     } else {
                         const int64_t at = int64_t(part) * FEW + r;
                         *reinterpret_cast<float4*>(a.part_o + at * D + d) = y;
-                        if (d == 0) a.part_l[at] = lse;
+                        if (d == 0) a.part_l[at] = make_float2(m, l);
                     }
                 }
                 asm volatile("bar.sync 1, 128;" ::: "memory");

@@ -610,7 +610,7 @@ __global__ void __launch_bounds__(CNT, 1) chunk_tensor_kernel(const ChunkArgs a,
                     __syncwarp();   // (tensor memory is read by whole warps)
                 }
                 if (on) {
-                    if (!whole) a.t_part_l[slot] = lse;
+                    if (!whole) a.t_part_l[slot] = make_float2(m, l * exp2f(-W::SHIFT) + bad);
                     else if (a.lse) a.lse[int64_t(sg.x.q0 + j) * a.Hq + h] = lse * 0.693147180559945309f;
                 }
                 // The CTA that has a tile's first part says how many CTAs have one.

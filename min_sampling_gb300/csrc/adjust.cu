@@ -175,7 +175,7 @@ __global__ void __launch_bounds__(COPY_NT) copy_kernel(const AdjustArgs a) {
 
 // Per token: its count, with bit 31 when it is in the history, and the number of its last bias plus one.
 template <typename T>
-__global__ void __launch_bounds__(CHANGE_NT, 3) change_kernel(const AdjustArgs a) {
+__global__ void __launch_bounds__(CHANGE_NT, 2) change_kernel(const AdjustArgs a) {
     constexpr uint32_t SEEN = 0x80000000u, EMPTY = 0xffffffffu;
     extern __shared__ __align__(16) uint32_t smem[];
     const int tid = threadIdx.x;
@@ -222,15 +222,13 @@ __global__ void __launch_bounds__(CHANGE_NT, 3) change_kernel(const AdjustArgs a
             for (int i = first + tid; i < min(first + STAGED, len); i += CHANGE_NT) f(staged[i - first], i);
         }
     };
-    // A token's new logit.
-    auto value = [&](int t, uint32_t count, bool seen, uint32_t bias) {
-        float z = Num<T>::get(x[t]);
-        if (seen) {
+    // A logit z, changed: `n` is its token's count and SEEN.
+    auto value = [&](float z, uint32_t n, bool biased, float bias) {
+        if (n) {
             z = z > 0.f ? z / rep : z * rep;
-            if (count) z = fmaf(-freq, float(count), z) - pres;
+            if (n & ~SEEN) z = fmaf(-freq, float(n & ~SEEN), z) - pres;
         }
-        if (bias) z += a.bias_values[b0 + int(bias) - 1];
-        return z;
+        return biased ? z + bias : z;
     };
     // Twice as many slots as this CTA's tokens are likely to be.
     const int all = len + b1 - b0, likely = (all >> a.split) + 32;
@@ -267,17 +265,31 @@ __global__ void __launch_bounds__(CHANGE_NT, 3) change_kernel(const AdjustArgs a
             find(a.bias_tokens[i], i, [&](uint32_t at, int i) { atomicMax(&which[at], uint32_t(i - b0 + 1)); });
         __syncthreads();
         if (!full) {
-            // Each slot's logit is computed, and once the copy is done written, by one thread.
-#pragma unroll 4
-            for (int i = tid; i < 1 << bits; i += CHANGE_NT) {
-                const uint32_t t = key[i], n = word[i];
-                if (t == EMPTY) continue;
-                if (!mask.bits<1>(int(t))) key[i] = EMPTY;      // (the copy's -infinity stays)
-                else word[i] = __float_as_uint(value(int(t), n & ~SEEN, n != 0, which[i]));
+            // Each slot's logit is computed, and once the copy is done written, by one thread; the loads of all of a thread's
+            // slots are in flight together.
+            constexpr int PER = SLOTS / CHANGE_NT;
+            uint32_t t[PER], b[PER];
+            float z[PER], add[PER];
+#pragma unroll
+            for (int j = 0; j < PER; ++j) {
+                const int i = tid + j * CHANGE_NT;
+                t[j] = EMPTY, b[j] = 0, add[j] = 0.f;
+                if (i < 1 << bits) t[j] = key[i];
+                if (t[j] != EMPTY) {
+                    z[j] = Num<T>::get(x[t[j]]);
+                    if (!mask.bits<1>(int(t[j]))) b[j] = EMPTY;     // (the copy's -infinity stays)
+                    else if (which[i]) b[j] = which[i], add[j] = a.bias_values[b0 + int(which[i]) - 1];
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < PER; ++j) {
+                if (b[j] == EMPTY) t[j] = EMPTY;
+                if (t[j] != EMPTY) z[j] = value(z[j], word[tid + j * CHANGE_NT], b[j] != 0, add[j]);
             }
             if (a.copied) grid_dependency_wait();
-            for (int i = tid; i < 1 << bits; i += CHANGE_NT)
-                if (key[i] != EMPTY) out[key[i]] = Num<T>::put(__uint_as_float(word[i]));
+#pragma unroll
+            for (int j = 0; j < PER; ++j)
+                if (t[j] != EMPTY) out[t[j]] = Num<T>::put(z[j]);
             return;
         }
     }
@@ -308,7 +320,8 @@ __global__ void __launch_bounds__(CHANGE_NT, 3) change_kernel(const AdjustArgs a
         __syncthreads();
         for (int i = tid; i < n; i += CHANGE_NT) {
             const uint32_t c = word[i], b = which[i];
-            if ((c | b) && mask.bits<1>(first + i)) out[first + i] = Num<T>::put(value(first + i, c & ~SEEN, c != 0, b));
+            if ((c | b) && mask.bits<1>(first + i))
+                out[first + i] = Num<T>::put(value(Num<T>::get(x[first + i]), c, b != 0, b ? a.bias_values[b0 + int(b) - 1] : 0.f));
         }
     }
 }

@@ -232,8 +232,9 @@ template <typename T>
 __device__ __forceinline__ bool odd_half(uint32_t x) { return (x & exponent_bits<T>()) == exponent_bits<T>(); }
 template <typename T>
 __device__ __forceinline__ bool odd_words(uint4 w) {
-    return odd_half<T>(w.x) || odd_half<T>(w.x >> 16) || odd_half<T>(w.y) || odd_half<T>(w.y >> 16) || odd_half<T>(w.z) ||
-           odd_half<T>(w.z >> 16) || odd_half<T>(w.w) || odd_half<T>(w.w >> 16);
+    // (an exponent of ones, and no other, carries into the bit above when its lowest bit is added)
+    constexpr uint32_t E = exponent_bits<T>(), M = E | E << 16, ONE = (E & (~E + 1)) | (E & (~E + 1)) << 16;
+    return ((((w.x & M) + ONE) | ((w.y & M) + ONE) | ((w.z & M) + ONE) | ((w.w & M) + ONE)) & 0x80008000u) != 0;
 }
 template <typename T>
 __device__ __forceinline__ uint32_t even_word(uint32_t x) {

@@ -383,15 +383,16 @@ __global__ void __launch_bounds__(32 * WM * WN) chunk_rows_kernel(const ChunkArg
 
 // ------------------------------------------------------------------ parts joined
 
-// 16 rows of a tile that was cut; `ys` CTAs for the tile whose first part CTA c of chunk_rows_kernel has, then as many
-// as it takes for each of the tensor cores'.  A warp takes a row at a time, each lane E neighbouring elements.
+// 16 rows of a tile that was cut, a warp each; `ys` CTAs for the tile whose first part CTA c of chunk_few_kernel (chunk_rows_kernel)
+// has, then as many as it takes for each of the tensor cores'.  A lane has E neighbouring elements, all parts' loads in flight
+// at once.  (Four rows a warp, one after the other: 21 us for the 148 rows and 9 parts of one short chunk, @@ now.)
 template <typename T, int D>
-__global__ void __launch_bounds__(128) join_chunk_kernel(const ChunkArgs a, int ys) {
-    constexpr int E = D / 32;
+__global__ void __launch_bounds__(512) join_chunk_kernel(const ChunkArgs a, int ys) {
+    constexpr int E = D / 32, P = 8;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const bool few = int(blockIdx.x) < a.grid * ys;
     const int b = int(blockIdx.x) - (few ? 0 : a.grid * ys), per = few ? ys : MANY / 16;
-    const int c = b / per, y16 = (b - c * per) * 16, MT = per * 16;
+    const int c = b / per, r = (b - c * per) * 16 + warp, MT = per * 16;
     const float* part_o = few ? a.part_o : a.t_part_o;
     const float2* part_l = few ? a.part_l : a.t_part_l;
     grid_dependency_wait();
@@ -399,37 +400,50 @@ __global__ void __launch_bounds__(128) join_chunk_kernel(const ChunkArgs a, int 
     const int4 s = (few ? a.split : a.t_split)[c];
     if (s.w == 0) return;
     const Request x = request(a, s.x);
-    const int M = x.rows(a);
+    const int row = s.z + r;
+    if (row >= x.rows(a)) return;
     // the first part is the one that starts its tile
-    auto slot = [&](int i) { return int64_t(2 * (c + i) + (i == 0)) * MT; };
-    for (int i = warp; i < 16; i += 4) {
-        const int r = y16 + i, row = s.z + r;
-        if (row >= M) return;
-        float m = -INFINITY;
-        for (int p = lane; p < s.w; p += 32) m = fmaxf(m, part_l[slot(p) + r].x);
+    auto slot = [&](int i) { return int64_t(2 * (c + i) + (i == 0)) * MT + r; };
+    float m = -INFINITY, l = 0.f, y[E];
 #pragma unroll
-        for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(FULL, m, d));
-        const float ms = m == -INFINITY ? 0.f : m;
-        // (a NaN part makes the sum NaN through its own weight)
-        float l = 0.f, y[E];
+    for (int e = 0; e < E; ++e) y[e] = 0.f;
+    // P parts at a time: their joint maximum, then their sums.  (A NaN part makes the sum NaN through its own weight.)
+    for (int p0 = 0; p0 < s.w; p0 += P) {
+        float2 w[P];
+        float o[P][E];
 #pragma unroll
-        for (int e = 0; e < E; ++e) y[e] = 0.f;
-#pragma unroll 4
-        for (int p = 0; p < s.w; ++p) {
-            const float2 part = part_l[slot(p) + r];
-            const float f = exp2f(part.x - ms) * part.y;
-            const float* o = part_o + (slot(p) + r) * D + lane * E;
-            l += f;
+        for (int j = 0; j < P; ++j) {
+            w[j] = make_float2(-INFINITY, 0.f);
+            if (p0 + j < s.w) {
+                w[j] = part_l[slot(p0 + j)];
+                const float* src = part_o + slot(p0 + j) * D + lane * E;
 #pragma unroll
-            for (int e = 0; e < E; ++e) y[e] += f * o[e];
+                for (int e = 0; e < E; ++e) o[j][e] = src[e];
+            }
         }
-        const float inv = l == 0.f ? 0.f : 1.f / l;
-        const int j = row / a.gs, h = s.y * a.gs + row % a.gs;
-        T* out = static_cast<T*>(a.out) + (x.q0 + j) * a.os[0] + h * a.os[1] + lane * E;
+        float mn = m;
 #pragma unroll
-        for (int e = 0; e < E; e += 2) *reinterpret_cast<uint32_t*>(out + e) = Mma<T>::pack(y[e] * inv, y[e + 1] * inv);
-        if (a.lse && lane == 0) a.lse[int64_t(x.q0 + j) * a.Hq + h] = (l == 0.f ? -INFINITY : m + log2f(l)) * 0.693147180559945309f;
+        for (int j = 0; j < P; ++j) mn = fmaxf(mn, w[j].x);
+        const float ms = mn == -INFINITY ? 0.f : mn, f0 = exp2f(m - ms);
+        m = mn;
+        l *= f0;
+#pragma unroll
+        for (int e = 0; e < E; ++e) y[e] *= f0;
+#pragma unroll
+        for (int j = 0; j < P; ++j)
+            if (p0 + j < s.w) {
+                const float f = exp2f(w[j].x - ms) * w[j].y;
+                l += f;
+#pragma unroll
+                for (int e = 0; e < E; ++e) y[e] += f * o[j][e];
+            }
     }
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    const int j = row / a.gs, h = s.y * a.gs + row % a.gs;
+    T* out = static_cast<T*>(a.out) + (x.q0 + j) * a.os[0] + h * a.os[1] + lane * E;
+#pragma unroll
+    for (int e = 0; e < E; e += 2) *reinterpret_cast<uint32_t*>(out + e) = Mma<T>::pack(y[e] * inv, y[e + 1] * inv);
+    if (a.lse && lane == 0) a.lse[int64_t(x.q0 + j) * a.Hq + h] = (l == 0.f ? -INFINITY : m + log2f(l)) * 0.693147180559945309f;
 }
 
 // ------------------------------------------------------------------ host
@@ -602,7 +616,7 @@ static fs_status run_chunk(ChunkArgs& a, const ChunkPlan& p, int dtype, void* st
     else st = FS_ERR_INVALID_ARG;   // (heads of up to 128 go to the tensor cores)
     if (st == FS_OK && a.t_grid > 0) st = launch_chunk_tensor(a, mapped ? &maps : nullptr, dtype, D, stream);
     if (st != FS_OK) return st;
-    return launch_pdl(join_chunk_kernel<T, D>, dim3(unsigned(a.grid * (p.MT / 16) + a.t_grid * (MANY / 16))), 128, 0, stream, a,
+    return launch_pdl(join_chunk_kernel<T, D>, dim3(unsigned(a.grid * (p.MT / 16) + a.t_grid * (MANY / 16))), 512, 0, stream, a,
                       p.MT / 16);
 }
 

@@ -11,6 +11,7 @@
 //   warps 8, 9      keys, half a tile each; warps 10, 11 values: page look-ups and copies into a ring of swizzled tiles
 //   warp 12         issues the products, PV of one tile and then its next S: in order, so that the weights have been read
 //                   when the scores behind them are written
+//   warp 13         looks values through that not every query sees, see below
 //   warp 14         what the next tiles are, into a ring that all roles read
 //   warp 15         queries of the next tile, as soon as the last product that reads the old ones is done
 // While one tile's softmax runs, the tensor cores have the other tile's products. (Keys 128 at a time and
@@ -55,7 +56,7 @@ struct ChunkTensorSmem {
     static constexpr int STAGES = D == 128 ? 5 : 11;
     static constexpr int KV = 2 * QTILE;
     static constexpr int BARS = KV + STAGES * TILE;
-    static constexpr int NBARS = 2 * STAGES + 16 + 2 * AHEAD;
+    static constexpr int NBARS = 3 * STAGES + 14 + 2 * AHEAD;
     static constexpr int SEGS = BARS + NBARS * 8;
     static constexpr int WORDS = SEGS + AHEAD * int(sizeof(Segment));
     static constexpr int TOTAL = WORDS + 160;
@@ -93,11 +94,11 @@ __global__ void __launch_bounds__(CNT, 1) chunk_tensor_kernel(const ChunkArgs a,
     const uint32_t base = smem_u32(mem);
     const int tid = threadIdx.x, warp = __shfl_sync(FULL, tid >> 5, 0), lane = tid & 31;
     // barriers: full[ST], empty[ST]; of each tile: queries there, queries done with, scores there, weights there
-    // (in two halves), product P V done; of each product, all done when a wait ran out; of each half of a value
-    // tile, landed; segments there, done with [AHEAD].  Then the segments, the tensor memory's address, a
+    // (in two halves), product P V done; of each product, all done when a wait ran out; landed, but still to be
+    // looked through [ST]; segments there, done with [AHEAD].  Then the segments, the tensor memory's address, a
     // flag, whose values had infinities taken out (four segments), which half key tiles miss pages (of sixteen tiles).
     const uint32_t full = base + S::BARS, empty = full + 8 * ST, qbar = empty + 8 * ST, qfree = qbar + 16, sbar = qfree + 16,
-                   pbar = sbar + 16, vbar = pbar + 32, xbar = vbar + 16, land = xbar + 16, segbar = land + 16, segfree = segbar + 8 * AHEAD;
+                   pbar = sbar + 16, vbar = pbar + 32, xbar = vbar + 16, land = xbar + 16, segbar = land + 8 * ST, segfree = segbar + 8 * AHEAD;
     volatile int* words = reinterpret_cast<volatile int*>(mem + S::WORDS);
     volatile int* dead = words + 1;
     volatile int* odd = words + 2;      // [4]
@@ -105,13 +106,14 @@ __global__ void __launch_bounds__(CNT, 1) chunk_tensor_kernel(const ChunkArgs a,
     Segment* segs = reinterpret_cast<Segment*>(mem + S::SEGS);
     // (set up while the launch before runs)
     if (warp == ROLES + 5) {
-        if (lane < ST) bar_init(full + 8 * lane, 2), bar_init(empty + 8 * lane, 1);
+        if (lane < ST) bar_init(full + 8 * lane, 2), bar_init(empty + 8 * lane, 1), bar_init(land + 8 * lane, 2);
         if (lane < 2) {
             bar_init(qbar + 8 * lane, 1), bar_init(qfree + 8 * lane, 1), bar_init(sbar + 8 * lane, 1);
-            bar_init(vbar + 8 * lane, 1), bar_init(xbar + 8 * lane, 1), bar_init(land + 8 * lane, 1);
+            bar_init(vbar + 8 * lane, 1), bar_init(xbar + 8 * lane, 1);
         }
-        // (a segment is read by four copying warps, the one that issues products, the queries' and eight of the softmax)
-        if (lane < AHEAD) bar_init(pbar + 8 * lane, 128), odd[lane] = 0, bar_init(segbar + 8 * lane, 1), bar_init(segfree + 8 * lane, 14);
+        // (a segment is read by four copying warps, the one that issues products, the one that looks values through, the
+        // queries' and eight of the softmax)
+        if (lane < AHEAD) bar_init(pbar + 8 * lane, 128), odd[lane] = 0, bar_init(segbar + 8 * lane, 1), bar_init(segfree + 8 * lane, 15);
         if (lane == 0) *dead = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -167,7 +169,7 @@ __global__ void __launch_bounds__(CNT, 1) chunk_tensor_kernel(const ChunkArgs a,
         const bool value = warp >= ROLES + 2;
         const int half = warp & 1, row = half * 64 + (lane & 15) * 4;
         const int64_t* str = value ? a.vc : a.kc;
-        uint32_t seq = 0, unit = 0, landed = 0;   // copies and key tiles before the segment; value tiles looked through
+        uint32_t seq = 0, unit = 0;   // copies and key tiles before the segment
         bool ok = true;
         for (uint32_t s = 0;; ++s) {
             const Segment& sg = next_segment(s, ok);
@@ -195,8 +197,8 @@ __global__ void __launch_bounds__(CNT, 1) chunk_tensor_kernel(const ChunkArgs a,
                     if (lane == 0) missing[2 * ((unit + i) & 15) + half] = any;
                 }
                 const uint32_t dst = base + S::KV + st * S::TILE;
-                const bool check = value && sg.partial(a, k0);
-                const uint32_t bar = check ? land + 8 * half : full + 8 * st;
+                // (values that not every query sees are looked through first)
+                const uint32_t bar = (value && sg.partial(a, k0) ? land : full) + 8 * st;
                 if (GATHER) {
                     if (lane == 0) bar_expect(bar, 64 * D * 2);
                     __syncwarp();
@@ -222,32 +224,10 @@ __global__ void __launch_bounds__(CNT, 1) chunk_tensor_kernel(const ChunkArgs a,
                     cp_async_wait<0>();
                 }
                 look_up(i + 1);
-                if (check) {
-                    // A value that only some of the tokens see may be infinite or NaN, which a weight of zero does not
-                    // cancel: such values are taken out of the tile, and added at the end to the outputs of the
-                    // queries that see them.
-                    if (GATHER) ok = __all_sync(FULL, bar_wait(bar, landed++ & 1, dead));
-                    if (!ok) break;
-                    __syncwarp();
-                    bool any = false;
-#pragma unroll 4
-                    for (int e = lane; e < 64 * DC; e += 32) {
-                        const uint32_t at = (e / 512) * (CK * 128) + half * 8192 + (e % 512) * 16;
-                        any |= odd_words<T>(*reinterpret_cast<const uint4*>(mem + (dst - base) + at));
-                    }
-                    if (__any_sync(FULL, any)) {
-                        for (int e = lane; e < 64 * DC; e += 32) {
-                            const uint32_t at = (e / 512) * (CK * 128) + half * 8192 + (e % 512) * 16;
-                            uint4* p = reinterpret_cast<uint4*>(mem + (dst - base) + at);
-                            *p = even_words<T>(*p);
-                        }
-                        odd[s & 3] = int(s) + 1;
-                    }
-                }
-                if (!GATHER || check) {
+                if (!GATHER) {
                     proxy_fence();
                     __syncwarp();
-                    if (lane == 0) bar_arrive(full + 8 * st);
+                    if (lane == 0) bar_arrive(bar);
                 }
             }
             if (!ok) break;
@@ -346,6 +326,40 @@ __global__ void __launch_bounds__(CNT, 1) chunk_tensor_kernel(const ChunkArgs a,
             bar_drain(xbar);
         }
         __syncwarp();
+    } else if (warp == ROLES + 5) {
+        // ================================================ values that not every query sees
+        // A value that only some of the tokens see may be infinite or NaN, which a weight of zero does not cancel: such values
+        // are taken out of the tile, and added at the end to the outputs of the queries that see them.
+        uint32_t seq = 0, uses = 0;     // copies before the segment; each stage's parity
+        bool ok = true;
+        for (uint32_t s = 0;; ++s) {
+            const Segment& sg = next_segment(s, ok);
+            if (!ok || sg.n == 0) break;
+            const int n = sg.n;
+#pragma unroll 1
+            for (int i = 0; i < n && ok; ++i) {
+                if (!sg.partial(a, sg.kt.at(sg.i0 + i))) continue;
+                const uint32_t st = (seq + values_copy(i, n)) % ST;
+                ok = __all_sync(FULL, bar_wait(land + 8 * st, uses >> st & 1, dead));
+                if (!ok) break;
+                uses ^= 1u << st;
+                uint4* tile = reinterpret_cast<uint4*>(mem + S::KV + st * S::TILE);
+                bool any = false;
+#pragma unroll 8
+                for (int e = lane; e < CK * DC; e += 32) any |= odd_words<T>(tile[e]);
+                if (__any_sync(FULL, any)) {
+                    for (int e = lane; e < CK * DC; e += 32) tile[e] = even_words<T>(tile[e]);
+                    odd[s & 3] = int(s) + 1;
+                }
+                proxy_fence();
+                __syncwarp();
+                if (lane < 2) bar_arrive(full + 8 * st);
+            }
+            if (!ok) break;
+            seq += 2 * n;
+            give_back(s);
+        }
+        if (!ok) *dead = 1;
     } else if (warp == ROLES + 6) {
         // ================================================ what the next tiles are
         int tile = words[6];

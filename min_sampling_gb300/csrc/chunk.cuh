@@ -11,7 +11,6 @@ namespace fsd {
 constexpr int FEW = 16;         // query rows that a tile of chunk_rows_kernel holds beside the tensor cores' tiles
 constexpr int MANY = 256;       // query rows of a tensor-core tile
 constexpr int FEW_START = 2;    // key tiles of 64 that start and end of such a tile take as long as
-constexpr int START = 3;        // key tiles that start and end of a tensor-core tile take as long as
 
 struct ChunkArgs {
     const void* q;
@@ -37,14 +36,12 @@ struct ChunkArgs {
                                 // logarithm
     int4* split;                // [grid]: request, head, row0, parts; parts 0: none
     // chunk_tensor_kernel's
-    int t_grid, t_tiles, t_least;   // t_grid 0: not launched
+    int t_grid;                 // 0: not launched
+    int t_start;                // units that start and end of a tile take as long as
     int out_32;                 // the output's rows are aligned to 32 bytes
     float* t_part_o;            // [2 t_grid][MANY][D]
     float2* t_part_l;
     int4* t_split;
-    int4* t_items;              // [t_tiles]: request, row0, units (and START for each tile) of a key/value head before (low, high word)
-    int* t_first;               // [R + 1]: tiles before a request
-    int* t_plan;                // tiles, units (low, high word) of a key/value head
 };
 
 // A request: its queries [q0, q0 + nq), query rows per key/value head (a row is a token's query head: token
@@ -134,48 +131,86 @@ __device__ __forceinline__ int64_t block_sum_before(int64_t mine, int64_t* words
     return before + x - mine;
 }
 
-// The tensor cores' tiles: MANY query rows of a request each, with the units before them. By one CTA.
+// A tensor-core tile of MANY query rows: a unit for every key tile, and t_start more.  (Of 128 rows or less it takes as long: it is
+// the chain of products and weights of a tile that is waited for, not their rate.)
+struct ManyTile {
+    int p_lo, p_hi;             // positions of its first and last token
+    KeyTiles<128> kt;
+    int units;
+    ManyTile() = default;
+    __device__ __forceinline__ ManyTile(const ChunkArgs& a, const Request& x, int row0) {
+        const int M = x.rows(a);
+        p_lo = x.pos(a, row0), p_hi = x.pos(a, min(row0 + MANY, M) - 1);
+        kt = KeyTiles<128>(a, p_lo, p_hi);
+        units = a.t_start + kt.n;
+    }
+    // Key tiles within the first n units.
+    __device__ __forceinline__ int tiles(int64_t n) const { return int(max(n - (units - kt.n), int64_t(0))); }
+};
+
+// A CTA's run of the tensor cores' units, of the tiles' for every key/value head.  It begins in the tile of rows row0 on of
+// request r, whose units (of all heads) have `before` units before them.
+struct ManyRun {
+    int64_t first, last, total, before;
+    int r, row0, ctas;
+    // The CTA of unit u.
+    __device__ __forceinline__ int owner(int64_t u) const { return int(((u + 1) * ctas - 1) / total); }
+};
+// Every CTA looks all requests over: threads share the requests to count their tiles, then the tiles to count their units.
+// words: 32 and NT more.  The run is in shared memory behind the next barrier; whether there is one.
 template <int NT>
-__device__ __forceinline__ void plan_tiles(const ChunkArgs& a, int64_t* words) {
-    const int tid = threadIdx.x;
-    auto tiles_of = [&](int r) {
-        const int M = request(a, r).rows(a);
+__device__ __forceinline__ bool many_run(const ChunkArgs& a, int cta, int64_t* words, ManyRun& run) {
+    const int tid = threadIdx.x, per = (a.R + NT - 1) / NT, r0 = min(tid * per, a.R), r1 = min(r0 + per, a.R);
+    int64_t* tiles_before = words + 32;     // [NT]: the tiles of the threads before
+    auto tiles_of = [&](const Request& x) {
+        const int M = x.rows(a);
         return M > a.rows_upto ? (M + MANY - 1) / MANY : 0;
     };
-    int64_t total, mine = 0;
-    const int per = (a.R + NT - 1) / NT, r0 = min(tid * per, a.R), r1 = min(r0 + per, a.R);
-    for (int r = r0; r < r1; ++r) mine += tiles_of(r);
-    int64_t at = block_sum_before<NT>(mine, words, total);
-    for (int r = r0; r < r1; ++r) {
-        a.t_first[r] = int(min(at, int64_t(a.t_tiles)));
-        at += tiles_of(r);
-    }
-    const int n = int(min(total, int64_t(a.t_tiles)));   // (no more unless query_starts descends)
-    if (tid == 0) a.t_first[a.R] = n;
+    auto units = [&](const Request& x, int row0) { return ManyTile(a, x, row0).units; };
+    int64_t tiles, total, mine = 0;
+    for (int r = r0; r < r1; ++r) mine += tiles_of(request(a, r));
+    tiles_before[tid] = block_sum_before<NT>(mine, words, tiles);
     __syncthreads();
-    const int each = (n + NT - 1) / NT, i0 = min(tid * each, n), i1 = min(i0 + each, n);
-    int first = 0;      // the request of tile i0: the last one that has no more than i0 tiles before it
-    for (int hi = a.R; i0 < i1 && hi - first > 1;) {
-        const int mid = (first + hi) / 2;
-        if (a.t_first[mid] <= i0) first = mid;
+    // tiles [i0, i1) are this thread's; the first is one of the last thread's that has no more than i0 before it
+    const int64_t each = (tiles + NT - 1) / NT, i0 = min(tid * each, tiles), i1 = min(i0 + each, tiles);
+    int lo = 0;
+    for (int hi = NT; i0 < i1 && hi - lo > 1;) {
+        const int mid = (lo + hi) / 2;
+        if (tiles_before[mid] <= i0) lo = mid;
         else hi = mid;
     }
-    auto units = [&](int& r, int i, int& row0) {
-        while (a.t_first[r + 1] <= i) ++r;
-        row0 = (i - a.t_first[r]) * MANY;
-        const Request x = request(a, r);
-        return KeyTiles<128>(a, x.pos(a, row0), x.pos(a, min(row0 + MANY, x.rows(a)) - 1)).n;
+    int64_t at = tiles_before[lo];
+    int r = lo * per;
+    Request x = {};
+    for (; i0 < i1 && r < a.R; at += tiles_of(x), ++r) {
+        x = request(a, r);
+        if (at + tiles_of(x) > i0) break;
+    }
+    // f(request, its number, first row) for each of them
+    auto walk = [&](auto f) {
+        Request y = x;
+        int k = r, row0 = int(i0 - at) * MANY;
+        for (int64_t i = i0; i < i1; ++i) {
+            while ((row0 >= y.rows(a) || y.rows(a) <= a.rows_upto) && k + 1 < a.R) y = request(a, ++k), row0 = 0;
+            if (!f(y, k, row0)) return;
+            row0 += MANY;
+        }
     };
     mine = 0;
-    int row0;
-    for (int i = i0, r = first; i < i1; ++i) mine += units(r, i, row0) + START;
-    at = block_sum_before<NT>(mine, words, total);
-    for (int i = i0, r = first; i < i1; ++i) {
-        const int u = units(r, i, row0) + START;
-        a.t_items[i] = make_int4(r, row0, int(uint32_t(at)), int(at >> 32));
-        at += u;
-    }
-    if (tid == 0) a.t_plan[0] = n, a.t_plan[1] = int(uint32_t(total)), a.t_plan[2] = int(total >> 32);
+    walk([&](const Request& y, int, int row0) { return mine += units(y, row0), true; });
+    int64_t before = block_sum_before<NT>(mine, words, total) * a.Hkv;
+    total *= a.Hkv;
+    const int ctas = int(max(min(int64_t(a.t_grid), total), int64_t(1)));
+    const int64_t first = cta < ctas ? total * cta / ctas : total, last = cta < ctas ? total * (cta + 1) / ctas : total;
+    if (tid == 0) run.first = first, run.last = last, run.total = total, run.ctas = ctas;
+    if (first < last && before <= first && first < before + mine * a.Hkv)
+        walk([&](const Request& y, int k, int row0) {
+            const int64_t n = int64_t(units(y, row0)) * a.Hkv;
+            if (first >= before + n) return before += n, true;
+            run.r = k, run.row0 = row0, run.before = before;
+            return false;
+        });
+    return first < last;
 }
 
 // A CTA's run of units, cut from all of the launch's in equal lengths.
@@ -208,6 +243,16 @@ __device__ __forceinline__ Run run_of(const ChunkArgs& a, int cta, int64_t* word
     run.place = Place{run.first < run.last ? int(words[16]) : 0, words[17], words[18]};
     __syncthreads();
     return run;
+}
+
+// The start of the kernel of few rows; whether a CTA has a run.  Behind the tensor cores' kernel it does not wait for that one, which
+// has waited for what comes before both of them; one CTA more waits for it in the end, so that what comes behind has both.
+__device__ __forceinline__ bool few_starts(const ChunkArgs& a) {
+    if (a.t_grid == 0) grid_dependency_wait();
+    allow_dependents();
+    if (int(blockIdx.x) < a.grid) return true;
+    grid_dependency_wait();
+    return false;
 }
 
 // Rows of no request become zeros.

@@ -39,7 +39,7 @@ struct ChunkSmem {
 // WM x WN warps over a tile of MT = 16 RM WM query rows and KT keys; each warp keeps its own running
 // maximum, sum and output over its share of the keys.  Bound by the reads of keys and values.
 template <typename T, int D, int MT, int WM, int WN, int RM, int KT>
-__global__ void __launch_bounds__(32 * WM * WN) chunk_rows_kernel(const ChunkArgs a) {
+__global__ void __launch_bounds__(32 * WM * WN) chunk_rows_kernel(const __grid_constant__ ChunkArgs a) {
     constexpr int NT = 32 * WM * WN;
     static_assert(MT == 16 * RM * WM && KT <= NT, "warp layout");
     using S = ChunkSmem<D, MT, KT>;
@@ -54,16 +54,8 @@ __global__ void __launch_bounds__(32 * WM * WN) chunk_rows_kernel(const ChunkArg
     int64_t* words = reinterpret_cast<int64_t*>(smem + S::OFF + 2 * 2 * KT * 8);     // scan, then the place found
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int wm = warp / WN, wn = warp % WN;
-    grid_dependency_wait();
-    allow_dependents();
-
-    if (a.t_grid > 0) {   // one CTA more, the first, for the tensor cores' plan
-        if (blockIdx.x == 0) {
-            plan_tiles<NT>(a, words);
-            return;
-        }
-    }
-    const int cta = int(blockIdx.x) - (a.t_grid > 0);
+    const int cta = int(blockIdx.x);
+    if (!few_starts(a)) return;
 
     // ---- this CTA's run of units
     const Run line = run_of<NT, MT, KT>(a, cta, words);
@@ -383,67 +375,112 @@ __global__ void __launch_bounds__(32 * WM * WN) chunk_rows_kernel(const ChunkArg
 
 // ------------------------------------------------------------------ parts joined
 
-// 16 rows of a tile that was cut, a warp each; `ys` CTAs for the tile whose first part CTA c of chunk_few_kernel (chunk_rows_kernel)
-// has, then as many as it takes for each of the tensor cores'.  A lane has E neighbouring elements, all parts' loads in flight
-// at once.  (Four rows a warp, one after the other: 21 us for the 148 rows and 9 parts of one short chunk, @@ now.)
+// A tile that was cut: its queries' first token, rows, head, first row, parts, and the CTA that has the first of them.
+struct JoinTile {
+    int q0, rows, head, row0, parts, cta;
+};
+constexpr int JOIN_CTAS = 2;    // on an SM
+
+// Rows of the list's tiles: a lane has K times 4 elements of one, P parts' loads in flight at once.
+template <typename T, int D, int K, int P>
+__device__ __forceinline__ void join_rows(const ChunkArgs& a, const JoinTile* tiles, int few_tiles, int MT, int all) {
+    constexpr int LANES = D / (4 * K), ROWS = 32 / LANES;   // of a row, of a warp
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, d = lane % LANES * 4, few_rows = few_tiles * MT;
+#pragma unroll 1
+    for (int at = (int(blockIdx.x) * 16 + warp) * ROWS; at < all; at += int(gridDim.x) * 16 * ROWS) {
+        const bool few = at < few_rows;
+        const int rows = few ? MT : MANY, n = few ? at : at - few_rows, r = n % rows + lane / LANES;
+        const JoinTile& s = tiles[(few ? 0 : few_tiles) + n / rows];
+        const int row = s.row0 + r, c = s.cta, parts = row < s.rows ? s.parts : 0;
+        const float* part_o = few ? a.part_o : a.t_part_o;
+        const float2* part_l = few ? a.part_l : a.t_part_l;
+        // the first part is the one that starts its tile
+        auto slot = [&](int i) { return (2 * (c + i) + (i == 0)) * rows + r; };
+        float m = -INFINITY, l = 0.f;
+        float4 y[K];
+#pragma unroll
+        for (int k = 0; k < K; ++k) y[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+        // P parts at a time: their joint maximum, then their sums.  (A NaN part makes the sum NaN through its own weight.)
+        for (int p0 = 0; p0 < parts; p0 += P) {
+            float2 w[P];
+            float4 o[P][K];
+#pragma unroll
+            for (int j = 0; j < P; ++j) {
+                w[j] = make_float2(-INFINITY, 0.f);
+                if (p0 + j < parts) {
+                    w[j] = part_l[slot(p0 + j)];
+#pragma unroll
+                    for (int k = 0; k < K; ++k)
+                        o[j][k] = *reinterpret_cast<const float4*>(part_o + slot(p0 + j) * D + d + k * LANES * 4);
+                }
+            }
+            float mn = m;
+#pragma unroll
+            for (int j = 0; j < P; ++j) mn = fmaxf(mn, w[j].x);
+            const float ms = mn == -INFINITY ? 0.f : mn, f0 = exp2f(m - ms);
+            m = mn;
+            l *= f0;
+#pragma unroll
+            for (int k = 0; k < K; ++k) y[k] = make_float4(y[k].x * f0, y[k].y * f0, y[k].z * f0, y[k].w * f0);
+#pragma unroll
+            for (int j = 0; j < P; ++j)
+                if (p0 + j < parts) {
+                    const float f = exp2f(w[j].x - ms) * w[j].y;
+                    l += f;
+#pragma unroll
+                    for (int k = 0; k < K; ++k)
+                        y[k] = make_float4(y[k].x + f * o[j][k].x, y[k].y + f * o[j][k].y, y[k].z + f * o[j][k].z,
+                                           y[k].w + f * o[j][k].w);
+                }
+        }
+        if (row >= s.rows) continue;
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        const int j = row / a.gs, h = s.head * a.gs + row % a.gs;
+        T* out = static_cast<T*>(a.out) + (s.q0 + j) * a.os[0] + h * a.os[1] + d;
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+            *reinterpret_cast<uint2*>(out + k * LANES * 4) =
+                make_uint2(Mma<T>::pack(y[k].x * inv, y[k].y * inv), Mma<T>::pack(y[k].z * inv, y[k].w * inv));
+        if (a.lse && d == 0) a.lse[int64_t(s.q0 + j) * a.Hq + h] = (l == 0.f ? -INFINITY : m + log2f(l)) * 0.693147180559945309f;
+    }
+}
+
+// The CTAs, as many as are resident, list the tiles that were cut and share their rows: so that a warp has a row or two and many
+// parts in flight where there are few rows, and else two parts of several rows.  (16 rows a CTA, 2736 CTAs that mostly found nothing to do:
+// 12 to 18 us; four rows a warp, one part after the other, 21 us for the 148 rows and 9 parts of one short chunk.)
 template <typename T, int D>
-__global__ void __launch_bounds__(512) join_chunk_kernel(const ChunkArgs a, int ys) {
-    constexpr int E = D / 32, P = 8;
+__global__ void __launch_bounds__(512, JOIN_CTAS) join_chunk_kernel(const __grid_constant__ ChunkArgs a, int MT) {
+    extern __shared__ JoinTile tiles[];     // [grid] of the few rows' CTAs, [t_grid] of the tensor cores'
+    __shared__ int count[2][16];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const bool few = int(blockIdx.x) < a.grid * ys;
-    const int b = int(blockIdx.x) - (few ? 0 : a.grid * ys), per = few ? ys : MANY / 16;
-    const int c = b / per, r = (b - c * per) * 16 + warp, MT = per * 16;
-    const float* part_o = few ? a.part_o : a.t_part_o;
-    const float2* part_l = few ? a.part_l : a.t_part_l;
     grid_dependency_wait();
     allow_dependents();
-    const int4 s = (few ? a.split : a.t_split)[c];
-    if (s.w == 0) return;
-    const Request x = request(a, s.x);
-    const int row = s.z + r;
-    if (row >= x.rows(a)) return;
-    // the first part is the one that starts its tile
-    auto slot = [&](int i) { return int64_t(2 * (c + i) + (i == 0)) * MT + r; };
-    float m = -INFINITY, l = 0.f, y[E];
-#pragma unroll
-    for (int e = 0; e < E; ++e) y[e] = 0.f;
-    // P parts at a time: their joint maximum, then their sums.  (A NaN part makes the sum NaN through its own weight.)
-    for (int p0 = 0; p0 < s.w; p0 += P) {
-        float2 w[P];
-        float o[P][E];
-#pragma unroll
-        for (int j = 0; j < P; ++j) {
-            w[j] = make_float2(-INFINITY, 0.f);
-            if (p0 + j < s.w) {
-                w[j] = part_l[slot(p0 + j)];
-                const float* src = part_o + slot(p0 + j) * D + lane * E;
-#pragma unroll
-                for (int e = 0; e < E; ++e) o[j][e] = src[e];
-            }
+    // The list, in the order of the CTAs, the same in all of this kernel's.
+    int few_tiles = 0, n_tiles = 0;
+    for (int i0 = 0; i0 < a.grid + a.t_grid; i0 += 512) {
+        const int i = i0 + int(threadIdx.x), c = i < a.grid ? i : i - a.grid;
+        const bool few = i < a.grid;
+        int4 s = make_int4(0, 0, 0, 0);
+        if (c < (few ? a.grid : a.t_grid)) s = (few ? a.split : a.t_split)[c];
+        const unsigned cut = __ballot_sync(FULL, s.w > 0), cut_few = __ballot_sync(FULL, few && s.w > 0);
+        __syncthreads();
+        if (lane == 0) count[0][warp] = __popc(cut_few), count[1][warp] = __popc(cut);
+        __syncthreads();
+        int here = n_tiles + __popc(cut & ((1u << lane) - 1));
+        for (int w = 0; w < 16; ++w) {
+            if (w < warp) here += count[1][w];
+            few_tiles += count[0][w], n_tiles += count[1][w];
         }
-        float mn = m;
-#pragma unroll
-        for (int j = 0; j < P; ++j) mn = fmaxf(mn, w[j].x);
-        const float ms = mn == -INFINITY ? 0.f : mn, f0 = exp2f(m - ms);
-        m = mn;
-        l *= f0;
-#pragma unroll
-        for (int e = 0; e < E; ++e) y[e] *= f0;
-#pragma unroll
-        for (int j = 0; j < P; ++j)
-            if (p0 + j < s.w) {
-                const float f = exp2f(w[j].x - ms) * w[j].y;
-                l += f;
-#pragma unroll
-                for (int e = 0; e < E; ++e) y[e] += f * o[j][e];
-            }
+        if (s.w > 0) {
+            const Request x = request(a, s.x);
+            tiles[here] = JoinTile{x.q0, x.rows(a), s.y, s.z, s.w, c};
+        }
     }
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    const int j = row / a.gs, h = s.y * a.gs + row % a.gs;
-    T* out = static_cast<T*>(a.out) + (x.q0 + j) * a.os[0] + h * a.os[1] + lane * E;
-#pragma unroll
-    for (int e = 0; e < E; e += 2) *reinterpret_cast<uint32_t*>(out + e) = Mma<T>::pack(y[e] * inv, y[e + 1] * inv);
-    if (a.lse && lane == 0) a.lse[int64_t(x.q0 + j) * a.Hq + h] = (l == 0.f ? -INFINITY : m + log2f(l)) * 0.693147180559945309f;
+    __syncthreads();
+    const int all = few_tiles * MT + (n_tiles - few_tiles) * MANY;
+    constexpr int K = D == 256 ? 2 : 1;
+    if (all <= int(gridDim.x) * 16) join_rows<T, D, K, 4 / K>(a, tiles, few_tiles, MT, all);
+    else join_rows<T, D, 2, 2>(a, tiles, few_tiles, MT, all);
 }
 
 // ------------------------------------------------------------------ host
@@ -553,8 +590,8 @@ struct ChunkPlan {
     int MT, KT;         // chunk_rows_kernel's tile
     int grid, least;    // its CTAs; key tiles of a CTA at least
     size_t part_o, part_l, split, bytes;   // offsets
-    int t_grid, t_least, t_tiles;          // the tensor cores' CTAs (0: not launched)
-    size_t t_part_o, t_part_l, t_split, t_items, t_first, t_plan;
+    int t_grid;                            // the tensor cores' CTAs (0: not launched)
+    size_t t_part_o, t_part_l, t_split;
 };
 
 static size_t add_bytes(size_t& at, size_t n) {
@@ -583,16 +620,12 @@ static ChunkPlan chunk_plan(const fs_paged_kv& c, int N, int R, int Hq, int widt
     if (tensor) {
         // One CTA per SM.  A request of FEW rows or less has no tile there.
         const int64_t all = int64_t(N) * gs;
-        p.t_least = 1;
-        p.t_tiles = int(std::min<int64_t>(all / MANY + std::min<int64_t>(R, all / (FEW + 1) + 1), 0x7fffffff));
-        const int64_t t_units = int64_t(p.t_tiles) * c.num_heads * ((int64_t(width) * c.page_size + 127) / 128 + 2 + START);
-        p.t_grid = int(std::max<int64_t>(1, std::min<int64_t>(sms, (t_units + p.t_least - 1) / p.t_least)));
+        const int64_t t_tiles = all / MANY + std::min<int64_t>(R, all / (FEW + 1) + 1);
+        const int64_t t_units = t_tiles * c.num_heads * ((int64_t(width) * c.page_size + 127) / 128 + 4);
+        p.t_grid = int(std::max<int64_t>(1, std::min<int64_t>(sms, t_units)));
         p.t_part_o = add_bytes(at, size_t(2) * p.t_grid * MANY * D * 4);
         p.t_part_l = add_bytes(at, size_t(2) * p.t_grid * MANY * 8);
         p.t_split = add_bytes(at, size_t(p.t_grid) * sizeof(int4));
-        p.t_items = add_bytes(at, size_t(p.t_tiles) * sizeof(int4));
-        p.t_first = add_bytes(at, (size_t(R) + 1) * 4);
-        p.t_plan = add_bytes(at, 16);
     }
     p.bytes = at;
     return p;
@@ -607,17 +640,19 @@ static fs_status launch_rows(const ChunkArgs& a, void* stream) {
 }
 
 template <typename T, int D>
-static fs_status run_chunk(ChunkArgs& a, const ChunkPlan& p, int dtype, void* stream) {
+static fs_status run_chunk(ChunkArgs& a, const ChunkPlan& p, int sms, int dtype, void* stream) {
     ChunkMaps maps = {};
     const bool mapped = chunk_maps(a, dtype, D, maps);
-    fs_status st;
+    fs_status st = FS_OK;
+    if (a.t_grid > 0) st = launch_chunk_tensor(a, mapped ? &maps : nullptr, dtype, D, stream);
+    if (st != FS_OK) return st;
     if (p.MT == FEW) st = mapped ? launch_chunk_few(a, maps, dtype, D, stream) : launch_rows<T, D, FEW, 1, 4, 1, 64>(a, stream);
     else if constexpr (D == 256) st = launch_rows<T, D, 64, 4, 1, 1, 32>(a, stream);
     else st = FS_ERR_INVALID_ARG;   // (heads of up to 128 go to the tensor cores)
-    if (st == FS_OK && a.t_grid > 0) st = launch_chunk_tensor(a, mapped ? &maps : nullptr, dtype, D, stream);
     if (st != FS_OK) return st;
-    return launch_pdl(join_chunk_kernel<T, D>, dim3(unsigned(a.grid * (p.MT / 16) + a.t_grid * (MANY / 16))), 512, 0, stream, a,
-                      p.MT / 16);
+    const unsigned most = unsigned(a.grid * (p.MT / 16) + a.t_grid * (MANY / 16));
+    return launch_pdl(join_chunk_kernel<T, D>, dim3(std::min(most, unsigned(JOIN_CTAS * sms))), 512,
+                      size_t(a.grid + a.t_grid) * sizeof(JoinTile), stream, a, p.MT);
 }
 
 static fs_status check_chunk(const fs_paged_kv* c, int N, int R, int Hq, int width, int most) {
@@ -727,25 +762,21 @@ fs_status fs_paged_chunk_attention(const fs_paged_kv* cache, const void* query, 
     a.part_l = reinterpret_cast<float2*>(ws + p.part_l);
     a.split = reinterpret_cast<int4*>(ws + p.split);
     a.t_grid = p.t_grid;
-    a.t_least = p.t_least;
+    a.t_start = cache->head_dim == 64 ? 2 : 3;
     a.out_32 = (reinterpret_cast<uintptr_t>(out) % 32 == 0 && a.os[0] % 16 == 0 && a.os[1] % 16 == 0);
-    a.t_tiles = p.t_tiles;
     if (p.t_grid > 0) {
         a.t_part_o = reinterpret_cast<float*>(ws + p.t_part_o);
         a.t_part_l = reinterpret_cast<float2*>(ws + p.t_part_l);
         a.t_split = reinterpret_cast<int4*>(ws + p.t_split);
-        a.t_items = reinterpret_cast<int4*>(ws + p.t_items);
-        a.t_first = reinterpret_cast<int*>(ws + p.t_first);
-        a.t_plan = reinterpret_cast<int*>(ws + p.t_plan);
     }
     const int D = cache->head_dim, dt = cache->dtype;
     if (dt == FS_BF16)
-        return D == 64    ? run_chunk<__nv_bfloat16, 64>(a, p, dt, stream)
-               : D == 128 ? run_chunk<__nv_bfloat16, 128>(a, p, dt, stream)
-                          : run_chunk<__nv_bfloat16, 256>(a, p, dt, stream);
-    return D == 64    ? run_chunk<__half, 64>(a, p, dt, stream)
-           : D == 128 ? run_chunk<__half, 128>(a, p, dt, stream)
-                      : run_chunk<__half, 256>(a, p, dt, stream);
+        return D == 64    ? run_chunk<__nv_bfloat16, 64>(a, p, sms, dt, stream)
+               : D == 128 ? run_chunk<__nv_bfloat16, 128>(a, p, sms, dt, stream)
+                          : run_chunk<__nv_bfloat16, 256>(a, p, sms, dt, stream);
+    return D == 64    ? run_chunk<__half, 64>(a, p, sms, dt, stream)
+           : D == 128 ? run_chunk<__half, 128>(a, p, sms, dt, stream)
+                      : run_chunk<__half, 256>(a, p, sms, dt, stream);
 }
 
 }  // extern "C"

@@ -43,7 +43,7 @@ struct FewSmem {
 };
 
 template <typename T, int D>
-__global__ void __launch_bounds__(FNT) chunk_few_kernel(const ChunkArgs a, const __grid_constant__ ChunkMaps maps) {
+__global__ void __launch_bounds__(FNT) chunk_few_kernel(const __grid_constant__ ChunkArgs a, const __grid_constant__ ChunkMaps maps) {
     using S = FewSmem<D>;
     constexpr int ST = S::STAGES, DC = D / 8;
     constexpr float UP = std::is_same<T, __half>::value ? 32768.f : 1.f;   // the weights' factor in the product
@@ -58,15 +58,8 @@ __global__ void __launch_bounds__(FNT) chunk_few_kernel(const ChunkArgs a, const
     volatile int* gone = dead + 1;      // [4], a warp whose wait ran out
     volatile int* missing = dead + 5;   // [ST]
     int64_t* words = reinterpret_cast<int64_t*>(mem + S::MERGE);     // while the run is looked up
-    grid_dependency_wait();
-    allow_dependents();
-    if (a.t_grid > 0) {   // one CTA more, the first, for the tensor cores' plan
-        if (blockIdx.x == 0) {
-            plan_tiles<FNT>(a, words);
-            return;
-        }
-    }
-    const int cta = int(blockIdx.x) - (a.t_grid > 0);
+    const int cta = int(blockIdx.x);
+    if (!few_starts(a)) return;
     const Run run = run_of<FNT, FEW, FK>(a, cta, words);
     if (tid == 0) {
         a.split[cta] = make_int4(0, 0, 0, 0);

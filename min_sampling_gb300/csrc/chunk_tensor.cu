@@ -59,7 +59,8 @@ struct ChunkTensorSmem {
     static constexpr int NBARS = 3 * STAGES + 14 + 2 * AHEAD;
     static constexpr int SEGS = BARS + NBARS * 8;
     static constexpr int WORDS = SEGS + AHEAD * int(sizeof(Segment));
-    static constexpr int TOTAL = WORDS + 160;
+    static constexpr int RUN = (WORDS + 160 + 7) / 8 * 8;
+    static constexpr int TOTAL = RUN + int(sizeof(ManyRun));
     static_assert(TOTAL <= 227 * 1024, "shared memory");
 };
 
@@ -71,6 +72,11 @@ __device__ __forceinline__ void fma_pair(float& x, float& y, float mul, float ad
 __device__ __forceinline__ void add_pair(float& x, float& y, float a, float b) {
     asm("{ .reg .b64 a, b; mov.b64 a, {%0, %1}; mov.b64 b, {%2, %3}; add.rn.f32x2 a, a, b; mov.b64 {%0, %1}, a; }"
         : "+f"(x), "+f"(y) : "f"(a), "f"(b));
+}
+
+template <int N> using Int = std::integral_constant<int, N>;
+__device__ __forceinline__ void max3(float& m, float x, float y) {    // (NaN loses)
+    asm("max.f32 %0, %0, %1, %2;" : "+f"(m) : "f"(x), "f"(y));
 }
 
 __device__ __forceinline__ void store32(void* p, const uint32_t (&x)[8]) {
@@ -86,7 +92,7 @@ __device__ __forceinline__ int values_copy(int i, int n) { return i == n - 1 ? 2
 // ------------------------------------------------------------------ the kernel
 
 template <typename T, int D, bool GATHER>
-__global__ void __launch_bounds__(CNT, 1) chunk_tensor_kernel(const ChunkArgs a, const __grid_constant__ ChunkMaps maps) {
+__global__ void __launch_bounds__(CNT, 1) chunk_tensor_kernel(const __grid_constant__ ChunkArgs a, const __grid_constant__ ChunkMaps maps) {
     using S = ChunkTensorSmem<D>;
     using W = Weights<T>;
     constexpr int ST = S::STAGES, DC = D / 8;
@@ -124,28 +130,16 @@ __global__ void __launch_bounds__(CNT, 1) chunk_tensor_kernel(const ChunkArgs a,
     grid_dependency_wait();
     allow_dependents();
 
-    // ---- this CTA's run of units
-    const int n_tiles = a.t_plan[0];
-    // (units and, for each tile of each key/value head, START more that its start and end take as long as)
-    const int64_t total = (int64_t(a.t_plan[2]) << 32 | uint32_t(a.t_plan[1])) * a.Hkv;
-    const int64_t run = max(int64_t(a.t_least), (total + a.t_grid - 1) / a.t_grid);
-    const int64_t first_unit = min(blockIdx.x * run, total), last = min(first_unit + run, total);
+    // ---- this CTA's run of units (the ring's memory is free for the search: the fence orders it before the copies)
+    const ManyRun& run = *reinterpret_cast<ManyRun*>(mem + S::RUN);
+    const bool any = many_run<CNT>(a, int(blockIdx.x), reinterpret_cast<int64_t*>(mem + S::KV), *reinterpret_cast<ManyRun*>(mem + S::RUN));
     if (tid == 0) a.t_split[blockIdx.x] = make_int4(0, 0, 0, 0);
-    for (int i = tid; i < n_tiles; i += CNT) {
-        const int4 it = a.t_items[i];
-        const int64_t before = (int64_t(it.w) << 32 | uint32_t(it.z)) * a.Hkv;
-        int64_t next = total;
-        if (i + 1 < n_tiles) {
-            const int4 up = a.t_items[i + 1];
-            next = (int64_t(up.w) << 32 | uint32_t(up.z)) * a.Hkv;
-        }
-        if (before <= first_unit && first_unit < next) words[6] = i;
-    }
+    proxy_fence();
     tmem_fence_before();
     __syncthreads();
     tmem_fence_after();
     const uint32_t tmem = __shfl_sync(FULL, uint32_t(words[0]), 0);
-    if (first_unit >= last) {
+    if (!any) {
         if (warp == ROLES + 4) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
         return;
     }
@@ -273,7 +267,7 @@ __global__ void __launch_bounds__(CNT, 1) chunk_tensor_kernel(const ChunkArgs a,
                     tmem_fence_after();
                     if (ok) {
 #pragma unroll
-                        for (int k = 4 * h; k < 4 * h + 4; ++k)
+                        for (int k = 6 * h; k < 6 + 2 * h; ++k)
                             mma_tmem(lead, o, p + 8 * k, v + k * (2048 >> 4), CK * 128, hi, PV, add || k > 0);
                     }
                 }
@@ -362,8 +356,9 @@ __global__ void __launch_bounds__(CNT, 1) chunk_tensor_kernel(const ChunkArgs a,
         if (!ok) *dead = 1;
     } else if (warp == ROLES + 6) {
         // ================================================ what the next tiles are
-        int tile = words[6];
-        int64_t u = first_unit;
+        int r = run.r, row0 = run.row0;
+        int64_t u = run.first, before = run.before;
+        const int64_t last = run.last;
         bool ok = true;
         for (uint32_t s = 0; ok; ++s) {
             if (s >= AHEAD) ok = __all_sync(FULL, bar_wait(segfree + 8 * (s % AHEAD), (s / AHEAD - 1) & 1, dead));
@@ -371,23 +366,36 @@ __global__ void __launch_bounds__(CNT, 1) chunk_tensor_kernel(const ChunkArgs a,
             Segment sg;
             sg.n = 0;
             if (u < last) {
-                const int4 it = a.t_items[tile];
-                sg.r = it.x, sg.row0 = it.y;
-                sg.x = request(a, it.x);
+                sg.r = r, sg.row0 = row0;
+                sg.x = request(a, r);
                 sg.M = sg.x.rows(a);
-                sg.p_lo = sg.x.pos(a, it.y), sg.p_hi = sg.x.pos(a, min(it.y + MANY, sg.M) - 1);
-                sg.kt = KeyTiles<CK>(a, sg.p_lo, sg.p_hi);
-                const int each = START + sg.kt.n;
-                const int64_t before = (int64_t(it.w) << 32 | uint32_t(it.z)) * a.Hkv, rel = u - before;
-                sg.head = int(rel / each);
+                const ManyTile tile(a, sg.x, row0);
+                const int each = tile.units;
+                sg.p_lo = tile.p_lo, sg.p_hi = tile.p_hi, sg.kt = tile.kt;
+                sg.head = int((u - before) / each);
                 const int64_t from = before + int64_t(sg.head) * each;     // of this head
-                sg.i0 = int(max(u - from - START, int64_t(0)));
-                sg.n = int(min(int64_t(each), last - from)) - START - sg.i0;
+                sg.i0 = tile.tiles(u - from);
+                sg.n = tile.tiles(min(int64_t(each), last - from)) - sg.i0;
                 sg.whole = sg.n == sg.kt.n;
-                sg.parts = sg.whole || sg.i0 > 0 ? 0 : int((from + each - 1) / run) - int(blockIdx.x) + 1;
+                sg.parts = sg.whole || sg.i0 > 0 ? 0 : run.owner(from + each - 1) - int(blockIdx.x) + 1;
                 u = min(from + each, last);
-                if (u >= before + int64_t(each) * a.Hkv) ++tile;
-                // (a run that ends within a tile's START leaves all of it to the next)
+                if (u < last && u >= before + int64_t(each) * a.Hkv) {
+                    before += int64_t(each) * a.Hkv;
+                    row0 += MANY;
+                    if (row0 >= sg.M) {     // the next request with more than FEW rows
+                        row0 = 0;
+                        for (unsigned hit = 0; hit == 0;) {
+                            const int k = r + 1 + lane;
+                            hit = __ballot_sync(FULL, k < a.R && request(a, min(k, a.R - 1)).rows(a) > a.rows_upto);
+                            r += hit ? __ffs(int(hit)) : 32;
+                            if (!hit && r >= a.R - 1) {     // (none is left: not with the lengths that the run was cut by)
+                                u = last;
+                                break;
+                            }
+                        }
+                    }
+                }
+                // (a run that ends within a tile's start leaves all of it to the next)
                 if (sg.n <= 0) sg.n = 0;
             }
             if (lane == 0) segs[s % AHEAD] = sg;
@@ -481,45 +489,50 @@ __global__ void __launch_bounds__(CNT, 1) chunk_tensor_kernel(const ChunkArgs a,
                     const bool edge = t_hi - k0 >= a.window, gone = missing[2 * ((unit + i) & 15)] | missing[2 * ((unit + i) & 15) + 1];
                     const bool some = k0 + CK > t_lo + 1 || edge;   // not every row sees all of the keys
                     const int lim = pos + 1 - k0, low = edge ? pos - a.window + 1 - k0 : 0, first = a.sinks - k0;
-                    if (gone || !(mul > 0.f)) {
-                        // Rare: scaled here, so that scores of keys not seen are -infinity whatever the scale; a key whose
-                        // page does not exist is NaN.
+                    if (some || gone || !(mul > 0.f)) {
+                        // Scores of keys not seen become -infinity, whatever the scale; a key whose page does not exist is NaN.
+                        // (In tensor memory, 32 at a time: unrolled over all the scores in registers, this code stood
+                        // between the maximum's and the weights', and was as slow where it ran.)
+                        const bool rare = gone || !(mul > 0.f);
+                        const float f = rare ? mul : 1.f;
+                        if (rare) mul = 1.f;
 #pragma unroll 1
                         for (int c = 0; c < CK; c += 32) {
                             uint32_t x[32];
                             tmem_ld32(x, sc + c);
+                            // the keys of these 32 that the row sees: below `lim`, and from `low` on or below `first`
+                            auto below = [](int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1; };
+                            const uint32_t see = below(lim - c) & (~below(low - c) | below(first - c));
+                            const uint32_t lost = gone ? missing_pages(a, sg.r, k0 + c) : 0u;
                             tmem_wait_ld();
-                            const unsigned lost = gone ? missing_pages(a, sg.r, k0 + c) : 0u;
+                            keep32(x);
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) {
-                                const int k = c + e;
-                                const bool see = k < lim && (k >= low || k < first);
-                                x[e] = !see ? 0xff800000u : lost >> e & 1 ? 0x7fffffffu : __float_as_uint(__uint_as_float(x[e]) * mul);
+                            for (int e = 0; e < 32; ++e) x[e] = see >> e & 1 ? __float_as_uint(__uint_as_float(x[e]) * f) : 0xff800000u;
+                            if (lost & see) {
+#pragma unroll
+                                for (int e = 0; e < 32; ++e)
+                                    if (lost & see & 1u << e) x[e] = 0x7fffffffu;
                             }
                             tmem_st32(sc + c, x);
                         }
                         tmem_wait_st();
-                        mul = 1.f;
                     }
+                    // The second half of the scores is on its way while the first half's maximum is taken.
                     uint32_t x[CK];
-#pragma unroll
-                    for (int c = 0; c < CK / 32; ++c) tmem_ld32(part<32>(x, c), sc + c * 32);
+                    auto load = [&](int i) { tmem_ld32(part<32>(x, i), sc + 32 * i); };
+                    load(0), load(1);
                     tmem_wait_ld();
-                    if (some) {
-#pragma unroll
-                        for (int c = 0; c < CK / 32; ++c) {
-                            // the keys of these 32 that the row sees: below `lim`, and from `low` on or below `first`
-                            auto below = [](int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1; };
-                            const uint32_t see = below(lim - 32 * c) & (~below(low - 32 * c) | below(first - 32 * c));
-#pragma unroll
-                            for (int e = 0; e < 32; ++e)
-                                if (!(see >> e & 1)) x[32 * c + e] = 0xff800000u;
-                        }
-                    }
+                    load(2), load(3);
                     float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                    for (int e = 0; e < CK; e += 2)
-                        m4[(e >> 1) & 3] = fmaxf(m4[(e >> 1) & 3], fmaxf(__uint_as_float(x[e]), __uint_as_float(x[e + 1])));
+                    for (int e = 0; e < CK; e += 2) {
+                        if (e == CK / 2) {
+                            tmem_wait_ld();
+                            keep32(part<32>(x, 2));
+                            keep32(part<32>(x, 3));
+                        }
+                        max3(m4[(e >> 1) & 3], __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
+                    }
                     float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
                     mx *= mul;
                     if (!(mx > -INFINITY)) mx = m;   // a scale of 0 times infinity, or nothing but NaN
@@ -546,17 +559,27 @@ __global__ void __launch_bounds__(CNT, 1) chunk_tensor_kernel(const ChunkArgs a,
                     // A maximum is a rounded product and a weight's exponent below is not: beyond 2^20 their difference, up
                     // to 2^-25 of the maximum, would count in the exponent (at 2^31 it is 2^6 and more).
                     if (__any_sync(FULL, fabsf(m) > 0x1p20f && m > -INFINITY)) {
+#pragma unroll 1
+                        for (int c = 0; c < CK; c += 32) {
+                            uint32_t y[32];
+                            tmem_ld32(y, sc + c);
+                            tmem_wait_ld();
 #pragma unroll
-                        for (int e = 0; e < CK; ++e) x[e] = __float_as_uint(__fmul_rn(__uint_as_float(x[e]), mul) - ms);
+                            for (int e = 0; e < 32; ++e) y[e] = __float_as_uint(__fmul_rn(__uint_as_float(y[e]), mul) - ms);
+                            tmem_st32(sc + c, y);
+                        }
+                        tmem_wait_st();
+                        load(0), load(1), load(2), load(3);
+                        tmem_wait_ld();
                         mul = 1.f;
                         off = W::SHIFT;
                     }
                     // ---- weights
                     float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
+                    // (three quarters of them first: the products that read those are done when the last quarter is there)
+                    auto weigh = [&](auto from, auto to) {
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-#pragma unroll
-                        for (int e = 64 * h; e < 64 * h + 64; e += 4) {
+                        for (int e = from; e < to; e += 4) {
                             float p0 = __uint_as_float(x[e]), p1 = __uint_as_float(x[e + 1]), p2 = __uint_as_float(x[e + 2]),
                                   p3 = __uint_as_float(x[e + 3]);
                             fma_pair(p0, p1, mul, off);
@@ -567,11 +590,20 @@ __global__ void __launch_bounds__(CNT, 1) chunk_tensor_kernel(const ChunkArgs a,
                             x[e / 2] = Mma<T>::pack(p0, p1);
                             x[e / 2 + 1] = Mma<T>::pack(p2, p3);
                         }
-                        tmem_st32(sc + 32 * h, part<32>(x, h));
+                    };
+                    auto there = [&](int h) {
                         tmem_wait_st();
                         tmem_fence_before();
                         bar_arrive(pbar + 16 * t + 8 * h);
-                    }
+                    };
+                    weigh(Int<0>(), Int<96>());
+                    tmem_st32(sc, part<32>(x, 0));
+                    tmem_st16(sc + 32, part<16>(x, 2));
+                    weigh(Int<96>(), Int<112>());
+                    there(0);
+                    weigh(Int<112>(), Int<128>());
+                    tmem_st16(sc + 48, part<16>(x, 3));
+                    there(1);
                     l += (s0 + s1) + (s2 + s3);
                 }
                 // ---- the row's output, once the last product is done

@@ -85,6 +85,13 @@ __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&x)[16]
         "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};"
         ::W8(x, 0), W8(x, 8), "r"(addr) : "memory");
 }
+// What is read from these registers is read behind this point (and so behind a wait before it).
+__device__ __forceinline__ void keep32(uint32_t (&x)[32]) {
+#define K8(x, i) "+r"(x[i]), "+r"(x[i + 1]), "+r"(x[i + 2]), "+r"(x[i + 3]), "+r"(x[i + 4]), "+r"(x[i + 5]), "+r"(x[i + 6]), "+r"(x[i + 7])
+    asm volatile("" : K8(x, 0), K8(x, 8));
+    asm volatile("" : K8(x, 16), K8(x, 24));
+#undef K8
+}
 #undef R8
 #undef W8
 

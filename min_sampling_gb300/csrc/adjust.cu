@@ -10,6 +10,9 @@
 //                  names it, counts them in a table in shared memory and computes
 //                  their logits, while the copy ends; then it writes them.  Where a table overflows, or there would be too many, the
 //                  tokens are counted by ranges, a word each.
+// 64 rows of 151936 logits in float32 with histories of 4096: 21 us, 3.7 TB/s (copied alone 10 us); 256 of 151665 in bf16
+// with masks and histories of 700: 42 us, 3.7 TB/s (copied alone 30 us): what is left is change_kernel's way through a history, of which
+// only the copy's last wave is beside it.
 // In place, and where there is nothing to mask or to change, one of them is left out. (In one launch, each CTA counting
 // for its own 8192 logits: 64 rows of 151936 28 us, 256 of 151665 with masks 64 us; a CTA's way through the history
 // is longer than that through its logits.)  No scratch memory, no order that matters: counts are integers, and of
@@ -108,16 +111,17 @@ struct Mask {
     int n;
     __device__ __forceinline__ Mask(const AdjustArgs& a, int row) : words(nullptr), nothing(false), n(a.words) {
         if (!a.allowed) return;
-        const int m = a.allowed_rows ? a.allowed_rows[row] : row;
+        const int m = a.allowed_rows ? __ldcg(a.allowed_rows + row) : row;
         nothing = m >= a.masks;
         if (m >= 0 && !nothing) words = a.allowed + int64_t(m) * a.words;
     }
-    template <int N>
+    template <int N, bool L2 = false>
     __device__ __forceinline__ uint32_t bits(int e) const {
         constexpr uint32_t ALL = (1u << N) - 1;
         if (!words) return nothing ? 0u : ALL;
         const int k = e >> 5;
-        return __funnelshift_r(words[k], (e & 31) > 32 - N && k + 1 < n ? words[k + 1] : 0u, e & 31) & ALL;
+        const uint32_t w = L2 ? __ldcg(words + k) : words[k];
+        return __funnelshift_r(w, (e & 31) > 32 - N && k + 1 < n ? words[k + 1] : 0u, e & 31) & ALL;
     }
 };
 
@@ -179,7 +183,7 @@ __global__ void __launch_bounds__(CHANGE_NT, 2) change_kernel(const AdjustArgs a
     constexpr uint32_t SEEN = 0x80000000u, EMPTY = 0xffffffffu;
     extern __shared__ __align__(16) uint32_t smem[];
     const int tid = threadIdx.x;
-    // (behind copy_kernel, what that one waited for is there)
+    // (Behind copy_kernel, what that one waited for is there: in L2, from which all is read; an SM's L1 may hold what was there before.)
     if (!a.copied) grid_dependency_wait();
     allow_dependents();
     const int row = blockIdx.x >> a.split, part = blockIdx.x & ((1 << a.split) - 1);
@@ -194,21 +198,21 @@ __global__ void __launch_bounds__(CHANGE_NT, 2) change_kernel(const AdjustArgs a
             for (int i = first + tid * 4; i < min(first + STAGED, last); i += CHANGE_NT * 4)    // (rows end behind whole words)
                 cp_async16(reinterpret_cast<float*>(staged + i - first), reinterpret_cast<const float*>(tok + i), 16);
         } else {
-            for (int i = first + tid; i < min(first + STAGED, last); i += CHANGE_NT)
-                cp_async4(reinterpret_cast<float*>(staged + i - first), reinterpret_cast<const float*>(tok + i), 4);
+            for (int i = first + tid; i < min(first + STAGED, last); i += CHANGE_NT) staged[i - first] = __ldcg(tok + i);
         }
         cp_async_commit();
     };
     if (hist) stage(0, a.history);
-    const int len = !hist ? 0 : a.lens ? min(max(a.lens[row], 0), a.history) : a.history;
-    const int prompt = a.prompt_lens ? a.prompt_lens[row] : 0;
+    const int len = !hist ? 0 : a.lens ? min(max(__ldcg(a.lens + row), 0), a.history) : a.history;
+    const int prompt = a.prompt_lens ? __ldcg(a.prompt_lens + row) : 0;
     int b0 = 0, b1 = 0;
-    if (a.bias_starts) b0 = min(max(a.bias_starts[row], 0), a.biases), b1 = max(min(a.bias_starts[row + 1], a.biases), b0);
+    if (a.bias_starts)
+        b0 = min(max(__ldcg(a.bias_starts + row), 0), a.biases), b1 = max(min(__ldcg(a.bias_starts + row + 1), a.biases), b0);
     const Mask mask(a, row);
     float rep = 1.f, pres = 0.f, freq = 0.f;
-    if (a.repetition) rep = a.repetition[row];
-    if (a.presence) pres = a.presence[row];
-    if (a.frequency) freq = a.frequency[row];
+    if (a.repetition) rep = __ldcg(a.repetition + row);
+    if (a.presence) pres = __ldcg(a.presence + row);
+    if (a.frequency) freq = __ldcg(a.frequency + row);
     // f(token, number in the history) for every token; the first STAGED are in shared memory.
     auto history = [&](bool again, auto f) {
         for (int first = 0; first < len; first += STAGED) {
@@ -262,7 +266,7 @@ __global__ void __launch_bounds__(CHANGE_NT, 2) change_kernel(const AdjustArgs a
             });
         });
         for (int i = b0 + tid; i < b1; i += CHANGE_NT)
-            find(a.bias_tokens[i], i, [&](uint32_t at, int i) { atomicMax(&which[at], uint32_t(i - b0 + 1)); });
+            find(__ldcg(a.bias_tokens + i), i, [&](uint32_t at, int i) { atomicMax(&which[at], uint32_t(i - b0 + 1)); });
         __syncthreads();
         if (!full) {
             // Each slot's logit is computed, and once the copy is done written, by one thread; the loads of all of a thread's
@@ -276,9 +280,9 @@ __global__ void __launch_bounds__(CHANGE_NT, 2) change_kernel(const AdjustArgs a
                 t[j] = EMPTY, b[j] = 0, add[j] = 0.f;
                 if (i < 1 << bits) t[j] = key[i];
                 if (t[j] != EMPTY) {
-                    z[j] = Num<T>::get(x[t[j]]);
-                    if (!mask.bits<1>(int(t[j]))) b[j] = EMPTY;     // (the copy's -infinity stays)
-                    else if (which[i]) b[j] = which[i], add[j] = a.bias_values[b0 + int(which[i]) - 1];
+                    z[j] = Num<T>::get(__ldcg(x + t[j]));
+                    if (!mask.bits<1, true>(int(t[j]))) b[j] = EMPTY;     // (the copy's -infinity stays)
+                    else if (which[i]) b[j] = which[i], add[j] = __ldcg(a.bias_values + b0 + int(which[i]) - 1);
                 }
             }
 #pragma unroll
@@ -353,11 +357,12 @@ static fs_status adjust_type(AdjustArgs& a, void* stream) {
     // (a row's first word may start up to 15 bytes before it)
     a.segs = int((a.V + 16 / int(sizeof(T)) - 1 + COPY_SEG<T> - 1) / COPY_SEG<T>);
     const bool in_place = a.x == a.out && (a.xs == a.os || a.B == 1), change = a.tokens || a.bias_starts;
-    // A row's CTAs: one for about 512 tokens of the history while all of them fit the GPU at once (three on an SM), and more
-    // than that only where the table would be too small.  (64 rows of 4096: 512 CTAs 14.3 us, 256 @@.)
+    // A row's CTAs: one for about 512 tokens of the history while all of them fit the GPU at once (two on an SM), and more
+    // than that only where the table would be too small.  (64 rows of 151936 and histories of 4096: 256 CTAs 28.7 us, 512 32.8, with
+    // the caches flushed.)
     a.split = 0;
     while (a.split < 6 && (512 << a.split) < a.history &&
-           ((int64_t(a.B) << (a.split + 1)) <= 3 * sms || 2 * ((a.history >> a.split) + 64) > SLOTS))
+           ((int64_t(a.B) << (a.split + 1)) <= 2 * sms || 2 * ((a.history >> a.split) + 64) > SLOTS))
         ++a.split;
     if (int64_t(a.B) * std::max(a.segs, 1 << a.split) > 0x7fffffffLL) return FS_ERR_UNSUPPORTED;
     const auto changes = [&](auto kernel) { return launch_adjust(kernel, unsigned(a.B << a.split), CHANGE_NT, (3 * SLOTS + 4 + STAGED) * 4, a, stream); };

@@ -52,11 +52,13 @@ struct Request {
     // Position of the token of a query row; below 0 it sees nothing.
     __device__ __forceinline__ int pos(const ChunkArgs& a, int row) const { return len - nq + row / a.gs; }
 };
+// (Read from L2, like the page tables: the kernel of few rows does not wait itself for what wrote them, and an SM's L1 may hold
+// what they were before.)
 __device__ __forceinline__ Request request(const ChunkArgs& a, int r) {
     Request x;
-    x.q0 = min(max(a.starts[r], 0), a.N);
-    x.nq = max(min(max(a.starts[r + 1], 0), a.N) - x.q0, 0);
-    x.len = int(min(int64_t(max(a.lens[r], 0)), int64_t(a.width) * a.page_size));
+    x.q0 = min(max(__ldcg(a.starts + r), 0), a.N);
+    x.nq = max(min(max(__ldcg(a.starts + r + 1), 0), a.N) - x.q0, 0);
+    x.len = int(min(int64_t(max(__ldcg(a.lens + r), 0)), int64_t(a.width) * a.page_size));
     return x;
 }
 
@@ -259,7 +261,8 @@ __device__ __forceinline__ bool few_starts(const ChunkArgs& a) {
 template <typename T, int D>
 __device__ __forceinline__ void zero_rest(const ChunkArgs& a, int cta, int threads) {
     constexpr int DC = D / 8;
-    const int lo = a.R > 0 ? min(max(a.starts[0], 0), a.N) : a.N, hi = a.R > 0 ? max(min(max(a.starts[a.R], 0), a.N), lo) : a.N;
+    const int lo = a.R > 0 ? min(max(__ldcg(a.starts), 0), a.N) : a.N,
+              hi = a.R > 0 ? max(min(max(__ldcg(a.starts + a.R), 0), a.N), lo) : a.N;
     const int rest = lo + a.N - hi;
     for (int64_t i = int64_t(cta) * threads + threadIdx.x; i < int64_t(rest) * a.Hq * DC; i += int64_t(a.grid) * threads) {
         const int c = int(i % DC), h = int(i / DC % a.Hq), j = int(i / DC / a.Hq), t = j < lo ? j : hi + j - lo;
@@ -295,11 +298,11 @@ template <typename T>
 __device__ __noinline__ void add_odd(const ChunkArgs& a, const int* table, int p, int k0, int n, int head, int d, float4& y) {
     for (int k = k0; k < k0 + n && k <= p; ++k) {
         if (!sees(a, p, k)) continue;
-        const int pi = k / a.page_size, page = table[pi];
+        const int pi = k / a.page_size, page = __ldcg(table + pi);
         if (page < 0 || page >= a.num_pages) continue;
         const T* v = static_cast<const T*>(a.v) + page * a.vc[0] + (k - pi * a.page_size) * a.vc[1] + head * a.vc[2] + d;
         auto odd = [&](int e) {
-            const float z = Mma<T>::get(v[e]);
+            const float z = Mma<T>::get(__ldcg(v + e));
             return fabsf(z) <= 3.402823466e38f ? 0.f : z;
         };
         y = make_float4(y.x + odd(0), y.y + odd(1), y.z + odd(2), y.w + odd(3));
@@ -312,7 +315,7 @@ static __device__ __noinline__ unsigned missing_pages(const ChunkArgs& a, int r,
     for (int e = 0; e < 32; ++e) {
         const int pi = (k0 + e) / a.page_size;
         if (pi >= a.width) break;
-        const int page = a.table[int64_t(r) * a.width + pi];
+        const int page = __ldcg(a.table + int64_t(r) * a.width + pi);
         if (page < 0 || page >= a.num_pages) bits |= 1u << e;
     }
     return bits;

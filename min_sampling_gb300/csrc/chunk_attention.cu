@@ -12,9 +12,12 @@
 // their maxima and sums in a fixed order (join_chunk_kernel; no atomics):
 //   m = max_i m_i,  l = sum_i 2^(m_i - m) l_i,  out = sum_i 2^(m_i - m) l_i out_i / l.
 //
-// chunk_few.cu: requests of up to 16 rows, single tokens above all.  chunk_tensor.cu: more rows, on the
-// 5th-generation tensor cores.  chunk_rows_kernel (mma.sync): many rows of heads of 256, and a few where the caches'
-// strides have no map for the copy engine.
+// Three launches: chunk_tensor.cu, requests of more than 16 rows, on the 5th-generation tensor cores; chunk_few.cu, requests of
+// up to 16 rows, single tokens above all; the parts joined.  The first two have lines of their own and do not wait for each other:
+// the SMs that are done with the first take the second's CTAs.  (The other way round, and one CTA planning
+// for all, 460 us for two chunks of 1021 tokens behind 16384 and 47 single tokens; 455 this way. On SMs
+// of their own beside the first they slowed its CTAs on the neighbouring SMs by a sixth: 490 us.)
+// chunk_rows_kernel (mma.sync) has many rows of heads of 256, and a few where the caches' strides have no map for the copy engine.
 #include "chunk.cuh"
 
 #include <numeric>
@@ -111,7 +114,7 @@ __global__ void __launch_bounds__(32 * WM * WN) chunk_rows_kernel(const __grid_c
             const int key = kt.at(i0 + tile) + tid;
             if (kt.seen(key)) {
                 const int pi = a.page_shift >= 0 ? key >> a.page_shift : key / a.page_size;
-                const int page = table[pi];
+                const int page = __ldcg(table + pi);
                 if (page >= 0 && page < a.num_pages) {
                     const int s = key - pi * a.page_size;
                     ko = page * a.kc[0] + s * a.kc[1] + head * a.kc[2];
@@ -762,7 +765,7 @@ fs_status fs_paged_chunk_attention(const fs_paged_kv* cache, const void* query, 
     a.part_l = reinterpret_cast<float2*>(ws + p.part_l);
     a.split = reinterpret_cast<int4*>(ws + p.split);
     a.t_grid = p.t_grid;
-    a.t_start = cache->head_dim == 64 ? 2 : 3;
+    a.t_start = cache->head_dim == 64 ? 2 : 3;   // (4500 and 8200 cycles, of 2600 and 2860 a unit)
     a.out_32 = (reinterpret_cast<uintptr_t>(out) % 32 == 0 && a.os[0] % 16 == 0 && a.os[1] % 16 == 0);
     if (p.t_grid > 0) {
         a.t_part_o = reinterpret_cast<float*>(ws + p.t_part_o);

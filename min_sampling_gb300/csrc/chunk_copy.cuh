@@ -56,7 +56,7 @@ struct Pages {
         for (int j = 0; j < 4; ++j) {
             if (j > 0 && a.page_shift >= 2) break;   // four keys of one page
             const int pi = a.page_shift >= 0 ? (key + j) >> a.page_shift : (key + j) / a.page_size;
-            at[j] = pi < a.width ? table[pi] : -1;
+            at[j] = pi < a.width ? __ldcg(table + pi) : -1;
         }
     }
     // -1 for a key that no query of the tile sees, and for one whose page does not exist.  Whether there is one of the latter:

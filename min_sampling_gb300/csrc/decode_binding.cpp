@@ -596,6 +596,10 @@ PyObject* chunk_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
             apart(to, "out", Span(*tensor(a[2])), "v_cache");
             if (!same_view(in_query, to)) apart(to, "out", in_query, "query");
         }
+        for (int i = 3; i < 6 && !none(a[10]); ++i) {
+            static const char* const others[] = {"page_table", "query_starts", "lens"};
+            if (const at::Tensor* t = tensor(a[i])) apart_bytes(Span(out), "out", Span(*t), others[i - 3]);
+        }
         no_gradient({&q, &cache, tensor(a[2]), tensor(a[10])});
         const int32_t N = size32(q.size(0), "the number of tokens"), Hq = size32(q.size(1), "the number of heads");
         if (Hq < 1 || Hq % kv.num_heads != 0) refuse("query must have a multiple of the caches' heads");

@@ -248,3 +248,30 @@ def test_captured_and_on_two_streams(ms):
     assert torch.equal(outs[1], want[1])
     c0 = dict(cs[0], lens=np.zeros(20, np.int32))
     _near(outs[0], c0, _expect(c0))
+
+
+@pytest.mark.parametrize("history", [902, 901])
+def test_steps_behind_one_another(ms, history):
+    """Logits, histories and lengths that change between calls which nobody waits for."""
+    import torch
+    c = _case(30, "f32", 20, 9001, history=history, bias=20, masks=7)
+
+    def steps(wait):
+        (x, tokens, lens, prompts), kw = _args(c)
+        x, outs = x.clone(), []
+        for i in range(12):
+            outs.append(ms.adjust_logits(x, tokens, lens, prompts, **kw))
+            if wait:
+                torch.cuda.synchronize()
+            x.neg_()
+            tokens.copy_(tokens.roll(1, 0))
+            lens.sub_(1).clamp_(min=0)
+            kw["allowed_rows"].copy_(kw["allowed_rows"].roll(1))
+            kw["bias_values"].neg_()
+            kw["frequency"].mul_(1.5)
+            if wait:
+                torch.cuda.synchronize()
+        torch.cuda.synchronize()
+        return outs
+    for a, b in zip(steps(False), steps(True)):
+        assert torch.equal(a, b)

@@ -402,3 +402,39 @@ def test_the_same_bits_every_time_captured_and_on_two_streams(ms):
     torch.cuda.synchronize()
     w0 = call(ms, short)
     assert torch.equal(outs[0][0], w0[0]) and torch.equal(outs[1][0], want[1][0]) and torch.equal(outs[1][1], want[1][1])
+
+
+def test_more_tiles_than_threads(ms):
+    """Requests, and tiles of the tensor cores, of which a thread of the search for a CTA's run has several; none at a run's start."""
+    new = np.tile([20, 1, 0, 3, 33], 260)
+    check(ms, case(30, "bf16", new, new + np.tile([0, 90, 7], 434)[:1300], 2, 2, 64, 16))
+    new = np.concatenate([np.ones(600, int), [700], np.ones(600, int), [17, 300]])
+    check(ms, case(31, "bf16", new, new + 40, 2, 1, 64, 16))
+    check(ms, case(32, "f16", [3000, 2, 1500], [3000, 3000, 1600], 24, 1, 128, 16), window=100, sinks=3)
+
+
+def test_steps_behind_one_another(ms):
+    """Lengths, starts, tables, queries and caches that change between calls which nobody waits for."""
+    import torch
+    for D, H in ((64, 4), (128, 1)):
+        c = case(33, "bf16", [1, 300, 2, 40, 1], [2600, 600, 50, 700, 900], 4, H, D, 16)
+        cu = lambda x: torch.from_numpy(np.ascontiguousarray(x)).cuda()
+
+        def steps(wait):
+            q, k, v, table, starts, lens = c["q"].clone(), c["k"].clone(), c["v"].clone(), cu(c["table"]), cu(c["starts"]), cu(c["lens"])
+            outs = []
+            for i in range(12):
+                outs.append(ms.paged_chunk_attention(q, k, v, table, starts, lens, return_lse=True))
+                if wait:
+                    torch.cuda.synchronize()
+                lens.sub_(1)
+                starts[1:5].add_(1 if i % 2 else -1)
+                table[:, :3].copy_(table[:, :3].roll(1, 1))
+                q.mul_(-1)
+                k[i].neg_(), v[i].neg_()
+                if wait:
+                    torch.cuda.synchronize()
+            torch.cuda.synchronize()
+            return outs
+        for (o, l), (o2, l2) in zip(steps(False), steps(True)):
+            assert torch.equal(o, o2) and torch.equal(l, l2)

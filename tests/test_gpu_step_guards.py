@@ -140,3 +140,16 @@ def test_outputs_that_share_memory_are_refused(ms):
         with pytest.raises(ValueError, match="share"):
             ms.paged_step_tables(**{**t, **b})
     ms.paged_step_tables(**{**t, **dict(lens=room[4:6], page_table=room[:4].view(2, 2))})
+
+
+@pytest.mark.parametrize("name", ["page_table", "query_starts", "lens"])
+def test_an_output_over_the_places_is_refused(ms, name):
+    import torch
+    c = _chunk()
+    room = torch.zeros(1280, dtype=torch.bfloat16, device="cuda")
+    x = c[name]
+    over = room.view(torch.int32)[:x.numel()].view(x.shape)
+    over.copy_(x)
+    with pytest.raises(ValueError, match="share"):
+        ms.paged_chunk_attention(**{**c, name: over}, out=room.view(5, 4, 64))
+    assert torch.equal(over, x)

@@ -272,23 +272,27 @@ __global__ void __launch_bounds__(CHANGE_NT, 2) change_kernel(const AdjustArgs a
             // Each slot's logit is computed, and once the copy is done written, by one thread; the loads of all of a thread's
             // slots are in flight together.
             constexpr int PER = SLOTS / CHANGE_NT;
-            uint32_t t[PER], b[PER];
+            uint32_t t[PER], biased = 0;
             float z[PER], add[PER];
 #pragma unroll
             for (int j = 0; j < PER; ++j) {
                 const int i = tid + j * CHANGE_NT;
-                t[j] = EMPTY, b[j] = 0, add[j] = 0.f;
-                if (i < 1 << bits) t[j] = key[i];
-                if (t[j] != EMPTY) {
-                    z[j] = Num<T>::get(__ldcg(x + t[j]));
-                    if (!mask.bits<1, true>(int(t[j]))) b[j] = EMPTY;     // (the copy's -infinity stays)
-                    else if (which[i]) b[j] = which[i], add[j] = __ldcg(a.bias_values + b0 + int(which[i]) - 1);
-                }
+                t[j] = i < 1 << bits ? key[i] : EMPTY;
+            }
+#pragma unroll
+            for (int j = 0; j < PER; ++j)
+                if (t[j] != EMPTY) z[j] = Num<T>::get(__ldcg(x + t[j]));
+#pragma unroll
+            for (int j = 0; j < PER; ++j) {
+                if (t[j] == EMPTY) continue;
+                const uint32_t b = which[tid + j * CHANGE_NT];
+                if (b) biased |= 1u << j, add[j] = __ldcg(a.bias_values + b0 + int(b) - 1);
             }
 #pragma unroll
             for (int j = 0; j < PER; ++j) {
-                if (b[j] == EMPTY) t[j] = EMPTY;
-                if (t[j] != EMPTY) z[j] = value(z[j], word[tid + j * CHANGE_NT], b[j] != 0, add[j]);
+                if (t[j] == EMPTY) continue;
+                if (mask.bits<1, true>(int(t[j]))) z[j] = value(z[j], word[tid + j * CHANGE_NT], biased >> j & 1, add[j]);
+                else t[j] = EMPTY;      // (the copy's -infinity stays)
             }
             if (a.copied) grid_dependency_wait();
 #pragma unroll

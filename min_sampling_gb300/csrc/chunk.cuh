@@ -52,13 +52,16 @@ struct Request {
     // Position of the token of a query row; below 0 it sees nothing.
     __device__ __forceinline__ int pos(const ChunkArgs& a, int row) const { return len - nq + row / a.gs; }
 };
-// (Read from L2, like the page tables: the kernel of few rows does not wait itself for what wrote them, and an SM's L1 may hold
-// what they were before.)
+// Lengths and tables, by a kernel that has waited for what comes before it or not (few rows behind the tensor cores): then from
+// L2, since an SM's L1 may hold what was there before.  (For all from L2, the window case took 113 us instead of 106.)
+template <bool WAITED>
+__device__ __forceinline__ int get(const ChunkArgs& a, const int* p) { return WAITED || a.t_grid == 0 ? *p : __ldcg(p); }
+template <bool WAITED>
 __device__ __forceinline__ Request request(const ChunkArgs& a, int r) {
     Request x;
-    x.q0 = min(max(__ldcg(a.starts + r), 0), a.N);
-    x.nq = max(min(max(__ldcg(a.starts + r + 1), 0), a.N) - x.q0, 0);
-    x.len = int(min(int64_t(max(__ldcg(a.lens + r), 0)), int64_t(a.width) * a.page_size));
+    x.q0 = min(max(get<WAITED>(a, a.starts + r), 0), a.N);
+    x.nq = max(min(max(get<WAITED>(a, a.starts + r + 1), 0), a.N) - x.q0, 0);
+    x.len = int(min(int64_t(max(get<WAITED>(a, a.lens + r), 0)), int64_t(a.width) * a.page_size));
     return x;
 }
 
@@ -170,7 +173,7 @@ __device__ __forceinline__ bool many_run(const ChunkArgs& a, int cta, int64_t* w
     };
     auto units = [&](const Request& x, int row0) { return ManyTile(a, x, row0).units; };
     int64_t tiles, total, mine = 0;
-    for (int r = r0; r < r1; ++r) mine += tiles_of(request(a, r));
+    for (int r = r0; r < r1; ++r) mine += tiles_of(request<true>(a, r));
     tiles_before[tid] = block_sum_before<NT>(mine, words, tiles);
     __syncthreads();
     // tiles [i0, i1) are this thread's; the first is one of the last thread's that has no more than i0 before it
@@ -185,7 +188,7 @@ __device__ __forceinline__ bool many_run(const ChunkArgs& a, int cta, int64_t* w
     int r = lo * per;
     Request x = {};
     for (; i0 < i1 && r < a.R; at += tiles_of(x), ++r) {
-        x = request(a, r);
+        x = request<true>(a, r);
         if (at + tiles_of(x) > i0) break;
     }
     // f(request, its number, first row) for each of them
@@ -193,7 +196,7 @@ __device__ __forceinline__ bool many_run(const ChunkArgs& a, int cta, int64_t* w
         Request y = x;
         int k = r, row0 = int(i0 - at) * MANY;
         for (int64_t i = i0; i < i1; ++i) {
-            while ((row0 >= y.rows(a) || y.rows(a) <= a.rows_upto) && k + 1 < a.R) y = request(a, ++k), row0 = 0;
+            while ((row0 >= y.rows(a) || y.rows(a) <= a.rows_upto) && k + 1 < a.R) y = request<true>(a, ++k), row0 = 0;
             if (!f(y, k, row0)) return;
             row0 += MANY;
         }
@@ -224,7 +227,7 @@ template <int NT, int MT, int KT>
 __device__ __forceinline__ Run run_of(const ChunkArgs& a, int cta, int64_t* words) {
     const int tid = threadIdx.x, per = (a.R + NT - 1) / NT, r0 = min(tid * per, a.R), r1 = min(r0 + per, a.R);
     int64_t mine = 0;
-    for (int r = r0; r < r1; ++r) mine += units_of<MT, KT>(a, request(a, r));
+    for (int r = r0; r < r1; ++r) mine += units_of<MT, KT>(a, request<false>(a, r));
     int64_t total, before = block_sum_before<NT>(mine, words, total);
     total *= a.Hkv;
     Run run;
@@ -233,7 +236,7 @@ __device__ __forceinline__ Run run_of(const ChunkArgs& a, int cta, int64_t* word
     run.last = min(run.first + run.length, total);
     if (run.first < run.last && before * a.Hkv <= run.first && run.first < (before + mine) * a.Hkv) {
         for (int r = r0; r < r1; ++r) {
-            const int64_t n = units_of<MT, KT>(a, request(a, r));
+            const int64_t n = units_of<MT, KT>(a, request<false>(a, r));
             if (run.first < (before + n) * a.Hkv) {
                 words[16] = r, words[17] = before * a.Hkv, words[18] = n;
                 break;
@@ -294,15 +297,15 @@ __device__ __forceinline__ uint4 even_words(uint4 w) {
 }
 // The infinite and NaN values, elements d .. d + 3 of a head, of the keys k0 .. k0 + n - 1 that the
 // token at position p sees, added to y.
-template <typename T>
+template <typename T, bool WAITED>
 __device__ __noinline__ void add_odd(const ChunkArgs& a, const int* table, int p, int k0, int n, int head, int d, float4& y) {
     for (int k = k0; k < k0 + n && k <= p; ++k) {
         if (!sees(a, p, k)) continue;
-        const int pi = k / a.page_size, page = __ldcg(table + pi);
+        const int pi = k / a.page_size, page = get<WAITED>(a, table + pi);
         if (page < 0 || page >= a.num_pages) continue;
         const T* v = static_cast<const T*>(a.v) + page * a.vc[0] + (k - pi * a.page_size) * a.vc[1] + head * a.vc[2] + d;
         auto odd = [&](int e) {
-            const float z = Mma<T>::get(__ldcg(v + e));
+            const float z = Mma<T>::get(WAITED ? v[e] : __ldcg(v + e));
             return fabsf(z) <= 3.402823466e38f ? 0.f : z;
         };
         y = make_float4(y.x + odd(0), y.y + odd(1), y.z + odd(2), y.w + odd(3));
@@ -310,12 +313,13 @@ __device__ __noinline__ void add_odd(const ChunkArgs& a, const int* table, int p
 }
 
 // Which of the keys k0 .. k0 + 31 of request r have no page (within what its table can name).
-static __device__ __noinline__ unsigned missing_pages(const ChunkArgs& a, int r, int k0) {
+template <bool WAITED>
+__device__ __noinline__ unsigned missing_pages(const ChunkArgs& a, int r, int k0) {
     unsigned bits = 0;
     for (int e = 0; e < 32; ++e) {
         const int pi = (k0 + e) / a.page_size;
         if (pi >= a.width) break;
-        const int page = __ldcg(a.table + int64_t(r) * a.width + pi);
+        const int page = get<WAITED>(a, a.table + int64_t(r) * a.width + pi);
         if (page < 0 || page >= a.num_pages) bits |= 1u << e;
     }
     return bits;

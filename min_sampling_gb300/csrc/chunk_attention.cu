@@ -71,10 +71,10 @@ __global__ void __launch_bounds__(32 * WM * WN) chunk_rows_kernel(const __grid_c
 #pragma unroll 1
     while (unit < last) {
         // ---- the tile that the unit lies in
-        Request x = request(a, pl.r);
+        Request x = request<false>(a, pl.r);
         while (unit >= pl.before + pl.units * a.Hkv) {
             pl.before += pl.units * a.Hkv;
-            x = request(a, ++pl.r);
+            x = request<false>(a, ++pl.r);
             pl.units = units_of<MT, KT>(a, x);
         }
         const int head = int((unit - pl.before) / pl.units);
@@ -114,7 +114,7 @@ __global__ void __launch_bounds__(32 * WM * WN) chunk_rows_kernel(const __grid_c
             const int key = kt.at(i0 + tile) + tid;
             if (kt.seen(key)) {
                 const int pi = a.page_shift >= 0 ? key >> a.page_shift : key / a.page_size;
-                const int page = __ldcg(table + pi);
+                const int page = get<false>(a, table + pi);
                 if (page >= 0 && page < a.num_pages) {
                     const int s = key - pi * a.page_size;
                     ko = page * a.kc[0] + s * a.kc[1] + head * a.kc[2];
@@ -357,7 +357,7 @@ __global__ void __launch_bounds__(32 * WM * WN) chunk_rows_kernel(const __grid_c
                 const int p = x.pos(a, row);
                 for (int t = 0; t < tiles; ++t) {
                     const int k0 = kt.at(i0 + t);
-                    if (partial(k0)) add_odd<T>(a, table, p, k0, KT, head, c * 4, y);
+                    if (partial(k0)) add_odd<T, false>(a, table, p, k0, KT, head, c * 4, y);
                 }
             }
             const int j = row / a.gs, h = head * a.gs + row % a.gs;
@@ -475,7 +475,7 @@ __global__ void __launch_bounds__(512, JOIN_CTAS) join_chunk_kernel(const __grid
             few_tiles += count[0][w], n_tiles += count[1][w];
         }
         if (s.w > 0) {
-            const Request x = request(a, s.x);
+            const Request x = request<true>(a, s.x);
             tiles[here] = JoinTile{x.q0, x.rows(a), s.y, s.z, s.w, c};
         }
     }

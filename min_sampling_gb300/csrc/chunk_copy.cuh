@@ -51,12 +51,13 @@ __device__ __forceinline__ void bar_expect(uint32_t bar, uint32_t bytes) {
 struct Pages {
     int at[4];
     // As the table has them; the loads are not waited for here.
+    template <bool WAITED>
     __device__ __forceinline__ void look_up(const ChunkArgs& a, const int* table, int key) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             if (j > 0 && a.page_shift >= 2) break;   // four keys of one page
             const int pi = a.page_shift >= 0 ? (key + j) >> a.page_shift : (key + j) / a.page_size;
-            at[j] = pi < a.width ? __ldcg(table + pi) : -1;
+            at[j] = pi < a.width ? get<WAITED>(a, table + pi) : -1;
         }
     }
     // -1 for a key that no query of the tile sees, and for one whose page does not exist.  Whether there is one of the latter:

@@ -75,7 +75,7 @@ __global__ void __launch_bounds__(FNT) chunk_few_kernel(const __grid_constant__ 
         // ================================================ what the next tiles are, and their copies
         Place pl = run.place;
         Request x = {};
-        if (run.first < run.last) x = request(a, pl.r);     // (there may be no requests at all)
+        if (run.first < run.last) x = request<false>(a, pl.r);     // (there may be no requests at all)
         int64_t unit = run.first;
         uint32_t c = 0;         // key tiles before
         bool ok = true;
@@ -88,7 +88,7 @@ __global__ void __launch_bounds__(FNT) chunk_few_kernel(const __grid_constant__ 
             if (unit < run.last) {
                 while (unit >= pl.before + pl.units * a.Hkv) {
                     pl.before += pl.units * a.Hkv;
-                    x = request(a, ++pl.r);
+                    x = request<false>(a, ++pl.r);
                     pl.units = units_of<FEW, FK>(a, x);
                 }
                 sg.r = pl.r, sg.x = x;
@@ -129,13 +129,13 @@ __global__ void __launch_bounds__(FNT) chunk_few_kernel(const __grid_constant__ 
             const int* table = a.table + int64_t(sg.r) * a.width;
             Pages pages;
             const int row = (lane & 15) * 4;
-            pages.look_up(a, table, sg.kt.at(sg.i0) + row);
+            pages.look_up<false>(a, table, sg.kt.at(sg.i0) + row);
 #pragma unroll 1
             for (int i = 0; i < sg.n; ++i, ++c) {
                 const uint32_t lap = c / ST, st = c - lap * ST;
                 const int k0 = sg.kt.at(sg.i0 + i);
                 Pages now = pages;
-                if (i + 1 < sg.n) pages.look_up(a, table, sg.kt.at(sg.i0 + i + 1) + row);
+                if (i + 1 < sg.n) pages.look_up<false>(a, table, sg.kt.at(sg.i0 + i + 1) + row);
                 if (lap > 0) ok = __all_sync(FULL, bar_wait(empty + 8 * st, (lap - 1) & 1, dead));
                 if (!ok) break;
                 const int any = __any_sync(FULL, now.resolve(a, sg.kt, k0 + row));
@@ -226,7 +226,7 @@ __global__ void __launch_bounds__(FNT) chunk_few_kernel(const __grid_constant__ 
                 // ---- running maximum, weights and sum
                 const int kbase = k0 + kr + (lane & 3) * 2;
                 const bool edge = sg.p_hi - k0 >= a.window;   // (uniform) below some token's window
-                const unsigned bits = missing[st] ? missing_pages(a, sg.r, k0 + kr) : 0u;
+                const unsigned bits = missing[st] ? missing_pages<false>(a, sg.r, k0 + kr) : 0u;
                 uint32_t pf[4];
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
@@ -348,7 +348,7 @@ __global__ void __launch_bounds__(FNT) chunk_few_kernel(const __grid_constant__ 
                         const int p = sg.x.pos(a, row);
                         for (int t = 0; t < n; ++t) {
                             const int k0 = sg.kt.at(sg.i0 + t);
-                            if (partial_keys(a, sg.p_lo, sg.p_hi, k0, FK)) add_odd<T>(a, table, p, k0, FK, sg.head, d, y);
+                            if (partial_keys(a, sg.p_lo, sg.p_hi, k0, FK)) add_odd<T, false>(a, table, p, k0, FK, sg.head, d, y);
                         }
                     }
                     const int j = row / a.gs, h = sg.head * a.gs + row - j * a.gs;

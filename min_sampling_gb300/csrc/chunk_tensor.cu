@@ -181,7 +181,7 @@ __global__ void __launch_bounds__(CNT, 1) chunk_tensor_kernel(const __grid_const
             const int* table = a.table + int64_t(sg.r) * a.width;
             Pages pages;
             auto look_up = [&](int i) {
-                if (i < n) pages.look_up(a, table, kt.at(i0 + i) + row);
+                if (i < n) pages.look_up<true>(a, table, kt.at(i0 + i) + row);
             };
             look_up(0);
 #pragma unroll 1
@@ -374,7 +374,7 @@ __global__ void __launch_bounds__(CNT, 1) chunk_tensor_kernel(const __grid_const
             sg.n = 0;
             if (u < last) {
                 sg.r = r, sg.row0 = row0;
-                sg.x = request(a, r);
+                sg.x = request<true>(a, r);
                 sg.M = sg.x.rows(a);
                 const ManyTile tile(a, sg.x, row0);
                 const int each = tile.units;
@@ -393,7 +393,7 @@ __global__ void __launch_bounds__(CNT, 1) chunk_tensor_kernel(const __grid_const
                         row0 = 0;
                         for (unsigned hit = 0; hit == 0;) {
                             const int k = r + 1 + lane;
-                            hit = __ballot_sync(FULL, k < a.R && request(a, min(k, a.R - 1)).rows(a) > a.rows_upto);
+                            hit = __ballot_sync(FULL, k < a.R && request<true>(a, min(k, a.R - 1)).rows(a) > a.rows_upto);
                             r += hit ? __ffs(int(hit)) : 32;
                             if (!hit && r >= a.R - 1) {     // (none is left: not with the lengths that the run was cut by)
                                 u = last;
@@ -510,7 +510,7 @@ __global__ void __launch_bounds__(CNT, 1) chunk_tensor_kernel(const __grid_const
                             // the keys of these 32 that the row sees: below `lim`, and from `low` on or below `first`
                             auto below = [](int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1; };
                             const uint32_t see = below(lim - c) & (~below(low - c) | below(first - c));
-                            const uint32_t lost = gone ? missing_pages(a, sg.r, k0 + c) : 0u;
+                            const uint32_t lost = gone ? missing_pages<true>(a, sg.r, k0 + c) : 0u;
                             tmem_wait_ld();
                             keep32(x);
 #pragma unroll
@@ -638,7 +638,7 @@ __global__ void __launch_bounds__(CNT, 1) chunk_tensor_kernel(const __grid_const
                             for (int e = 0; e < 32; e += 4) {
                                 float4 z = make_float4(__uint_as_float(y[e]), __uint_as_float(y[e + 1]), __uint_as_float(y[e + 2]),
                                                        __uint_as_float(y[e + 3]));
-                                add_odd<T>(a, a.table + int64_t(sg.r) * a.width, pos, k0, CK, sg.head, c + e, z);
+                                add_odd<T, true>(a, a.table + int64_t(sg.r) * a.width, pos, k0, CK, sg.head, c + e, z);
                                 y[e] = __float_as_uint(z.x), y[e + 1] = __float_as_uint(z.y);
                                 y[e + 2] = __float_as_uint(z.z), y[e + 3] = __float_as_uint(z.w);
                             }

@@ -765,7 +765,7 @@ fs_status fs_paged_chunk_attention(const fs_paged_kv* cache, const void* query, 
     a.part_l = reinterpret_cast<float2*>(ws + p.part_l);
     a.split = reinterpret_cast<int4*>(ws + p.split);
     a.t_grid = p.t_grid;
-    a.t_start = cache->head_dim == 64 ? 2 : 3;   // (4500 and 8200 cycles, of 2600 and 2860 a unit)
+    a.t_start = cache->head_dim == 64 ? 2 : 3;   // (about 5000 and 8200 cycles, of 2150 and 2860 a unit)
     a.out_32 = (reinterpret_cast<uintptr_t>(out) % 32 == 0 && a.os[0] % 16 == 0 && a.os[1] % 16 == 0);
     if (p.t_grid > 0) {
         a.t_part_o = reinterpret_cast<float*>(ws + p.t_part_o);

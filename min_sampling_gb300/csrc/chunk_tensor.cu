@@ -4,13 +4,14 @@
 // A tile of up to 256 query rows (two tiles of 128) runs over its keys, 128 at a time:
 //   S = Q K^T,  P = 2^(S - m),  O += P V.
 // S, P and O live in tensor memory (S 128 x 128 float32 and O 128 x D for each of the two tiles, all
-// of the 512 columns); S is turned into P (16 bits) in place, and P feeds the second product from there.
+// of the 512 columns; heads of 64 leave room for a third S, so that scores are there when a softmax asks for them: 2150 cycles
+// for 256 rows and 128 keys, 2600 without); S is turned into P (16 bits) in place, and P feeds the second product from there.
 // Roles of the 16 warps:
 //   warps 0-3, 4-7  softmax of tile 0 / tile 1, one thread per row: maximum, weights, sum; O is rescaled
 //                   only when a maximum grows by more than 2^GROWTH; at the end the row's output
 //   warps 8, 9      keys, half a tile each; warps 10, 11 values: page look-ups and copies into a ring of swizzled tiles
-//   warp 12         issues the products, PV of one tile and then its next S: in order, so that the weights have been read
-//                   when the scores behind them are written
+//   warp 12         issues the products, PV and then the next S that goes into the same columns: in order, so that
+//                   the weights have been read when the scores behind them are written
 //   warp 13         looks values through that not every query sees, see below
 //   warp 14         what the next tiles are, into a ring that all roles read
 //   warp 15         queries of the next tile, as soon as the last product that reads the old ones is done
@@ -29,8 +30,8 @@
 // Measured, bf16, 32 heads over 8 of 128: a prompt of 8190 tokens 420 us, 1.3 PFLOP/s, two thirds of the rate of the largest
 // library product. For 256 rows and 128 keys the products take 2048 cycles, a tile's scores 1570 (load 330, maximum
 // 260, weights 980) and then its products and the hand-overs, together 2860: that chain bounds it, and where 16-token
-// pages are read by all SMs at once 400 cycles of waiting for keys and values.  Heads of 64: 2600 cycles, the same chain around products of
-// 1024.  A tile's end (64 KB written by 256 threads, 32 bytes a store and clock) takes as long as t_start units.
+// pages are read by all SMs at once 400 cycles of waiting for keys and values.  Heads of 64: 2150 cycles, the weights', of two
+// tiles at a time.  A tile's end (64 KB written by 256 threads, 32 bytes a store and clock) takes as long as t_start units.
 //
 // One CTA per SM takes an equal run of units (key tiles) of the launch's line of work, see many_run; all
 // roles walk the run's tiles at their own pace, so keys of the next tile are on their way while one is finished.
@@ -63,7 +64,7 @@ struct ChunkTensorSmem {
     static constexpr int STAGES = D == 128 ? 5 : 11;
     static constexpr int KV = 2 * QTILE;
     static constexpr int BARS = KV + STAGES * TILE;
-    static constexpr int NBARS = 3 * STAGES + 14 + 2 * AHEAD;
+    static constexpr int NBARS = 3 * STAGES + 22 + 2 * AHEAD;
     static constexpr int SEGS = BARS + NBARS * 8;
     static constexpr int WORDS = SEGS + AHEAD * int(sizeof(Segment));
     static constexpr int RUN = (WORDS + 160 + 7) / 8 * 8;
@@ -106,27 +107,34 @@ __global__ void __launch_bounds__(CNT, 1) chunk_tensor_kernel(const __grid_const
     extern __shared__ __align__(1024) unsigned char mem[];
     const uint32_t base = smem_u32(mem);
     const int tid = threadIdx.x, warp = __shfl_sync(FULL, tid >> 5, 0), lane = tid & 31;
-    // barriers: full[ST], empty[ST]; of each tile: queries there, queries done with, scores there, weights there
-    // (in two halves), product P V done; of each product, all done when a wait ran out; landed, but still to be
-    // looked through [ST]; segments there, done with [AHEAD].  Then the segments, the tensor memory's address, a
+    // barriers: full[ST], empty[ST]; of each tile: queries there, queries done with, scores there [2], weights there
+    // (in two parts) [2][2], product P V done [2]; of each product, all done when a wait ran out; landed, but still to be
+    // looked through [ST]; segments there, done with [AHEAD].  (Two by turns where scores are two units ahead of a product.)  Then the segments, the tensor memory's address, a
     // flag, whose values had infinities taken out (four segments), which half key tiles miss pages (of sixteen tiles).
     const uint32_t full = base + S::BARS, empty = full + 8 * ST, qbar = empty + 8 * ST, qfree = qbar + 16, sbar = qfree + 16,
-                   pbar = sbar + 16, vbar = pbar + 32, xbar = vbar + 16, land = xbar + 16, segbar = land + 8 * ST, segfree = segbar + 8 * AHEAD;
+                   pbar = sbar + 32, vbar = pbar + 64, xbar = vbar + 32, land = xbar + 16, segbar = land + 8 * ST, segfree = segbar + 8 * AHEAD;
     volatile int* words = reinterpret_cast<volatile int*>(mem + S::WORDS);
     volatile int* dead = words + 1;
     volatile int* odd = words + 2;      // [4]
     volatile int* missing = words + 8;  // [16][2]
     Segment* segs = reinterpret_cast<Segment*>(mem + S::SEGS);
+    // Heads of 64 leave room for a third S: the scores of unit c (2 i + t, key tile i of query tile t of a segment) lie in S
+    // c % 3, and are written once the weights of unit c - 3 have been read: while the softmax of both tiles has work.
+    // Heads of 128 have one S for each tile.
+    constexpr bool DEEP = D == 64;
+    auto s_col = [](uint32_t b) { return b == 2 ? 384u : b * CK; };   // O lies between the second and the third
+    // of tile t's u-th key tile since the start: where its barriers are, and the parity to wait for
+    auto turn = [](int t, uint32_t u) { return DEEP ? 2 * t + (u & 1) : uint32_t(t); };
+    auto phase = [](uint32_t u) { return DEEP ? u >> 1 & 1 : u & 1; };
     // (set up while the launch before runs)
     if (warp == ROLES + 5) {
         if (lane < ST) bar_init(full + 8 * lane, 2), bar_init(empty + 8 * lane, 1), bar_init(land + 8 * lane, 2);
-        if (lane < 2) {
-            bar_init(qbar + 8 * lane, 1), bar_init(qfree + 8 * lane, 1), bar_init(sbar + 8 * lane, 1);
-            bar_init(vbar + 8 * lane, 1), bar_init(xbar + 8 * lane, 1);
-        }
+        if (lane < 2) bar_init(qbar + 8 * lane, 1), bar_init(qfree + 8 * lane, 1), bar_init(xbar + 8 * lane, 1);
+        if (lane < 4) bar_init(sbar + 8 * lane, 1), bar_init(vbar + 8 * lane, 1);
+        if (lane < 8) bar_init(pbar + 8 * lane, 128);
         // (a segment is read by four copying warps, the one that issues products, the one that looks values through, the
         // queries' and eight of the softmax)
-        if (lane < AHEAD) bar_init(pbar + 8 * lane, 128), odd[lane] = 0, bar_init(segbar + 8 * lane, 1), bar_init(segfree + 8 * lane, 15);
+        if (lane < AHEAD) odd[lane] = 0, bar_init(segbar + 8 * lane, 1), bar_init(segfree + 8 * lane, 15);
         if (lane == 0) *dead = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -248,7 +256,7 @@ __global__ void __launch_bounds__(CNT, 1) chunk_tensor_kernel(const __grid_const
         const uint32_t tm = __reduce_max_sync(FULL, tmem);
         bool ok = true;
         uint32_t at = 0, lap = 0;       // the next copy's stage in the ring, and its parity
-        uint32_t uses[2] = {0, 0}, done[2] = {0, 0};   // segments and products P V of each tile, modulo 2
+        uint32_t uses[2] = {0, 0}, made[2] = {0, 0}, done[2] = {0, 0};   // segments, modulo 2; key tiles' scores; products P V
         for (uint32_t s = 0;; ++s) {
             const Segment& sg = next_segment(s, ok);
             if (!ok) break;
@@ -256,21 +264,21 @@ __global__ void __launch_bounds__(CNT, 1) chunk_tensor_kernel(const __grid_const
             if (n == 0) break;
             give_back(s);
             auto wait = [&](uint32_t bar, uint32_t parity) { ok = ok && __all_sync(FULL, bar_wait(bar, parity, dead)); };
-            auto scores = [&](bool last, int t, uint32_t st) {
+            auto scores = [&](bool last, int t, uint32_t st, uint32_t b) {
                 const uint32_t q = q_op + t * (S::QTILE >> 4), k = k_op + st * (S::TILE >> 4);
 #pragma unroll
                 for (int d = 0; d < D / 16; ++d)
-                    mma_smem(lead, tm + t * CK, q + (((d >> 2) * (CM * 128) + (d & 3) * 32) >> 4), 0,
+                    mma_smem(lead, tm + s_col(b), q + (((d >> 2) * (CM * 128) + (d & 3) * 32) >> 4), 0,
                              k + (((d >> 2) * (CK * 128) + (d & 3) * 32) >> 4), 0, hi, QK, d > 0);
-                mma_commit(lead, sbar + 8 * t);
+                mma_commit(lead, sbar + 8 * turn(t, made[t]++));
                 if (last) mma_commit(lead, qfree + 8 * t);
                 if (t + 1 == int(tiles)) mma_commit(lead, empty + 8 * st);
             };
-            auto weighted = [&](bool add, int t, uint32_t st) {
-                const uint32_t p = tm + t * CK, o = tm + 2 * CK + t * D, v = k_op + st * (S::TILE >> 4);
+            auto weighted = [&](bool add, int t, uint32_t st, uint32_t b) {
+                const uint32_t p = tm + s_col(b), o = tm + 2 * CK + t * D, v = k_op + st * (S::TILE >> 4);
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    wait(pbar + 16 * t + 8 * h, done[t]);
+                    wait(pbar + 16 * turn(t, done[t]) + 8 * h, phase(done[t]));
                     tmem_fence_after();
                     if (ok) {
 #pragma unroll
@@ -278,7 +286,8 @@ __global__ void __launch_bounds__(CNT, 1) chunk_tensor_kernel(const __grid_const
                             mma_tmem(lead, o, p + 8 * k, v + k * (2048 >> 4), CK * 128, hi, PV, add || k > 0);
                     }
                 }
-                done[t] ^= 1;
+                if (DEEP) mma_commit(lead, vbar + 8 * turn(t, done[t]));
+                ++done[t];
                 if (t + 1 == int(tiles)) mma_commit(lead, empty + 8 * st);
             };
             auto forward = [&](uint32_t& pos, uint32_t& par) { par ^= pos + 1 == ST ? 1 : 0, pos = pos + 1 == ST ? 0 : pos + 1; };
@@ -290,32 +299,58 @@ __global__ void __launch_bounds__(CNT, 1) chunk_tensor_kernel(const __grid_const
                     wait(qbar + 8 * t, uses[t]);
                     uses[t] ^= 1;
                     tmem_fence_after();
-                    if (ok) scores(n == 1, t, at);
+                    if (ok) scores(n == 1, t, at, t);
                 }
             forward(at, lap);
-#pragma unroll 1
-            for (uint32_t i = 0; i < n && ok; ++i) {
-                // the next keys, then these values; the last values alone
-                const bool more = i + 1 < n;
-                const uint32_t kst = at, kpar = lap;
-                if (more) forward(at, lap);
-                const uint32_t vst = at, vpar = lap;
-                forward(at, lap);
-                wait(full + 8 * vst, vpar);
-                weighted(i > 0, 0, vst);
-                if (more) {
-                    wait(full + 8 * kst, kpar);
+            if constexpr (DEEP) {
+                uint32_t kst = 0, b = 0;    // the keys of the second tile's next scores; the S of this unit's first tile
+                auto ahead = [&](uint32_t j, uint32_t b) {      // the first tile's scores of key tile j
+                    if (j >= n) return;
+                    kst = at;
+                    wait(full + 8 * at, lap);
+                    forward(at, lap);
                     tmem_fence_after();
-                    if (ok) scores(i + 2 == n, 0, kst);
-                } else {
-                    mma_commit(lead, vbar);
+                    if (ok) scores(j + 1 == n, 0, kst, b);
+                };
+                ahead(1, 2);
+#pragma unroll 1
+                for (uint32_t i = 0; i < n && ok; ++i) {
+                    const uint32_t vst = at, b1 = b == 2 ? 0 : b + 1;
+                    wait(full + 8 * vst, lap);
+                    forward(at, lap);
+                    weighted(i > 0, 0, vst, b);
+                    if (tiles == 2) {
+                        if (i + 1 < n && ok) scores(i + 2 == n, 1, kst, b);
+                        weighted(i > 0, 1, vst, b1);
+                    }
+                    ahead(i + 2, b1);
+                    b = b1 == 2 ? 0 : b1 + 1;
                 }
-                if (tiles == 2) {
-                    weighted(i > 0, 1, vst);
+            } else {
+#pragma unroll 1
+                for (uint32_t i = 0; i < n && ok; ++i) {
+                    // the next keys, then these values; the last values alone
+                    const bool more = i + 1 < n;
+                    const uint32_t kst = at, kpar = lap;
+                    if (more) forward(at, lap);
+                    const uint32_t vst = at, vpar = lap;
+                    forward(at, lap);
+                    wait(full + 8 * vst, vpar);
+                    weighted(i > 0, 0, vst, 0);
                     if (more) {
-                        if (ok) scores(i + 2 == n, 1, kst);
+                        wait(full + 8 * kst, kpar);
+                        tmem_fence_after();
+                        if (ok) scores(i + 2 == n, 0, kst, 0);
                     } else {
-                        mma_commit(lead, vbar + 8);
+                        mma_commit(lead, vbar);
+                    }
+                    if (tiles == 2) {
+                        weighted(i > 0, 1, vst, 1);
+                        if (more) {
+                            if (ok) scores(i + 2 == n, 1, kst, 1);
+                        } else {
+                            mma_commit(lead, vbar + 8);
+                        }
                     }
                 }
             }
@@ -470,7 +505,7 @@ __global__ void __launch_bounds__(CNT, 1) chunk_tensor_kernel(const __grid_const
         asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
         const int t = warp >> 2, r = tid & 127;
         const uint32_t lanes = uint32_t(warp & 3) << 21;   // the warp's 32 lanes of tensor memory
-        const uint32_t sc = tmem + t * CK + lanes, oc = tmem + 2 * CK + t * D + lanes;
+        const uint32_t oc = tmem + 2 * CK + t * D + lanes;
         bool ok = true;
         uint32_t done = 0, unit = 0, ends = 0;      // scores of this tile; key tiles of segments before; segments of this tile
 #pragma unroll 1
@@ -488,7 +523,8 @@ __global__ void __launch_bounds__(CNT, 1) chunk_tensor_kernel(const __grid_const
 #pragma unroll 1
                 for (int i = 0; i < n; ++i) {
                     const int at = i0 + i, k0 = (at < few ? at : at - few + skip) * CK;
-                    ok = __all_sync(FULL, bar_wait(sbar + 8 * t, done & 1, dead));
+                    const uint32_t turns = turn(t, done), sc = tmem + lanes + s_col(DEEP ? uint32_t(2 * i + t) % 3 : uint32_t(t));
+                    ok = __all_sync(FULL, bar_wait(sbar + 8 * turns, phase(done), dead));
                     if (!ok) break;
                     ++done;
                     tmem_fence_after();
@@ -549,7 +585,12 @@ __global__ void __launch_bounds__(CNT, 1) chunk_tensor_kernel(const __grid_const
                         m = mn;
                         l *= f;
                         if (i > 0) {
-                            // (the last product of this tile was done before these scores were begun)
+                            // (with one S the last product of this tile was done before these scores were begun)
+                            if (DEEP) {
+                                ok = __all_sync(FULL, bar_wait(vbar + 8 * turn(t, done), phase(done - 2), dead));
+                                if (!ok) break;
+                                tmem_fence_after();
+                            }
 #pragma unroll 1
                             for (int c = 0; c < D; c += 16) {
                                 uint32_t y[16];
@@ -601,7 +642,7 @@ __global__ void __launch_bounds__(CNT, 1) chunk_tensor_kernel(const __grid_const
                     auto there = [&](int h) {
                         tmem_wait_st();
                         tmem_fence_before();
-                        bar_arrive(pbar + 16 * t + 8 * h);
+                        bar_arrive(pbar + 16 * turns + 8 * h);
                     };
                     weigh(Int<0>(), Int<96>());
                     tmem_st32(sc, part<32>(x, 0));
@@ -614,7 +655,8 @@ __global__ void __launch_bounds__(CNT, 1) chunk_tensor_kernel(const __grid_const
                     l += (s0 + s1) + (s2 + s3);
                 }
                 // ---- the row's output, once the last product is done
-                ok = ok && __all_sync(FULL, bar_wait(vbar + 8 * t, ends++ & 1, dead));
+                const uint32_t end = DEEP ? done - 1 : ends++;
+                ok = ok && __all_sync(FULL, bar_wait(vbar + 8 * turn(t, end), phase(end), dead));
                 tmem_fence_after();
                 const float bad = (!ok || *dead) ? __int_as_float(0x7fffffff) : 0.f;
                 const float inv = (l == 0.f ? 0.f : 1.f / l) + bad;

@@ -8,7 +8,7 @@
 
 namespace fsd {
 
-constexpr int FEW = 16;         // query rows that a tile of chunk_rows_kernel holds beside the tensor cores' tiles
+constexpr int FEW = 16;         // query rows that a tile of chunk_few_kernel holds beside the tensor cores' tiles
 constexpr int MANY = 256;       // query rows of a tensor-core tile
 constexpr int FEW_START = 2;    // key tiles of 64 that start and end of such a tile take as long as
 
@@ -172,6 +172,7 @@ __device__ __forceinline__ bool many_run(const ChunkArgs& a, int cta, int64_t* w
         return M > a.rows_upto ? (M + MANY - 1) / MANY : 0;
     };
     auto units = [&](const Request& x, int row0) { return ManyTile(a, x, row0).units; };
+    if (tid == 0) run.r = run.row0 = 0, run.before = 0;    // (a request that there is, whatever the lengths)
     int64_t tiles, total, mine = 0;
     for (int r = r0; r < r1; ++r) mine += tiles_of(request<true>(a, r));
     tiles_before[tid] = block_sum_before<NT>(mine, words, tiles);

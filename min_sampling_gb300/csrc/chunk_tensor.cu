@@ -578,7 +578,10 @@ __global__ void __launch_bounds__(CNT, 1) chunk_tensor_kernel(const __grid_const
                     }
                     float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
                     mx *= mul;
-                    if (!(mx > -INFINITY)) mx = m;   // a scale of 0 times infinity, or nothing but NaN
+                    // A scale of 0 times infinity, or nothing but NaN.  Rows behind the request's have the queries of whatever
+                    // request comes next (with its outputs, where those are written over them): without a maximum they have no
+                    // part in the votes below, which decide how the warp's other rows are rounded.
+                    if (!on || !(mx > -INFINITY)) mx = m;
                     if (__any_sync(FULL, mx - m > W::GROWTH)) {   // (the difference is exact where it decides)
                         const float mn = fmaxf(m, mx);
                         const float f = m == -INFINITY ? 0.f : exp2_fast(m - mn);

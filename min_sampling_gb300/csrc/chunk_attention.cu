@@ -597,6 +597,9 @@ struct ChunkPlan {
     size_t t_part_o, t_part_l, t_split;
 };
 
+// A workspace lies at any multiple of 16 bytes; the tensor cores' parts are written 32 bytes a store.
+constexpr size_t WS_ALIGN = 32;
+
 static size_t add_bytes(size_t& at, size_t n) {
     const size_t here = at;
     at += (n + 255) & ~size_t(255);
@@ -630,7 +633,7 @@ static ChunkPlan chunk_plan(const fs_paged_kv& c, int N, int R, int Hq, int widt
         p.t_part_l = add_bytes(at, size_t(2) * p.t_grid * MANY * 8);
         p.t_split = add_bytes(at, size_t(p.t_grid) * sizeof(int4));
     }
-    p.bytes = at;
+    p.bytes = at + WS_ALIGN - 16;    // (room to round a workspace's address up)
     return p;
 }
 
@@ -760,7 +763,7 @@ fs_status fs_paged_chunk_attention(const fs_paged_kv* cache, const void* query, 
     a.rows_upto = p.t_grid > 0 ? FEW : 0x7fffffff;
     a.grid = p.grid;
     a.least = p.least;
-    unsigned char* ws = static_cast<unsigned char*>(workspace);
+    unsigned char* ws = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(workspace) + WS_ALIGN - 1) & ~uintptr_t(WS_ALIGN - 1));
     a.part_o = reinterpret_cast<float*>(ws + p.part_o);
     a.part_l = reinterpret_cast<float2*>(ws + p.part_l);
     a.split = reinterpret_cast<int4*>(ws + p.split);

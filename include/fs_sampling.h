@@ -572,6 +572,11 @@ fs_status fs_paged_chunk_attention_workspace_bytes(const fs_paged_kv* cache, int
                                                    int32_t q_heads, int32_t table_width, int32_t max_queries,
                                                    size_t* bytes);
 
+/* The kernels of fs_paged_chunk_attention hand tiles from one role to the next over barriers.  No wait for one takes longer than
+ * `cycles` clock cycles of the GPU (4e9, about two seconds, until this is called); a CTA whose wait runs out ends without having
+ * answered for its rows.  For all later calls of the process; a captured call keeps the limit that it was captured with.  Meant for tests. */
+fs_status fs_paged_chunk_attention_wait_limit(int64_t cycles);
+
 /* Penalties, biases and grammar masks on logits, row by row, in this order, in float32 and rounded once:
  *   repetition  of a token that is in the row's history: z > 0 ? z / repetition : z * repetition
  *   frequency   z - frequency * count, count: how often the token is in the history behind the prompt

@@ -28,6 +28,7 @@ struct ChunkArgs {
     int window, sinks;          // window: INT_MAX without one
     float scale;                // the score's scale times log2(e)
     int zero_rest;              // rows of no request get zeros (and lse -infinity)
+    long long patience;         // clock cycles before a wait gives up
     int rows_upto;              // chunk_rows_kernel takes requests of up to this many query rows a key/value head
     // chunk_rows_kernel: CTAs, their parts, what the parts belong to
     int grid, least;            // least: units (key tiles) of a CTA at least

@@ -20,6 +20,7 @@
 // chunk_rows_kernel (mma.sync) has many rows of heads of 256, and a few where the caches' strides have no map for the copy engine.
 #include "chunk.cuh"
 
+#include <atomic>
 #include <numeric>
 #include <type_traits>
 
@@ -661,6 +662,9 @@ static fs_status run_chunk(ChunkArgs& a, const ChunkPlan& p, int sms, int dtype,
                       size_t(a.grid + a.t_grid) * sizeof(JoinTile), stream, a, p.MT);
 }
 
+// The longest wait of the kernels for their own copies and products, in clock cycles.
+static std::atomic<int64_t> wait_limit{PATIENCE};
+
 static fs_status check_chunk(const fs_paged_kv* c, int N, int R, int Hq, int width, int most) {
     if (!c || N < 0 || R < 0 || Hq < 1 || width < 0 || most < 1) return FS_ERR_INVALID_ARG;
     if (c->num_pages < 0 || c->page_size < 1 || c->num_heads < 1 || c->head_dim < 1) return FS_ERR_INVALID_ARG;
@@ -693,6 +697,12 @@ fs_status fs_paged_chunk_attention_workspace_bytes(const fs_paged_kv* cache, int
     st = device_limits(sms, optin);
     if (st != FS_OK) return st;
     *bytes = chunk_plan(*cache, tokens, requests, q_heads, table_width, max_queries, sms).bytes;
+    return FS_OK;
+}
+
+fs_status fs_paged_chunk_attention_wait_limit(int64_t cycles) {
+    if (cycles < 0) return FS_ERR_INVALID_ARG;
+    fsd::wait_limit.store(cycles, std::memory_order_relaxed);
     return FS_OK;
 }
 
@@ -760,6 +770,7 @@ fs_status fs_paged_chunk_attention(const fs_paged_kv* cache, const void* query, 
     a.sinks = window == 0 ? 0 : sinks;
     a.scale = scale * 1.44269504088896341f;
     a.zero_rest = zero_rest;
+    a.patience = wait_limit.load(std::memory_order_relaxed);
     a.rows_upto = p.t_grid > 0 ? FEW : 0x7fffffff;
     a.grid = p.grid;
     a.least = p.least;

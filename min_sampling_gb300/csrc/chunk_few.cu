@@ -81,7 +81,7 @@ __global__ void __launch_bounds__(FNT) chunk_few_kernel(const __grid_constant__ 
         bool ok = true;
         for (uint32_t s = 0;; ++s) {
             const uint32_t slot = s % FAHEAD;
-            if (s >= FAHEAD) ok = __all_sync(FULL, bar_wait(segfree + 8 * slot, (s / FAHEAD - 1) & 1, dead));
+            if (s >= FAHEAD) ok = __all_sync(FULL, bar_wait(segfree + 8 * slot, (s / FAHEAD - 1) & 1, dead, a.patience));
             if (!ok) break;
             FewSegment sg;
             sg.n = 0;
@@ -136,7 +136,7 @@ __global__ void __launch_bounds__(FNT) chunk_few_kernel(const __grid_constant__ 
                 const int k0 = sg.kt.at(sg.i0 + i);
                 Pages now = pages;
                 if (i + 1 < sg.n) pages.look_up<false>(a, table, sg.kt.at(sg.i0 + i + 1) + row);
-                if (lap > 0) ok = __all_sync(FULL, bar_wait(empty + 8 * st, (lap - 1) & 1, dead));
+                if (lap > 0) ok = __all_sync(FULL, bar_wait(empty + 8 * st, (lap - 1) & 1, dead, a.patience));
                 if (!ok) break;
                 const int any = __any_sync(FULL, now.resolve(a, sg.kt, k0 + row));
                 if (lane == 0) {
@@ -159,10 +159,9 @@ __global__ void __launch_bounds__(FNT) chunk_few_kernel(const __grid_constant__ 
         float* merge = reinterpret_cast<float*>(mem + S::MERGE);
         for (uint32_t s = 0;; ++s) {
             const uint32_t slot = s % FAHEAD;
-            bool ok = __all_sync(FULL, bar_wait(segbar + 8 * slot, (s / FAHEAD) & 1, dead));
+            bool ok = __all_sync(FULL, bar_wait(segbar + 8 * slot, (s / FAHEAD) & 1, dead, a.patience));
             const FewSegment& sg = segs[slot];
             const int n = ok ? sg.n : 0;
-            if (ok && n == 0) break;
             float o[D / 8][4];
             float mrow[2] = {-INFINITY, -INFINITY}, lrow[2] = {0.f, 0.f};
             int pos[2] = {0, 0};
@@ -173,8 +172,8 @@ __global__ void __launch_bounds__(FNT) chunk_few_kernel(const __grid_constant__ 
                 for (int e = 0; e < 4; ++e) o[f][e] = 0.f;
             const uint32_t qs = base + S::Q + slot * S::QTILE;
             uint32_t qf[D <= 128 ? D / 16 : 1][4];
-            if (ok) {
-                ok = __all_sync(FULL, bar_wait(qbar + 8 * slot, (s / FAHEAD) & 1, dead));
+            if (n > 0) {
+                ok = __all_sync(FULL, bar_wait(qbar + 8 * slot, (s / FAHEAD) & 1, dead, a.patience));
                 if constexpr (D <= 128) {
 #pragma unroll
                     for (int kk = 0; kk < D / 16; ++kk) ldsm4(qf[kk], qs + tile_at<FEW>(lane & 15, kk * 2 + (lane >> 4)));
@@ -186,7 +185,7 @@ __global__ void __launch_bounds__(FNT) chunk_few_kernel(const __grid_constant__ 
             for (int i = 0; i < n && ok; ++i, ++c) {
                 const uint32_t lap = c / ST, st = c - lap * ST;
                 const int k0 = sg.kt.at(sg.i0 + i);
-                ok = __all_sync(FULL, bar_wait(full + 8 * st, lap & 1, dead));
+                ok = __all_sync(FULL, bar_wait(full + 8 * st, lap & 1, dead, a.patience));
                 if (!ok) break;
                 const uint32_t ks = base + st * 2 * S::TILE, vs = ks + S::TILE;
                 // A value that only some of the tokens see may be infinite or NaN, which a weight of zero does not
@@ -300,7 +299,9 @@ __global__ void __launch_bounds__(FNT) chunk_few_kernel(const __grid_constant__ 
             if (lane == 0) gone[warp] = ok ? odd_any : 2;
             asm volatile("bar.sync 1, 128;" ::: "memory");
             const int f0 = gone[0], f1 = gone[1], f2 = gone[2], f3 = gone[3];
-            if (f0 == 2 || f1 == 2 || f2 == 2 || f3 == 2) break;   // (all four, so that none waits for another; *dead is set)
+            // All four leave here and nowhere else, at a run's end or when one of them has given up (*dead is set): a warp that saw
+            // the end and left by itself would be waited for by one whose wait for the same segment ran out.
+            if (n == 0 || f0 == 2 || f1 == 2 || f2 == 2 || f3 == 2) break;
             const bool fix = (f0 | f1 | f2 | f3) != 0;
             float scale[2];
 #pragma unroll

@@ -161,7 +161,7 @@ __global__ void __launch_bounds__(CNT, 1) chunk_tensor_kernel(const __grid_const
 
     // The s-th segment, once it is described; and given back, by each warp.
     auto next_segment = [&](uint32_t s, bool& ok) -> const Segment& {
-        ok = ok && __all_sync(FULL, bar_wait(segbar + 8 * (s % AHEAD), (s / AHEAD) & 1, dead));
+        ok = ok && __all_sync(FULL, bar_wait(segbar + 8 * (s % AHEAD), (s / AHEAD) & 1, dead, a.patience));
         return segs[s % AHEAD];
     };
     auto give_back = [&](uint32_t s) {
@@ -196,7 +196,7 @@ __global__ void __launch_bounds__(CNT, 1) chunk_tensor_kernel(const __grid_const
             for (int i = 0; i < n; ++i) {
                 const int k0 = kt.at(i0 + i);
                 const uint32_t c = seq + (value ? values_copy(i, n) : keys_copy(i)), lap = c / ST, st = c - lap * ST;
-                if (lap > 0 && !__all_sync(FULL, bar_wait(empty + 8 * st, (lap - 1) & 1, dead))) {
+                if (lap > 0 && !__all_sync(FULL, bar_wait(empty + 8 * st, (lap - 1) & 1, dead, a.patience))) {
                     ok = false;
                     break;
                 }
@@ -263,7 +263,7 @@ __global__ void __launch_bounds__(CNT, 1) chunk_tensor_kernel(const __grid_const
             const uint32_t n = __reduce_max_sync(FULL, uint32_t(sg.n)), tiles = __reduce_max_sync(FULL, sg.two() ? 2u : 1u);
             if (n == 0) break;
             give_back(s);
-            auto wait = [&](uint32_t bar, uint32_t parity) { ok = ok && __all_sync(FULL, bar_wait(bar, parity, dead)); };
+            auto wait = [&](uint32_t bar, uint32_t parity) { ok = ok && __all_sync(FULL, bar_wait(bar, parity, dead, a.patience)); };
             auto scores = [&](bool last, int t, uint32_t st, uint32_t b) {
                 const uint32_t q = q_op + t * (S::QTILE >> 4), k = k_op + st * (S::TILE >> 4);
 #pragma unroll
@@ -376,7 +376,7 @@ __global__ void __launch_bounds__(CNT, 1) chunk_tensor_kernel(const __grid_const
             for (int i = 0; i < n && ok; ++i) {
                 if (!sg.partial(a, sg.kt.at(sg.i0 + i))) continue;
                 const uint32_t st = (seq + values_copy(i, n)) % ST;
-                ok = __all_sync(FULL, bar_wait(land + 8 * st, uses >> st & 1, dead));
+                ok = __all_sync(FULL, bar_wait(land + 8 * st, uses >> st & 1, dead, a.patience));
                 if (!ok) break;
                 uses ^= 1u << st;
                 uint4* tile = reinterpret_cast<uint4*>(mem + S::KV + st * S::TILE);
@@ -403,7 +403,7 @@ __global__ void __launch_bounds__(CNT, 1) chunk_tensor_kernel(const __grid_const
         const int64_t last = run.last;
         bool ok = true;
         for (uint32_t s = 0; ok; ++s) {
-            if (s >= AHEAD) ok = __all_sync(FULL, bar_wait(segfree + 8 * (s % AHEAD), (s / AHEAD - 1) & 1, dead));
+            if (s >= AHEAD) ok = __all_sync(FULL, bar_wait(segfree + 8 * (s % AHEAD), (s / AHEAD - 1) & 1, dead, a.patience));
             if (!ok) break;
             Segment sg;
             sg.n = 0;
@@ -455,7 +455,7 @@ __global__ void __launch_bounds__(CNT, 1) chunk_tensor_kernel(const __grid_const
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
                 if (t == 1 && !sg.two()) break;
-                if (uses[t] > 0) ok = ok && __all_sync(FULL, bar_wait(qfree + 8 * t, (uses[t] - 1) & 1, dead));
+                if (uses[t] > 0) ok = ok && __all_sync(FULL, bar_wait(qfree + 8 * t, (uses[t] - 1) & 1, dead, a.patience));
                 if (!ok) break;
                 ++uses[t];
                 const int row0 = sg.row0 + t * CM;
@@ -524,7 +524,7 @@ __global__ void __launch_bounds__(CNT, 1) chunk_tensor_kernel(const __grid_const
                 for (int i = 0; i < n; ++i) {
                     const int at = i0 + i, k0 = (at < few ? at : at - few + skip) * CK;
                     const uint32_t turns = turn(t, done), sc = tmem + lanes + s_col(DEEP ? uint32_t(2 * i + t) % 3 : uint32_t(t));
-                    ok = __all_sync(FULL, bar_wait(sbar + 8 * turns, phase(done), dead));
+                    ok = __all_sync(FULL, bar_wait(sbar + 8 * turns, phase(done), dead, a.patience));
                     if (!ok) break;
                     ++done;
                     tmem_fence_after();
@@ -590,7 +590,7 @@ __global__ void __launch_bounds__(CNT, 1) chunk_tensor_kernel(const __grid_const
                         if (i > 0) {
                             // (with one S the last product of this tile was done before these scores were begun)
                             if (DEEP) {
-                                ok = __all_sync(FULL, bar_wait(vbar + 8 * turn(t, done), phase(done - 2), dead));
+                                ok = __all_sync(FULL, bar_wait(vbar + 8 * turn(t, done), phase(done - 2), dead, a.patience));
                                 if (!ok) break;
                                 tmem_fence_after();
                             }
@@ -659,7 +659,7 @@ __global__ void __launch_bounds__(CNT, 1) chunk_tensor_kernel(const __grid_const
                 }
                 // ---- the row's output, once the last product is done
                 const uint32_t end = DEEP ? done - 1 : ends++;
-                ok = ok && __all_sync(FULL, bar_wait(vbar + 8 * turn(t, end), phase(end), dead));
+                ok = ok && __all_sync(FULL, bar_wait(vbar + 8 * turn(t, end), phase(end), dead, a.patience));
                 tmem_fence_after();
                 const float bad = (!ok || *dead) ? __int_as_float(0x7fffffff) : 0.f;
                 const float inv = (l == 0.f ? 0.f : 1.f / l) + bad;

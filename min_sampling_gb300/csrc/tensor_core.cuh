@@ -27,14 +27,14 @@ __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
 }
 // False when the wait ran out here or in another role of the CTA.  (A try suspends the thread for some time by itself; with
 // a time of 2 us asked for, a warp woke up later: chunks of 1021 tokens behind 16384 431 us, 412 without.)
-__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile int* dead) {
+__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile int* dead, long long patience = PATIENCE) {
     if (bar_try(bar, parity)) return true;
     const long long start = clock64();
     for (uint32_t i = 1;; ++i) {
         if (bar_try(bar, parity)) return true;
         if ((i & 7) == 0) {
             if (*dead) return false;
-            if (clock64() - start > PATIENCE) break;
+            if (clock64() - start > patience) break;
         }
     }
     *dead = 1;

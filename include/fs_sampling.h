@@ -573,8 +573,9 @@ fs_status fs_paged_chunk_attention_workspace_bytes(const fs_paged_kv* cache, int
                                                    size_t* bytes);
 
 /* The kernels of fs_paged_chunk_attention hand tiles from one role to the next over barriers.  No wait for one takes longer than
- * `cycles` clock cycles of the GPU (4e9, about two seconds, until this is called); a CTA whose wait runs out ends without having
- * answered for its rows.  For all later calls of the process; a captured call keeps the limit that it was captured with.  Meant for tests. */
+ * `cycles` clock cycles of the GPU (4e9, about two seconds, until this is called); a CTA whose wait runs out writes NaN for
+ * all rows that it has keys of.  A shorter limit is kept to the cycle by the role that describes tiles for the others; theirs run out with
+ * it.  For all later calls of the process; a captured call keeps the limit that it was captured with.  Meant for tests. */
 fs_status fs_paged_chunk_attention_wait_limit(int64_t cycles);
 
 /* Penalties, biases and grammar masks on logits, row by row, in this order, in float32 and rounded once:

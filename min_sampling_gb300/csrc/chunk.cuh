@@ -276,6 +276,24 @@ __device__ __forceinline__ void zero_rest(const ChunkArgs& a, int cta, int threa
     }
 }
 
+// A tile of a CTA that gave up, sg its part: NaN for its rows (of a cut tile, for the sums that they are joined by).  By one warp.
+template <typename T, int D, int ROWS, typename Seg>
+__device__ __forceinline__ void lost_tile(const ChunkArgs& a, const Seg& sg, float2* part_l, int4* split, int cta, int lane) {
+    const float nan = __int_as_float(0x7fffffff);
+#pragma unroll 1
+    for (int r = 0; r < min(ROWS, sg.M - sg.row0); ++r) {
+        const int row = sg.row0 + r, j = row / a.gs, h = sg.head * a.gs + row - j * a.gs;
+        if (sg.whole) {
+            T* out = static_cast<T*>(a.out) + (sg.x.q0 + j) * a.os[0] + h * a.os[1];
+            if (lane < D / 8) *reinterpret_cast<uint4*>(out + lane * 8) = make_uint4(0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu);
+            if (lane == 0 && a.lse) a.lse[int64_t(sg.x.q0 + j) * a.Hq + h] = nan;
+        } else if (lane == 0) {
+            part_l[int64_t(2 * cta + (sg.i0 == 0)) * ROWS + r] = make_float2(-INFINITY, nan);
+        }
+    }
+    if (sg.parts > 0 && lane == 0) split[cta] = make_int4(sg.r, sg.head, sg.row0, sg.parts);
+}
+
 // ------------------------------------------------------------------ infinite and NaN values
 
 // Whether an element of a 16-byte word is infinite or NaN, and the word with zeros in their place.

@@ -7,6 +7,7 @@
 // tile's end.  Nothing but the ring's barriers ties them together, so the reads go on over the ends of tiles and
 // requests.  64 requests of up to 8192 tokens, 8 heads of 128: 170 us, 6.4 TB/s (with copies by the four
 // warps themselves, a tile ahead and a barrier each, 250 us).
+// Every wait on a barrier is bounded; one that runs out marks the CTA, which then writes NaN for all rows of its run.
 #include "chunk_copy.cuh"
 
 #include "fragments.cuh"
@@ -24,6 +25,44 @@ struct FewSegment {
     Request x;
     KeyTiles<FK> kt;
     int p_lo, p_hi;             // positions of the first and last token
+};
+
+// A CTA's way along its run.
+struct FewLine {
+    Place pl;
+    Request x;
+    int64_t unit;
+    __device__ __forceinline__ FewLine(const ChunkArgs& a, const Run& run) : pl(run.place), x{}, unit(run.first) {
+        if (run.first < run.last) x = request<false>(a, pl.r);     // (there may be no requests at all)
+    }
+    // The segment that the next unit lies in; n = 0: none.
+    __device__ __forceinline__ FewSegment next(const ChunkArgs& a, const Run& run, int cta) {
+        FewSegment sg;
+        sg.n = 0;
+        if (unit >= run.last) return sg;
+        while (unit >= pl.before + pl.units * a.Hkv) {
+            pl.before += pl.units * a.Hkv;
+            x = request<false>(a, ++pl.r);
+            pl.units = units_of<FEW, FK>(a, x);
+        }
+        sg.r = pl.r, sg.x = x;
+        sg.head = int((unit - pl.before) / pl.units);
+        sg.M = x.rows(a);
+        int64_t from = pl.before + int64_t(sg.head) * pl.units;   // the tile's first unit
+        sg.row0 = 0;
+        for (;; from += sg.kt.n + FEW_START, sg.row0 += FEW) {
+            sg.p_lo = x.pos(a, sg.row0), sg.p_hi = x.pos(a, min(sg.row0 + FEW, sg.M) - 1);
+            sg.kt = KeyTiles<FK>(a, sg.p_lo, sg.p_hi);
+            if (unit < from + sg.kt.n + FEW_START) break;
+        }
+        const int each = sg.kt.n + FEW_START;
+        sg.i0 = int(max(unit - from - FEW_START, int64_t(0)));
+        sg.n = max(int(min(int64_t(each), run.last - from)) - FEW_START - sg.i0, 0);
+        sg.whole = sg.n == sg.kt.n;
+        sg.parts = sg.whole || sg.i0 > 0 ? 0 : int((from + each - 1) / run.length) - cta + 1;
+        unit = min(from + each, run.last);
+        return sg;      // (a run that ends within a tile's FEW_START leaves all of it to the next)
+    }
 };
 
 template <int D>
@@ -71,44 +110,22 @@ __global__ void __launch_bounds__(FNT) chunk_few_kernel(const __grid_constant__ 
     if (a.zero_rest) zero_rest<T, D>(a, cta, FNT);
     __syncthreads();
 
+    // Every role's end.  Copies that one which gave up has in flight land (a microsecond or two) before their memory is anyone
+    // else's.
+    auto all_done = [&]() {
+        for (int i = 0; *dead && i < 1000; ++i) __nanosleep(1000);
+        asm volatile("bar.sync 2, %0;" ::"n"(FNT) : "memory");
+    };
     if (warp == 4) {
         // ================================================ what the next tiles are, and their copies
-        Place pl = run.place;
-        Request x = {};
-        if (run.first < run.last) x = request<false>(a, pl.r);     // (there may be no requests at all)
-        int64_t unit = run.first;
+        FewLine line(a, run);
         uint32_t c = 0;         // key tiles before
         bool ok = true;
         for (uint32_t s = 0;; ++s) {
             const uint32_t slot = s % FAHEAD;
-            if (s >= FAHEAD) ok = __all_sync(FULL, bar_wait(segfree + 8 * slot, (s / FAHEAD - 1) & 1, dead, a.patience));
+            if (s >= FAHEAD) ok = __all_sync(FULL, bar_wait_exactly(segfree + 8 * slot, (s / FAHEAD - 1) & 1, dead, a.patience));
             if (!ok) break;
-            FewSegment sg;
-            sg.n = 0;
-            if (unit < run.last) {
-                while (unit >= pl.before + pl.units * a.Hkv) {
-                    pl.before += pl.units * a.Hkv;
-                    x = request<false>(a, ++pl.r);
-                    pl.units = units_of<FEW, FK>(a, x);
-                }
-                sg.r = pl.r, sg.x = x;
-                sg.head = int((unit - pl.before) / pl.units);
-                sg.M = x.rows(a);
-                int64_t from = pl.before + int64_t(sg.head) * pl.units;   // the tile's first unit
-                sg.row0 = 0;
-                for (;; from += sg.kt.n + FEW_START, sg.row0 += FEW) {
-                    sg.p_lo = x.pos(a, sg.row0), sg.p_hi = x.pos(a, min(sg.row0 + FEW, sg.M) - 1);
-                    sg.kt = KeyTiles<FK>(a, sg.p_lo, sg.p_hi);
-                    if (unit < from + sg.kt.n + FEW_START) break;
-                }
-                const int each = sg.kt.n + FEW_START;
-                sg.i0 = int(max(unit - from - FEW_START, int64_t(0)));
-                sg.n = max(int(min(int64_t(each), run.last - from)) - FEW_START - sg.i0, 0);
-                sg.whole = sg.n == sg.kt.n;
-                sg.parts = sg.whole || sg.i0 > 0 ? 0 : int((from + each - 1) / run.length) - cta + 1;
-                unit = min(from + each, run.last);
-                // (a run that ends within a tile's FEW_START leaves all of it to the next)
-            }
+            const FewSegment sg = line.next(a, run, cta);
             if (lane == 0) segs[slot] = sg;
             if (sg.n > 0) {
                 // queries: rows 4 q .. 4 q + 3 by lane (q, block)
@@ -117,7 +134,7 @@ __global__ void __launch_bounds__(FNT) chunk_few_kernel(const __grid_constant__ 
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const int row = sg.row0 + q * 4 + j, tok = row / a.gs;
-                    rows[j] = row < sg.M ? (x.q0 + tok) * maps.q.step[0] + (sg.head * a.gs + row - tok * a.gs) * maps.q.step[1] : -1;
+                    rows[j] = row < sg.M ? (sg.x.q0 + tok) * maps.q.step[0] + (sg.head * a.gs + row - tok * a.gs) * maps.q.step[1] : -1;
                 }
                 if (lane == 0) bar_expect(qbar + 8 * slot, S::QTILE);
                 __syncwarp();
@@ -151,6 +168,13 @@ __global__ void __launch_bounds__(FNT) chunk_few_kernel(const __grid_constant__ 
             if (!ok) break;
         }
         if (!ok) *dead = 1;
+        all_done();
+        if (*dead) {    // what has been written of the run's rows is not told apart from what has not
+            line = FewLine(a, run);
+            for (FewSegment sg = line.next(a, run, cta); sg.n > 0; sg = line.next(a, run, cta))
+                lost_tile<T, D, FEW>(a, sg, a.part_l, a.split, cta, lane);
+        }
+        return;
     } else {
         // ================================================ 16 keys of each tile a warp
         uint32_t c = 0;
@@ -371,9 +395,7 @@ __global__ void __launch_bounds__(FNT) chunk_few_kernel(const __grid_constant__ 
             if (lane == 0) bar_arrive(segfree + 8 * slot);
         }
     }
-    // Copies that a role which gave up has in flight land (a microsecond or two) before their memory is anyone else's.
-    __syncthreads();
-    for (int i = 0; *dead && i < 1000; ++i) __nanosleep(1000);
+    all_done();
 }
 
 template <typename T, int D>

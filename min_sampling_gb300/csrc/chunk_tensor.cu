@@ -36,7 +36,7 @@
 // One CTA per SM takes an equal run of units (key tiles) of the launch's line of work, see many_run; all
 // roles walk the run's tiles at their own pace, so keys of the next tile are on their way while one is finished.
 // Every wait on a barrier is bounded; one that runs out marks the CTA, which then drains its copies
-// and products, frees its tensor memory and writes NaN.
+// and products, frees its tensor memory and writes NaN for all rows of its run.
 #include "chunk_copy.cuh"
 
 namespace fsd {
@@ -56,6 +56,52 @@ struct Segment {
     int p_lo, p_hi;             // positions of the first and last token
     __device__ __forceinline__ bool two() const { return M - row0 > CM; }   // rows for the second tile
     __device__ __forceinline__ bool partial(const ChunkArgs& a, int k0) const { return partial_keys(a, p_lo, p_hi, k0, CK); }
+};
+
+// A CTA's way along its run.  Warp-collective.
+struct ManyLine {
+    int r, row0;
+    int64_t u, before;
+    __device__ __forceinline__ explicit ManyLine(const ManyRun& run) : r(run.r), row0(run.row0), u(run.first), before(run.before) {}
+    // The segment that the next unit lies in; n = 0: none.
+    __device__ __forceinline__ Segment next(const ChunkArgs& a, const ManyRun& run, int cta, int lane) {
+        const int64_t last = run.last;
+        Segment sg;
+        sg.n = 0;
+        if (u >= last) return sg;
+        sg.r = r, sg.row0 = row0;
+        sg.x = request<true>(a, r);
+        sg.M = sg.x.rows(a);
+        const ManyTile tile(a, sg.x, row0);
+        const int each = tile.units;
+        sg.p_lo = tile.p_lo, sg.p_hi = tile.p_hi, sg.kt = tile.kt;
+        sg.head = int((u - before) / each);
+        const int64_t from = before + int64_t(sg.head) * each;     // of this head
+        sg.i0 = tile.tiles(u - from);
+        sg.n = tile.tiles(min(int64_t(each), last - from)) - sg.i0;
+        sg.whole = sg.n == sg.kt.n;
+        sg.parts = sg.whole || sg.i0 > 0 ? 0 : run.owner(from + each - 1) - cta + 1;
+        u = min(from + each, last);
+        if (u < last && u >= before + int64_t(each) * a.Hkv) {
+            before += int64_t(each) * a.Hkv;
+            row0 += MANY;
+            if (row0 >= sg.M) {     // the next request with more than FEW rows
+                row0 = 0;
+                for (unsigned hit = 0; hit == 0;) {
+                    const int k = r + 1 + lane;
+                    hit = __ballot_sync(FULL, k < a.R && request<true>(a, min(k, a.R - 1)).rows(a) > a.rows_upto);
+                    r += hit ? __ffs(int(hit)) : 32;
+                    if (!hit && r >= a.R - 1) {     // (none is left: not with the lengths that the run was cut by)
+                        u = last;
+                        break;
+                    }
+                }
+            }
+        }
+        // (a run that ends within a tile's start leaves all of it to the next)
+        if (sg.n <= 0) sg.n = 0;
+        return sg;
+    }
 };
 
 template <int D>
@@ -167,6 +213,15 @@ __global__ void __launch_bounds__(CNT, 1) chunk_tensor_kernel(const __grid_const
     auto give_back = [&](uint32_t s) {
         __syncwarp();
         if (lane == 0) bar_arrive(segfree + 8 * (s % AHEAD));
+    };
+
+    // Every role's end.  Copies that one which gave up has in flight land (a microsecond or two) before their memory is anyone
+    // else's.
+    auto all_done = [&]() {
+        for (int i = 0; *dead && i < 1000; ++i) __nanosleep(1000);
+        tmem_fence_before();
+        asm volatile("bar.sync 1, %0;" ::"n"(CNT) : "memory");
+        tmem_fence_after();
     };
 
     // Registers: 128 a thread at launch (512 threads); 200 for the softmax's two warpgroups and 56 for the other
@@ -398,53 +453,25 @@ __global__ void __launch_bounds__(CNT, 1) chunk_tensor_kernel(const __grid_const
         if (!ok) *dead = 1;
     } else if (warp == ROLES + 6) {
         // ================================================ what the next tiles are
-        int r = run.r, row0 = run.row0;
-        int64_t u = run.first, before = run.before;
-        const int64_t last = run.last;
+        ManyLine line(run);
         bool ok = true;
         for (uint32_t s = 0; ok; ++s) {
-            if (s >= AHEAD) ok = __all_sync(FULL, bar_wait(segfree + 8 * (s % AHEAD), (s / AHEAD - 1) & 1, dead, a.patience));
+            if (s >= AHEAD) ok = __all_sync(FULL, bar_wait_exactly(segfree + 8 * (s % AHEAD), (s / AHEAD - 1) & 1, dead, a.patience));
             if (!ok) break;
-            Segment sg;
-            sg.n = 0;
-            if (u < last) {
-                sg.r = r, sg.row0 = row0;
-                sg.x = request<true>(a, r);
-                sg.M = sg.x.rows(a);
-                const ManyTile tile(a, sg.x, row0);
-                const int each = tile.units;
-                sg.p_lo = tile.p_lo, sg.p_hi = tile.p_hi, sg.kt = tile.kt;
-                sg.head = int((u - before) / each);
-                const int64_t from = before + int64_t(sg.head) * each;     // of this head
-                sg.i0 = tile.tiles(u - from);
-                sg.n = tile.tiles(min(int64_t(each), last - from)) - sg.i0;
-                sg.whole = sg.n == sg.kt.n;
-                sg.parts = sg.whole || sg.i0 > 0 ? 0 : run.owner(from + each - 1) - int(blockIdx.x) + 1;
-                u = min(from + each, last);
-                if (u < last && u >= before + int64_t(each) * a.Hkv) {
-                    before += int64_t(each) * a.Hkv;
-                    row0 += MANY;
-                    if (row0 >= sg.M) {     // the next request with more than FEW rows
-                        row0 = 0;
-                        for (unsigned hit = 0; hit == 0;) {
-                            const int k = r + 1 + lane;
-                            hit = __ballot_sync(FULL, k < a.R && request<true>(a, min(k, a.R - 1)).rows(a) > a.rows_upto);
-                            r += hit ? __ffs(int(hit)) : 32;
-                            if (!hit && r >= a.R - 1) {     // (none is left: not with the lengths that the run was cut by)
-                                u = last;
-                                break;
-                            }
-                        }
-                    }
-                }
-                // (a run that ends within a tile's start leaves all of it to the next)
-                if (sg.n <= 0) sg.n = 0;
-            }
+            const Segment sg = line.next(a, run, int(blockIdx.x), lane);
             if (lane == 0) segs[s % AHEAD] = sg;
             __syncwarp();
             if (lane == 0) bar_arrive(segbar + 8 * (s % AHEAD));
             if (sg.n == 0) break;
         }
+        // A CTA that gave up: what has been written of its run's rows is not told apart from what has not.
+        all_done();
+        if (*dead) {
+            line = ManyLine(run);
+            for (Segment sg = line.next(a, run, int(blockIdx.x), lane); sg.n > 0; sg = line.next(a, run, int(blockIdx.x), lane))
+                lost_tile<T, D, MANY>(a, sg, a.t_part_l, a.t_split, int(blockIdx.x), lane);
+        }
+        return;
     } else if (warp == ROLES + 7) {
         // ================================================ queries
         bool ok = true;
@@ -660,10 +687,10 @@ __global__ void __launch_bounds__(CNT, 1) chunk_tensor_kernel(const __grid_const
                 // ---- the row's output, once the last product is done
                 const uint32_t end = DEEP ? done - 1 : ends++;
                 ok = ok && __all_sync(FULL, bar_wait(vbar + 8 * turn(t, end), phase(end), dead, a.patience));
+                if (!ok) break;
                 tmem_fence_after();
-                const float bad = (!ok || *dead) ? __int_as_float(0x7fffffff) : 0.f;
-                const float inv = (l == 0.f ? 0.f : 1.f / l) + bad;
-                const float lse = (l == 0.f ? -INFINITY : m + (log2f(l) - W::SHIFT)) + bad;
+                const float inv = l == 0.f ? 0.f : 1.f / l;
+                const float lse = l == 0.f ? -INFINITY : m + (log2f(l) - W::SHIFT);
                 const bool whole = sg.whole, fix = odd[s & 3] == int(s) + 1;
                 const int j = on ? row / a.gs : 0, h = sg.head * a.gs + (on ? row - j * a.gs : 0);
                 T* out = static_cast<T*>(a.out) + (sg.x.q0 + j) * a.os[0] + h * a.os[1];
@@ -708,7 +735,7 @@ __global__ void __launch_bounds__(CNT, 1) chunk_tensor_kernel(const __grid_const
                     __syncwarp();   // (tensor memory is read by whole warps)
                 }
                 if (on) {
-                    if (!whole) a.t_part_l[slot] = make_float2(m, l * exp2f(-W::SHIFT) + bad);
+                    if (!whole) a.t_part_l[slot] = make_float2(m, l * exp2f(-W::SHIFT));
                     else if (a.lse) a.lse[int64_t(sg.x.q0 + j) * a.Hq + h] = lse * 0.693147180559945309f;
                 }
                 // The CTA that has a tile's first part says how many CTAs have one.
@@ -719,11 +746,7 @@ __global__ void __launch_bounds__(CNT, 1) chunk_tensor_kernel(const __grid_const
             give_back(s);
         }
     }
-    // Copies that a role which gave up has in flight land (a microsecond or two) before their memory is anyone else's.
-    for (int i = 0; *dead && i < 1000; ++i) __nanosleep(1000);
-    tmem_fence_before();
-    __syncthreads();
-    tmem_fence_after();
+    all_done();
     if (warp == ROLES + 4) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
 }
 

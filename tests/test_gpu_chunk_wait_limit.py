@@ -1,5 +1,5 @@
-"""Attention of chunks whose waits run out: a limit on the kernels' waits for their own copies and products, so short that
-some of them give up.  Every launch ends, and calls behind it are as if it had not been."""
+"""Attention of chunks whose waits run out: a limit on the kernels' waits, so short that CTAs give up in the middle of their
+work.  Every launch ends, what was not computed is NaN, and calls behind it are as if it had not been."""
 import ctypes
 
 import numpy as np
@@ -10,7 +10,7 @@ from tests.test_gpu_chunk_attention import call, case
 
 pytestmark = pytest.mark.gpu
 DEFAULT = 4 * 10 ** 9
-LIMITS = [0, 300, 1000, 3000, 10000, 30000]     # clock cycles; a key tile takes 1000 to 3000
+LIMITS = [0, 1000, 3000, 10000, 20000, 30000, 50000, 80000]     # clock cycles; a key tile takes 1000 to 3000
 
 
 @pytest.fixture(scope="module")
@@ -32,20 +32,51 @@ def limit(ms):
     to(DEFAULT)
 
 
-CASES = {"few": ([1, 3, 2] * 9, [5000, 300, 70] * 9), "many": ([300, 40, 700], [4000, 900, 700]), "both": ([1, 300, 2], [9000, 3000, 50])}
+# More tiles for a CTA than are described ahead, cut ones and whole ones; of requests with few rows, with many, with both.
+CASES = {"few": ([1, 3, 2, 1] * 50, [300, 70, 20, 900] * 50), "many": ([40, 7, 300, 90] * 35, [150, 60, 350, 100] * 35),
+         "both": ([1, 40, 3, 90] * 40, [500, 100, 50, 300] * 40)}
 
 
 @pytest.mark.parametrize("D", [64, 128, 256])
 @pytest.mark.parametrize("kind", CASES)
 def test_every_launch_ends(ms, limit, D, kind):
     import torch
-    c = case(60, "bf16", *CASES[kind], 8, 2, D, 16)
-    want, lse = call(ms, c)
+    c = case(60, "bf16", *CASES[kind], 16, 8, D, 16)
+    hint = dict(max_queries=4 if kind == "few" else None)
+    want, lse = call(ms, c, **hint)
     torch.cuda.synchronize()
     for cycles in LIMITS:
         limit(cycles)
-        call(ms, c, out=torch.empty_like(want))
+        call(ms, c, out=torch.empty_like(want), **hint)
         torch.cuda.synchronize()
         limit(DEFAULT)
-        out, l = call(ms, c)
+        out, l = call(ms, c, **hint)
         assert torch.equal(out, want) and torch.equal(l, lse)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("kind", CASES)
+def test_every_row_is_right_or_nan(ms, limit, dtype, D, kind):
+    """Nothing of what an output or a workspace held before shows: each head of each token is the answer's bits or NaN, its lse
+    too, and rows of no request are as they were."""
+    import torch
+    if D == 256 and kind != "few":
+        pytest.skip("many rows of heads of 256 have no waits of this kind")
+    c = case(61, dtype, *CASES[kind], 16, 8, D, 16, lead=2, tail=3)
+    hint = dict(max_queries=4 if kind == "few" else None)
+    want, lse = call(ms, c, out=torch.full_like(c["q"], 7.0), **hint)
+    lost = []
+    for cycles in LIMITS + [0] * 4:
+        torch.full((1 << 26,), 7.0, device="cuda")    # what the allocator hands out next
+        limit(cycles)
+        out, l = call(ms, c, out=torch.full_like(c["q"], 7.0), **hint)
+        torch.cuda.synchronize()
+        limit(DEFAULT)
+        gone = torch.isnan(out).all(-1)
+        lost.append(int(gone.sum()))
+        same = (out == want).all(-1) & (l == lse)
+        assert bool((same | (gone & torch.isnan(l))).all()), (cycles, lost)
+        n = int(c["starts"][-1])
+        assert bool((out[:2] == 7).all()) and bool((out[n:] == 7).all())
+    assert max(lost) > 0, lost  # (of no cycles: the first wait that is not over when it is looked at)

@@ -34,7 +34,8 @@ struct Refused {
 
 bool none(PyObject* o) { return o == nullptr || o == Py_None; }
 
-const at::Tensor* tensor(PyObject* o) { return THPVariable_Check(o) ? &THPVariable_Unpack(o) : nullptr; }
+// (None is asked about first: whether it is an instance of a tensor's class takes Python about 0.1 us to answer)
+const at::Tensor* tensor(PyObject* o) { return !none(o) && THPVariable_Check(o) ? &THPVariable_Unpack(o) : nullptr; }
 
 int dtype_of(at::ScalarType t) {
     switch (t) {

@@ -533,7 +533,8 @@ fs_status fs_shared_prefix_attention_workspace_bytes(const fs_paged_kv* cache, i
  * A request gets all that it asks for or nothing.  It is granted if the pages that requests 0 .. r ask for together
  * are no more than the free ones (or it needs none itself) and the tokens that they ask for together
  * are no more than the budget; a request whose lens[r] is negative or which would
- * have more than table_width * page_size tokens asks for nothing.  Page numbers are copied, not checked.  What is
+ * have more than table_width * page_size tokens asks for nothing.  One that asks for more than the budget, or for more pages than there
+ * are, is not granted in any step, and with it none behind it that needs tokens, or pages: cut what is asked for to a step's size.  Page numbers are copied, not checked.  What is
  * written shares no memory with what is read. */
 fs_status fs_paged_step_tables(const int32_t* lens, const int32_t* new_lens, int32_t requests, int32_t* page_table,
                                int32_t table_width, const int32_t* free_pages, int32_t free_size,

@@ -464,7 +464,8 @@ def paged_step_tables(lens, new_lens, page_table, free_pages, free_count, page_s
     lens, new_lens: [R] int32.  page_table: [R, width] int32; the entries of the new pages are written, with pages from
     the top of the stack free_pages ([F] int32), of whose entries the first free_count[0] are free.  A request gets
     all that it asks for or nothing: it is granted if the requests up to it ask for no more pages than
-    are free (or it needs none) and for no more than max_tokens tokens together.
+    are free (or it needs none) and for no more than max_tokens tokens together.  One that asks for more than max_tokens, or than
+    there are pages, is never granted and holds back those behind it: cut new_lens to what a step can hold.
     Returns (query_starts [R + 1], rows [max_tokens], positions [max_tokens], totals [R], free_left [1]), all
     int32: the tokens of request r lie at query_starts[r] up to query_starts[r + 1] in the step's batch; each
     token's request and place, as append_paged_kv takes them (-1 behind the last one); the tokens that each

@@ -10,8 +10,8 @@
 //                  names it, counts them in a table in shared memory and computes
 //                  their logits, while the copy ends; then it writes them.  Where a table overflows, or there would be too many, the
 //                  tokens are counted by ranges, a word each.
-// 64 rows of 151936 logits in float32 with histories of 4096: 21 us, 3.7 TB/s (copied alone 10 us); 256 of 151665 in bf16
-// with masks and histories of 700: 42 us, 3.7 TB/s (copied alone 30 us): what is left is change_kernel's way through a history, of which
+// 64 rows of 151936 logits in float32 with histories of 4096: 23 us, 3.5 TB/s (copied alone 10 us); 256 of 151665 in bf16
+// with masks and histories of 700: 41 us, 3.8 TB/s (copied alone 30 us): what is left is change_kernel's way through a history, of which
 // only the copy's last wave is beside it.
 // In place, and where there is nothing to mask or to change, one of them is left out. (In one launch, each CTA counting
 // for its own 8192 logits: 64 rows of 151936 28 us, 256 of 151665 with masks 64 us; a CTA's way through the history

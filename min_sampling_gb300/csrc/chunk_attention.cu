@@ -15,8 +15,8 @@
 // Three launches: chunk_tensor.cu, requests of more than 16 rows, on the 5th-generation tensor cores; chunk_few.cu, requests of
 // up to 16 rows, single tokens above all; the parts joined.  The first two have lines of their own and do not wait for each other:
 // the SMs that are done with the first take the second's CTAs.  (The other way round, and one CTA planning
-// for all, 460 us for two chunks of 1021 tokens behind 16384 and 47 single tokens; 455 this way. On SMs
-// of their own beside the first they slowed its CTAs on the neighbouring SMs by a sixth: 490 us.)
+// for all, 5 us more for two chunks of 1021 tokens behind 16384 and 47 single tokens, of 465. On SMs
+// of their own beside the first they slowed its CTAs on the neighbouring SMs by a sixth: 35 us more.)
 // chunk_rows_kernel (mma.sync) has many rows of heads of 256, and a few where the caches' strides have no map for the copy engine.
 #include "chunk.cuh"
 

@@ -5,7 +5,7 @@
 // a time, into a ring that is as deep as shared memory allows (two CTAs on an SM, 192 KB on their way); four
 // warps take 16 of the 64 keys each (mma.sync) with a running maximum, sum and output of their own, joined at the
 // tile's end.  Nothing but the ring's barriers ties them together, so the reads go on over the ends of tiles and
-// requests.  64 requests of up to 8192 tokens, 8 heads of 128: 170 us, 6.4 TB/s (with copies by the four
+// requests.  64 requests of up to 8192 tokens, 8 heads of 128: 175 us, 6.2 TB/s (with copies by the four
 // warps themselves, a tile ahead and a barrier each, 250 us).
 // Every wait on a barrier is bounded; one that runs out marks the CTA, which then writes NaN for all rows of its run.
 #include "chunk_copy.cuh"

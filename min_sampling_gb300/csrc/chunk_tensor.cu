@@ -27,7 +27,7 @@
 // the instruction cache holds neither.  Of a tile's weights three quarters are announced first, so that the
 // product that reads the last quarter is 128 cycles and not 256.
 //
-// Measured, bf16, 32 heads over 8 of 128: a prompt of 8190 tokens 403 to 422 us, 1.3 PFLOP/s, two thirds of the rate of the largest
+// Measured, bf16, 32 heads over 8 of 128: a prompt of 8190 tokens 420 to 426 us, 1.3 PFLOP/s, two thirds of the rate of the largest
 // library product. For 256 rows and 128 keys the products take 2048 cycles, a tile's scores 1570 (load 330, maximum
 // 260, weights 980) and then its products and the hand-overs, together 2860: that chain bounds it, and where 16-token
 // pages are read by all SMs at once 400 cycles of waiting for keys and values.  Heads of 64: 2150 cycles, the weights', of two
